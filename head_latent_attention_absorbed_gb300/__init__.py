@@ -19,7 +19,11 @@ from ._binding import (_check, _stream, step_call, EXPORTED, LIB_PATH, MLA_BF16,
                        decode_attn_noalloc, decode_combine, decode_split, decode_step, dims,
                        dtype_code, heads_per_cta, load, num_splits, out_proj, plan,
                        set_launch_overlap, set_split_parts,
-                       workspace_bytes)
+                       workspace_bytes, MLA_DEV_PAGE_OUT_OF_RANGE, MLA_DEV_POOL_EXHAUSTED,
+                       MlaPaging, cache_append_paged, decode_attn_paged, decode_attn_sparse,
+                       page_index, paged_num_splits, paged_workspace_bytes, pages_extend,
+                       pages_release, paging, select_pages, select_workspace_bytes,
+                       sparse_workspace_bytes)
 
 __all__ = [
     "EXPORTED", "LIB_PATH", "MLA_BF16", "MLA_F32", "MLA_FP8_E4M3", "MLA_DEV_LENGTH_OUT_OF_RANGE",
@@ -30,6 +34,10 @@ __all__ = [
     "decode_attn_noalloc", "decode_split", "decode_combine", "decode_step", "dims",
     "dtype_code", "load", "num_splits", "out_proj", "workspace_bytes", "DecodeStep", "HostStep",
     "cache_append", "wo_proj", "set_launch_overlap", "plan", "set_split_parts", "heads_per_cta",
+    "MLA_DEV_PAGE_OUT_OF_RANGE", "MLA_DEV_POOL_EXHAUSTED", "MlaPaging", "paging",
+    "pages_extend", "pages_release", "cache_append_paged", "decode_attn_paged",
+    "paged_num_splits", "paged_workspace_bytes", "page_index", "select_pages",
+    "select_workspace_bytes", "decode_attn_sparse", "sparse_workspace_bytes",
 ]
 
 

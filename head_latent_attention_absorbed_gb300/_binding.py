@@ -19,6 +19,8 @@ MLA_F32, MLA_BF16, MLA_FP8_E4M3 = 0, 1, 2
 MLA_DEV_LENGTH_OUT_OF_RANGE = 1
 MLA_DEV_PIPELINE_TIMEOUT = 2
 MLA_DEV_BOUNDS = 4
+MLA_DEV_PAGE_OUT_OF_RANGE = 8
+MLA_DEV_POOL_EXHAUSTED = 16
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
           3: "MLA_ERR_WORKSPACE", 4: "MLA_ERR_CUDA"}
 EXPORTED = ("mla_absorb_q", "mla_decode_num_splits", "mla_decode_workspace_bytes",
@@ -31,13 +33,22 @@ EXPORTED = ("mla_absorb_q", "mla_decode_num_splits", "mla_decode_workspace_bytes
             "mla_status_string", "mla_last_error_message", "mla_test_set_split_hooks",
             "mla_set_launch_overlap", "mla_decode_plan", "mla_test_set_split_debug",
             "mla_test_set_split_form", "mla_built_with_checks", "mla_debug_bounds_word",
-            "mla_set_split_parts", "mla_decode_heads_per_cta")
+            "mla_set_split_parts", "mla_decode_heads_per_cta",
+            "mla_pages_extend", "mla_pages_release", "mla_cache_append_paged",
+            "mla_paged_num_splits", "mla_paged_workspace_bytes", "mla_decode_attn_paged",
+            "mla_page_index", "mla_select_workspace_bytes", "mla_select_pages",
+            "mla_sparse_workspace_bytes", "mla_decode_attn_sparse")
 
 
 class MlaDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("d_c", ctypes.c_int32),
                 ("d_rope", ctypes.c_int32), ("d_nope", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("s_max", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class MlaPaging(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32)]
 
 
 class MlaError(RuntimeError):
@@ -124,6 +135,32 @@ def load(path: Optional[str] = None):
     lib.mla_decode_plan.argtypes = [D, I32, ctypes.POINTER(I32), ctypes.POINTER(I32),
                                     ctypes.POINTER(I32)]
     lib.mla_decode_plan.restype = ctypes.c_int
+    G = ctypes.POINTER(MlaPaging)
+    F = ctypes.c_float
+    lib.mla_pages_extend.argtypes = [I32, G, P, P, I32, P, P, P, P, P, P, P, P, P, P]
+    lib.mla_pages_extend.restype = ctypes.c_int
+    lib.mla_pages_release.argtypes = [I32, G, P, P, P, P, P, P, P]
+    lib.mla_pages_release.restype = ctypes.c_int
+    lib.mla_cache_append_paged.argtypes = [D, G, I32, I32, P, P, P, ctypes.c_double, P, P, P]
+    lib.mla_cache_append_paged.restype = ctypes.c_int
+    lib.mla_paged_num_splits.argtypes = [D, G, I32, I32, I32]
+    lib.mla_paged_num_splits.restype = I32
+    lib.mla_paged_workspace_bytes.argtypes = [D, G, I32, I32, I32]
+    lib.mla_paged_workspace_bytes.restype = SZ
+    lib.mla_decode_attn_paged.argtypes = [D, G, I32, I32, P, P, P, P, P, F, I32, P, SZ, P, P, P, P]
+    lib.mla_decode_attn_paged.restype = ctypes.c_int
+    lib.mla_page_index.argtypes = [D, G, I32, P, P, P, P, P, P, P, P]
+    lib.mla_page_index.restype = ctypes.c_int
+    lib.mla_select_workspace_bytes.argtypes = [D, G, I32]
+    lib.mla_select_workspace_bytes.restype = SZ
+    lib.mla_select_pages.argtypes = [D, G, I32, I32, P, P, P, P, P, P, I32, I32, I32, P, SZ, P, P,
+                                     P, P]
+    lib.mla_select_pages.restype = ctypes.c_int
+    lib.mla_sparse_workspace_bytes.argtypes = [D, G, I32, I32, I32, I32]
+    lib.mla_sparse_workspace_bytes.restype = SZ
+    lib.mla_decode_attn_sparse.argtypes = [D, G, I32, I32, P, P, P, P, P, P, P, F, I32, I32, I32,
+                                           I32, P, SZ, P, P, P, P, P, P]
+    lib.mla_decode_attn_sparse.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -412,3 +449,271 @@ def ov_proj(d: MlaDims, o_c, w_ov, y, stream=None) -> None:
     _cuda_contig(o_c, w_ov, y)
     _check(load().mla_ov_proj(ctypes.byref(d), int(w_ov.shape[0]), _ptr(o_c), _ptr(w_ov), _ptr(y),
                               _stream(stream)))
+
+
+# ------------------------------------------------------------------- paged cache
+
+def paging(page_size: int, num_pages: int, table_stride: int) -> MlaPaging:
+    """The pool's shape: rows per page, pages, and entries per block-table row."""
+    return MlaPaging(page_size, num_pages, table_stride)
+
+
+def _io_code(torch_dtype) -> int:
+    """Query and output type of the paged calls."""
+    import torch
+    if torch_dtype == torch.bfloat16:
+        return MLA_BF16
+    _require(torch_dtype == torch.float32, "queries must be fp32 or bf16")
+    return MLA_F32
+
+
+def _on_device(*ts):
+    """Contiguous CUDA tensors on the current device, the one whose stream the
+    call is enqueued on."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    for t in ts:
+        if t is not None:
+            _require(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
+            _require(t.get_device() == dev, "tensors must be on the current CUDA device")
+
+
+def _sized(name: str, t, dtype, numel: int):
+    _require(t.dtype == dtype and t.numel() == numel,
+             f"{name} must hold {numel} values of {dtype}")
+
+
+def _status_word(t):
+    if t is not None:
+        import torch
+        _require(t.dtype == torch.int32 and t.numel() >= 1, "dev_status must hold an int32")
+
+
+def _pool(d: MlaDims, pg: MlaPaging, cache):
+    _require(dtype_code(cache.dtype) == d.dtype, "the cache's dtype differs from the dims'")
+    _require(cache.numel() == pg.num_pages * pg.page_size * (d.d_c + d.d_rope),
+             "the cache must hold num_pages x page_size rows")
+
+
+def _table(pg: MlaPaging, t, batch: int):
+    import torch
+    _sized("block_table", t, torch.int32, batch * pg.table_stride)
+
+
+def _queries(d: MlaDims, q_len: int, q_abs, q_pe, o_c=None, lse=None) -> int:
+    """Checks the query side of a paged call; returns its io_dtype."""
+    import torch
+    rows = d.batch * q_len * d.heads
+    _require(q_len >= 1, "q_len must be >= 1")
+    _sized("q_abs", q_abs, q_abs.dtype, rows * d.d_c)
+    _sized("q_pe", q_pe, q_abs.dtype, rows * d.d_rope)
+    if o_c is not None:
+        _sized("o_c", o_c, q_abs.dtype, rows * d.d_c)
+    if lse is not None:
+        _sized("lse", lse, torch.float32, rows)
+    return _io_code(q_abs.dtype)
+
+
+def pages_extend(pg: MlaPaging, cached_lens, new_lens, block_table, free_list, num_free, lengths,
+                 row_starts, slots, positions, num_free_out=None, dev_status=None,
+                 stream=None) -> None:
+    """Block tables and slot maps of one step from the requests' lengths.
+
+    Takes pages from the free stack for the rows that new_lens adds, and writes
+    lengths, row_starts, slots and positions (padded to slots.numel() with -1 and
+    0).  All or nothing: see mla_pages_extend.  ``num_free`` is updated in place
+    unless ``num_free_out`` is given.
+    """
+    import torch
+    i32 = torch.int32
+    out = num_free if num_free_out is None else num_free_out
+    _on_device(cached_lens, new_lens, block_table, free_list, num_free, out, lengths, row_starts,
+               slots, positions, dev_status)
+    B, n = cached_lens.numel(), slots.numel()
+    _sized("cached_lens", cached_lens, i32, B)
+    _sized("new_lens", new_lens, i32, B)
+    _sized("lengths", lengths, i32, B)
+    _sized("row_starts", row_starts, i32, B + 1)
+    _sized("slots", slots, torch.int64, n)
+    _sized("positions", positions, i32, n)
+    _sized("free_list", free_list, i32, pg.num_pages)
+    _sized("num_free", num_free, i32, 1)
+    _sized("num_free_out", out, i32, 1)
+    _table(pg, block_table, B)
+    _status_word(dev_status)
+    _check(load().mla_pages_extend(B, ctypes.byref(pg), _ptr(cached_lens), _ptr(new_lens), n,
+                                   _ptr(block_table), _ptr(free_list), _ptr(num_free), _ptr(out),
+                                   _ptr(lengths), _ptr(row_starts), _ptr(slots), _ptr(positions),
+                                   _ptr(dev_status), _stream(stream)))
+
+
+def pages_release(pg: MlaPaging, finished, lengths, block_table, free_list, num_free,
+                  dev_status=None, stream=None) -> None:
+    """Push the pages of the requests with finished[b] != 0 back on the free stack."""
+    import torch
+    i32 = torch.int32
+    _on_device(finished, lengths, block_table, free_list, num_free, dev_status)
+    B = finished.numel()
+    _sized("finished", finished, i32, B)
+    _sized("lengths", lengths, i32, B)
+    _sized("free_list", free_list, i32, pg.num_pages)
+    _sized("num_free", num_free, i32, 1)
+    _table(pg, block_table, B)
+    _status_word(dev_status)
+    _check(load().mla_pages_release(B, ctypes.byref(pg), _ptr(finished), _ptr(lengths),
+                                    _ptr(block_table), _ptr(free_list), _ptr(num_free),
+                                    _ptr(dev_status), _stream(stream)))
+
+
+def cache_append_paged(d: MlaDims, pg: MlaPaging, rows, positions, slots, cache,
+                       rope_base: float = 10000.0, dev_status=None, stream=None) -> None:
+    """Write latent rows [n, 576] (fp32 or bf16) into their slots, the RoPE key
+    rotated at its position; a slot of -1 is skipped."""
+    import torch
+    _on_device(rows, positions, slots, cache, dev_status)
+    n = slots.numel()
+    _sized("rows", rows, rows.dtype, n * (d.d_c + d.d_rope))
+    _sized("positions", positions, torch.int32, n)
+    _sized("slots", slots, torch.int64, n)
+    _pool(d, pg, cache)
+    _status_word(dev_status)
+    _check(load().mla_cache_append_paged(ctypes.byref(d), ctypes.byref(pg), n,
+                                         dtype_code(rows.dtype), _ptr(rows), _ptr(positions),
+                                         _ptr(slots), float(rope_base), _ptr(cache),
+                                         _ptr(dev_status), _stream(stream)))
+
+
+def paged_num_splits(d: MlaDims, pg: MlaPaging, io_dtype, q_len: int = 1,
+                     requested: int = 0) -> int:
+    """Chunks per sequence decode_attn_paged uses for queries of ``io_dtype``."""
+    n = int(load().mla_paged_num_splits(ctypes.byref(d), ctypes.byref(pg), _io_code(io_dtype),
+                                        int(q_len), int(requested)))
+    _require(n > 0, load().mla_last_error_message().decode())
+    return n
+
+
+def paged_workspace_bytes(d: MlaDims, pg: MlaPaging, io_dtype, q_len: int = 1,
+                          requested: int = 0) -> int:
+    """Workspace bytes of decode_attn_paged for queries of ``io_dtype``."""
+    n = int(load().mla_paged_workspace_bytes(ctypes.byref(d), ctypes.byref(pg),
+                                             _io_code(io_dtype), int(q_len), int(requested)))
+    _require(n > 0, load().mla_last_error_message().decode())
+    return n
+
+
+def decode_attn_paged(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_table, lengths, o_c,
+                      workspace, softmax_scale: float, q_len: int = 1,
+                      num_splits_requested: int = 0, lse=None, dev_status=None,
+                      stream=None) -> None:
+    """decode_attn_multi over a paged cache; q_abs, q_pe and o_c all fp32 or all bf16."""
+    import torch
+    _on_device(q_abs, q_pe, cache, block_table, lengths, o_c, workspace, lse, dev_status)
+    io = _queries(d, q_len, q_abs, q_pe, o_c, lse)
+    _pool(d, pg, cache)
+    _table(pg, block_table, d.batch)
+    _sized("lengths", lengths, torch.int32, d.batch)
+    _status_word(dev_status)
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(load().mla_decode_attn_paged(ctypes.byref(d), ctypes.byref(pg), io, int(q_len),
+                                        _ptr(q_abs), _ptr(q_pe), _ptr(cache), _ptr(block_table),
+                                        _ptr(lengths), float(softmax_scale),
+                                        int(num_splits_requested), _ptr(workspace), nbytes,
+                                        _ptr(o_c), _ptr(lse), _ptr(dev_status), _stream(stream)))
+
+
+def page_index(d: MlaDims, pg: MlaPaging, cache, block_table, first_rows, lengths, max_new: int,
+               codes, scales, dev_status=None, stream=None) -> None:
+    """Index rows (int8 mean row and scale, by page number) of the pages that hold
+    rows [first_rows[b], lengths[b]) of each sequence."""
+    import torch
+    _on_device(cache, block_table, first_rows, lengths, codes, scales, dev_status)
+    _pool(d, pg, cache)
+    _table(pg, block_table, d.batch)
+    _sized("first_rows", first_rows, torch.int32, d.batch)
+    _sized("lengths", lengths, torch.int32, d.batch)
+    _index(d, pg, codes, scales)
+    _status_word(dev_status)
+    _check(load().mla_page_index(ctypes.byref(d), ctypes.byref(pg), int(max_new), _ptr(cache),
+                                 _ptr(block_table), _ptr(first_rows), _ptr(lengths), _ptr(codes),
+                                 _ptr(scales), _ptr(dev_status), _stream(stream)))
+
+
+def _index(d: MlaDims, pg: MlaPaging, codes, scales):
+    import torch
+    _sized("codes", codes, torch.int8, pg.num_pages * (d.d_c + d.d_rope))
+    _sized("scales", scales, torch.float32, pg.num_pages)
+
+
+def _choice(d: MlaDims, q_len: int, sel_table, sel_lengths) -> int:
+    """Checks the outputs of a page selection; returns top_pages."""
+    import torch
+    rows = d.batch * q_len
+    _require(sel_table.dim() == 2, "sel_table must have one row per token")
+    _sized("sel_table", sel_table, torch.int32, rows * sel_table.shape[1])
+    _sized("sel_lengths", sel_lengths, torch.int32, rows)
+    return int(sel_table.shape[1])
+
+
+def select_workspace_bytes(d: MlaDims, pg: MlaPaging, q_len: int = 1) -> int:
+    n = int(load().mla_select_workspace_bytes(ctypes.byref(d), ctypes.byref(pg), int(q_len)))
+    _require(n > 0, load().mla_last_error_message().decode())
+    return n
+
+
+def select_pages(d: MlaDims, pg: MlaPaging, q_abs, q_pe, block_table, lengths, codes, scales,
+                 sel_table, sel_lengths, workspace, q_len: int = 1, keep_first: int = 1,
+                 keep_last: int = 1, dev_status=None, stream=None) -> None:
+    """The pages each token attends: its first and last ones and the best by the
+    index's score, sel_table.shape[1] in all, as a block table of their own."""
+    import torch
+    _on_device(q_abs, q_pe, block_table, lengths, codes, scales, sel_table, sel_lengths,
+               workspace, dev_status)
+    io = _queries(d, q_len, q_abs, q_pe)
+    _table(pg, block_table, d.batch)
+    _sized("lengths", lengths, torch.int32, d.batch)
+    _index(d, pg, codes, scales)
+    top = _choice(d, q_len, sel_table, sel_lengths)
+    _status_word(dev_status)
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(load().mla_select_pages(ctypes.byref(d), ctypes.byref(pg), io, int(q_len), _ptr(q_abs),
+                                   _ptr(q_pe), _ptr(block_table), _ptr(lengths), _ptr(codes),
+                                   _ptr(scales), top, int(keep_first), int(keep_last),
+                                   _ptr(workspace), nbytes, _ptr(sel_table), _ptr(sel_lengths),
+                                   _ptr(dev_status), _stream(stream)))
+
+
+def sparse_workspace_bytes(d: MlaDims, pg: MlaPaging, io_dtype, top_pages: int, q_len: int = 1,
+                           requested: int = 0) -> int:
+    """Workspace bytes of decode_attn_sparse for queries of ``io_dtype``."""
+    n = int(load().mla_sparse_workspace_bytes(ctypes.byref(d), ctypes.byref(pg),
+                                              _io_code(io_dtype), int(q_len), int(top_pages),
+                                              int(requested)))
+    _require(n > 0, load().mla_last_error_message().decode())
+    return n
+
+
+def decode_attn_sparse(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_table, lengths, codes,
+                       scales, sel_table, sel_lengths, o_c, workspace, softmax_scale: float,
+                       q_len: int = 1, keep_first: int = 1, keep_last: int = 1,
+                       num_splits_requested: int = 0, lse=None, dev_status=None,
+                       stream=None) -> None:
+    """select_pages, then decode_attn_paged over the pages kept."""
+    import torch
+    _on_device(q_abs, q_pe, cache, block_table, lengths, codes, scales, sel_table, sel_lengths,
+               o_c, workspace, lse, dev_status)
+    io = _queries(d, q_len, q_abs, q_pe, o_c, lse)
+    _pool(d, pg, cache)
+    _table(pg, block_table, d.batch)
+    _sized("lengths", lengths, torch.int32, d.batch)
+    _index(d, pg, codes, scales)
+    top = _choice(d, q_len, sel_table, sel_lengths)
+    _status_word(dev_status)
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(load().mla_decode_attn_sparse(ctypes.byref(d), ctypes.byref(pg), io, int(q_len),
+                                         _ptr(q_abs), _ptr(q_pe), _ptr(cache), _ptr(block_table),
+                                         _ptr(lengths), _ptr(codes), _ptr(scales),
+                                         float(softmax_scale), top, int(keep_first),
+                                         int(keep_last), int(num_splits_requested),
+                                         _ptr(workspace), nbytes, _ptr(sel_table),
+                                         _ptr(sel_lengths), _ptr(o_c), _ptr(lse),
+                                         _ptr(dev_status), _stream(stream)))

@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "mla_common.cuh"
+#include "mla_paged.cuh"
 #include "mla_split.cuh"
 
 namespace mla {
@@ -70,7 +71,8 @@ constexpr float kRescaleLog2 = 8.f;
 // head group.  A CTA of an ordinary grid has one item (its blockIdx); a
 // persistent CTA has the items plan_items gives it, streamed back to back.
 struct SplitItem {
-  int row0;        // cache row (of the [B*s_max, 576] view) of the item's first row
+  int row0;        // cache row (of the [B*s_max, 576] view) of the item's first row; of a
+                   // paged cache, the row within its sequence
   int tiles;       // 128-row tiles
   int t0;          // index of its first tile in the CTA's tile stream
   int valid_last;  // rows of its last tile that belong to the item
@@ -275,7 +277,7 @@ __device__ void plan_items(const SplitParams& p, SplitItem* items, volatile int*
         const int r0 = j * p.chunk, r1 = min(r0 + p.chunk, len);
         const int it = (r1 - r0 + kTileRows - 1) / kTileRows;
         SplitItem m;
-        m.row0 = cache_seq(p, v) * p.s_max + r0;
+        m.row0 = p.table ? r0 : cache_seq(p, v) * p.s_max + r0;
         m.tiles = it;
         m.t0 = 0;
         m.valid_last = r1 - (r0 + (it - 1) * kTileRows);
@@ -363,7 +365,12 @@ __device__ __forceinline__ float reduce8_heads(float v[8], int lane) {
 // that query into the query area once the score MMAs of the item are done (the
 // score issuers wait for it).  Only the CTA's last tile takes the special tail
 // path (its boxes read in place from ring A).
-template <int kG, bool kPersist>
+//
+// A paged cache (kPaged; chunks are whole tiles) differs in where a box comes
+// from: a tile's 128 rows are boxes of up to 128 (ring A) or 64 (ring B) rows
+// of one page each, issued by as many lanes, which look the next tile's pages
+// up one tile ahead.  The query may then be bf16 as it is stored.
+template <int kG, bool kPersist, bool kPaged>
 __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     split_tc_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_half,
                     const SplitParams p) {
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   const bool pair = kG == 32 && p.tpc == 2;
   constexpr bool persist = kPersist;
   // Rows of the cache's [sequences * s_max, 576] view (index checks).
-  const long long cache_rows = static_cast<long long>(p.B / p.q_len) * p.s_max;
+  const long long cache_rows = kPaged ? 0 : static_cast<long long>(p.B / p.q_len) * p.s_max;
   (void)cache_rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) { return bars + 8 * i; };
@@ -452,6 +459,45 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   // softmax thread loads nine float4 at a time before converting them.
   // signal: arrive on named barrier 3 once the first pass's loads are issued.
   auto load_query = [&](int v, int h0, bool signal = false) {
+    if (kPaged && p.io_bf16) {
+      // bf16 queries: the high part is the value, the low part zero.  Eight
+      // values per load, as many of them in flight as the fp32 path has.
+      constexpr int kNA = kHeadGroup * kDc / 8, kNQ = kNA + kHeadGroup * kDr / 8;
+      constexpr int kEach = (kNQ + kSoftThreads - 1) / kSoftThreads;
+      static_assert(kEach <= 9, "at most nine loads per thread");
+      uint4 q8[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int idx = tid + i * kSoftThreads;
+        const int n = idx < kNA ? idx / (kDc / 8) : (idx - kNA) / (kDr / 8);
+        const size_t row = pair ? size_t(v + n / 16) * p.H + h0 + n % 16 : size_t(v) * p.H + h0 + n;
+        q8[i] = make_uint4(0, 0, 0, 0);
+        if (idx >= kNQ || !MLA_IN_BOUNDS(row < size_t(p.B) * p.H)) continue;
+        q8[i] = idx < kNA ? reinterpret_cast<const uint4*>(
+                                static_cast<const __nv_bfloat16*>(p.q_abs) + row * kDc)[idx % (kDc / 8)]
+                          : reinterpret_cast<const uint4*>(
+                                static_cast<const __nv_bfloat16*>(p.q_pe) +
+                                row * kDr)[(idx - kNA) % (kDr / 8)];
+      }
+      if (signal) named_bar_arrive(3, kSoftThreads + 32);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int idx = tid + i * kSoftThreads;
+        if (idx >= kNQ) break;
+        const int h = idx < kNA ? idx / (kDc / 8) : (idx - kNA) / (kDr / 8);
+        const int k = idx < kNA ? 8 * (idx % (kDc / 8)) : kDc + 8 * ((idx - kNA) % (kDr / 8));
+        const int box = k >> 6, ch = (k & 63) >> 3;
+        const uint32_t o_hi = box * kQBoxBytes + sw128(h, ch);
+        const uint32_t o_lo = box * kQBoxBytes + sw128(h + kHeadGroup, ch);
+        if (MLA_IN_BOUNDS(o_hi + 16 <= 9u * kQBoxBytes &&
+                          (kParts == 1 || o_lo + 16 <= 9u * kQBoxBytes))) {
+          *reinterpret_cast<uint4*>(smem + kOffQ + o_hi) = q8[i];
+          if (kParts == 2) *reinterpret_cast<uint4*>(smem + kOffQ + o_lo) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+      return;
+    }
     const float4* qa = reinterpret_cast<const float4*>(static_cast<const float*>(p.q_abs) +
                                                        (size_t(v) * p.H + h0) * kDc);
     const float4* qp = reinterpret_cast<const float4*>(static_cast<const float*>(p.q_pe) +
@@ -500,6 +546,40 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     }
     fence_proxy_async_smem();
   };
+  // Paged cache, ring A (whole warp): a 128-row box is `pieces` boxes of
+  // `box_rows` rows; lane i < pieces knows the pool row of piece i.
+  const int box_rows = kPaged ? min(1 << p.page_shift, kTileRows) : kTileRows;
+  const int pieces = kTileRows / box_rows;
+  // Pool row of this lane's piece (of `rows` rows) of the tile at row r of query
+  // group v's sequence, which ends at row len.
+  auto piece_row = [&](int v, int r, int len, int rows) {
+    return paged_row(p, cache_seq(p, v), r + lane * rows, lane * rows < kTileRows ? len : 0);
+  };
+  auto paged_box = [&](uint32_t dst, int column, int row, uint32_t full) {
+    if (lane < pieces)
+      tma_load_2d(dst + lane * box_rows * 128, &tmap, column, row, full, keep);
+  };
+  int row_a = 0;   // this lane's piece of the tile ring A is at
+  auto paged_fills = [&](int from, int to) {
+    if (lane == 0) {
+      if (from == 0) {
+        for (int i = 0; i < kSlotsA; ++i) {
+          mbar_init(bar(BAR_FULLA + i), 1);
+          mbar_init(bar(BAR_EMPTYA + i), 1);
+        }
+        fence_mbarrier_init();
+        prefetch_tmap(&tmap);
+      }
+      for (int pos = from; pos < to; ++pos) mbar_arrive_expect_tx(bar(BAR_FULLA + pos), kBoxBytes);
+    }
+    __syncwarp();
+    for (int pos = from; pos < to; ++pos)
+      paged_box(sbase + kOffA + pos * kBoxBytes, 64 * pos, row_a, bar(BAR_FULLA + pos));
+  };
+  // The rows of an item's sequence: where its last tile's dead rows begin.
+  auto item_end = [&](const SplitItem& m) {
+    return m.row0 + (m.tiles - 1) * kTileRows + m.zero_from;
+  };
   const bool ring_a = warp == kWarpA && lane == 0;
   int len_first = 0, len_pair = 0;   // paired tokens: rows of the earlier and later token
   int r0_one = 0;                    // one-item CTA: the chunk's first row in its sequence
@@ -514,19 +594,27 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     // issued the query's loads (named barrier 3), so that those do not queue
     // behind every CTA's first-fill burst.
     if (warp == kWarpA) {
-      if (lane == 0) first_fills(items[0].row0, 0, 2);
+      if (kPaged) {
+        row_a = piece_row(qv0, items[0].row0, item_end(items[0]), box_rows);
+        paged_fills(0, 2);
+      } else if (lane == 0) {
+        first_fills(items[0].row0, 0, 2);
+      }
       __syncwarp();
       named_bar_sync(3, kSoftThreads + 32);
-      if (lane == 0) first_fills(items[0].row0, 2, kSlotsA);
+      if (kPaged)
+        paged_fills(2, kSlotsA);
+      else if (lane == 0)
+        first_fills(items[0].row0, 2, kSlotsA);
     }
   } else {
     const int g = blockIdx.x, j = blockIdx.y, b = pair ? 2 * blockIdx.z : blockIdx.z;
     const int r0 = j * p.chunk;
     r0_one = r0;
-    const int row_base = cache_seq(p, b) * p.s_max + r0;
+    const int row_base = kPaged ? r0 : cache_seq(p, b) * p.s_max + r0;
     qv0 = b;
     qh0 = g * (pair ? kHeadGroup / 2 : kHeadGroup);
-    if (ring_a && p.fill_early) first_fills(row_base);
+    if (!kPaged && ring_a && p.fill_early) first_fills(row_base);
     // Launched after mla_absorb_q with programmatic serialization: everything up
     // to the query load (set-up, TMEM, the cache stream) overlaps that kernel.
     const int len = clamp_length(p, pair ? b + 1 : b, tid == 0 && g == 0 && j == 0);
@@ -535,11 +623,16 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     if (r0 >= len) {
       // Chunk past the end of this sequence: nothing to do once early copies
       // (into this CTA's shared memory) have landed.
-      if (ring_a && p.fill_early)
+      if (!kPaged && ring_a && p.fill_early)
         for (int pos = 0; pos < kSlotsA; ++pos) mbar_wait_bounded(bar(BAR_FULLA + pos), 0);
       return;
     }
-    if (ring_a && !p.fill_early) first_fills(row_base);
+    if (kPaged && warp == kWarpA) {
+      row_a = piece_row(b, r0, len, box_rows);
+      paged_fills(0, kSlotsA);
+    } else if (ring_a && !p.fill_early) {
+      first_fills(row_base);
+    }
     if (tid == 0) {
       // The last tile may reach past the chunk into the next chunk's rows (finite
       // cache data; their scores are masked) and past the sequence's end, where
@@ -687,7 +780,120 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   };
 
 
-  if (warp == kWarpA) {
+  if (kPaged && warp == kWarpA) {
+    // ------------------------------------------------------------ ring A, paged
+    int issued = kSlotsA;
+    Cursor c{0, items[0].tiles};
+    bool go = true;
+    for (int t = 0; t < T && go; ++t) {
+      if (p.stop_after_tiles > 0 && t >= p.stop_after_tiles) break;   // test hook
+      // The next tile's pages, asked for while this tile's boxes go out.
+      int row_next = 0;
+      if (t + 1 < T) {
+        seek(c, t + 1);
+        row_next = piece_row(items[c.i].qv, row_of(c, t + 1), item_end(items[c.i]), box_rows);
+      }
+      for (int k = 0; k < 9 && go; ++k) {
+        const int pos = 9 * t + k, sl = pos % kSlotsA, use = pos / kSlotsA;
+        if (pos < kSlotsA) continue;   // issued before the CTA-wide barrier
+        if (lane == 0) {
+          go = !*abort_flag &&
+               wait_or_abort(bar(BAR_EMPTYA + sl), (use - 1) & 1, abort_flag, wait_ns);
+          if (go) mbar_arrive_expect_tx(bar(BAR_FULLA + sl), kBoxBytes);
+        }
+        go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) break;
+        paged_box(sbase + kOffA + sl * kBoxBytes, 64 * box_at(t, k), row_a, bar(BAR_FULLA + sl));
+        issued = pos + 1;
+      }
+      row_a = row_next;
+    }
+    if (lane == 0 && *abort_flag)
+      for (int pos = issued > kSlotsA ? issued - kSlotsA : 0; pos < issued; ++pos)
+        drain_phase(bar(BAR_FULLA + pos % kSlotsA), (pos / kSlotsA) & 1, wait_ns);
+  } else if (kPaged && warp == kWarpB) {
+    // ------------------------------------------------------------ ring B, paged
+    // A tile is np pieces of brows rows of one page; lane i < np knows the pool
+    // row of piece i.  The order of the requests is the dense cache's (below).
+    const int brows = min(1 << p.page_shift, kTileRows / 2), np = kTileRows / brows;
+    const uint64_t stream = l2_evict_first_policy();
+    if (lane == 0) prefetch_tmap(&tmap_half);
+    int issued = 0;
+    uint32_t armed_x = 0;
+    Cursor c{0, items[0].tiles};
+    bool go = true;
+    // Lane 0 waits; the answer goes to the whole warp.
+    auto ready = [&](bool wait, uint32_t b, uint32_t parity) {
+      int ok = 1;
+      if (lane == 0) ok = !*abort_flag && (!wait || wait_or_abort(b, parity, abort_flag, wait_ns));
+      go = __shfl_sync(0xffffffffu, ok, 0) != 0;
+      return go;
+    };
+    auto arm = [&](uint32_t b, uint32_t bytes) {
+      if (lane == 0) mbar_arrive_expect_tx(b, bytes);
+      __syncwarp();
+    };
+    // 128 rows of latent box k of the tile whose pieces start at `row`.
+    auto whole_box = [&](uint32_t dst, int k, int row, uint32_t full) {
+      if (lane < np) tma_load_2d(dst + lane * brows * 128, &tmap_half, 64 * k, row, full, stream);
+    };
+    // Row half kh of latent boxes 2 mb and 2 mb + 1: np / 2 pieces of each.
+    auto half_pair = [&](uint32_t dst, int mb, int kh, int row, uint32_t full) {
+      const int i = lane & (np / 2 - 1), h = lane / (np / 2);
+      const int r = __shfl_sync(0xffffffffu, row, kh * (np / 2) + i);
+      if (lane < np)
+        tma_load_2d(dst + h * kHalfBox + i * brows * 128, &tmap_half, 64 * (2 * mb + h), r, full,
+                    stream);
+    };
+    int row_b = piece_row(items[0].qv, items[0].row0, item_end(items[0]), brows);
+    for (int t = 0; t < T && go; ++t) {
+      int row_next = 0;
+      if (t + 1 < T) {
+        seek(c, t + 1);
+        row_next = piece_row(items[c.i].qv, row_of(c, t + 1), item_end(items[c.i]), brows);
+      }
+      if (kResidentTail && t == T - 1) {
+        if (!ready(true, bar(BAR_LASTA), 0)) break;
+        bool second = false;
+        for (int k = 0; k < 8; ++k) {
+          if (tail_res(k >> 1)) continue;
+          if (k >= 2 && !second) {
+            if (T >= 2 && !ready(true, bar(BAR_PVPREV), 0)) break;
+            second = true;
+          }
+          arm(bar(BAR_FULLX + k), kBoxBytes);
+          whole_box(sbase + tail_box_off(k), k, row_b, bar(BAR_FULLX + k));
+          armed_x |= 1u << k;
+        }
+        break;
+      }
+      bool lasta = false;
+      for (int u = 0; u < 8 && go; ++u) {
+        const int mb = u & 3, kh = u >> 2;
+        if (borrowed(t, u)) {
+          const int x = borrow_x(u);
+          if (!ready(!lasta, bar(BAR_LASTA), 0)) break;
+          lasta = true;
+          arm(bar(BAR_FULLX + x), 2 * kHalfBox);
+          half_pair(sbase + borrow_off(x), mb, kh, row_b, bar(BAR_FULLX + x));
+          armed_x |= 1u << x;
+          continue;
+        }
+        const int pos = 8 * t + u, sl = pos % kSlotsB, use = pos / kSlotsB;
+        if (!ready(use > 0, bar(BAR_EMPTYB + sl), (use - 1) & 1)) break;
+        arm(bar(BAR_FULLB + sl), 2 * kHalfBox);
+        half_pair(sbase + kOffB + 2 * sl * kHalfBox, mb, kh, row_b, bar(BAR_FULLB + sl));
+        issued = pos + 1;
+      }
+      row_b = row_next;
+    }
+    if (lane == 0 && *abort_flag) {
+      for (int pos = issued > kSlotsB ? issued - kSlotsB : 0; pos < issued; ++pos)
+        drain_phase(bar(BAR_FULLB + pos % kSlotsB), (pos / kSlotsB) & 1, wait_ns);
+      for (int k = 0; k < 8; ++k)
+        if (armed_x >> k & 1u) drain_phase(bar(BAR_FULLX + k), 0, wait_ns);
+    }
+  } else if (!kPaged && warp == kWarpA) {
     // ------------------------------------------------------------ ring A (HBM)
     if (lane == 0) {
       int issued = kSlotsA;   // stream positions issued so far (the first fills included)
@@ -713,7 +919,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
         for (int pos = issued > kSlotsA ? issued - kSlotsA : 0; pos < issued; ++pos)
           drain_phase(bar(BAR_FULLA + pos % kSlotsA), (pos / kSlotsA) & 1, wait_ns);
     }
-  } else if (warp == kWarpB) {
+  } else if (!kPaged && warp == kWarpB) {
     // ------------------------------------------------------------ ring B (L2)
     if (lane == 0) {
       prefetch_tmap(&tmap_half);
@@ -1346,6 +1552,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
 
 // fp32 path: one CTA per (head, chunk, sequence); each warp runs its own online
 // softmax over every fourth row, then the four warp states are merged.
+template <bool kPaged>
 __global__ void __launch_bounds__(kThreads)
     split_f32_kernel(const SplitParams p) {
   const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
@@ -1369,12 +1576,19 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   for (int t = r0 + warp; t < r1; t += kWarps) {
-    const float* row = cache + (size_t(cache_seq(p, b)) * p.s_max + t) * kRow;
+    size_t at = size_t(cache_seq(p, b)) * p.s_max + t;
+    bool there = true;
+    if (kPaged) {   // rows of a page that does not exist read as zeros
+      const int id = page_of(p, cache_seq(p, b), t);
+      there = id >= 0;
+      at = (size_t(there ? id : 0) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+    }
+    const float* row = cache + at * kRow;
     float c[18];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 18; ++i) {
-      c[i] = row[lane + 32 * i];
+      c[i] = !kPaged || there ? row[lane + 32 * i] : 0.f;
       dot = fmaf(q[i], c[i], dot);
     }
 #pragma unroll
@@ -1419,18 +1633,26 @@ __global__ void __launch_bounds__(kThreads)
 // every load of a group in flight at once; a running maximum keeps the weights
 // finite (each thread recomputes the group's weights itself, so there is no
 // shared memory and no barrier).
+// o_c is fp32, or bf16 (rounded once, here) where the caller's queries are.
+__device__ __forceinline__ void store_out4(float* dst, float4 v) {
+  *reinterpret_cast<float4*>(dst) = v;
+}
+__device__ __forceinline__ void store_out4(__nv_bfloat16* dst, float4 v) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
 constexpr int kCombineChunk = 20;
+template <typename Out>
 __global__ void __launch_bounds__(32)
-    combine_kernel(const SplitParams p, float* o_c, float* lse_out) {
+    combine_kernel(const SplitParams p, Out* o_c, float* lse_out) {
   const int h = blockIdx.x, b = blockIdx.y;
   const int tid = blockIdx.z * 32 + threadIdx.x;   // float4 column of the 512
   const int len = clamp_length(p, b, false);   // a caller input, not the split's output
   pdl_wait();   // the partials come from the split kernel just before
   int nsplit = (len + p.chunk - 1) / p.chunk;
   if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
-  float* out = o_c + (size_t(b) * p.H + h) * kDc;
+  Out* out = o_c + (size_t(b) * p.H + h) * kDc;
   if (nsplit == 0) {
-    reinterpret_cast<float4*>(out)[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    store_out4(out + 4 * tid, make_float4(0.f, 0.f, 0.f, 0.f));
     if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = -INFINITY;
     if (threadIdx.x == 0) pdl_launch_dependents();
     return;
@@ -1472,7 +1694,7 @@ __global__ void __launch_bounds__(32)
     m = cm;
   }
   const float inv = 1.f / sum;
-  reinterpret_cast<float4*>(out)[tid] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  store_out4(out + 4 * tid, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = m + logf(sum);
 }
 
@@ -1489,8 +1711,9 @@ constexpr int kCombineMaxWarps = 8;
 // and 128 chunks of 4 x 16 heads take one wave).  The warp states are merged in
 // dynamic shared memory.
 constexpr int kCombineGroup = 16;
+template <typename Out>
 __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
-    combine_warps_kernel(const SplitParams p, float* o_c, float* lse_out) {
+    combine_warps_kernel(const SplitParams p, Out* o_c, float* lse_out) {
   extern __shared__ float4 s_acc[];   // [W][32], then s_m[W], s_sum[W]
   const int h = blockIdx.x, b = blockIdx.y;
   const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1499,10 +1722,10 @@ __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
   pdl_wait();   // the partials come from the split kernel just before
   int nsplit = (len + p.chunk - 1) / p.chunk;
   if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
-  float* out = o_c + (size_t(b) * p.H + h) * kDc;
+  Out* out = o_c + (size_t(b) * p.H + h) * kDc;
   if (nsplit == 0) {
     if (warp == 0) {
-      reinterpret_cast<float4*>(out)[col] = make_float4(0.f, 0.f, 0.f, 0.f);
+      store_out4(out + 4 * col, make_float4(0.f, 0.f, 0.f, 0.f));
       if (col == 0 && lse_out) lse_out[size_t(b) * p.H + h] = -INFINITY;
     }
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -1572,7 +1795,7 @@ __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
     m = M;
   }
   const float inv = 1.f / sum;
-  reinterpret_cast<float4*>(out)[col] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  store_out4(out + 4 * col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   if (col == 0 && lse_out) lse_out[size_t(b) * p.H + h] = m + logf(sum);
 }
 
@@ -1696,9 +1919,17 @@ __global__ void __launch_bounds__(128)
 // ------------------------------------------------------------------------- host side
 // Heads per CTA of the decode kernel: 32 for a bf16 cache whose head count
 // allows it, else 16 (the FP8 kernel always takes 16).
-int tc_heads_per_cta(const mla_dims* d) {
+// A paged call's choice goes by its query type: bf16 queries are one part as
+// they stand and a bf16 output rounds more than a one-part P does, while fp32
+// queries and outputs keep the hi + lo pairs at every head count.
+struct PlanOpts {
+  bool pair = false;     // two tokens of a multi-token step per CTA
+  bool paged = false;    // a paged cache: chunks are whole tiles
+  int io = MLA_F32;      // query and output type of a paged call
+};
+int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
   if (d->dtype != MLA_BF16) return kHeadGroup;
-  if (d->heads % 64 == 0 && g_split_parts.load() != 2) return 64;
+  if (d->heads % 64 == 0 && g_split_parts.load() != 2 && !(o.paged && o.io != MLA_BF16)) return 64;
   return d->heads % 32 == 0 ? 32 : kHeadGroup;
 }
 
@@ -1710,14 +1941,14 @@ bool pair_tokens(const mla_dims* cache_dims, int q_len) {
   return cache_dims->dtype == MLA_BF16 && cache_dims->heads % 32 != 0 && q_len % 2 == 0;
 }
 
-template <int kG, bool kPersist>
+template <int kG, bool kPersist, bool kPaged = false>
 mla_status launch_split_tc(const CUtensorMap& tmap, const CUtensorMap& tmap_half,
                            const SplitParams& p, int heads, cudaStream_t s, const char* who) {
   using L = TcPlan<kG, kPersist>;
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_tc_kernel<kG, kPersist>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(split_tc_kernel<kG, kPersist, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(L::kSmem)) != cudaSuccess) {
       set_error("%s: cannot reserve %zu bytes of shared memory", who, L::kSmem);
       return MLA_ERR_CUDA;
@@ -1740,7 +1971,7 @@ mla_status launch_split_tc(const CUtensorMap& tmap, const CUtensorMap& tmap_half
   // 70.4 us with the early fetch everywhere).
   SplitParams q = p;
   q.fill_early = !p.persist && static_cast<long long>(grid.x) * grid.y * grid.z <= sms;
-  launch_pdl(split_tc_kernel<kG, kPersist>, grid, dim3(L::kThreads), L::kSmem, s, tmap, tmap_half, q);
+  launch_pdl(split_tc_kernel<kG, kPersist, kPaged>, grid, dim3(L::kThreads), L::kSmem, s, tmap, tmap_half, q);
   return MLA_OK;
 }
 // How the split kernel cuts the rows: chunk rows, chunks per sequence, and
@@ -1783,46 +2014,52 @@ int device_sms() {
 //    again, about 56 rows' worth of traffic and epilogue; measured on 64 ragged
 //    sequences: 16 chunks of 512 rows beat 22 of 384), and the combine's cost
 //    per chunk.
-SplitPlan plan_split_compute(const mla_dims* d, int requested, bool pair, long long sms);
+SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& opts,
+                             long long sms);
 
 // plan_split is a pure function of the dims, the request, the pairing, the two
 // process-wide switches and the SM count; a decode step asks for it twice per
 // call, and the search over chunk counts is the larger part of the step's host
 // work (measured: 19.6 us of host time per mla_decode_step call with it, from
 // Python with prepared arguments), so each thread keeps its last few answers.
-SplitPlan plan_split(const mla_dims* d, int requested, bool pair = false) {
+SplitPlan plan_split(const mla_dims* d, int requested, const PlanOpts& opts = {}) {
+  constexpr int kKeys = 11;
   struct Entry {
-    int key[9];
+    int key[kKeys];
     SplitPlan plan;
   };
   constexpr int kEntries = 8;
   thread_local Entry memo[kEntries];
   thread_local int filled = 0, next = 0;
   const long long sms = device_sms();
-  const int key[9] = {d->batch, d->heads, d->s_max, d->dtype, requested, pair ? 1 : 0,
-                      g_split_form.load(), g_split_parts.load(), static_cast<int>(sms)};
+  const int key[kKeys] = {d->batch, d->heads, d->s_max, d->dtype, requested, opts.pair ? 1 : 0,
+                          g_split_form.load(), g_split_parts.load(), static_cast<int>(sms),
+                          opts.paged ? 1 : 0, opts.io};
   for (int i = 0; i < filled; ++i) {
     bool same = true;
-    for (int k = 0; k < 9; ++k) same = same && memo[i].key[k] == key[k];
+    for (int k = 0; k < kKeys; ++k) same = same && memo[i].key[k] == key[k];
     if (same) return memo[i].plan;
   }
-  const SplitPlan plan = plan_split_compute(d, requested, pair, sms);
+  const SplitPlan plan = plan_split_compute(d, requested, opts, sms);
   Entry& e = memo[next];
-  for (int k = 0; k < 9; ++k) e.key[k] = key[k];
+  for (int k = 0; k < kKeys; ++k) e.key[k] = key[k];
   e.plan = plan;
   next = (next + 1) % kEntries;
   if (filled < kEntries) ++filled;
   return plan;
 }
 
-SplitPlan plan_split_compute(const mla_dims* d, int requested, bool pair, long long sms) {
+SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& opts,
+                             long long sms) {
   const int S = d->s_max;
-  const int max_splits = (S + kChunkAlign - 1) / kChunkAlign;
+  const bool pair = opts.pair;
   const bool tiled = d->dtype != MLA_F32;   // bf16 and FP8 kernels: one CTA per SM
-  const long long groups = d->dtype == MLA_F32 ? d->heads : d->heads / tc_heads_per_cta(d);
+  const int np_align = opts.paged && tiled ? kTileRows : kChunkAlign;
+  const int max_splits = (S + np_align - 1) / np_align;
+  const long long groups = d->dtype == MLA_F32 ? d->heads : d->heads / tc_heads_per_cta(d, opts);
   const long long per_split = pair ? static_cast<long long>(d->batch) * d->heads / 32
                                    : static_cast<long long>(d->batch) * groups;
-  const bool can_persist = d->dtype == MLA_BF16 && !pair && tc_heads_per_cta(d) == 16;
+  const bool can_persist = d->dtype == MLA_BF16 && !pair && tc_heads_per_cta(d, opts) == 16;
   const long long slots = tiled ? sms : 4ll * sms;
   auto chunk_of = [&](int s, int align) {
     return ((S + s - 1) / s + align - 1) / align * align;
@@ -1834,7 +2071,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, bool pair, long l
     double& best = np_cost;
     const int lo = requested > 0 ? requested : 1, hi = requested > 0 ? requested : max_splits;
     for (int s = lo; s <= hi && s <= max_splits; ++s) {
-      const int chunk = chunk_of(s, kChunkAlign);
+      const int chunk = chunk_of(s, np_align);
       const int s_eff = (S + chunk - 1) / chunk;
       if (requested <= 0 && s_eff != s) continue;
       const long long waves = (per_split * s_eff + slots - 1) / slots;
@@ -1846,8 +2083,8 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, bool pair, long l
         np_splits = s_eff;
       }
     }
-    if (np_chunk == 0) {   // more chunks requested than row groups: one per 8 rows
-      np_chunk = kChunkAlign;
+    if (np_chunk == 0) {   // more chunks requested than row groups: one per 8 rows (or tile)
+      np_chunk = np_align;
       np_splits = (S + np_chunk - 1) / np_chunk;
     }
   }
@@ -1884,8 +2121,8 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, bool pair, long l
   return {p_chunk, p_splits, true};
 }
 
-int chunk_rows(const mla_dims* d, int requested, int* splits_out, bool pair = false) {
-  const SplitPlan pl = plan_split(d, requested, pair);
+int chunk_rows(const mla_dims* d, int requested, int* splits_out, const PlanOpts& opts = {}) {
+  const SplitPlan pl = plan_split(d, requested, opts);
   *splits_out = pl.splits;
   return pl.chunk;
 }
@@ -1953,7 +2190,7 @@ extern "C" int32_t mla_decode_multi_num_splits(const mla_dims* dims, int32_t q_l
   mla_dims qd = *dims;
   qd.batch = dims->batch * q_len;
   int splits = 0;
-  chunk_rows(&qd, requested, &splits, pair_tokens(dims, q_len));
+  chunk_rows(&qd, requested, &splits, PlanOpts{pair_tokens(dims, q_len)});
   return splits;
 }
 
@@ -1963,7 +2200,7 @@ extern "C" size_t mla_decode_multi_workspace_bytes(const mla_dims* dims, int32_t
   mla_dims qd = *dims;
   qd.batch = dims->batch * q_len;
   int splits = 0;
-  chunk_rows(&qd, requested, &splits, pair_tokens(dims, q_len));
+  chunk_rows(&qd, requested, &splits, PlanOpts{pair_tokens(dims, q_len)});
   return workspace_bytes(&qd, splits);
 }
 
@@ -2001,6 +2238,22 @@ extern "C" void mla_test_set_split_hooks(uint64_t wait_ns, int32_t stop_after_ti
   g_hook_stop_tiles.store(stop_after_tiles > 0 ? stop_after_tiles : 0);
 }
 
+// The cache of a paged call: its pool's shape, the block table and the query
+// and output type.
+struct PagedView {
+  const mla_paging* paging;
+  const int32_t* table;
+  int io;
+};
+
+static PlanOpts plan_opts(const mla_dims* dims, int q_len, const PagedView* view) {
+  PlanOpts o;
+  o.pair = pair_tokens(dims, q_len);
+  o.paged = view != nullptr;
+  o.io = view ? view->io : MLA_F32;
+  return o;
+}
+
 // Validates the arguments shared by the split and combine halves and fills the
 // kernel parameters.  `dims` describes the cache (dims->batch sequences); with
 // q_len query tokens per sequence the queries, partials and outputs have
@@ -2009,14 +2262,16 @@ extern "C" void mla_test_set_split_hooks(uint64_t wait_ns, int32_t stop_after_ti
 static mla_status prepare(const char* who, const mla_dims* dims, int q_len, const void* q_abs,
                           const void* q_pe, const void* cache, const int32_t* lengths,
                           float softmax_scale, int32_t num_splits, void* workspace,
-                          size_t ws_bytes, int32_t* dev_status, SplitParams* p) {
+                          size_t ws_bytes, int32_t* dev_status, SplitParams* p,
+                          const PagedView* view = nullptr) {
   mla_status st = check_dims(dims, who);
   if (st != MLA_OK) return st;
   if (q_len < 1 || static_cast<long long>(dims->batch) * q_len > (1ll << 30)) {
     set_error("%s: q_len=%d must be >= 1 with batch*q_len <= 2^30", who, q_len);
     return MLA_ERR_INVALID_ARG;
   }
-  const bool pair = pair_tokens(dims, q_len);
+  const PlanOpts opts = plan_opts(dims, q_len, view);
+  const bool pair = opts.pair;
   mla_dims qd = *dims;   // one row of queries per (sequence, token)
   qd.batch = dims->batch * q_len;
   dims = &qd;
@@ -2036,7 +2291,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
     set_error("%s: num_splits must be >= 0", who);
     return MLA_ERR_INVALID_ARG;
   }
-  const SplitPlan plan = plan_split(dims, num_splits, pair);
+  const SplitPlan plan = plan_split(dims, num_splits, opts);
   const int splits = plan.splits, chunk = plan.chunk;
   const size_t need = workspace_bytes(dims, splits);
   if (ws_bytes < need) {
@@ -2068,6 +2323,11 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   p->wait_ns = g_hook_wait_ns.load();
   p->debug = g_hook_debug.load();
   p->stop_after_tiles = g_hook_stop_tiles.load();
+  p->table = view ? view->table : nullptr;
+  p->table_stride = view ? view->paging->table_stride : 0;
+  p->page_shift = view ? page_shift_of(view->paging) : 0;
+  p->num_pages = view ? view->paging->num_pages : 0;
+  p->io_bf16 = view && view->io == MLA_BF16 ? 1 : 0;
   return MLA_OK;
 }
 
@@ -2076,14 +2336,14 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
                                const void* q_abs, const void* q_pe, const void* cache,
                                const int32_t* lengths, float softmax_scale, int32_t num_splits,
                                void* workspace, size_t ws_bytes, int32_t* dev_status,
-                               void* stream) {
+                               void* stream, const PagedView* view = nullptr) {
   if (!q_abs || !q_pe || !cache) {
     set_error("%s: a required pointer is NULL", who);
     return MLA_ERR_INVALID_ARG;
   }
   SplitParams p;
   mla_status st = prepare(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
-                          num_splits, workspace, ws_bytes, dev_status, &p);
+                          num_splits, workspace, ws_bytes, dev_status, &p, view);
   if (st != MLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
@@ -2099,12 +2359,16 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
     // promoted to 256 bytes (a row's next box comes with it from HBM); the PV
     // pass re-reads rows already in L2 and asks for 128 bytes at a time
     // (measured: 256-byte promotion there costs 1.5 % on the large caches).
+    // A paged cache's boxes stay inside a page.
     CUtensorMap tmap, tmap_half;
-    const cuuint64_t gdim[2] = {cuuint64_t(kRow), cuuint64_t(dims->batch) * dims->s_max};
+    const cuuint64_t gdim[2] = {cuuint64_t(kRow), view_rows(p)};
     const cuuint64_t gstride[1] = {cuuint64_t(kRow) * 2};
     const cuuint32_t estride[2] = {1, 1};
     for (int v = 0; v < 2; ++v) {
-      const cuuint32_t box[2] = {64, cuuint32_t(v == 0 ? kTileRows : kTileRows / 2)};
+      const int rows = v == 0 ? kTileRows : kTileRows / 2;
+      const cuuint32_t box[2] = {64, cuuint32_t(view && view->paging->page_size < rows
+                                                    ? view->paging->page_size
+                                                    : rows)};
       CUresult r = enc(v == 0 ? &tmap : &tmap_half, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                        const_cast<void*>(cache), gdim, gstride, box, estride,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -2116,39 +2380,56 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
         return MLA_ERR_CUDA;
       }
     }
-    const int per_cta = p.tpc == 2 ? 32 : tc_heads_per_cta(dims);
-    st = per_cta == 64   ? launch_split_tc<64, false>(tmap, tmap_half, p, dims->heads, s, who)
+    const int per_cta = p.tpc == 2 ? 32 : tc_heads_per_cta(dims, plan_opts(dims, q_len, view));
+    if (view)
+      st = per_cta == 64   ? launch_split_tc<64, false, true>(tmap, tmap_half, p, dims->heads, s, who)
+           : per_cta == 32 ? launch_split_tc<32, false, true>(tmap, tmap_half, p, dims->heads, s, who)
+           : p.persist     ? launch_split_tc<16, true, true>(tmap, tmap_half, p, dims->heads, s, who)
+                           : launch_split_tc<16, false, true>(tmap, tmap_half, p, dims->heads, s, who);
+    else
+      st = per_cta == 64   ? launch_split_tc<64, false>(tmap, tmap_half, p, dims->heads, s, who)
          : per_cta == 32 ? launch_split_tc<32, false>(tmap, tmap_half, p, dims->heads, s, who)
          : p.persist     ? launch_split_tc<16, true>(tmap, tmap_half, p, dims->heads, s, who)
                          : launch_split_tc<16, false>(tmap, tmap_half, p, dims->heads, s, who);
     if (st != MLA_OK) return st;
   } else {
     dim3 grid(dims->heads, p.splits, p.B);
-    split_f32_kernel<<<grid, kThreads, 0, s>>>(p);
+    if (view)
+      split_f32_kernel<true><<<grid, kThreads, 0, s>>>(p);
+    else
+      split_f32_kernel<false><<<grid, kThreads, 0, s>>>(p);
   }
   return launch_status(who);
 }
 
+template <typename Out>
+static void launch_combine(const SplitParams& p, int heads, Out* o_c, float* lse,
+                           cudaStream_t s) {
+  const int cw = combine_warps(p.splits);
+  if (cw == 1)
+    launch_pdl(combine_kernel<Out>, dim3(heads, p.B, kDc / 128), dim3(32), 0, s, p, o_c, lse);
+  else
+    launch_pdl(combine_warps_kernel<Out>, dim3(heads, p.B, kDc / 128), dim3(32 * cw),
+               size_t(cw) * (32 * sizeof(float4) + 2 * sizeof(float)), s, p, o_c, lse);
+}
+
 static mla_status decode_combine(const char* who, const mla_dims* dims, int q_len,
                                  const int32_t* lengths, int32_t num_splits,
-                                 const void* workspace, size_t ws_bytes, float* o_c, float* lse,
-                                 void* stream) {
+                                 const void* workspace, size_t ws_bytes, void* o_c, float* lse,
+                                 void* stream, const PagedView* view = nullptr) {
   if (!o_c || !aligned16(o_c)) {
     set_error("%s: o_c must be a non-NULL 16-byte aligned pointer", who);
     return MLA_ERR_INVALID_ARG;
   }
   SplitParams p;
   mla_status st = prepare(who, dims, q_len, nullptr, nullptr, nullptr, lengths, 1.f, num_splits,
-                          const_cast<void*>(workspace), ws_bytes, nullptr, &p);
+                          const_cast<void*>(workspace), ws_bytes, nullptr, &p, view);
   if (st != MLA_OK) return st;
-  const int cw = combine_warps(p.splits);
-  if (cw == 1)
-    launch_pdl(combine_kernel, dim3(dims->heads, p.B, kDc / 128), dim3(32), 0,
-               static_cast<cudaStream_t>(stream), p, o_c, lse);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.io_bf16)
+    launch_combine(p, dims->heads, static_cast<__nv_bfloat16*>(o_c), lse, s);
   else
-    launch_pdl(combine_warps_kernel, dim3(dims->heads, p.B, kDc / 128), dim3(32 * cw),
-               size_t(cw) * (32 * sizeof(float4) + 2 * sizeof(float)),
-               static_cast<cudaStream_t>(stream), p, o_c, lse);
+    launch_combine(p, dims->heads, static_cast<float*>(o_c), lse, s);
   return launch_status(who);
 }
 
@@ -2206,6 +2487,94 @@ extern "C" mla_status mla_decode_attn(const mla_dims* dims, const void* q_abs, c
     return st;
   }
   return mla_decode_combine(dims, lengths, num_splits, workspace, ws_bytes, o_c, lse, stream);
+}
+
+// ---------------------------------------------------------------- paged cache
+// Checks that a paged call makes beyond prepare()'s.
+mla_status mla::check_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
+                            int32_t io_dtype, int32_t q_len) {
+  mla_status st = check_dims(dims, who);
+  if (st == MLA_OK) st = check_paging(paging, who);
+  if (st == MLA_OK) st = check_io(dims, io_dtype, who);
+  if (st != MLA_OK) return st;
+  if (dims->s_max > static_cast<long long>(paging->table_stride) * paging->page_size) {
+    set_error("%s: s_max=%d rows do not fit a table of %d pages of %d rows", who, dims->s_max,
+              paging->table_stride, paging->page_size);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (q_len < 1) {
+    set_error("%s: q_len=%d must be >= 1", who, q_len);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(dims->batch) * q_len > 65535) {
+    set_error("%s: batch*q_len=%lld exceeds 65535", who,
+              static_cast<long long>(dims->batch) * q_len);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  return MLA_OK;
+}
+
+extern "C" int32_t mla_paged_num_splits(const mla_dims* dims, const mla_paging* paging,
+                                        int32_t io_dtype, int32_t q_len, int32_t requested) {
+  if (check_paged("mla_paged_num_splits", dims, paging, io_dtype, q_len) != MLA_OK) return 0;
+  const PagedView view{paging, nullptr, io_dtype};
+  mla_dims qd = *dims;
+  qd.batch = dims->batch * q_len;
+  int splits = 0;
+  chunk_rows(&qd, requested, &splits, plan_opts(dims, q_len, &view));
+  return splits;
+}
+
+extern "C" size_t mla_paged_workspace_bytes(const mla_dims* dims, const mla_paging* paging,
+                                            int32_t io_dtype, int32_t q_len, int32_t requested) {
+  const int splits = mla_paged_num_splits(dims, paging, io_dtype, q_len, requested);
+  if (splits == 0) return 0;
+  mla_dims qd = *dims;
+  qd.batch = dims->batch * q_len;
+  return workspace_bytes(&qd, splits);
+}
+
+static mla_status check_attn(const char* who, const mla_dims* dims, const PagedView& view,
+                             int q_len, const void* q_abs, const void* q_pe, const void* cache,
+                             const int32_t* lengths, float softmax_scale, int32_t num_splits,
+                             void* workspace, size_t ws_bytes, void* o_c) {
+  mla_status st = check_paged(who, dims, view.paging, view.io, q_len);
+  if (st != MLA_OK) return st;
+  if (!q_abs || !q_pe || !cache || !view.table || !o_c || !aligned16(o_c)) {
+    set_error("%s: pointers must not be NULL, o_c 16-byte aligned", who);
+    return MLA_ERR_INVALID_ARG;
+  }
+  SplitParams p;
+  return prepare(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
+                 workspace, ws_bytes, nullptr, &p, &view);
+}
+
+mla_status mla::check_attn_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
+                                 int32_t io_dtype, const void* q_abs, const void* q_pe,
+                                 const void* cache, const int32_t* block_table,
+                                 const int32_t* lengths, float softmax_scale, int32_t num_splits,
+                                 void* workspace, size_t ws_bytes, void* o_c) {
+  return check_attn(who, dims, PagedView{paging, block_table, io_dtype}, 1, q_abs, q_pe, cache,
+                    lengths, softmax_scale, num_splits, workspace, ws_bytes, o_c);
+}
+
+extern "C" mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
+                                            int32_t io_dtype, int32_t q_len, const void* q_abs,
+                                            const void* q_pe, const void* cache,
+                                            const int32_t* block_table, const int32_t* lengths,
+                                            float softmax_scale, int32_t num_splits,
+                                            void* workspace, size_t ws_bytes, void* o_c,
+                                            float* lse, int32_t* dev_status, void* stream) {
+  const char* who = "mla_decode_attn_paged";
+  const PagedView view{paging, block_table, io_dtype};
+  mla_status st = check_attn(who, dims, view, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
+                             num_splits, workspace, ws_bytes, o_c);
+  if (st != MLA_OK) return st;
+  st = decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
+                    workspace, ws_bytes, dev_status, stream, &view);
+  if (st != MLA_OK) return st;
+  return decode_combine(who, dims, q_len, lengths, num_splits, workspace, ws_bytes, o_c, lse,
+                        stream, &view);
 }
 
 // Largest batch x heads for which mla_decode_step fuses the combine with W_UV.

@@ -146,7 +146,13 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
   const size_t bh = size_t(b) * p.H + h;
   const int c = 4 * t;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < kRow)
+  if (c < kRow && p.io_bf16) {
+    const uint2 q2 = *reinterpret_cast<const uint2*>(
+        c < kDc ? static_cast<const __nv_bfloat16*>(p.q_abs) + bh * kDc + c
+                : static_cast<const __nv_bfloat16*>(p.q_pe) + bh * kDr + (c - kDc));
+    v = make_float4(__uint_as_float(q2.x << 16), __uint_as_float(q2.x & 0xffff0000u),
+                    __uint_as_float(q2.y << 16), __uint_as_float(q2.y & 0xffff0000u));
+  } else if (c < kRow)
     v = c < kDc ? *reinterpret_cast<const float4*>(static_cast<const float*>(p.q_abs) + bh * kDc + c)
                 : *reinterpret_cast<const float4*>(static_cast<const float*>(p.q_pe) + bh * kDr +
                                                    (c - kDc));
@@ -183,6 +189,9 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
   }
 }
 
+// kPaged: the cache is a pool of pages; a tile's boxes are boxes of up to 128
+// rows of one page each, one lane of the producer warp per page.
+template <bool kPaged>
 __global__ void __launch_bounds__(kF8Threads, 1)
     split_fp8_kernel(const __grid_constant__ CUtensorMap tmap, const SplitParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   // the sequence are finite and get P = 0.
   const int zero_from = len - (r0 + (T - 1) * kF8Rows);
   const bool zero_last = zero_from < kF8Rows;
-  const int row_base = cache_seq(p, b) * p.s_max + r0;
+  const int row_base = kPaged ? r0 : cache_seq(p, b) * p.s_max + r0;
   const int h0 = g * kHeadGroup;
 
   // The cache stream starts first: the producer sets up the barriers and
@@ -224,6 +233,30 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       tma_load_2d(sbase + kOffTile + bf * kF8Tile + m * kF8Box, &tmap, 128 * m,
                   row_base + t * kF8Rows, bar(B_FULL + bf), pol);
   };
+  // Paged: lane i < pieces issues the boxes of piece i of the tile, whose first
+  // pool row is `row`.
+  const int box_rows = kPaged ? min(1 << p.page_shift, kF8Rows) : kF8Rows;
+  const int pieces = kF8Rows / box_rows;
+  auto piece_row = [&](int t) {
+    return paged_row(p, cache_seq(p, b), r0 + t * kF8Rows + lane * box_rows,
+                     lane * box_rows < kF8Rows ? len : 0);
+  };
+  auto issue_paged = [&](int t, int row) {
+    const int bf = t & 1;
+    if (lane == 0) mbar_arrive_expect_tx(bar(B_FULL + bf), kF8Tile);
+    __syncwarp();
+    const uint64_t pol = l2_evict_first_policy();
+    if (lane < pieces)
+#pragma unroll
+      for (int m = 0; m < kF8Boxes; ++m)
+        tma_load_2d(sbase + kOffTile + bf * kF8Tile + m * kF8Box + lane * box_rows * 128, &tmap,
+                    128 * m, row, bar(B_FULL + bf), pol);
+  };
+  int row_ahead[2] = {0, 0};   // pieces of the next tiles to issue, looked up ahead
+  if (kPaged && warp == 8) {
+    row_ahead[0] = piece_row(0);
+    row_ahead[1] = T > 1 ? piece_row(1) : 0;
+  }
   if (warp == 8 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_FULL + i), 1);
@@ -238,10 +271,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tmap(&tmap);
-    for (int t = 0; t < 2 && t < T; ++t) issue(t);
+    for (int t = 0; t < 2 && t < T && !kPaged; ++t) issue(t);
   }
   if (warp == 8) {
     __syncwarp();
+    if (kPaged) {
+      issue_paged(0, row_ahead[0]);
+      if (T > 1) issue_paged(1, row_ahead[1]);
+    }
     tmem_alloc(smem_u32(slot_ptr), kTmemCols);
   }
   tc_fence_before();
@@ -251,9 +288,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int issued = T < 2 ? T : 2;
+    int issued_paged = T < 2 ? T : 2;
+    if (kPaged) {
+      int row = T > 2 ? piece_row(2) : 0;
       for (int t = 2; t < T; ++t) {
+        const int next = t + 1 < T ? piece_row(t + 1) : 0;
+        int ok = 1;
+        if (lane == 0) ok = f8_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        issue_paged(t, row);
+        issued_paged = t + 1;
+        row = next;
+      }
+    }
+    if (lane == 0) {
+      int issued = kPaged ? issued_paged : T < 2 ? T : 2;
+      for (int t = 2; t < T && !kPaged; ++t) {
         if (!f8_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag)) break;
         issue(t);
         issued = t + 1;
@@ -550,9 +600,11 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   // The cache [B * s_max rows, 576 bytes] in 128-row x 128-byte boxes (128-byte
   // swizzle); the fifth box of a row reaches past column 576 and reads zeros.
   CUtensorMap tmap;
-  const cuuint64_t gdim[2] = {cuuint64_t(kRow), cuuint64_t(p.B / p.q_len) * p.s_max};
+  // A paged cache's boxes stay inside a page.
+  const cuuint64_t gdim[2] = {cuuint64_t(kRow), view_rows(p)};
   const cuuint64_t gstride[1] = {cuuint64_t(kRow)};
-  const cuuint32_t box[2] = {128, cuuint32_t(kF8Rows)};
+  const int page = 1 << p.page_shift;
+  const cuuint32_t box[2] = {128, cuuint32_t(p.table && page < kF8Rows ? page : kF8Rows)};
   const cuuint32_t estride[2] = {1, 1};
   CUresult r = enc(&tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), gdim,
                    gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -565,7 +617,9 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(split_fp8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kF8Smem)) != cudaSuccess ||
+        cudaFuncSetAttribute(split_fp8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(kF8Smem)) != cudaSuccess) {
       set_error("%s: cannot reserve %zu bytes of shared memory", who, kF8Smem);
       return MLA_ERR_CUDA;
@@ -574,7 +628,8 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   }
   launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
   dim3 grid(p.H / kHeadGroup, p.splits, p.B);
-  launch_pdl(split_fp8_kernel, grid, dim3(kF8Threads), kF8Smem, stream, tmap, p);
+  launch_pdl(p.table ? split_fp8_kernel<true> : split_fp8_kernel<false>, grid, dim3(kF8Threads),
+             kF8Smem, stream, tmap, p);
   return launch_status(who);
 }
 

@@ -28,7 +28,30 @@ struct SplitParams {
   unsigned long long wait_ns;   // limit of each bounded wait (0: kWaitNs)
   int stop_after_tiles;         // ring A issues only this many tiles of a chunk (0: all)
   int32_t* debug;               // where timed-out CTAs record their first failed wait
+  // Paged cache: row r of sequence b is pool row
+  // table[b * table_stride + (r >> page_shift)] * 2^page_shift + r % 2^page_shift.
+  const int32_t* table;         // NULL: a dense cache
+  int table_stride, page_shift, num_pages;
+  int io_bf16;                  // paged calls: q_abs, q_pe and o_c are bf16 (else fp32)
 };
+
+// The page that holds row r of cache sequence `seq`, or -1 (reported) when the
+// table's entry names none.  r lies inside the sequence.
+__device__ __forceinline__ int page_of(const SplitParams& p, int seq, int r) {
+  const int id = p.table[static_cast<size_t>(seq) * p.table_stride + (r >> p.page_shift)];
+  if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages)) return id;
+  report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+  return -1;
+}
+
+// First pool row of a box of rows r, r + 1, ... of one page (the box lies inside
+// the page).  Boxes past the sequence's `len` rows, and boxes of pages that do
+// not exist, start past the pool: TMA fills them with zeros.
+__device__ __forceinline__ int paged_row(const SplitParams& p, int seq, int r, int len) {
+  const int id = r < len ? page_of(p, seq, r) : -1;
+  return id < 0 ? p.num_pages << p.page_shift
+                : (id << p.page_shift) + (r & ((1 << p.page_shift) - 1));
+}
 
 // FP8 cache: the query of one (sequence, 16-head group) as the split kernel's
 // shared memory holds it -- five 128-column boxes of 64 rows (4 E4M3 parts x
@@ -62,6 +85,12 @@ __device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool re
 // It runs as two launches: the query's E4M3 image, then the split itself.
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who);
+
+// Rows a cache view holds: B / q_len sequences of s_max rows, or a pool's pages.
+inline uint64_t view_rows(const SplitParams& p) {
+  return p.table ? static_cast<uint64_t>(p.num_pages) << p.page_shift
+                 : static_cast<uint64_t>(p.B / p.q_len) * p.s_max;
+}
 
 // mla_absorb_q's work (named `who` in error messages), with the decode kernel's
 // first cache rows prefetched into L2 when pf.cache is set, and (bf16, `early`)

@@ -94,6 +94,8 @@ typedef struct mla_dims {
 #define MLA_DEV_LENGTH_OUT_OF_RANGE 1  /* some lengths[b] < 1 (< q_len) or > s_max */
 #define MLA_DEV_PIPELINE_TIMEOUT 2     /* a bounded wait in a kernel's pipeline gave up */
 #define MLA_DEV_BOUNDS 4               /* checked build: an index outside its buffer (skipped) */
+#define MLA_DEV_PAGE_OUT_OF_RANGE 8    /* paged cache: a page or slot outside the pool */
+#define MLA_DEV_POOL_EXHAUSTED 16      /* paged cache: more pages wanted than are free */
 
 /*
  * mla_absorb_q -- absorbed query and rotated RoPE query for one decode step.
@@ -431,6 +433,246 @@ mla_status mla_decode_step_multi(const mla_dims* dims, int32_t q_len, const void
                                  void* workspace, size_t workspace_bytes, float* q_abs,
                                  float* q_pe, float* o_c, float* lse, float* out,
                                  int32_t* dev_status, void* stream);
+
+/*
+ * ------------------------------------------------------------- paged cache
+ *
+ * The paged latent cache: rows live in a pool of pages of page_size rows, and
+ * a block table names the pages of each sequence, so that a sequence holds as
+ * many pages as its length needs ("Multi-Head Latent Attention" 2.1-2.2 and
+ * "Transformer and KV Cache Basics" preallocate one dense buffer per
+ * sequence; the paging of that buffer is this library's).
+ *
+ *   cache        [num_pages, page_size, d_c + d_rope] dtype: the pool.  Row t of
+ *                sequence b is row t % page_size of page
+ *                block_table[b, t / page_size]
+ *   block_table  [B, table_stride] int32 (device).  Entries past a sequence's
+ *                last page are never used and may hold anything
+ *   page_size    a power of two from 16 to 256
+ *   num_pages    pages of the pool; num_pages * page_size < 2^31
+ *   table_stride entries per row of the block table
+ *
+ * Page numbers live on the device and cannot be checked on the host.  An entry
+ * outside [0, num_pages) that a call needs sets MLA_DEV_PAGE_OUT_OF_RANGE and
+ * nothing outside the pool is touched; what each call does with it is said
+ * there.  Two sequences may share pages (a common prefix) in every call that
+ * only reads them.
+ *
+ * The paged calls read block_table and lengths (and the cache) before they wait
+ * for their predecessor on the stream, as the dense calls read lengths: a
+ * kernel of the caller that allows early launch must not write those.  No call
+ * of this section allows its successor to start early before it has finished
+ * writing, except the attention calls, which write only their outputs and
+ * workspace.
+ */
+typedef struct mla_paging {
+  int32_t page_size;      /* rows per page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages;      /* pages in the pool                     */
+  int32_t table_stride;   /* block-table entries per sequence      */
+} mla_paging;
+
+/*
+ * mla_pages_extend -- block tables and slot maps of one step, built on the GPU.
+ *
+ * Request b holds cached_lens[b] rows and gains new_lens[b] >= 0.  With
+ * have = ceil(cached / page_size) and want = ceil((cached + new) / page_size),
+ * want - have pages are taken from the free stack, requests in order:
+ * the k-th page taken is free_list[num_free - 1 - k].  Then
+ *   block_table[b, have..want-1]  the pages taken (other entries untouched)
+ *   num_free_out                  num_free less the pages taken
+ *   lengths[b]                    cached_lens[b] + new_lens[b]
+ *   row_starts[b]                 new rows of the requests before b; row_starts[B] = all
+ *   positions[t], slots[t]        of new row t (requests in order): its position in its
+ *                                 sequence, and page * page_size + position % page_size;
+ *                                 for t >= row_starts[B]: 0 and -1 (no row)
+ * All or nothing: with a negative length, a request longer than the table's
+ * row, or more than max_tokens new rows (MLA_DEV_LENGTH_OUT_OF_RANGE), or fewer
+ * free pages than wanted or num_free outside [0, num_pages]
+ * (MLA_DEV_POOL_EXHAUSTED), no page is taken, lengths = cached_lens,
+ * row_starts = 0 and every slot is -1.  A page number outside the pool (in
+ * free_list, or block_table's last page of a request) sets
+ * MLA_DEV_PAGE_OUT_OF_RANGE; slots in it are -1, and a table entry taken from
+ * such a free_list entry is -1.
+ *
+ * cached_lens, new_lens, lengths [B] int32; row_starts [B + 1] int32;
+ * slots [max_tokens] int64; positions [max_tokens] int32; free_list
+ * [num_pages] int32; num_free, num_free_out one int32 each; all on the device.
+ * lengths may be cached_lens and num_free_out may be num_free; no other outputs
+ * may overlap inputs.  1 <= batch <= 16384, max_tokens >= 1.
+ */
+mla_status mla_pages_extend(int32_t batch, const mla_paging* paging, const int32_t* cached_lens,
+                            const int32_t* new_lens, int32_t max_tokens, int32_t* block_table,
+                            const int32_t* free_list, const int32_t* num_free,
+                            int32_t* num_free_out, int32_t* lengths, int32_t* row_starts,
+                            int64_t* slots, int32_t* positions, int32_t* dev_status,
+                            void* stream);
+
+/*
+ * mla_pages_release -- finished requests give their pages back.
+ *
+ * For each b with finished[b] != 0 (in order), the ceil(lengths[b] / page_size)
+ * pages of its row are pushed on the free stack (free_list[num_free] upwards,
+ * num_free grows), its table entries become -1 and lengths[b] becomes 0.  All
+ * or nothing: a length outside the table's row
+ * (MLA_DEV_LENGTH_OUT_OF_RANGE), a page number outside the pool
+ * (MLA_DEV_PAGE_OUT_OF_RANGE) or a stack that would pass num_pages
+ * (MLA_DEV_POOL_EXHAUSTED) changes nothing.  A page shared by several requests
+ * must not be released through more than one of them.
+ *
+ * finished, lengths [B] int32; free_list [num_pages] int32; num_free one int32
+ * (lengths, block_table, free_list and num_free are changed in place).
+ */
+mla_status mla_pages_release(int32_t batch, const mla_paging* paging, const int32_t* finished,
+                             int32_t* lengths, int32_t* block_table, int32_t* free_list,
+                             int32_t* num_free, int32_t* dev_status, void* stream);
+
+/*
+ * mla_cache_append_paged -- new latent rows into their slots.
+ *
+ *   cache row slots[t], 0:d_c          = rows[t, 0:d_c]
+ *   cache row slots[t], d_c:d_c+d_rope = RoPE(rows[t, d_c:], positions[t])
+ * (rows: the output of kv_a_proj, one row per new token; the rotation is
+ *  mla_cache_append's: adjacent pairs, angle positions[t] rope_base^(-2i/d_rope),
+ *  reduced to a fraction of a turn in 64-bit fixed point.)  fp32 arithmetic;
+ * each value is rounded once to the cache's type (MLA_FP8_E4M3: to nearest even,
+ * saturating at +-448).
+ *
+ * rows [num_rows, d_c + d_rope] row_dtype: MLA_F32, or MLA_BF16 with a bf16 or
+ * FP8 cache; positions [num_rows] int32; slots [num_rows] int64 (both as
+ * mla_pages_extend writes them).  slots[t] = -1: no row.  Any other slot outside
+ * the pool sets MLA_DEV_PAGE_OUT_OF_RANGE, a negative position
+ * MLA_DEV_LENGTH_OUT_OF_RANGE; such a row is not written.  A slot named twice
+ * keeps one of its rows, or a mixture of them.  dims: dtype is the cache's;
+ * batch and s_max are only checked.  num_rows = 0 does nothing.
+ */
+mla_status mla_cache_append_paged(const mla_dims* dims, const mla_paging* paging,
+                                  int32_t num_rows, int32_t row_dtype, const void* rows,
+                                  const int32_t* positions, const int64_t* slots,
+                                  double rope_base, void* cache, int32_t* dev_status,
+                                  void* stream);
+
+/*
+ * mla_decode_attn_paged -- mla_decode_attn_multi over a paged cache.
+ *
+ * Scores, softmax, causal mask of q_len tokens per sequence, o_c and lse are
+ * those of mla_decode_attn_multi, with row t of sequence b where the block
+ * table says.  dims->batch = B sequences; dims->s_max: the longest length this
+ * call may meet (lengths above it are reported and clamped), at most
+ * table_stride * page_size; chunks are planned for it.  B * q_len <= 65535.
+ *
+ * io_dtype is the type of q_abs, q_pe and o_c:
+ *   MLA_F32   as in the dense calls (every cache type).  With a bf16 cache the
+ *             query and P enter the tensor cores as hi + lo bf16 pairs at every
+ *             head count.
+ *   MLA_BF16  bf16 queries and outputs (bf16 and FP8 caches), as a serving
+ *             engine keeps them.  The query enters as it is; P is hi + lo, or at
+ *             multiples of 64 heads one bf16 part (2^-9 relative, less than the
+ *             output's own rounding), 64 heads per CTA.
+ * lse is fp32, accumulation fp32.
+ *
+ * q_abs [B*q_len, H, d_c], q_pe [B*q_len, H, d_rope], o_c [B*q_len, H, d_c]
+ * (out) io_dtype; lse [B*q_len, H] fp32 (out, may be NULL); lengths [B] int32;
+ * workspace >= mla_paged_workspace_bytes(...) bytes.  A needed page outside the
+ * pool sets MLA_DEV_PAGE_OUT_OF_RANGE and its rows count as zeros.
+ * mla_paged_num_splits gives the chunk count used (0: invalid arguments).
+ */
+int32_t mla_paged_num_splits(const mla_dims* dims, const mla_paging* paging, int32_t io_dtype,
+                             int32_t q_len, int32_t requested);
+size_t mla_paged_workspace_bytes(const mla_dims* dims, const mla_paging* paging,
+                                 int32_t io_dtype, int32_t q_len, int32_t requested);
+mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
+                                 int32_t io_dtype, int32_t q_len, const void* q_abs,
+                                 const void* q_pe, const void* cache,
+                                 const int32_t* block_table, const int32_t* lengths,
+                                 float softmax_scale, int32_t num_splits, void* workspace,
+                                 size_t workspace_bytes, void* o_c, float* lse,
+                                 int32_t* dev_status, void* stream);
+
+/*
+ * mla_page_index -- the index rows of the pages a step touched.
+ *
+ * For every page that holds rows [first_rows[b], lengths[b]) of a sequence, from
+ * the n rows of the page inside the sequence (those before first_rows[b] too):
+ *   m        = the page's largest magnitude, e with 2^(e-1) <= m < 2^e
+ *   sum[d]   = sum over rows of round(x[d] 2^(20-e))      (integers, exact)
+ *   codes[d] = round(sum[d] * (127 / max |sum|))          (int8)
+ *   scale    = max |sum| / 127 / n * 2^(e-20)             (fp32)
+ * so codes[d] * scale is the mean row to 8 bits.  Integer sums make the index
+ * independent of the order of summation.  A page of zeros, of magnitudes below
+ * 1e-30, or with an infinity gets zeros; NaN values give unspecified codes.
+ *
+ * codes [num_pages, d_c + d_rope] int8 and scales [num_pages] fp32 by page
+ * number (out: only touched pages change).  first_rows, lengths [B] int32;
+ * first_rows = lengths: nothing to do.  max_new >= 1: the most rows any request
+ * gained; a request that gained more, or a length outside the table's row, sets
+ * MLA_DEV_LENGTH_OUT_OF_RANGE (the pages of its first max_new rows are done; a
+ * bad length does none).  A page outside the pool sets
+ * MLA_DEV_PAGE_OUT_OF_RANGE and is skipped.  dims: batch and dtype.
+ */
+mla_status mla_page_index(const mla_dims* dims, const mla_paging* paging, int32_t max_new,
+                          const void* cache, const int32_t* block_table,
+                          const int32_t* first_rows, const int32_t* lengths, int8_t* codes,
+                          float* scales, int32_t* dev_status, void* stream);
+
+/*
+ * mla_select_pages -- the pages a token attends, by a cheap score.
+ *
+ * Token r = b * q_len + i sees n = lengths[b] - (q_len - 1 - i) rows in
+ * P = ceil(n / page_size) pages.  With P <= top_pages it keeps them all.
+ * Otherwise it keeps its first keep_first and last keep_last pages and, of the
+ * others, the top_pages - keep_first - keep_last with the highest score, the
+ * lower position winning ties:
+ *   q       = [q_abs ; q_pe] per head, c_h = round(q * (127 / max |q|)) (int8),
+ *             a_h = max |q| / 127 (both 0 for max |q| < 1e-30)
+ *   score   = scales[page] * max over heads of a_h * (c_h . codes[page])
+ * -- the largest logit of the page's mean row over the heads, to 8 bits.  The
+ * dot product is exact (integers), the rest a fixed chain of fp32 products, so
+ * the choice does not depend on the order of summation, on the batch or on the
+ * device.  All heads share one choice, since they share the cached row.
+ *
+ * sel_table [B*q_len, top_pages] int32 (out): the kept pages' numbers in order
+ * of position, then -1; sel_lengths [B*q_len] int32 (out): the rows they hold.
+ * Every page but the last is whole, so these are the block table and lengths of
+ * an mla_decode_attn_paged call with batch B*q_len and q_len 1 that computes
+ * exactly the attention over the kept pages.
+ *
+ * dims: batch, heads, s_max (longest length), dtype (the cache's).  io_dtype,
+ * q_abs, q_pe as mla_decode_attn_paged.  codes, scales: mla_page_index's, for
+ * every page but a token's last keep_last ones.  codes 16-byte aligned.
+ * keep_first >= 0, keep_last >= 1, keep_first + keep_last <= top_pages <=
+ * table_stride or more (a larger top_pages keeps every page).
+ * workspace >= mla_select_workspace_bytes(dims, paging, q_len) bytes.
+ * A page outside the pool sets MLA_DEV_PAGE_OUT_OF_RANGE and scores -infinity.
+ */
+size_t mla_select_workspace_bytes(const mla_dims* dims, const mla_paging* paging, int32_t q_len);
+mla_status mla_select_pages(const mla_dims* dims, const mla_paging* paging, int32_t io_dtype,
+                            int32_t q_len, const void* q_abs, const void* q_pe,
+                            const int32_t* block_table, const int32_t* lengths,
+                            const int8_t* codes, const float* scales, int32_t top_pages,
+                            int32_t keep_first, int32_t keep_last, void* workspace,
+                            size_t workspace_bytes, int32_t* sel_table, int32_t* sel_lengths,
+                            int32_t* dev_status, void* stream);
+
+/*
+ * mla_decode_attn_sparse -- mla_select_pages, then mla_decode_attn_paged over
+ * the kept pages (one call, one workspace of
+ * mla_sparse_workspace_bytes(dims, paging, io_dtype, q_len, top_pages,
+ * num_splits) bytes).  With top_pages at least ceil(s_max / page_size) it
+ * attends every row.  Arguments as those two calls'; sel_table and sel_lengths
+ * are written as well.
+ */
+size_t mla_sparse_workspace_bytes(const mla_dims* dims, const mla_paging* paging,
+                                  int32_t io_dtype, int32_t q_len, int32_t top_pages,
+                                  int32_t requested);
+mla_status mla_decode_attn_sparse(const mla_dims* dims, const mla_paging* paging,
+                                  int32_t io_dtype, int32_t q_len, const void* q_abs,
+                                  const void* q_pe, const void* cache,
+                                  const int32_t* block_table, const int32_t* lengths,
+                                  const int8_t* codes, const float* scales, float softmax_scale,
+                                  int32_t top_pages, int32_t keep_first, int32_t keep_last,
+                                  int32_t num_splits, void* workspace, size_t workspace_bytes,
+                                  int32_t* sel_table, int32_t* sel_lengths, void* o_c,
+                                  float* lse, int32_t* dev_status, void* stream);
 
 /* Static English name of a status code. */
 const char* mla_status_string(mla_status status);
