@@ -523,12 +523,12 @@ __global__ void __launch_bounds__(IndexPlan<T>::kThreads)
   }
   peak = block_max<L::kThreads>(peak, part_i);
   const bool good = live && peak > 0;
-  const float pf = static_cast<float>(peak), inv = good ? 127.f / pf : 0.f;
+  const float pf = static_cast<float>(peak), inv = good ? __frcp_rn(pf) * 127.f : 0.f;
   for (int d = tid; d < kRow; d += L::kThreads)
     p.codes[static_cast<size_t>(id) * kRow + d] =
         good ? static_cast<int8_t>(__float2int_rn(static_cast<float>(sums[0][d]) * inv)) : 0;
   if (tid == 0)
-    p.scales[id] = good ? ldexpf(pf / 127.f / static_cast<float>(n), ex - 20) : 0.f;
+    p.scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
 }
 
 template <typename T>

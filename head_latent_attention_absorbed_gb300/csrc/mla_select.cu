@@ -36,7 +36,7 @@ struct SelectParams {
   const int8_t* codes;
   const float* scales;
   float* scores;        // [R, width]
-  float* a;             // [R, groups * group]: max |q| / 127 per head
+  float* a;             // [R, groups * group]: max |q| (1/127) per head
   uint8_t* image;       // [R, groups][9 boxes][group rows][128 B], 128-byte swizzle
   int32_t *sel_table, *sel_lengths, *status;
   int R, H, q_len, s_max, group, groups, io_bf16;
@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(128) select_query_kernel(const SelectParams p)
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   const bool live = top >= kTinyQuery;
-  const float inv = live ? 127.f / top : 0.f;
-  if (lane == 0) p.a[static_cast<size_t>(r) * padded + h] = live ? top / 127.f : 0.f;
+  const float inv = live ? __frcp_rn(top) * 127.f : 0.f;
+  if (lane == 0) p.a[static_cast<size_t>(r) * padded + h] = live ? top * (1.f / 127.f) : 0.f;
   const int g = h / p.group, n = h % p.group;
   uint8_t* img = p.image + (static_cast<size_t>(r) * p.groups + g) * (kBoxes * p.group * 128);
 #pragma unroll

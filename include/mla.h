@@ -595,9 +595,9 @@ mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
  * the n rows of the page inside the sequence (those before first_rows[b] too):
  *   m        = the page's largest magnitude, e with 2^(e-1) <= m < 2^e
  *   sum[d]   = sum over rows of round(x[d] 2^(20-e))      (integers, exact)
- *   codes[d] = round(sum[d] * (127 / max |sum|))          (int8)
- *   scale    = max |sum| / 127 / n * 2^(e-20)             (fp32)
- * so codes[d] * scale is the mean row to 8 bits.  Integer sums make the index
+ *   codes[d] = round(sum[d] * (127 * (1 / max |sum|)))    (int8)
+ *   scale    = max |sum| * (1/127) / n * 2^(e-20)         (fp32)
+ * (each fp32 operation rounded to nearest), so codes[d] * scale is the mean row to 8 bits.  Integer sums make the index
  * independent of the order of summation.  A page of zeros, of magnitudes below
  * 1e-30, or with an infinity gets zeros; NaN values give unspecified codes.
  *
@@ -622,8 +622,8 @@ mla_status mla_page_index(const mla_dims* dims, const mla_paging* paging, int32_
  * Otherwise it keeps its first keep_first and last keep_last pages and, of the
  * others, the top_pages - keep_first - keep_last with the highest score, the
  * lower position winning ties:
- *   q       = [q_abs ; q_pe] per head, c_h = round(q * (127 / max |q|)) (int8),
- *             a_h = max |q| / 127 (both 0 for max |q| < 1e-30)
+ *   q       = [q_abs ; q_pe] per head, c_h = round(q * (127 * (1 / max |q|)))
+ *             (int8), a_h = max |q| * (1/127) (both 0 for max |q| < 1e-30)
  *   score   = scales[page] * max over heads of a_h * (c_h . codes[page])
  * -- the largest logit of the page's mean row over the heads, to 8 bits.  The
  * dot product is exact (integers), the rest a fixed chain of fp32 products, so

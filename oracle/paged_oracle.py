@@ -132,9 +132,10 @@ def page_index(rows):
     peak = int(np.abs(fixed).max())
     if peak == 0:
         return zero
-    inv = np.float32(127) / np.float32(peak)
+    inv = np.float32(1) / np.float32(peak)
+    inv = inv * np.float32(127)
     codes = np.rint(fixed.astype(np.float32) * inv).astype(np.int8)
-    scale = np.float32(peak) / np.float32(127)
+    scale = np.float32(peak) * (np.float32(1) / np.float32(127))
     scale = scale / np.float32(len(x))
     return codes, np.float32(np.ldexp(scale, e - 20))
 
@@ -145,8 +146,9 @@ def page_scores(q, codes, scales):
     top = np.abs(q).max(1)
     live = top >= TINY
     safe = np.where(live, top, np.float32(1))
-    inv = np.where(live, np.float32(127) / safe, np.float32(0)).astype(np.float32)
-    a = np.where(live, safe / np.float32(127), np.float32(0)).astype(np.float32)
+    inv = (np.float32(1) / safe) * np.float32(127)
+    inv = np.where(live, inv, np.float32(0)).astype(np.float32)
+    a = np.where(live, safe * (np.float32(1) / np.float32(127)), np.float32(0)).astype(np.float32)
     c = np.rint(q * inv[:, None]).astype(np.int64)
     dot = (c @ codes.astype(np.int64).T).astype(np.float32)
     v = (a[:, None] * dot).max(0)
