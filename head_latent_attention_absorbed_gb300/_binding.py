@@ -452,66 +452,67 @@ def ov_proj(d: MlaDims, o_c, w_ov, y, stream=None) -> None:
 
 
 # ------------------------------------------------------------------- paged cache
+#
+# The paged calls check every tensor they hand over (device, layout, type, size):
+# a wrong table or slot type would send a kernel outside its buffers.  The checks
+# are spelled out in one expression per call, since a small call takes less time
+# on the GPU than a loop of checks takes here (a decode step's block tables: 12 us
+# of host time with a helper call per tensor, 7 us so); only a call that fails
+# them goes through _explain for a message.
 
 def paging(page_size: int, num_pages: int, table_stride: int) -> MlaPaging:
     """The pool's shape: rows per page, pages, and entries per block-table row."""
     return MlaPaging(page_size, num_pages, table_stride)
 
 
+_I32 = _I64 = _I8 = _F32 = _BF16 = _ROW_TYPE = None
+_device = _raw_stream = None
+
+
+def _paged_lib():
+    """The library; the first call fetches what the checks compare with."""
+    global _I32, _I64, _I8, _F32, _BF16, _ROW_TYPE, _device, _raw_stream
+    if _device is None:
+        import torch
+        _I32, _I64, _I8 = torch.int32, torch.int64, torch.int8
+        _F32, _BF16 = torch.float32, torch.bfloat16
+        _ROW_TYPE = {MLA_F32: torch.float32, MLA_BF16: torch.bfloat16,
+                     MLA_FP8_E4M3: torch.float8_e4m3fn}
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _device = torch._C._cuda_getDevice
+    return _lib if _lib is not None else load()
+
+
+def _stream_on(dev: int, stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _explain(dev: int, **want):
+    """Raises the ValueError of the first tensor that is not as wanted:
+    name=(tensor, dtype, number of values)."""
+    for name, (t, dtype, numel) in want.items():
+        if t is None:
+            continue
+        _require(t.is_cuda and t.get_device() == dev,
+                 f"{name} must be a CUDA tensor on the current device")
+        _require(t.is_contiguous(), f"{name} must be contiguous")
+        _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+        _require(numel < 0 or t.numel() == numel, f"{name} must hold {numel} values, not {t.numel()}")
+    raise ValueError("a tensor of this call is not as documented")
+
+
+def _is(t, dev, dtype, numel) -> bool:
+    return (t.get_device() == dev and t.dtype is dtype and t.numel() == numel
+            and t.is_contiguous())
+
+
 def _io_code(torch_dtype) -> int:
     """Query and output type of the paged calls."""
-    import torch
-    if torch_dtype == torch.bfloat16:
-        return MLA_BF16
-    _require(torch_dtype == torch.float32, "queries must be fp32 or bf16")
-    return MLA_F32
-
-
-def _on_device(*ts):
-    """Contiguous CUDA tensors on the current device, the one whose stream the
-    call is enqueued on."""
-    import torch
-    dev = torch._C._cuda_getDevice()
-    for t in ts:
-        if t is not None:
-            _require(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
-            _require(t.get_device() == dev, "tensors must be on the current CUDA device")
-
-
-def _sized(name: str, t, dtype, numel: int):
-    _require(t.dtype == dtype and t.numel() == numel,
-             f"{name} must hold {numel} values of {dtype}")
-
-
-def _status_word(t):
-    if t is not None:
-        import torch
-        _require(t.dtype == torch.int32 and t.numel() >= 1, "dev_status must hold an int32")
-
-
-def _pool(d: MlaDims, pg: MlaPaging, cache):
-    _require(dtype_code(cache.dtype) == d.dtype, "the cache's dtype differs from the dims'")
-    _require(cache.numel() == pg.num_pages * pg.page_size * (d.d_c + d.d_rope),
-             "the cache must hold num_pages x page_size rows")
-
-
-def _table(pg: MlaPaging, t, batch: int):
-    import torch
-    _sized("block_table", t, torch.int32, batch * pg.table_stride)
-
-
-def _queries(d: MlaDims, q_len: int, q_abs, q_pe, o_c=None, lse=None) -> int:
-    """Checks the query side of a paged call; returns its io_dtype."""
-    import torch
-    rows = d.batch * q_len * d.heads
-    _require(q_len >= 1, "q_len must be >= 1")
-    _sized("q_abs", q_abs, q_abs.dtype, rows * d.d_c)
-    _sized("q_pe", q_pe, q_abs.dtype, rows * d.d_rope)
-    if o_c is not None:
-        _sized("o_c", o_c, q_abs.dtype, rows * d.d_c)
-    if lse is not None:
-        _sized("lse", lse, torch.float32, rows)
-    return _io_code(q_abs.dtype)
+    _paged_lib()
+    _require(torch_dtype is _BF16 or torch_dtype is _F32, "queries must be fp32 or bf16")
+    return MLA_BF16 if torch_dtype is _BF16 else MLA_F32
 
 
 def pages_extend(pg: MlaPaging, cached_lens, new_lens, block_table, free_list, num_free, lengths,
@@ -524,70 +525,94 @@ def pages_extend(pg: MlaPaging, cached_lens, new_lens, block_table, free_list, n
     0).  All or nothing: see mla_pages_extend.  ``num_free`` is updated in place
     unless ``num_free_out`` is given.
     """
-    import torch
-    i32 = torch.int32
+    lib = _paged_lib()
+    dev, i32 = _device(), _I32
     out = num_free if num_free_out is None else num_free_out
-    _on_device(cached_lens, new_lens, block_table, free_list, num_free, out, lengths, row_starts,
-               slots, positions, dev_status)
     B, n = cached_lens.numel(), slots.numel()
-    _sized("cached_lens", cached_lens, i32, B)
-    _sized("new_lens", new_lens, i32, B)
-    _sized("lengths", lengths, i32, B)
-    _sized("row_starts", row_starts, i32, B + 1)
-    _sized("slots", slots, torch.int64, n)
-    _sized("positions", positions, i32, n)
-    _sized("free_list", free_list, i32, pg.num_pages)
-    _sized("num_free", num_free, i32, 1)
-    _sized("num_free_out", out, i32, 1)
-    _table(pg, block_table, B)
-    _status_word(dev_status)
-    _check(load().mla_pages_extend(B, ctypes.byref(pg), _ptr(cached_lens), _ptr(new_lens), n,
-                                   _ptr(block_table), _ptr(free_list), _ptr(num_free), _ptr(out),
-                                   _ptr(lengths), _ptr(row_starts), _ptr(slots), _ptr(positions),
-                                   _ptr(dev_status), _stream(stream)))
+    pages = pg.num_pages
+    if not (cached_lens.get_device() == new_lens.get_device() == block_table.get_device()
+            == free_list.get_device() == num_free.get_device() == out.get_device()
+            == lengths.get_device() == row_starts.get_device() == slots.get_device()
+            == positions.get_device() == dev
+            and cached_lens.dtype is i32 and new_lens.dtype is i32 and block_table.dtype is i32
+            and free_list.dtype is i32 and num_free.dtype is i32 and out.dtype is i32
+            and lengths.dtype is i32 and row_starts.dtype is i32 and slots.dtype is _I64
+            and positions.dtype is i32
+            and new_lens.numel() == B and lengths.numel() == B and row_starts.numel() == B + 1
+            and positions.numel() == n and free_list.numel() == pages and num_free.numel() == 1
+            and out.numel() == 1 and block_table.numel() == B * pg.table_stride
+            and cached_lens.is_contiguous() and new_lens.is_contiguous()
+            and block_table.is_contiguous() and free_list.is_contiguous()
+            and lengths.is_contiguous() and row_starts.is_contiguous() and slots.is_contiguous()
+            and positions.is_contiguous()
+            and (dev_status is None or _is(dev_status, dev, i32, 1))):
+        _explain(dev, cached_lens=(cached_lens, i32, B), new_lens=(new_lens, i32, B),
+                 block_table=(block_table, i32, B * pg.table_stride),
+                 free_list=(free_list, i32, pages), num_free=(num_free, i32, 1),
+                 num_free_out=(out, i32, 1), lengths=(lengths, i32, B),
+                 row_starts=(row_starts, i32, B + 1), slots=(slots, _I64, n),
+                 positions=(positions, i32, n), dev_status=(dev_status, i32, 1))
+    code = lib.mla_pages_extend(
+        B, pg, cached_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(),
+        free_list.data_ptr(), num_free.data_ptr(), out.data_ptr(), lengths.data_ptr(),
+        row_starts.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def pages_release(pg: MlaPaging, finished, lengths, block_table, free_list, num_free,
                   dev_status=None, stream=None) -> None:
     """Push the pages of the requests with finished[b] != 0 back on the free stack."""
-    import torch
-    i32 = torch.int32
-    _on_device(finished, lengths, block_table, free_list, num_free, dev_status)
-    B = finished.numel()
-    _sized("finished", finished, i32, B)
-    _sized("lengths", lengths, i32, B)
-    _sized("free_list", free_list, i32, pg.num_pages)
-    _sized("num_free", num_free, i32, 1)
-    _table(pg, block_table, B)
-    _status_word(dev_status)
-    _check(load().mla_pages_release(B, ctypes.byref(pg), _ptr(finished), _ptr(lengths),
-                                    _ptr(block_table), _ptr(free_list), _ptr(num_free),
-                                    _ptr(dev_status), _stream(stream)))
+    lib = _paged_lib()
+    dev, i32, B = _device(), _I32, finished.numel()
+    if not (_is(finished, dev, i32, B) and _is(lengths, dev, i32, B)
+            and _is(block_table, dev, i32, B * pg.table_stride)
+            and _is(free_list, dev, i32, pg.num_pages) and _is(num_free, dev, i32, 1)
+            and (dev_status is None or _is(dev_status, dev, i32, 1))):
+        _explain(dev, finished=(finished, i32, B), lengths=(lengths, i32, B),
+                 block_table=(block_table, i32, B * pg.table_stride),
+                 free_list=(free_list, i32, pg.num_pages), num_free=(num_free, i32, 1),
+                 dev_status=(dev_status, i32, 1))
+    code = lib.mla_pages_release(B, pg, finished.data_ptr(), lengths.data_ptr(),
+                                 block_table.data_ptr(), free_list.data_ptr(),
+                                 num_free.data_ptr(),
+                                 None if dev_status is None else dev_status.data_ptr(),
+                                 _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def cache_append_paged(d: MlaDims, pg: MlaPaging, rows, positions, slots, cache,
                        rope_base: float = 10000.0, dev_status=None, stream=None) -> None:
     """Write latent rows [n, 576] (fp32 or bf16) into their slots, the RoPE key
     rotated at its position; a slot of -1 is skipped."""
-    import torch
-    _on_device(rows, positions, slots, cache, dev_status)
-    n = slots.numel()
-    _sized("rows", rows, rows.dtype, n * (d.d_c + d.d_rope))
-    _sized("positions", positions, torch.int32, n)
-    _sized("slots", slots, torch.int64, n)
-    _pool(d, pg, cache)
-    _status_word(dev_status)
-    _check(load().mla_cache_append_paged(ctypes.byref(d), ctypes.byref(pg), n,
-                                         dtype_code(rows.dtype), _ptr(rows), _ptr(positions),
-                                         _ptr(slots), float(rope_base), _ptr(cache),
-                                         _ptr(dev_status), _stream(stream)))
+    lib = _paged_lib()
+    dev, n, row, kind = _device(), slots.numel(), d.d_c + d.d_rope, rows.dtype
+    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * row
+    if not (rows.get_device() == positions.get_device() == slots.get_device()
+            == cache.get_device() == dev
+            and (kind is _BF16 or kind is _F32) and positions.dtype is _I32
+            and slots.dtype is _I64 and cache.dtype is ct
+            and rows.numel() == n * row and positions.numel() == n and cache.numel() == cn
+            and rows.is_contiguous() and positions.is_contiguous() and slots.is_contiguous()
+            and cache.is_contiguous()
+            and (dev_status is None or _is(dev_status, dev, _I32, 1))):
+        _explain(dev, rows=(rows, kind if kind is _BF16 else _F32, n * row),
+                 positions=(positions, _I32, n), slots=(slots, _I64, n), cache=(cache, ct, cn),
+                 dev_status=(dev_status, _I32, 1))
+    code = lib.mla_cache_append_paged(
+        d, pg, n, MLA_BF16 if kind is _BF16 else MLA_F32, rows.data_ptr(), positions.data_ptr(),
+        slots.data_ptr(), rope_base, cache.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def paged_num_splits(d: MlaDims, pg: MlaPaging, io_dtype, q_len: int = 1,
                      requested: int = 0) -> int:
     """Chunks per sequence decode_attn_paged uses for queries of ``io_dtype``."""
-    n = int(load().mla_paged_num_splits(ctypes.byref(d), ctypes.byref(pg), _io_code(io_dtype),
-                                        int(q_len), int(requested)))
+    n = int(load().mla_paged_num_splits(d, pg, _io_code(io_dtype), int(q_len), int(requested)))
     _require(n > 0, load().mla_last_error_message().decode())
     return n
 
@@ -595,8 +620,8 @@ def paged_num_splits(d: MlaDims, pg: MlaPaging, io_dtype, q_len: int = 1,
 def paged_workspace_bytes(d: MlaDims, pg: MlaPaging, io_dtype, q_len: int = 1,
                           requested: int = 0) -> int:
     """Workspace bytes of decode_attn_paged for queries of ``io_dtype``."""
-    n = int(load().mla_paged_workspace_bytes(ctypes.byref(d), ctypes.byref(pg),
-                                             _io_code(io_dtype), int(q_len), int(requested)))
+    n = int(load().mla_paged_workspace_bytes(d, pg, _io_code(io_dtype), int(q_len),
+                                             int(requested)))
     _require(n > 0, load().mla_last_error_message().decode())
     return n
 
@@ -606,58 +631,106 @@ def decode_attn_paged(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_table
                       num_splits_requested: int = 0, lse=None, dev_status=None,
                       stream=None) -> None:
     """decode_attn_multi over a paged cache; q_abs, q_pe and o_c all fp32 or all bf16."""
-    import torch
-    _on_device(q_abs, q_pe, cache, block_table, lengths, o_c, workspace, lse, dev_status)
-    io = _queries(d, q_len, q_abs, q_pe, o_c, lse)
-    _pool(d, pg, cache)
-    _table(pg, block_table, d.batch)
-    _sized("lengths", lengths, torch.int32, d.batch)
-    _status_word(dev_status)
-    nbytes = workspace.numel() * workspace.element_size()
-    _check(load().mla_decode_attn_paged(ctypes.byref(d), ctypes.byref(pg), io, int(q_len),
-                                        _ptr(q_abs), _ptr(q_pe), _ptr(cache), _ptr(block_table),
-                                        _ptr(lengths), float(softmax_scale),
-                                        int(num_splits_requested), _ptr(workspace), nbytes,
-                                        _ptr(o_c), _ptr(lse), _ptr(dev_status), _stream(stream)))
+    lib = _paged_lib()
+    dev, io, B, dc, dr = _device(), q_abs.dtype, d.batch, d.d_c, d.d_rope
+    rows = B * q_len * d.heads
+    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * (dc + dr)
+    if not (q_abs.get_device() == q_pe.get_device() == cache.get_device()
+            == block_table.get_device() == lengths.get_device() == o_c.get_device()
+            == workspace.get_device() == dev
+            and (io is _BF16 or io is _F32) and q_pe.dtype is io and o_c.dtype is io
+            and cache.dtype is ct and block_table.dtype is _I32 and lengths.dtype is _I32
+            and q_abs.numel() == rows * dc and q_pe.numel() == rows * dr
+            and o_c.numel() == rows * dc and cache.numel() == cn
+            and block_table.numel() == B * pg.table_stride and lengths.numel() == B
+            and q_abs.is_contiguous() and q_pe.is_contiguous() and cache.is_contiguous()
+            and block_table.is_contiguous() and lengths.is_contiguous() and o_c.is_contiguous()
+            and workspace.is_contiguous()
+            and (lse is None or _is(lse, dev, _F32, rows))
+            and (dev_status is None or _is(dev_status, dev, _I32, 1))):
+        _io_code(io)
+        _explain(dev, q_abs=(q_abs, io, rows * dc), q_pe=(q_pe, io, rows * dr),
+                 o_c=(o_c, io, rows * dc), cache=(cache, ct, cn),
+                 block_table=(block_table, _I32, B * pg.table_stride),
+                 lengths=(lengths, _I32, B), workspace=(workspace, workspace.dtype, -1),
+                 lse=(lse, _F32, rows), dev_status=(dev_status, _I32, 1))
+    code = lib.mla_decode_attn_paged(
+        d, pg, MLA_BF16 if io is _BF16 else MLA_F32, q_len, q_abs.data_ptr(), q_pe.data_ptr(),
+        cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), softmax_scale,
+        num_splits_requested, workspace.data_ptr(), workspace.numel() * workspace.itemsize,
+        o_c.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def page_index(d: MlaDims, pg: MlaPaging, cache, block_table, first_rows, lengths, max_new: int,
                codes, scales, dev_status=None, stream=None) -> None:
     """Index rows (int8 mean row and scale, by page number) of the pages that hold
     rows [first_rows[b], lengths[b]) of each sequence."""
-    import torch
-    _on_device(cache, block_table, first_rows, lengths, codes, scales, dev_status)
-    _pool(d, pg, cache)
-    _table(pg, block_table, d.batch)
-    _sized("first_rows", first_rows, torch.int32, d.batch)
-    _sized("lengths", lengths, torch.int32, d.batch)
-    _index(d, pg, codes, scales)
-    _status_word(dev_status)
-    _check(load().mla_page_index(ctypes.byref(d), ctypes.byref(pg), int(max_new), _ptr(cache),
-                                 _ptr(block_table), _ptr(first_rows), _ptr(lengths), _ptr(codes),
-                                 _ptr(scales), _ptr(dev_status), _stream(stream)))
-
-
-def _index(d: MlaDims, pg: MlaPaging, codes, scales):
-    import torch
-    _sized("codes", codes, torch.int8, pg.num_pages * (d.d_c + d.d_rope))
-    _sized("scales", scales, torch.float32, pg.num_pages)
-
-
-def _choice(d: MlaDims, q_len: int, sel_table, sel_lengths) -> int:
-    """Checks the outputs of a page selection; returns top_pages."""
-    import torch
-    rows = d.batch * q_len
-    _require(sel_table.dim() == 2, "sel_table must have one row per token")
-    _sized("sel_table", sel_table, torch.int32, rows * sel_table.shape[1])
-    _sized("sel_lengths", sel_lengths, torch.int32, rows)
-    return int(sel_table.shape[1])
+    lib = _paged_lib()
+    dev, i32, B, row, pages = _device(), _I32, d.batch, d.d_c + d.d_rope, pg.num_pages
+    ct = _ROW_TYPE.get(d.dtype)
+    if not (cache.get_device() == block_table.get_device() == first_rows.get_device()
+            == lengths.get_device() == codes.get_device() == scales.get_device() == dev
+            and cache.dtype is ct and block_table.dtype is i32 and first_rows.dtype is i32
+            and lengths.dtype is i32 and codes.dtype is _I8 and scales.dtype is _F32
+            and cache.numel() == pages * pg.page_size * row
+            and block_table.numel() == B * pg.table_stride and first_rows.numel() == B
+            and lengths.numel() == B and codes.numel() == pages * row and scales.numel() == pages
+            and cache.is_contiguous() and block_table.is_contiguous()
+            and first_rows.is_contiguous() and lengths.is_contiguous() and codes.is_contiguous()
+            and scales.is_contiguous()
+            and (dev_status is None or _is(dev_status, dev, i32, 1))):
+        _explain(dev, cache=(cache, ct, pages * pg.page_size * row),
+                 block_table=(block_table, i32, B * pg.table_stride),
+                 first_rows=(first_rows, i32, B), lengths=(lengths, i32, B),
+                 codes=(codes, _I8, pages * row), scales=(scales, _F32, pages),
+                 dev_status=(dev_status, i32, 1))
+    code = lib.mla_page_index(
+        d, pg, max_new, cache.data_ptr(), block_table.data_ptr(), first_rows.data_ptr(),
+        lengths.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def select_workspace_bytes(d: MlaDims, pg: MlaPaging, q_len: int = 1) -> int:
-    n = int(load().mla_select_workspace_bytes(ctypes.byref(d), ctypes.byref(pg), int(q_len)))
+    n = int(load().mla_select_workspace_bytes(d, pg, int(q_len)))
     _require(n > 0, load().mla_last_error_message().decode())
     return n
+
+
+def _check_selection(dev, d, pg, q_abs, q_pe, block_table, lengths, codes, scales, sel_table,
+                     sel_lengths, workspace, q_len, dev_status) -> int:
+    """The checks select_pages and decode_attn_sparse share; returns io_dtype."""
+    i32, io, B, dc, dr, pages = _I32, q_abs.dtype, d.batch, d.d_c, d.d_rope, pg.num_pages
+    R = B * q_len
+    rows = R * d.heads
+    top = sel_table.shape[1] if sel_table.dim() == 2 else -1
+    if not (q_abs.get_device() == q_pe.get_device() == block_table.get_device()
+            == lengths.get_device() == codes.get_device() == scales.get_device()
+            == sel_table.get_device() == sel_lengths.get_device() == workspace.get_device() == dev
+            and (io is _BF16 or io is _F32) and q_pe.dtype is io and block_table.dtype is i32
+            and lengths.dtype is i32 and codes.dtype is _I8 and scales.dtype is _F32
+            and sel_table.dtype is i32 and sel_lengths.dtype is i32 and top >= 0
+            and q_abs.numel() == rows * dc and q_pe.numel() == rows * dr
+            and block_table.numel() == B * pg.table_stride and lengths.numel() == B
+            and codes.numel() == pages * (dc + dr) and scales.numel() == pages
+            and sel_table.numel() == R * top and sel_lengths.numel() == R
+            and q_abs.is_contiguous() and q_pe.is_contiguous() and block_table.is_contiguous()
+            and lengths.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()
+            and sel_table.is_contiguous() and sel_lengths.is_contiguous()
+            and workspace.is_contiguous()
+            and (dev_status is None or _is(dev_status, dev, i32, 1))):
+        _io_code(io)
+        _require(top >= 0, "sel_table must have one row per token")
+        _explain(dev, q_abs=(q_abs, io, rows * dc), q_pe=(q_pe, io, rows * dr),
+                 block_table=(block_table, i32, B * pg.table_stride), lengths=(lengths, i32, B),
+                 codes=(codes, _I8, pages * (dc + dr)), scales=(scales, _F32, pages),
+                 sel_table=(sel_table, i32, R * top), sel_lengths=(sel_lengths, i32, R),
+                 workspace=(workspace, workspace.dtype, -1), dev_status=(dev_status, i32, 1))
+    return MLA_BF16 if io is _BF16 else MLA_F32
 
 
 def select_pages(d: MlaDims, pg: MlaPaging, q_abs, q_pe, block_table, lengths, codes, scales,
@@ -665,29 +738,25 @@ def select_pages(d: MlaDims, pg: MlaPaging, q_abs, q_pe, block_table, lengths, c
                  keep_last: int = 1, dev_status=None, stream=None) -> None:
     """The pages each token attends: its first and last ones and the best by the
     index's score, sel_table.shape[1] in all, as a block table of their own."""
-    import torch
-    _on_device(q_abs, q_pe, block_table, lengths, codes, scales, sel_table, sel_lengths,
-               workspace, dev_status)
-    io = _queries(d, q_len, q_abs, q_pe)
-    _table(pg, block_table, d.batch)
-    _sized("lengths", lengths, torch.int32, d.batch)
-    _index(d, pg, codes, scales)
-    top = _choice(d, q_len, sel_table, sel_lengths)
-    _status_word(dev_status)
-    nbytes = workspace.numel() * workspace.element_size()
-    _check(load().mla_select_pages(ctypes.byref(d), ctypes.byref(pg), io, int(q_len), _ptr(q_abs),
-                                   _ptr(q_pe), _ptr(block_table), _ptr(lengths), _ptr(codes),
-                                   _ptr(scales), top, int(keep_first), int(keep_last),
-                                   _ptr(workspace), nbytes, _ptr(sel_table), _ptr(sel_lengths),
-                                   _ptr(dev_status), _stream(stream)))
+    lib = _paged_lib()
+    dev = _device()
+    io = _check_selection(dev, d, pg, q_abs, q_pe, block_table, lengths, codes, scales, sel_table,
+                          sel_lengths, workspace, q_len, dev_status)
+    code = lib.mla_select_pages(
+        d, pg, io, q_len, q_abs.data_ptr(), q_pe.data_ptr(), block_table.data_ptr(),
+        lengths.data_ptr(), codes.data_ptr(), scales.data_ptr(), sel_table.shape[1], keep_first,
+        keep_last, workspace.data_ptr(), workspace.numel() * workspace.itemsize,
+        sel_table.data_ptr(), sel_lengths.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
 
 
 def sparse_workspace_bytes(d: MlaDims, pg: MlaPaging, io_dtype, top_pages: int, q_len: int = 1,
                            requested: int = 0) -> int:
     """Workspace bytes of decode_attn_sparse for queries of ``io_dtype``."""
-    n = int(load().mla_sparse_workspace_bytes(ctypes.byref(d), ctypes.byref(pg),
-                                              _io_code(io_dtype), int(q_len), int(top_pages),
-                                              int(requested)))
+    n = int(load().mla_sparse_workspace_bytes(d, pg, _io_code(io_dtype), int(q_len),
+                                              int(top_pages), int(requested)))
     _require(n > 0, load().mla_last_error_message().decode())
     return n
 
@@ -698,22 +767,22 @@ def decode_attn_sparse(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_tabl
                        num_splits_requested: int = 0, lse=None, dev_status=None,
                        stream=None) -> None:
     """select_pages, then decode_attn_paged over the pages kept."""
-    import torch
-    _on_device(q_abs, q_pe, cache, block_table, lengths, codes, scales, sel_table, sel_lengths,
-               o_c, workspace, lse, dev_status)
-    io = _queries(d, q_len, q_abs, q_pe, o_c, lse)
-    _pool(d, pg, cache)
-    _table(pg, block_table, d.batch)
-    _sized("lengths", lengths, torch.int32, d.batch)
-    _index(d, pg, codes, scales)
-    top = _choice(d, q_len, sel_table, sel_lengths)
-    _status_word(dev_status)
-    nbytes = workspace.numel() * workspace.element_size()
-    _check(load().mla_decode_attn_sparse(ctypes.byref(d), ctypes.byref(pg), io, int(q_len),
-                                         _ptr(q_abs), _ptr(q_pe), _ptr(cache), _ptr(block_table),
-                                         _ptr(lengths), _ptr(codes), _ptr(scales),
-                                         float(softmax_scale), top, int(keep_first),
-                                         int(keep_last), int(num_splits_requested),
-                                         _ptr(workspace), nbytes, _ptr(sel_table),
-                                         _ptr(sel_lengths), _ptr(o_c), _ptr(lse),
-                                         _ptr(dev_status), _stream(stream)))
+    lib = _paged_lib()
+    dev = _device()
+    io = _check_selection(dev, d, pg, q_abs, q_pe, block_table, lengths, codes, scales, sel_table,
+                          sel_lengths, workspace, q_len, dev_status)
+    rows = d.batch * q_len * d.heads
+    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * (d.d_c + d.d_rope)
+    if not (_is(cache, dev, ct, cn) and _is(o_c, dev, q_abs.dtype, rows * d.d_c)
+            and (lse is None or _is(lse, dev, _F32, rows))):
+        _explain(dev, cache=(cache, ct, cn), o_c=(o_c, q_abs.dtype, rows * d.d_c),
+                 lse=(lse, _F32, rows))
+    code = lib.mla_decode_attn_sparse(
+        d, pg, io, q_len, q_abs.data_ptr(), q_pe.data_ptr(), cache.data_ptr(),
+        block_table.data_ptr(), lengths.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+        softmax_scale, sel_table.shape[1], keep_first, keep_last, num_splits_requested,
+        workspace.data_ptr(), workspace.numel() * workspace.itemsize, sel_table.data_ptr(),
+        sel_lengths.data_ptr(), o_c.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)

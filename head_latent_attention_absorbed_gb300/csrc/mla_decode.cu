@@ -625,6 +625,11 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
       // (into this CTA's shared memory) have landed.
       if (!kPaged && ring_a && p.fill_early)
         for (int pos = 0; pos < kSlotsA; ++pos) mbar_wait_bounded(bar(BAR_FULLA + pos), 0);
+      if (kPaged && p.direct) {
+        pdl_wait();
+        for (int u = 0; u < (pair ? 2 : 1); ++u)
+          write_no_rows(p, b + u, qh0, pair ? kHeadGroup / 2 : kHeadGroup, tid, blockDim.x);
+      }
       return;
     }
     if (kPaged && warp == kWarpA) {
@@ -1220,13 +1225,21 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
           mme = lane == h ? mm[h] : mme;
         }
         const size_t n_part = size_t(p.B) * p.H * p.splits;   // rows of the partials
-        if (wq == 0 && lane < kGroupHeads &&
+        if (wq == 0 && lane < kGroupHeads && (!kPaged || p.part_lse) &&
             MLA_IN_BOUNDS(base + size_t(hw + lane) * p.splits < n_part))
           p.part_lse[base + size_t(hw + lane) * p.splits] =
               Lme > 0.f ? (mme + log2f(Lme)) * kLn2 : -INFINITY;
         // Two parts: columns hb.. (hi) and kG + hb.. (lo) of each O^T block, summed;
         // one part: columns hb..hb+15 (heads hb..hb+7, then hb+8..hb+15).
         const size_t head_stride = size_t(p.splits) * kDc;
+        // A value of the partial, or of a bf16 result that no combine follows.
+        const bool bf16_out = kPaged && p.direct && p.io_bf16;
+        auto put = [&](float* at, float v) {
+          if (bf16_out)
+            reinterpret_cast<__nv_bfloat16*>(p.part_o)[at - p.part_o] = __float2bfloat16_rn(v);
+          else
+            *at = v;
+        };
         if (!kEarlyBlocks) {
           uint32_t x4[4][8], y4[4][8];
 #pragma unroll
@@ -1242,10 +1255,11 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
             if (!MLA_IN_BOUNDS(base + size_t(hw + h) * p.splits < n_part)) continue;
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb)
-              orow[128 * mb] = (kParts == 2 ? __uint_as_float(x4[mb][h]) + __uint_as_float(y4[mb][h])
-                                : h < 8     ? __uint_as_float(x4[mb][h & 7])
-                                            : __uint_as_float(y4[mb][h & 7])) *
-                               inv[h];
+              put(orow + 128 * mb,
+                  (kParts == 2 ? __uint_as_float(x4[mb][h]) + __uint_as_float(y4[mb][h])
+                   : h < 8     ? __uint_as_float(x4[mb][h & 7])
+                               : __uint_as_float(y4[mb][h & 7])) *
+                      inv[h]);
           }
         }
         auto store_blocks = [&](int mb0) {   // O^T blocks mb0 and mb0 + 1
@@ -1263,10 +1277,11 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
             if (!MLA_IN_BOUNDS(base + size_t(hw + h) * p.splits < n_part)) continue;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              orow[128 * q] = (kParts == 2 ? __uint_as_float(x4[q][h]) + __uint_as_float(y4[q][h])
-                               : h < 8     ? __uint_as_float(x4[q][h & 7])
-                                           : __uint_as_float(y4[q][h & 7])) *
-                              inv[h];
+              put(orow + 128 * q,
+                  (kParts == 2 ? __uint_as_float(x4[q][h]) + __uint_as_float(y4[q][h])
+                   : h < 8     ? __uint_as_float(x4[q][h & 7])
+                               : __uint_as_float(y4[q][h & 7])) *
+                      inv[h]);
           }
         };
         if (kEarlyBlocks) {
@@ -1552,7 +1567,6 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
 
 // fp32 path: one CTA per (head, chunk, sequence); each warp runs its own online
 // softmax over every fourth row, then the four warp states are merged.
-template <bool kPaged>
 __global__ void __launch_bounds__(kThreads)
     split_f32_kernel(const SplitParams p) {
   const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
@@ -1576,19 +1590,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   for (int t = r0 + warp; t < r1; t += kWarps) {
-    size_t at = size_t(cache_seq(p, b)) * p.s_max + t;
-    bool there = true;
-    if (kPaged) {   // rows of a page that does not exist read as zeros
-      const int id = page_of(p, cache_seq(p, b), t);
-      there = id >= 0;
-      at = (size_t(there ? id : 0) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-    }
-    const float* row = cache + at * kRow;
+    const float* row = cache + (size_t(cache_seq(p, b)) * p.s_max + t) * kRow;
     float c[18];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 18; ++i) {
-      c[i] = !kPaged || there ? row[lane + 32 * i] : 0.f;
+      c[i] = row[lane + 32 * i];
       dot = fmaf(q[i], c[i], dot);
     }
 #pragma unroll
@@ -1624,6 +1631,107 @@ __global__ void __launch_bounds__(kThreads)
     p.part_o[base * kDc + c] = v / L;
   }
   if (tid == 0) p.part_lse[base] = (M + log2f(L)) * kLn2;
+}
+
+// fp32 path over a paged cache: one CTA per (head, chunk, sequence), eight warps.
+// A warp takes four consecutive rows at a time (chunks and pages are multiples of
+// four rows, so they share a page and one lookup) and keeps all their loads in
+// flight: with one row at a time, as above, a short chunk is a chain of load,
+// reduction and update latencies.  Lane l holds values 64 i + 2 l, + 1 of a row.
+// Bound by latency for short sequences and by L2 for long ones (every head reads
+// the rows).
+constexpr int kF32Warps = 8, kF32Rows = 4;
+__global__ void __launch_bounds__(32 * kF32Warps)
+    split_f32_paged_kernel(const SplitParams p) {
+  __shared__ float wm[kF32Warps], wl[kF32Warps], wo[kF32Warps][kDc];
+  const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int len = clamp_length(p, b, tid == 0 && h == 0 && j == 0);
+  const int r0 = j * p.chunk;
+  if (r0 >= len) {
+    if (p.direct) write_no_rows(p, b, h, 1, tid, 32 * kF32Warps);
+    return;
+  }
+  const int r1 = min(r0 + p.chunk, len);
+  const size_t bh = size_t(b) * p.H + h;
+  const float2* qa = reinterpret_cast<const float2*>(static_cast<const float*>(p.q_abs) + bh * kDc);
+  const float2* qp = reinterpret_cast<const float2*>(static_cast<const float*>(p.q_pe) + bh * kDr);
+  float2 q[9];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) q[i] = i < 8 ? qa[32 * i + lane] : qp[lane];
+  const float* cache = static_cast<const float*>(p.cache);
+  const int seq = cache_seq(p, b), mask = (1 << p.page_shift) - 1;
+  float m = -INFINITY, l = 0.f;
+  float2 acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
+  for (int t = r0 + kF32Rows * warp; t < r1; t += kF32Rows * kF32Warps) {
+    const int id = page_of(p, seq, t);   // rows of a page that does not exist read as zeros
+    const float2* row = reinterpret_cast<const float2*>(
+        cache + ((size_t(id < 0 ? 0 : id) << p.page_shift) + (t & mask)) * kRow);
+    float2 c[kF32Rows][9];
+    float s[kF32Rows];
+#pragma unroll
+    for (int u = 0; u < kF32Rows; ++u)
+#pragma unroll
+      for (int i = 0; i < 9; ++i)
+        c[u][i] = id >= 0 && t + u < r1 ? row[u * (kRow / 2) + 32 * i + lane]
+                                        : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kF32Rows; ++u) {
+      s[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) s[u] = fmaf(q[i].y, c[u][i].y, fmaf(q[i].x, c[u][i].x, s[u]));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int u = 0; u < kF32Rows; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kF32Rows; ++u) {
+      s[u] = t + u < r1 ? s[u] * p.scale_log2 : -INFINITY;
+      mn = fmaxf(mn, s[u]);
+    }
+    const float alpha = exp2f(m - mn);
+    l *= alpha;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = make_float2(acc[i].x * alpha, acc[i].y * alpha);
+#pragma unroll
+    for (int u = 0; u < kF32Rows; ++u) {
+      const float w = exp2f(s[u] - mn);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[i].x = fmaf(w, c[u][i].x, acc[i].x);
+        acc[i].y = fmaf(w, c[u][i].y, acc[i].y);
+      }
+    }
+    m = mn;
+  }
+  if (lane == 0) {
+    wm[warp] = m;
+    wl[warp] = l;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) reinterpret_cast<float2*>(wo[warp])[32 * i + lane] = acc[i];
+  __syncthreads();
+  float M = -INFINITY, L = 0.f, f[kF32Warps];
+#pragma unroll
+  for (int w = 0; w < kF32Warps; ++w) M = fmaxf(M, wm[w]);
+#pragma unroll
+  for (int w = 0; w < kF32Warps; ++w) {
+    f[w] = wm[w] == -INFINITY ? 0.f : exp2f(wm[w] - M);
+    L += f[w] * wl[w];
+  }
+  const size_t base = bh * p.splits + j;
+  for (int c = tid; c < kDc; c += 32 * kF32Warps) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kF32Warps; ++w) v = fmaf(f[w], wo[w][c], v);
+    p.part_o[base * kDc + c] = v / L;
+  }
+  if (tid == 0 && p.part_lse) p.part_lse[base] = (M + log2f(L)) * kLn2;
 }
 
 // Merge of the chunk partials of one (sequence, head):
@@ -2066,7 +2174,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   };
   // One CTA per chunk.
   int np_chunk = 0, np_splits = 0;
-  double np_cost = 1e300;
+  double np_cost = 1e300, np_join = 0.0;
   {
     double& best = np_cost;
     const int lo = requested > 0 ? requested : 1, hi = requested > 0 ? requested : max_splits;
@@ -2076,13 +2184,18 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
       if (requested <= 0 && s_eff != s) continue;
       const long long waves = (per_split * s_eff + slots - 1) / slots;
       const int rows = tiled ? (chunk + kTileRows - 1) / kTileRows * kTileRows : chunk;
-      const double cost = double(waves) * (rows + 96) + 4.0 * s_eff;
+      // A paged call with one chunk has no combine (about 2.5 us, what a CTA
+      // streams 100 rows in).
+      const double join = opts.paged && s_eff > 1 ? 100.0 : 0.0;
+      const double cost = double(waves) * (rows + 96) + 4.0 * s_eff + join;
       if (cost < best) {
         best = cost;
         np_chunk = chunk;
         np_splits = s_eff;
+        np_join = join;
       }
     }
+    np_cost -= np_join;   // the persistent estimate below leaves it out too
     if (np_chunk == 0) {   // more chunks requested than row groups: one per 8 rows (or tile)
       np_chunk = np_align;
       np_splits = (S + np_chunk - 1) / np_chunk;
@@ -2328,6 +2441,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   p->page_shift = view ? page_shift_of(view->paging) : 0;
   p->num_pages = view ? view->paging->num_pages : 0;
   p->io_bf16 = view && view->io == MLA_BF16 ? 1 : 0;
+  p->direct = 0;
   return MLA_OK;
 }
 
@@ -2336,7 +2450,8 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
                                const void* q_abs, const void* q_pe, const void* cache,
                                const int32_t* lengths, float softmax_scale, int32_t num_splits,
                                void* workspace, size_t ws_bytes, int32_t* dev_status,
-                               void* stream, const PagedView* view = nullptr) {
+                               void* stream, const PagedView* view = nullptr,
+                               void* direct_o = nullptr, float* direct_lse = nullptr) {
   if (!q_abs || !q_pe || !cache) {
     set_error("%s: a required pointer is NULL", who);
     return MLA_ERR_INVALID_ARG;
@@ -2345,6 +2460,11 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   mla_status st = prepare(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
                           num_splits, workspace, ws_bytes, dev_status, &p, view);
   if (st != MLA_OK) return st;
+  if (direct_o) {
+    p.direct = 1;
+    p.part_o = static_cast<float*>(direct_o);
+    p.part_lse = direct_lse;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
   if (dims->dtype == MLA_BF16) {
@@ -2395,9 +2515,9 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   } else {
     dim3 grid(dims->heads, p.splits, p.B);
     if (view)
-      split_f32_kernel<true><<<grid, kThreads, 0, s>>>(p);
+      split_f32_paged_kernel<<<grid, 32 * kF32Warps, 0, s>>>(p);
     else
-      split_f32_kernel<false><<<grid, kThreads, 0, s>>>(p);
+      split_f32_kernel<<<grid, kThreads, 0, s>>>(p);
   }
   return launch_status(who);
 }
@@ -2570,6 +2690,12 @@ extern "C" mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_pagi
   mla_status st = check_attn(who, dims, view, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
                              num_splits, workspace, ws_bytes, o_c);
   if (st != MLA_OK) return st;
+  mla_dims qd = *dims;
+  qd.batch = dims->batch * q_len;
+  const SplitPlan plan = plan_split(&qd, num_splits, plan_opts(dims, q_len, &view));
+  if (plan.splits == 1 && !plan.persist)   // the one chunk's partial is the result
+    return decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
+                        workspace, ws_bytes, dev_status, stream, &view, o_c, lse);
   st = decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
                     workspace, ws_bytes, dev_status, stream, &view);
   if (st != MLA_OK) return st;

@@ -210,7 +210,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
   const int r0 = j * p.chunk;
-  if (r0 >= len) return;   // chunk past the end of this sequence: nothing to do
+  if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
+    if (kPaged && p.direct) {
+      pdl_wait();
+      write_no_rows(p, b, g * kHeadGroup, kHeadGroup, tid, kF8Threads);
+    }
+    return;
+  }
   const int r1 = min(r0 + p.chunk, len);
   const int T = (r1 - r0 + kF8Rows - 1) / kF8Rows;
   const int last_valid = r1 - (r0 + (T - 1) * kF8Rows);
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         Lme = lane == h ? L : Lme;
         mme = lane == h ? m[h] : mme;
       }
-      if (wq == 0 && lane < kHalf)
+      if (wq == 0 && lane < kHalf && (!kPaged || p.part_lse))
         p.part_lse[base + size_t(hb + lane) * p.splits] =
             Lme > 0.f ? (mme + log2f(Lme)) * kLn2 : -INFINITY;
       float* row0 = p.part_o + (base + size_t(hb) * p.splits) * kDc + 32 * wq + lane;
@@ -571,10 +577,15 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         tmem_wait_ld();
         float* row = row0 + 128 * mb;
 #pragma unroll
-        for (int h = 0; h < kHalf; ++h, row += head_stride)
-          *row = (__uint_as_float(o1[h]) +
-                  (__uint_as_float(o2[h]) * 0.0625f + __uint_as_float(o3[h]) * 0.00390625f)) *
-                 inv[h];
+        for (int h = 0; h < kHalf; ++h, row += head_stride) {
+          const float v = (__uint_as_float(o1[h]) + (__uint_as_float(o2[h]) * 0.0625f +
+                                                     __uint_as_float(o3[h]) * 0.00390625f)) *
+                          inv[h];
+          if (kPaged && p.direct && p.io_bf16)
+            reinterpret_cast<__nv_bfloat16*>(p.part_o)[row - p.part_o] = __float2bfloat16_rn(v);
+          else
+            *row = v;
+        }
       }
     }
   }

@@ -33,7 +33,24 @@ struct SplitParams {
   const int32_t* table;         // NULL: a dense cache
   int table_stride, page_shift, num_pages;
   int io_bf16;                  // paged calls: q_abs, q_pe and o_c are bf16 (else fp32)
+  // Paged calls with one chunk per sequence: the partial is the result, so the
+  // split writes o_c (part_o, fp32 or bf16) and lse (part_lse, may be NULL) itself
+  // and no combine follows.
+  int direct;
 };
+
+// o_c = 0 and lse = -inf of `heads` heads from h0 of query group v, which attends
+// no row (direct calls; `threads` threads of the CTA, after the PDL wait).
+__device__ __forceinline__ void write_no_rows(const SplitParams& p, int v, int h0, int heads,
+                                              int tid, int threads) {
+  const size_t row = static_cast<size_t>(v) * p.H + h0;
+  const size_t bytes = p.io_bf16 ? 2 : 4;
+  uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.part_o) + row * kDc * bytes);
+  for (int i = tid; i < static_cast<int>(heads * kDc * bytes / 16); i += threads)
+    o[i] = make_uint4(0, 0, 0, 0);
+  if (p.part_lse)
+    for (int i = tid; i < heads; i += threads) p.part_lse[row + i] = __uint_as_float(0xff800000u);
+}
 
 // The page that holds row r of cache sequence `seq`, or -1 (reported) when the
 // table's entry names none.  r lies inside the sequence.

@@ -128,7 +128,7 @@ def test_pages_outside_the_pool_read_as_zeros(cuda_lib, dtype, io, heads, bad):
     c.run().check(status=mla.MLA_DEV_PAGE_OUT_OF_RANGE)
 
 
-@pytest.mark.parametrize("dtype,io,heads", [("bf16", BF16, 16), ("fp8", F32, 16), ("f32", F32, 16)])
+@pytest.mark.parametrize("dtype,io,heads", [("bf16", BF16, 16), ("bf16", F32, 32), ("fp8", F32, 16)])
 def test_paged_equals_dense(cuda_lib, dtype, io, heads):
     """With fp32 queries the paged call gives the dense call's bits when the chunks are
     the same; with bf16 queries, the dense call on the same values, rounded."""
@@ -245,6 +245,7 @@ def test_refuses_wrong_tensors(cuda_lib):
     with_(table=c.dev["table"].long())
     with_(table=c.dev["table"][:, 1:])
     with_(lengths=c.dev["lengths"][:1])
+    with_(lengths=c.dev["lengths"].repeat(2)[::2])
     c.ws = c.ws[:100]
     with pytest.raises(mla.MlaError):
         c.run()

@@ -66,7 +66,8 @@ def draw_tables(rng, B, page, width, most_new):
 @pytest.mark.parametrize("B,page,width,most,room", [
     (1, 16, 4, 40, 0), (1, 64, 2, 0, 1), (7, 32, 9, 100, 3), (64, 64, 130, 1, 0),
     (300, 16, 20, 200, 5), (1025, 128, 3, 2, 0), (2050, 16, 3, 17, 11), (16384, 256, 2, 1, 0),
-    (40, 64, 60, 3000, 1)])
+    (40, 64, 60, 3000, 1),
+    (3, 16, 900, 14000, 2), (5000, 16, 9, 5, 0)])
 def test_extend_matches_the_oracle(cuda_lib, B, page, width, most, room):
     rng = np.random.RandomState(B + page)
     cached, new, table, free, nf, pages = draw_tables(rng, B, page, width, most)

@@ -235,27 +235,36 @@ def test_refusals_before_any_launch(lib):
 
 
 def test_binding_refuses_host_tensors_and_wrong_types(lib):
+    """Every paged wrapper names what is wrong before it calls the library (on a
+    machine without a GPU every tensor is one on the wrong device)."""
     mla, _ = lib
     import torch
-    pg = mla.paging(64, 10, 2)
-    d = mla.dims(2, 16, 100, mla.MLA_BF16)
-    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)
     from head_latent_attention_absorbed_gb300 import _binding as b
-    with pytest.raises(ValueError):
-        b._sized("lengths", z(3), torch.int64, 3)
-    with pytest.raises(ValueError):
-        b._sized("lengths", z(3), torch.int32, 4)
-    with pytest.raises(ValueError):
-        b._pool(d, pg, z(10, 64, 576, dt=torch.float32))         # dims say bf16
-    with pytest.raises(ValueError):
-        b._pool(d, pg, z(9, 64, 576, dt=torch.bfloat16))
-    with pytest.raises(ValueError):
-        b._table(pg, z(2, 3), 2)
-    with pytest.raises(ValueError):
-        b._queries(d, 1, z(2, 16, 512, dt=torch.bfloat16), z(2, 16, 64, dt=torch.float32))
-    with pytest.raises(ValueError):
-        b._queries(d, 1, z(2, 16, 512, dt=torch.float16), z(2, 16, 64, dt=torch.float16))
-    assert b._queries(d, 2, z(4, 16, 512, dt=torch.bfloat16), z(4, 16, 64, dt=torch.bfloat16),
-                      z(4, 16, 512, dt=torch.bfloat16), z(4, 16, dt=torch.float32)) == mla.MLA_BF16
-    with pytest.raises(ValueError):
-        b._choice(d, 1, z(2, 4), z(3))
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)
+    pg = mla.paging(64, 10, 2)
+    b._paged_lib()
+
+    class Fake:
+        """A tensor that says it is on device 0."""
+
+        def __init__(self, t):
+            self.t, self.dtype, self.is_cuda = t, t.dtype, True
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    good = Fake(z(3))
+    assert b._is(good, 0, torch.int32, 3)
+    assert not b._is(good, 1, torch.int32, 3) and not b._is(good, 0, torch.int64, 3)
+    assert not b._is(good, 0, torch.int32, 4) and not b._is(Fake(z(3, 2)[:, 0]), 0, torch.int32, 3)
+    for t, dt, n, word in [(z(3), torch.int32, 3, "device"), (good, torch.int64, 3, "int64"),
+                           (good, torch.int32, 4, "4 values"),
+                           (Fake(z(3, 2)[:, 0]), torch.int32, 3, "contiguous")]:
+        with pytest.raises(ValueError, match=word):
+            b._explain(0, lengths=(t, dt, n))
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        b._io_code(torch.float16)
+    assert b._io_code(torch.bfloat16) == mla.MLA_BF16 and b._io_code(torch.float32) == mla.MLA_F32
