@@ -2035,7 +2035,14 @@ struct PlanOpts {
   bool paged = false;    // a paged cache: chunks are whole tiles
   int io = MLA_F32;      // query and output type of a paged call
 };
+// A paged call with bf16 queries runs as SM pairs at multiples of 128 heads
+// (mla_pair.cu), 64 heads per CTA.
+bool pair_form(const mla_dims* d, const PlanOpts& o) {
+  return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && d->heads % 128 == 0 &&
+         g_split_parts.load() != 2;
+}
 int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
+  if (pair_form(d, o)) return 64;
   if (d->dtype != MLA_BF16) return kHeadGroup;
   if (d->heads % 64 == 0 && g_split_parts.load() != 2 && !(o.paged && o.io != MLA_BF16)) return 64;
   return d->heads % 32 == 0 ? 32 : kHeadGroup;
@@ -2173,6 +2180,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
     return ((S + s - 1) / s + align - 1) / align * align;
   };
   // One CTA per chunk.
+  const bool pairs = pair_form(d, opts);
   int np_chunk = 0, np_splits = 0;
   double np_cost = 1e300, np_join = 0.0;
   {
@@ -2186,8 +2194,15 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
       const int rows = tiled ? (chunk + kTileRows - 1) / kTileRows * kTileRows : chunk;
       // A paged call with one chunk has no combine (about 2.5 us, what a CTA
       // streams 100 rows in).
-      const double join = opts.paged && s_eff > 1 ? 100.0 : 0.0;
-      const double cost = double(waves) * (rows + 96) + 4.0 * s_eff + join;
+      double join = opts.paged && s_eff > 1 ? 100.0 : 0.0;
+      double cost = double(waves) * (rows + 96) + 4.0 * s_eff + join;
+      // SM pairs (75 rows per us): a CTA's start and end cost 4 us, the combine 6 us, and
+      // each chunk 5.5 us per 4096 heads x tokens (a partial of 2 KB written and read;
+      // measured on 32 x 16384 rows x 128 heads: 207, 142, 183, 154 and 157 us at 1, 2, 3,
+      // 4 and 7 chunks, on 32 x 2048 rows 30.3, 39.6 and 50.9 at 1, 2 and 4).
+      if (pairs)
+        cost = double(waves) * (rows + 300) +
+               (s_eff > 1 ? 450.0 + 0.1 * s_eff * d->batch * d->heads : 0.0);
       if (cost < best) {
         best = cost;
         np_chunk = chunk;
@@ -2466,6 +2481,8 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
     p.part_lse = direct_lse;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (view && pair_form(dims, plan_opts(dims, q_len, view)))
+    return launch_split_pair(p, cache, dims->dtype == MLA_FP8_E4M3, s, who);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
   if (dims->dtype == MLA_BF16) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();

@@ -103,6 +103,12 @@ __device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool re
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who);
 
+// The paged split with bf16 queries at multiples of 128 heads (mla_pair.cu): a pair
+// of SMs takes 128 heads; same partials, chunks of whole tiles.  With an E4M3 cache
+// the queries' codes go to p.q_img first.
+mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
+                             cudaStream_t stream, const char* who);
+
 // Rows a cache view holds: B / q_len sequences of s_max rows, or a pool's pages.
 inline uint64_t view_rows(const SplitParams& p) {
   return p.table ? static_cast<uint64_t>(p.num_pages) << p.page_shift

@@ -63,31 +63,36 @@ def attention_bounds(q, rows, p, z, dtype, io, heads):
     """Elementwise bounds of |o - exact| and |lse - exact| for one token.
 
     q [H, 576], rows [n, 576] exact inputs; p [H, n] exact weights; z [H] exact
-    sums of exp(s - max).  Per score: the query's rounding (hi + lo bf16 pairs
-    2^-18 of each value, four E4M3 parts 2^-16 of the largest, bf16 and fp32
-    queries on the fp32 path none), products summed in fp32 (600 terms of 2^-23,
-    the tensor core truncating), and the softmax's base change and exp2 (2^-21
-    of the score, 2^-20 of the weight).  Per weight: hi + lo 2^-18, one part
-    2^-9, three E4M3 parts 2^-12 and 2^-18 of the largest weight.  The sums over
+    sums of exp(s - max).  Half a step is 2^-8 of a bf16 value and 2^-4 of an E4M3
+    one.  Per score: the query's rounding (hi + lo bf16 pairs 2^-16 of each value;
+    E4M3 parts in units of the head's largest value: four 2^-16, two of a bf16
+    query the last part's smallest step, 2^-17; bf16 and fp32 queries otherwise
+    none), products summed in fp32 (600 terms of 2^-23, the tensor core
+    truncating), and the softmax's base change and exp2 (2^-21 of the score, 2^-20
+    of the weight).  Per weight: hi + lo 2^-16, one part 2^-8, three E4M3 parts
+    2^-12 and 2^-18 of the largest weight, two parts 2^-8 and 2^-17.  The sums over
     rows add (n + 200) 2^-23 of the sum of magnitudes; the output rounds by half a
     step of its type.
     """
     n = len(rows)
     a = np.abs(q) @ np.abs(rows).T * SCALE                     # [H, n] sums of |q c|
+    two = dtype == "fp8" and io == torch.bfloat16 and heads % 128 == 0
     if dtype == "fp8":
-        dq = 2.0 ** -16 * np.abs(q).max(1, keepdims=True) * np.abs(rows).sum(1)[None] * SCALE
-        dp, floor = 2.0 ** -12, 2.0 ** -18
+        dq = (2.0 ** (-17 if two else -16) * np.abs(q).max(1, keepdims=True)
+              * np.abs(rows).sum(1)[None] * SCALE)
+        dp, floor = (2.0 ** -8, 2.0 ** -17) if two else (2.0 ** -12, 2.0 ** -18)
     else:
-        dq = (2.0 ** -18 if dtype == "bf16" and io == torch.float32 else 0.0) * a
+        dq = (2.0 ** -16 if dtype == "bf16" and io == torch.float32 else 0.0) * a
         one = dtype == "bf16" and io == torch.bfloat16 and heads % 64 == 0
-        dp = 0.0 if dtype == "f32" else 2.0 ** -9 if one else 2.0 ** -18
+        dp = 0.0 if dtype == "f32" else 2.0 ** -8 if one else 2.0 ** -16
         floor = 0.0
     ds = (dq + a * (600 * 2.0 ** -23 + 2.0 ** -21)).max(1)     # [H]
     rel = 2 * ds + dp + 2.0 ** -20 + (n + 200) * 2.0 ** -23
     mag = p @ np.abs(rows[:, :D_C])                            # [H, 512]
     tail = floor / z[:, None] * np.abs(rows[:, :D_C]).sum(0)[None]
     do = 2 * rel[:, None] * mag + 2 * tail
-    dl = ds + 2 * dp + n * floor / z + 2.0 ** -19 + (n + 200) * 2.0 ** -23
+    summed = 2 * dp + n * floor / z if dtype == "fp8" and not two else 0.0   # else unrounded
+    dl = ds + summed + 2.0 ** -19 + (n + 200) * 2.0 ** -23
     return do, dl
 
 

@@ -54,7 +54,8 @@ F32, BF16 = torch.float32, torch.bfloat16
 EDGES = [1, 15, 16, 17, 127, 128, 129, 300]
 KINDS = [("f32", F32, 5), ("f32", F32, 16), ("bf16", F32, 16), ("bf16", BF16, 16), ("bf16", F32, 32),
          ("bf16", BF16, 48), ("bf16", BF16, 64), ("bf16", F32, 64), ("fp8", F32, 16),
-         ("fp8", BF16, 32)]
+         ("fp8", BF16, 32), ("bf16", BF16, 128), ("fp8", BF16, 128), ("bf16", BF16, 256),
+         ("bf16", F32, 128), ("fp8", F32, 128)]
 
 
 @pytest.mark.parametrize("dtype,io,heads", KINDS)
@@ -153,7 +154,7 @@ def test_paged_equals_dense(cuda_lib, dtype, io, heads):
 
 
 @pytest.mark.parametrize("dtype,io,heads", [("bf16", BF16, 16), ("bf16", BF16, 64), ("fp8", BF16, 16),
-                                            ("f32", F32, 3)])
+                                            ("f32", F32, 3), ("bf16", BF16, 128), ("fp8", BF16, 128)])
 def test_same_bits_each_time_and_from_a_graph(cuda_lib, dtype, io, heads):
     """Two runs, a side stream and two graphs that share a workspace give the same bits."""
     c = Call(cuda_lib, [1000, 257, 40], 16, dtype, io, heads, seed=5).run()

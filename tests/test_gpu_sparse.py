@@ -92,7 +92,7 @@ class Sparse:
 
 @pytest.mark.parametrize("dtype,io,heads", [("f32", F32, 1), ("f32", F32, 5), ("bf16", BF16, 16),
                                             ("bf16", F32, 32), ("bf16", BF16, 48), ("bf16", BF16, 64),
-                                            ("fp8", BF16, 128), ("fp8", F32, 80)])
+                                            ("fp8", BF16, 128), ("fp8", F32, 80), ("bf16", BF16, 128)])
 @pytest.mark.parametrize("page,top,kf,kl", [(16, 4, 1, 1), (16, 9, 0, 2), (32, 2, 1, 1), (64, 3, 1, 1)])
 def test_sparse_matches_the_oracle(cuda_lib, dtype, io, heads, page, top, kf, kl):
     lengths = [1, page, top * page, top * page + 1, 20 * page + 5, 33 * page]
