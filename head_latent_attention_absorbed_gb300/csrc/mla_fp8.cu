@@ -88,12 +88,31 @@ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// One elected thread of the converged warp issues.  (From a branch of one thread an
+// MMA cost about 140 cycles, most of it moving its operands to uniform registers; in
+// warp-uniform code they stay there.)
 __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_elected(uint32_t dst, const CUtensorMap* m, int x, int y,
+                                                 uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
       : "memory");
 }
 
@@ -109,6 +128,13 @@ __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile 
       return false;
     }
   }
+}
+
+// The same by a whole warp, which leaves it converged (as the .aligned tensor-core
+// instructions after it need).
+__device__ __forceinline__ void f8_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  f8_wait(bar, parity, abort);
+  __syncwarp();
 }
 
 // E4M3 encoding (round to nearest even, saturating at +-448) and the exact
@@ -207,7 +233,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   auto bar = [&](int i) { return bars + 8 * i; };
 
   const int g = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
   const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
   const int r0 = j * p.chunk;
   if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
@@ -228,63 +255,51 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int row_base = kPaged ? r0 : cache_seq(p, b) * p.s_max + r0;
   const int h0 = g * kHeadGroup;
 
-  // The cache stream starts first: the producer sets up the barriers and
+  // The cache stream starts first: the producer warp sets up the barriers and
   // issues the first two tiles before the CTA-wide barrier.
-  auto issue = [&](int t) {
-    const int bf = t & 1;
-    mbar_arrive_expect_tx(bar(B_FULL + bf), kF8Tile);
-    const uint64_t pol = l2_evict_first_policy();
-#pragma unroll
-    for (int m = 0; m < kF8Boxes; ++m)
-      tma_load_2d(sbase + kOffTile + bf * kF8Tile + m * kF8Box, &tmap, 128 * m,
-                  row_base + t * kF8Rows, bar(B_FULL + bf), pol);
-  };
-  // Paged: lane i < pieces issues the boxes of piece i of the tile, whose first
-  // pool row is `row`.
+  // A tile is `pieces` boxes of box_rows rows (paged: of one page each); lane i knows
+  // the first row of piece i, and the next tile's are looked up ahead.
   const int box_rows = kPaged ? min(1 << p.page_shift, kF8Rows) : kF8Rows;
   const int pieces = kF8Rows / box_rows;
   auto piece_row = [&](int t) {
-    return paged_row(p, cache_seq(p, b), r0 + t * kF8Rows + lane * box_rows,
-                     lane * box_rows < kF8Rows ? len : 0);
+    return kPaged ? paged_row(p, cache_seq(p, b), r0 + t * kF8Rows + lane * box_rows,
+                              lane * box_rows < kF8Rows ? len : 0)
+                  : row_base + t * kF8Rows;
   };
-  auto issue_paged = [&](int t, int row) {
+  const uint64_t pol = l2_evict_first_policy();
+  auto issue = [&](int t, int row) {
     const int bf = t & 1;
     if (lane == 0) mbar_arrive_expect_tx(bar(B_FULL + bf), kF8Tile);
     __syncwarp();
-    const uint64_t pol = l2_evict_first_policy();
-    if (lane < pieces)
-#pragma unroll
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i) {
+      const int r = __shfl_sync(0xffffffffu, row, i);
+#pragma unroll 1
       for (int m = 0; m < kF8Boxes; ++m)
-        tma_load_2d(sbase + kOffTile + bf * kF8Tile + m * kF8Box + lane * box_rows * 128, &tmap,
-                    128 * m, row, bar(B_FULL + bf), pol);
+        tma_load_elected(sbase + kOffTile + bf * kF8Tile + m * kF8Box + i * box_rows * 128, &tmap,
+                         128 * m, r, bar(B_FULL + bf), pol);
+    }
   };
-  int row_ahead[2] = {0, 0};   // pieces of the next tiles to issue, looked up ahead
-  if (kPaged && warp == 8) {
-    row_ahead[0] = piece_row(0);
-    row_ahead[1] = T > 1 ? piece_row(1) : 0;
-  }
-  if (warp == 8 && lane == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(B_FULL + i), 1);
-      mbar_init(bar(B_EMPTY + i), 1);
-      mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_SFREE + i), 8);
-      mbar_init(bar(B_PFULL + i), 8);
-      mbar_init(bar(B_ODONE + i), 1);
-    }
-    mbar_init(bar(B_QREADY), 1);
-    mbar_init(bar(B_DONE), 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-    prefetch_tmap(&tmap);
-    for (int t = 0; t < 2 && t < T && !kPaged; ++t) issue(t);
-  }
   if (warp == 8) {
-    __syncwarp();
-    if (kPaged) {
-      issue_paged(0, row_ahead[0]);
-      if (T > 1) issue_paged(1, row_ahead[1]);
+    const int row0 = piece_row(0), row1 = T > 1 ? piece_row(1) : 0;
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(B_FULL + i), 1);
+        mbar_init(bar(B_EMPTY + i), 1);
+        mbar_init(bar(B_SFULL + i), 1);
+        mbar_init(bar(B_SFREE + i), 8);
+        mbar_init(bar(B_PFULL + i), 8);
+        mbar_init(bar(B_ODONE + i), 1);
+      }
+      mbar_init(bar(B_QREADY), 1);
+      mbar_init(bar(B_DONE), 1);
+      *abort_flag = 0;
+      fence_mbarrier_init();
+      prefetch_tmap(&tmap);
     }
+    __syncwarp();
+    issue(0, row0);
+    if (T > 1) issue(1, row1);
     tmem_alloc(smem_u32(slot_ptr), kTmemCols);
   }
   tc_fence_before();
@@ -294,59 +309,45 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
-    int issued_paged = T < 2 ? T : 2;
-    if (kPaged) {
-      int row = T > 2 ? piece_row(2) : 0;
-      for (int t = 2; t < T; ++t) {
-        const int next = t + 1 < T ? piece_row(t + 1) : 0;
-        int ok = 1;
-        if (lane == 0) ok = f8_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        issue_paged(t, row);
-        issued_paged = t + 1;
-        row = next;
-      }
+    int issued = T < 2 ? T : 2, row = T > 2 ? piece_row(2) : 0;
+    for (int t = 2; t < T; ++t) {
+      const int next = t + 1 < T ? piece_row(t + 1) : 0;
+      f8_warp_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      issue(t, row);
+      issued = t + 1;
+      row = next;
     }
-    if (lane == 0) {
-      int issued = kPaged ? issued_paged : T < 2 ? T : 2;
-      for (int t = 2; t < T && !kPaged; ++t) {
-        if (!f8_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag)) break;
-        issue(t);
-        issued = t + 1;
-      }
-      // Tiles still in flight land before the CTA may leave (bounded waits).
-      for (int t = issued > 2 ? issued - 2 : 0; t < issued; ++t) {
-        const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar(B_FULL + (t & 1)), (t >> 1) & 1))
-          if (globaltimer_ns() - t0 > kWaitNs) {
-            *abort_flag = 1;
-            break;
-          }
-      }
-    }
+    // Tiles still in flight land before the CTA may leave (bounded waits).
+    for (int t = issued > 2 ? issued - 2 : 0; t < issued; ++t)
+      if (!mbar_wait_bounded(bar(B_FULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
   } else if (warp == 9) {
     // ------------------------------------------------------------ score MMAs
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3(128, kQN, 0);
-      f8_wait(bar(B_QREADY), 0, abort_flag);
-      for (int t = 0; t < T && !*abort_flag; ++t) {
-        const int bf = t & 1;
-        if (!f8_wait(bar(B_FULL + bf), (t >> 1) & 1, abort_flag)) break;
-        if (t >= 2 && !f8_wait(bar(B_SFREE + bf), ((t - 2) >> 1) & 1, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + 64 * bf;
+    // The whole warp runs along, converged at every MMA; boxes are not unrolled (code
+    // that runs once a tile is fetched anew each time).
+    constexpr uint32_t idesc_s = idesc_e4m3(128, kQN, 0);
+    const uint64_t a0 = umma_desc_sw128(sbase + kOffTile, 16, 1024);
+    const uint64_t q0 = umma_desc_sw128(sbase + kOffQ, 16, 1024);
+    f8_warp_wait(bar(B_QREADY), 0, abort_flag);
+    for (int t = 0; t < T; ++t) {
+      const int bf = t & 1;
+      f8_warp_wait(bar(B_FULL + bf), (t >> 1) & 1, abort_flag);
+      if (t >= 2) f8_warp_wait(bar(B_SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + 64 * bf;
+#pragma unroll 1
+      for (int m = 0; m < kF8Boxes; ++m) {
+        const uint64_t a = a0 + static_cast<uint64_t>((bf * kF8Tile + m * kF8Box) >> 4);
+        const uint64_t q = q0 + static_cast<uint64_t>((m * kQBox) >> 4);
+        // a K step of 32 E4M3 columns moves the start by 32 B; the fifth box
+        // holds 64 real columns
 #pragma unroll
-        for (int m = 0; m < kF8Boxes; ++m) {
-          const uint64_t a = umma_desc_sw128(sbase + kOffTile + bf * kF8Tile + m * kF8Box, 16, 1024);
-          const uint64_t q = umma_desc_sw128(sbase + kOffQ + m * kQBox, 16, 1024);
-          // a K step of 32 E4M3 columns moves the start by 32 B; the fifth box
-          // holds 64 real columns
-          const int ks = m < 4 ? 4 : 2;
-          for (int k = 0; k < ks; ++k)
-            umma_e4m3(d, a + 2 * k, q + 2 * k, idesc_s, (m > 0 || k > 0) ? 1u : 0u);
-        }
-        umma_commit(bar(B_SFULL + bf));
+        for (int k = 0; k < 4; ++k)
+          if (k < 2 || m < 4)
+            umma_e4m3(d, a + 2 * k, q + 2 * k, idesc_s, k > 0 ? 1u : (m > 0 ? 1u : 0u));
       }
+      commit_elected(bar(B_SFULL + bf));
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ query image, PV MMAs
@@ -356,29 +357,32 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_arrive_expect_tx(bar(B_QREADY), static_cast<uint32_t>(kFp8QImage));
       bulk_g2s(sbase + kOffQ, img, static_cast<uint32_t>(kFp8QBoxes), bar(B_QREADY));
       bulk_g2s(sbase + kOffSigma, img + kFp8QBoxes, 16 * sizeof(float), bar(B_QREADY));
-      constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
-      for (int t = 0; t < T && !*abort_flag; ++t) {
-        const int bf = t & 1;
-        if (!f8_wait(bar(B_PFULL + bf), (t >> 1) & 1, abort_flag)) break;
-        tc_fence_after();
-        const uint64_t pd = umma_desc_sw128(sbase + kOffP + bf * kPBuf, 16, 1024);
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          // C^T block mb: latent columns 128 mb.. (MN-major, one 128-byte
-          // span), K = tile rows in 8-row groups 1024 B apart
-          const uint64_t c = umma_desc_sw128(sbase + kOffTile + bf * kF8Tile + mb * kF8Box,
-                                             kF8Box, 1024);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
-            umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
-                      idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
-        }
-        umma_commit(bar(B_ODONE + bf));
-        umma_commit(bar(B_EMPTY + bf));
-      }
-      umma_commit(bar(B_DONE));
-      mbar_wait_bounded(bar(B_DONE), 0);
     }
+    __syncwarp();
+    constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
+    const uint64_t p0 = umma_desc_sw128(sbase + kOffP, 16, 1024);
+    const uint64_t c0 = umma_desc_sw128(sbase + kOffTile, kF8Box, 1024);
+    for (int t = 0; t < T; ++t) {
+      const int bf = t & 1;
+      f8_warp_wait(bar(B_PFULL + bf), (t >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+      const uint64_t pd = p0 + static_cast<uint64_t>((bf * kPBuf) >> 4);
+#pragma unroll 1
+      for (int mb = 0; mb < 4; ++mb) {
+        // C^T block mb: latent columns 128 mb.. (MN-major, one 128-byte
+        // span), K = tile rows in 8-row groups 1024 B apart
+        const uint64_t c = c0 + static_cast<uint64_t>((bf * kF8Tile + mb * kF8Box) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
+          umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
+                    idesc_o, ks > 0 ? 1u : (t > 0 ? 1u : 0u));
+      }
+      commit_elected(bar(B_ODONE + bf));
+      commit_elected(bar(B_EMPTY + bf));
+    }
+    commit_elected(bar(B_DONE));
+    mbar_wait_bounded(bar(B_DONE), 0);
   } else {
     // ------------------------------------------------------------ softmax warps
     const int gp = warp >> 2, wq = warp & 3;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int row = 32 * wq + lane;                     // tile row held by this thread
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
 
-    f8_wait(bar(B_QREADY), 0, abort_flag);   // the query image and its scales
+    f8_warp_wait(bar(B_QREADY), 0, abort_flag);   // the query image and its scales
     float qsig[kHalf];
 #pragma unroll
     for (int h = 0; h < kHalf; ++h) qsig[h] = sigma[hb + h] * p.scale_log2;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     for (int t = 0; t < T; ++t) {
       const int sb = t & 1;
       const int valid = t == T - 1 ? last_valid : kF8Rows;
-      f8_wait(bar(B_SFULL + sb), (t >> 1) & 1, abort_flag);
+      f8_warp_wait(bar(B_SFULL + sb), (t >> 1) & 1, abort_flag);
       tc_fence_after();
       float sc[kHalf], tt[kHalf];
       {
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           l[h] *= alpha[h];
         }
         if (t > 0) {
-          f8_wait(bar(B_ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+          f8_warp_wait(bar(B_ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
           tc_fence_after();
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         l[2 * h2 + 1] += used1;
       }
       // P^T buffer sb was last read by the PV of tile t-2.
-      if (t >= 2) f8_wait(bar(B_ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
+      if (t >= 2) f8_warp_wait(bar(B_ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
       {
         // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
         // 16 part + n is part `part` of head n; the K index is the tile row.
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       lsum[(hb + lane) * 4 + wq] = v;
     }
     // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
-    f8_wait(bar(B_ODONE + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag);
+    f8_warp_wait(bar(B_ODONE + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag);
     tc_fence_after();
     named_bar_sync(1, kF8Soft);
     if (!*abort_flag) {
