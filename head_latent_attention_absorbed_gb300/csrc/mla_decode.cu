@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   auto item_end = [&](const SplitItem& m) {
     return m.row0 + (m.tiles - 1) * kTileRows + m.zero_from;
   };
+  if (kPaged && p.late) pdl_wait();
   const bool ring_a = warp == kWarpA && lane == 0;
   int len_first = 0, len_pair = 0;   // paired tokens: rows of the earlier and later token
   int r0_one = 0;                    // one-item CTA: the chunk's first row in its sequence
@@ -628,7 +629,8 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
       if (kPaged && p.direct) {
         pdl_wait();
         for (int u = 0; u < (pair ? 2 : 1); ++u)
-          write_no_rows(p, b + u, qh0, pair ? kHeadGroup / 2 : kHeadGroup, tid, blockDim.x);
+          write_no_rows(p, size_t(b + u) * p.H + qh0, pair ? kHeadGroup / 2 : kHeadGroup, tid,
+                        blockDim.x);
       }
       return;
     }
@@ -1646,10 +1648,11 @@ __global__ void __launch_bounds__(32 * kF32Warps)
   __shared__ float wm[kF32Warps], wl[kF32Warps], wo[kF32Warps][kDc];
   const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (p.late) pdl_wait();
   const int len = clamp_length(p, b, tid == 0 && h == 0 && j == 0);
   const int r0 = j * p.chunk;
   if (r0 >= len) {
-    if (p.direct) write_no_rows(p, b, h, 1, tid, 32 * kF32Warps);
+    if (p.direct) write_no_rows(p, size_t(b) * p.H + h, 1, tid, 32 * kF32Warps);
     return;
   }
   const int r1 = min(r0 + p.chunk, len);
@@ -2034,12 +2037,18 @@ struct PlanOpts {
   bool pair = false;     // two tokens of a multi-token step per CTA
   bool paged = false;    // a paged cache: chunks are whole tiles
   int io = MLA_F32;      // query and output type of a paged call
+  int q_len = 1;         // tokens per sequence
 };
-// A paged call with bf16 queries runs as SM pairs at multiples of 128 heads
-// (mla_pair.cu), 64 heads per CTA.
+// Query rows (heads x tokens) of a sequence from which a paged call with bf16 queries
+// runs as SM pairs (mla_pair.cu), whose tile costs the same for 16 rows as for 128.
+// Measured against the kernels of 16 to 64 heads per CTA (us, CTA / pair): bf16 cache, 8 x
+// 4096 rows, 16 rows 13.7 / 15.0, 32 18.6 / 15.8, 48 26.4 / 16.4, 64 23.7 / 17.0; 4 x
+// 65536, 16 rows 58 / 61, 32 70 / 63, 64 80 / 65; E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48
+// 19.5 / 18.1; 4 x 65536, 32 rows 60 / 53, 48 91 / 53.
+constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
-  return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && d->heads % 128 == 0 &&
-         g_split_parts.load() != 2;
+  return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
+         d->heads * o.q_len >= (d->dtype == MLA_BF16 ? kPairMinBf16 : kPairMinFp8);
 }
 int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
   if (pair_form(d, o)) return 64;
@@ -2138,7 +2147,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
 // work (measured: 19.6 us of host time per mla_decode_step call with it, from
 // Python with prepared arguments), so each thread keeps its last few answers.
 SplitPlan plan_split(const mla_dims* d, int requested, const PlanOpts& opts = {}) {
-  constexpr int kKeys = 11;
+  constexpr int kKeys = 12;
   struct Entry {
     int key[kKeys];
     SplitPlan plan;
@@ -2149,7 +2158,7 @@ SplitPlan plan_split(const mla_dims* d, int requested, const PlanOpts& opts = {}
   const long long sms = device_sms();
   const int key[kKeys] = {d->batch, d->heads, d->s_max, d->dtype, requested, opts.pair ? 1 : 0,
                           g_split_form.load(), g_split_parts.load(), static_cast<int>(sms),
-                          opts.paged ? 1 : 0, opts.io};
+                          opts.paged ? 1 : 0, opts.io, opts.q_len};
   for (int i = 0; i < filled; ++i) {
     bool same = true;
     for (int k = 0; k < kKeys; ++k) same = same && memo[i].key[k] == key[k];
@@ -2172,8 +2181,10 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   const int np_align = opts.paged && tiled ? kTileRows : kChunkAlign;
   const int max_splits = (S + np_align - 1) / np_align;
   const long long groups = d->dtype == MLA_F32 ? d->heads : d->heads / tc_heads_per_cta(d, opts);
-  const long long per_split = pair ? static_cast<long long>(d->batch) * d->heads / 32
-                                   : static_cast<long long>(d->batch) * groups;
+  const long long per_split =
+      pair_form(d, opts) ? 2ll * (d->batch / opts.q_len) * pair_groups(d->heads * opts.q_len)
+      : pair             ? static_cast<long long>(d->batch) * d->heads / 32
+                         : static_cast<long long>(d->batch) * groups;
   const bool can_persist = d->dtype == MLA_BF16 && !pair && tc_heads_per_cta(d, opts) == 16;
   const long long slots = tiled ? sms : 4ll * sms;
   auto chunk_of = [&](int s, int align) {
@@ -2372,13 +2383,15 @@ struct PagedView {
   const mla_paging* paging;
   const int32_t* table;
   int io;
+  bool late = false;   // SplitParams::late
 };
 
 static PlanOpts plan_opts(const mla_dims* dims, int q_len, const PagedView* view) {
   PlanOpts o;
-  o.pair = pair_tokens(dims, q_len);
   o.paged = view != nullptr;
   o.io = view ? view->io : MLA_F32;
+  o.q_len = q_len;
+  o.pair = pair_tokens(dims, q_len) && !pair_form(dims, o);
   return o;
 }
 
@@ -2457,6 +2470,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   p->num_pages = view ? view->paging->num_pages : 0;
   p->io_bf16 = view && view->io == MLA_BF16 ? 1 : 0;
   p->direct = 0;
+  p->late = view && view->late ? 1 : 0;
   return MLA_OK;
 }
 
@@ -2532,7 +2546,7 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   } else {
     dim3 grid(dims->heads, p.splits, p.B);
     if (view)
-      split_f32_paged_kernel<<<grid, 32 * kF32Warps, 0, s>>>(p);
+      launch_pdl(split_f32_paged_kernel, grid, dim3(32 * kF32Warps), 0, s, p);
     else
       split_f32_kernel<<<grid, kThreads, 0, s>>>(p);
   }
@@ -2695,6 +2709,25 @@ mla_status mla::check_attn_paged(const char* who, const mla_dims* dims, const ml
                     lengths, softmax_scale, num_splits, workspace, ws_bytes, o_c);
 }
 
+// The launches of mla_decode_attn_paged, its arguments checked.
+static mla_status attn_paged(const char* who, const mla_dims* dims, const PagedView& view,
+                             int q_len, const void* q_abs, const void* q_pe, const void* cache,
+                             const int32_t* lengths, float softmax_scale, int32_t num_splits,
+                             void* workspace, size_t ws_bytes, void* o_c, float* lse,
+                             int32_t* dev_status, void* stream) {
+  mla_dims qd = *dims;
+  qd.batch = dims->batch * q_len;
+  const SplitPlan plan = plan_split(&qd, num_splits, plan_opts(dims, q_len, &view));
+  if (plan.splits == 1 && !plan.persist)   // the one chunk's partial is the result
+    return decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
+                        workspace, ws_bytes, dev_status, stream, &view, o_c, lse);
+  const mla_status st = decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
+                                     num_splits, workspace, ws_bytes, dev_status, stream, &view);
+  if (st != MLA_OK) return st;
+  return decode_combine(who, dims, q_len, lengths, num_splits, workspace, ws_bytes, o_c, lse,
+                        stream, &view);
+}
+
 extern "C" mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
                                             int32_t io_dtype, int32_t q_len, const void* q_abs,
                                             const void* q_pe, const void* cache,
@@ -2704,20 +2737,37 @@ extern "C" mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_pagi
                                             float* lse, int32_t* dev_status, void* stream) {
   const char* who = "mla_decode_attn_paged";
   const PagedView view{paging, block_table, io_dtype};
-  mla_status st = check_attn(who, dims, view, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
-                             num_splits, workspace, ws_bytes, o_c);
+  const mla_status st = check_attn(who, dims, view, q_len, q_abs, q_pe, cache, lengths,
+                                   softmax_scale, num_splits, workspace, ws_bytes, o_c);
   if (st != MLA_OK) return st;
-  mla_dims qd = *dims;
-  qd.batch = dims->batch * q_len;
-  const SplitPlan plan = plan_split(&qd, num_splits, plan_opts(dims, q_len, &view));
-  if (plan.splits == 1 && !plan.persist)   // the one chunk's partial is the result
-    return decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
-                        workspace, ws_bytes, dev_status, stream, &view, o_c, lse);
-  st = decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
-                    workspace, ws_bytes, dev_status, stream, &view);
+  return attn_paged(who, dims, view, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
+                    num_splits, workspace, ws_bytes, o_c, lse, dev_status, stream);
+}
+
+mla_status mla::attn_queries(const char* who, const mla_dims* dims, const mla_paging* paging,
+                             int32_t io_dtype, const void* q_abs, const void* q_pe,
+                             const int32_t* lengths, int32_t num_splits, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (dims->dtype != MLA_FP8_E4M3) return MLA_OK;
+  const PagedView view{paging, lengths, io_dtype};   // the table is not read here
+  SplitParams p;
+  const mla_status st = prepare(who, dims, 1, q_abs, q_pe, nullptr, lengths, 1.f, num_splits,
+                                workspace, ws_bytes, nullptr, &p, &view);
   if (st != MLA_OK) return st;
-  return decode_combine(who, dims, q_len, lengths, num_splits, workspace, ws_bytes, o_c, lse,
-                        stream, &view);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return pair_form(dims, plan_opts(dims, 1, &view)) ? launch_pair_queries(p, s, who)
+                                                    : launch_fp8_queries(p, s, who);
+}
+
+mla_status mla::attn_selected(const char* who, const mla_dims* dims, const mla_paging* paging,
+                              int32_t io_dtype, const void* q_abs, const void* q_pe,
+                              const void* cache, const int32_t* sel_table,
+                              const int32_t* sel_lengths, float softmax_scale,
+                              int32_t num_splits, void* workspace, size_t ws_bytes, void* o_c,
+                              float* lse, int32_t* dev_status, void* stream) {
+  const PagedView view{paging, sel_table, io_dtype, true};
+  return attn_paged(who, dims, view, 1, q_abs, q_pe, cache, sel_lengths, softmax_scale,
+                    num_splits, workspace, ws_bytes, o_c, lse, dev_status, stream);
 }
 
 // Largest batch x heads for which mla_decode_step fuses the combine with W_UV.

@@ -235,12 +235,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int g = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
+  if (kPaged && p.late) pdl_wait();
   const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
   const int r0 = j * p.chunk;
   if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
     if (kPaged && p.direct) {
       pdl_wait();
-      write_no_rows(p, b, g * kHeadGroup, kHeadGroup, tid, kF8Threads);
+      write_no_rows(p, size_t(b) * p.H + g * kHeadGroup, kHeadGroup, tid, kF8Threads);
     }
     return;
   }
@@ -605,6 +606,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
 }  // namespace
 
+mla_status launch_fp8_queries(const SplitParams& p, cudaStream_t stream, const char* who) {
+  launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
+  return launch_status(who);
+}
+
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -641,7 +647,7 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
     }
     attr_done.set(dev);
   }
-  launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
+  if (!p.late) launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
   dim3 grid(p.H / kHeadGroup, p.splits, p.B);
   launch_pdl(p.table ? split_fp8_kernel<true> : split_fp8_kernel<false>, grid, dim3(kF8Threads),
              kF8Smem, stream, tmap, p);

@@ -34,4 +34,19 @@ mla_status check_attn_paged(const char* who, const mla_dims* dims, const mla_pag
                             const int32_t* lengths, float softmax_scale, int32_t num_splits,
                             void* workspace, size_t ws_bytes, void* o_c);
 
+// mla_decode_attn_paged with q_len 1 in two steps around the selection of its pages, the
+// arguments checked: attn_queries makes the queries' FP8 codes (E4M3 caches; nothing
+// otherwise), attn_selected does the rest, launched to start early under the kernel that
+// writes sel_table and sel_lengths.
+mla_status attn_queries(const char* who, const mla_dims* dims, const mla_paging* paging,
+                        int32_t io_dtype, const void* q_abs, const void* q_pe,
+                        const int32_t* lengths, int32_t num_splits, void* workspace,
+                        size_t ws_bytes, void* stream);
+mla_status attn_selected(const char* who, const mla_dims* dims, const mla_paging* paging,
+                         int32_t io_dtype, const void* q_abs, const void* q_pe,
+                         const void* cache, const int32_t* sel_table,
+                         const int32_t* sel_lengths, float softmax_scale, int32_t num_splits,
+                         void* workspace, size_t ws_bytes, void* o_c, float* lse,
+                         int32_t* dev_status, void* stream);
+
 }  // namespace mla

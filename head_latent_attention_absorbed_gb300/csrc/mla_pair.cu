@@ -1,5 +1,5 @@
-// The paged split for multiples of 128 heads and bf16 queries: a pair of SMs
-// takes 128 heads.
+// The paged split for bf16 queries: a pair of SMs takes up to 128 query rows (heads, and
+// the tokens of a multi-token step, which attend the same sequence) of one sequence.
 //
 // Per head the score of row t is q . c_t / sqrt(d_h + d_R), an online softmax over
 // the chunk's rows, and o = sum_t p_t c_t ("Multi-Head Latent Attention" 3.3, 3.6;
@@ -9,8 +9,8 @@
 // N = 64 heads) read it again from shared memory for every 64 heads.
 //
 // Here heads are the M of the MMAs and rows (or latent columns) the N, and two CTAs
-// of a cluster work as one tcgen05 pair (cta_group::2): CTA i holds heads 64 i ..
-// 64 i + 63 as its half of A, and each brings only half of every B operand:
+// of a cluster work as one tcgen05 pair (cta_group::2): CTA i holds half of the heads
+// (64 of 128) as its half of A, and each brings only half of every B operand:
 //   scores  S[128 heads x 128 rows] = Q[128 x 576] . C^T     CTA i: rows 64 i ..
 //   output  O[128 x 512] += P[128 x 128 rows] . C[128 x 512]  CTA i: 256 of the latent
 //                                                             columns, all 128 rows
@@ -22,22 +22,25 @@
 //
 // bf16 cache: the queries are bf16 as they are and P is rounded once to bf16 (at most
 // 2^-8 relative and unbiased, so less in the weighted sum than the bf16 output's own
-// rounding).  E4M3 cache (kind::f8f6f4): a
-// query (8 significant bits) is exactly the sum of two E4M3 parts in units of a power
-// of two per head (what falls below the second part's smallest step is 2^-17 of the
-// head's largest value), and P is two parts as well (2^-8 at most, 6e-4 rms).  The
-// parts have equal weight, so they accumulate in the same accumulators, as twice the
-// K.  P's parts are kept out of E4M3's subnormals by a reference 2^7 below the
-// running maximum.
+// rounding).  E4M3 cache (kind::f8f6f4): a query (8 significant bits) is exactly the sum
+// of two E4M3 parts in units of a power of two per head (what falls below the second
+// part's smallest step is 2^-17 of the head's largest value), and P is an E4M3 part and
+// its remainder as E5M2 (2^-7 at most).  The parts have equal weight, so they accumulate
+// in the same accumulators, as twice the K.  E5M2's exponents keep small weights: with
+// the softmax's reference 2^3 below the running maximum, whose room up to 2^8.5 lets the
+// maximum grow 2^5.5 before O is rescaled, the smallest step is 2^-19 of the largest
+// weight.  (An E4M3 remainder is twice as exact for large weights but ends at 2^-9, which
+// wants the reference at 2^7 and leaves 2^1.5: O was then rescaled in most of a chunk's
+// first tiles, at 2000 cycles.)
 //
 // Tensor memory per CTA: S_0 and S_1 (the scores are their sum; each has its own issuing
 // warp), two buffers of 64 columns each (lane l < 64: head l, rows 0-63
 // of the tile; lane 64 + l: head l, rows 64-127), O two tiles of 128 columns (lane l:
 // head l, latents 256 j + 0..127; lane 64 + l: 256 j + 128..255).
 //
-// Warps (448 threads): 0-7 softmax and epilogue; 8 score rows (TMA); 9 query and
-// output operand (TMA); 10-11 score MMAs, 12-13 output MMAs (the even CTA's issue for
-// the pair).  The even CTA's barriers collect both CTAs' copies and softmax warps;
+// Warps: 8 (bf16) or 16 (E4M3) softmax and epilogue; then one each for the score rows
+// (TMA) and for the query and the output operand (TMA), two for the score MMAs and two
+// for the output MMAs (the even CTA's issue for the pair).  The even CTA's barriers collect both CTAs' copies and softmax warps;
 // tcgen05.commit signals both CTAs.  Every wait is bounded.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -49,14 +52,17 @@ namespace mla {
 namespace {
 
 constexpr int kPHeads = 64;                    // heads per CTA
-constexpr int kPThreads = 448;
-constexpr int kPSoft = 256;                    // softmax threads
 constexpr int kPBox = 64 * 128;                // 64 rows of 128 bytes
 constexpr int kPBufBytes = 2 * kPBox;          // P: two K halves (bf16) or two parts (E4M3)
 constexpr uint32_t kPTmem = 512;
 
 template <bool kFp8>
 struct PairPlan {
+  // Softmax warps: each thread takes kCols scores of one head.  E4M3's conversions make its softmax the longest stage of a tile, so it
+  // gets twice the warps.
+  static constexpr int kSoftWarps = kFp8 ? 16 : 8, kSoft = 32 * kSoftWarps;
+  static constexpr int kThreads = kSoft + 6 * 32;
+  static constexpr int kSlices = kSoftWarps / 4, kCols = 64 / kSlices;
   static constexpr int kBoxCols = kFp8 ? 128 : 64;          // columns of a 128-byte box
   static constexpr int kBoxes = kFp8 ? 5 : 9;               // score boxes of a row
   static constexpr int kParts = kFp8 ? 2 : 1;
@@ -71,8 +77,8 @@ struct PairPlan {
   static constexpr int kOffS = kOffQ + kQBytes;
   static constexpr int kOffV = kOffS + kSlotsS * kPBox;
   static constexpr int kOffP = kOffV + kSlotsV * kUnit;
-  static constexpr int kOffRed = kOffP + kPBufs * kPBufBytes;   // [2][4][64] maxima
-  static constexpr int kOffBar = kOffRed + 2 * 4 * kPHeads * 4;
+  static constexpr int kOffRed = kOffP + kPBufs * kPBufBytes;   // [2][2 kSlices][64] maxima
+  static constexpr int kOffBar = kOffRed + 2 * 2 * kSlices * kPHeads * 4;
   // full / empty of the rings; S and P hand-overs; the query; the last tile's units
   static constexpr int FULLS = 0, EMPTYS = FULLS + kSlotsS, FULLV = EMPTYS + kSlotsS,
                        EMPTYV = FULLV + kSlotsV, SREADY = EMPTYV + kSlotsV, SFREE = SREADY + 2,
@@ -83,7 +89,7 @@ struct PairPlan {
   static constexpr size_t kSmem = 1024 + kOffAbort + 8;
   // Reference of the softmax below the running maximum, and how far a maximum may
   // pass it before O is rescaled (log2): E4M3 weights stay in [0, 2^8.5].
-  static constexpr float kBias = kFp8 ? 7.f : 0.f, kGrow = kFp8 ? 1.5f : 8.f;
+  static constexpr float kBias = kFp8 ? 3.f : 0.f, kGrow = kFp8 ? 5.5f : 8.f;
   // Epilogue staging (over the query, the rings and P): 64 rows of 512 values, 16 bytes
   // apart.
   static constexpr int kStageRow = kDc * 4 + 16;
@@ -151,8 +157,19 @@ __device__ __forceinline__ void cluster_sync_all() {
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// 32 columns of this thread's lane, loaded: load and wait are one statement, so that no
+// 16 or 32 columns of this thread's lane, loaded: load and wait are one statement, so that no
 // use of the registers can be scheduled between them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -232,7 +249,7 @@ __global__ void __launch_bounds__(128) pair_query_kernel(const SplitParams p, ui
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kPThreads, 1)
+__global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
     split_pair_kernel(const __grid_constant__ CUtensorMap tmap,
                       const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_qpe, const SplitParams p,
@@ -247,31 +264,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
-  const int j = blockIdx.y, v = blockIdx.z, h0 = blockIdx.x * kPHeads;
+  // Query rows (tokens x heads) of the sequence, dealt evenly to its CTAs: this CTA's
+  // are flat0 .. flat0 + mine - 1 of all; rows past them up to 64 are computed as well
+  // (other rows of the query, or zeros) and dropped.
+  const int j = blockIdx.y, seq = blockIdx.z, all = p.q_len * p.H;
+  const int share = (all + gridDim.x - 1) / gridDim.x;
+  const int first = blockIdx.x * share, mine = min(share, all - first);
+  const int flat0 = seq * all + first;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
-  const int len = clamp_length(p, v, tid == 0 && blockIdx.x == 0 && j == 0);
+  if (p.late) pdl_wait();
+  // Rows of the sequence, all of which its last token attends.
+  const int len = clamp_length(p, (seq + 1) * p.q_len - 1, tid == 0 && blockIdx.x == 0 && j == 0);
   const int r0 = j * p.chunk;
   if (r0 >= len) {   // both CTAs of the pair: the chunk lies past the sequence
     if (p.direct) {
       pdl_wait();
-      write_no_rows(p, v, h0, kPHeads, tid, kPThreads);
+      write_no_rows(p, flat0, mine, tid, L::kThreads);
     }
     return;
   }
   const int r1 = min(r0 + p.chunk, len);
   const int T = (r1 - r0 + kTileRows - 1) / kTileRows;
-  const int valid_last = r1 - (r0 + (T - 1) * kTileRows);
   // Rows of the last tile past the sequence's end may hold anything (NaN included):
   // they are zeroed in the output operand.
   const int zero_from = len - (r0 + (T - 1) * kTileRows);
   const bool zero_last = zero_from < kTileRows;
-  const int seq = cache_seq(p, v);
   const uint32_t lead = mapa_shared(bars, 0);   // the even CTA's barriers
   auto bar = [&](int i) { return bars + 8 * i; };
   auto lbar = [&](int i) { return lead + 8 * i; };
 
-  if (tid == 256) {
+  if (tid == L::kSoft) {
     for (int i = 0; i < L::kSlotsS; ++i) {
       mbar_init(bar(L::FULLS + i), 1);
       mbar_init(bar(L::EMPTYS + i), 1);
@@ -282,14 +305,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::SREADY + i), 2);                 // one commit per issuer
-      mbar_init(bar(L::SFREE + i), 2 * kPSoft / 32);    // both CTAs' softmax warps
-      mbar_init(bar(L::PREADY + i), 2 * kPSoft / 32);
+      mbar_init(bar(L::SFREE + i), 2 * L::kSoftWarps);  // both CTAs' softmax warps
+      mbar_init(bar(L::PREADY + i), 2 * L::kSoftWarps);
       mbar_init(bar(L::PVDONE + i), 2);
     }
     mbar_init(bar(L::QFULL), 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(L::LASTV + i), 1);
-      mbar_init(bar(L::ZEROED + i), 2 * kPSoft / 32);
+      mbar_init(bar(L::ZEROED + i), 2 * L::kSoftWarps);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -297,7 +320,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     prefetch_tmap(&tmap_q);
     if (!kFp8) prefetch_tmap(&tmap_qpe);
   }
-  if (warp == 10) {
+  // Role warps after the softmax warps.
+  constexpr int kWarpS = L::kSoftWarps, kWarpV = kWarpS + 1, kWarpScore = kWarpS + 2,
+                kWarpOut = kWarpS + 4;
+  if (warp == kWarpScore) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(slot_ptr)),
                  "r"(kPTmem)
@@ -313,7 +339,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // Pieces of one page each: rows of a box, and pieces of 64 rows.
   const int brows = min(1 << p.page_shift, 64), np = 64 / brows;
 
-  if (warp == 8) {
+  if (warp == kWarpS) {
     // ------------------------------------------------------------ score rows (HBM)
     // This CTA's 64 rows of each tile; lane i < np holds piece i's pool row.
     const uint64_t keep = l2_evict_last_policy();   // read again as the output operand
@@ -342,20 +368,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       row = next;
     }
-  } else if (warp == 9) {
+  } else if (warp == kWarpV) {
     // ------------------------------------------------------------ query, output operand (L2)
     const uint64_t stream = l2_evict_first_policy();
     pdl_wait();   // the query comes from the kernel before
     if (leader) expect_one(bar(L::QFULL), 2 * L::kQBytes);
-    const int qrow = v * p.H + h0;
 #pragma unroll 1
     for (int i = 0; i < L::kParts * L::kBoxes; ++i) {
       if (kFp8)
         tma_load_pair(sbase + L::kOffQ + i * kPBox, &tmap_q, 128 * (i % L::kBoxes),
-                      (i / L::kBoxes) * p.B * p.H + qrow, lbar(L::QFULL), stream);
+                      (i / L::kBoxes) * p.B * p.H + flat0, lbar(L::QFULL), stream);
       else
         tma_load_pair(sbase + L::kOffQ + i * kPBox, i < 8 ? &tmap_q : &tmap_qpe,
-                      i < 8 ? 64 * i : 0, qrow, lbar(L::QFULL), stream);
+                      i < 8 ? 64 * i : 0, flat0, lbar(L::QFULL), stream);
     }
     // Unit u of a tile: row half u >> 1, latent columns 256 (u & 1) + 128 rank ..;
     // lane i < 2 np holds the pool row of piece i of the tile's 128 rows.
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       row = next;
     }
-  } else if (warp == 10 || warp == 11) {
+  } else if (warp == kWarpScore || warp == kWarpScore + 1) {
     // ------------------------------------------------------------ score MMAs (even CTA)
     // Issuer i takes the boxes of the stream with parity i (so every other ring slot)
     // into accumulators S_i, which the softmax adds.  The whole warp runs along,
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // looked at once a tile.  Not unrolled over boxes: these warps run each instruction
     // once a tile, and straight code for 36 MMAs is fetched anew every time.
     if (leader) {
-      const int i = warp - 10;
+      const int i = warp - kWarpScore;
       constexpr uint32_t idesc = (1u << 4) | (kFp8 ? 0u : (1u << 7) | (1u << 10)) |
                                  (128u >> 3 << 17) | (128u >> 4 << 24);
       const uint64_t q0 = umma_desc_sw128(sbase + L::kOffQ, 16, 1024);
@@ -433,11 +458,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         commit_pair(bar(L::SREADY + sb));
       }
     }
-  } else if (warp == 12 || warp == 13) {
+  } else if (warp == kWarpOut || warp == kWarpOut + 1) {
     // ------------------------------------------------------------ output MMAs (even CTA)
     // Issuer jj takes the units of O tile jj.
     if (leader) {
-      const int jj = warp - 12;
+      const int jj = warp - kWarpOut;
       constexpr uint32_t idesc = (1u << 4) | (kFp8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 16) |
                                  (256u >> 3 << 17) | (128u >> 4 << 24);
       const uint64_t p0 = umma_desc_sw128(sbase + L::kOffP, 16, 1024);
@@ -466,7 +491,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                ((kFp8 ? part * kPBox + 64 * kh : kh * kPBox) >> 4);
 #pragma unroll
             for (int ks = 0; ks < (kFp8 ? 2 : 4); ++ks)
-              mma_pair<kFp8>(d, a + 2 * ks, b + ks * ((kFp8 ? 4096 : 2048) >> 4), idesc,
+              mma_pair<kFp8>(d, a + 2 * ks, b + ks * ((kFp8 ? 4096 : 2048) >> 4),
+                             idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
                              part > 0 || ks > 0 ? 1u : (t > 0 || kh > 0 ? 1u : 0u));
           }
           commit_pair(bar(L::EMPTYV + sl));
@@ -477,14 +503,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax
     // Warp w: lanes 32 (w & 3) .. of tensor memory, so head 32 (w & 1) + lane of the
-    // tile's row half (w >> 1) & 1, and the column half w >> 2 of those 64 rows.
+    // tile's row half (w >> 1) & 1, and the column slice w >> 2 of those 64 rows.
+    constexpr int kCols = L::kCols, kSlices = L::kSlices;
     const int qd = warp & 3, hh = warp >> 2;
-    const int head = 32 * (qd & 1) + lane, row0 = 64 * (qd >> 1) + 32 * hh;
+    const int head = 32 * (qd & 1) + lane, row0 = 64 * (qd >> 1) + kCols * hh;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qd) << 16);
-    const int part_of = 2 * (qd >> 1) + hh;   // which quarter of the tile's rows
+    const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
     // E4M3: the head's unit, written by the kernel before (known complete once the
     // first scores are).
     float scale = p.scale_log2;
+    // Columns of the chunk this head's token attends: a token before the last sees fewer.
+    const int token = (first + min(head, mine - 1)) / p.H;
+    const int limit = min(r1, len - (p.q_len - 1 - token)) - r0 - row0;
     float m = -INFINITY, l = 0.f;
     // A wait that gives up leaves the loop running (every later wait then returns at
     // once), so that all softmax warps meet at the same barriers.
@@ -492,29 +522,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int sb = t & 1;
       warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
       if (kFp8 && t == 0)
-        scale *= __ldcg(sigma + static_cast<size_t>(v) * p.H + h0 + head);
+        scale *= __ldcg(sigma + flat0 + min(head, mine - 1));
       tc_fence_after();
-      float x[32], y[32];
-      tmem_ld32(lanes + 64 * sb + 32 * hh, reinterpret_cast<uint32_t*>(x));
-      tmem_ld32(lanes + 128 + 64 * sb + 32 * hh, reinterpret_cast<uint32_t*>(y));
+      float x[kCols], y[kCols];
+      const uint32_t s_at = lanes + 64 * sb + kCols * hh;
+      if constexpr (kCols == 32) {
+        tmem_ld32(s_at, reinterpret_cast<uint32_t*>(x));
+        tmem_ld32(s_at + 128, reinterpret_cast<uint32_t*>(y));
+      } else {
+        tmem_ld16(s_at, reinterpret_cast<uint32_t*>(x));
+        tmem_ld16(s_at + 128, reinterpret_cast<uint32_t*>(y));
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(lbar(L::SFREE + sb));
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] += y[i];
-      if (t == T - 1) {
+      for (int i = 0; i < kCols; ++i) x[i] += y[i];
+      if (__any_sync(0xffffffffu, t * kTileRows + kCols > limit)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (row0 + i >= valid_last) x[i] = -INFINITY;
+        for (int i = 0; i < kCols; ++i)
+          if (t * kTileRows + i >= limit) x[i] = -INFINITY;
       }
       float mx = x[0];
 #pragma unroll
-      for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
-      float* rd = red + sb * 4 * kPHeads;
+      for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
+      float* rd = red + sb * 2 * kSlices * kPHeads;
       rd[part_of * kPHeads + head] = mx;
-      named_bar_sync(1, kPSoft);
-      mx = fmaxf(fmaxf(rd[head], rd[kPHeads + head]),
-                 fmaxf(rd[2 * kPHeads + head], rd[3 * kPHeads + head])) * scale - L::kBias;
+      named_bar_sync(1, L::kSoft);
+      mx = rd[head];
+#pragma unroll
+      for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, rd[i * kPHeads + head]);
+      mx = mx * scale - L::kBias;
       if (__any_sync(0xffffffffu, mx > m + L::kGrow)) {
         // Move the references of the warp's heads (the four warps of the same heads
         // decide alike); rescale the sum and this warp's share of O.
@@ -526,8 +564,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {   // O columns 128 hh .. + 127 of the 256
-            const uint32_t at = lanes + L::kOCol + 128 * hh + 32 * c;
+          for (int c = 0; c < 8 / kSlices; ++c) {   // this warp's slice of O's 256 columns
+            const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 32 * c;
             float o[32];
             tmem_ld32(at, reinterpret_cast<uint32_t*>(o));
 #pragma unroll
@@ -540,7 +578,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kCols; ++i) {
         x[i] = ex2(fmaf(x[i], scale, -ref));
         l += x[i];
       }
@@ -551,7 +589,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (kFp8) {
         // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kCols / 16; ++c) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -564,7 +602,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
               const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
                   static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3)));
               const uint32_t f2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - g.x, y1 - g.y),
-                                                           __NV_SATFINITE, __NV_E4M3);
+                                                           __NV_SATFINITE, __NV_E5M2);
               a |= f1 << (16 * e);
               b |= f2 << (16 * e);
             }
@@ -578,8 +616,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       } else {
         // Row `head` of the box of this row half, 128 bytes of 64 tile rows.
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(pb + (qd >> 1) * kPBox + sw128(head, 4 * hh + c)) =
+        for (int c = 0; c < kCols / 8; ++c)
+          *reinterpret_cast<uint4*>(pb + (qd >> 1) * kPBox + sw128(head, kCols / 8 * hh + c)) =
               make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
                          pack_bf16(x[8 * c + 4], x[8 * c + 5]),
                          pack_bf16(x[8 * c + 6], x[8 * c + 7]));
@@ -594,7 +632,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           warp_wait(bar(L::LASTV + u), 0, abort_flag);
           const int from = max(0, zero_from - 64 * (u >> 1));
           uint8_t* unit = smem + L::kOffV + ((4 * t + u) % L::kSlotsV) * L::kUnit;
-          for (int i = tid; i < (64 - from) * 8 * (L::kUnit / kPBox); i += kPSoft) {
+          for (int i = tid; i < (64 - from) * 8 * (L::kUnit / kPBox); i += L::kSoft) {
             const int box = i / ((64 - from) * 8), r = i % ((64 - from) * 8);
             *reinterpret_cast<uint4*>(unit + box * kPBox + from * 128 + 16 * r) =
                 make_uint4(0, 0, 0, 0);
@@ -608,37 +646,39 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (tid == 0) pdl_launch_dependents();   // the combine waits for this grid anyway
     // The row sums of a head's four threads, its log-sum-exp, and O / sum through
     // shared memory (over operands that nothing reads any more) to whole rows.
-    named_bar_sync(1, kPSoft);   // every read of the maxima is done
+    named_bar_sync(1, L::kSoft);   // every read of the maxima is done
     red[part_of * kPHeads + head] = l;
     warp_wait(bar(L::PVDONE + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag);
     tc_fence_after();
-    named_bar_sync(1, kPSoft);
+    named_bar_sync(1, L::kSoft);
     if (!*abort_flag) {
-      const float sum = (red[head] + red[kPHeads + head]) +
-                        (red[2 * kPHeads + head] + red[3 * kPHeads + head]);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * kSlices; ++i) sum += red[i * kPHeads + head];
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const size_t row = (static_cast<size_t>(v) * p.H + h0) * p.splits + j;   // of head h0
-      if (part_of == 0 && p.part_lse)
+      const size_t row = static_cast<size_t>(flat0) * p.splits + j;   // of the first
+      if (part_of == 0 && head < mine && p.part_lse)
         p.part_lse[row + static_cast<size_t>(head) * p.splits] =
             sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
       uint8_t* stage = smem;
-      // O tile hh (latents 256 hh ..): this lane's 128 columns are latents 256 hh +
-      // 128 (qd >> 1) ..
-      float* mine = reinterpret_cast<float*>(stage + head * L::kStageRow) + 256 * hh +
-                    128 * (qd >> 1);
+      // This warp's slice of O's columns: in tile jj = col0 / 128 the lane's 128 columns
+      // are latents 256 jj + 128 (qd >> 1) ..
+      const int col0 = 256 / kSlices * hh;
+      float* to = reinterpret_cast<float*>(stage + head * L::kStageRow) + 256 * (col0 >> 7) +
+                  128 * (qd >> 1) + (col0 & 127);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8 / kSlices; ++c) {
         float o[32];
-        tmem_ld32(lanes + L::kOCol + 128 * hh + 32 * c, reinterpret_cast<uint32_t*>(o));
+        tmem_ld32(lanes + L::kOCol + col0 + 32 * c, reinterpret_cast<uint32_t*>(o));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(mine + 32 * c + 4 * i) =
+          *reinterpret_cast<float4*>(to + 32 * c + 4 * i) =
               make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
                           o[4 * i + 3] * inv);
       }
-      named_bar_sync(1, kPSoft);
+      named_bar_sync(1, L::kSoft);
       const bool bf16_out = p.direct && p.io_bf16;
-      for (int h = warp; h < kPHeads; h += kPSoft / 32) {
+      for (int h = warp; h < mine; h += L::kSoftWarps) {
         const float4* src = reinterpret_cast<const float4*>(stage + h * L::kStageRow);
         const size_t at = (row + static_cast<size_t>(h) * p.splits) * kDc;
 #pragma unroll
@@ -663,7 +703,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // neither CTA leaves while the other's MMAs or barriers use it
-  if (warp == 10) {
+  if (warp == kWarpScore) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPTmem)
                  : "memory");
@@ -687,8 +727,8 @@ mla_status launch_pair(const CUtensorMap& cache, const CUtensorMap& q, const CUt
     attr_done.set(dev);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.H / kPHeads, p.splits, p.B);
-  cfg.blockDim = dim3(kPThreads);
+  cfg.gridDim = dim3(2 * pair_groups(p.q_len * p.H), p.splits, p.B / p.q_len);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -704,6 +744,18 @@ mla_status launch_pair(const CUtensorMap& cache, const CUtensorMap& q, const CUt
 }
 
 }  // namespace
+
+// The queries' codes in p.q_img: two parts, then a unit per row.
+static uint8_t* pair_codes(const SplitParams& p) { return p.q_img; }
+static float* pair_units(const SplitParams& p) {
+  return reinterpret_cast<float*>(p.q_img + size_t(2) * p.B * p.H * kQ8Row);
+}
+
+mla_status launch_pair_queries(const SplitParams& p, cudaStream_t stream, const char* who) {
+  launch_pdl(pair_query_kernel, dim3(static_cast<unsigned>((size_t(p.B) * p.H + 3) / 4)),
+             dim3(128), 0, stream, p, pair_codes(p), pair_units(p));
+  return launch_status(who);
+}
 
 mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
                              cudaStream_t stream, const char* who) {
@@ -728,13 +780,12 @@ mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
   };
   const uint64_t rows = static_cast<uint64_t>(p.B) * p.H;
   const int page = 1 << p.page_shift;
-  uint8_t* codes = p.q_img;
-  float* sigma = reinterpret_cast<float*>(p.q_img + 2 * rows * kQ8Row);
+  const float* sigma = pair_units(p);
   CUtensorMap tm, tq, tp;
   encode(&tm, cache, kRow, view_rows(p), fp8 ? 1 : 2, page < 64 ? page : 64,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (fp8) {
-    encode(&tq, codes, kQ8Row, 2 * rows, 1, kPHeads, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    encode(&tq, pair_codes(p), kQ8Row, 2 * rows, 1, kPHeads, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     tp = tq;
   } else {
     encode(&tq, p.q_abs, kDc, rows, 2, kPHeads, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
@@ -745,8 +796,10 @@ mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
     return MLA_ERR_CUDA;
   }
   if (!fp8) return launch_pair<false>(tm, tq, tp, p, nullptr, stream, who);
-  launch_pdl(pair_query_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream,
-             p, codes, sigma);
+  if (!p.late) {
+    const mla_status st = launch_pair_queries(p, stream, who);
+    if (st != MLA_OK) return st;
+  }
   return launch_pair<true>(tm, tq, tp, p, sigma, stream, who);
 }
 

@@ -43,6 +43,7 @@ struct SelectParams {
   int width;            // pages of s_max rows
   int page_shift, table_stride, num_pages;
   int top, keep_first, keep_last;
+  int early;            // the reader of the choice waits for it before it reads anything of it
 };
 
 // Rows token r attends (as the attention kernels clamp them).
@@ -118,6 +119,24 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t biased) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
+// One elected thread of the converged warp issues.  (From a branch of one thread the
+// operands' moves to uniform registers cost over 100 cycles an MMA.)
+__device__ __forceinline__ void mma_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
+      : "memory");
+}
+
 // grid (ceil(width / 128), R).  The CTA's 128 pages (rows of the table, so
 // anywhere in the pool) are read as int8, 576 bytes a page, and written to
 // shared memory as the fp16 A operand; the query image of a head group is the B
@@ -134,15 +153,17 @@ static_assert(kScoreSmem + 4096 <= 232448, "shared memory");
 __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const SelectParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_id[kScorePages];
-  __shared__ float s_scale[kScorePages], s_half[kScorePages];
+  __shared__ float s_scale[kScorePages], s_half[kScorePages], s_a[kMaxGroup];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_bar[2];   // query image landed; MMAs finished
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem), bars = smem_u32(s_bar);
   const int r = blockIdx.y, j0 = blockIdx.x * kScorePages;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
   const int P = token_pages(p, token_rows(p, r, false));
+  pdl_launch_dependents();             // the choice waits for this grid before it reads
   if (P <= p.top || j0 >= P) return;   // every page is kept, or none of these exists
   if (tid < kScorePages) {
     const int j = j0 + tid;
@@ -206,21 +227,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
   if (tid == 0) load_group(0);
   float best = -INFINITY;
   bool ok = true;
+  const uint32_t idesc = idesc_f16(kScorePages, p.group);
+  const uint64_t da0 = umma_desc_sw128(sbase + kOffPages, 16, 1024);
+  const uint64_t db0 = umma_desc_sw128(sbase + kOffQuery, 16, 1024);
   for (int g = 0; g < p.groups; ++g) {
-    if (tid == 0) {
-      if (mbar_wait_bounded(bars, g & 1)) {
-        tc_fence_after();
-        const uint32_t idesc = idesc_f16(kScorePages, p.group);
-        for (int i = 0; i < kBoxes; ++i) {
-          const uint64_t da = umma_desc_sw128(sbase + kOffPages + i * kPageBox, 16, 1024);
-          const uint64_t db = umma_desc_sw128(sbase + kOffQuery + i * p.group * 128, 16, 1024);
+    if (warp == 0 && __all_sync(0xffffffffu, mbar_wait_bounded(bars, g & 1))) {
+      // The warp issues as one (see mma_elected); boxes are not unrolled, so that the
+      // loop's code is fetched once.
+      tc_fence_after();
+#pragma unroll 1
+      for (int i = 0; i < kBoxes; ++i) {
+        const uint64_t da = da0 + static_cast<uint64_t>(i * (kPageBox >> 4));
+        const uint64_t db = db0 + static_cast<uint64_t>(i * p.group * 8);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)   // 16 columns (32 bytes) a step
-            umma_bf16(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0 ? 1u : 0u);
-        }
-        umma_commit(bars + 8);
+        for (int k = 0; k < 4; ++k)   // 16 columns (32 bytes) a step
+          mma_elected(tmem, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : (i > 0 ? 1u : 0u));
       }
+      commit_elected(bars + 8);
     }
+    __syncwarp();
+    if (tid >= 64 && tid < 64 + p.group) s_a[tid - 64] = a[g * p.group + tid - 64];
     // Every thread waits for the accumulators (bounded: a copy that never landed
     // leaves the MMAs unissued, and every thread gives up).
     ok = __syncthreads_and(mbar_wait_bounded(bars + 8, g & 1));
@@ -235,7 +261,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int h = g * p.group + c0 + c + i;
-        if (h < p.H) best = fmaxf(best, a[h] * __uint_as_float(d[i]));
+        if (h < p.H) best = fmaxf(best, s_a[c0 + c + i] * __uint_as_float(d[i]));
       }
     }
     tc_fence_before();
@@ -254,10 +280,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
   if (warp == 0) tmem_dealloc(tmem, 64);
 }
 
-// One CTA per token.  Radix selection, eight bits a pass from the top, finds the
-// score of the last page kept (scores as unsigned integers in the same order)
-// and how many pages tied with it are kept; one ordered pass then writes the
-// kept pages.  Bound by latency: five passes over at most a few thousand scores.
+// One CTA per token.  Radix selection (scores as unsigned integers in the same order),
+// eight bits a pass from the highest bit in which any two differ, narrows down the score
+// of the last page kept until the pages that share its leading bits are all kept, or only
+// equal scores are left, of which the lowest positions are kept; one ordered pass then
+// writes the kept pages.  Bound by latency; from the top byte on, with scores of similar
+// size, the first passes count everything in one bin (five passes and its atomics: 7.5 us
+// for 1024 pages).
 constexpr int kPickThreads = 1024;
 constexpr int kPickHold = 8192;   // scores kept in shared memory, else read again each pass
 
@@ -268,12 +297,13 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
 
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
   __shared__ uint32_t keys[kPickHold];
-  __shared__ int hist[256], s_found[2], s_part[32];
+  __shared__ int hist[256], s_found[3], s_part[32];
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = token_rows(p, r, tid == 0);
   const int P = token_pages(p, n);
   const int32_t* row = p.table + static_cast<size_t>(r / p.q_len) * p.table_stride;
   int32_t* out = p.sel_table + static_cast<size_t>(r) * p.top;
+  if (p.early) pdl_launch_dependents();
   pdl_wait();   // the scores; and the readers of the last choice are done
   if (P <= p.top) {
     for (int j = tid; j < p.top; j += kPickThreads) out[j] = j < P ? row[j] : -1;
@@ -288,9 +318,27 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
   auto key = [&](int j) { return held ? keys[j - lo] : ordered_bits(scores[j]); };
   int want = p.top - p.keep_first - p.keep_last;   // of the scored pages, fewer than there are
   uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  if (tid < 256) hist[tid] = 0;
+  if (want > 0) {
+    // The bits in which any key differs from the first.
+    const uint32_t key0 = ordered_bits(scores[lo]);
+    uint32_t differ = 0;
+    for (int j = lo + tid; j < hi; j += kPickThreads) differ |= key(j) ^ key0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) differ |= __shfl_xor_sync(0xffffffffu, differ, off);
+    if (lane == 0) s_part[warp] = static_cast<int>(differ);
     __syncthreads();
+    differ = static_cast<uint32_t>(s_part[lane]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) differ |= __shfl_xor_sync(0xffffffffu, differ, off);
+    const int same = __clz(differ);   // leading bits that all keys share
+    mask = same > 0 ? ~(0xffffffffu >> same) : 0u;
+    if (same >= 32) mask = 0xffffffffu;
+    prefix = key0 & mask;
+  }
+  bool open = want > 0;   // pages with the prefix still to be told apart
+  while (open && mask != 0xffffffffu) {
+    const int shift = max(0, 24 - __popc(mask));   // eight more bits, or what is left
     for (int j = lo + tid; j < hi; j += kPickThreads) {
       const uint32_t k = key(j);
       if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
@@ -317,6 +365,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
         if (above < want && above + c[i] >= want) {
           s_found[0] = 255 - 8 * lane - i;
           s_found[1] = want - above;
+          s_found[2] = c[i];
         }
         above += c[i];
       }
@@ -325,9 +374,11 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
     prefix |= static_cast<uint32_t>(s_found[0]) << shift;
     mask |= 255u << shift;
     want = s_found[1];   // still wanted among the pages with this prefix
+    open = s_found[2] > want;
+    if (tid < 256) hist[tid] = 0;
     __syncthreads();
   }
-  // want: pages kept of those whose score equals the threshold (0: none scored).
+  // want: pages kept of those that have the prefix (0: none scored).
   const bool any = p.top > p.keep_first + p.keep_last;
   int base_more = 0, base_tie = 0;
   for (int j0 = 0; j0 < P; j0 += kPickThreads) {
@@ -335,7 +386,8 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
     const bool forced = j < P && (j < lo || j >= hi);
     const bool scored = any && j < P && !forced;
     const uint32_t k = scored ? key(j) : 0;
-    const int more = forced || (scored && k > prefix), tie = scored && k == prefix;
+    const int more = forced || (scored && (k & mask) > prefix);
+    const int tie = scored && (k & mask) == prefix;
     // Both counts in one scan: kept outright in the low half, ties in the high.
     const int packed = more | tie << 16;
     int incl = packed;
@@ -455,6 +507,7 @@ mla_status prepare_select(const char* who, const mla_dims* d, const mla_paging* 
   p->top = top;
   p->keep_first = keep_first;
   p->keep_last = keep_last;
+  p->early = 0;
   return MLA_OK;
 }
 
@@ -557,9 +610,13 @@ extern "C" mla_status mla_decode_attn_sparse(
   st = check_attn_paged(who, &d, &pg, io_dtype, q_abs, q_pe, cache, sel_table, sel_lengths,
                         softmax_scale, num_splits, attn_ws, ws_bytes - mine, o_c);
   if (st != MLA_OK) return st;
-  st = launch_select(who, p, static_cast<cudaStream_t>(stream));
+  p.early = 1;
+  // What the attention can do before it knows its pages goes first.
+  st = attn_queries(who, &d, &pg, io_dtype, q_abs, q_pe, sel_lengths, num_splits, attn_ws,
+                    ws_bytes - mine, stream);
+  if (st == MLA_OK) st = launch_select(who, p, static_cast<cudaStream_t>(stream));
   if (st != MLA_OK) return st;
-  return mla_decode_attn_paged(&d, &pg, io_dtype, 1, q_abs, q_pe, cache, sel_table, sel_lengths,
-                               softmax_scale, num_splits, attn_ws, ws_bytes - mine, o_c, lse,
-                               dev_status, stream);
+  return attn_selected(who, &d, &pg, io_dtype, q_abs, q_pe, cache, sel_table, sel_lengths,
+                       softmax_scale, num_splits, attn_ws, ws_bytes - mine, o_c, lse, dev_status,
+                       stream);
 }

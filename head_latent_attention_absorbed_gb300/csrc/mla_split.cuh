@@ -37,13 +37,16 @@ struct SplitParams {
   // split writes o_c (part_o, fp32 or bf16) and lse (part_lse, may be NULL) itself
   // and no combine follows.
   int direct;
+  // Attention over a page selection: table and lengths come from the kernel just before
+  // (which lets this one start early), so they are read after the PDL wait; the queries'
+  // FP8 codes were made before the selection.
+  int late;
 };
 
-// o_c = 0 and lse = -inf of `heads` heads from h0 of query group v, which attends
-// no row (direct calls; `threads` threads of the CTA, after the PDL wait).
-__device__ __forceinline__ void write_no_rows(const SplitParams& p, int v, int h0, int heads,
+// o_c = 0 and lse = -inf of `heads` heads from `row` (query group x H + head), which
+// attend no row (direct calls; `threads` threads of the CTA, after the PDL wait).
+__device__ __forceinline__ void write_no_rows(const SplitParams& p, size_t row, int heads,
                                               int tid, int threads) {
-  const size_t row = static_cast<size_t>(v) * p.H + h0;
   const size_t bytes = p.io_bf16 ? 2 : 4;
   uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.part_o) + row * kDc * bytes);
   for (int i = tid; i < static_cast<int>(heads * kDc * bytes / 16); i += threads)
@@ -103,11 +106,18 @@ __device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool re
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who);
 
-// The paged split with bf16 queries at multiples of 128 heads (mla_pair.cu): a pair
-// of SMs takes 128 heads; same partials, chunks of whole tiles.  With an E4M3 cache
-// the queries' codes go to p.q_img first.
+// The paged split with bf16 queries as SM pairs (mla_pair.cu): the query rows of a
+// sequence (heads x tokens) in groups of up to 128, two CTAs a group; same partials,
+// chunks of whole tiles.  With an E4M3 cache the queries' codes go to p.q_img first.
+constexpr int kPairRows = 128;
+inline int pair_groups(int rows) { return (rows + kPairRows - 1) / kPairRows; }
 mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
                              cudaStream_t stream, const char* who);
+
+// The kernels that make the queries' FP8 codes, which both calls above run first unless
+// p.late is set.
+mla_status launch_fp8_queries(const SplitParams& p, cudaStream_t stream, const char* who);
+mla_status launch_pair_queries(const SplitParams& p, cudaStream_t stream, const char* who);
 
 // Rows a cache view holds: B / q_len sequences of s_max rows, or a pool's pages.
 inline uint64_t view_rows(const SplitParams& p) {

@@ -565,12 +565,12 @@ mla_status mla_cache_append_paged(const mla_dims* dims, const mla_paging* paging
  *             query and P enter the tensor cores as hi + lo bf16 pairs at every
  *             head count.
  *   MLA_BF16  bf16 queries and outputs (bf16 and FP8 caches), as a serving
- *             engine keeps them.  The query enters as it is.  With a bf16 cache P
- *             is hi + lo, or at multiples of 64 heads one bf16 part (at most 2^-8
- *             relative: less in the weighted sum than the output's own rounding);
- *             with an FP8 cache P is three E4M3 parts, or two at multiples of 128
- *             heads (2^-8).  At multiples of 128 heads two CTAs on a pair of SMs
- *             take 128 heads, otherwise a CTA takes 64, 32 or 16.
+ *             engine keeps them.  The query enters as it is.  From 32 (bf16 cache) or
+ *             48 (FP8) query rows heads * q_len per sequence on, two CTAs on a pair of
+ *             SMs take up to 128 of them, and P is one bf16 part (at most 2^-8
+ *             relative: less in the weighted sum than the output's own rounding), or
+ *             with an FP8 cache an E4M3 part and its E5M2 remainder (2^-7); with fewer
+ *             rows P is as for MLA_F32.  mla_set_split_parts(2) asks for that always.
  * lse is fp32, accumulation fp32.
  *
  * q_abs [B*q_len, H, d_c], q_pe [B*q_len, H, d_rope], o_c [B*q_len, H, d_c]
