@@ -88,9 +88,7 @@ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One elected thread of the converged warp issues.  (From a branch of one thread an
-// MMA cost about 140 cycles, most of it moving its operands to uniform registers; in
-// warp-uniform code they stay there.)
+// One elected thread of the converged warp issues (as umma_bf16_elected).
 __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
@@ -99,23 +97,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t 
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_elected(uint32_t dst, const CUtensorMap* m, int x, int y,
-                                                 uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void commit_elected(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar)
-      : "memory");
-}
-
 __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
@@ -277,7 +258,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int r = __shfl_sync(0xffffffffu, row, i);
 #pragma unroll 1
       for (int m = 0; m < kF8Boxes; ++m)
-        tma_load_elected(sbase + kOffTile + bf * kF8Tile + m * kF8Box + i * box_rows * 128, &tmap,
+        tma_load_2d_elected(sbase + kOffTile + bf * kF8Tile + m * kF8Box + i * box_rows * 128, &tmap,
                          128 * m, r, bar(B_FULL + bf), pol);
     }
   };
@@ -348,7 +329,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (k < 2 || m < 4)
             umma_e4m3(d, a + 2 * k, q + 2 * k, idesc_s, k > 0 ? 1u : (m > 0 ? 1u : 0u));
       }
-      commit_elected(bar(B_SFULL + bf));
+      umma_commit_elected(bar(B_SFULL + bf));
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ query image, PV MMAs
@@ -379,10 +360,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
                     idesc_o, ks > 0 ? 1u : (t > 0 ? 1u : 0u));
       }
-      commit_elected(bar(B_ODONE + bf));
-      commit_elected(bar(B_EMPTY + bf));
+      umma_commit_elected(bar(B_ODONE + bf));
+      umma_commit_elected(bar(B_EMPTY + bf));
     }
-    commit_elected(bar(B_DONE));
+    umma_commit_elected(bar(B_DONE));
     mbar_wait_bounded(bar(B_DONE), 0);
   } else {
     // ------------------------------------------------------------ softmax warps

@@ -113,13 +113,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void expect_one(uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(bytes)
-      : "memory");
-}
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -355,7 +348,7 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
 #pragma unroll 1
       for (int k = 0; k < L::kBoxes; ++k) {
         warp_wait(bar(L::EMPTYS + sl), phase, abort_flag);
-        if (leader) expect_one(bar(L::FULLS + sl), 2 * kPBox);
+        if (leader) expect_tx_elected(bar(L::FULLS + sl), 2 * kPBox);
         const uint32_t dst = sbase + L::kOffS + sl * kPBox, full = lbar(L::FULLS + sl);
 #pragma unroll 1
         for (int i = 0; i < np; ++i)
@@ -372,7 +365,7 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
     // ------------------------------------------------------------ query, output operand (L2)
     const uint64_t stream = l2_evict_first_policy();
     pdl_wait();   // the query comes from the kernel before
-    if (leader) expect_one(bar(L::QFULL), 2 * L::kQBytes);
+    if (leader) expect_tx_elected(bar(L::QFULL), 2 * L::kQBytes);
 #pragma unroll 1
     for (int i = 0; i < L::kParts * L::kBoxes; ++i) {
       if (kFp8)
@@ -397,9 +390,9 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
       for (int u = 0; u < 4; ++u) {
         warp_wait(bar(L::EMPTYV + sl), phase, abort_flag);
         if (last)
-          expect_one(bar(L::LASTV + u), L::kUnit);
+          expect_tx_elected(bar(L::LASTV + u), L::kUnit);
         else if (leader)
-          expect_one(bar(L::FULLV + sl), 2 * L::kUnit);
+          expect_tx_elected(bar(L::FULLV + sl), 2 * L::kUnit);
         const uint32_t full = last ? mapa_shared(bar(L::LASTV + u), rank) : lbar(L::FULLV + sl);
         const uint32_t dst = sbase + L::kOffV + sl * L::kUnit;
         const int x = 256 * (u & 1) + 128 * rank;

@@ -119,24 +119,6 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t biased) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One elected thread of the converged warp issues.  (From a branch of one thread the
-// operands' moves to uniform registers cost over 100 cycles an MMA.)
-__device__ __forceinline__ void mma_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void commit_elected(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar)
-      : "memory");
-}
-
 // grid (ceil(width / 128), R).  The CTA's 128 pages (rows of the table, so
 // anywhere in the pool) are read as int8, 576 bytes a page, and written to
 // shared memory as the fp16 A operand; the query image of a head group is the B
@@ -232,7 +214,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
   const uint64_t db0 = umma_desc_sw128(sbase + kOffQuery, 16, 1024);
   for (int g = 0; g < p.groups; ++g) {
     if (warp == 0 && __all_sync(0xffffffffu, mbar_wait_bounded(bars, g & 1))) {
-      // The warp issues as one (see mma_elected); boxes are not unrolled, so that the
+      // The warp issues as one (see umma_bf16_elected; kind::f16 takes fp16 as well); boxes are not unrolled, so that the
       // loop's code is fetched once.
       tc_fence_after();
 #pragma unroll 1
@@ -241,9 +223,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
         const uint64_t db = db0 + static_cast<uint64_t>(i * p.group * 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k)   // 16 columns (32 bytes) a step
-          mma_elected(tmem, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : (i > 0 ? 1u : 0u));
+          umma_bf16_elected(tmem, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : (i > 0 ? 1u : 0u));
       }
-      commit_elected(bars + 8);
+      umma_commit_elected(bars + 8);
     }
     __syncwarp();
     if (tid >= 64 && tid < 64 + p.group) s_a[tid - 64] = a[g * p.group + tid - 64];
