@@ -189,18 +189,6 @@ __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity,
     if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
-// Exclusive prefix sum of x over the warp's lanes, and the warp's total.
-__device__ __forceinline__ int warp_exclusive_scan(int x, int lane, int* total) {
-  int incl = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  *total = __shfl_sync(0xffffffffu, incl, 31);
-  return incl - x;
-}
-
 // Persistent grid: the items of CTA c of G, computed by one whole warp.  Every
 // (head group, query group, chunk) with rows is an item; items are ordered by
 // head group, then query group, then chunk, which numbers every tile of every
@@ -1754,41 +1742,34 @@ __device__ __forceinline__ void store_out4(float* dst, float4 v) {
 __device__ __forceinline__ void store_out4(__nv_bfloat16* dst, float4 v) {
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
-constexpr int kCombineChunk = 20;
-template <typename Out>
-__global__ void __launch_bounds__(32)
-    combine_kernel(const SplitParams p, Out* o_c, float* lse_out) {
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int tid = blockIdx.z * 32 + threadIdx.x;   // float4 column of the 512
-  const int len = clamp_length(p, b, false);   // a caller input, not the split's output
-  pdl_wait();   // the partials come from the split kernel just before
-  int nsplit = (len + p.chunk - 1) / p.chunk;
-  if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
-  Out* out = o_c + (size_t(b) * p.H + h) * kDc;
-  if (nsplit == 0) {
-    store_out4(out + 4 * tid, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = -INFINITY;
-    if (threadIdx.x == 0) pdl_launch_dependents();
-    return;
-  }
-  const size_t row0 = (size_t(b) * p.H + h) * p.splits;   // this (b, h)'s chunks, contiguous
-  const float* lse_bh = p.part_lse + row0;
-  const float4* po = reinterpret_cast<const float4*>(p.part_o + row0 * kDc) + tid;
+// Partials of query group b, which attends len rows.  (The clamp matters after a split that
+// gave up before it had counted.)
+__device__ __forceinline__ int partials_of(const SplitParams& p, int b, int len) {
+  if (!p.pieces) return (len + p.chunk - 1) / p.chunk;
+  return len > 0 ? min(max(__ldcg(p.pieces + b), 0), p.splits) : 0;
+}
+constexpr int kCombineChunk = 20, kCombineFew = 4;
+constexpr long long kCombineFewRows = 512;
+// One thread's float4 column: the weighted mean of nsplit > 0 partials, and their joint
+// log-sum-exp; kGroup partials' loads in flight.
+template <int kGroup>
+__device__ __forceinline__ float4 combine_column(const float* lse_bh, const float4* po, int nsplit,
+                                                 float* lse) {
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < nsplit; s0 += kCombineChunk) {
-    float ls[kCombineChunk];
-    float4 v[kCombineChunk];
+  for (int s0 = 0; s0 < nsplit; s0 += kGroup) {
+    float ls[kGroup];
+    float4 v[kGroup];
 #pragma unroll
-    for (int u = 0; u < kCombineChunk; ++u) {
+    for (int u = 0; u < kGroup; ++u) {
       const bool ok = s0 + u < nsplit;
       ls[u] = ok ? lse_bh[s0 + u] : -INFINITY;
       v[u] = ok ? po[size_t(s0 + u) * (kDc / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (s0 + kCombineChunk >= nsplit && threadIdx.x == 0) pdl_launch_dependents();
+    if (s0 + kGroup >= nsplit && threadIdx.x == 0) pdl_launch_dependents();
     float cm = m;
 #pragma unroll
-    for (int u = 0; u < kCombineChunk; ++u) cm = fmaxf(cm, ls[u]);
+    for (int u = 0; u < kGroup; ++u) cm = fmaxf(cm, ls[u]);
     // cm is finite: every chunk with rows has a finite lse.
     const float r = m == -INFINITY ? 0.f : expf(m - cm);
     sum *= r;
@@ -1797,7 +1778,7 @@ __global__ void __launch_bounds__(32)
     acc.z *= r;
     acc.w *= r;
 #pragma unroll
-    for (int u = 0; u < kCombineChunk; ++u) {
+    for (int u = 0; u < kGroup; ++u) {
       const float w = s0 + u < nsplit ? expf(ls[u] - cm) : 0.f;
       sum += w;
       acc.x = fmaf(w, v[u].x, acc.x);
@@ -1808,8 +1789,35 @@ __global__ void __launch_bounds__(32)
     m = cm;
   }
   const float inv = 1.f / sum;
-  store_out4(out + 4 * tid, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = m + logf(sum);
+  *lse = m + logf(sum);
+  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+// grid (H, B, 128 / kThreads), a float4 column a thread.  Whole rows per CTA, since with a
+// CTA per warp the number of CTAs is what costs (4096 rows of two partials 17.6 us, so 5.4);
+// but many partials of few rows in CTAs of one warp, more of which find room beside the
+// split's last CTAs (16 of 128 rows, split and combine: 11.1 us against 12.0).
+template <typename Out, int kGroup, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    combine_kernel(const SplitParams p, Out* o_c, float* lse_out) {
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int tid = blockIdx.z * kThreads + threadIdx.x;   // float4 column of the 512
+  const int len = clamp_length(p, b, false);   // a caller input, not the split's output
+  pdl_wait();   // the partials come from the split kernel just before
+  int nsplit = partials_of(p, b, len);
+  if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
+  Out* out = o_c + (size_t(b) * p.H + h) * kDc;
+  if (nsplit == 0) {
+    store_out4(out + 4 * tid, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = -INFINITY;
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    return;
+  }
+  const size_t row0 = (size_t(b) * p.H + h) * p.splits;   // this (b, h)'s chunks, contiguous
+  float lse;
+  const float4 o = combine_column<kGroup>(
+      p.part_lse + row0, reinterpret_cast<const float4*>(p.part_o + row0 * kDc) + tid, nsplit, &lse);
+  store_out4(out + 4 * tid, o);
+  if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = lse;
 }
 
 // The same merge for many chunks (more than 16): grid (H, B, 4), CTA z owns
@@ -1834,7 +1842,7 @@ __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
   const int col = blockIdx.z * 32 + lane;      // float4 column of the 512
   const int len = clamp_length(p, b, false);   // a caller input, not the split's output
   pdl_wait();   // the partials come from the split kernel just before
-  int nsplit = (len + p.chunk - 1) / p.chunk;
+  int nsplit = partials_of(p, b, len);
   if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
   Out* out = o_c + (size_t(b) * p.H + h) * kDc;
   if (nsplit == 0) {
@@ -2031,16 +2039,17 @@ __global__ void __launch_bounds__(128)
 }
 
 // ------------------------------------------------------------------------- host side
-// Heads per CTA of the decode kernel: 32 for a bf16 cache whose head count
-// allows it, else 16 (the FP8 kernel always takes 16).
-// A paged call's choice goes by its query type: bf16 queries are one part as
-// they stand and a bf16 output rounds more than a one-part P does, while fp32
-// queries and outputs keep the hi + lo pairs at every head count.
+// Heads per CTA of the decode kernel: for a dense bf16 cache 64 or 32 where the head count
+// is a multiple, else 16 (the FP8 kernel always takes 16).
+// A paged call's choice goes by its query type: bf16 queries are one part as they stand and
+// run as SM pairs (64 heads per CTA) from the sizes below; fp32 queries and outputs keep the
+// hi + lo pairs at every head count.
 struct PlanOpts {
   bool pair = false;     // two tokens of a multi-token step per CTA
   bool paged = false;    // a paged cache: chunks are whole tiles
   int io = MLA_F32;      // query and output type of a paged call
   int q_len = 1;         // tokens per sequence
+  bool late = false;     // over a page selection
 };
 // Query rows (heads x tokens) of a sequence from which a paged call with bf16 queries
 // runs as SM pairs (mla_pair.cu), whose tile costs the same for 16 rows as for 128.
@@ -2049,6 +2058,12 @@ struct PlanOpts {
 // 65536, 16 rows 58 / 61, 32 70 / 63, 64 80 / 65; E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48
 // 19.5 / 18.1; 4 x 65536, 32 rows 60 / 53, 48 91 / 53.
 constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
+// Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
+// shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
+// 8192 rows, 64 sequences 56 / 46, 16 (6.7 tiles) 21.9 / 18.1, 8 (3.4) 15.3 / 15.7; all
+// full, 256 x 2048 79 / 78, 64 x 4096 43.4 / 43.9, 32 x 4096 (6.7) 23.8 / 24.9, 16 x 4096
+// (3.4) 15.5 / 18.1.
+constexpr int kShareMinTiles = 4;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
   return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
          d->heads * o.q_len >= (d->dtype == MLA_BF16 ? kPairMinBf16 : kPairMinFp8);
@@ -2056,7 +2071,7 @@ bool pair_form(const mla_dims* d, const PlanOpts& o) {
 int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
   if (pair_form(d, o)) return 64;
   if (d->dtype != MLA_BF16) return kHeadGroup;
-  if (d->heads % 64 == 0 && g_split_parts.load() != 2 && !(o.paged && o.io != MLA_BF16)) return 64;
+  if (d->heads % 64 == 0 && g_split_parts.load() != 2 && !o.paged) return 64;
   return d->heads % 32 == 0 ? 32 : kHeadGroup;
 }
 
@@ -2108,7 +2123,7 @@ struct SplitPlan {
   bool persist;
 };
 
-int device_sms() {
+long long current_sms() {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -2117,6 +2132,9 @@ int device_sms() {
   }
   return sms;
 }
+}  // namespace
+int share_runs(int groups) { return static_cast<int>(current_sms() / groups); }
+namespace {
 
 // Rows per KV chunk and the resulting chunk count, and the launch form.
 //  - One CTA per chunk.  With `requested` = 0 the count minimises a makespan
@@ -2150,7 +2168,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
 // work (measured: 19.6 us of host time per mla_decode_step call with it, from
 // Python with prepared arguments), so each thread keeps its last few answers.
 SplitPlan plan_split(const mla_dims* d, int requested, const PlanOpts& opts = {}) {
-  constexpr int kKeys = 12;
+  constexpr int kKeys = 13;
   struct Entry {
     int key[kKeys];
     SplitPlan plan;
@@ -2158,10 +2176,10 @@ SplitPlan plan_split(const mla_dims* d, int requested, const PlanOpts& opts = {}
   constexpr int kEntries = 8;
   thread_local Entry memo[kEntries];
   thread_local int filled = 0, next = 0;
-  const long long sms = device_sms();
+  const long long sms = current_sms();
   const int key[kKeys] = {d->batch, d->heads, d->s_max, d->dtype, requested, opts.pair ? 1 : 0,
                           g_split_form.load(), g_split_parts.load(), static_cast<int>(sms),
-                          opts.paged ? 1 : 0, opts.io, opts.q_len};
+                          opts.paged ? 1 : 0, opts.io, opts.q_len, opts.late ? 1 : 0};
   for (int i = 0; i < filled; ++i) {
     bool same = true;
     for (int k = 0; k < kKeys; ++k) same = same && memo[i].key[k] == key[k];
@@ -2232,6 +2250,15 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   }
   const bool np_one_wave = per_split * np_splits <= slots;
   const int form = g_split_form.load();
+  if (opts.paged && !opts.late && d->dtype == MLA_FP8_E4M3 && !pairs && requested <= 0 &&
+      form != 2 && d->batch <= kShareGroups && groups <= sms) {
+    // Equal shares of a paged FP8 cache's tiles: twice the partials that full sequences
+    // would need, so that shares may shrink with the lengths.
+    const long long seq = (S + kTileRows - 1) / kTileRows, runs = sms / groups;
+    const long long each = (d->batch * seq + runs - 1) / runs, half = (each + 1) / 2;
+    if (d->batch * seq < (1ll << 30) && (form == 1 || each >= kShareMinTiles))
+      return {np_chunk, static_cast<int>((seq + half - 1) / half + 1), true};
+  }
   if (!can_persist || form == 2 || (form == 0 && requested > 0 && np_one_wave))
     return {np_chunk, np_splits, false};
   // Persistent.
@@ -2269,15 +2296,18 @@ int chunk_rows(const mla_dims* d, int requested, int* splits_out, const PlanOpts
   return pl.chunk;
 }
 
-// Partial outputs, their log-sum-exps, and (FP8 cache) the query images.
-size_t workspace_bytes(const mla_dims* d, int splits) {
+// Partial outputs, their log-sum-exps, (FP8 cache) the query images and (paged) the
+// numbers of partials.
+size_t workspace_bytes(const mla_dims* d, int splits, bool paged = false) {
   const size_t n = size_t(d->batch) * splits * d->heads;
   const size_t o_bytes = (n * kDc * sizeof(float) + 255) / 256 * 256;
   const size_t lse_bytes = (n * sizeof(float) + 255) / 256 * 256;
   const size_t img = d->dtype == MLA_FP8_E4M3
                          ? (size_t(d->batch) * (d->heads / kHeadGroup) * kFp8QImage + 255) / 256 * 256
                          : 0;
-  return o_bytes + lse_bytes + img;
+  const size_t pieces =
+      paged && img ? (size_t(d->batch) * sizeof(int32_t) + 255) / 256 * 256 : 0;
+  return o_bytes + lse_bytes + img + pieces;
 }
 
 }  // namespace
@@ -2394,6 +2424,7 @@ static PlanOpts plan_opts(const mla_dims* dims, int q_len, const PagedView* view
   o.paged = view != nullptr;
   o.io = view ? view->io : MLA_F32;
   o.q_len = q_len;
+  o.late = view && view->late;
   o.pair = pair_tokens(dims, q_len) && !pair_form(dims, o);
   return o;
 }
@@ -2437,7 +2468,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   }
   const SplitPlan plan = plan_split(dims, num_splits, opts);
   const int splits = plan.splits, chunk = plan.chunk;
-  const size_t need = workspace_bytes(dims, splits);
+  const size_t need = workspace_bytes(dims, splits, view != nullptr);
   if (ws_bytes < need) {
     set_error("%s: workspace %zu bytes < %zu needed", who, ws_bytes, need);
     return MLA_ERR_WORKSPACE;
@@ -2474,6 +2505,10 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   p->io_bf16 = view && view->io == MLA_BF16 ? 1 : 0;
   p->direct = 0;
   p->late = view && view->late ? 1 : 0;
+  p->pieces = view && p->q_img && plan.persist
+                  ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + need) -
+                        (size_t(dims->batch) * sizeof(int32_t) + 255) / 256 * 64
+                  : nullptr;
   return MLA_OK;
 }
 
@@ -2536,10 +2571,9 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
     }
     const int per_cta = p.tpc == 2 ? 32 : tc_heads_per_cta(dims, plan_opts(dims, q_len, view));
     if (view)
-      st = per_cta == 64   ? launch_split_tc<64, false, true>(tmap, tmap_half, p, dims->heads, s, who)
-           : per_cta == 32 ? launch_split_tc<32, false, true>(tmap, tmap_half, p, dims->heads, s, who)
-           : p.persist     ? launch_split_tc<16, true, true>(tmap, tmap_half, p, dims->heads, s, who)
-                           : launch_split_tc<16, false, true>(tmap, tmap_half, p, dims->heads, s, who);
+      st = per_cta == 32 ? launch_split_tc<32, false, true>(tmap, tmap_half, p, dims->heads, s, who)
+           : p.persist ? launch_split_tc<16, true, true>(tmap, tmap_half, p, dims->heads, s, who)
+                       : launch_split_tc<16, false, true>(tmap, tmap_half, p, dims->heads, s, who);
     else
       st = per_cta == 64   ? launch_split_tc<64, false>(tmap, tmap_half, p, dims->heads, s, who)
          : per_cta == 32 ? launch_split_tc<32, false>(tmap, tmap_half, p, dims->heads, s, who)
@@ -2559,9 +2593,18 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
 template <typename Out>
 static void launch_combine(const SplitParams& p, int heads, Out* o_c, float* lse,
                            cudaStream_t s) {
-  const int cw = combine_warps(p.splits);
-  if (cw == 1)
-    launch_pdl(combine_kernel<Out>, dim3(heads, p.B, kDc / 128), dim3(32), 0, s, p, o_c, lse);
+  // An equal-share plan has room for twice the partials of full sequences.
+  const int cw = combine_warps(p.pieces ? p.splits / 2 : p.splits);
+  // Few partials: fewer slots, so fewer registers and more CTAs per SM.
+  const bool few = p.splits <= (p.pieces ? 4 * kCombineFew : kCombineFew);
+  const bool quarters = !few && static_cast<long long>(heads) * p.B <= kCombineFewRows;
+  if (cw == 1 && quarters)
+    launch_pdl(combine_kernel<Out, kCombineChunk, 32>, dim3(heads, p.B, kDc / 128), dim3(32), 0, s,
+               p, o_c, lse);
+  else if (cw == 1)
+    launch_pdl(few ? combine_kernel<Out, kCombineFew, 128>
+                   : combine_kernel<Out, kCombineChunk, 128>,
+               dim3(heads, p.B), dim3(128), 0, s, p, o_c, lse);
   else
     launch_pdl(combine_warps_kernel<Out>, dim3(heads, p.B, kDc / 128), dim3(32 * cw),
                size_t(cw) * (32 * sizeof(float4) + 2 * sizeof(float)), s, p, o_c, lse);
@@ -2679,13 +2722,23 @@ extern "C" int32_t mla_paged_num_splits(const mla_dims* dims, const mla_paging* 
   return splits;
 }
 
+size_t mla::selected_workspace_bytes(const char* who, const mla_dims* dims,
+                                     const mla_paging* paging, int32_t io_dtype,
+                                     int32_t requested) {
+  if (check_paged(who, dims, paging, io_dtype, 1) != MLA_OK) return 0;
+  const PagedView view{paging, nullptr, io_dtype, true};
+  int splits = 0;
+  chunk_rows(dims, requested, &splits, plan_opts(dims, 1, &view));
+  return workspace_bytes(dims, splits, true);
+}
+
 extern "C" size_t mla_paged_workspace_bytes(const mla_dims* dims, const mla_paging* paging,
                                             int32_t io_dtype, int32_t q_len, int32_t requested) {
   const int splits = mla_paged_num_splits(dims, paging, io_dtype, q_len, requested);
   if (splits == 0) return 0;
   mla_dims qd = *dims;
   qd.batch = dims->batch * q_len;
-  return workspace_bytes(&qd, splits);
+  return workspace_bytes(&qd, splits, true);
 }
 
 static mla_status check_attn(const char* who, const mla_dims* dims, const PagedView& view,
@@ -2703,12 +2756,12 @@ static mla_status check_attn(const char* who, const mla_dims* dims, const PagedV
                  workspace, ws_bytes, nullptr, &p, &view);
 }
 
-mla_status mla::check_attn_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
+mla_status mla::check_attn_selected(const char* who, const mla_dims* dims, const mla_paging* paging,
                                  int32_t io_dtype, const void* q_abs, const void* q_pe,
                                  const void* cache, const int32_t* block_table,
                                  const int32_t* lengths, float softmax_scale, int32_t num_splits,
                                  void* workspace, size_t ws_bytes, void* o_c) {
-  return check_attn(who, dims, PagedView{paging, block_table, io_dtype}, 1, q_abs, q_pe, cache,
+  return check_attn(who, dims, PagedView{paging, block_table, io_dtype, true}, 1, q_abs, q_pe, cache,
                     lengths, softmax_scale, num_splits, workspace, ws_bytes, o_c);
 }
 
@@ -2752,7 +2805,7 @@ mla_status mla::attn_queries(const char* who, const mla_dims* dims, const mla_pa
                              const int32_t* lengths, int32_t num_splits, void* workspace,
                              size_t ws_bytes, void* stream) {
   if (dims->dtype != MLA_FP8_E4M3) return MLA_OK;
-  const PagedView view{paging, lengths, io_dtype};   // the table is not read here
+  const PagedView view{paging, lengths, io_dtype, true};   // the table is not read here
   SplitParams p;
   const mla_status st = prepare(who, dims, 1, q_abs, q_pe, nullptr, lengths, 1.f, num_splits,
                                 workspace, ws_bytes, nullptr, &p, &view);

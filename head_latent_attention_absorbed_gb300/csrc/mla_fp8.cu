@@ -67,13 +67,14 @@ enum {
   B_SFREE = 6,     // [2] softmax read S[t & 1]
   B_PFULL = 8,     // [2] P of the tile written (and the tile's dead rows zeroed)
   B_ODONE = 10,    // [2] PV of the tile finished
-  B_QREADY = 12,   // query parts written
+  B_QREADY = 12,   // query parts written (once an item)
   B_DONE = 13,     // every MMA finished
   kNumBars = 14
 };
 constexpr int kOffSlot = kOffBar + 8 * kNumBars;
 constexpr int kOffAbort = kOffSlot + 16;
-constexpr size_t kF8Smem = 1024 + kOffAbort + 16;
+constexpr int kOffShare = kOffAbort + 16;   // TileShare of the CTA
+constexpr size_t kF8Smem = 1024 + kOffShare + 32;
 constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64 (64 columns each), O^T at 128..319
 constexpr uint32_t kOCol = 128;       // O^T block mb at kOCol + kPN mb
 constexpr float kRescaleLog2 = 8.f;
@@ -196,9 +197,20 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
   }
 }
 
+// One item of a CTA: consecutive tiles of one query group.
+struct F8Item {
+  int v, j;       // query group, index of the partial among its own
+  int r0, tiles;  // first row, 128-row tiles
+  int len;        // rows the query group attends
+};
+
 // kPaged: the cache is a pool of pages; a tile's boxes are boxes of up to 128
 // rows of one page each, one lane of the producer warp per page.
-template <bool kPaged>
+// kShare (paged): one CTA per SM takes an equal run of all query groups' tiles (take_share),
+// one item per query group it meets, streamed back to back: the copies and score MMAs of
+// the next item run while the last one's output is written.  Otherwise a CTA has one item,
+// its chunk.
+template <bool kPaged, bool kShare>
 __global__ void __launch_bounds__(kF8Threads, 1)
     split_fp8_kernel(const __grid_constant__ CUtensorMap tmap, const SplitParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -213,29 +225,48 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   auto bar = [&](int i) { return bars + 8 * i; };
 
-  const int g = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
-  if (kPaged && p.late) pdl_wait();
-  const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
-  const int r0 = j * p.chunk;
-  if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
-    if (kPaged && p.direct) {
-      pdl_wait();
-      write_no_rows(p, size_t(b) * p.H + g * kHeadGroup, kHeadGroup, tid, kF8Threads);
+  const int groups = p.H / kHeadGroup;
+  const int g = kShare ? blockIdx.x % groups : blockIdx.x, h0 = g * kHeadGroup;
+  F8Item first;    // the CTA's first item
+  int T, row_end;  // tiles of the CTA; row at which an item that ends inside a sequence ends
+  TileShare share;
+  if (!kShare) {
+    const int j = blockIdx.y, b = blockIdx.z;
+    if (kPaged && p.late) pdl_wait();
+    const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
+    const int r0 = j * p.chunk;
+    if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
+      if (kPaged && p.direct) {
+        pdl_wait();
+        write_no_rows(p, size_t(b) * p.H + h0, kHeadGroup, tid, kF8Threads);
+      }
+      return;
     }
-    return;
+    row_end = min(r0 + p.chunk, len);
+    T = (row_end - r0 + kF8Rows - 1) / kF8Rows;
+    first = F8Item{b, j, r0, T, len};
   }
-  const int r1 = min(r0 + p.chunk, len);
-  const int T = (r1 - r0 + kF8Rows - 1) / kF8Rows;
-  const int last_valid = r1 - (r0 + (T - 1) * kF8Rows);
-  // Rows of the last tile past the sequence's end may hold anything (NaN
-  // included); they are zeroed before its PV.  Rows past the chunk but inside
-  // the sequence are finite and get P = 0.
-  const int zero_from = len - (r0 + (T - 1) * kF8Rows);
-  const bool zero_last = zero_from < kF8Rows;
-  const int row_base = kPaged ? r0 : cache_seq(p, b) * p.s_max + r0;
-  const int h0 = g * kHeadGroup;
+  auto first_item = [&] {   // of a share
+    T = share.tiles;
+    const int len = clamp_length(p, share.v, false);
+    first = F8Item{share.v, share.off > 0 ? static_cast<int>(blockIdx.x / groups) -
+                                                (share.first - share.off) / share.each
+                                          : 0,
+                   share.off * kF8Rows, min((len + kF8Rows - 1) / kF8Rows - share.off, T), len};
+  };
+  // The item after `it`, which ends before the CTA's tile t < T: the start of the next
+  // query group that attends any row.
+  auto next_item = [&](F8Item it, int t) {
+    do {
+      ++it.v;
+      it.len = clamp_length(p, it.v, false);
+    } while (it.len == 0 && it.v + 1 < p.B);
+    it.j = it.r0 = 0;
+    it.tiles = max(1, min((it.len + kF8Rows - 1) / kF8Rows, T - t));
+    return it;
+  };
 
   // The cache stream starts first: the producer warp sets up the barriers and
   // issues the first two tiles before the CTA-wide barrier.
@@ -243,12 +274,23 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   // the first row of piece i, and the next tile's are looked up ahead.
   const int box_rows = kPaged ? min(1 << p.page_shift, kF8Rows) : kF8Rows;
   const int pieces = kF8Rows / box_rows;
-  auto piece_row = [&](int t) {
-    return kPaged ? paged_row(p, cache_seq(p, b), r0 + t * kF8Rows + lane * box_rows,
-                              lane * box_rows < kF8Rows ? len : 0)
-                  : row_base + t * kF8Rows;
+  auto piece_row = [&](const F8Item& it, int i) {   // of the item's tile i
+    const int r = it.r0 + i * kF8Rows;
+    return kPaged ? paged_row(p, cache_seq(p, it.v), r + lane * box_rows,
+                              lane * box_rows < kF8Rows ? it.len : 0)
+                  : cache_seq(p, it.v) * p.s_max + r;
   };
   const uint64_t pol = l2_evict_first_policy();
+  // The query image of group v, by one thread.  Of a share the scales stay behind: this
+  // copy may run ahead of the softmax, which reads them from global memory.
+  auto load_query = [&](int v) {
+    const uint8_t* img = p.q_img + (size_t(v) * groups + g) * kFp8QImage;
+    mbar_arrive_expect_tx(bar(B_QREADY),
+                          static_cast<uint32_t>(kShare ? kFp8QBoxes : kFp8QImage));
+    bulk_g2s(sbase + kOffQ, img, static_cast<uint32_t>(kFp8QBoxes), bar(B_QREADY));
+    if (!kShare)
+      bulk_g2s(sbase + kOffSigma, img + kFp8QBoxes, 16 * sizeof(float), bar(B_QREADY));
+  };
   auto issue = [&](int t, int row) {
     const int bf = t & 1;
     if (lane == 0) mbar_arrive_expect_tx(bar(B_FULL + bf), kF8Tile);
@@ -262,8 +304,31 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                          128 * m, r, bar(B_FULL + bf), pol);
     }
   };
+  // The producer's place: its next tile is tile i of `it`, with pieces at `row`; step()
+  // moves on after tile t.
+  F8Item it;
+  int i = 0, row = 0;
+  auto step = [&](int t) {
+    if (t + 1 >= T) return;
+    if (++i == it.tiles) {
+      it = next_item(it, t + 1);
+      i = 0;
+    }
+    row = piece_row(it, i);
+  };
   if (warp == 8) {
-    const int row0 = piece_row(0), row1 = T > 1 ? piece_row(1) : 0;
+    if (kShare) {
+      share = take_share(p, blockIdx.x / groups, gridDim.x / groups, lane, blockIdx.x == 0);
+      if (lane == 0) *reinterpret_cast<TileShare*>(smem + kOffShare) = share;
+      if (share.tiles > 0)
+        first_item();
+      else
+        T = 0;
+    }
+    if (T > 0) {
+      it = first;
+      row = piece_row(it, 0);
+    }
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(B_FULL + i), 1);
@@ -280,25 +345,49 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       prefetch_tmap(&tmap);
     }
     __syncwarp();
-    issue(0, row0);
-    if (T > 1) issue(1, row1);
-    tmem_alloc(smem_u32(slot_ptr), kTmemCols);
+    if (!kShare) {   // both first tiles belong to the one item
+      for (int t = 0; t < min(T, 2); ++t) {
+        issue(t, row);
+        step(t);
+      }
+    } else if (T > 0) {
+      issue(0, row);
+    }
+    if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kShare) {
+    share = *reinterpret_cast<const TileShare*>(smem + kOffShare);
+    if (share.tiles <= 0) {   // more CTAs than tiles
+      pdl_wait();
+      return;
+    }
+    if (warp != 8) first_item();
+  }
   const uint32_t tmem = *slot_ptr;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
-    int issued = T < 2 ? T : 2, row = T > 2 ? piece_row(2) : 0;
-    for (int t = 2; t < T; ++t) {
-      const int next = t + 1 < T ? piece_row(t + 1) : 0;
-      f8_warp_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+    int issued = kShare ? 1 : min(T, 2);
+    if (kShare) step(0);
+    for (int t = issued; t < T; ++t) {
+      if (t >= 2) f8_warp_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       issue(t, row);
       issued = t + 1;
-      row = next;
+      if (kShare && i == 0) {
+        // The next item's query, once the last score MMA of the one before has read its own.
+        f8_warp_wait(bar(B_SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        if (lane == 0) {
+          pdl_wait();
+          load_query(it.v);
+        }
+        __syncwarp();
+      }
+      step(t);
     }
     // Tiles still in flight land before the CTA may leave (bounded waits).
     for (int t = issued > 2 ? issued - 2 : 0; t < issued; ++t)
@@ -310,9 +399,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     constexpr uint32_t idesc_s = idesc_e4m3(128, kQN, 0);
     const uint64_t a0 = umma_desc_sw128(sbase + kOffTile, 16, 1024);
     const uint64_t q0 = umma_desc_sw128(sbase + kOffQ, 16, 1024);
-    f8_warp_wait(bar(B_QREADY), 0, abort_flag);
+    F8Item cur = first;
+    int left = 0, n = 0;   // tiles left of the item; items begun
     for (int t = 0; t < T; ++t) {
       const int bf = t & 1;
+      if (left == 0) {
+        if (t > 0) cur = next_item(cur, t);
+        left = cur.tiles;
+        if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
+          // The run with a query group's first tile says how many runs it spans.
+          const int s = share.first + t, tiles = (cur.len + kF8Rows - 1) / kF8Rows;
+          p.pieces[cur.v] = (s + tiles - 1) / share.each - s / share.each + 1;
+        }
+        f8_warp_wait(bar(B_QREADY), n & 1, abort_flag);
+        ++n;
+      }
+      --left;
       f8_warp_wait(bar(B_FULL + bf), (t >> 1) & 1, abort_flag);
       if (t >= 2) f8_warp_wait(bar(B_SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
@@ -335,17 +437,20 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // ------------------------------------------------------------ query image, PV MMAs
     if (lane == 0) {
       pdl_wait();   // the image is written by the kernel before
-      const uint8_t* img = p.q_img + (size_t(b) * (p.H / kHeadGroup) + g) * kFp8QImage;
-      mbar_arrive_expect_tx(bar(B_QREADY), static_cast<uint32_t>(kFp8QImage));
-      bulk_g2s(sbase + kOffQ, img, static_cast<uint32_t>(kFp8QBoxes), bar(B_QREADY));
-      bulk_g2s(sbase + kOffSigma, img + kFp8QBoxes, 16 * sizeof(float), bar(B_QREADY));
+      load_query(first.v);
     }
     __syncwarp();
     constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
     const uint64_t p0 = umma_desc_sw128(sbase + kOffP, 16, 1024);
     const uint64_t c0 = umma_desc_sw128(sbase + kOffTile, kF8Box, 1024);
-    for (int t = 0; t < T; ++t) {
+    F8Item cur = first;
+    int done = 0;   // tiles of the item accumulated
+    for (int t = 0; t < T; ++t, ++done) {
       const int bf = t & 1;
+      if (kShare && done == cur.tiles) {
+        cur = next_item(cur, t);
+        done = 0;
+      }
       f8_warp_wait(bar(B_PFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
@@ -358,7 +463,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
           umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
-                    idesc_o, ks > 0 ? 1u : (t > 0 ? 1u : 0u));
+                    idesc_o, ks > 0 ? 1u : (done > 0 ? 1u : 0u));
       }
       umma_commit_elected(bar(B_ODONE + bf));
       umma_commit_elected(bar(B_EMPTY + bf));
@@ -372,205 +477,236 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int row = 32 * wq + lane;                     // tile row held by this thread
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
 
-    f8_warp_wait(bar(B_QREADY), 0, abort_flag);   // the query image and its scales
+    const int last_rows = kShare ? 0 : row_end - (first.r0 + (first.tiles - 1) * kF8Rows);
+    F8Item cur = first;
     float qsig[kHalf];
+    auto read_scales = [&] {   // of the item
+      const float4* sg = reinterpret_cast<const float4*>(
+          p.q_img + (size_t(cur.v) * groups + g) * kFp8QImage + kFp8QBoxes + 4 * hb);
+      const float4 s0 = __ldcg(sg), s1 = __ldcg(sg + 1);
+      const float s[kHalf] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-    for (int h = 0; h < kHalf; ++h) qsig[h] = sigma[hb + h] * p.scale_log2;
-
-    float m[kHalf], l[kHalf];
+      for (int h = 0; h < kHalf; ++h) qsig[h] = s[h] * p.scale_log2;
+    };
+    if (kShare) {
+      // Not by B_QREADY, which may move on by two phases before a slow warp looks.
+      pdl_wait();
+      read_scales();
+    } else {
+      f8_warp_wait(bar(B_QREADY), 0, abort_flag);   // the query image and its scales
 #pragma unroll
-    for (int h = 0; h < kHalf; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+      for (int h = 0; h < kHalf; ++h) qsig[h] = sigma[hb + h] * p.scale_log2;
     }
-    for (int t = 0; t < T; ++t) {
-      const int sb = t & 1;
-      const int valid = t == T - 1 ? last_valid : kF8Rows;
-      f8_warp_wait(bar(B_SFULL + sb), (t >> 1) & 1, abort_flag);
-      tc_fence_after();
-      float sc[kHalf], tt[kHalf];
-      {
-        uint32_t s1[8], s2[8], s3[8], s4[8];
-        tmem_ld8_nowait(tmem + lane_base + 64 * sb + hb, s1);
-        tmem_ld8_nowait(tmem + lane_base + 64 * sb + kHeadGroup + hb, s2);
-        tmem_ld8_nowait(tmem + lane_base + 64 * sb + 2 * kHeadGroup + hb, s3);
-        tmem_ld8_nowait(tmem + lane_base + 64 * sb + 3 * kHeadGroup + hb, s4);
-        tmem_wait_ld();
-        const bool rv = row < valid;
+    for (int t0 = 0; t0 < T;) {   // items; t0: the item's first tile among the CTA's
+      const int tiles = cur.tiles;
+      // Rows of the last tile past the sequence's end may hold anything (NaN
+      // included); they are zeroed before its PV.  Rows past the chunk but inside
+      // the sequence are finite and get P = 0.
+      const int zero_from = cur.len - (cur.r0 + (tiles - 1) * kF8Rows);
+      const bool zero_last = zero_from < kF8Rows;
+      const int last_valid = kShare ? min(zero_from, kF8Rows) : last_rows;
+
+      float m[kHalf], l[kHalf];
+#pragma unroll
+      for (int h = 0; h < kHalf; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      for (int t = t0; t < t0 + tiles; ++t) {
+        const int sb = t & 1;
+        const int valid = t == t0 + tiles - 1 ? last_valid : kF8Rows;
+        f8_warp_wait(bar(B_SFULL + sb), (t >> 1) & 1, abort_flag);
+        tc_fence_after();
+        float sc[kHalf], tt[kHalf];
+        {
+          uint32_t s1[8], s2[8], s3[8], s4[8];
+          tmem_ld8_nowait(tmem + lane_base + 64 * sb + hb, s1);
+          tmem_ld8_nowait(tmem + lane_base + 64 * sb + kHeadGroup + hb, s2);
+          tmem_ld8_nowait(tmem + lane_base + 64 * sb + 2 * kHeadGroup + hb, s3);
+          tmem_ld8_nowait(tmem + lane_base + 64 * sb + 3 * kHeadGroup + hb, s4);
+          tmem_wait_ld();
+          const bool rv = row < valid;
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {
+            const float s = __uint_as_float(s1[h]) +
+                            (__uint_as_float(s2[h]) * 0.0625f +
+                             (__uint_as_float(s3[h]) * 0.00390625f +
+                              __uint_as_float(s4[h]) * 0.000244140625f));
+            sc[h] = rv ? s * qsig[h] : -INFINITY;
+            tt[h] = sc[h];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
+        // tile maximum per head: warp, then the group's four warps
+#pragma unroll
+        for (int h = 0; h < kHalf; ++h)
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
+        float* rd = red + sb * kHeadGroup * 4;
+        if (lane < kHalf) {
+          float v = tt[0];
+#pragma unroll
+          for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
+          rd[(hb + lane) * 4 + wq] = v;
+        }
+        named_bar_sync(1, kF8Soft);
+        bool need = false;
+        float tmax[kHalf];
 #pragma unroll
         for (int h = 0; h < kHalf; ++h) {
-          const float s = __uint_as_float(s1[h]) +
-                          (__uint_as_float(s2[h]) * 0.0625f +
-                           (__uint_as_float(s3[h]) * 0.00390625f +
-                            __uint_as_float(s4[h]) * 0.000244140625f));
-          sc[h] = rv ? s * qsig[h] : -INFINITY;
-          tt[h] = sc[h];
+          const float4 q4 = *reinterpret_cast<const float4*>(rd + (hb + h) * 4);
+          tmax[h] = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
+          need |= tmax[h] > m[h] + kRescaleLog2;
         }
+        if (need) {
+          // Move this group's reference maxima; rescale its row sums and the O^T
+          // columns it owns (in TMEM, after the previous PV finished).
+          float alpha[kHalf];
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {
+            const float mn = fmaxf(m[h], tmax[h]);
+            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= alpha[h];
+          }
+          if (t > t0) {
+            f8_warp_wait(bar(B_ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+              for (int part = 0; part < kPParts; ++part) {
+                const uint32_t col = kOCol + kPN * mb + kHeadGroup * part + hb;
+                uint32_t r[8];
+                float o[8];
+                tmem_ld8_nowait(tmem + lane_base + col, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < kHalf; ++h) o[h] = __uint_as_float(r[h]) * alpha[h];
+                tmem_st8(tmem + lane_base + col, o);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // p in [0, 2^8] as three E4M3 parts, two heads per conversion; the row
+        // sum takes the value the PV uses.
+        uint16_t pp[kPParts][kHalf / 2];
+#pragma unroll
+        for (int h2 = 0; h2 < kHalf / 2; ++h2) {
+          float v0, v1;
+          {
+            const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
+            const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
+            v0 = ex2(sc[2 * h2] - mu0);
+            v1 = ex2(sc[2 * h2 + 1] - mu1);
+          }
+          float used0 = 0.f, used1 = 0.f, wgt = 1.f;
+#pragma unroll
+          for (int part = 0; part < kPParts; ++part) {
+            pp[part][h2] = to_e4m3x2(v0, v1);
+            const float2 f = from_e4m3x2(pp[part][h2]);
+            used0 += f.x * wgt;
+            used1 += f.y * wgt;
+            v0 = (v0 - f.x) * 16.f;
+            v1 = (v1 - f.y) * 16.f;
+            wgt *= 0.0625f;
+          }
+          l[2 * h2] += used0;
+          l[2 * h2 + 1] += used1;
+        }
+        // P^T buffer sb was last read by the PV of tile t-2.
+        if (t >= 2) f8_warp_wait(bar(B_ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
+        {
+          // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
+          // 16 part + n is part `part` of head n; the K index is the tile row.
+          uint8_t* pbuf = smem + kOffP + sb * kPBuf;
+#pragma unroll
+          for (int part = 0; part < kPParts; ++part)
+#pragma unroll
+            for (int h2 = 0; h2 < kHalf / 2; ++h2) {
+              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2, row)] = pp[part][h2] & 0xFF;
+              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2 + 1, row)] = pp[part][h2] >> 8;
+            }
+        }
+        if (t == t0 + tiles - 1 && zero_last) {
+          // Latent boxes 0-3 of the last tile: rows past the sequence's end -> 0.
+          uint8_t* tile = smem + kOffTile + (t & 1) * kF8Tile;
+          const int nrow = kF8Rows - zero_from;
+          for (int c = tid; c < 4 * nrow * 8; c += kF8Soft) {
+            const int mb = c / (nrow * 8), rem = c % (nrow * 8);
+            *reinterpret_cast<uint4*>(tile + mb * kF8Box + (zero_from + rem / 8) * 128 + (rem % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + sb));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
-      // tile maximum per head: warp, then the group's four warps
+      t0 += tiles;
+      // The combine may start launching: it waits for this grid anyway.
+      if (tid == 0 && t0 == T) pdl_launch_dependents();
+      // Softmax denominators over the chunk's rows.
 #pragma unroll
       for (int h = 0; h < kHalf; ++h)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-          tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
-      float* rd = red + sb * kHeadGroup * 4;
+        for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
       if (lane < kHalf) {
-        float v = tt[0];
+        float v = l[0];
 #pragma unroll
-        for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
-        rd[(hb + lane) * 4 + wq] = v;
+        for (int h = 1; h < kHalf; ++h) v = lane == h ? l[h] : v;
+        lsum[(hb + lane) * 4 + wq] = v;
       }
+      const F8Item out = cur;
+      if (kShare && t0 < T) {   // fetched while the last PV runs
+        cur = next_item(cur, t0);
+        read_scales();
+      }
+      // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
+      f8_warp_wait(bar(B_ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      tc_fence_after();
       named_bar_sync(1, kF8Soft);
-      bool need = false;
-      float tmax[kHalf];
-#pragma unroll
-      for (int h = 0; h < kHalf; ++h) {
-        const float4 q4 = *reinterpret_cast<const float4*>(rd + (hb + h) * 4);
-        tmax[h] = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
-        need |= tmax[h] > m[h] + kRescaleLog2;
-      }
-      if (need) {
-        // Move this group's reference maxima; rescale its row sums and the O^T
-        // columns it owns (in TMEM, after the previous PV finished).
-        float alpha[kHalf];
+      if (!*abort_flag) {
+        const size_t base = (size_t(out.v) * p.H + h0) * p.splits + out.j;
+        // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
+        // here, 1 <= L <= 2^8 x rows), branch-free; lane h of the first warp of
+        // each group writes head h's log-sum-exp.
+        float inv[kHalf], Lme = 0.f, mme = 0.f;
 #pragma unroll
         for (int h = 0; h < kHalf; ++h) {
-          const float mn = fmaxf(m[h], tmax[h]);
-          alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
-          m[h] = mn;
-          l[h] *= alpha[h];
+          const float4 q4 = *reinterpret_cast<const float4*>(lsum + (hb + h) * 4);
+          const float L = (q4.x + q4.y) + (q4.z + q4.w);
+          inv[h] = L > 0.f ? __fdividef(1.f, L) : 0.f;
+          Lme = lane == h ? L : Lme;
+          mme = lane == h ? m[h] : mme;
         }
-        if (t > 0) {
-          f8_warp_wait(bar(B_ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-          tc_fence_after();
+        if (wq == 0 && lane < kHalf && (!kPaged || p.part_lse))
+          p.part_lse[base + size_t(hb + lane) * p.splits] =
+              Lme > 0.f ? (mme + log2f(Lme)) * kLn2 : -INFINITY;
+        float* row0 = p.part_o + (base + size_t(hb) * p.splits) * kDc + 32 * wq + lane;
+        const size_t head_stride = size_t(p.splits) * kDc;
 #pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
+        for (int mb = 0; mb < 4; ++mb) {
+          uint32_t o1[8], o2[8], o3[8];
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + hb, o1);
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + kHeadGroup + hb, o2);
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + 2 * kHeadGroup + hb, o3);
+          tmem_wait_ld();
+          float* row = row0 + 128 * mb;
 #pragma unroll
-            for (int part = 0; part < kPParts; ++part) {
-              const uint32_t col = kOCol + kPN * mb + kHeadGroup * part + hb;
-              uint32_t r[8];
-              float o[8];
-              tmem_ld8_nowait(tmem + lane_base + col, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int h = 0; h < kHalf; ++h) o[h] = __uint_as_float(r[h]) * alpha[h];
-              tmem_st8(tmem + lane_base + col, o);
-            }
+          for (int h = 0; h < kHalf; ++h, row += head_stride) {
+            const float v = (__uint_as_float(o1[h]) + (__uint_as_float(o2[h]) * 0.0625f +
+                                                       __uint_as_float(o3[h]) * 0.00390625f)) *
+                            inv[h];
+            if (kPaged && p.direct && p.io_bf16)
+              reinterpret_cast<__nv_bfloat16*>(p.part_o)[row - p.part_o] = __float2bfloat16_rn(v);
+            else
+              *row = v;
           }
-          tmem_wait_st();
-        }
-      }
-      // p in [0, 2^8] as three E4M3 parts, two heads per conversion; the row
-      // sum takes the value the PV uses.
-      uint16_t pp[kPParts][kHalf / 2];
-#pragma unroll
-      for (int h2 = 0; h2 < kHalf / 2; ++h2) {
-        float v0, v1;
-        {
-          const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
-          const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
-          v0 = ex2(sc[2 * h2] - mu0);
-          v1 = ex2(sc[2 * h2 + 1] - mu1);
-        }
-        float used0 = 0.f, used1 = 0.f, wgt = 1.f;
-#pragma unroll
-        for (int part = 0; part < kPParts; ++part) {
-          pp[part][h2] = to_e4m3x2(v0, v1);
-          const float2 f = from_e4m3x2(pp[part][h2]);
-          used0 += f.x * wgt;
-          used1 += f.y * wgt;
-          v0 = (v0 - f.x) * 16.f;
-          v1 = (v1 - f.y) * 16.f;
-          wgt *= 0.0625f;
-        }
-        l[2 * h2] += used0;
-        l[2 * h2 + 1] += used1;
-      }
-      // P^T buffer sb was last read by the PV of tile t-2.
-      if (t >= 2) f8_warp_wait(bar(B_ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
-      {
-        // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
-        // 16 part + n is part `part` of head n; the K index is the tile row.
-        uint8_t* pbuf = smem + kOffP + sb * kPBuf;
-#pragma unroll
-        for (int part = 0; part < kPParts; ++part)
-#pragma unroll
-          for (int h2 = 0; h2 < kHalf / 2; ++h2) {
-            pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2, row)] = pp[part][h2] & 0xFF;
-            pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2 + 1, row)] = pp[part][h2] >> 8;
-          }
-      }
-      if (t == T - 1 && zero_last) {
-        // Latent boxes 0-3 of the last tile: rows past the sequence's end -> 0.
-        uint8_t* tile = smem + kOffTile + (t & 1) * kF8Tile;
-        const int nrow = kF8Rows - zero_from;
-        for (int c = tid; c < 4 * nrow * 8; c += kF8Soft) {
-          const int mb = c / (nrow * 8), rem = c % (nrow * 8);
-          *reinterpret_cast<uint4*>(tile + mb * kF8Box + (zero_from + rem / 8) * 128 + (rem % 8) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_PFULL + sb));
-    }
-    // The combine may start launching: it waits for this grid anyway.
-    if (tid == 0) pdl_launch_dependents();
-    // Softmax denominators over the chunk's rows.
-#pragma unroll
-    for (int h = 0; h < kHalf; ++h)
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-    if (lane < kHalf) {
-      float v = l[0];
-#pragma unroll
-      for (int h = 1; h < kHalf; ++h) v = lane == h ? l[h] : v;
-      lsum[(hb + lane) * 4 + wq] = v;
-    }
-    // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
-    f8_warp_wait(bar(B_ODONE + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag);
-    tc_fence_after();
-    named_bar_sync(1, kF8Soft);
-    if (!*abort_flag) {
-      const size_t base = (size_t(b) * p.H + h0) * p.splits + j;
-      // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
-      // here, 1 <= L <= 2^8 x rows), branch-free; lane h of the first warp of
-      // each group writes head h's log-sum-exp.
-      float inv[kHalf], Lme = 0.f, mme = 0.f;
-#pragma unroll
-      for (int h = 0; h < kHalf; ++h) {
-        const float4 q4 = *reinterpret_cast<const float4*>(lsum + (hb + h) * 4);
-        const float L = (q4.x + q4.y) + (q4.z + q4.w);
-        inv[h] = L > 0.f ? __fdividef(1.f, L) : 0.f;
-        Lme = lane == h ? L : Lme;
-        mme = lane == h ? m[h] : mme;
-      }
-      if (wq == 0 && lane < kHalf && (!kPaged || p.part_lse))
-        p.part_lse[base + size_t(hb + lane) * p.splits] =
-            Lme > 0.f ? (mme + log2f(Lme)) * kLn2 : -INFINITY;
-      float* row0 = p.part_o + (base + size_t(hb) * p.splits) * kDc + 32 * wq + lane;
-      const size_t head_stride = size_t(p.splits) * kDc;
-#pragma unroll
-      for (int mb = 0; mb < 4; ++mb) {
-        uint32_t o1[8], o2[8], o3[8];
-        tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + hb, o1);
-        tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + kHeadGroup + hb, o2);
-        tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + 2 * kHeadGroup + hb, o3);
-        tmem_wait_ld();
-        float* row = row0 + 128 * mb;
-#pragma unroll
-        for (int h = 0; h < kHalf; ++h, row += head_stride) {
-          const float v = (__uint_as_float(o1[h]) + (__uint_as_float(o2[h]) * 0.0625f +
-                                                     __uint_as_float(o3[h]) * 0.00390625f)) *
-                          inv[h];
-          if (kPaged && p.direct && p.io_bf16)
-            reinterpret_cast<__nv_bfloat16*>(p.part_o)[row - p.part_o] = __float2bfloat16_rn(v);
-          else
-            *row = v;
         }
       }
     }
@@ -619,19 +755,24 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_fp8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kF8Smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(split_fp8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kF8Smem)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(split_fp8_kernel<false, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess ||
+        cudaFuncSetAttribute(split_fp8_kernel<true, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess ||
+        cudaFuncSetAttribute(split_fp8_kernel<true, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess) {
       set_error("%s: cannot reserve %zu bytes of shared memory", who, kF8Smem);
       return MLA_ERR_CUDA;
     }
     attr_done.set(dev);
   }
   if (!p.late) launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
-  dim3 grid(p.H / kHeadGroup, p.splits, p.B);
-  launch_pdl(p.table ? split_fp8_kernel<true> : split_fp8_kernel<false>, grid, dim3(kF8Threads),
-             kF8Smem, stream, tmap, p);
+  const int groups = p.H / kHeadGroup;
+  const dim3 grid = p.persist ? dim3(share_runs(groups) * groups) : dim3(groups, p.splits, p.B);
+  launch_pdl(p.persist ? split_fp8_kernel<true, true>
+             : p.table ? split_fp8_kernel<true, false>
+                       : split_fp8_kernel<false, false>,
+             grid, dim3(kF8Threads), kF8Smem, stream, tmap, p);
   return launch_status(who);
 }
 

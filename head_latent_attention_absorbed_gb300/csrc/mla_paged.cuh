@@ -26,9 +26,11 @@ mla_status check_io(const mla_dims* d, int32_t io_dtype, const char* who);
 mla_status check_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
                        int32_t io_dtype, int32_t q_len);
 
-// Every argument check of mla_decode_attn_paged with q_len 1, without a launch
-// (mla_decode.cu).
-mla_status check_attn_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
+// The workspace of the attention over a page selection (mla_decode.cu).
+size_t selected_workspace_bytes(const char* who, const mla_dims* dims, const mla_paging* paging,
+                                int32_t io_dtype, int32_t requested);
+// Its argument checks, without a launch.
+mla_status check_attn_selected(const char* who, const mla_dims* dims, const mla_paging* paging,
                             int32_t io_dtype, const void* q_abs, const void* q_pe,
                             const void* cache, const int32_t* block_table,
                             const int32_t* lengths, float softmax_scale, int32_t num_splits,

@@ -566,7 +566,7 @@ extern "C" size_t mla_sparse_workspace_bytes(const mla_dims* dims, const mla_pag
   mla_dims d;
   mla_paging pg;
   kept_view(dims, paging, q_len, top_pages, &d, &pg);
-  const size_t attn = mla_paged_workspace_bytes(&d, &pg, io_dtype, 1, requested);
+  const size_t attn = selected_workspace_bytes(who, &d, &pg, io_dtype, requested);
   return attn ? select_space(dims, paging, q_len).total + attn : 0;
 }
 
@@ -589,7 +589,7 @@ extern "C" mla_status mla_decode_attn_sparse(
   const size_t mine = select_space(dims, paging, q_len).total;
   uint8_t* attn_ws = static_cast<uint8_t*>(workspace) + mine;
   // The attention's arguments are checked before the first launch.
-  st = check_attn_paged(who, &d, &pg, io_dtype, q_abs, q_pe, cache, sel_table, sel_lengths,
+  st = check_attn_selected(who, &d, &pg, io_dtype, q_abs, q_pe, cache, sel_table, sel_lengths,
                         softmax_scale, num_splits, attn_ws, ws_bytes - mine, o_c);
   if (st != MLA_OK) return st;
   p.early = 1;

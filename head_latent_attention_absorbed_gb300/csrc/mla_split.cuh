@@ -41,6 +41,8 @@ struct SplitParams {
   // (which lets this one start early), so they are read after the PDL wait; the queries'
   // FP8 codes were made before the selection.
   int late;
+  // Paged FP8 cache, equal shares (persist): how many partials each query group has.
+  int32_t* pieces;
 };
 
 // o_c = 0 and lse = -inf of `heads` heads from `row` (query group x H + head), which
@@ -89,9 +91,9 @@ __device__ __forceinline__ int cache_seq(const SplitParams& p, int v) { return v
 // Basics", mask design for multi-token decoding), so the token sees the first
 // lengths[b] - (q_len - 1 - i) rows.  A length outside [q_len, s_max] is
 // reported and clamped.
-__device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool report_it) {
-  int full = p.lengths[v / p.q_len];
-  const int back = p.q_len - 1 - v % p.q_len;
+__device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool report_it,
+                                            int full) {   // full: the length as given
+  const int back = p.q_len == 1 ? 0 : p.q_len - 1 - v % p.q_len;
   if (full < p.q_len || full > p.s_max) {
     if (report_it) report(p.status, MLA_DEV_LENGTH_OUT_OF_RANGE);
     full = full < 0 ? 0 : (full > p.s_max ? p.s_max : full);
@@ -99,12 +101,86 @@ __device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool re
   const int len = full - back;
   return len < 0 ? 0 : len;
 }
+__device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool report_it) {
+  return clamp_length(p, v, report_it, p.lengths[p.q_len == 1 ? v : v / p.q_len]);
+}
+
+// Exclusive prefix sum of x over the warp's lanes, and the warp's total.
+__device__ __forceinline__ int warp_exclusive_scan(int x, int lane, int* total) {
+  int incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  *total = __shfl_sync(0xffffffffu, incl, 31);
+  return incl - x;
+}
+
+// Equal shares of a paged call's tiles.  The tiles of all query groups, one after another,
+// are cut into runs of `each`, one per CTA; a run may end inside a sequence and start with
+// the rest of another, and each (run, query group) that meet is one partial.  A sequence of
+// n tiles has at most ceil(n / each) + 1 of them, which `each` keeps within p.splits.
+constexpr int kShareGroups = 512;   // query groups the planning warp holds, 16 a lane
+struct TileShare {
+  int each;    // tiles per run
+  int first;   // this run's first tile among all
+  int tiles;   // and how many it has
+  int v, off;  // its first tile: tile `off` of query group v
+};
+// Run c of `runs`, by one whole warp.
+__device__ __forceinline__ TileShare take_share(const SplitParams& p, int c, int runs, int lane,
+                                                bool report_it) {
+  constexpr int kEach = kShareGroups / 32;
+  int n[kEach], sum = 0, top = 0;
+  // All loads first (a report may follow each check, and no load moves above it); blocks of
+  // 32 groups that are not there are skipped, not computed.
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int v = 32 * i + lane;
+    n[i] = 0;
+    if (32 * i < p.B && v < p.B) n[i] = p.lengths[p.q_len == 1 ? v : v / p.q_len];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= p.B) break;
+    const int v = 32 * i + lane;
+    if (v < p.B) n[i] = (clamp_length(p, v, report_it, n[i]) + 127) / 128;
+    sum += n[i];
+    top = max(top, n[i]);
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  top = __reduce_max_sync(0xffffffffu, top);
+  TileShare s;
+  s.each = max(1, max((sum + runs - 1) / runs, (top + p.splits - 2) / (p.splits - 1)));
+  s.first = static_cast<int>(min(static_cast<long long>(c) * s.each, static_cast<long long>(sum)));
+  s.tiles = min(s.each, sum - s.first);
+  s.v = s.off = 0;
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= p.B || base > s.first) break;
+    int total;
+    const int at = base + warp_exclusive_scan(n[i], lane, &total);
+    const uint32_t hit = __ballot_sync(0xffffffffu, s.first >= at && s.first < at + n[i]);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s.v = 32 * i + src;
+      s.off = s.first - __shfl_sync(0xffffffffu, at, src);
+      break;
+    }
+    base += total;
+  }
+  return s;
+}
 
 // The FP8 (E4M3) cache's split kernel (mla_fp8.cu): same grid, partials and
 // launch overlap as the bf16 one.
 // It runs as two launches: the query's E4M3 image, then the split itself.
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who);
+// Runs of an equal-share grid: one CTA per SM, the same number of each head group.
+int share_runs(int groups);
 
 // The paged split with bf16 queries as SM pairs (mla_pair.cu): the query rows of a
 // sequence (heads x tokens) in groups of up to 128, two CTAs a group; same partials,

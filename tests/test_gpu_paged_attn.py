@@ -101,6 +101,68 @@ def test_persistent_grid(cuda_lib, io, page):
     c.check(tokens=[0, 17, 39])
 
 
+def share_lengths(kind, B):
+    rng = np.random.RandomState(B)
+    if kind == "ragged":
+        n = rng.randint(0, 900, B)
+        n[:5] = [0, 1, 128, 129, 899]
+    elif kind == "one long":              # all but one sequence short or empty
+        n = rng.randint(0, 3, B)
+        n[B // 2] = 6000
+    else:                                 # "edges": multiples of a tile, and one more row
+        n = 128 * rng.randint(0, 6, B) + rng.randint(0, 2, B)
+    return n
+
+
+@pytest.mark.parametrize("kind", ["ragged", "one long", "edges"])
+@pytest.mark.parametrize("io,heads,q_len,page", [(F32, 16, 1, 16), (BF16, 16, 1, 64),
+                                                 (BF16, 32, 1, 256), (F32, 128, 1, 64),
+                                                 (F32, 16, 3, 32), (BF16, 16, 2, 128)])
+@pytest.mark.parametrize("B", [7, 70])
+def test_equal_shares(cuda_lib, kind, io, heads, q_len, page, B):
+    """The FP8 cache's tiles in equal runs: runs that start and end inside a sequence,
+    hold several, one tile each, and fewer tiles than CTAs."""
+    mla = cuda_lib
+    lengths = share_lengths(kind, B)
+    if q_len > 1:
+        lengths = np.maximum(lengths, q_len)
+    mla.load().mla_test_set_split_form(1)
+    try:
+        c = Call(mla, lengths, page, "fp8", io, heads, q_len=q_len, seed=B + heads)
+        c.run()
+        first = c.o.clone()
+        c.check(tokens=range(0, B * q_len, max(1, B * q_len // 12)),
+                status=0 if lengths.min() else mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+        c.o.fill_(7)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(first, c.o)   # no order of arrival changes a bit
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
+def test_equal_shares_by_size(cuda_lib):
+    """Enough tiles that the planner takes equal shares itself; 512 query groups are the
+    most it takes them for, and a length past s_max is cut and reported there too."""
+    mla = cuda_lib
+    rng = np.random.RandomState(4)
+    lengths = rng.randint(1, 4000, 60)
+    c = Call(mla, lengths, 64, "fp8", BF16, 16, seed=3).run()
+    c.check(tokens=[0, 11, 31, 32, 59])
+    lengths = rng.randint(0, 1200, 512)
+    lengths[511] = 1200
+    c = Call(mla, lengths, 64, "fp8", BF16, 16, seed=5).run()
+    c.check(tokens=[0, 255, 256, 510, 511], status=0 if lengths.min() else
+            mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+    lengths = np.concatenate([lengths, [1000]])
+    c = Call(mla, lengths, 64, "fp8", BF16, 16, seed=5).run()
+    c.check(tokens=[0, 511, 512], status=0 if lengths.min() else mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+    lengths = np.full(40, 3000)
+    c = Call(mla, lengths, 64, "fp8", F32, 16, seed=6, s_max=2900).run()
+    c.lengths = np.full(40, 2900)
+    c.check(tokens=[0, 39], status=mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+
+
 @pytest.mark.parametrize("dtype,io,heads", KINDS)
 def test_empty_and_bad_lengths(cuda_lib, dtype, io, heads):
     """No rows: zeros and -inf, with the status bit; a length above s_max is cut there."""
