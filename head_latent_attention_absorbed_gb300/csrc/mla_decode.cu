@@ -1806,6 +1806,10 @@ __global__ void __launch_bounds__(kThreads)
   int nsplit = partials_of(p, b, len);
   if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
   Out* out = o_c + (size_t(b) * p.H + h) * kDc;
+  if (p.out && nsplit == 1) {   // written by the split
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    return;
+  }
   if (nsplit == 0) {
     store_out4(out + 4 * tid, make_float4(0.f, 0.f, 0.f, 0.f));
     if (tid == 0 && lse_out) lse_out[size_t(b) * p.H + h] = -INFINITY;
@@ -1845,6 +1849,10 @@ __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
   int nsplit = partials_of(p, b, len);
   if (!MLA_IN_BOUNDS(nsplit <= p.splits)) nsplit = p.splits;   // partials past the workspace
   Out* out = o_c + (size_t(b) * p.H + h) * kDc;
+  if (p.out && nsplit == 1) {   // written by the split
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    return;
+  }
   if (nsplit == 0) {
     if (warp == 0) {
       store_out4(out + 4 * col, make_float4(0.f, 0.f, 0.f, 0.f));
@@ -2064,6 +2072,13 @@ constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
 // full, 256 x 2048 79 / 78, 64 x 4096 43.4 / 43.9, 32 x 4096 (6.7) 23.8 / 24.9, 16 x 4096
 // (3.4) 15.5 / 18.1.
 constexpr int kShareMinTiles = 4;
+// The same for SM pairs: tiles per pair (bf16, E4M3), and sequences per pair up to which
+// (more are balanced as they are, with one chunk each and no combine).  64 heads, chunks /
+// shares: bf16, 512 to 8192 rows, 16 sequences (13.5 tiles) 34.1 / 29.1, 76 114 / 93, 152
+// 204 / 166, 200 245 / 214, 256 of 100 to 2048 95 / 106; 512 to 4096, 16 (6.7) 22.6 / 23.9,
+// 24 (10.1) 27.6 / 28.0; all full, 16 x 8192 40.7 / 44.4, 76 x 8192 127 / 136; E4M3, 32 of
+// 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82.
+constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
   return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
          d->heads * o.q_len >= (d->dtype == MLA_BF16 ? kPairMinBf16 : kPairMinFp8);
@@ -2121,6 +2136,7 @@ mla_status launch_split_tc(const CUtensorMap& tmap, const CUtensorMap& tmap_half
 struct SplitPlan {
   int chunk, splits;
   bool persist;
+  bool share = false;   // equal shares (take_share); splits is what the workspace holds
 };
 
 long long current_sms() {
@@ -2133,7 +2149,7 @@ long long current_sms() {
   return sms;
 }
 }  // namespace
-int share_runs(int groups) { return static_cast<int>(current_sms() / groups); }
+int share_runs(int ctas) { return static_cast<int>(current_sms() / ctas); }
 namespace {
 
 // Rows per KV chunk and the resulting chunk count, and the launch form.
@@ -2250,14 +2266,20 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   }
   const bool np_one_wave = per_split * np_splits <= slots;
   const int form = g_split_form.load();
-  if (opts.paged && !opts.late && d->dtype == MLA_FP8_E4M3 && !pairs && requested <= 0 &&
-      form != 2 && d->batch <= kShareGroups && groups <= sms) {
-    // Equal shares of a paged FP8 cache's tiles: twice the partials that full sequences
-    // would need, so that shares may shrink with the lengths.
-    const long long seq = (S + kTileRows - 1) / kTileRows, runs = sms / groups;
-    const long long each = (d->batch * seq + runs - 1) / runs, half = (each + 1) / 2;
-    if (d->batch * seq < (1ll << 30) && (form == 1 || each >= kShareMinTiles))
-      return {np_chunk, static_cast<int>((seq + half - 1) / half + 1), true};
+  // Equal shares of a paged call's tiles (E4M3, and SM pairs): room for twice the partials
+  // that full sequences would need, so that shares may shrink with the lengths.
+  const long long sets = pairs ? d->batch / opts.q_len : d->batch;
+  const long long ctas = pairs ? 2ll * pair_groups(d->heads * opts.q_len) : groups;
+  if (opts.paged && !opts.late && (pairs || d->dtype == MLA_FP8_E4M3) && requested <= 0 &&
+      form != 2 && sets <= kShareSets && ctas <= sms) {
+    const long long seq = (S + kTileRows - 1) / kTileRows, runs = sms / ctas;
+    const long long each = (sets * seq + runs - 1) / runs, half = (each + 1) / 2;
+    const bool pays =
+        !pairs ? each >= kShareMinTiles
+               : each >= (d->dtype == MLA_BF16 ? kSharePairTilesBf16 : kSharePairTilesFp8) &&
+                     sets <= kSharePairSets * runs;
+    if (sets * seq < (1ll << 30) && (form == 1 || pays))
+      return {np_chunk, static_cast<int>((seq + half - 1) / half + 1), false, true};
   }
   if (!can_persist || form == 2 || (form == 0 && requested > 0 && np_one_wave))
     return {np_chunk, np_splits, false};
@@ -2305,8 +2327,9 @@ size_t workspace_bytes(const mla_dims* d, int splits, bool paged = false) {
   const size_t img = d->dtype == MLA_FP8_E4M3
                          ? (size_t(d->batch) * (d->heads / kHeadGroup) * kFp8QImage + 255) / 256 * 256
                          : 0;
-  const size_t pieces =
-      paged && img ? (size_t(d->batch) * sizeof(int32_t) + 255) / 256 * 256 : 0;
+  const size_t pieces = paged && d->dtype != MLA_F32
+                            ? (size_t(d->batch) * sizeof(int32_t) + 255) / 256 * 256
+                            : 0;
   return o_bytes + lse_bytes + img + pieces;
 }
 
@@ -2504,8 +2527,10 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   p->num_pages = view ? view->paging->num_pages : 0;
   p->io_bf16 = view && view->io == MLA_BF16 ? 1 : 0;
   p->direct = 0;
+  p->out = nullptr;
+  p->out_lse = nullptr;
   p->late = view && view->late ? 1 : 0;
-  p->pieces = view && p->q_img && plan.persist
+  p->pieces = plan.share
                   ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + need) -
                         (size_t(dims->batch) * sizeof(int32_t) + 255) / 256 * 64
                   : nullptr;
@@ -2527,13 +2552,17 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   mla_status st = prepare(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
                           num_splits, workspace, ws_bytes, dev_status, &p, view);
   if (st != MLA_OK) return st;
-  if (direct_o) {
+  const bool pairs = view && pair_form(dims, plan_opts(dims, q_len, view));
+  if (direct_o && p.pieces) {   // (only the pairs write there)
+    p.out = direct_o;
+    p.out_lse = direct_lse;
+  } else if (direct_o) {
     p.direct = 1;
     p.part_o = static_cast<float*>(direct_o);
     p.part_lse = direct_lse;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (view && pair_form(dims, plan_opts(dims, q_len, view)))
+  if (pairs)
     return launch_split_pair(p, cache, dims->dtype == MLA_FP8_E4M3, s, who);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
   if (dims->dtype == MLA_BF16) {
@@ -2622,6 +2651,7 @@ static mla_status decode_combine(const char* who, const mla_dims* dims, int q_le
   mla_status st = prepare(who, dims, q_len, nullptr, nullptr, nullptr, lengths, 1.f, num_splits,
                           const_cast<void*>(workspace), ws_bytes, nullptr, &p, view);
   if (st != MLA_OK) return st;
+  if (p.pieces && pair_form(dims, plan_opts(dims, q_len, view))) p.out = o_c;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.io_bf16)
     launch_combine(p, dims->heads, static_cast<__nv_bfloat16*>(o_c), lse, s);
@@ -2774,12 +2804,12 @@ static mla_status attn_paged(const char* who, const mla_dims* dims, const PagedV
   mla_dims qd = *dims;
   qd.batch = dims->batch * q_len;
   const SplitPlan plan = plan_split(&qd, num_splits, plan_opts(dims, q_len, &view));
-  if (plan.splits == 1 && !plan.persist)   // the one chunk's partial is the result
-    return decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
-                        workspace, ws_bytes, dev_status, stream, &view, o_c, lse);
-  const mla_status st = decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale,
-                                     num_splits, workspace, ws_bytes, dev_status, stream, &view);
-  if (st != MLA_OK) return st;
+  const bool direct = plan.splits == 1 && !plan.persist;   // the one chunk's partial is the result
+  const mla_status st =
+      decode_split(who, dims, q_len, q_abs, q_pe, cache, lengths, softmax_scale, num_splits,
+                   workspace, ws_bytes, dev_status, stream, &view,
+                   direct || plan.share ? o_c : nullptr, direct || plan.share ? lse : nullptr);
+  if (st != MLA_OK || direct) return st;
   return decode_combine(who, dims, q_len, lengths, num_splits, workspace, ws_bytes, o_c, lse,
                         stream, &view);
 }

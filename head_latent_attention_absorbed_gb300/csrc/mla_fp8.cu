@@ -197,18 +197,13 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
   }
 }
 
-// One item of a CTA: consecutive tiles of one query group.
-struct F8Item {
-  int v, j;       // query group, index of the partial among its own
-  int r0, tiles;  // first row, 128-row tiles
-  int len;        // rows the query group attends
-};
-
 // kPaged: the cache is a pool of pages; a tile's boxes are boxes of up to 128
 // rows of one page each, one lane of the producer warp per page.
 // kShare (paged): one CTA per SM takes an equal run of all query groups' tiles (take_share),
 // one item per query group it meets, streamed back to back: the copies and score MMAs of
-// the next item run while the last one's output is written.  Otherwise a CTA has one item,
+// the next item run while the last one's output is written.  (Writing it one tile later,
+// from a second O^T buffer, cost more registers and code than it saved: 47.7 us against
+// 46.3 on 64 sequences of 512 to 8192 rows; with chunks 56.)  Otherwise a CTA has one item,
 // its chunk.
 template <bool kPaged, bool kShare>
 __global__ void __launch_bounds__(kF8Threads, 1)
@@ -229,8 +224,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
   const int groups = p.H / kHeadGroup;
   const int g = kShare ? blockIdx.x % groups : blockIdx.x, h0 = g * kHeadGroup;
-  F8Item first;    // the CTA's first item
-  int T, row_end;  // tiles of the CTA; row at which an item that ends inside a sequence ends
+  TileItem first{0, 0, 0, 0, 0};   // the CTA's first item (none: T = 0)
+  int T = 0, row_end = 0;  // tiles of the CTA; row at which an item that ends inside a sequence ends
   TileShare share;
   if (!kShare) {
     const int j = blockIdx.y, b = blockIdx.z;
@@ -246,27 +241,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     row_end = min(r0 + p.chunk, len);
     T = (row_end - r0 + kF8Rows - 1) / kF8Rows;
-    first = F8Item{b, j, r0, T, len};
+    first = TileItem{b, j, r0, T, len};
   }
-  auto first_item = [&] {   // of a share
-    T = share.tiles;
-    const int len = clamp_length(p, share.v, false);
-    first = F8Item{share.v, share.off > 0 ? static_cast<int>(blockIdx.x / groups) -
-                                                (share.first - share.off) / share.each
-                                          : 0,
-                   share.off * kF8Rows, min((len + kF8Rows - 1) / kF8Rows - share.off, T), len};
+  auto begin_share = [&] {
+    T = uniform(share.tiles);
+    first = first_item<false>(p, share, blockIdx.x / groups);
   };
-  // The item after `it`, which ends before the CTA's tile t < T: the start of the next
-  // query group that attends any row.
-  auto next_item = [&](F8Item it, int t) {
-    do {
-      ++it.v;
-      it.len = clamp_length(p, it.v, false);
-    } while (it.len == 0 && it.v + 1 < p.B);
-    it.j = it.r0 = 0;
-    it.tiles = max(1, min((it.len + kF8Rows - 1) / kF8Rows, T - t));
-    return it;
-  };
+  auto item_after = [&](const TileItem& it, int t) { return next_item<false>(p, it, T - t); };
 
   // The cache stream starts first: the producer warp sets up the barriers and
   // issues the first two tiles before the CTA-wide barrier.
@@ -274,7 +255,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   // the first row of piece i, and the next tile's are looked up ahead.
   const int box_rows = kPaged ? min(1 << p.page_shift, kF8Rows) : kF8Rows;
   const int pieces = kF8Rows / box_rows;
-  auto piece_row = [&](const F8Item& it, int i) {   // of the item's tile i
+  auto piece_row = [&](const TileItem& it, int i) {   // of the item's tile i
     const int r = it.r0 + i * kF8Rows;
     return kPaged ? paged_row(p, cache_seq(p, it.v), r + lane * box_rows,
                               lane * box_rows < kF8Rows ? it.len : 0)
@@ -306,22 +287,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   };
   // The producer's place: its next tile is tile i of `it`, with pieces at `row`; step()
   // moves on after tile t.
-  F8Item it;
+  TileItem it;
   int i = 0, row = 0;
   auto step = [&](int t) {
     if (t + 1 >= T) return;
     if (++i == it.tiles) {
-      it = next_item(it, t + 1);
+      it = item_after(it, t + 1);
       i = 0;
     }
     row = piece_row(it, i);
   };
   if (warp == 8) {
     if (kShare) {
-      share = take_share(p, blockIdx.x / groups, gridDim.x / groups, lane, blockIdx.x == 0);
+      share = take_share<false>(p, blockIdx.x / groups, gridDim.x / groups, lane, blockIdx.x == 0);
       if (lane == 0) *reinterpret_cast<TileShare*>(smem + kOffShare) = share;
       if (share.tiles > 0)
-        first_item();
+        begin_share();
       else
         T = 0;
     }
@@ -364,7 +345,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       pdl_wait();
       return;
     }
-    if (warp != 8) first_item();
+    if (warp != 8) begin_share();
   }
   const uint32_t tmem = *slot_ptr;
 
@@ -399,17 +380,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     constexpr uint32_t idesc_s = idesc_e4m3(128, kQN, 0);
     const uint64_t a0 = umma_desc_sw128(sbase + kOffTile, 16, 1024);
     const uint64_t q0 = umma_desc_sw128(sbase + kOffQ, 16, 1024);
-    F8Item cur = first;
+    TileItem cur = first;
     int left = 0, n = 0;   // tiles left of the item; items begun
     for (int t = 0; t < T; ++t) {
       const int bf = t & 1;
       if (left == 0) {
-        if (t > 0) cur = next_item(cur, t);
+        if (t > 0) cur = item_after(cur, t);
         left = cur.tiles;
         if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
           // The run with a query group's first tile says how many runs it spans.
-          const int s = share.first + t, tiles = (cur.len + kF8Rows - 1) / kF8Rows;
-          p.pieces[cur.v] = (s + tiles - 1) / share.each - s / share.each + 1;
+          p.pieces[cur.v] = count_pieces(cur, share.first + t, share.each);
         }
         f8_warp_wait(bar(B_QREADY), n & 1, abort_flag);
         ++n;
@@ -443,12 +423,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
     const uint64_t p0 = umma_desc_sw128(sbase + kOffP, 16, 1024);
     const uint64_t c0 = umma_desc_sw128(sbase + kOffTile, kF8Box, 1024);
-    F8Item cur = first;
+    TileItem cur = first;
     int done = 0;   // tiles of the item accumulated
     for (int t = 0; t < T; ++t, ++done) {
       const int bf = t & 1;
       if (kShare && done == cur.tiles) {
-        cur = next_item(cur, t);
+        cur = item_after(cur, t);
         done = 0;
       }
       f8_warp_wait(bar(B_PFULL + bf), (t >> 1) & 1, abort_flag);
@@ -478,7 +458,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
 
     const int last_rows = kShare ? 0 : row_end - (first.r0 + (first.tiles - 1) * kF8Rows);
-    F8Item cur = first;
+    TileItem cur = first;
     float qsig[kHalf];
     auto read_scales = [&] {   // of the item
       const float4* sg = reinterpret_cast<const float4*>(
@@ -661,9 +641,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int h = 1; h < kHalf; ++h) v = lane == h ? l[h] : v;
         lsum[(hb + lane) * 4 + wq] = v;
       }
-      const F8Item out = cur;
+      const TileItem out = cur;
       if (kShare && t0 < T) {   // fetched while the last PV runs
-        cur = next_item(cur, t0);
+        cur = item_after(cur, t0);
         read_scales();
       }
       // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
@@ -768,8 +748,8 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   }
   if (!p.late) launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
   const int groups = p.H / kHeadGroup;
-  const dim3 grid = p.persist ? dim3(share_runs(groups) * groups) : dim3(groups, p.splits, p.B);
-  launch_pdl(p.persist ? split_fp8_kernel<true, true>
+  const dim3 grid = p.pieces ? dim3(share_runs(groups) * groups) : dim3(groups, p.splits, p.B);
+  launch_pdl(p.pieces  ? split_fp8_kernel<true, true>
              : p.table ? split_fp8_kernel<true, false>
                        : split_fp8_kernel<false, false>,
              grid, dim3(kF8Threads), kF8Smem, stream, tmap, p);

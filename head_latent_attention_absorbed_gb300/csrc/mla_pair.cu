@@ -40,8 +40,9 @@
 //
 // Warps: 8 (bf16) or 16 (E4M3) softmax and epilogue; then one each for the score rows
 // (TMA) and for the query and the output operand (TMA), two for the score MMAs and two
-// for the output MMAs (the even CTA's issue for the pair).  The even CTA's barriers collect both CTAs' copies and softmax warps;
-// tcgen05.commit signals both CTAs.  Every wait is bounded.
+// for the output MMAs (the even CTA's issue for the pair); with equal shares one more for
+// the later items' queries.  The even CTA's barriers collect both CTAs' copies and softmax
+// warps; tcgen05.commit signals both CTAs.  Every wait is bounded.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
@@ -58,10 +59,10 @@ constexpr uint32_t kPTmem = 512;
 
 template <bool kFp8>
 struct PairPlan {
-  // Softmax warps: each thread takes kCols scores of one head.  E4M3's conversions make its softmax the longest stage of a tile, so it
-  // gets twice the warps.
+  // Softmax warps: each thread takes kCols scores of one head.  E4M3's conversions make its
+  // softmax the longest stage of a tile, so it gets twice the warps.
   static constexpr int kSoftWarps = kFp8 ? 16 : 8, kSoft = 32 * kSoftWarps;
-  static constexpr int kThreads = kSoft + 6 * 32;
+  static constexpr int kThreads = kSoft + 6 * 32, kShareThreads = kThreads + 32;
   static constexpr int kSlices = kSoftWarps / 4, kCols = 64 / kSlices;
   static constexpr int kBoxCols = kFp8 ? 128 : 64;          // columns of a 128-byte box
   static constexpr int kBoxes = kFp8 ? 5 : 9;               // score boxes of a row
@@ -78,15 +79,18 @@ struct PairPlan {
   static constexpr int kOffV = kOffS + kSlotsS * kPBox;
   static constexpr int kOffP = kOffV + kSlotsV * kUnit;
   static constexpr int kOffRed = kOffP + kPBufs * kPBufBytes;   // [2][2 kSlices][64] maxima
-  static constexpr int kOffBar = kOffRed + 2 * 2 * kSlices * kPHeads * 4;
-  // full / empty of the rings; S and P hand-overs; the query; the last tile's units
+  static constexpr int kOffSum = kOffRed + 2 * 2 * kSlices * kPHeads * 4;   // row sums
+  static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
+  // full / empty of the rings; S and P hand-overs; the query; the last tile's units; the
+  // query read for the last time (kShare)
   static constexpr int FULLS = 0, EMPTYS = FULLS + kSlotsS, FULLV = EMPTYS + kSlotsS,
                        EMPTYV = FULLV + kSlotsV, SREADY = EMPTYV + kSlotsV, SFREE = SREADY + 2,
                        PREADY = SFREE + 2, PVDONE = PREADY + 2, QFULL = PVDONE + 2,
-                       LASTV = QFULL + 1, ZEROED = LASTV + 4, kBars = ZEROED + 4;
+                       LASTV = QFULL + 1, ZEROED = LASTV + 4, QFREE = ZEROED + 4, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffSlot + 8;
-  static constexpr size_t kSmem = 1024 + kOffAbort + 8;
+  static constexpr int kOffShare = kOffAbort + 8;   // TileShare of the pair
+  static constexpr size_t kSmem = 1024 + kOffShare + 24;
   // Reference of the softmax below the running maximum, and how far a maximum may
   // pass it before O is rescaled (log2): E4M3 weights stay in [0, 2^8.5].
   static constexpr float kBias = kFp8 ? 3.f : 0.f, kGrow = kFp8 ? 5.5f : 8.f;
@@ -95,7 +99,8 @@ struct PairPlan {
   static constexpr int kStageRow = kDc * 4 + 16;
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kOffRed >= kPHeads * kStageRow, "epilogue staging");
-  static_assert(kSlotsS % 2 == 0 && kSlotsV % 2 == 0, "ring lengths");
+  static_assert(kPBufs * kPBufBytes == kSoftWarps * 32 * 64, "an item's output through P");
+  static_assert(kSlotsS % 2 == 0 && kSlotsV == 4, "ring lengths");
   static_assert(kOffS % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kOffBar % 8 == 0, "mbarriers");
 };
@@ -241,8 +246,14 @@ __global__ void __launch_bounds__(128) pair_query_kernel(const SplitParams p, ui
   }
 }
 
-template <bool kFp8>
-__global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
+// kShare: one pair per two SMs takes an equal run of all sequences' tiles (take_share), an
+// item per sequence it meets; the next item's rows and query are fetched and its scores
+// computed while the last one's output is written (a change of item costs about 2.5 us, the
+// softmax of its first tile behind that write).  Otherwise a pair has one item, its chunk.
+// 64 sequences of 512 to 8192 bf16 rows x 32 heads 110 -> 77 us, x 128 heads 113 -> 89.
+template <bool kFp8, bool kShare>
+__global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
+                                         : PairPlan<kFp8>::kThreads, 1)
     split_pair_kernel(const __grid_constant__ CUtensorMap tmap,
                       const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_qpe, const SplitParams p,
@@ -260,29 +271,38 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
   // Query rows (tokens x heads) of the sequence, dealt evenly to its CTAs: this CTA's
   // are flat0 .. flat0 + mine - 1 of all; rows past them up to 64 are computed as well
   // (other rows of the query, or zeros) and dropped.
-  const int j = blockIdx.y, seq = blockIdx.z, all = p.q_len * p.H;
-  const int share = (all + gridDim.x - 1) / gridDim.x;
-  const int first = blockIdx.x * share, mine = min(share, all - first);
-  const int flat0 = seq * all + first;
+  const int all = p.q_len * p.H, parts = kShare ? 2 * pair_groups(all) : gridDim.x;
+  const int dealt = (all + parts - 1) / parts, part = kShare ? blockIdx.x % parts : blockIdx.x;
+  const int first = part * dealt, mine = min(dealt, all - first);
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
   if (p.late) pdl_wait();
-  // Rows of the sequence, all of which its last token attends.
-  const int len = clamp_length(p, (seq + 1) * p.q_len - 1, tid == 0 && blockIdx.x == 0 && j == 0);
-  const int r0 = j * p.chunk;
-  if (r0 >= len) {   // both CTAs of the pair: the chunk lies past the sequence
-    if (p.direct) {
-      pdl_wait();
-      write_no_rows(p, flat0, mine, tid, L::kThreads);
+  // Rows of a sequence, all of which its last token attends, count.
+  TileItem item0{0, 0, 0, 0, 0};   // the pair's first item (none: T = 0)
+  int T = 0;        // tiles of the pair
+  TileShare share;
+  if (!kShare) {
+    const int j = blockIdx.y, seq = blockIdx.z;
+    const int len =
+        clamp_length(p, (seq + 1) * p.q_len - 1, tid == 0 && blockIdx.x == 0 && j == 0);
+    const int r0 = j * p.chunk;
+    if (r0 >= len) {   // both CTAs of the pair: the chunk lies past the sequence
+      if (p.direct) {
+        pdl_wait();
+        write_no_rows(p, seq * all + first, mine, tid, L::kThreads);
+      }
+      return;
     }
-    return;
+    T = (min(r0 + p.chunk, len) - r0 + kTileRows - 1) / kTileRows;
+    item0 = TileItem{seq, j, r0, T, len};
   }
-  const int r1 = min(r0 + p.chunk, len);
-  const int T = (r1 - r0 + kTileRows - 1) / kTileRows;
-  // Rows of the last tile past the sequence's end may hold anything (NaN included):
+  // Rows of an item's last tile past the sequence's end may hold anything (NaN included):
   // they are zeroed in the output operand.
-  const int zero_from = len - (r0 + (T - 1) * kTileRows);
-  const bool zero_last = zero_from < kTileRows;
+  auto zero_from = [&](const TileItem& it) {
+    return it.len - (it.r0 + (it.tiles - 1) * kTileRows);
+  };
+  auto zero_last = [&](const TileItem& it) { return zero_from(it) < kTileRows; };
+  auto item_after = [&](const TileItem& it, int t) { return next_item<true>(p, it, T - t); };
   const uint32_t lead = mapa_shared(bars, 0);   // the even CTA's barriers
   auto bar = [&](int i) { return bars + 8 * i; };
   auto lbar = [&](int i) { return lead + 8 * i; };
@@ -303,6 +323,7 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
       mbar_init(bar(L::PVDONE + i), 2);
     }
     mbar_init(bar(L::QFULL), 1);
+    mbar_init(bar(L::QFREE), 2);   // one commit per score issuer
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(L::LASTV + i), 1);
       mbar_init(bar(L::ZEROED + i), 2 * L::kSoftWarps);
@@ -313,9 +334,14 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
     prefetch_tmap(&tmap_q);
     if (!kFp8) prefetch_tmap(&tmap_qpe);
   }
+  if (kShare && warp == L::kSoftWarps) {
+    __syncwarp();
+    share = take_share<true>(p, blockIdx.x / parts, gridDim.x / parts, lane, blockIdx.x == 0);
+    if (lane == 0) *reinterpret_cast<TileShare*>(smem + L::kOffShare) = share;
+  }
   // Role warps after the softmax warps.
   constexpr int kWarpS = L::kSoftWarps, kWarpV = kWarpS + 1, kWarpScore = kWarpS + 2,
-                kWarpOut = kWarpS + 4;
+                kWarpOut = kWarpS + 4, kWarpQuery = kWarpS + 6;   // the last of kShare only
   if (warp == kWarpScore) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(slot_ptr)),
@@ -328,43 +354,18 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
   cluster_sync_all();   // the barriers of both CTAs exist
   tc_fence_after();
   const uint32_t tmem = *slot_ptr;
-
-  // Pieces of one page each: rows of a box, and pieces of 64 rows.
-  const int brows = min(1 << p.page_shift, 64), np = 64 / brows;
-
-  if (warp == kWarpS) {
-    // ------------------------------------------------------------ score rows (HBM)
-    // This CTA's 64 rows of each tile; lane i < np holds piece i's pool row.
-    const uint64_t keep = l2_evict_last_policy();   // read again as the output operand
-    auto rows_of = [&](int t) {
-      return paged_row(p, seq, r0 + t * kTileRows + 64 * rank + lane * brows,
-                       lane < np ? len : 0);
-    };
-    int row = rows_of(0), sl = 0;
-    uint32_t phase = 1;   // of the slot's release before this use: the first uses pass
-    for (int t = 0; t < T; ++t) {
-      const int next = t + 1 < T ? rows_of(t + 1) : 0;
-      if (__any_sync(0xffffffffu, *abort_flag)) break;
-#pragma unroll 1
-      for (int k = 0; k < L::kBoxes; ++k) {
-        warp_wait(bar(L::EMPTYS + sl), phase, abort_flag);
-        if (leader) expect_tx_elected(bar(L::FULLS + sl), 2 * kPBox);
-        const uint32_t dst = sbase + L::kOffS + sl * kPBox, full = lbar(L::FULLS + sl);
-#pragma unroll 1
-        for (int i = 0; i < np; ++i)
-          tma_load_pair(dst + i * brows * 128, &tmap, L::kBoxCols * k,
-                        __shfl_sync(0xffffffffu, row, i), full, keep);
-        if (++sl == L::kSlotsS) {
-          sl = 0;
-          phase ^= 1;
-        }
-      }
-      row = next;
-    }
-  } else if (warp == kWarpV) {
-    // ------------------------------------------------------------ query, output operand (L2)
+  if (kShare) {
+    share = *reinterpret_cast<const TileShare*>(smem + L::kOffShare);
+    T = uniform(max(share.tiles, 0));   // none: more pairs than tiles
+    if (T > 0)
+      item0 = first_item<true>(p, share, blockIdx.x / parts);
+    else
+      pdl_wait();
+  }
+  // This CTA's half of the queries of sequence v, by a whole warp after its PDL wait.
+  auto load_query = [&](int v) {
     const uint64_t stream = l2_evict_first_policy();
-    pdl_wait();   // the query comes from the kernel before
+    const int flat0 = v * all + first;
     if (leader) expect_tx_elected(bar(L::QFULL), 2 * L::kQBytes);
 #pragma unroll 1
     for (int i = 0; i < L::kParts * L::kBoxes; ++i) {
@@ -375,40 +376,111 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
         tma_load_pair(sbase + L::kOffQ + i * kPBox, i < 8 ? &tmap_q : &tmap_qpe,
                       i < 8 ? 64 * i : 0, flat0, lbar(L::QFULL), stream);
     }
+  };
+
+  // Pieces of one page each: rows of a box, and pieces of 64 rows.
+  const int brows = min(1 << p.page_shift, 64), np = 64 / brows;
+
+  if (warp == kWarpS) {
+    // ------------------------------------------------------------ score rows (HBM)
+    // This CTA's 64 rows of each tile; lane i < np holds piece i's pool row.
+    const uint64_t keep = l2_evict_last_policy();   // read again as the output operand
+    auto rows_of = [&](const TileItem& it, int i) {
+      return paged_row(p, it.v, it.r0 + i * kTileRows + 64 * rank + lane * brows,
+                       lane < np ? it.len : 0);
+    };
+    TileItem it = item0;
+    int row = T > 0 ? rows_of(it, 0) : 0, sl = 0;
+    uint32_t phase = 1;   // of the slot's release before this use: the first uses pass
+    for (int t0 = 0; t0 < T;) {   // items
+      const int end = t0 + it.tiles;
+      TileItem then = it;
+      if (kShare && end < T) then = item_after(it, end);
+      for (int i = 0; i < it.tiles; ++i) {
+        const int next = i + 1 < it.tiles     ? rows_of(it, i + 1)
+                         : kShare && end < T ? rows_of(then, 0)
+                                             : 0;
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+#pragma unroll 1
+        for (int k = 0; k < L::kBoxes; ++k) {
+          warp_wait(bar(L::EMPTYS + sl), phase, abort_flag);
+          if (leader) expect_tx_elected(bar(L::FULLS + sl), 2 * kPBox);
+          const uint32_t dst = sbase + L::kOffS + sl * kPBox, full = lbar(L::FULLS + sl);
+#pragma unroll 1
+          for (int i = 0; i < np; ++i)
+            tma_load_pair(dst + i * brows * 128, &tmap, L::kBoxCols * k,
+                          __shfl_sync(0xffffffffu, row, i), full, keep);
+          if (++sl == L::kSlotsS) {
+            sl = 0;
+            phase ^= 1;
+          }
+        }
+        row = next;
+      }
+      t0 = end;
+      it = then;
+    }
+  } else if (kShare && warp == kWarpQuery) {
+    // ------------------------------------------------------------ the later items' queries
+    // Each once the scores of the item before are done, which read the query it replaces.
+    TileItem it = item0;
+    for (int t = it.tiles, n = 0; 0 < t && t < T; t += it.tiles, ++n) {
+      it = item_after(it, t);
+      warp_wait(bar(L::QFREE), n & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      pdl_wait();
+      load_query(it.v);
+    }
+  } else if (warp == kWarpV) {
+    // ------------------------------------------------------------ query, output operand (L2)
+    const uint64_t stream = l2_evict_first_policy();
+    pdl_wait();   // the query comes from the kernel before
+    if (T > 0) load_query(item0.v);
     // Unit u of a tile: row half u >> 1, latent columns 256 (u & 1) + 128 rank ..;
     // lane i < 2 np holds the pool row of piece i of the tile's 128 rows.
-    auto rows_of = [&](int t) {
-      return paged_row(p, seq, r0 + t * kTileRows + lane * brows, lane < 2 * np ? len : 0);
+    auto rows_of = [&](const TileItem& it, int i) {
+      return paged_row(p, it.v, it.r0 + i * kTileRows + lane * brows, lane < 2 * np ? it.len : 0);
     };
-    int row = rows_of(0), sl = 0;
+    TileItem it = item0;
+    int row = T > 0 ? rows_of(it, 0) : 0, sl = 0;
     uint32_t phase = 1;
-    for (int t = 0; t < T; ++t) {
-      const int next = t + 1 < T ? rows_of(t + 1) : 0;
-      if (__any_sync(0xffffffffu, *abort_flag)) break;
-      const bool last = zero_last && t == T - 1;   // these land on the CTA's own barriers
+    for (int t0 = 0; t0 < T;) {   // items
+      const int end = t0 + it.tiles;
+      const bool zero = zero_last(it);
+      TileItem then = it;
+      if (kShare && end < T) then = item_after(it, end);
+      for (int i = 0; i < it.tiles; ++i) {
+        const bool last = zero && i == it.tiles - 1;   // these land on the CTA's own barriers
+        const int next = i + 1 < it.tiles     ? rows_of(it, i + 1)
+                         : kShare && end < T ? rows_of(then, 0)
+                                             : 0;
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
 #pragma unroll 1
-      for (int u = 0; u < 4; ++u) {
-        warp_wait(bar(L::EMPTYV + sl), phase, abort_flag);
-        if (last)
-          expect_tx_elected(bar(L::LASTV + u), L::kUnit);
-        else if (leader)
-          expect_tx_elected(bar(L::FULLV + sl), 2 * L::kUnit);
-        const uint32_t full = last ? mapa_shared(bar(L::LASTV + u), rank) : lbar(L::FULLV + sl);
-        const uint32_t dst = sbase + L::kOffV + sl * L::kUnit;
-        const int x = 256 * (u & 1) + 128 * rank;
+        for (int u = 0; u < 4; ++u) {
+          warp_wait(bar(L::EMPTYV + sl), phase, abort_flag);
+          if (last)
+            expect_tx_elected(bar(L::LASTV + u), L::kUnit);
+          else if (leader)
+            expect_tx_elected(bar(L::FULLV + sl), 2 * L::kUnit);
+          const uint32_t full = last ? mapa_shared(bar(L::LASTV + u), rank) : lbar(L::FULLV + sl);
+          const uint32_t dst = sbase + L::kOffV + sl * L::kUnit;
+          const int x = 256 * (u & 1) + 128 * rank;
 #pragma unroll 1
-        for (int i = 0; i < np; ++i) {
-          const int r = __shfl_sync(0xffffffffu, row, (u >> 1) * np + i);
-          tma_load_pair(dst + i * brows * 128, &tmap, x, r, full, stream);
-          if (!kFp8)   // a bf16 unit is two 64-column boxes
-            tma_load_pair(dst + kPBox + i * brows * 128, &tmap, x + 64, r, full, stream);
+          for (int i = 0; i < np; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, (u >> 1) * np + i);
+            tma_load_pair(dst + i * brows * 128, &tmap, x, r, full, stream);
+            if (!kFp8)   // a bf16 unit is two 64-column boxes
+              tma_load_pair(dst + kPBox + i * brows * 128, &tmap, x + 64, r, full, stream);
+          }
+          if (++sl == L::kSlotsV) {
+            sl = 0;
+            phase ^= 1;
+          }
         }
-        if (++sl == L::kSlotsV) {
-          sl = 0;
-          phase ^= 1;
-        }
+        row = next;
       }
-      row = next;
+      t0 = end;
+      it = then;
     }
   } else if (warp == kWarpScore || warp == kWarpScore + 1) {
     // ------------------------------------------------------------ score MMAs (even CTA)
@@ -423,32 +495,45 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
                                  (128u >> 3 << 17) | (128u >> 4 << 24);
       const uint64_t q0 = umma_desc_sw128(sbase + L::kOffQ, 16, 1024);
       const uint64_t s0 = umma_desc_sw128(sbase + L::kOffS, 16, 1024);
-      warp_wait(bar(L::QFULL), 0, abort_flag);
-      for (int t = 0; t < T; ++t) {
-        const int sb = t & 1;
-        if (t >= 2) warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        const uint32_t d = tmem + 128 * i + 64 * sb;
-        uint32_t more = 0;
+      TileItem it = item0;
+      for (int t0 = 0, n = 0; t0 < T; ++n) {   // items
+        const int end = t0 + it.tiles;
+        if (kShare && warp == kWarpScore && blockIdx.x % parts == 0 && it.r0 == 0)
+          // The run with a sequence's first tile says how many runs it spans.
+          for (int q = lane; q < p.q_len; q += 32)
+            p.pieces[it.v * p.q_len + q] = count_pieces(it, share.first + t0, share.each);
+        warp_wait(bar(L::QFULL), n & 1, abort_flag);
+        for (int t = t0; t < end; ++t) {
+          const int sb = t & 1;
+          if (t >= 2) warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
+          if (__any_sync(0xffffffffu, *abort_flag)) break;
+          const uint32_t d = tmem + 128 * i + 64 * sb;
+          uint32_t more = 0;
 #pragma unroll 1
-        for (int k = (L::kBoxes * t + i) & 1; k < L::kBoxes; k += 2) {
-          const int pos = L::kBoxes * t + k, sl = pos % L::kSlotsS;
-          warp_wait(bar(L::FULLS + sl), (pos / L::kSlotsS) & 1, abort_flag);
-          tc_fence_after();
-          const uint64_t b = s0 + static_cast<uint64_t>(sl * (kPBox >> 4));
+          for (int k = (L::kBoxes * t + i) & 1; k < L::kBoxes; k += 2) {
+            const int pos = L::kBoxes * t + k, sl = pos % L::kSlotsS;
+            warp_wait(bar(L::FULLS + sl), (pos / L::kSlotsS) & 1, abort_flag);
+            tc_fence_after();
+            const uint64_t b = s0 + static_cast<uint64_t>(sl * (kPBox >> 4));
 #pragma unroll
-          for (int part = 0; part < L::kParts; ++part) {
-            const uint64_t a = q0 + static_cast<uint64_t>((part * L::kBoxes + k) * (kPBox >> 4));
-            // 32 bytes of K a step; the fifth E4M3 box holds 64 columns: two steps
+            for (int part = 0; part < L::kParts; ++part) {
+              const uint64_t a = q0 + static_cast<uint64_t>((part * L::kBoxes + k) * (kPBox >> 4));
+              // 32 bytes of K a step; the fifth E4M3 box holds 64 columns: two steps
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              if (!kFp8 || ks < 2 || k < 4)
-                mma_pair<kFp8>(d, a + 2 * ks, b + 2 * ks, idesc, part > 0 || ks > 0 ? 1u : more);
+              for (int ks = 0; ks < 4; ++ks)
+                if (!kFp8 || ks < 2 || k < 4)
+                  mma_pair<kFp8>(d, a + 2 * ks, b + 2 * ks, idesc, part > 0 || ks > 0 ? 1u : more);
+            }
+            more = 1;
+            commit_pair(bar(L::EMPTYS + sl));
           }
-          more = 1;
-          commit_pair(bar(L::EMPTYS + sl));
+          commit_pair(bar(L::SREADY + sb));
         }
-        commit_pair(bar(L::SREADY + sb));
+        t0 = end;
+        if (kShare && t0 < T) {
+          commit_pair(bar(L::QFREE));
+          it = item_after(it, t0);
+        }
       }
     }
   } else if (warp == kWarpOut || warp == kWarpOut + 1) {
@@ -462,35 +547,45 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
       // rows (K) in groups of eight 1024 bytes apart; bf16: two 64-column boxes
       const uint64_t v0 = umma_desc_sw128(sbase + L::kOffV, kPBox, 1024);
       const uint32_t d = tmem + L::kOCol + 128 * jj;
-      for (int t = 0; t < T; ++t) {
-        const int pb = t & 1;
-        warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        const bool last = zero_last && t == T - 1;
+      TileItem it = item0;
+      int zeroed = 0;   // zeroed last tiles so far
+      for (int t0 = 0; t0 < T;) {   // items
+        const int end = t0 + it.tiles;
+        const bool zero = zero_last(it);
+        for (int t = t0; t < end; ++t) {
+          const int pb = t & 1;
+          warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
+          if (__any_sync(0xffffffffu, *abort_flag)) break;
+          const bool last = zero && t == end - 1;
 #pragma unroll 1
-        for (int kh = 0; kh < 2; ++kh) {
-          const int u = 2 * kh + jj, pos = 4 * t + u, sl = pos % L::kSlotsV;
-          if (last)
-            warp_wait(bar(L::ZEROED + u), 0, abort_flag);
-          else
-            warp_wait(bar(L::FULLV + sl), (pos / L::kSlotsV) & 1, abort_flag);
-          tc_fence_after();
-          const uint64_t b = v0 + static_cast<uint64_t>(sl * (L::kUnit >> 4));
-          // 64 rows: bf16 four steps of 16 (2 KB of rows, 32 bytes of P's box kh); E4M3
-          // two steps of 32 (4 KB; 32 bytes of each part's row, the half at byte 64 kh)
+          for (int kh = 0; kh < 2; ++kh) {
+            // A tile's four units take the ring's four slots; zeroed ones pass FULLV by.
+            const int u = 2 * kh + jj, sl = u;
+            if (last)
+              warp_wait(bar(L::ZEROED + u), zeroed & 1, abort_flag);
+            else
+              warp_wait(bar(L::FULLV + sl), (t - zeroed) & 1, abort_flag);
+            tc_fence_after();
+            const uint64_t b = v0 + static_cast<uint64_t>(sl * (L::kUnit >> 4));
+            // 64 rows: bf16 four steps of 16 (2 KB of rows, 32 bytes of P's box kh); E4M3
+            // two steps of 32 (4 KB; 32 bytes of each part's row, the half at byte 64 kh)
 #pragma unroll
-          for (int part = 0; part < L::kParts; ++part) {
-            const uint64_t a = p0 + static_cast<uint64_t>(t % L::kPBufs * (kPBufBytes >> 4)) +
-                               ((kFp8 ? part * kPBox + 64 * kh : kh * kPBox) >> 4);
+            for (int part = 0; part < L::kParts; ++part) {
+              const uint64_t a = p0 + static_cast<uint64_t>(t % L::kPBufs * (kPBufBytes >> 4)) +
+                                 ((kFp8 ? part * kPBox + 64 * kh : kh * kPBox) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < (kFp8 ? 2 : 4); ++ks)
-              mma_pair<kFp8>(d, a + 2 * ks, b + ks * ((kFp8 ? 4096 : 2048) >> 4),
-                             idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
-                             part > 0 || ks > 0 ? 1u : (t > 0 || kh > 0 ? 1u : 0u));
+              for (int ks = 0; ks < (kFp8 ? 2 : 4); ++ks)
+                mma_pair<kFp8>(d, a + 2 * ks, b + ks * ((kFp8 ? 4096 : 2048) >> 4),
+                               idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
+                               part > 0 || ks > 0 ? 1u : (t > t0 || kh > 0 ? 1u : 0u));
+            }
+            commit_pair(bar(L::EMPTYV + sl));
           }
-          commit_pair(bar(L::EMPTYV + sl));
+          commit_pair(bar(L::PVDONE + pb));
         }
-        commit_pair(bar(L::PVDONE + pb));
+        t0 = end;
+        zeroed += zero ? 1 : 0;
+        if (kShare && t0 < T) it = item_after(it, t0);
       }
     }
   } else {
@@ -502,189 +597,231 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
     const int head = 32 * (qd & 1) + lane, row0 = 64 * (qd >> 1) + kCols * hh;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qd) << 16);
     const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
-    // E4M3: the head's unit, written by the kernel before (known complete once the
-    // first scores are).
-    float scale = p.scale_log2;
-    // Columns of the chunk this head's token attends: a token before the last sees fewer.
-    const int token = (first + min(head, mine - 1)) / p.H;
-    const int limit = min(r1, len - (p.q_len - 1 - token)) - r0 - row0;
-    float m = -INFINITY, l = 0.f;
-    // A wait that gives up leaves the loop running (every later wait then returns at
-    // once), so that all softmax warps meet at the same barriers.
-    for (int t = 0; t < T; ++t) {
-      const int sb = t & 1;
-      warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
-      if (kFp8 && t == 0)
-        scale *= __ldcg(sigma + flat0 + min(head, mine - 1));
-      tc_fence_after();
-      float x[kCols], y[kCols];
-      const uint32_t s_at = lanes + 64 * sb + kCols * hh;
-      if constexpr (kCols == 32) {
-        tmem_ld32(s_at, reinterpret_cast<uint32_t*>(x));
-        tmem_ld32(s_at + 128, reinterpret_cast<uint32_t*>(y));
-      } else {
-        tmem_ld16(s_at, reinterpret_cast<uint32_t*>(x));
-        tmem_ld16(s_at + 128, reinterpret_cast<uint32_t*>(y));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(lbar(L::SFREE + sb));
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) x[i] += y[i];
-      if (__any_sync(0xffffffffu, t * kTileRows + kCols > limit)) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (t * kTileRows + i >= limit) x[i] = -INFINITY;
-      }
-      float mx = x[0];
-#pragma unroll
-      for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
-      float* rd = red + sb * 2 * kSlices * kPHeads;
-      rd[part_of * kPHeads + head] = mx;
-      named_bar_sync(1, L::kSoft);
-      mx = rd[head];
-#pragma unroll
-      for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, rd[i * kPHeads + head]);
-      mx = mx * scale - L::kBias;
-      if (__any_sync(0xffffffffu, mx > m + L::kGrow)) {
-        // Move the references of the warp's heads (the four warps of the same heads
-        // decide alike); rescale the sum and this warp's share of O.
-        const float mn = fmaxf(m, mx);
-        const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
-        m = mn;
-        l *= alpha;
-        if (t > 0) {
-          warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 8 / kSlices; ++c) {   // this warp's slice of O's 256 columns
-            const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 32 * c;
-            float o[32];
-            tmem_ld32(at, reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_st8(at + 8 * i, o + 8 * i);
-          }
-          tmem_wait_st();
+    const int back = p.q_len - 1 - (first + min(head, mine - 1)) / p.H;   // tokens behind its own
+    TileItem it = item0;
+    int zeroed = 0;   // zeroed last tiles so far
+    for (int t0 = 0; t0 < T;) {   // items; t0: the item's first tile among the pair's
+      const int flat0 = it.v * all + first, tiles = it.tiles;
+      const bool zero = zero_last(it);
+      // E4M3: the head's unit, written by the kernel before (known complete once the
+      // first scores are).
+      float scale = p.scale_log2;
+      // Rows from this thread's first on that its head's token attends: one before the last
+      // token sees fewer.
+      const int limit = min(tiles * kTileRows, it.len - back - it.r0) - row0 + t0 * kTileRows;
+      float m = -INFINITY, l = 0.f;
+      // A wait that gives up leaves the loop running (every later wait then returns at
+      // once), so that all softmax warps meet at the same barriers.
+      for (int t = t0; t < t0 + tiles; ++t) {
+        const int sb = t & 1;
+        warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
+        if (kFp8 && t == t0)
+          scale *= __ldcg(sigma + flat0 + min(head, mine - 1));
+        tc_fence_after();
+        float x[kCols], y[kCols];
+        const uint32_t s_at = lanes + 64 * sb + kCols * hh;
+        if constexpr (kCols == 32) {
+          tmem_ld32(s_at, reinterpret_cast<uint32_t*>(x));
+          tmem_ld32(s_at + 128, reinterpret_cast<uint32_t*>(y));
+        } else {
+          tmem_ld16(s_at, reinterpret_cast<uint32_t*>(x));
+          tmem_ld16(s_at + 128, reinterpret_cast<uint32_t*>(y));
         }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lbar(L::SFREE + sb));
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        x[i] = ex2(fmaf(x[i], scale, -ref));
-        l += x[i];
-      }
-      // P's buffer was last read by the output MMAs of tile t - kPBufs.
-      if (t >= L::kPBufs)
-        warp_wait(bar(L::PVDONE + ((t - L::kPBufs) & 1)), ((t - L::kPBufs) >> 1) & 1, abort_flag);
-      uint8_t* pb = smem + L::kOffP + (t % L::kPBufs) * kPBufBytes;
-      if (kFp8) {
-        // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
+        for (int i = 0; i < kCols; ++i) x[i] += y[i];
+        if (__any_sync(0xffffffffu, t * kTileRows + kCols > limit)) {
 #pragma unroll
-        for (int c = 0; c < kCols / 16; ++c) {
-          uint32_t hi[4], lo[4];
+          for (int i = 0; i < kCols; ++i)
+            if (t * kTileRows + i >= limit) x[i] = -INFINITY;
+        }
+        float mx = x[0];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t a = 0, b = 0;
+        for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
+        float* rd = red + sb * 2 * kSlices * kPHeads;
+        rd[part_of * kPHeads + head] = mx;
+        named_bar_sync(1, L::kSoft);
+        mx = rd[head];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y0 = x[16 * c + 4 * w + 2 * e], y1 = x[16 * c + 4 * w + 2 * e + 1];
-              const uint32_t f1 =
-                  __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-              const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                  static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3)));
-              const uint32_t f2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - g.x, y1 - g.y),
-                                                           __NV_SATFINITE, __NV_E5M2);
-              a |= f1 << (16 * e);
-              b |= f2 << (16 * e);
+        for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, rd[i * kPHeads + head]);
+        mx = mx * scale - L::kBias;
+        if (__any_sync(0xffffffffu, mx > m + L::kGrow)) {
+          // Move the references of the warp's heads (the four warps of the same heads
+          // decide alike); rescale the sum and this warp's share of O.
+          const float mn = fmaxf(m, mx);
+          const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
+          m = mn;
+          l *= alpha;
+          if (t > t0) {
+            warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8 / kSlices; ++c) {   // this warp's slice of O's 256 columns
+              const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 32 * c;
+              float o[32];
+              tmem_ld32(at, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tmem_st8(at + 8 * i, o + 8 * i);
             }
-            hi[w] = a;
-            lo[w] = b;
+            tmem_wait_st();
           }
-          const uint32_t at = sw128(head, row0 / 16 + c);
-          *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pb + kPBox + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-      } else {
-        // Row `head` of the box of this row half, 128 bytes of 64 tile rows.
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int c = 0; c < kCols / 8; ++c)
-          *reinterpret_cast<uint4*>(pb + (qd >> 1) * kPBox + sw128(head, kCols / 8 * hh + c)) =
-              make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
-                         pack_bf16(x[8 * c + 4], x[8 * c + 5]),
-                         pack_bf16(x[8 * c + 6], x[8 * c + 7]));
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(lbar(L::PREADY + sb));
-      if (t == T - 1 && zero_last) {
-        // As each unit of the last tile lands in this CTA, zero its rows past the end.
-        for (int u = 0; u < 4; ++u) {
-          warp_wait(bar(L::LASTV + u), 0, abort_flag);
-          const int from = max(0, zero_from - 64 * (u >> 1));
-          uint8_t* unit = smem + L::kOffV + ((4 * t + u) % L::kSlotsV) * L::kUnit;
-          for (int i = tid; i < (64 - from) * 8 * (L::kUnit / kPBox); i += L::kSoft) {
-            const int box = i / ((64 - from) * 8), r = i % ((64 - from) * 8);
-            *reinterpret_cast<uint4*>(unit + box * kPBox + from * 128 + 16 * r) =
-                make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kCols; ++i) {
+          x[i] = ex2(fmaf(x[i], scale, -ref));
+          l += x[i];
+        }
+        // P's buffer was last read by the output MMAs of tile t - kPBufs.
+        if (t >= L::kPBufs)
+          warp_wait(bar(L::PVDONE + ((t - L::kPBufs) & 1)), ((t - L::kPBufs) >> 1) & 1, abort_flag);
+        uint8_t* pb = smem + L::kOffP + (t % L::kPBufs) * kPBufBytes;
+        if (kFp8) {
+          // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t a = 0, b = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float y0 = x[16 * c + 4 * w + 2 * e], y1 = x[16 * c + 4 * w + 2 * e + 1];
+                const uint32_t f1 =
+                    __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+                const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3)));
+                const uint32_t f2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - g.x, y1 - g.y),
+                                                             __NV_SATFINITE, __NV_E5M2);
+                a |= f1 << (16 * e);
+                b |= f2 << (16 * e);
+              }
+              hi[w] = a;
+              lo[w] = b;
+            }
+            const uint32_t at = sw128(head, row0 / 16 + c);
+            *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(pb + kPBox + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(lbar(L::ZEROED + u));
+        } else {
+          // Row `head` of the box of this row half, 128 bytes of 64 tile rows.
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c)
+            *reinterpret_cast<uint4*>(pb + (qd >> 1) * kPBox + sw128(head, kCols / 8 * hh + c)) =
+                make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
+                           pack_bf16(x[8 * c + 4], x[8 * c + 5]),
+                           pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lbar(L::PREADY + sb));
+        if (t == t0 + tiles - 1 && zero) {
+          // As each unit of the last tile lands in this CTA, zero its rows past the end.
+          for (int u = 0; u < 4; ++u) {
+            warp_wait(bar(L::LASTV + u), zeroed & 1, abort_flag);
+            const int from = max(0, zero_from(it) - 64 * (u >> 1));
+            uint8_t* unit = smem + L::kOffV + u * L::kUnit;
+            for (int i = tid; i < (64 - from) * 8 * (L::kUnit / kPBox); i += L::kSoft) {
+              const int box = i / ((64 - from) * 8), r = i % ((64 - from) * 8);
+              *reinterpret_cast<uint4*>(unit + box * kPBox + from * 128 + 16 * r) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(lbar(L::ZEROED + u));
+          }
         }
       }
-    }
-    if (tid == 0) pdl_launch_dependents();   // the combine waits for this grid anyway
-    // The row sums of a head's four threads, its log-sum-exp, and O / sum through
-    // shared memory (over operands that nothing reads any more) to whole rows.
-    named_bar_sync(1, L::kSoft);   // every read of the maxima is done
-    red[part_of * kPHeads + head] = l;
-    warp_wait(bar(L::PVDONE + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag);
-    tc_fence_after();
-    named_bar_sync(1, L::kSoft);
-    if (!*abort_flag) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2 * kSlices; ++i) sum += red[i * kPHeads + head];
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const size_t row = static_cast<size_t>(flat0) * p.splits + j;   // of the first
-      if (part_of == 0 && head < mine && p.part_lse)
-        p.part_lse[row + static_cast<size_t>(head) * p.splits] =
-            sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-      uint8_t* stage = smem;
-      // This warp's slice of O's columns: in tile jj = col0 / 128 the lane's 128 columns
-      // are latents 256 jj + 128 (qd >> 1) ..
-      const int col0 = 256 / kSlices * hh;
-      float* to = reinterpret_cast<float*>(stage + head * L::kStageRow) + 256 * (col0 >> 7) +
-                  128 * (qd >> 1) + (col0 & 127);
-#pragma unroll 1
-      for (int c = 0; c < 8 / kSlices; ++c) {
-        float o[32];
-        tmem_ld32(lanes + L::kOCol + col0 + 32 * c, reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(to + 32 * c + 4 * i) =
-              make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
-                          o[4 * i + 3] * inv);
-      }
+      t0 += tiles;
+      zeroed += zero ? 1 : 0;
+      if (tid == 0 && t0 == T) pdl_launch_dependents();   // the combine waits for this grid anyway
+      // The row sums of a head's four threads, its log-sum-exp, and O / sum through
+      // shared memory (over operands that nothing reads any more) to whole rows.
+      float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
+      sums[part_of * kPHeads + head] = l;
+      warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      tc_fence_after();
       named_bar_sync(1, L::kSoft);
-      const bool bf16_out = p.direct && p.io_bf16;
-      for (int h = warp; h < mine; h += L::kSoftWarps) {
-        const float4* src = reinterpret_cast<const float4*>(stage + h * L::kStageRow);
-        const size_t at = (row + static_cast<size_t>(h) * p.splits) * kDc;
+      if (!*abort_flag) {
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 o = src[32 * i + lane];
+        for (int i = 0; i < 2 * kSlices; ++i) sum += sums[i * kPHeads + head];
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const bool whole = kShare ? whole_set(it) : p.direct != 0;   // the result itself
+        const size_t stride = whole ? 1 : p.splits;
+        const size_t row = static_cast<size_t>(flat0) * stride + (whole ? 0 : it.j);   // the first's
+        float* o_to = kShare && whole ? static_cast<float*>(p.out) : p.part_o;
+        float* lse_to = kShare && whole ? p.out_lse : p.part_lse;
+        const bool bf16_out = whole && p.io_bf16;
+        // Four values of row h, column x.
+        auto put = [&](int h, int x, float4 o) {
+          const size_t at = (row + static_cast<size_t>(h) * stride) * kDc + x;
           if (bf16_out)
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.part_o) + at + 128 * i +
-                                      4 * lane) =
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(o_to) + at) =
                 make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
           else
-            *reinterpret_cast<float4*>(p.part_o + at + 128 * i + 4 * lane) = o;
+            *reinterpret_cast<float4*>(o_to + at) = o;
+        };
+        if (part_of == 0 && head < mine && lse_to)
+          lse_to[row + static_cast<size_t>(head) * stride] =
+              sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        if (kShare && t0 < T) {
+          // The next item's operands are on their way to where the last one stages: each
+          // warp turns its 32 heads' columns over in its part of P, 16 at a time, and
+          // writes 64 bytes of eight rows at once.  (P of the next tile is written behind
+          // the barrier of its maxima.)
+          const int col0 = 256 / kSlices * hh;
+          const int at = 256 * (col0 >> 7) + 128 * (qd >> 1) + (col0 & 127);   // latent
+          float4* mine4 = reinterpret_cast<float4*>(smem + L::kOffP) + 128 * warp;
+          const int h0 = 32 * (qd & 1);
+#pragma unroll 1
+          for (int c = 0; c < 16 / kSlices; ++c) {
+            float o[16];
+            tmem_ld16(lanes + L::kOCol + col0 + 16 * c, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mine4[4 * lane + (i ^ (lane >> 1 & 3))] = make_float4(
+                  o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2), q = lane & 3;
+              if (h0 + r < mine)
+                put(h0 + r, at + 16 * c + 4 * q, mine4[4 * r + (q ^ (r >> 1 & 3))]);
+            }
+            __syncwarp();
+          }
+        } else {
+          uint8_t* stage = smem;
+          // This warp's slice of O's columns: in tile jj = col0 / 128 the lane's 128 columns
+          // are latents 256 jj + 128 (qd >> 1) ..
+          const int col0 = 256 / kSlices * hh;
+          float* to = reinterpret_cast<float*>(stage + head * L::kStageRow) + 256 * (col0 >> 7) +
+                      128 * (qd >> 1) + (col0 & 127);
+#pragma unroll 1
+          for (int c = 0; c < 8 / kSlices; ++c) {
+            float o[32];
+            tmem_ld32(lanes + L::kOCol + col0 + 32 * c, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(to + 32 * c + 4 * i) =
+                  make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
+                              o[4 * i + 3] * inv);
+          }
+          named_bar_sync(1, L::kSoft);
+          for (int h = warp; h < mine; h += L::kSoftWarps) {
+            const float4* src = reinterpret_cast<const float4*>(stage + h * L::kStageRow);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(h, 128 * i + 4 * lane, src[32 * i + lane]);
+          }
         }
       }
+      if (kShare && t0 < T) it = item_after(it, t0);
     }
   }
   // A CTA that gave up may have copies in flight: they land long before this.
@@ -704,15 +841,15 @@ __global__ void __launch_bounds__(PairPlan<kFp8>::kThreads, 1)
   if (tid == 0 && *abort_flag) report(p.status, MLA_DEV_PIPELINE_TIMEOUT);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kShare>
 mla_status launch_pair(const CUtensorMap& cache, const CUtensorMap& q, const CUtensorMap& qpe,
                        const SplitParams& p, const float* sigma, cudaStream_t s, const char* who) {
   using L = PairPlan<kFp8>;
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_pair_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(L::kSmem)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(split_pair_kernel<kFp8, kShare>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem)) != cudaSuccess) {
       cudaGetLastError();
       set_error("%s: cannot reserve %zu bytes of shared memory", who, L::kSmem);
       return MLA_ERR_CUDA;
@@ -720,8 +857,9 @@ mla_status launch_pair(const CUtensorMap& cache, const CUtensorMap& q, const CUt
     attr_done.set(dev);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pair_groups(p.q_len * p.H), p.splits, p.B / p.q_len);
-  cfg.blockDim = dim3(L::kThreads);
+  const int ctas = 2 * pair_groups(p.q_len * p.H);   // of a row
+  cfg.gridDim = kShare ? dim3(share_runs(ctas) * ctas) : dim3(ctas, p.splits, p.B / p.q_len);
+  cfg.blockDim = dim3(kShare ? L::kShareThreads : L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -732,7 +870,7 @@ mla_status launch_pair(const CUtensorMap& cache, const CUtensorMap& q, const CUt
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = launch_overlap_enabled() ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, split_pair_kernel<kFp8>, cache, q, qpe, p, sigma);
+  cudaLaunchKernelEx(&cfg, split_pair_kernel<kFp8, kShare>, cache, q, qpe, p, sigma);
   return launch_status(who);
 }
 
@@ -788,12 +926,15 @@ mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
     set_error("%s: cuTensorMapEncodeTiled failed (%d)", who, int(bad));
     return MLA_ERR_CUDA;
   }
-  if (!fp8) return launch_pair<false>(tm, tq, tp, p, nullptr, stream, who);
+  if (!fp8)
+    return p.pieces ? launch_pair<false, true>(tm, tq, tp, p, nullptr, stream, who)
+                    : launch_pair<false, false>(tm, tq, tp, p, nullptr, stream, who);
   if (!p.late) {
     const mla_status st = launch_pair_queries(p, stream, who);
     if (st != MLA_OK) return st;
   }
-  return launch_pair<true>(tm, tq, tp, p, sigma, stream, who);
+  return p.pieces ? launch_pair<true, true>(tm, tq, tp, p, sigma, stream, who)
+                  : launch_pair<true, false>(tm, tq, tp, p, sigma, stream, who);
 }
 
 }  // namespace mla

@@ -41,8 +41,10 @@ struct SplitParams {
   // (which lets this one start early), so they are read after the PDL wait; the queries'
   // FP8 codes were made before the selection.
   int late;
-  // Paged FP8 cache, equal shares (persist): how many partials each query group has.
+  // Equal shares (take_share): how many partials each query group has; NULL otherwise.
   int32_t* pieces;
+  void* out;                    // SM pairs, equal shares: o_c (else NULL) and lse (may be
+  float* out_lse;               // NULL), where an item that is a whole set writes its result
 };
 
 // o_c = 0 and lse = -inf of `heads` heads from `row` (query group x H + head), which
@@ -117,35 +119,49 @@ __device__ __forceinline__ int warp_exclusive_scan(int x, int lane, int* total) 
   return incl - x;
 }
 
-// Equal shares of a paged call's tiles.  The tiles of all query groups, one after another,
-// are cut into runs of `each`, one per CTA; a run may end inside a sequence and start with
-// the rest of another, and each (run, query group) that meet is one partial.  A sequence of
-// n tiles has at most ceil(n / each) + 1 of them, which `each` keeps within p.splits.
-constexpr int kShareGroups = 512;   // query groups the planning warp holds, 16 a lane
+// Equal shares of a paged call's tiles.  The tiles of all its rows sets -- one per query
+// group, or per sequence where a kernel takes a sequence's tokens together (kSeq) -- one
+// after another are cut into runs of `each`, one per CTA or pair of CTAs.  A run may end
+// inside a set and start with the rest of another; each (run, set) that meet is an item and
+// gives one partial.  A set of n tiles has at most ceil(n / each) + 1 of them, which `each`
+// keeps within p.splits.
+constexpr int kShareSets = 512;   // sets the planning warp holds, 16 a lane
 struct TileShare {
   int each;    // tiles per run
   int first;   // this run's first tile among all
   int tiles;   // and how many it has
-  int v, off;  // its first tile: tile `off` of query group v
+  int v, off;  // its first tile: tile `off` of set v
 };
+struct TileItem {
+  int v, j;       // set, index of the partial among the set's own
+  int r0, tiles;  // first row, 128-row tiles
+  int len;        // rows of the set
+};
+template <bool kSeq>
+__device__ __forceinline__ int set_length(const SplitParams& p, int v) {
+  return clamp_length(p, kSeq ? (v + 1) * p.q_len - 1 : v, false);
+}
 // Run c of `runs`, by one whole warp.
+template <bool kSeq>
 __device__ __forceinline__ TileShare take_share(const SplitParams& p, int c, int runs, int lane,
                                                 bool report_it) {
-  constexpr int kEach = kShareGroups / 32;
+  constexpr int kEach = kShareSets / 32;
+  const int sets = kSeq ? p.B / p.q_len : p.B;
   int n[kEach], sum = 0, top = 0;
   // All loads first (a report may follow each check, and no load moves above it); blocks of
-  // 32 groups that are not there are skipped, not computed.
+  // 32 sets that are not there are skipped, not computed.
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int v = 32 * i + lane;
     n[i] = 0;
-    if (32 * i < p.B && v < p.B) n[i] = p.lengths[p.q_len == 1 ? v : v / p.q_len];
+    if (32 * i < sets && v < sets) n[i] = p.lengths[kSeq || p.q_len == 1 ? v : v / p.q_len];
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    if (32 * i >= p.B) break;
+    if (32 * i >= sets) break;
     const int v = 32 * i + lane;
-    if (v < p.B) n[i] = (clamp_length(p, v, report_it, n[i]) + 127) / 128;
+    if (v < sets)
+      n[i] = (clamp_length(p, kSeq ? (v + 1) * p.q_len - 1 : v, report_it, n[i]) + 127) / 128;
     sum += n[i];
     top = max(top, n[i]);
   }
@@ -159,7 +175,7 @@ __device__ __forceinline__ TileShare take_share(const SplitParams& p, int c, int
   int base = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    if (32 * i >= p.B || base > s.first) break;
+    if (32 * i >= sets || base > s.first) break;
     int total;
     const int at = base + warp_exclusive_scan(n[i], lane, &total);
     const uint32_t hit = __ballot_sync(0xffffffffu, s.first >= at && s.first < at + n[i]);
@@ -173,20 +189,51 @@ __device__ __forceinline__ TileShare take_share(const SplitParams& p, int c, int
   }
   return s;
 }
+// A value that all lanes hold, known to the compiler as such: what decides the loops around
+// the warps' MMAs and copies has to be, or their operands are moved lane by lane.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// The first item of run c, which has tiles; by whole warps, as next_item.
+template <bool kSeq>
+__device__ __forceinline__ TileItem first_item(const SplitParams& p, const TileShare& s, int c) {
+  const int v = uniform(s.v), off = uniform(s.off), len = uniform(set_length<kSeq>(p, v));
+  return TileItem{v, off > 0 ? c - (s.first - off) / s.each : 0, off * 128,
+                  uniform(min((len + 127) / 128 - off, s.tiles)), len};
+}
+// The item after `it`, with `left` > 0 tiles of the run to go: the start of the next set
+// that has any row.  (The bounds matter only if the lengths change under the kernel.)
+template <bool kSeq>
+__device__ __forceinline__ TileItem next_item(const SplitParams& p, TileItem it, int left) {
+  const int sets = kSeq ? p.B / p.q_len : p.B;
+  do {
+    it.v = uniform(min(it.v + 1, sets - 1));
+    it.len = uniform(set_length<kSeq>(p, it.v));
+  } while (it.len == 0 && it.v + 1 < sets);
+  it.j = it.r0 = 0;
+  it.tiles = uniform(max(1, min((it.len + 127) / 128, left)));
+  return it;
+}
+// Whether an item is its whole set.
+__device__ __forceinline__ bool whole_set(const TileItem& it) {
+  return it.r0 == 0 && it.tiles * 128 >= it.len;
+}
+// Partials of a set whose first tile is tile s of all.
+__device__ __forceinline__ int count_pieces(const TileItem& it, int s, int each) {
+  return (s + (it.len + 127) / 128 - 1) / each - s / each + 1;
+}
 
 // The FP8 (E4M3) cache's split kernel (mla_fp8.cu): same grid, partials and
 // launch overlap as the bf16 one.
 // It runs as two launches: the query's E4M3 image, then the split itself.
 mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_t stream,
                             const char* who);
-// Runs of an equal-share grid: one CTA per SM, the same number of each head group.
-int share_runs(int groups);
+// Runs of an equal-share grid whose rows each pass `ctas` CTAs: one CTA per SM.
+int share_runs(int ctas);
 
 // The paged split with bf16 queries as SM pairs (mla_pair.cu): the query rows of a
 // sequence (heads x tokens) in groups of up to 128, two CTAs a group; same partials,
 // chunks of whole tiles.  With an E4M3 cache the queries' codes go to p.q_img first.
 constexpr int kPairRows = 128;
-inline int pair_groups(int rows) { return (rows + kPairRows - 1) / kPairRows; }
+constexpr int pair_groups(int rows) { return (rows + kPairRows - 1) / kPairRows; }
 mla_status launch_split_pair(const SplitParams& p, const void* cache, bool fp8,
                              cudaStream_t stream, const char* who);
 

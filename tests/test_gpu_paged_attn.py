@@ -141,6 +141,34 @@ def test_equal_shares(cuda_lib, kind, io, heads, q_len, page, B):
         mla.load().mla_test_set_split_form(0)
 
 
+@pytest.mark.parametrize("kind", ["ragged", "one long", "edges"])
+@pytest.mark.parametrize("dtype,heads,q_len,page", [("bf16", 32, 1, 16), ("bf16", 128, 1, 64),
+                                                    ("bf16", 160, 1, 256), ("bf16", 16, 3, 32),
+                                                    ("fp8", 48, 1, 16), ("fp8", 128, 1, 64),
+                                                    ("fp8", 256, 1, 128), ("fp8", 64, 2, 32)])
+@pytest.mark.parametrize("B", [7, 70])
+def test_equal_shares_of_pairs(cuda_lib, kind, dtype, heads, q_len, page, B):
+    """The same with SM pairs, in a workspace that is 16-byte aligned and no more."""
+    mla = cuda_lib
+    lengths = share_lengths(kind, B)
+    if q_len > 1:
+        lengths = np.maximum(lengths, q_len)
+    mla.load().mla_test_set_split_form(1)
+    try:
+        c = Call(mla, lengths, page, dtype, BF16, heads, q_len=q_len, seed=B + heads)
+        c.ws = torch.empty(c.ws.numel() + 16, dtype=torch.uint8, device="cuda")[16:]
+        c.run()
+        first = c.o.clone()
+        c.check(tokens=range(0, B * q_len, max(1, B * q_len // 8)),
+                status=0 if lengths.min() else mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+        c.o.fill_(7)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(first, c.o)
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
 def test_equal_shares_by_size(cuda_lib):
     """Enough tiles that the planner takes equal shares itself; 512 query groups are the
     most it takes them for, and a length past s_max is cut and reported there too."""
