@@ -387,11 +387,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if (left == 0) {
         if (t > 0) cur = item_after(cur, t);
         left = cur.tiles;
+        f8_warp_wait(bar(B_QREADY), n & 1, abort_flag);
         if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
-          // The run with a query group's first tile says how many runs it spans.
+          // The run with a query group's first tile says how many runs it spans.  (Not
+          // before a query is here, fetched behind the PDL wait: the combine of the call
+          // before may still be reading its own counts.)
           p.pieces[cur.v] = count_pieces(cur, share.first + t, share.each);
         }
-        f8_warp_wait(bar(B_QREADY), n & 1, abort_flag);
         ++n;
       }
       --left;

@@ -498,11 +498,13 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
       TileItem it = item0;
       for (int t0 = 0, n = 0; t0 < T; ++n) {   // items
         const int end = t0 + it.tiles;
+        warp_wait(bar(L::QFULL), n & 1, abort_flag);
         if (kShare && warp == kWarpScore && blockIdx.x % parts == 0 && it.r0 == 0)
-          // The run with a sequence's first tile says how many runs it spans.
+          // The run with a sequence's first tile says how many runs it spans.  (Not before a
+          // query is here, fetched behind the PDL wait: the combine of the call before may
+          // still be reading its own counts.)
           for (int q = lane; q < p.q_len; q += 32)
             p.pieces[it.v * p.q_len + q] = count_pieces(it, share.first + t0, share.each);
-        warp_wait(bar(L::QFULL), n & 1, abort_flag);
         for (int t = t0; t < end; ++t) {
           const int sb = t & 1;
           if (t >= 2) warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);

@@ -169,6 +169,85 @@ def test_equal_shares_of_pairs(cuda_lib, kind, dtype, heads, q_len, page, B):
         mla.load().mla_test_set_split_form(0)
 
 
+SHARED = [("fp8", BF16, 16), ("fp8", F32, 32), ("bf16", BF16, 64), ("fp8", BF16, 128)]
+
+
+@pytest.mark.parametrize("dtype,io,heads", SHARED)
+def test_equal_shares_back_to_back(cuda_lib, dtype, io, heads):
+    """Calls that follow one another on one workspace, unsynchronised, with lengths that
+    change between them: each gives what it gives alone.  The counts of one call's partials
+    may not reach the combine of another."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(1)
+    try:
+        calls = []
+        for seed, lengths in enumerate((share_lengths("ragged", 24) + 1,
+                                        share_lengths("one long", 24) + 1, np.full(24, 640))):
+            calls.append(Call(mla, lengths, 64, dtype, io, heads, seed=seed, s_max=7000,
+                              width=110))
+        for c in calls:
+            c.ws = calls[0].ws
+        alone = []
+        for c in calls:
+            c.run()
+            torch.cuda.synchronize()
+            alone.append((c.o.clone(), c.lse.clone()))
+            c.check(tokens=[0, 11, 12, 23])
+        outs = [[torch.full_like(c.o, 7) for _ in range(12)] for c in calls]
+        torch.cuda.synchronize()
+        for k in range(12):
+            for c, o in zip(calls, outs):
+                c.o = o[k]
+                c.run()
+        torch.cuda.synchronize()
+        for (o, lse), c, got in zip(alone, calls, outs):
+            assert all(torch.equal(o, g) for g in got)
+            assert torch.equal(lse, c.lse)
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
+@pytest.mark.parametrize("dtype,io,heads", SHARED)
+def test_equal_shares_captured(cuda_lib, dtype, io, heads):
+    """A captured call cuts its shares anew from the lengths of each replay; without lse."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(1)
+    try:
+        c = Call(mla, [1500] * 20, 64, dtype, io, heads, seed=5)
+        c.lse = None
+        c.run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run()
+        c.lse = torch.empty((20, heads), device="cuda")
+        for lengths in (share_lengths("ragged", 20), [1] * 20, [1500] * 20, [0] * 19 + [1500]):
+            c.dev["lengths"].copy_(i32(lengths))
+            graph.replay()
+            got = c.o.clone()
+            c.o.fill_(7)
+            c.run()
+            torch.cuda.synchronize()
+            assert torch.equal(got, c.o)
+            c.lengths = np.asarray(lengths)
+            # rows between the length and the page's end are finite here; so are the pages
+            c.check(tokens=[0, 1, 10, 19],
+                    status=int(c.status.item()))
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
+@pytest.mark.parametrize("dtype,io,heads", SHARED)
+def test_equal_shares_of_one_long_sequence(cuda_lib, dtype, io, heads):
+    """One sequence over all CTAs: over a hundred partials."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(1)
+    try:
+        Call(mla, [40001], 64, dtype, io, heads, seed=6).run().check()
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
 def test_equal_shares_by_size(cuda_lib):
     """Enough tiles that the planner takes equal shares itself; 512 query groups are the
     most it takes them for, and a length past s_max is cut and reported there too."""
