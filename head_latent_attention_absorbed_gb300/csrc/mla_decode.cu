@@ -2068,9 +2068,9 @@ struct PlanOpts {
 constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
 // Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
-// 8192 rows, 64 sequences 56 / 46, 16 (6.7 tiles) 21.9 / 18.1, 8 (3.4) 15.3 / 15.7; all
-// full, 256 x 2048 79 / 78, 64 x 4096 43.4 / 43.9, 32 x 4096 (6.7) 23.8 / 24.9, 16 x 4096
-// (3.4) 15.5 / 18.1.
+// 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
+// full, 256 x 2048 75 / 73, 64 x 4096 40.8 / 40.9, 32 x 4096 (6.7) 24.6 / 25.4, 16 x 4096
+// (3.4) 16.1 / 18.6.
 constexpr int kShareMinTiles = 4;
 // The same for SM pairs: tiles per pair (bf16, E4M3), and sequences per pair up to which
 // (more are balanced as they are, with one chunk each and no combine).  64 heads, chunks /

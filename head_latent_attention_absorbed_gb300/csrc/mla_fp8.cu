@@ -61,15 +61,15 @@ constexpr int kOffLsum = kOffRed + 2 * kHeadGroup * 4 * 4;  // [16 heads][4 warp
 constexpr int kOffSigma = kOffLsum + kHeadGroup * 4 * 4;    // query scale per head
 constexpr int kOffBar = kOffSigma + kHeadGroup * 4;
 enum {
-  B_FULL = 0,      // [2] tile landed
-  B_EMPTY = 2,     // [2] tile's PV finished: buffer free
-  B_SFULL = 4,     // [2] scores of the tile in S[t & 1]
-  B_SFREE = 6,     // [2] softmax read S[t & 1]
-  B_PFULL = 8,     // [2] P of the tile written (and the tile's dead rows zeroed)
-  B_ODONE = 10,    // [2] PV of the tile finished
-  B_QREADY = 12,   // query parts written (once an item)
-  B_DONE = 13,     // every MMA finished
-  kNumBars = 14
+  B_FULL = 0,                      // [2][5] box landed
+  B_EMPTY = B_FULL + 2 * kF8Boxes,  // [2][5] the box's last MMA finished: free
+  B_SFULL = B_EMPTY + 2 * kF8Boxes,  // [2] scores of the tile in S[t & 1]
+  B_SFREE = B_SFULL + 2,   // [2] softmax read S[t & 1]
+  B_PFULL = B_SFREE + 2,   // [2] P of the tile written (and the tile's dead rows zeroed)
+  B_ODONE = B_PFULL + 2,   // [2] PV of the tile finished
+  B_QREADY = B_ODONE + 2,  // query parts written (once an item)
+  B_DONE = B_QREADY + 1,   // every MMA finished
+  kNumBars = B_DONE + 1
 };
 constexpr int kOffSlot = kOffBar + 8 * kNumBars;
 constexpr int kOffAbort = kOffSlot + 16;
@@ -203,9 +203,12 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
 // one item per query group it meets, streamed back to back: the copies and score MMAs of
 // the next item run while the last one's output is written.  (Writing it one tile later,
 // from a second O^T buffer, cost more registers and code than it saved: 47.7 us against
-// 46.3 on 64 sequences of 512 to 8192 rows; with chunks 56.)  Otherwise a CTA has one item,
-// its chunk.
-template <bool kPaged, bool kShare>
+// 46.3 on 64 sequences of 512 to 8192 rows, when that took 56 with chunks; 44 and 54 since
+// boxes are handed over one by one.)  Otherwise a CTA has one item, its chunk.
+// kShort: a chunk of one or two tiles, whose buffers are not filled again: one barrier for a
+// whole tile.  Longer chunks hand over box by box (dense, 8 x 4096 rows in two tiles 11.1 us
+// against 11.6; 4 x 65536 38.7 against 35.0, 128 heads 419 against 401).
+template <bool kPaged, bool kShare, bool kShort>
 __global__ void __launch_bounds__(kF8Threads, 1)
     split_fp8_kernel(const __grid_constant__ CUtensorMap tmap, const SplitParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -272,17 +275,34 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if (!kShare)
       bulk_g2s(sbase + kOffSigma, img + kFp8QBoxes, 16 * sizeof(float), bar(B_QREADY));
   };
+  // Box by box, so that a tile's first scores start while its last box is on its way, and a
+  // box is fetched again as soon as its own MMAs are done: the fifth, which only the scores
+  // read, first.
+  auto full = [&](int bf, int m) { return bar(B_FULL + (kShort ? bf : kF8Boxes * bf + m)); };
+  auto copy_box = [&](int bf, int m, int i, int r) {
+    tma_load_2d_elected(sbase + kOffTile + bf * kF8Tile + m * kF8Box + i * box_rows * 128, &tmap,
+                        128 * m, r, full(bf, m), pol);
+  };
   auto issue = [&](int t, int row) {
     const int bf = t & 1;
-    if (lane == 0) mbar_arrive_expect_tx(bar(B_FULL + bf), kF8Tile);
-    __syncwarp();
+    if (kShort) {
+      expect_tx_elected(full(bf, 0), kF8Tile);
 #pragma unroll 1
-    for (int i = 0; i < pieces; ++i) {
-      const int r = __shfl_sync(0xffffffffu, row, i);
+      for (int i = 0; i < pieces; ++i) {
+        const int r = __shfl_sync(0xffffffffu, row, i);
 #pragma unroll 1
-      for (int m = 0; m < kF8Boxes; ++m)
-        tma_load_2d_elected(sbase + kOffTile + bf * kF8Tile + m * kF8Box + i * box_rows * 128, &tmap,
-                         128 * m, r, bar(B_FULL + bf), pol);
+        for (int m = 0; m < kF8Boxes; ++m) copy_box(bf, m, i, r);
+      }
+      return;
+    }
+#pragma unroll 1
+    for (int k = 0; k < kF8Boxes; ++k) {
+      const int m = t < 2 ? k : k == 0 ? kF8Boxes - 1 : k - 1;
+      if (t >= 2)
+        f8_warp_wait(bar(B_EMPTY + kF8Boxes * bf + m), ((t - 2) >> 1) & 1, abort_flag);
+      expect_tx_elected(full(bf, m), kF8Box);
+#pragma unroll 1
+      for (int i = 0; i < pieces; ++i) copy_box(bf, m, i, __shfl_sync(0xffffffffu, row, i));
     }
   };
   // The producer's place: its next tile is tile i of `it`, with pieces at `row`; step()
@@ -310,21 +330,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       it = first;
       row = piece_row(it, 0);
     }
-    if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(B_FULL + i), 1);
-        mbar_init(bar(B_EMPTY + i), 1);
-        mbar_init(bar(B_SFULL + i), 1);
-        mbar_init(bar(B_SFREE + i), 8);
-        mbar_init(bar(B_PFULL + i), 8);
-        mbar_init(bar(B_ODONE + i), 1);
-      }
-      mbar_init(bar(B_QREADY), 1);
-      mbar_init(bar(B_DONE), 1);
-      *abort_flag = 0;
-      fence_mbarrier_init();
-      prefetch_tmap(&tmap);
-    }
+    // One barrier a lane: the first copies wait for this.
+    static_assert(kNumBars <= 32, "a barrier per lane");
+    if (lane < kNumBars && (kShare || lane != B_QREADY))
+      mbar_init(bar(lane), lane >= B_SFREE && lane < B_ODONE ? 8 : 1);   // S read, P written: 8 warps
+    if (lane == 0) *abort_flag = 0;
+    fence_mbarrier_init();
+    if (lane == 0) prefetch_tmap(&tmap);
     __syncwarp();
     if (!kShare) {   // both first tiles belong to the one item
       for (int t = 0; t < min(T, 2); ++t) {
@@ -335,6 +347,15 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       issue(0, row);
     }
     if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
+  } else if (!kShare && warp == 10) {
+    // Nothing goes on without the query, so its copy does not wait for the CTA's barrier.
+    if (lane == 0) {
+      mbar_init(bar(B_QREADY), 1);
+      fence_mbarrier_init();
+      pdl_wait();   // the image is written by the kernel before
+      load_query(first.v);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -354,7 +375,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     int issued = kShare ? 1 : min(T, 2);
     if (kShare) step(0);
     for (int t = issued; t < T; ++t) {
-      if (t >= 2) f8_warp_wait(bar(B_EMPTY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+      // Looked at once a tile; a wait inside that gave up leaves copies that land anyway.
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       issue(t, row);
       issued = t + 1;
@@ -372,7 +393,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     // Tiles still in flight land before the CTA may leave (bounded waits).
     for (int t = issued > 2 ? issued - 2 : 0; t < issued; ++t)
-      if (!mbar_wait_bounded(bar(B_FULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
+      for (int m = 0; m < (kShort ? 1 : kF8Boxes); ++m)
+        if (!mbar_wait_bounded(full(t & 1, m), (t >> 1) & 1)) *abort_flag = 1;
   } else if (warp == 9) {
     // ------------------------------------------------------------ score MMAs
     // The whole warp runs along, converged at every MMA; boxes are not unrolled (code
@@ -397,13 +419,17 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         ++n;
       }
       --left;
-      f8_warp_wait(bar(B_FULL + bf), (t >> 1) & 1, abort_flag);
+      if (kShort) f8_warp_wait(full(bf, 0), 0, abort_flag);
       if (t >= 2) f8_warp_wait(bar(B_SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       const uint32_t d = tmem + 64 * bf;
 #pragma unroll 1
       for (int m = 0; m < kF8Boxes; ++m) {
+        if (!kShort) {
+          f8_warp_wait(full(bf, m), (t >> 1) & 1, abort_flag);
+          tc_fence_after();
+        }
         const uint64_t a = a0 + static_cast<uint64_t>((bf * kF8Tile + m * kF8Box) >> 4);
         const uint64_t q = q0 + static_cast<uint64_t>((m * kQBox) >> 4);
         // a K step of 32 E4M3 columns moves the start by 32 B; the fifth box
@@ -414,10 +440,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             umma_e4m3(d, a + 2 * k, q + 2 * k, idesc_s, k > 0 ? 1u : (m > 0 ? 1u : 0u));
       }
       umma_commit_elected(bar(B_SFULL + bf));
+      if (!kShort && t + 2 < T) umma_commit_elected(bar(B_EMPTY + kF8Boxes * bf + 4));
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ query image, PV MMAs
-    if (lane == 0) {
+    if (kShare && lane == 0) {
       pdl_wait();   // the image is written by the kernel before
       load_query(first.v);
     }
@@ -446,9 +473,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
           umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
                     idesc_o, ks > 0 ? 1u : (done > 0 ? 1u : 0u));
+        if (!kShort && t + 2 < T)   // fetched again
+          umma_commit_elected(bar(B_EMPTY + kF8Boxes * bf + mb));
       }
       umma_commit_elected(bar(B_ODONE + bf));
-      umma_commit_elected(bar(B_EMPTY + bf));
     }
     umma_commit_elected(bar(B_DONE));
     mbar_wait_bounded(bar(B_DONE), 0);
@@ -737,12 +765,13 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_fp8_kernel<false, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(split_fp8_kernel<true, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(split_fp8_kernel<true, true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kF8Smem)) != cudaSuccess) {
+    bool ok = true;
+    for (auto k : {split_fp8_kernel<false, false, false>, split_fp8_kernel<false, false, true>,
+                   split_fp8_kernel<true, false, false>, split_fp8_kernel<true, false, true>,
+                   split_fp8_kernel<true, true, false>})
+      ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      int(kF8Smem)) == cudaSuccess;
+    if (!ok) {
       set_error("%s: cannot reserve %zu bytes of shared memory", who, kF8Smem);
       return MLA_ERR_CUDA;
     }
@@ -751,9 +780,12 @@ mla_status launch_split_fp8(const SplitParams& p, const void* cache, cudaStream_
   if (!p.late) launch_pdl(fp8_q_prep_kernel, dim3(p.H, p.B), dim3(160), 0, stream, p);
   const int groups = p.H / kHeadGroup;
   const dim3 grid = p.pieces ? dim3(share_runs(groups) * groups) : dim3(groups, p.splits, p.B);
-  launch_pdl(p.pieces  ? split_fp8_kernel<true, true>
-             : p.table ? split_fp8_kernel<true, false>
-                       : split_fp8_kernel<false, false>,
+  const bool few = p.chunk <= 2 * kF8Rows;
+  launch_pdl(p.pieces  ? split_fp8_kernel<true, true, false>
+             : p.table ? (few ? split_fp8_kernel<true, false, true>
+                              : split_fp8_kernel<true, false, false>)
+                       : (few ? split_fp8_kernel<false, false, true>
+                              : split_fp8_kernel<false, false, false>),
              grid, dim3(kF8Threads), kF8Smem, stream, tmap, p);
   return launch_status(who);
 }
