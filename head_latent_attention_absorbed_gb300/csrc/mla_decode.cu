@@ -2061,17 +2061,18 @@ struct PlanOpts {
 };
 // Query rows (heads x tokens) of a sequence from which a paged call with bf16 queries
 // runs as SM pairs (mla_pair.cu), whose tile costs the same for 16 rows as for 128.
-// Measured against the kernels of 16 to 64 heads per CTA (us, CTA / pair): bf16 cache, 8 x
-// 4096 rows, 16 rows 13.7 / 15.0, 32 18.6 / 15.8, 48 26.4 / 16.4, 64 23.7 / 17.0; 4 x
-// 65536, 16 rows 58 / 61, 32 70 / 63, 64 80 / 65; E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48
-// 19.5 / 18.1; 4 x 65536, 32 rows 60 / 53, 48 91 / 53.
+// Measured against the kernels of 16 and 32 heads per CTA (us, CTA / pair): bf16 cache, 8 x
+// 4096 rows, 16 query rows 13.7 / 15.0, 32 17.7 / 15.7, 48 26.3 / 16.2, 64 24.5 / 17.1; 4 x
+// 65536, 16 rows 58 / 61, 32 68 / 65, 64 105 / 68; 64 sequences of 512 to 8192, 32 rows
+// 99 / 76, 128 268 / 89.  E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48 22.9 / 17.1; 4 x 65536,
+// 32 rows 61 / 53, 48 88 / 56.
 constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
 // Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
 // 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
 // full, 256 x 2048 75 / 73, 64 x 4096 40.8 / 40.9, 32 x 4096 (6.7) 24.6 / 25.4, 16 x 4096
 // (3.4) 16.1 / 18.6.
-constexpr int kShareMinTiles = 4;
+constexpr int kShareMinTiles = 5;
 // The same for SM pairs: tiles per pair (bf16, E4M3), and sequences per pair up to which
 // (more are balanced as they are, with one chunk each and no combine).  64 heads, chunks /
 // shares: bf16, 512 to 8192 rows, 16 sequences (13.5 tiles) 34.1 / 29.1, 76 114 / 93, 152
@@ -2244,13 +2245,14 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
       // streams 100 rows in).
       double join = opts.paged && s_eff > 1 ? 100.0 : 0.0;
       double cost = double(waves) * (rows + 96) + 4.0 * s_eff + join;
-      // SM pairs (75 rows per us): a CTA's start and end cost 4 us, the combine 6 us, and
-      // each chunk 5.5 us per 4096 heads x tokens (a partial of 2 KB written and read;
-      // measured on 32 x 16384 rows x 128 heads: 207, 142, 183, 154 and 157 us at 1, 2, 3,
-      // 4 and 7 chunks, on 32 x 2048 rows 30.3, 39.6 and 50.9 at 1, 2 and 4).
+      // SM pairs (75 rows per us): a CTA's start and end cost 4 us, the combine 1.6 us, and
+      // each chunk 4.5 us per 4096 heads x tokens (a partial of 2 KB written and read;
+      // measured, 128 heads: 32 x 16384 rows 208, 128, 171, 141 and 154 us at 1, 2, 3, 4 and
+      // 7 chunks, 32 x 2048 30.1, 27.1, 38.9 and 37.7 at 1 to 4, 16 x 2048 29.6, 23.3, 20.5
+      // and 18.4, 1 x 8192 21.2, 15.5, 15.4, 14.1 and 17.5 at 8, 16, 22, 32 and 64).
       if (pairs)
         cost = double(waves) * (rows + 300) +
-               (s_eff > 1 ? 450.0 + 0.1 * s_eff * d->batch * d->heads : 0.0);
+               (s_eff > 1 ? 120.0 + 0.08 * s_eff * d->batch * d->heads : 0.0);
       if (cost < best) {
         best = cost;
         np_chunk = chunk;
