@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int groups = p.H / kHeadGroup;
   const int g = kShare ? blockIdx.x % groups : blockIdx.x, h0 = g * kHeadGroup;
   TileItem first{0, 0, 0, 0, 0};   // the CTA's first item (none: T = 0)
-  int T = 0, row_end = 0;  // tiles of the CTA; row at which an item that ends inside a sequence ends
+  int T = 0, row_end = 0;  // tiles of the CTA; the row behind its chunk
   TileShare share;
   if (!kShare) {
     const int j = blockIdx.y, b = blockIdx.z;
@@ -332,8 +332,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     // One barrier a lane: the first copies wait for this.
     static_assert(kNumBars <= 32, "a barrier per lane");
-    if (lane < kNumBars && (kShare || lane != B_QREADY))
-      mbar_init(bar(lane), lane >= B_SFREE && lane < B_ODONE ? 8 : 1);   // S read, P written: 8 warps
+    if (lane < kNumBars && (kShare || lane != B_QREADY)) {
+      // S read and P written: eight warps
+      mbar_init(bar(lane), lane >= B_SFREE && lane < B_ODONE ? 8 : 1);
+    }
     if (lane == 0) *abort_flag = 0;
     fence_mbarrier_init();
     if (lane == 0) prefetch_tmap(&tmap);

@@ -578,6 +578,15 @@ mla_status mla_cache_append_paged(const mla_dims* dims, const mla_paging* paging
  * workspace >= mla_paged_workspace_bytes(...) bytes.  A needed page outside the
  * pool sets MLA_DEV_PAGE_OUT_OF_RANGE and its rows count as zeros.
  * mla_paged_num_splits gives the chunk count used (0: invalid arguments).
+ *
+ * num_splits = 0 lets the library cut the rows.  For bf16 queries of 32 or more
+ * rows and for FP8 caches, batches with enough rows are then cut into equal runs
+ * of 128-row tiles over all sequences, by the lengths that the kernels read: a
+ * ragged batch keeps every SM busy to the end (mla_paged_num_splits gives the
+ * most pieces that the workspace has room for).  Where a sequence is cut then
+ * depends on the other lengths, and with it its last bits; a call repeated gives
+ * the same bits.  num_splits > 0 cuts every sequence into chunks of the same rows,
+ * whatever the others' lengths.
  */
 int32_t mla_paged_num_splits(const mla_dims* dims, const mla_paging* paging, int32_t io_dtype,
                              int32_t q_len, int32_t requested);
@@ -600,9 +609,10 @@ mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
  *   sum[d]   = sum over rows of round(x[d] 2^(20-e))      (integers, exact)
  *   codes[d] = round(sum[d] * (127 * (1 / max |sum|)))    (int8)
  *   scale    = max |sum| * (1/127) / n * 2^(e-20)         (fp32)
- * (each fp32 operation rounded to nearest), so codes[d] * scale is the mean row to 8 bits.  Integer sums make the index
- * independent of the order of summation.  A page of zeros, of magnitudes below
- * 1e-30, or with an infinity gets zeros; NaN values give unspecified codes.
+ * (each fp32 operation rounded to nearest), so codes[d] * scale is the mean row
+ * to 8 bits.  Integer sums make the index independent of the order of summation.
+ * A page of zeros, of magnitudes below 1e-30, or with an infinity gets zeros; NaN
+ * values give unspecified codes.
  *
  * codes [num_pages, d_c + d_rope] int8 and scales [num_pages] fp32 by page
  * number (out: only touched pages change).  first_rows, lengths [B] int32;
