@@ -334,8 +334,9 @@ __device__ __forceinline__ float reduce8_heads(float v[8], int lane) {
 //   warps W+4, W+5: PV MMAs, each over two of the four O^T blocks:
 //               O^T[512 x N] += C^T[512 x 128] . P^T[128 x N]  (M=128 blocks,
 //               each in two 64-row halves; C read MN-major from a ring-B pair)
-//             The four issuing warps run warp-uniform code with one elected thread
-//             (see umma_bf16_elected).
+//             A thread issues one tcgen05.mma per ~100 cycles whatever the
+//             shape (N = 32 or 64), so four issuing threads keep the tensor
+//             pipe fed.
 //   warps 0..W-1: one tile row per thread, a group of four warps per 8 heads
 //             (heads 8i..8i+7 in warps 4i..4i+3): softmax across the rows, P^T
 //             (hi | lo bf16) to shared memory; O^T accumulates in TMEM against a
@@ -412,8 +413,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   // Rows of the cache's [sequences * s_max, 576] view (index checks).
   const long long cache_rows = kPaged ? 0 : static_cast<long long>(p.B / p.q_len) * p.s_max;
   (void)cache_rows;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) { return bars + 8 * i; };
 
   // The cache stream starts before anything else: ring A's producer sets up its
@@ -544,10 +544,8 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     return paged_row(p, cache_seq(p, v), r + lane * rows, lane * rows < kTileRows ? len : 0);
   };
   auto paged_box = [&](uint32_t dst, int column, int row, uint32_t full) {
-#pragma unroll 1
-    for (int i = 0; i < pieces; ++i)
-      tma_load_2d_elected(dst + i * box_rows * 128, &tmap, column,
-                          __shfl_sync(0xffffffffu, row, i), full, keep);
+    if (lane < pieces)
+      tma_load_2d(dst + lane * box_rows * 128, &tmap, column, row, full, keep);
   };
   int row_a = 0;   // this lane's piece of the tile ring A is at
   auto paged_fills = [&](int from, int to) {
@@ -563,7 +561,6 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
       for (int pos = from; pos < to; ++pos) mbar_arrive_expect_tx(bar(BAR_FULLA + pos), kBoxBytes);
     }
     __syncwarp();
-#pragma unroll 1
     for (int pos = from; pos < to; ++pos)
       paged_box(sbase + kOffA + pos * kBoxBytes, 64 * pos, row_a, bar(BAR_FULLA + pos));
   };
@@ -791,14 +788,16 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
         seek(c, t + 1);
         row_next = piece_row(items[c.i].qv, row_of(c, t + 1), item_end(items[c.i]), box_rows);
       }
-#pragma unroll 1
       for (int k = 0; k < 9 && go; ++k) {
         const int pos = 9 * t + k, sl = pos % kSlotsA, use = pos / kSlotsA;
         if (pos < kSlotsA) continue;   // issued before the CTA-wide barrier
-        go = __all_sync(0xffffffffu, wait_or_abort(bar(BAR_EMPTYA + sl), (use - 1) & 1,
-                                                   abort_flag, wait_ns));
+        if (lane == 0) {
+          go = !*abort_flag &&
+               wait_or_abort(bar(BAR_EMPTYA + sl), (use - 1) & 1, abort_flag, wait_ns);
+          if (go) mbar_arrive_expect_tx(bar(BAR_FULLA + sl), kBoxBytes);
+        }
+        go = __shfl_sync(0xffffffffu, go, 0);
         if (!go) break;
-        expect_tx_elected(bar(BAR_FULLA + sl), kBoxBytes);
         paged_box(sbase + kOffA + sl * kBoxBytes, 64 * box_at(t, k), row_a, bar(BAR_FULLA + sl));
         issued = pos + 1;
       }
@@ -818,27 +817,28 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     uint32_t armed_x = 0;
     Cursor c{0, items[0].tiles};
     bool go = true;
+    // Lane 0 waits; the answer goes to the whole warp.
     auto ready = [&](bool wait, uint32_t b, uint32_t parity) {
-      go = __all_sync(0xffffffffu, !*abort_flag && (!wait || wait_or_abort(b, parity, abort_flag,
-                                                                          wait_ns)));
+      int ok = 1;
+      if (lane == 0) ok = !*abort_flag && (!wait || wait_or_abort(b, parity, abort_flag, wait_ns));
+      go = __shfl_sync(0xffffffffu, ok, 0) != 0;
       return go;
+    };
+    auto arm = [&](uint32_t b, uint32_t bytes) {
+      if (lane == 0) mbar_arrive_expect_tx(b, bytes);
+      __syncwarp();
     };
     // 128 rows of latent box k of the tile whose pieces start at `row`.
     auto whole_box = [&](uint32_t dst, int k, int row, uint32_t full) {
-#pragma unroll 1
-      for (int i = 0; i < np; ++i)
-        tma_load_2d_elected(dst + i * brows * 128, &tmap_half, 64 * k,
-                            __shfl_sync(0xffffffffu, row, i), full, stream);
+      if (lane < np) tma_load_2d(dst + lane * brows * 128, &tmap_half, 64 * k, row, full, stream);
     };
     // Row half kh of latent boxes 2 mb and 2 mb + 1: np / 2 pieces of each.
     auto half_pair = [&](uint32_t dst, int mb, int kh, int row, uint32_t full) {
-#pragma unroll 1
-      for (int i = 0; i < np / 2; ++i) {
-        const int r = __shfl_sync(0xffffffffu, row, kh * (np / 2) + i);
-        tma_load_2d_elected(dst + i * brows * 128, &tmap_half, 128 * mb, r, full, stream);
-        tma_load_2d_elected(dst + kHalfBox + i * brows * 128, &tmap_half, 128 * mb + 64, r, full,
-                            stream);
-      }
+      const int i = lane & (np / 2 - 1), h = lane / (np / 2);
+      const int r = __shfl_sync(0xffffffffu, row, kh * (np / 2) + i);
+      if (lane < np)
+        tma_load_2d(dst + h * kHalfBox + i * brows * 128, &tmap_half, 64 * (2 * mb + h), r, full,
+                    stream);
     };
     int row_b = piece_row(items[0].qv, items[0].row0, item_end(items[0]), brows);
     for (int t = 0; t < T && go; ++t) {
@@ -856,28 +856,27 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
             if (T >= 2 && !ready(true, bar(BAR_PVPREV), 0)) break;
             second = true;
           }
-          expect_tx_elected(bar(BAR_FULLX + k), kBoxBytes);
+          arm(bar(BAR_FULLX + k), kBoxBytes);
           whole_box(sbase + tail_box_off(k), k, row_b, bar(BAR_FULLX + k));
           armed_x |= 1u << k;
         }
         break;
       }
       bool lasta = false;
-#pragma unroll 1
       for (int u = 0; u < 8 && go; ++u) {
         const int mb = u & 3, kh = u >> 2;
         if (borrowed(t, u)) {
           const int x = borrow_x(u);
           if (!ready(!lasta, bar(BAR_LASTA), 0)) break;
           lasta = true;
-          expect_tx_elected(bar(BAR_FULLX + x), 2 * kHalfBox);
+          arm(bar(BAR_FULLX + x), 2 * kHalfBox);
           half_pair(sbase + borrow_off(x), mb, kh, row_b, bar(BAR_FULLX + x));
           armed_x |= 1u << x;
           continue;
         }
         const int pos = 8 * t + u, sl = pos % kSlotsB, use = pos / kSlotsB;
         if (!ready(use > 0, bar(BAR_EMPTYB + sl), (use - 1) & 1)) break;
-        expect_tx_elected(bar(BAR_FULLB + sl), 2 * kHalfBox);
+        arm(bar(BAR_FULLB + sl), 2 * kHalfBox);
         half_pair(sbase + kOffB + 2 * sl * kHalfBox, mb, kh, row_b, bar(BAR_FULLB + sl));
         issued = pos + 1;
       }
@@ -997,11 +996,6 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     named_bar_sync(2, kSoftThreads + 64);
   }
 
-  // The MMA issuers run as whole warps, converged at every MMA and commit: a wait's answer
-  // is the same for all lanes.
-  auto warp_ok = [&](uint32_t b, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(b, parity, abort_flag, wait_ns)) != 0;
-  };
   // One PV unit: O^T block u % 4 (of the O^T buffer at column ocol) += C^T (pair
   // u of tile t) . P^T (row half u / 4); four MMAs; `fresh`: the tile is its
   // item's first (the block starts from zero); `zmid`: a tile before the last
@@ -1013,11 +1007,11 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
       // Block mb's two 64-column boxes 2mb, 2mb + 1 (128 rows each, kBoxBytes
       // apart): still in ring A or read again into the ring-B space.
       const int k0 = 2 * mb;
-      if (zero_last && (!warp_ok(bar(BAR_ZEROX + k0), 0) ||
-                        !warp_ok(bar(BAR_ZEROX + k0 + 1), 0)))
+      if (zero_last && (!wait_or_abort(bar(BAR_ZEROX + k0), 0, abort_flag, wait_ns) ||
+                        !wait_or_abort(bar(BAR_ZEROX + k0 + 1), 0, abort_flag, wait_ns)))
         return false;
-      if (!tail_res(mb) && (!warp_ok(bar(BAR_FULLX + k0), 0) ||
-                     !warp_ok(bar(BAR_FULLX + k0 + 1), 0)))
+      if (!tail_res(mb) && (!wait_or_abort(bar(BAR_FULLX + k0), 0, abort_flag, wait_ns) ||
+                     !wait_or_abort(bar(BAR_FULLX + k0 + 1), 0, abort_flag, wait_ns)))
         return false;
       tc_fence_after();
       const uint64_t c = umma_desc_sw128(sbase + kOffA, kBoxBytes, 1024) +
@@ -1026,7 +1020,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
                           static_cast<uint64_t>(((t % kPBufs) * kPBytes + kh * kPSub) >> 4);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        umma_bf16_elected(tmem + ocol + kQN * mb, c + ((ks * 2048) >> 4), pd + ((ks * 32) >> 4), idesc_o,
+        umma_bf16(tmem + ocol + kQN * mb, c + ((ks * 2048) >> 4), pd + ((ks * 32) >> 4), idesc_o,
                   (!fresh || kh > 0 || ks > 0) ? 1u : 0u);
       return true;
     }
@@ -1034,12 +1028,13 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     const bool bw = borrowed(t, u);
     const int x = bw ? borrow_x(u) : 0;
     if (t == T - 1 && zero_last &&
-        !warp_ok(bw ? bar(BAR_ZEROX + x) : bar(BAR_ZEROB + sl), 0))
+        !wait_or_abort(bw ? bar(BAR_ZEROX + x) : bar(BAR_ZEROB + sl), 0, abort_flag, wait_ns))
       return false;
     // A zeroed tile before the last zeroes each slot twice (units u and u + 4),
     // so the zeroing of unit u completes the phase of parity u / 4.
-    if (zmid && !warp_ok(bar(BAR_ZEROB + sl), kh)) return false;
-    if (!warp_ok(bw ? bar(BAR_FULLX + x) : bar(BAR_FULLB + sl), bw ? 0 : (pos / kSlotsB) & 1))
+    if (zmid && !wait_or_abort(bar(BAR_ZEROB + sl), kh, abort_flag, wait_ns)) return false;
+    if (!wait_or_abort(bw ? bar(BAR_FULLX + x) : bar(BAR_FULLB + sl), bw ? 0 : (pos / kSlotsB) & 1,
+                       abort_flag, wait_ns))
       return false;
     tc_fence_after();
     // MN-major pair: two 64-column boxes kHalfBox apart; the descriptor's
@@ -1050,24 +1045,26 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
                         static_cast<uint64_t>(((t % kPBufs) * kPBytes + kh * kPSub) >> 4);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
-      umma_bf16_elected(tmem + ocol + kQN * mb, c + ((ks * 2048) >> 4), pd + ((ks * 32) >> 4), idesc_o,
+      umma_bf16(tmem + ocol + kQN * mb, c + ((ks * 2048) >> 4), pd + ((ks * 32) >> 4), idesc_o,
                 (!fresh || kh > 0 || ks > 0) ? 1u : 0u);
-    if (!bw) umma_commit_elected(bar(BAR_EMPTYB + sl));
+    if (!bw) umma_commit(bar(BAR_EMPTYB + sl));
     return true;
   };
   // Before item i's first PV: the epilogue of item i - kOBufs has read the O^T
   // buffer item i accumulates into.
   auto wait_drain = [&](int i) {
-    return i < L::kOBufs || warp_ok(bar(BAR_ODRAIN + i % L::kOBufs),
-                                          ((i - L::kOBufs) / L::kOBufs) & 1);
+    return i < L::kOBufs || wait_or_abort(bar(BAR_ODRAIN + i % L::kOBufs),
+                                          ((i - L::kOBufs) / L::kOBufs) & 1, abort_flag, wait_ns);
   };
 
   if (warp == kWarpS0 || warp == kWarpS1) {
     // ------------------------------------------------------------ score MMA issuers
     // Issuer i takes the boxes whose stream position 9t + k has parity i, so it
     // owns ring-A slots i, i + 2, i + 4 and meets each slot's phases in order;
-    // it accumulates them into its own S_i and the softmax adds S_0 + S_1.
-    {
+    // it accumulates them into its own S_i and the softmax adds S_0 + S_1.  One
+    // thread issues a tcgen05.mma only every ~100 cycles, so the work is spread
+    // over threads.
+    if (lane == 0) {
       const int i = warp == kWarpS0 ? 0 : 1;
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kQN, 0, 0);
       // Base descriptors; a K step only moves the 14-bit start-address field,
@@ -1082,16 +1079,16 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
         if (kMulti && __builtin_expect(c.i > 0 && t == items[c.i].t0 && new_query(c.i), 0)) {
           // The previous item's score MMAs release the query area; the softmax
           // warps fill it with this item's query.
-          umma_commit_elected(bar(BAR_QFREE));
-          if (!warp_ok(bar(BAR_QREADY), qk & 1)) break;
+          umma_commit(bar(BAR_QFREE));
+          if (!wait_or_abort(bar(BAR_QREADY), qk & 1, abort_flag, wait_ns)) break;
           ++qk;
         }
         const int sb = t & 1;
-        if (t >= 2 && !warp_ok(bar(BAR_SFREE + sb), ((t - 2) >> 1) & 1)) break;
+        if (t >= 2 && !wait_or_abort(bar(BAR_SFREE + sb), ((t - 2) >> 1) & 1, abort_flag, wait_ns)) break;
         bool ok = true, first = true;
         for (int k = (9 * t + i) & 1; k < 9; k += 2) {
           const int pos = 9 * t + k, sl = pos % kSlotsA;
-          if (!warp_ok(bar(BAR_FULLA + sl), (pos / kSlotsA) & 1)) {
+          if (!wait_or_abort(bar(BAR_FULLA + sl), (pos / kSlotsA) & 1, abort_flag, wait_ns)) {
             ok = false;
             break;
           }
@@ -1100,46 +1097,46 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
           const uint64_t q = dQ0 + static_cast<uint64_t>((box_at(t, k) * kQBoxBytes) >> 4);
 #pragma unroll
           for (int s4 = 0; s4 < 4; ++s4)
-            umma_bf16_elected(dS + kQN * sb, a + ((s4 * 32) >> 4), q + ((s4 * 32) >> 4), idesc_s,
+            umma_bf16(dS + kQN * sb, a + ((s4 * 32) >> 4), q + ((s4 * 32) >> 4), idesc_s,
                       (!first || s4 > 0) ? 1u : 0u);
-          umma_commit_elected(bar(BAR_EMPTYA + sl));
+          umma_commit(bar(BAR_EMPTYA + sl));
           first = false;
         }
         if (!ok) break;
-        umma_commit_elected(bar(BAR_SFULL + sb));
-        if (lane == 0) s_issued[i] = t + 1;
+        umma_commit(bar(BAR_SFULL + sb));
+        s_issued[i] = t + 1;
       }
-      umma_commit_elected(bar(BAR_LASTA));   // ring A and the query area are free for the last pairs
+      umma_commit(bar(BAR_LASTA));   // ring A and the query area are free for the last pairs
       // The last tile's PV is the tail of the kernel: these two threads take O^T
       // blocks 2 and 3 of it (after the PV issuers have finished tile T-2, the
       // previous writers of those blocks).
       {
         const int t = T - 1;
-        bool ok = !__any_sync(0xffffffffu, *abort_flag);
-        if (ok && T >= 2 && !warp_ok(bar(BAR_PVPREV), 0)) ok = false;
+        bool ok = !*abort_flag;
+        if (ok && T >= 2 && !wait_or_abort(bar(BAR_PVPREV), 0, abort_flag, wait_ns)) ok = false;
         if (ok && fin_first && !wait_drain(fin_item)) ok = false;
-        if (ok && !warp_ok(bar(BAR_PFULL + (t & 1)), (t >> 1) & 1)) ok = false;
+        if (ok && !wait_or_abort(bar(BAR_PFULL + (t & 1)), (t >> 1) & 1, abort_flag, wait_ns)) ok = false;
         if (ok && pv_unit(t, 2 + i, fin_first, obuf_col(fin_item), false) &&
-            (!kHalfP || warp_ok(bar(BAR_PFULL1 + (t & 1)), (t >> 1) & 1)))
+            (!kHalfP || wait_or_abort(bar(BAR_PFULL1 + (t & 1)), (t >> 1) & 1, abort_flag, wait_ns)))
           pv_unit(t, 6 + i, fin_first, obuf_col(fin_item), false);
-        umma_commit_elected(bar(BAR_ODONE2));
+        umma_commit(bar(BAR_ODONE2));
       }
       // Every MMA this thread issued has finished before TMEM is released.
-      umma_commit_elected(bar(BAR_DONE));
+      umma_commit(bar(BAR_DONE));
       mbar_wait_bounded(bar(BAR_DONE), 0);
     }
   } else if (warp == kWarpPV0 || warp == kWarpPV1) {
     // ------------------------------------------------------------ PV MMA issuers
     // Issuer i takes O^T blocks mb = i and i + 2 (ring-B slots i and i + 2); of
     // the last tile only block i (the score issuers take blocks 2 and 3).
-    {
+    if (lane == 0) {
       const int i = warp - kWarpPV0;
       Cursor c{0, items[0].tiles};
       for (int t = 0; t < T; ++t) {
         seek(c, t);
         const bool fresh = t == items[c.i].t0;
         if (fresh && !wait_drain(c.i)) break;
-        if (!warp_ok(bar(BAR_PFULL + (t & 1)), (t >> 1) & 1)) break;
+        if (!wait_or_abort(bar(BAR_PFULL + (t & 1)), (t >> 1) & 1, abort_flag, wait_ns)) break;
         bool ok = true;
         const int step = t == T - 1 ? 4 : 2;
         const bool zmid = zero_mid(c, t);
@@ -1147,8 +1144,8 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
           if (kHalfP && u >= 4 && u - step < 4) {
             // Rows 0-63 of P are free once this thread's MMAs so far have
             // finished; rows 64-127 are needed from here on.
-            umma_commit_elected(bar(BAR_P0FREE + (t & 1)));
-            if (!warp_ok(bar(BAR_PFULL1 + (t & 1)), (t >> 1) & 1)) {
+            umma_commit(bar(BAR_P0FREE + (t & 1)));
+            if (!wait_or_abort(bar(BAR_PFULL1 + (t & 1)), (t >> 1) & 1, abort_flag, wait_ns)) {
               ok = false;
               break;
             }
@@ -1156,10 +1153,10 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
           ok = pv_unit(t, u, fresh, obuf_col(c.i), zmid);
         }
         if (!ok) break;
-        umma_commit_elected(bar(BAR_ODONE + (t & 1)));
-        if (t == T - 2) umma_commit_elected(bar(BAR_PVPREV));
+        umma_commit(bar(BAR_ODONE + (t & 1)));
+        if (t == T - 2) umma_commit(bar(BAR_PVPREV));
       }
-      umma_commit_elected(bar(BAR_DONE));
+      umma_commit(bar(BAR_DONE));
       mbar_wait_bounded(bar(BAR_DONE), 0);
     }
   } else if (warp < kSoftWarps) {
