@@ -1727,11 +1727,11 @@ __global__ void __launch_bounds__(32 * kF32Warps)
 
 // Merge of the chunk partials of one (sequence, head):
 //   L = log sum_j exp(lse_j),  o_c = sum_j exp(lse_j - L) o_j.
-// grid (H, B, 4), one warp per CTA: thread t of CTA z owns latent columns
-// [128z + 4t, 128z + 4t + 4).  Chunks are taken kCombineChunk at a time with
+// Each thread owns four latent columns.  Partials are taken kGroup at a time with
 // every load of a group in flight at once; a running maximum keeps the weights
 // finite (each thread recomputes the group's weights itself, so there is no
-// shared memory and no barrier).
+// shared memory and no barrier).  Groups of kCombineFew where a row has few
+// partials (39 registers against 119, so more CTAs per SM), else kCombineChunk.
 // o_c is fp32, or bf16 (rounded once, here) where the caller's queries are.
 __device__ __forceinline__ void store_out4(float* dst, float4 v) {
   *reinterpret_cast<float4*>(dst) = v;

@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
   const uint64_t db0 = umma_desc_sw128(sbase + kOffQuery, 16, 1024);
   for (int g = 0; g < p.groups; ++g) {
     if (warp == 0 && __all_sync(0xffffffffu, mbar_wait_bounded(bars, g & 1))) {
-      // The warp issues as one (see umma_bf16_elected; kind::f16 takes fp16 as well); boxes are not unrolled, so that the
-      // loop's code is fetched once.
+      // The warp issues as one (see umma_bf16_elected; kind::f16 takes fp16 as well); boxes
+      // are not unrolled, so that the loop's code is fetched once.
       tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < kBoxes; ++i) {
