@@ -399,7 +399,10 @@ inline int current_device() {
 bool launch_overlap_enabled();
 
 // Launches `kernel` with programmatic stream serialization (see pdl_wait), or
-// as a plain launch when overlap is switched off.
+// as a plain launch when overlap is switched off.  A successor's wait covers this
+// grid alone: for it to be ordered behind the kernels before this one as well, this
+// grid may not end before its own wait has passed.  So a CTA waits on every way out,
+// or is one whose grid has another that does (the first along an axis).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args&&... args) {

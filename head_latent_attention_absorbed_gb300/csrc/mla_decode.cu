@@ -1639,6 +1639,7 @@ __global__ void __launch_bounds__(32 * kF32Warps)
   if (p.late) pdl_wait();
   const int len = clamp_length(p, b, tid == 0 && h == 0 && j == 0);
   const int r0 = j * p.chunk;
+  pdl_wait();   // the queries, and the readers of the workspace and of o_c
   if (r0 >= len) {
     if (p.direct) write_no_rows(p, size_t(b) * p.H + h, 1, tid, 32 * kF32Warps);
     return;

@@ -1,0 +1,89 @@
+"""Paged calls that follow one another without a synchronisation: each gives the bits it
+gives alone, whatever the calls before it still have in flight."""
+import numpy as np
+import pytest
+import torch
+
+from _paged import D_C, D_R
+from test_gpu_paged_attn import BF16, F32, Call, i32
+
+pytestmark = pytest.mark.gpu
+ROUNDS = 12
+
+
+def alone_and_together(calls, chain):
+    """chain(k, round) queues call k and returns its outputs; each is held to what it gave
+    alone."""
+    alone = []
+    for k in range(len(calls)):
+        got = chain(k, ROUNDS)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in got])
+    torch.cuda.synchronize()
+    outs = [[chain(k, r) for k in range(len(calls))] for r in range(ROUNDS)]
+    torch.cuda.synchronize()
+    for row in outs:
+        for got, want in zip(row, alone):
+            assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def absorb_inputs(seed, rows, heads):
+    g = torch.Generator().manual_seed(seed)
+    x = dict(q_nope=torch.randn((rows, heads, 128), generator=g).bfloat16().cuda(),
+             q_rope=torch.randn((rows, heads, D_R), generator=g).bfloat16().cuda(),
+             w_uk=(torch.randn((heads, 128, D_C), generator=g) * 0.02).bfloat16().cuda())
+    return x, i32(np.arange(rows))
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_f32_calls_on_one_workspace(cuda_lib, splits):
+    """fp32 caches, lengths that change from call to call, one chunk and several: partials
+    and results of one call are not overwritten under the combine of another."""
+    calls = [Call(cuda_lib, lengths, 16, "f32", F32, 16, splits=splits, seed=k, s_max=1000,
+                  width=70)
+             for k, lengths in enumerate(([1000, 7, 400, 33], [64, 900, 1, 512], [250] * 4))]
+    for c in calls:
+        c.ws = calls[0].ws
+        c.outs = [(torch.full_like(c.o, 7), torch.full_like(c.lse, 7)) for _ in range(ROUNDS + 1)]
+
+    def chain(k, r):
+        calls[k].o, calls[k].lse = calls[k].outs[r]
+        calls[k].run()
+        return calls[k].outs[r]
+
+    alone_and_together(calls, chain)
+    for c in calls:
+        c.o, c.lse = c.outs[0]
+        c.check()
+    # one output as well: the last call's result stands
+    for _ in range(ROUNDS):
+        for c in calls:
+            c.o, c.lse = calls[0].outs[0]
+            c.run()
+    torch.cuda.synchronize()
+    for got, want in zip(calls[0].outs[0], calls[-1].outs[ROUNDS]):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_f32_call_behind_the_absorb(cuda_lib, splits):
+    """The queries come from mla_absorb_q, which lets its successor start at once."""
+    mla = cuda_lib
+    B, H = 24, 16
+    calls = [Call(mla, np.random.RandomState(k).randint(1, 300, B), 16, "f32", F32, H, splits=splits,
+                  seed=k, s_max=300, width=30) for k in range(3)]
+    d = mla.dims(B, H, 300, mla.MLA_BF16)
+    x = [absorb_inputs(k, B, H) for k in range(3)]
+
+    def chain(k, r):
+        c = calls[k]
+        ins, pos = x[k]
+        c.ws = calls[0].ws
+        c.dev["q_abs"], c.dev["q_pe"] = calls[0].dev["q_abs"], calls[0].dev["q_pe"]
+        c.o, c.lse = torch.full_like(c.o, 7), torch.full_like(c.lse, 7)
+        mla.absorb_q(d, ins["q_nope"], ins["q_rope"], ins["w_uk"], pos, c.dev["q_abs"],
+                     c.dev["q_pe"])
+        c.run()
+        return c.o, c.lse
+
+    alone_and_together(calls, chain)
