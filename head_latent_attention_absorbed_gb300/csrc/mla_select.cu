@@ -145,8 +145,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_score_kernel(const Sele
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
   const int P = token_pages(p, token_rows(p, r, false));
-  pdl_launch_dependents();             // the choice waits for this grid before it reads
-  if (P <= p.top || j0 >= P) return;   // every page is kept, or none of these exists
+  pdl_launch_dependents();        // the choice waits for this grid before it reads
+  if (P <= p.top || j0 >= P) {    // every page is kept, or none of these exists
+    if (j0 == 0) pdl_wait();      // the grid may not end before the queries' codes are made
+    return;
+  }
   if (tid < kScorePages) {
     const int j = j0 + tid;
     int id = -1;

@@ -6,6 +6,7 @@ import torch
 
 from _paged import D_C, D_R
 from test_gpu_paged_attn import BF16, F32, Call, i32
+from test_gpu_sparse import Sparse
 
 pytestmark = pytest.mark.gpu
 ROUNDS = 12
@@ -87,3 +88,73 @@ def test_f32_call_behind_the_absorb(cuda_lib, splits):
         return c.o, c.lse
 
     alone_and_together(calls, chain)
+
+
+SHORT = [("bf16", F32, 16), ("bf16", F32, 64), ("bf16", BF16, 16), ("bf16", BF16, 64),
+         ("fp8", F32, 16), ("fp8", BF16, 32), ("fp8", BF16, 128), ("f32", F32, 4)]
+
+
+def short_sparse(mla, k, dtype, io, heads, long, B=20, page=16, top=6):
+    """A sparse call whose s_max spans 40 pages, over sequences of at most `top` pages
+    (`long`: all but one)."""
+    c = Sparse(mla, [40 * page] * B, page, dtype, io, heads, top, seed=k)
+    c.lengths = np.random.RandomState(k).randint(1, page * top + 1, B)
+    if long:
+        c.lengths[k] = 39 * page + 3
+    c.dev["lengths"].copy_(i32(c.lengths))
+    c.outs = [(torch.full_like(c.o, 7), torch.full_like(c.lse, 7)) for _ in range(ROUNDS + 1)]
+    return c
+
+
+@pytest.mark.parametrize("dtype,io,heads", SHORT)
+@pytest.mark.parametrize("long", [False, True])
+def test_sparse_calls_on_short_sequences(cuda_lib, dtype, io, heads, long):
+    """No sequence holds more pages than are kept (or one alone does), so that the score
+    kernel has nothing to do: calls with other queries and lengths on one workspace and one
+    selection."""
+    calls = [short_sparse(cuda_lib, k, dtype, io, heads, long) for k in range(3)]
+    for c in calls:
+        c.ws, c.sel, c.sel_len = calls[0].ws, calls[0].sel, calls[0].sel_len
+
+    def chain(k, r):
+        c = calls[k]
+        c.o, c.lse = c.outs[r]
+        c.run()
+        return c.outs[r]
+
+    alone_and_together(calls, chain)
+    for c in calls:
+        c.o, c.lse = c.outs[0]
+        c.run().check()
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 16), ("bf16", 64), ("fp8", 16)])
+@pytest.mark.parametrize("long", [False, True])
+def test_absorb_sparse_out_proj(cuda_lib, dtype, heads, long):
+    """The library's own chain: queries of mla_absorb_q, which lets its successor start at
+    once, a sparse call on short sequences, and mla_out_proj."""
+    mla, B = cuda_lib, 40
+    calls = [short_sparse(mla, k, dtype, F32, heads, long, B) for k in range(3)]
+    x = [absorb_inputs(k, B, heads) for k in range(3)]
+    w_uv = (torch.randn((heads, 128, D_C), generator=torch.Generator().manual_seed(9)) * 0.04
+            ).bfloat16().cuda()
+    outs = [[torch.full((B, heads, 128), 7.0, device="cuda") for _ in range(ROUNDS + 1)]
+            for _ in calls]
+    one = calls[0]
+
+    def chain(k, r):
+        c, (ins, pos) = calls[k], x[k]
+        c.ws, c.sel, c.sel_len, c.o, c.lse = one.ws, one.sel, one.sel_len, one.o, one.lse
+        c.dev["q_abs"], c.dev["q_pe"] = one.dev["q_abs"], one.dev["q_pe"]
+        mla.absorb_q(c.d, ins["q_nope"], ins["q_rope"], ins["w_uk"], pos, c.dev["q_abs"],
+                     c.dev["q_pe"])
+        c.run()
+        mla.out_proj(c.d, c.o, w_uv, outs[k][r])
+        return (outs[k][r],)
+
+    alone_and_together(calls, chain)
+    for k, c in enumerate(calls):
+        chain(k, 0)
+        torch.cuda.synchronize()
+        c.q_abs, c.q_pe = c.dev["q_abs"].cpu(), c.dev["q_pe"].cpu()
+        c.check()

@@ -28,7 +28,7 @@ def test_the_reading_finds_missing_waits():
     assert found == ["a_kernel", "b_kernel"]
 
 
-@pytest.mark.parametrize("kernel", ["split_f32_paged_kernel"])
+@pytest.mark.parametrize("kernel", ["split_f32_paged_kernel", "page_score_kernel"])
 def test_every_way_out_waits(kernel):
     assert kernel in _pdl.overlapped_kernels(SOURCE)
     assert _pdl.unwaited_exits(kernel, SOURCE) == []
