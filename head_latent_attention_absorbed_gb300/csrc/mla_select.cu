@@ -283,6 +283,8 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
   __shared__ uint32_t keys[kPickHold];
   __shared__ int hist[256], s_found[3], s_part[32];
+  __shared__ uint32_t s_differ[32];   // its own: with all keys equal no barrier parts its
+                                      // readers from the first writers of s_part
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = token_rows(p, r, tid == 0);
   const int P = token_pages(p, n);
@@ -311,9 +313,9 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
     for (int j = lo + tid; j < hi; j += kPickThreads) differ |= key(j) ^ key0;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) differ |= __shfl_xor_sync(0xffffffffu, differ, off);
-    if (lane == 0) s_part[warp] = static_cast<int>(differ);
+    if (lane == 0) s_differ[warp] = differ;
     __syncthreads();
-    differ = static_cast<uint32_t>(s_part[lane]);
+    differ = s_differ[lane];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) differ |= __shfl_xor_sync(0xffffffffu, differ, off);
     const int same = __clz(differ);   // leading bits that all keys share

@@ -282,3 +282,29 @@ def test_serving_loop(cuda_lib):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     assert int(nf.item()) == pages and sorted(free.cpu().tolist()) == list(range(pages))
+
+
+@pytest.mark.parametrize("pages,top", [(8, 7), (33, 3), (1025, 64), (9001, 700)])
+def test_all_scores_equal_again_and_again(cuda_lib, pages, top):
+    """Zero queries, as in a warm-up: every score ties in every token of many, and the
+    lowest positions are kept each time, without a synchronisation in between."""
+    mla, R = cuda_lib, 40
+    s = Sparse(mla, [16 * pages], 16, "bf16", BF16, 16, top, seed=pages)
+    s.d = mla.dims(R, 16, 16 * pages, mla.MLA_BF16)
+    table = s.dev["table"].expand(R, -1).contiguous()
+    q_abs = torch.zeros((R, 16, D_C), dtype=BF16, device="cuda")
+    q_pe = torch.zeros((R, 16, 64), dtype=BF16, device="cuda")
+    lengths = torch.full((R,), 16 * pages, dtype=torch.int32, device="cuda")
+    ws = torch.empty(mla.select_workspace_bytes(s.d, s.pg), dtype=torch.uint8, device="cuda")
+    want = table[0].cpu()[list(range(top - 1)) + [pages - 1]].tolist()
+    sels = [torch.full((R, top), 77, dtype=torch.int32, device="cuda") for _ in range(25)]
+    lens = torch.full((R,), 77, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for sel in sels:
+        mla.select_pages(s.d, s.pg, q_abs, q_pe, table, lengths, s.codes, s.scales, sel, lens, ws,
+                         dev_status=s.status)
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    for sel in sels:
+        assert sel.cpu().tolist() == [want] * R
+    assert lens.cpu().tolist() == [16 * top] * R

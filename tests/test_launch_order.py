@@ -1,5 +1,7 @@
 """Kernels that start before their predecessor has finished wait for it on every way
 out (read out of the sources: see _pdl)."""
+import re
+
 import pytest
 
 import _pdl
@@ -32,3 +34,28 @@ def test_the_reading_finds_missing_waits():
 def test_every_way_out_waits(kernel):
     assert kernel in _pdl.overlapped_kernels(SOURCE)
     assert _pdl.unwaited_exits(kernel, SOURCE) == []
+
+
+def rewritten_without_barrier(kernel, read, text):
+    """Whether the shared array that the statement `read` (a pattern with the array's name as
+    its group) reads may be written again before every thread has read it: loops may run no
+    time, so that barriers inside them count for nothing."""
+    body = _pdl.body_of(kernel, text)
+    m = re.search(read, body)
+    rest = body[m.end():]
+    while loop := re.search(r"\bwhile\s*\(", rest):
+        c = _pdl.closing(rest, loop.end() - 1)
+        rest = rest[:loop.start()] + rest[_pdl.statement(rest, c)[2]:]
+    write = re.search(rf"\b{m.group(1)}\[[^\]]*\]\s*=(?!=)", rest)
+    return bool(write) and "__syncthreads()" not in rest[:write.start()]
+
+
+def test_the_choice_keeps_its_shared_words_apart():
+    """With all scores equal, nothing but straight code lies between the read of the warps'
+    differing bits and the counts of the ordered pass."""
+    bad = "__global__ void x_kernel() { n = s[lane]; while (n) { __syncthreads(); } s[warp] = 1; }"
+    assert rewritten_without_barrier("x_kernel", r"n = (\w+)\[lane\]", bad)
+    good = bad.replace("} s[warp]", "} __syncthreads(); s[warp]")
+    assert not rewritten_without_barrier("x_kernel", r"n = (\w+)\[lane\]", good)
+    read = r"differ = (?:static_cast<uint32_t>\()?(\w+)\[lane\]"
+    assert not rewritten_without_barrier("page_pick_kernel", read, SOURCE)
