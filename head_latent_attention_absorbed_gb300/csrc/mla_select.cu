@@ -293,7 +293,12 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
   if (p.early) pdl_launch_dependents();
   pdl_wait();   // the scores; and the readers of the last choice are done
   if (P <= p.top) {
-    for (int j = tid; j < p.top; j += kPickThreads) out[j] = j < P ? row[j] : -1;
+    for (int j = tid; j < p.top; j += kPickThreads) {
+      const int id = j < P ? row[j] : -1;   // of a token that no score kernel has looked at
+      if (j < P && static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages))
+        report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+      out[j] = id;
+    }
     if (tid == 0) p.sel_lengths[r] = n;
     return;
   }

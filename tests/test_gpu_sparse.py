@@ -308,3 +308,27 @@ def test_all_scores_equal_again_and_again(cuda_lib, pages, top):
     for sel in sels:
         assert sel.cpu().tolist() == [want] * R
     assert lens.cpu().tolist() == [16 * top] * R
+
+
+@pytest.mark.parametrize("s_max", [16 * 4, 16 * 40])
+@pytest.mark.parametrize("bad", [-1, 60, 1 << 30, -(1 << 31)])
+def test_select_reports_pages_it_keeps_unscored(cuda_lib, s_max, bad):
+    """A token that keeps all its pages: a number that names no page is reported there too,
+    whether other tokens are scored or none can be."""
+    mla = cuda_lib
+    s = Sparse(mla, [60, 40, 17], 16, "bf16", BF16, 16, 4, seed=12)
+    assert s.pages <= 60
+    table = torch.full((3, 40), -1, dtype=torch.int32, device="cuda")
+    table[:, :4] = s.dev["table"][:, :4]
+    s.dev["table"], s.pg = table, mla.paging(16, s.pages, 40)
+    s.d = mla.dims(3, 16, s_max, mla.MLA_BF16)
+    s.ws = torch.empty(mla.select_workspace_bytes(s.d, s.pg), dtype=torch.uint8, device="cuda")
+    s.select()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0        # entries past a token's pages may hold anything
+    table[1, 2] = bad
+    s.select()
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == mla.MLA_DEV_PAGE_OUT_OF_RANGE
+    assert s.sel[1].cpu().tolist() == [int(table[1, 0]), int(table[1, 1]), bad, -1]
+    assert s.sel_len.cpu().tolist() == [60, 40, 17]
