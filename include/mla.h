@@ -458,12 +458,12 @@ mla_status mla_decode_step_multi(const mla_dims* dims, int32_t q_len, const void
  * there.  Two sequences may share pages (a common prefix) in every call that
  * only reads them.
  *
- * The paged calls read block_table and lengths (and the cache) before they wait
- * for their predecessor on the stream, as the dense calls read lengths: a
- * kernel of the caller that allows early launch must not write those.  No call
- * of this section allows its successor to start early before it has finished
- * writing, except the attention calls, which write only their outputs and
- * workspace.
+ * The paged calls read block_table, lengths, the cache and, in the calls that select
+ * pages, codes and scales before they wait for their predecessor on the stream, as the
+ * dense calls read lengths and the cache: a kernel of the caller that allows early launch
+ * must not write those.  No call of this section allows its successor to start early
+ * before it has finished writing, except the attention calls, which write only their
+ * outputs and workspace.
  */
 typedef struct mla_paging {
   int32_t page_size;      /* rows per page: 16, 32, 64, 128 or 256 */

@@ -1,5 +1,6 @@
 """Kernels that start before their predecessor has finished wait for it on every way
 out (read out of the sources: see _pdl)."""
+import os
 import re
 
 import pytest
@@ -59,3 +60,20 @@ def test_the_choice_keeps_its_shared_words_apart():
     assert not rewritten_without_barrier("x_kernel", r"n = (\w+)\[lane\]", good)
     read = r"differ = (?:static_cast<uint32_t>\()?(\w+)\[lane\]"
     assert not rewritten_without_barrier("page_pick_kernel", read, SOURCE)
+
+
+def test_the_header_names_what_is_read_early():
+    """The selection's kernels: inputs of the caller that stand before the wait of every CTA
+    that goes on are in the header's list of what is read early."""
+    header = " ".join(open(os.path.join(_pdl.ROOT, "include", "mla.h")).read().split("\n * "))
+    listed = re.search(r"The paged calls read (.*?) before they wait", header).group(1)
+    inputs = dict(q_abs="q_abs", q_pe="q_pe", table="block_table", lengths="lengths",
+                  codes="codes", scales="scales")
+    helpers = dict(lengths=r"token_rows\(p,")            # reads p.lengths
+    for kernel in ("select_query_kernel", "page_score_kernel", "page_pick_kernel"):
+        body = _pdl.body_of(kernel, SOURCE)
+        early = re.split(r"\n  pdl_wait\(\);", body)[0]    # the kernel's own wait
+        assert early != body
+        for field, name in inputs.items():
+            if re.search(rf"\bp\.{field}\b", early) or re.search(helpers.get(field, "$^"), early):
+                assert name in listed, f"{kernel} reads {name} before its wait"
