@@ -1799,6 +1799,7 @@ __global__ void __launch_bounds__(kThreads)
     combine_kernel(const SplitParams p, Out* o_c, float* lse_out) {
   const int h = blockIdx.x, b = blockIdx.y;
   const int tid = blockIdx.z * kThreads + threadIdx.x;   // float4 column of the 512
+  if (p.late) pdl_wait();   // a selection's lengths are no caller input
   const int len = clamp_length(p, b, false);   // a caller input, not the split's output
   pdl_wait();   // the partials come from the split kernel just before
   int nsplit = partials_of(p, b, len);
@@ -1842,6 +1843,7 @@ __global__ void __launch_bounds__(32 * kCombineMaxWarps, 2)
   const int h = blockIdx.x, b = blockIdx.y;
   const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = blockIdx.z * 32 + lane;      // float4 column of the 512
+  if (p.late) pdl_wait();   // a selection's lengths are no caller input
   const int len = clamp_length(p, b, false);   // a caller input, not the split's output
   pdl_wait();   // the partials come from the split kernel just before
   int nsplit = partials_of(p, b, len);

@@ -77,3 +77,13 @@ def test_the_header_names_what_is_read_early():
         for field, name in inputs.items():
             if re.search(rf"\bp\.{field}\b", early) or re.search(helpers.get(field, "$^"), early):
                 assert name in listed, f"{kernel} reads {name} before its wait"
+
+
+@pytest.mark.parametrize("kernel", ["split_f32_paged_kernel", "split_fp8_kernel",
+                                    "split_pair_kernel", "split_tc_kernel", "combine_kernel",
+                                    "combine_warps_kernel"])
+def test_lengths_of_a_selection_are_read_behind_a_wait(kernel):
+    """Over a page selection (p.late) lengths are written by a kernel of the same call."""
+    body = _pdl.body_of(kernel, SOURCE)
+    first = re.search(r"\bclamp_length\(", body).start()
+    assert re.search(r"if \((kPaged && )?p\.late\) pdl_wait\(\);", body[:first])
