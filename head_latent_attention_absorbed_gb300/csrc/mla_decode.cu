@@ -576,7 +576,10 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   if (persist) {
     if (warp == kWarpA) plan_items(p, items, counts, lane);
     __syncthreads();
-    if (counts[0] == 0) return;   // no tile for this CTA
+    if (counts[0] == 0) {   // no tile for this CTA (for none of them where no row is)
+      if (blockIdx.x == 0) pdl_wait();
+      return;
+    }
     qv0 = items[0].qv;
     qh0 = items[0].h0;
     // Two boxes at once; the other first boxes once the softmax warps have
@@ -614,8 +617,8 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
       // (into this CTA's shared memory) have landed.
       if (!kPaged && ring_a && p.fill_early)
         for (int pos = 0; pos < kSlotsA; ++pos) mbar_wait_bounded(bar(BAR_FULLA + pos), 0);
+      if ((kPaged && p.direct) || r0 == 0) pdl_wait();   // no row at all: see launch_pdl
       if (kPaged && p.direct) {
-        pdl_wait();
         for (int u = 0; u < (pair ? 2 : 1); ++u)
           write_no_rows(p, size_t(b + u) * p.H + qh0, pair ? kHeadGroup / 2 : kHeadGroup, tid,
                         blockDim.x);

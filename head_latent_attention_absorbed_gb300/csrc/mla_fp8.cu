@@ -236,10 +236,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
     const int r0 = j * p.chunk;
     if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
-      if (kPaged && p.direct) {
-        pdl_wait();
-        write_no_rows(p, size_t(b) * p.H + h0, kHeadGroup, tid, kF8Threads);
-      }
+      if ((kPaged && p.direct) || r0 == 0) pdl_wait();   // no row at all: see launch_pdl
+      if (kPaged && p.direct) write_no_rows(p, size_t(b) * p.H + h0, kHeadGroup, tid, kF8Threads);
       return;
     }
     row_end = min(r0 + p.chunk, len);

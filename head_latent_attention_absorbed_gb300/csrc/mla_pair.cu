@@ -287,10 +287,8 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
         clamp_length(p, (seq + 1) * p.q_len - 1, tid == 0 && blockIdx.x == 0 && j == 0);
     const int r0 = j * p.chunk;
     if (r0 >= len) {   // both CTAs of the pair: the chunk lies past the sequence
-      if (p.direct) {
-        pdl_wait();
-        write_no_rows(p, seq * all + first, mine, tid, L::kThreads);
-      }
+      if (p.direct || r0 == 0) pdl_wait();   // no row at all: see launch_pdl
+      if (p.direct) write_no_rows(p, seq * all + first, mine, tid, L::kThreads);
       return;
     }
     T = (min(r0 + p.chunk, len) - r0 + kTileRows - 1) / kTileRows;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from _paged import D_C, D_R
-from test_gpu_paged_attn import BF16, F32, Call, i32
+from test_gpu_paged_attn import BF16, F32, KINDS, Call, i32
 from test_gpu_sparse import Sparse
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,37 @@ def test_absorb_sparse_out_proj(cuda_lib, dtype, heads, long):
         torch.cuda.synchronize()
         c.q_abs, c.q_pe = c.dev["q_abs"].cpu(), c.dev["q_pe"].cpu()
         c.check()
+
+
+@pytest.mark.parametrize("dtype,io,heads", KINDS)
+@pytest.mark.parametrize("form,splits", [(0, 1), (0, 3), (1, 0)])
+def test_a_call_without_any_row(cuda_lib, dtype, io, heads, form, splits):
+    """Every sequence empty, as in a batch of nothing but padding, between two calls with rows
+    on the same workspace and outputs: it gives zeros and -inf, and the others what they give
+    alone."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(form)
+    try:
+        calls = [Call(mla, [600, 40, 300], 16, dtype, io, heads, splits=splits, seed=k, s_max=600,
+                      width=40) for k in range(2)]
+        none = Call(mla, [0, 0, 0], 16, dtype, io, heads, splits=splits, seed=2, s_max=600, width=40)
+        alone = []
+        for c in calls + [none]:
+            c.ws, c.o, c.lse = calls[0].ws, calls[0].o, calls[0].lse
+            c.run()
+            torch.cuda.synchronize()
+            alone.append((c.o.clone(), c.lse.clone()))
+        assert (alone[2][0] == 0).all() and torch.isneginf(alone[2][1]).all()
+        kept = []
+        for _ in range(ROUNDS):
+            for c in (calls[0], none, calls[1]):
+                c.run()
+            kept.append((calls[0].o.clone(), calls[0].lse.clone()))
+            none.run()
+        torch.cuda.synchronize()
+        for o, lse in kept:
+            assert torch.equal(o, alone[1][0]) and torch.equal(lse, alone[1][1])
+        assert (none.o == 0).all() and torch.isneginf(none.lse).all()
+        assert int(none.status.item()) == mla.MLA_DEV_LENGTH_OUT_OF_RANGE
+    finally:
+        mla.load().mla_test_set_split_form(0)
