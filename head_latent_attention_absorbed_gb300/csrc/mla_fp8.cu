@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(160) fp8_q_prep_kernel(const SplitParams p) {
   mx = fmaxf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), wmax[4]);
   int ex = 0;
   frexpf(mx, &ex);   // mx = f 2^ex, f in [0.5, 1)
+  ex = max(ex, -100);   // keeps 1 / sg finite; smaller queries score as zero to 2^-100
   const float sg = mx > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
   const float inv = 1.f / sg;   // exact: a power of two
   if (t == 0) reinterpret_cast<float*>(img + kFp8QBoxes)[hh] = sg;

@@ -419,3 +419,14 @@ def test_refuses_wrong_tensors(cuda_lib):
     c.ws = c.ws[:100]
     with pytest.raises(mla.MlaError):
         c.run()
+
+
+@pytest.mark.parametrize("dtype,io,heads", KINDS)
+@pytest.mark.parametrize("size", [0.0, 1e-42, 1e-37, 1e-30])
+def test_tiny_queries(cuda_lib, dtype, io, heads, size):
+    """Queries of zeros, and of hardly anything with zeros among it: every row weighs the same."""
+    c = Call(cuda_lib, [300, 17], 32, dtype, io, heads, seed=11)
+    c.q_abs, c.q_pe = (c.q_abs.float() * size).to(io), (c.q_pe.float() * size).to(io)
+    c.q_abs[:, :, ::3] = 0
+    c.dev["q_abs"], c.dev["q_pe"] = c.q_abs.cuda(), c.q_pe.cuda()
+    c.run().check()
