@@ -1,0 +1,65 @@
+"""Corners of the paged calls: lengths below the tokens of a step, more chunks than tiles,
+large batches, every kind with several tokens in the sparse call."""
+import numpy as np
+import pytest
+import torch
+
+from _paged import D_C
+from test_gpu_paged_attn import BF16, F32, KINDS, Call
+from test_gpu_sparse import Sparse
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,io,heads", KINDS)
+@pytest.mark.parametrize("form,splits,q_len", [(0, 0, 2), (0, 3, 4), (1, 0, 3), (1, 0, 4)])
+def test_lengths_below_the_tokens(cuda_lib, dtype, io, heads, form, splits, q_len):
+    """A sequence with fewer rows than new tokens: its first tokens see nothing, and the
+    status says so."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(form)
+    try:
+        c = Call(mla, [1, 300, 0, q_len - 1, q_len], 16, dtype, io, heads, q_len=q_len,
+                 splits=splits, seed=q_len)
+        c.run().check(status=mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
+@pytest.mark.parametrize("dtype,io,heads", KINDS)
+def test_more_chunks_than_tiles(cuda_lib, dtype, io, heads):
+    Call(cuda_lib, [700, 129, 1, 513], 64, dtype, io, heads, splits=1000, seed=1).run().check()
+
+
+@pytest.mark.parametrize("dtype,io,heads", [("f32", F32, 1), ("bf16", F32, 16), ("bf16", BF16, 16),
+                                            ("bf16", BF16, 32), ("fp8", BF16, 16),
+                                            ("fp8", BF16, 48)])
+def test_large_batch(cuda_lib, dtype, io, heads):
+    """Thousands of short sequences."""
+    rng = np.random.RandomState(1)
+    c = Call(cuda_lib, rng.randint(1, 40, 5003), 16, dtype, io, heads, seed=2)
+    c.run().check(tokens=list(range(0, 5003, 419)) + [5002])
+
+
+@pytest.mark.parametrize("dtype,io,heads", [("f32", F32, 5), ("bf16", F32, 16), ("bf16", BF16, 64),
+                                            ("bf16", F32, 64), ("fp8", F32, 16), ("fp8", BF16, 32),
+                                            ("fp8", BF16, 128)])
+@pytest.mark.parametrize("q_len", [2, 3])
+def test_sparse_tokens_of_every_kind(cuda_lib, dtype, io, heads, q_len):
+    """Several tokens, some of a sequence that keep every page and some that choose, also
+    with lengths below the tokens."""
+    mla, page, top = cuda_lib, 16, 5
+    lengths = [page * top + 1, page * 33, q_len, page * top + q_len]
+    Sparse(mla, lengths, page, dtype, io, heads, top, q_len=q_len, seed=q_len).run().check()
+    s = Sparse(mla, [1, page * 20, q_len - 1], page, dtype, io, heads, top, q_len=q_len, seed=q_len)
+    s.run().check(status=mla.MLA_DEV_LENGTH_OUT_OF_RANGE)
+
+
+@pytest.mark.parametrize("dtype,io,heads", [("bf16", BF16, 16), ("fp8", BF16, 128), ("f32", F32, 3)])
+def test_sparse_in_a_barely_aligned_workspace(cuda_lib, dtype, io, heads):
+    s = Sparse(cuda_lib, [16 * 30 + 1, 16 * 9], 16, dtype, io, heads, 4, seed=3)
+    s.ws = torch.empty(s.ws.numel() + 16, dtype=torch.uint8, device="cuda")[16:]
+    o = torch.full((4, heads, D_C), 3.0, dtype=io, device="cuda")
+    s.o = o[:2]
+    s.run().check()
+    assert (o[2:] == 3).all()
