@@ -205,15 +205,16 @@ __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity,
 // items.  Writes items[0..n) with their first tile in the CTA's stream and
 // counts[0] = n, counts[1] = tiles; n > kMaxItems (never planned) raises
 // MLA_DEV_PIPELINE_TIMEOUT and keeps the first kMaxItems.
+template <bool kPaged>
 __device__ void plan_items(const SplitParams& p, SplitItem* items, volatile int* counts,
                            int lane) {
   const int groups = p.H / 16, ct = p.chunk / kTileRows;
   const long long G = gridDim.x, c = blockIdx.x;
   // Lengths of the first 32 query groups, one load per lane, kept for both passes.
-  const int len_lane = lane < p.B ? clamp_length(p, lane, c == 0) : 0;
+  const int len_lane = lane < p.B ? plain_length(p, lane, c == 0) : 0;
   auto length_of = [&](int v0, bool report_it) {
     const int v = v0 + lane;
-    return v0 == 0 ? len_lane : v < p.B ? clamp_length(p, v, report_it) : 0;
+    return v0 == 0 ? len_lane : v < p.B ? plain_length(p, v, report_it) : 0;
   };
   // Non-negative quotients; 32-bit division when both operands fit (the
   // planner's tile counts always do in practice; 64-bit division is a long
@@ -265,7 +266,7 @@ __device__ void plan_items(const SplitParams& p, SplitItem* items, volatile int*
         const int r0 = j * p.chunk, r1 = min(r0 + p.chunk, len);
         const int it = (r1 - r0 + kTileRows - 1) / kTileRows;
         SplitItem m;
-        m.row0 = p.table ? r0 : cache_seq(p, v) * p.s_max + r0;
+        m.row0 = kPaged ? r0 : cache_seq(p, v) * p.s_max + r0;
         m.tiles = it;
         m.t0 = 0;
         m.valid_last = r1 - (r0 + (it - 1) * kTileRows);
@@ -574,10 +575,10 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   int r0_one = 0;                    // one-item CTA: the chunk's first row in its sequence
   int qv0 = 0, qh0 = 0;              // query group and first head of the CTA's first item
   if (persist) {
-    if (warp == kWarpA) plan_items(p, items, counts, lane);
+    if (warp == kWarpA) plan_items<kPaged>(p, items, counts, lane);
     __syncthreads();
-    if (counts[0] == 0) {   // no tile for this CTA (for none of them where no row is)
-      if (blockIdx.x == 0) pdl_wait();
+    if (counts[0] == 0) {   // no tile for this CTA (for none where there is no row at all)
+      pdl_wait();
       return;
     }
     qv0 = items[0].qv;
@@ -1969,7 +1970,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int i = 0; i < 2; ++i)   // 256 lines of 128 bytes, two per thread
     asm volatile("prefetch.global.L2 [%0];" ::"l"(wslice + 8 * (tid + 128 * i)));
-  const int len = clamp_length(p, b, false);   // a caller input, not the split's output
+  const int len = plain_length(p, b, false);   // a caller input, not the split's output
   pdl_wait();   // the partials come from the split kernel just before
   // The next kernel (the next step's mla_absorb_q) may launch now and fetch its
   // weights; it waits for this grid before it reads or writes anything else.
