@@ -81,12 +81,12 @@ struct PairPlan {
   static constexpr int kOffRed = kOffP + kPBufs * kPBufBytes;   // [2][2 kSlices][64] maxima
   static constexpr int kOffSum = kOffRed + 2 * 2 * kSlices * kPHeads * 4;   // row sums
   static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
-  // full / empty of the rings; S and P hand-overs; the query; the last tile's units; the
+  // full / empty of the rings; S and P hand-overs; the query; the units to clean; the
   // query read for the last time (kShare)
   static constexpr int FULLS = 0, EMPTYS = FULLS + kSlotsS, FULLV = EMPTYS + kSlotsS,
                        EMPTYV = FULLV + kSlotsV, SREADY = EMPTYV + kSlotsV, SFREE = SREADY + 2,
                        PREADY = SFREE + 2, PVDONE = PREADY + 2, QFULL = PVDONE + 2,
-                       LASTV = QFULL + 1, ZEROED = LASTV + 4, QFREE = ZEROED + 4, kBars = QFREE + 1;
+                       CLEANV = QFULL + 1, CLEANED = CLEANV + 4, QFREE = CLEANED + 4, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffSlot + 8;
   static constexpr int kOffShare = kOffAbort + 8;   // TileShare of the pair
@@ -154,6 +154,15 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
+}
+// Eight bf16 or sixteen E4M3 values with NaN and infinities (E4M3 has none) as zeros.
+template <bool kFp8>
+__device__ __forceinline__ uint4 finite_only(uint4 v) {
+  auto word = [](uint32_t w) {
+    return w & ~(kFp8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                      : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u));
+  };
+  return make_uint4(word(v.x), word(v.y), word(v.z), word(v.w));
 }
 // 16 or 32 columns of this thread's lane, loaded: load and wait are one statement, so that no
 // use of the registers can be scheduled between them.
@@ -294,12 +303,13 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
     T = (min(r0 + p.chunk, len) - r0 + kTileRows - 1) / kTileRows;
     item0 = TileItem{seq, j, r0, T, len};
   }
-  // Rows of an item's last tile past the sequence's end may hold anything (NaN included):
-  // they are zeroed in the output operand.
-  auto zero_from = [&](const TileItem& it) {
-    return it.len - (it.r0 + (it.tiles - 1) * kTileRows);
+  // Rows past the sequence's end may hold anything (NaN included), and so may, for the
+  // tokens that do not attend them, the rows of the step's later tokens: from the first row
+  // that some token does not attend on, the output operand is cleaned.  Tiles of an item
+  // before its first one to clean:
+  auto clean_tiles = [&](const TileItem& it) {
+    return min(it.tiles, max(it.len - (p.q_len - 1) - it.r0, 0) / kTileRows);
   };
-  auto zero_last = [&](const TileItem& it) { return zero_from(it) < kTileRows; };
   auto item_after = [&](const TileItem& it, int t) { return next_item<true>(p, it, T - t); };
   const uint32_t lead = mapa_shared(bars, 0);   // the even CTA's barriers
   auto bar = [&](int i) { return bars + 8 * i; };
@@ -323,8 +333,8 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
     mbar_init(bar(L::QFULL), 1);
     mbar_init(bar(L::QFREE), 2);   // one commit per score issuer
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(L::LASTV + i), 1);
-      mbar_init(bar(L::ZEROED + i), 2 * L::kSoftWarps);
+      mbar_init(bar(L::CLEANV + i), 1);
+      mbar_init(bar(L::CLEANED + i), 2 * L::kSoftWarps);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -444,11 +454,11 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
     uint32_t phase = 1;
     for (int t0 = 0; t0 < T;) {   // items
       const int end = t0 + it.tiles;
-      const bool zero = zero_last(it);
+      const int clean = clean_tiles(it);
       TileItem then = it;
       if (kShare && end < T) then = item_after(it, end);
       for (int i = 0; i < it.tiles; ++i) {
-        const bool last = zero && i == it.tiles - 1;   // these land on the CTA's own barriers
+        const bool own = i >= clean;   // these land on the CTA's own barriers
         const int next = i + 1 < it.tiles     ? rows_of(it, i + 1)
                          : kShare && end < T ? rows_of(then, 0)
                                              : 0;
@@ -456,11 +466,11 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           warp_wait(bar(L::EMPTYV + sl), phase, abort_flag);
-          if (last)
-            expect_tx_elected(bar(L::LASTV + u), L::kUnit);
+          if (own)
+            expect_tx_elected(bar(L::CLEANV + u), L::kUnit);
           else if (leader)
             expect_tx_elected(bar(L::FULLV + sl), 2 * L::kUnit);
-          const uint32_t full = last ? mapa_shared(bar(L::LASTV + u), rank) : lbar(L::FULLV + sl);
+          const uint32_t full = own ? mapa_shared(bar(L::CLEANV + u), rank) : lbar(L::FULLV + sl);
           const uint32_t dst = sbase + L::kOffV + sl * L::kUnit;
           const int x = 256 * (u & 1) + 128 * rank;
 #pragma unroll 1
@@ -548,23 +558,21 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
       const uint64_t v0 = umma_desc_sw128(sbase + L::kOffV, kPBox, 1024);
       const uint32_t d = tmem + L::kOCol + 128 * jj;
       TileItem it = item0;
-      int zeroed = 0;   // zeroed last tiles so far
+      int cleaned = 0;   // cleaned tiles so far
       for (int t0 = 0; t0 < T;) {   // items
-        const int end = t0 + it.tiles;
-        const bool zero = zero_last(it);
+        const int end = t0 + it.tiles, clean = t0 + clean_tiles(it);
         for (int t = t0; t < end; ++t) {
           const int pb = t & 1;
           warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
           if (__any_sync(0xffffffffu, *abort_flag)) break;
-          const bool last = zero && t == end - 1;
 #pragma unroll 1
           for (int kh = 0; kh < 2; ++kh) {
-            // A tile's four units take the ring's four slots; zeroed ones pass FULLV by.
+            // A tile's four units take the ring's four slots; cleaned ones pass FULLV by.
             const int u = 2 * kh + jj, sl = u;
-            if (last)
-              warp_wait(bar(L::ZEROED + u), zeroed & 1, abort_flag);
+            if (t >= clean)
+              warp_wait(bar(L::CLEANED + u), cleaned & 1, abort_flag);
             else
-              warp_wait(bar(L::FULLV + sl), (t - zeroed) & 1, abort_flag);
+              warp_wait(bar(L::FULLV + sl), (t - cleaned) & 1, abort_flag);
             tc_fence_after();
             const uint64_t b = v0 + static_cast<uint64_t>(sl * (L::kUnit >> 4));
             // 64 rows: bf16 four steps of 16 (2 KB of rows, 32 bytes of P's box kh); E4M3
@@ -582,9 +590,9 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
             commit_pair(bar(L::EMPTYV + sl));
           }
           commit_pair(bar(L::PVDONE + pb));
+          if (t >= clean) ++cleaned;
         }
         t0 = end;
-        zeroed += zero ? 1 : 0;
         if (kShare && t0 < T) it = item_after(it, t0);
       }
     }
@@ -599,10 +607,10 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
     const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
     const int back = p.q_len - 1 - (first + min(head, mine - 1)) / p.H;   // tokens behind its own
     TileItem it = item0;
-    int zeroed = 0;   // zeroed last tiles so far
+    int cleaned = 0;   // cleaned tiles so far
     for (int t0 = 0; t0 < T;) {   // items; t0: the item's first tile among the pair's
       const int flat0 = it.v * all + first, tiles = it.tiles;
-      const bool zero = zero_last(it);
+      const int clean = t0 + clean_tiles(it);
       // E4M3: the head's unit, written by the kernel before (known complete once the
       // first scores are).
       float scale = p.scale_log2;
@@ -720,25 +728,29 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(lbar(L::PREADY + sb));
-        if (t == t0 + tiles - 1 && zero) {
-          // As each unit of the last tile lands in this CTA, zero its rows past the end.
+        if (t >= clean) {
+          // As each unit of the tile lands in this CTA: rows past the end become zeros, and in
+          // the rows that some token does not attend NaN and infinities do.  (The tokens that
+          // attend such a row have them from its scores.)
+          const int end = it.len - it.r0 - (t - t0) * kTileRows;   // behind the last row
           for (int u = 0; u < 4; ++u) {
-            warp_wait(bar(L::LASTV + u), zeroed & 1, abort_flag);
-            const int from = max(0, zero_from(it) - 64 * (u >> 1));
+            warp_wait(bar(L::CLEANV + u), cleaned & 1, abort_flag);
+            const int from = max(0, end - (p.q_len - 1) - 64 * (u >> 1));
             uint8_t* unit = smem + L::kOffV + u * L::kUnit;
             for (int i = tid; i < (64 - from) * 8 * (L::kUnit / kPBox); i += L::kSoft) {
               const int box = i / ((64 - from) * 8), r = i % ((64 - from) * 8);
-              *reinterpret_cast<uint4*>(unit + box * kPBox + from * 128 + 16 * r) =
-                  make_uint4(0, 0, 0, 0);
+              uint4* at = reinterpret_cast<uint4*>(unit + box * kPBox + from * 128 + 16 * r);
+              *at = from + (r >> 3) < end - 64 * (u >> 1) ? finite_only<kFp8>(*at)
+                                                          : make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_cluster(lbar(L::ZEROED + u));
+            if (lane == 0) arrive_cluster(lbar(L::CLEANED + u));
           }
+          ++cleaned;
         }
       }
       t0 += tiles;
-      zeroed += zero ? 1 : 0;
       if (tid == 0 && t0 == T) pdl_launch_dependents();   // the combine waits for this grid anyway
       // The row sums of a head's four threads, its log-sum-exp, and O / sum through
       // shared memory (over operands that nothing reads any more) to whole rows.

@@ -63,3 +63,40 @@ def test_sparse_in_a_barely_aligned_workspace(cuda_lib, dtype, io, heads):
     s.o = o[:2]
     s.run().check()
     assert (o[2:] == 3).all()
+
+
+def poison_row(call, b, t, value):
+    """Row t of sequence b of a call's pool on the GPU becomes `value` (E4M3: NaN) in every
+    third column, the RoPE key's among them."""
+    pool, page = call.dev["pool"], call.pg.page_size
+    at = int(call.table[b, t // page])
+    if call.dtype == "fp8":
+        pool.view(torch.uint8)[at, t % page, ::3] = 0x7F
+    else:
+        pool[at, t % page, ::3] = value
+
+
+@pytest.mark.parametrize("dtype,io,heads", [k for k in KINDS if k != ("bf16", F32, 16)])
+@pytest.mark.parametrize("form,q_len", [(0, 2), (1, 2), (0, 3), (1, 4)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_later_tokens_row_is_not_seen(cuda_lib, dtype, io, heads, form, q_len, value):
+    """Rows that the last token of a step attends and the tokens before it do not: NaN and
+    infinities there do not reach the earlier tokens, wherever in a tile the rows lie."""
+    mla = cuda_lib
+    lengths = [127, 128, 129, 130, 256, 300, 257 + q_len, q_len, 5]
+    mla.load().mla_test_set_split_form(form)
+    try:
+        c = Call(mla, lengths, 16, dtype, io, heads, q_len=q_len, seed=q_len)
+        for b, n in enumerate(lengths):
+            poison_row(c, b, n - 1, value)
+        c.run().check(tokens=[r for r in range(len(lengths) * q_len) if r % q_len < q_len - 1])
+        last = c.o.view(len(lengths), q_len, heads, D_C)[:, -1].float()
+        assert not torch.isfinite(last).any()
+        # every row of the step but the first token's
+        c = Call(mla, lengths, 16, dtype, io, heads, q_len=q_len, seed=q_len)
+        for b, n in enumerate(lengths):
+            for t in range(n - q_len + 1, n):
+                poison_row(c, b, t, value)
+        c.run().check(tokens=range(0, len(lengths) * q_len, q_len))
+    finally:
+        mla.load().mla_test_set_split_form(0)
