@@ -359,7 +359,11 @@ __device__ __forceinline__ float reduce8_heads(float v[8], int lane) {
 // from: a tile's 128 rows are boxes of up to 128 (ring A) or 64 (ring B) rows
 // of one page each, issued by as many lanes, which look the next tile's pages
 // up one tile ahead.  The query may then be bf16 as it is stored.
-template <int kG, bool kPersist, bool kPaged>
+//
+// kTwo: two tokens of a multi-token step x 16 heads in place of 32 heads.  (An instance of
+// its own: asked at run time, the cleaning of the second token's row cost 64 ragged
+// sequences of 32 heads 1 %.)
+template <int kG, bool kPersist, bool kPaged, bool kTwo = false>
 __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     split_tc_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tmap_half,
                     const SplitParams p) {
@@ -409,7 +413,8 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   // columns 0-15 are the 16 heads of query group b, 16-31 those of b + 1, the
   // next token of the same sequence; the tiles follow the later token's rows
   // and each 8-head softmax group masks the rows past its own token.
-  const bool pair = kG == 32 && p.tpc == 2;
+  constexpr bool pair = kTwo;
+  static_assert(!kTwo || (kG == 32 && !kPersist), "two tokens x 16 heads of a one-item CTA");
   constexpr bool persist = kPersist;
   // Rows of the cache's [sequences * s_max, 576] view (index checks).
   const long long cache_rows = kPaged ? 0 : static_cast<long long>(p.B / p.q_len) * p.s_max;
@@ -711,7 +716,9 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   const int fin_item = n_items - 1;
   const int last_row = fin.row0 + (fin.tiles - 1) * kTileRows;
   const int zero_from = fin.zero_from;
-  const bool zero_last = zero_from < kTileRows;
+  // Paired tokens: the last row is the later token's alone, and is cleaned for the earlier
+  // one (NaN and infinities become zeros; the later token has them from its scores).
+  const bool zero_last = zero_from - (pair ? 1 : 0) < kTileRows;
   const bool fin_first = T - 1 == fin.t0;     // the last tile is its item's first
   // Item i accumulates into O^T buffer i % kOBufs.
   auto obuf_col = [&](int i) { return kOCol + static_cast<uint32_t>(i % L::kOBufs) * kOBufCols; };
@@ -1440,7 +1447,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
         // exist only when it is the first tile too (first fills).
         if (kResidentTail) {
           // Whole 128-row boxes: in ring A (landed before the scores this thread
-          // has read) or once read again.
+          // has read) or once read again.  (Tokens are never paired here.)
           const int nrow = kTileRows - zero_from;
           for (int k = 0; k < 8; ++k) {
             if (!tail_res(k >> 1)) wait_or_abort(bar(BAR_FULLX + k), 0, abort_flag, wait_ns);
@@ -1469,6 +1476,11 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
             const int o = h * kHalfBox + (first + rem / 8) * 128 + (rem % 8) * 16;
             if (MLA_IN_BOUNDS(o >= 0 && o + 16 <= 2 * kHalfBox))
               *reinterpret_cast<uint4*>(pr + o) = make_uint4(0, 0, 0, 0);
+          }
+          const int row = zero_from - 1 - 64 * kh;   // the later token's own, in this half?
+          if (pair && static_cast<unsigned>(row) < 64u && tid < 16) {
+            uint4* at = reinterpret_cast<uint4*>(pr + (tid >> 3) * kHalfBox + row * 128 + (tid & 7) * 16);
+            *at = finite_only<false>(*at);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -2103,14 +2115,14 @@ bool pair_tokens(const mla_dims* cache_dims, int q_len) {
   return cache_dims->dtype == MLA_BF16 && cache_dims->heads % 32 != 0 && q_len % 2 == 0;
 }
 
-template <int kG, bool kPersist, bool kPaged = false>
+template <int kG, bool kPersist, bool kPaged = false, bool kTwo = false>
 mla_status launch_split_tc(const CUtensorMap& tmap, const CUtensorMap& tmap_half,
                            const SplitParams& p, int heads, cudaStream_t s, const char* who) {
   using L = TcPlan<kG, kPersist>;
   static DeviceFlags attr_done;
   const int dev = current_device();
   if (!attr_done.test(dev)) {
-    if (cudaFuncSetAttribute(split_tc_kernel<kG, kPersist, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(split_tc_kernel<kG, kPersist, kPaged, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(L::kSmem)) != cudaSuccess) {
       set_error("%s: cannot reserve %zu bytes of shared memory", who, L::kSmem);
       return MLA_ERR_CUDA;
@@ -2125,15 +2137,15 @@ mla_status launch_split_tc(const CUtensorMap& tmap, const CUtensorMap& tmap_half
   // Paired tokens: 16-head slices, two query groups per CTA.  A persistent grid
   // has one CTA per SM.
   const dim3 grid = p.persist ? dim3(sms > 0 ? sms : 1)
-                              : dim3(p.tpc == 2 ? heads / 16 : heads / kG, p.splits,
-                                     p.tpc == 2 ? p.B / 2 : p.B);
+                              : dim3(kTwo ? heads / 16 : heads / kG, p.splits,
+                                     kTwo ? p.B / 2 : p.B);
   // A CTA whose chunk lies past its sequence's end would fetch its first boxes
   // for nothing; that costs little in a one-wave grid, but in several waves it
   // delays the CTAs behind it (measured: 64 ragged sequences, split 67.9 ->
   // 70.4 us with the early fetch everywhere).
   SplitParams q = p;
   q.fill_early = !p.persist && static_cast<long long>(grid.x) * grid.y * grid.z <= sms;
-  launch_pdl(split_tc_kernel<kG, kPersist, kPaged>, grid, dim3(L::kThreads), L::kSmem, s, tmap, tmap_half, q);
+  launch_pdl(split_tc_kernel<kG, kPersist, kPaged, kTwo>, grid, dim3(L::kThreads), L::kSmem, s, tmap, tmap_half, q);
   return MLA_OK;
 }
 // How the split kernel cuts the rows: chunk rows, chunks per sequence, and
@@ -2604,13 +2616,15 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
         return MLA_ERR_CUDA;
       }
     }
-    const int per_cta = p.tpc == 2 ? 32 : tc_heads_per_cta(dims, plan_opts(dims, q_len, view));
+    const int per_cta = tc_heads_per_cta(dims, plan_opts(dims, q_len, view));
     if (view)
-      st = per_cta == 32 ? launch_split_tc<32, false, true>(tmap, tmap_half, p, dims->heads, s, who)
+      st = p.tpc == 2 ? launch_split_tc<32, false, true, true>(tmap, tmap_half, p, dims->heads, s, who)
+           : per_cta == 32 ? launch_split_tc<32, false, true>(tmap, tmap_half, p, dims->heads, s, who)
            : p.persist ? launch_split_tc<16, true, true>(tmap, tmap_half, p, dims->heads, s, who)
                        : launch_split_tc<16, false, true>(tmap, tmap_half, p, dims->heads, s, who);
     else
-      st = per_cta == 64   ? launch_split_tc<64, false>(tmap, tmap_half, p, dims->heads, s, who)
+      st = p.tpc == 2      ? launch_split_tc<32, false, false, true>(tmap, tmap_half, p, dims->heads, s, who)
+         : per_cta == 64   ? launch_split_tc<64, false>(tmap, tmap_half, p, dims->heads, s, who)
          : per_cta == 32 ? launch_split_tc<32, false>(tmap, tmap_half, p, dims->heads, s, who)
          : p.persist     ? launch_split_tc<16, true>(tmap, tmap_half, p, dims->heads, s, who)
                          : launch_split_tc<16, false>(tmap, tmap_half, p, dims->heads, s, who);

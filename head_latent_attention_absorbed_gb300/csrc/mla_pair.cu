@@ -155,15 +155,6 @@ __device__ __forceinline__ void cluster_sync_all() {
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// Eight bf16 or sixteen E4M3 values with NaN and infinities (E4M3 has none) as zeros.
-template <bool kFp8>
-__device__ __forceinline__ uint4 finite_only(uint4 v) {
-  auto word = [](uint32_t w) {
-    return w & ~(kFp8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                      : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u));
-  };
-  return make_uint4(word(v.x), word(v.y), word(v.z), word(v.w));
-}
 // 16 or 32 columns of this thread's lane, loaded: load and wait are one statement, so that no
 // use of the registers can be scheduled between them.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {

@@ -116,6 +116,16 @@ __device__ __forceinline__ int clamp_length(const SplitParams& p, int v, bool re
   return clamp_length(p, v, report_it, p.lengths[p.q_len == 1 ? v : v / p.q_len]);
 }
 
+// Eight bf16 or sixteen E4M3 values with NaN and infinities (E4M3 has none) as zeros.
+template <bool kFp8>
+__device__ __forceinline__ uint4 finite_only(uint4 v) {
+  auto word = [](uint32_t w) {
+    return w & ~(kFp8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                      : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u));
+  };
+  return make_uint4(word(v.x), word(v.y), word(v.z), word(v.w));
+}
+
 // Exclusive prefix sum of x over the warp's lanes, and the warp's total.
 __device__ __forceinline__ int warp_exclusive_scan(int x, int lane, int* total) {
   int incl = x;

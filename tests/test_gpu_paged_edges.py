@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _paged import D_C
+from _paged import D_C, DT, SCALE
 from test_gpu_paged_attn import BF16, F32, KINDS, Call
 from test_gpu_sparse import Sparse
 
@@ -76,7 +76,7 @@ def poison_row(call, b, t, value):
         pool[at, t % page, ::3] = value
 
 
-@pytest.mark.parametrize("dtype,io,heads", [k for k in KINDS if k != ("bf16", F32, 16)])
+@pytest.mark.parametrize("dtype,io,heads", KINDS)
 @pytest.mark.parametrize("form,q_len", [(0, 2), (1, 2), (0, 3), (1, 4)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_a_later_tokens_row_is_not_seen(cuda_lib, dtype, io, heads, form, q_len, value):
@@ -100,3 +100,38 @@ def test_a_later_tokens_row_is_not_seen(cuda_lib, dtype, io, heads, form, q_len,
         c.run().check(tokens=range(0, len(lengths) * q_len, q_len))
     finally:
         mla.load().mla_test_set_split_form(0)
+
+
+@pytest.mark.parametrize("dtype,heads", [("f32", 5), ("bf16", 16), ("bf16", 32), ("bf16", 48),
+                                         ("bf16", 64), ("fp8", 16)])
+@pytest.mark.parametrize("q_len,splits", [(2, 0), (2, 3), (3, 0), (4, 0)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_later_tokens_row_is_not_seen_dense(cuda_lib, dtype, heads, q_len, splits, value):
+    """The same over a dense cache: the earlier tokens' bits are those over finite rows."""
+    mla, S = cuda_lib, 600
+    lengths = [127, 128, 129, 130, 256, 300, 600, q_len]
+    B = len(lengths)
+    g = torch.Generator().manual_seed(q_len)
+    cache = torch.randn((B, S, 576), generator=g).to(DT[dtype]).cuda()
+    q_abs = (torch.randn((B * q_len, heads, D_C), generator=g) * 0.3).cuda()
+    q_pe = torch.randn((B * q_len, heads, 64), generator=g).cuda()
+    d = mla.dims(B, heads, S, mla.dtype_code(DT[dtype]))
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    ws = torch.empty(int(mla.load().mla_decode_multi_workspace_bytes(d, q_len, splits)),
+                     dtype=torch.uint8, device="cuda")
+
+    def run():
+        o, lse = torch.empty_like(q_abs), torch.empty((B * q_len, heads), device="cuda")
+        mla.decode_attn_multi(d, q_len, q_abs, q_pe, cache, n, o, ws, SCALE, splits, lse=lse)
+        torch.cuda.synchronize()
+        return o.view(B, q_len, heads, D_C), lse.view(B, q_len, heads)
+
+    want, want_lse = run()
+    for b, k in enumerate(lengths):
+        if dtype == "fp8":
+            cache.view(torch.uint8)[b, k - 1, ::3] = 0x7F
+        else:
+            cache[b, k - 1, ::3] = value
+    got, lse = run()
+    assert torch.equal(got[:, :-1], want[:, :-1]) and torch.equal(lse[:, :-1], want_lse[:, :-1])
+    assert not torch.isfinite(got[:, -1]).any()
