@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(128) pair_query_kernel(const SplitParams p, ui
 // item per sequence it meets; the next item's rows and query are fetched and its scores
 // computed while the last one's output is written (a change of item costs about 2.5 us, the
 // softmax of its first tile behind that write).  Otherwise a pair has one item, its chunk.
-// 64 sequences of 512 to 8192 bf16 rows x 32 heads 110 -> 77 us, x 128 heads 113 -> 89.
+// 64 sequences of 512 to 8192 bf16 rows x 32 heads 110 -> 77 us, x 128 heads 113 -> 91.
 template <bool kFp8, bool kShare>
 __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
                                          : PairPlan<kFp8>::kThreads, 1)

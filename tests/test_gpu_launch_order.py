@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _paged import D_C, D_R
+from _paged import D_C, D_R, DT, SCALE
 from test_gpu_paged_attn import BF16, F32, KINDS, Call, i32
 from test_gpu_sparse import Sparse
 
@@ -192,3 +192,55 @@ def test_a_call_without_any_row(cuda_lib, dtype, io, heads, form, splits):
         assert int(none.status.item()) == mla.MLA_DEV_LENGTH_OUT_OF_RANGE
     finally:
         mla.load().mla_test_set_split_form(0)
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 16), ("bf16", 32), ("fp8", 16)])
+def test_decode_steps_over_pages(cuda_lib, dtype, heads):
+    """Decode steps as a server runs them, none synchronised: pages, the new rows, queries of
+    mla_absorb_q, attention over the pages, mla_out_proj.  The same bits as the dense calls
+    over the rows that the pages hold."""
+    mla, B, page, S, steps = cuda_lib, 6, 16, 512, 5
+    rng = np.random.RandomState(heads)
+    start = rng.randint(1, S - steps, B)
+    start[:2] = [page * 3, S - steps]
+    pages, width = B * (S // page) + 3, S // page
+    pg, d = mla.paging(page, pages, width), mla.dims(B, heads, S, mla.dtype_code(DT[dtype]))
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    free, nf, lengths, starts, status = i32(rng.permutation(pages)), i32([pages]), z(B), z(B + 1), z(1)
+    pool = torch.full((pages, page, 576), float("nan")).to(DT[dtype]).cuda()
+    T = int(start.sum())
+    slots, pos = z(T, dt=torch.int64), z(T)
+    mla.pages_extend(pg, lengths, i32(start), table, free, nf, lengths, starts, slots, pos,
+                     dev_status=status)
+    mla.cache_append_paged(d, pg, torch.from_numpy(rng.randn(T, 576)).bfloat16().cuda(), pos, slots,
+                           pool, dev_status=status)
+    ws = z(max(mla.paged_workspace_bytes(d, pg, F32, 1, 2), mla.workspace_bytes(d, 2)), dt=torch.uint8)
+    q_abs, q_pe, o = z(B, heads, D_C, dt=F32), z(B, heads, D_R, dt=F32), z(B, heads, D_C, dt=F32)
+    w_uv = torch.from_numpy(rng.randn(heads, 128, D_C) * 0.04).bfloat16().cuda()
+    x = [absorb_inputs(k, B, heads)[0] for k in range(steps)]
+    rows = [torch.from_numpy(rng.randn(B, 576)).bfloat16().cuda() for _ in range(steps)]
+    one, slot, at = torch.ones(B, dtype=torch.int32, device="cuda"), z(B, dt=torch.int64), z(B)
+    outs, kept = [z(B, heads, 128, dt=F32) for _ in range(2 * steps)], []
+    torch.cuda.synchronize()
+    for k in range(steps):
+        mla.pages_extend(pg, lengths, one, table, free, nf, lengths, starts, slot, at,
+                         dev_status=status)
+        mla.cache_append_paged(d, pg, rows[k], at, slot, pool, dev_status=status)
+        mla.absorb_q(d, x[k]["q_nope"], x[k]["q_rope"], x[k]["w_uk"], at, q_abs, q_pe)
+        mla.decode_attn_paged(d, pg, q_abs, q_pe, pool, table, lengths, o, ws, SCALE,
+                              num_splits_requested=2, dev_status=status)
+        mla.out_proj(d, o, w_uv, outs[k])
+        kept.append((table.clone(), lengths.clone(), at.clone()))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and lengths.cpu().tolist() == (start + steps).tolist()
+    flat = pool.view(torch.uint8).view(pages, -1)
+    for k, (tab, n, p) in enumerate(kept):
+        cache = torch.zeros((B, width, flat.shape[1]), dtype=torch.uint8, device="cuda")
+        live = tab >= 0
+        cache[live] = flat[tab[live].long()]
+        mla.absorb_q(d, x[k]["q_nope"], x[k]["q_rope"], x[k]["w_uk"], p, q_abs, q_pe)
+        mla.decode_attn(d, q_abs, q_pe, cache.view(DT[dtype]).view(B, S, 576), n, o, ws, SCALE, 2)
+        mla.out_proj(d, o, w_uv, outs[steps + k])
+        torch.cuda.synchronize()
+        assert torch.isfinite(outs[k]).all() and torch.equal(outs[k], outs[steps + k])
