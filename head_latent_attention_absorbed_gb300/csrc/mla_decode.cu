@@ -719,6 +719,9 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
   // Paired tokens: the last row is the later token's alone, and is cleaned for the earlier
   // one (NaN and infinities become zeros; the later token has them from its scores).
   const bool zero_last = zero_from - (pair ? 1 : 0) < kTileRows;
+  // Whether row half kh of the last tile has any row to clean; asked of paired tokens only,
+  // whose full tiles would pay for both halves.
+  auto half_cleaned = [&](int kh) { return !pair || zero_from - 1 < 64 * (kh + 1); };
   const bool fin_first = T - 1 == fin.t0;     // the last tile is its item's first
   // Item i accumulates into O^T buffer i % kOBufs.
   auto obuf_col = [&](int i) { return kOCol + static_cast<uint32_t>(i % L::kOBufs) * kOBufCols; };
@@ -1038,7 +1041,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
     const int pos = 8 * t + u, sl = pos % kSlotsB;
     const bool bw = borrowed(t, u);
     const int x = bw ? borrow_x(u) : 0;
-    if (t == T - 1 && zero_last &&
+    if (t == T - 1 && zero_last && half_cleaned(kh) &&
         !wait_or_abort(bw ? bar(BAR_ZEROX + x) : bar(BAR_ZEROB + sl), 0, abort_flag, wait_ns))
       return false;
     // A zeroed tile before the last zeroes each slot twice (units u and u + 4),
@@ -1463,6 +1466,7 @@ __global__ void __launch_bounds__(TcPlan<kG, kPersist>::kThreads, 1)
         }
         for (int u = 0; u < 8 && !kResidentTail; ++u) {
           const int kh = u >> 2;
+          if (!half_cleaned(kh)) continue;
           const int first = max(0, zero_from - 64 * kh);   // first row of this half to clear
           const int nrow = 64 - first;
           const int pos = 8 * t + u, sl = pos % kSlotsB;
