@@ -244,3 +244,30 @@ def test_decode_steps_over_pages(cuda_lib, dtype, heads):
         mla.out_proj(d, o, w_uv, outs[steps + k])
         torch.cuda.synchronize()
         assert torch.isfinite(outs[k]).all() and torch.equal(outs[k], outs[steps + k])
+
+
+def test_calls_at_once_on_two_streams(cuda_lib):
+    """Different calls on two streams, each with its own workspace and outputs, at the same
+    time: the bits they give alone."""
+    left = [Call(cuda_lib, [900, 300, 41] * 8, 16, dtype, io, heads, seed=k)
+            for k, (dtype, io, heads) in enumerate([("fp8", BF16, 128), ("bf16", BF16, 16),
+                                                    ("bf16", BF16, 64), ("f32", F32, 5)])]
+    right = [short_sparse(cuda_lib, k, dtype, io, heads, True)
+             for k, (dtype, io, heads) in enumerate([("bf16", BF16, 16), ("fp8", BF16, 128),
+                                                     ("fp8", F32, 16), ("bf16", F32, 32)])]
+    alone = []
+    for c in left + right:
+        c.run()
+        torch.cuda.synchronize()
+        alone.append((c.o.clone(), c.lse.clone()))
+        c.o.fill_(7), c.lse.fill_(7)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for pair in zip(left, right):
+            for stream, c in zip(streams, pair):
+                with torch.cuda.stream(stream):
+                    c.run()
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(left + right, alone):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse) and int(c.status.item()) == 0
