@@ -620,8 +620,9 @@ mla_status mla_decode_attn_paged(const mla_dims* dims, const mla_paging* paging,
  * gained; a request that gained more, or a length outside the table's row, sets
  * MLA_DEV_LENGTH_OUT_OF_RANGE (the pages of its first max_new rows are done; a
  * bad length does none).  A page outside the pool sets
- * MLA_DEV_PAGE_OUT_OF_RANGE and is skipped.  A page that several sequences touch
- * gets the index of one of them, which differ only where n does.  dims: batch and dtype.
+ * MLA_DEV_PAGE_OUT_OF_RANGE and is skipped.  A page that several sequences touch in one
+ * call must hold the same n rows in each (otherwise its index is a mixture of theirs).
+ * dims: batch and dtype.
  */
 mla_status mla_page_index(const mla_dims* dims, const mla_paging* paging, int32_t max_new,
                           const void* cache, const int32_t* block_table,
