@@ -23,7 +23,7 @@ from ._binding import (_check, _stream, step_call, EXPORTED, LIB_PATH, MLA_BF16,
                        MlaPaging, cache_append_paged, decode_attn_paged, decode_attn_sparse,
                        page_index, paged_num_splits, paged_workspace_bytes, pages_extend,
                        pages_release, paging, select_pages, select_workspace_bytes,
-                       sparse_workspace_bytes)
+                       sparse_workspace_bytes, MLA_FP4_E2M1, cache_read_paged, pool_bytes)
 
 __all__ = [
     "EXPORTED", "LIB_PATH", "MLA_BF16", "MLA_F32", "MLA_FP8_E4M3", "MLA_DEV_LENGTH_OUT_OF_RANGE",
@@ -38,6 +38,7 @@ __all__ = [
     "pages_extend", "pages_release", "cache_append_paged", "decode_attn_paged",
     "paged_num_splits", "paged_workspace_bytes", "page_index", "select_pages",
     "select_workspace_bytes", "decode_attn_sparse", "sparse_workspace_bytes",
+    "MLA_FP4_E2M1", "cache_read_paged", "pool_bytes",
 ]
 
 

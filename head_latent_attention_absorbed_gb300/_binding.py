@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmla_gb300.so")
 CHECK_LIB_PATH = os.path.join(PKG, "libmla_gb300_check.so")   # the checked build
 
-MLA_F32, MLA_BF16, MLA_FP8_E4M3 = 0, 1, 2
+MLA_F32, MLA_BF16, MLA_FP8_E4M3, MLA_FP4_E2M1 = 0, 1, 2, 3
 MLA_DEV_LENGTH_OUT_OF_RANGE = 1
 MLA_DEV_PIPELINE_TIMEOUT = 2
 MLA_DEV_BOUNDS = 4
@@ -37,7 +37,8 @@ EXPORTED = ("mla_absorb_q", "mla_decode_num_splits", "mla_decode_workspace_bytes
             "mla_pages_extend", "mla_pages_release", "mla_cache_append_paged",
             "mla_paged_num_splits", "mla_paged_workspace_bytes", "mla_decode_attn_paged",
             "mla_page_index", "mla_select_workspace_bytes", "mla_select_pages",
-            "mla_sparse_workspace_bytes", "mla_decode_attn_sparse")
+            "mla_sparse_workspace_bytes", "mla_decode_attn_sparse", "mla_pool_bytes",
+            "mla_cache_read_paged")
 
 
 class MlaDims(ctypes.Structure):
@@ -161,6 +162,10 @@ def load(path: Optional[str] = None):
     lib.mla_decode_attn_sparse.argtypes = [D, G, I32, I32, P, P, P, P, P, P, P, F, I32, I32, I32,
                                            I32, P, SZ, P, P, P, P, P, P]
     lib.mla_decode_attn_sparse.restype = ctypes.c_int
+    lib.mla_pool_bytes.argtypes = [D, G]
+    lib.mla_pool_bytes.restype = SZ
+    lib.mla_cache_read_paged.argtypes = [D, G, P, P, P, P, P, I32, I32, P, P, P]
+    lib.mla_cache_read_paged.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -477,7 +482,7 @@ def _paged_lib():
         _I32, _I64, _I8 = torch.int32, torch.int64, torch.int8
         _F32, _BF16 = torch.float32, torch.bfloat16
         _ROW_TYPE = {MLA_F32: torch.float32, MLA_BF16: torch.bfloat16,
-                     MLA_FP8_E4M3: torch.float8_e4m3fn}
+                     MLA_FP8_E4M3: torch.float8_e4m3fn, MLA_FP4_E2M1: torch.uint8}
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _device = torch._C._cuda_getDevice
     return _lib if _lib is not None else load()
@@ -506,6 +511,19 @@ def _explain(dev: int, **want):
 def _is(t, dev, dtype, numel) -> bool:
     return (t.get_device() == dev and t.dtype is dtype and t.numel() == numel
             and t.is_contiguous())
+
+
+def _pool_numel(d: MlaDims, pg: MlaPaging) -> int:
+    """Elements of a pool: values, or of a 4-bit pool bytes (uint8)."""
+    row = 400 if d.dtype == MLA_FP4_E2M1 else d.d_c + d.d_rope
+    return pg.num_pages * pg.page_size * row
+
+
+def pool_bytes(d: MlaDims, pg: MlaPaging) -> int:
+    """Bytes of a pool of these pages (of a 4-bit one: the elements of its uint8 tensor)."""
+    n = int(load().mla_pool_bytes(d, pg))
+    _require(n > 0, load().mla_last_error_message().decode())
+    return n
 
 
 def _io_code(torch_dtype) -> int:
@@ -589,7 +607,7 @@ def cache_append_paged(d: MlaDims, pg: MlaPaging, rows, positions, slots, cache,
     rotated at its position; a slot of -1 is skipped."""
     lib = _paged_lib()
     dev, n, row, kind = _device(), slots.numel(), d.d_c + d.d_rope, rows.dtype
-    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * row
+    ct, cn = _ROW_TYPE.get(d.dtype), _pool_numel(d, pg)
     if not (rows.get_device() == positions.get_device() == slots.get_device()
             == cache.get_device() == dev
             and (kind is _BF16 or kind is _F32) and positions.dtype is _I32
@@ -604,6 +622,32 @@ def cache_append_paged(d: MlaDims, pg: MlaPaging, rows, positions, slots, cache,
     code = lib.mla_cache_append_paged(
         d, pg, n, MLA_BF16 if kind is _BF16 else MLA_F32, rows.data_ptr(), positions.data_ptr(),
         slots.data_ptr(), rope_base, cache.data_ptr(),
+        None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
+    if code:
+        _check(code)
+
+
+def cache_read_paged(d: MlaDims, pg: MlaPaging, cache, block_table, lengths, row_starts, rows,
+                     first_rows=None, dev_status=None, stream=None) -> None:
+    """Cached rows into rows [n, 576] (fp32 or bf16), sequence after sequence: rows
+    row_starts[b] .. are the rows of sequence b from first_rows[b] (default 0) on."""
+    lib = _paged_lib()
+    dev, i32, B, row, kind = _device(), _I32, d.batch, d.d_c + d.d_rope, rows.dtype
+    ct, cn = _ROW_TYPE.get(d.dtype), _pool_numel(d, pg)
+    n = rows.numel() // row
+    if not (_is(cache, dev, ct, cn) and _is(block_table, dev, i32, B * pg.table_stride)
+            and _is(lengths, dev, i32, B) and _is(row_starts, dev, i32, B + 1)
+            and (kind is _BF16 or kind is _F32) and _is(rows, dev, kind, n * row)
+            and (first_rows is None or _is(first_rows, dev, i32, B))
+            and (dev_status is None or _is(dev_status, dev, i32, 1))):
+        _explain(dev, cache=(cache, ct, cn), block_table=(block_table, i32, B * pg.table_stride),
+                 lengths=(lengths, i32, B), row_starts=(row_starts, i32, B + 1),
+                 rows=(rows, kind if kind is _BF16 else _F32, n * row),
+                 first_rows=(first_rows, i32, B), dev_status=(dev_status, i32, 1))
+    code = lib.mla_cache_read_paged(
+        d, pg, cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), row_starts.data_ptr(),
+        None if first_rows is None else first_rows.data_ptr(), n,
+        MLA_BF16 if kind is _BF16 else MLA_F32, rows.data_ptr(),
         None if dev_status is None else dev_status.data_ptr(), _stream_on(dev, stream))
     if code:
         _check(code)
@@ -634,7 +678,7 @@ def decode_attn_paged(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_table
     lib = _paged_lib()
     dev, io, B, dc, dr = _device(), q_abs.dtype, d.batch, d.d_c, d.d_rope
     rows = B * q_len * d.heads
-    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * (dc + dr)
+    ct, cn = _ROW_TYPE.get(d.dtype), _pool_numel(d, pg)
     if not (q_abs.get_device() == q_pe.get_device() == cache.get_device()
             == block_table.get_device() == lengths.get_device() == o_c.get_device()
             == workspace.get_device() == dev
@@ -670,19 +714,19 @@ def page_index(d: MlaDims, pg: MlaPaging, cache, block_table, first_rows, length
     rows [first_rows[b], lengths[b]) of each sequence."""
     lib = _paged_lib()
     dev, i32, B, row, pages = _device(), _I32, d.batch, d.d_c + d.d_rope, pg.num_pages
-    ct = _ROW_TYPE.get(d.dtype)
+    ct, cn = _ROW_TYPE.get(d.dtype), _pool_numel(d, pg)
     if not (cache.get_device() == block_table.get_device() == first_rows.get_device()
             == lengths.get_device() == codes.get_device() == scales.get_device() == dev
             and cache.dtype is ct and block_table.dtype is i32 and first_rows.dtype is i32
             and lengths.dtype is i32 and codes.dtype is _I8 and scales.dtype is _F32
-            and cache.numel() == pages * pg.page_size * row
+            and cache.numel() == cn
             and block_table.numel() == B * pg.table_stride and first_rows.numel() == B
             and lengths.numel() == B and codes.numel() == pages * row and scales.numel() == pages
             and cache.is_contiguous() and block_table.is_contiguous()
             and first_rows.is_contiguous() and lengths.is_contiguous() and codes.is_contiguous()
             and scales.is_contiguous()
             and (dev_status is None or _is(dev_status, dev, i32, 1))):
-        _explain(dev, cache=(cache, ct, pages * pg.page_size * row),
+        _explain(dev, cache=(cache, ct, cn),
                  block_table=(block_table, i32, B * pg.table_stride),
                  first_rows=(first_rows, i32, B), lengths=(lengths, i32, B),
                  codes=(codes, _I8, pages * row), scales=(scales, _F32, pages),
@@ -772,7 +816,7 @@ def decode_attn_sparse(d: MlaDims, pg: MlaPaging, q_abs, q_pe, cache, block_tabl
     io = _check_selection(dev, d, pg, q_abs, q_pe, block_table, lengths, codes, scales, sel_table,
                           sel_lengths, workspace, q_len, dev_status)
     rows = d.batch * q_len * d.heads
-    ct, cn = _ROW_TYPE.get(d.dtype), pg.num_pages * pg.page_size * (d.d_c + d.d_rope)
+    ct, cn = _ROW_TYPE.get(d.dtype), _pool_numel(d, pg)
     if not (_is(cache, dev, ct, cn) and _is(o_c, dev, q_abs.dtype, rows * d.d_c)
             and (lse is None or _is(lse, dev, _F32, rows))):
         _explain(dev, cache=(cache, ct, cn), o_c=(o_c, q_abs.dtype, rows * d.d_c),

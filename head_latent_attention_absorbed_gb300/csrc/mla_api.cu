@@ -18,7 +18,7 @@ void set_error(const char* fmt, ...) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-mla_status check_dims(const mla_dims* d, const char* who) {
+mla_status check_dims(const mla_dims* d, const char* who, bool paged) {
   if (!d) {
     set_error("%s: dims is NULL", who);
     return MLA_ERR_INVALID_ARG;
@@ -33,12 +33,18 @@ mla_status check_dims(const mla_dims* d, const char* who) {
               d->d_c, d->d_rope, d->d_nope, d->d_v);
     return MLA_ERR_UNSUPPORTED;
   }
-  if (d->dtype != MLA_F32 && d->dtype != MLA_BF16 && d->dtype != MLA_FP8_E4M3) {
-    set_error("%s: dtype %d is not MLA_F32, MLA_BF16 or MLA_FP8_E4M3", who, d->dtype);
+  if (d->dtype == MLA_FP4_E2M1 && !paged) {
+    set_error("%s: MLA_FP4_E2M1 is a type of the paged cache only", who);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (d->dtype != MLA_F32 && d->dtype != MLA_BF16 && d->dtype != MLA_FP8_E4M3 &&
+      d->dtype != MLA_FP4_E2M1) {
+    set_error("%s: dtype %d is not MLA_F32, MLA_BF16%s or MLA_FP8_E4M3", who, d->dtype,
+              paged ? ", MLA_FP4_E2M1" : "");
     return MLA_ERR_UNSUPPORTED;
   }
   if (d->dtype != MLA_F32 && d->heads % kHeadGroup != 0) {
-    set_error("%s: bf16 and FP8 kernels need heads to be a multiple of %d (got %d)", who, kHeadGroup,
+    set_error("%s: bf16, FP8 and 4-bit kernels need heads to be a multiple of %d (got %d)", who, kHeadGroup,
               d->heads);
     return MLA_ERR_UNSUPPORTED;
   }

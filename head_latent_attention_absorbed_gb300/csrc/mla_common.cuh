@@ -30,7 +30,8 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // ----------------------------------------------------------------- host-side status
 void set_error(const char* fmt, ...);
-mla_status check_dims(const mla_dims* d, const char* who);
+// `paged`: for a call on the paged cache, which has the 4-bit type too.
+mla_status check_dims(const mla_dims* d, const char* who, bool paged = false);
 bool aligned16(const void* p);
 mla_status launch_status(const char* who);
 

@@ -18,6 +18,7 @@
 
 #include "mla_common.cuh"
 #include "mla_paged.cuh"
+#include "mla_q4.cuh"
 #include "mla_split.cuh"
 
 namespace mla {
@@ -2101,7 +2102,8 @@ constexpr int kShareMinTiles = 5;
 // 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82.
 constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
-  return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
+  return o.paged && o.io == MLA_BF16 && (d->dtype == MLA_BF16 || d->dtype == MLA_FP8_E4M3) &&
+         g_split_parts.load() != 2 &&
          d->heads * o.q_len >= (d->dtype == MLA_BF16 ? kPairMinBf16 : kPairMinFp8);
 }
 int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
@@ -2484,7 +2486,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
                           float softmax_scale, int32_t num_splits, void* workspace,
                           size_t ws_bytes, int32_t* dev_status, SplitParams* p,
                           const PagedView* view = nullptr) {
-  mla_status st = check_dims(dims, who);
+  mla_status st = check_dims(dims, who, view != nullptr);
   if (st != MLA_OK) return st;
   if (q_len < 1 || static_cast<long long>(dims->batch) * q_len > (1ll << 30)) {
     set_error("%s: q_len=%d must be >= 1 with batch*q_len <= 2^30", who, q_len);
@@ -2587,6 +2589,7 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   if (pairs)
     return launch_split_pair(p, cache, dims->dtype == MLA_FP8_E4M3, s, who);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
+  if (dims->dtype == MLA_FP4_E2M1) return launch_split_q4(p, cache, s, who);
   if (dims->dtype == MLA_BF16) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) {
@@ -2744,7 +2747,7 @@ extern "C" mla_status mla_decode_attn(const mla_dims* dims, const void* q_abs, c
 // Checks that a paged call makes beyond prepare()'s.
 mla_status mla::check_paged(const char* who, const mla_dims* dims, const mla_paging* paging,
                             int32_t io_dtype, int32_t q_len) {
-  mla_status st = check_dims(dims, who);
+  mla_status st = check_dims(dims, who, true);
   if (st == MLA_OK) st = check_paging(paging, who);
   if (st == MLA_OK) st = check_io(dims, io_dtype, who);
   if (st != MLA_OK) return st;

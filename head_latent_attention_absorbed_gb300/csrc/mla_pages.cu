@@ -39,7 +39,7 @@ mla_status check_paging(const mla_paging* pg, const char* who) {
 
 mla_status check_io(const mla_dims* d, int32_t io_dtype, const char* who) {
   if (io_dtype != MLA_F32 && !(io_dtype == MLA_BF16 && d->dtype != MLA_F32)) {
-    set_error("%s: io_dtype %d must be MLA_F32, or MLA_BF16 with a bf16 or FP8 cache", who,
+    set_error("%s: io_dtype %d must be MLA_F32, or MLA_BF16 with a bf16, FP8 or 4-bit cache", who,
               io_dtype);
     return MLA_ERR_UNSUPPORTED;
   }
@@ -344,80 +344,6 @@ constexpr int kAppendWarps = 8;
 constexpr int kAppendEach = 4;
 constexpr int kAppendRows = kAppendWarps * kAppendEach;
 
-struct RopeTurns {
-  uint64_t t[kDr / 2];
-};
-
-// Eight values as loaded, and as fp32.
-struct Raw8bf16 {
-  uint4 q;
-  __device__ __forceinline__ void load(const __nv_bfloat16* src) {
-    q = __ldcs(reinterpret_cast<const uint4*>(src));
-  }
-  __device__ __forceinline__ void values(float* v) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
-struct Raw8f32 {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* src) {
-    a = __ldcs(reinterpret_cast<const float4*>(src));
-    b = __ldcs(reinterpret_cast<const float4*>(src + 4));
-  }
-  __device__ __forceinline__ void values(float* v) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-};
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> : Raw8bf16 {};
-template <>
-struct Raw8<float> : Raw8f32 {};
-__device__ __forceinline__ void store8(float* dst, const float* v) {
-  *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float* v) {
-  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(__nv_fp8_storage_t* dst, const float* v) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {   // nearest even, saturating at +-448
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | hi << 16;
-  }
-  *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-}
-
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* src) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(src));
-}
-__device__ __forceinline__ float2 load_pair(const float* src) {
-  return *reinterpret_cast<const float2*>(src);
-}
-__device__ __forceinline__ void store_pair(float* dst, float x, float y) {
-  *reinterpret_cast<float2*>(dst) = make_float2(x, y);
-}
-__device__ __forceinline__ void store_pair(__nv_bfloat16* dst, float x, float y) {
-  *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x, y);
-}
-__device__ __forceinline__ void store_pair(__nv_fp8_storage_t* dst, float x, float y) {
-  *reinterpret_cast<uint16_t*>(dst) =
-      __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-}
-
 template <typename In, typename Out>
 __global__ void __launch_bounds__(32 * kAppendWarps)
     append_paged_kernel(const In* __restrict__ rows, const int32_t* __restrict__ positions,
@@ -460,13 +386,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
       raw[u][i].values(v);
       store8(dst + 256 * i + 8 * lane, v);
     }
-    // half turns in [-1, 1) from the phase's top 32 bits
-    const uint64_t phase = static_cast<uint64_t>(pos[u]) * turn;
-    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-    float sn, cs;
-    sincospif(half_turns, &sn, &cs);
-    store_pair(dst + kDc + 2 * lane, pair[u].x * cs - pair[u].y * sn,
-               pair[u].x * sn + pair[u].y * cs);
+    const float2 k = rotated(pair[u], pos[u], turn);
+    store_pair(dst + kDc + 2 * lane, k.x, k.y);
   }
 }
 
@@ -884,7 +805,7 @@ extern "C" mla_status mla_cache_append_paged(const mla_dims* dims, const mla_pag
                                              const int64_t* slots, double rope_base, void* cache,
                                              int32_t* dev_status, void* stream) {
   const char* who = "mla_cache_append_paged";
-  mla_status st = check_dims(dims, who);
+  mla_status st = check_dims(dims, who, true);
   if (st == MLA_OK) st = check_paging(paging, who);
   if (st != MLA_OK) return st;
   if (num_rows < 0 || !(rope_base > 0.0) || !isfinite(rope_base)) {
@@ -892,7 +813,7 @@ extern "C" mla_status mla_cache_append_paged(const mla_dims* dims, const mla_pag
     return MLA_ERR_INVALID_ARG;
   }
   if (row_dtype != MLA_F32 && !(row_dtype == MLA_BF16 && dims->dtype != MLA_F32)) {
-    set_error("%s: row_dtype %d must be MLA_F32, or MLA_BF16 with a bf16 or FP8 cache", who,
+    set_error("%s: row_dtype %d must be MLA_F32, or MLA_BF16 with a bf16, FP8 or 4-bit cache", who,
               row_dtype);
     return MLA_ERR_UNSUPPORTED;
   }
@@ -901,12 +822,10 @@ extern "C" mla_status mla_cache_append_paged(const mla_dims* dims, const mla_pag
     set_error("%s: pointers must not be NULL, rows and cache 16-byte aligned", who);
     return MLA_ERR_INVALID_ARG;
   }
-  RopeTurns turns;
-  for (int i = 0; i < kDr / 2; ++i) {
-    const double t = pow(rope_base, -2.0 * i / kDr) / 6.283185307179586476925;
-    // the fraction of a turn per position; a base below 1 has whole turns to drop
-    turns.t[i] = static_cast<uint64_t>(ldexp(t - floor(t), 64));
-  }
+  if (dims->dtype == MLA_FP4_E2M1)
+    return append_q4(who, paging, num_rows, row_dtype == MLA_F32, rows, positions, slots, rope_base,
+                     cache, dev_status, static_cast<cudaStream_t>(stream));
+  const RopeTurns turns = rope_turns(rope_base);
   const dim3 grid((num_rows + kAppendRows - 1) / kAppendRows);
   const int64_t pool = static_cast<int64_t>(paging->num_pages) * paging->page_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -935,7 +854,7 @@ extern "C" mla_status mla_page_index(const mla_dims* dims, const mla_paging* pag
                                      const int32_t* lengths, int8_t* codes, float* scales,
                                      int32_t* dev_status, void* stream) {
   const char* who = "mla_page_index";
-  mla_status st = check_dims(dims, who);
+  mla_status st = check_dims(dims, who, true);
   if (st == MLA_OK) st = check_paging(paging, who);
   if (st != MLA_OK) return st;
   if (max_new < 1) {
@@ -953,6 +872,9 @@ extern "C" mla_status mla_page_index(const mla_dims* dims, const mla_paging* pag
   const long long most = (static_cast<long long>(max_new) + paging->page_size - 2) / paging->page_size + 1;
   const int touched = static_cast<int>(most < paging->table_stride ? most : paging->table_stride);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dims->dtype == MLA_FP4_E2M1)
+    return page_index_q4(who, paging, dims->batch, max_new, touched, cache, block_table, first_rows,
+                         lengths, codes, scales, dev_status, s);
   if (dims->dtype == MLA_F32) return launch_index<float>(p, dims->batch, touched, s, who);
   if (dims->dtype == MLA_BF16) return launch_index<__nv_bfloat16>(p, dims->batch, touched, s, who);
   return launch_index<__nv_fp8_storage_t>(p, dims->batch, touched, s, who);

@@ -1,0 +1,403 @@
+// Rows into a 4-bit pool and out of any: the 4-bit form of mla_cache_append_paged,
+// mla_cache_read_paged for every pool, and the page index over 4-bit pages.
+#include "mla_q4.cuh"
+
+namespace mla {
+namespace {
+
+// ------------------------------------------------------------- rows into slots
+// Bound by HBM: 576 values read, 400 bytes written per row.  A warp moves a row, as in
+// append_paged_kernel; two lanes share a block of 16 latents, so its largest magnitude is one
+// exchange, and the exponents of a row's blocks are gathered into words over half a warp.
+constexpr int kWarps = 8, kEach = 4, kRows = kWarps * kEach;
+
+// e + 8 of the block whose largest magnitude has these fp32 bits (NaN counts above infinity:
+// both take the largest e).
+__device__ __forceinline__ uint32_t q4_exponent(uint32_t top) {
+  const int e = static_cast<int>(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 2 : 1);
+  return static_cast<uint32_t>(min(max(e, kQ4ExpMin), kQ4ExpMax) - kQ4ExpMin);
+}
+
+template <typename In>
+__global__ void __launch_bounds__(32 * kWarps)
+    append_q4_kernel(const In* __restrict__ rows, const int32_t* __restrict__ positions,
+                     const int64_t* __restrict__ slots, uint8_t* __restrict__ pool,
+                     const __grid_constant__ RopeTurns turns, int32_t* status, int n,
+                     int64_t pool_rows, int page_shift) {
+  const int lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * kRows + (threadIdx.x >> 5);
+  int64_t slot[kEach];
+  int pos[kEach];
+  Raw8<In> raw[kEach][2];
+  float2 pair[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int r = r0 + u * kWarps;
+    slot[u] = -1;
+    pos[u] = 0;
+    if (r < n) {
+      const In* row = rows + static_cast<size_t>(r) * kRow;
+      slot[u] = slots[r];
+      pos[u] = positions[r];
+      raw[u][0].load(row + 8 * lane);
+      raw[u][1].load(row + 256 + 8 * lane);
+      pair[u] = load_pair(row + kDc + 2 * lane);
+    }
+  }
+  const uint64_t turn = turns.t[lane];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    if (slot[u] < 0 || slot[u] >= pool_rows || pos[u] < 0) {
+      if (lane == 0 && slot[u] != -1)
+        report(status, slot[u] < 0 || slot[u] >= pool_rows ? MLA_DEV_PAGE_OUT_OF_RANGE
+                                                           : MLA_DEV_LENGTH_OUT_OF_RANGE);
+      continue;
+    }
+    const Q4Page<uint8_t> page(pool, static_cast<int>(slot[u] >> page_shift), page_shift);
+    const int r = static_cast<int>(slot[u]) & ((1 << page_shift) - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[8];
+      raw[u][i].values(v);
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const uint32_t e8 = q4_exponent(top);
+      const float inv = __uint_as_float((127 - kQ4ExpMin - e8) << 23);   // 2^-e: exact products
+      uint32_t code = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)   // to nearest even, saturating at 6
+        code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
+                    make_float2(v[2 * k] * inv, v[2 * k + 1] * inv), __NV_E2M1,
+                    cudaRoundNearest)) << (8 * k);
+      reinterpret_cast<uint32_t*>(page.codes + r * kQ4CodeBytes)[32 * i + lane] = code;
+      uint32_t word = (lane & 1) ? 0u : e8 << (4 * ((lane >> 1) & 7));
+#pragma unroll
+      for (int off = 2; off < 16; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
+      if ((lane & 15) == 0)
+        reinterpret_cast<uint32_t*>(page.exps + r * kQ4ExpBytes)[2 * i + (lane >> 4)] = word;
+    }
+    const float2 k = rotated(pair[u], pos[u], turn);
+    *reinterpret_cast<uint32_t*>(page.keys + q4_key_at(r, lane)) = pack_bf16(k.x, k.y);
+  }
+}
+
+// ------------------------------------------------------------- rows out of pages
+// Bound by HBM: a row read, 576 values written.  A warp takes kEach consecutive rows of the
+// packed output, whose sequence its lanes find together (32 steps of the row starts a round).
+struct ReadParams {
+  const void* pool;
+  const int32_t *table, *lengths, *starts, *first;   // first may be NULL: zeros
+  int32_t* status;
+  int B, num_rows, page_shift, table_stride, num_pages;
+};
+
+// Last index i in [0, n) with starts[i] <= x, or 0; by a whole warp.
+__device__ __forceinline__ int warp_search(const int32_t* starts, int n, int x, int lane) {
+  int lo = 0, size = n;   // the answer lies in [lo, lo + size)
+  while (size > 1) {
+    const int step = (size + 31) / 32;
+    const int at = lo + lane * step;
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane * step < size && starts[min(at, n)] <= x);
+    const int k = hit ? 31 - __clz(hit) : 0;
+    size = min(step, size - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+template <typename T>
+struct RowLane {   // of a pool of whole rows
+  Raw8<T> raw[2];
+  float2 key;
+  __device__ __forceinline__ void load(const void* pool, int id, int r, int page_shift, int lane) {
+    const T* row = static_cast<const T*>(pool) + ((static_cast<size_t>(id) << page_shift) + r) * kRow;
+    raw[0].load(row + 8 * lane);
+    raw[1].load(row + 256 + 8 * lane);
+    key = load_pair(row + kDc + 2 * lane);
+  }
+  __device__ __forceinline__ void values(int i, int, float* v) const { raw[i].values(v); }
+  __device__ __forceinline__ float2 pair() const { return key; }
+};
+template <>
+struct RowLane<__nv_fp8_storage_t> {
+  uint2 raw[2];
+  uint16_t key;
+  __device__ __forceinline__ void load(const void* pool, int id, int r, int page_shift, int lane) {
+    const uint8_t* row =
+        static_cast<const uint8_t*>(pool) + ((static_cast<size_t>(id) << page_shift) + r) * kRow;
+    raw[0] = __ldcs(reinterpret_cast<const uint2*>(row + 8 * lane));
+    raw[1] = __ldcs(reinterpret_cast<const uint2*>(row + 256 + 8 * lane));
+    key = *reinterpret_cast<const uint16_t*>(row + kDc + 2 * lane);
+  }
+  static __device__ __forceinline__ float2 two(uint32_t v) {
+    return __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3)));
+  }
+  __device__ __forceinline__ void values(int i, int, float* v) const {
+    const uint32_t w[2] = {raw[i].x, raw[i].y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = two(w[k >> 1] >> (16 * (k & 1)));
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ float2 pair() const { return two(key); }
+};
+struct FourBit {};
+template <>
+struct RowLane<FourBit> : Q4Lane {
+  __device__ __forceinline__ void load(const void* pool, int id, int r, int page_shift, int lane) {
+    Q4Lane::load(Q4Page<const uint8_t>(static_cast<const uint8_t*>(pool), id, page_shift), r, lane);
+  }
+};
+
+template <typename T, typename Out>
+__global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const ReadParams p, Out* rows) {
+  const int lane = threadIdx.x & 31;
+  const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kEach;
+  const int end = min(p.starts[p.B], p.num_rows);
+  if (t0 >= end) return;
+  int b = warp_search(p.starts, p.B, t0, lane);
+  int next = p.starts[b + 1], start = p.starts[b];
+  RowLane<T> in[kEach];
+  bool have[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int t = t0 + u;
+    have[u] = false;
+    if (t >= end) continue;
+    if (t >= next) {   // empty sequences are passed over
+      b = warp_search(p.starts, p.B, t, lane);
+      start = p.starts[b];
+      next = p.starts[b + 1];
+    }
+    const long long pos = static_cast<long long>(t) - start + (p.first ? p.first[b] : 0);
+    if (pos < 0 || pos >= p.lengths[b] ||
+        pos >= static_cast<long long>(p.table_stride) << p.page_shift) {
+      if (lane == 0) report(p.status, MLA_DEV_LENGTH_OUT_OF_RANGE);
+      continue;
+    }
+    const int id = p.table[static_cast<size_t>(b) * p.table_stride + (pos >> p.page_shift)];
+    if (id < 0 || id >= p.num_pages) {
+      if (lane == 0) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+      continue;
+    }
+    have[u] = true;
+    in[u].load(p.pool, id, static_cast<int>(pos) & ((1 << p.page_shift) - 1), p.page_shift, lane);
+  }
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    if (t0 + u >= end) break;
+    Out* row = rows + static_cast<size_t>(t0 + u) * kRow;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float2 k = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (have[u]) in[u].values(i, lane, v);
+      store8(row + 256 * i + 8 * lane, v);
+    }
+    if (have[u]) k = in[u].pair();
+    store_pair(row + kDc + 2 * lane, k.x, k.y);
+  }
+}
+
+// ------------------------------------------------------------- the page index
+// page_index_kernel's definition over 4-bit pages; a CTA per touched page, which reads it
+// twice (its largest magnitude, then the sums; the second time from L1 or L2).
+// A latent is a multiple of 2^-9 and at most 384, so the maximum is a maximum of exact values.
+constexpr float kQ4Tiny = 1e-30f;
+__global__ void __launch_bounds__(32 * kWarps)
+    page_index_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ table,
+                         const int32_t* __restrict__ first_rows, const int32_t* __restrict__ lengths,
+                         int8_t* codes, float* scales, int32_t* status, int page_shift,
+                         int table_stride, int num_pages, int max_new, int most) {
+  __shared__ float tops[kWarps];
+  __shared__ int sums[kWarps][kRow];
+  __shared__ int peaks[kWarps];
+  const int b = static_cast<int>(blockIdx.x / most), jj = static_cast<int>(blockIdx.x % most);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int first = first_rows[b], len = lengths[b];
+  const bool bad = first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
+  if (tid == 0 && jj == 0 && (bad || static_cast<long long>(len) - first > max_new))
+    report(status, MLA_DEV_LENGTH_OUT_OF_RANGE);
+  const long long j = static_cast<long long>(first >> page_shift) + jj;
+  if (bad || first >= len || (j << page_shift) >= len) return;
+  const int n = static_cast<int>(min(1ll << page_shift, len - (j << page_shift)));
+  const int id = table[static_cast<size_t>(b) * table_stride + j];
+  if (id < 0 || id >= num_pages) {
+    if (tid == 0) report(status, MLA_DEV_PAGE_OUT_OF_RANGE);
+    return;
+  }
+  const Q4Page<const uint8_t> page(pool, id, page_shift);
+  float top = 0.f;
+  for (int r = warp; r < n; r += kWarps) {
+    Q4Lane x;
+    x.load(page, r, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[8];
+      x.values(i, lane, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
+    }
+    const float2 k = x.pair();
+    top = fmaxf(top, fmaxf(fabsf(k.x), fabsf(k.y)));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+  int ex = 0;
+  frexpf(top, &ex);   // top = m 2^ex, m in [0.5, 1)
+  const float unit = ldexpf(1.f, 20 - ex);
+  const bool live = top >= kQ4Tiny && top <= 3.0e38f;
+  constexpr float kMagic = 12582912.f;   // 1.5 2^23: the sum's low bits are the rounded integer
+  int sum[18];
+#pragma unroll
+  for (int i = 0; i < 18; ++i) sum[i] = 0;
+  auto add = [&](int i, float v) {
+    sum[i] += static_cast<int>(__float_as_uint(fmaf(v, unit, kMagic)) - __float_as_uint(kMagic));
+  };
+  for (int r = warp; r < n; r += kWarps) {
+    Q4Lane x;
+    x.load(page, r, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[8];
+      x.values(i, lane, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(8 * i + k, v[k]);
+    }
+    const float2 k = x.pair();
+    add(16, k.x);
+    add(17, k.y);
+  }
+#pragma unroll
+  for (int i = 0; i < 18; ++i)
+    sums[warp][i < 16 ? 256 * (i >> 3) + 8 * lane + (i & 7) : kDc + 2 * lane + (i & 1)] = sum[i];
+  __syncthreads();
+  int total[3] = {0, 0, 0}, peak = 0;   // of columns tid, tid + 256 and tid + 512
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = tid + 32 * kWarps * i;
+    if (c < kRow)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) total[i] += sums[w][c];
+    peak = max(peak, abs(total[i]));
+  }
+  peak = __reduce_max_sync(0xffffffffu, peak);
+  if (lane == 0) peaks[warp] = peak;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) peak = max(peak, peaks[w]);
+  const bool good = live && peak > 0;
+  const float pf = static_cast<float>(peak), inv = good ? __frcp_rn(pf) * 127.f : 0.f;
+  int8_t* out = codes + static_cast<size_t>(id) * kRow;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = tid + 32 * kWarps * i;
+    if (c < kRow)
+      out[c] = good ? static_cast<int8_t>(__float2int_rn(static_cast<float>(total[i]) * inv)) : 0;
+  }
+  if (tid == 0)
+    scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
+}
+
+template <typename T>
+void launch_read(const ReadParams& p, int32_t out_dtype, void* rows, cudaStream_t s) {
+  const dim3 grid((p.num_rows + kRows - 1) / kRows), block(32 * kWarps);
+  if (out_dtype == MLA_F32)
+    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<float*>(rows));
+  else
+    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<__nv_bfloat16*>(rows));
+}
+
+}  // namespace
+
+mla_status append_q4(const char* who, const mla_paging* paging, int num_rows, bool f32_rows,
+                     const void* rows, const int32_t* positions, const int64_t* slots,
+                     double rope_base, void* cache, int32_t* status, cudaStream_t s) {
+  const dim3 grid((num_rows + kRows - 1) / kRows);
+  const int64_t pool = static_cast<int64_t>(paging->num_pages) * paging->page_size;
+  auto go = [&](auto* in) {
+    append_q4_kernel<<<grid, 32 * kWarps, 0, s>>>(in, positions, slots,
+                                                  static_cast<uint8_t*>(cache), rope_turns(rope_base),
+                                                  status, num_rows, pool, page_shift_of(paging));
+  };
+  if (f32_rows)
+    go(static_cast<const float*>(rows));
+  else
+    go(static_cast<const __nv_bfloat16*>(rows));
+  return launch_status(who);
+}
+
+mla_status page_index_q4(const char* who, const mla_paging* paging, int batch, int max_new, int most,
+                         const void* cache, const int32_t* table, const int32_t* first_rows,
+                         const int32_t* lengths, int8_t* codes, float* scales, int32_t* status,
+                         cudaStream_t s) {
+  const long long items = static_cast<long long>(batch) * most;
+  if (items >= (1ll << 31)) {
+    set_error("%s: batch=%d requests of up to %d touched pages exceed 2^31", who, batch, most);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  page_index_q4_kernel<<<static_cast<unsigned>(items), 32 * kWarps, 0, s>>>(
+      static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes, scales, status,
+      page_shift_of(paging), paging->table_stride, paging->num_pages, max_new, most);
+  return launch_status(who);
+}
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" size_t mla_pool_bytes(const mla_dims* dims, const mla_paging* paging) {
+  const char* who = "mla_pool_bytes";
+  if (check_dims(dims, who, true) != MLA_OK || check_paging(paging, who) != MLA_OK) return 0;
+  const size_t row = dims->dtype == MLA_FP4_E2M1   ? kQ4RowBytes
+                     : dims->dtype == MLA_FP8_E4M3 ? kRow
+                     : dims->dtype == MLA_BF16     ? 2 * kRow
+                                                   : 4 * kRow;
+  return static_cast<size_t>(paging->num_pages) * paging->page_size * row;
+}
+
+extern "C" mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
+                                           const void* cache, const int32_t* block_table,
+                                           const int32_t* lengths, const int32_t* row_starts,
+                                           const int32_t* first_rows, int32_t num_rows,
+                                           int32_t row_dtype, void* rows, int32_t* dev_status,
+                                           void* stream) {
+  const char* who = "mla_cache_read_paged";
+  mla_status st = check_dims(dims, who, true);
+  if (st == MLA_OK) st = check_paging(paging, who);
+  if (st != MLA_OK) return st;
+  if (num_rows < 0) {
+    set_error("%s: num_rows=%d must be >= 0", who, num_rows);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (row_dtype != MLA_F32 && row_dtype != MLA_BF16) {
+    set_error("%s: row_dtype %d must be MLA_F32 or MLA_BF16", who, row_dtype);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (num_rows == 0) return MLA_OK;
+  if (!cache || !block_table || !lengths || !row_starts || !rows || !aligned16(cache) ||
+      !aligned16(rows)) {
+    set_error("%s: pointers must not be NULL, cache and rows 16-byte aligned", who);
+    return MLA_ERR_INVALID_ARG;
+  }
+  const ReadParams p{cache, block_table, lengths, row_starts, first_rows, dev_status,
+                     dims->batch, num_rows, page_shift_of(paging), paging->table_stride,
+                     paging->num_pages};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (dims->dtype) {
+    case MLA_F32: launch_read<float>(p, row_dtype, rows, s); break;
+    case MLA_BF16: launch_read<__nv_bfloat16>(p, row_dtype, rows, s); break;
+    case MLA_FP8_E4M3: launch_read<__nv_fp8_storage_t>(p, row_dtype, rows, s); break;
+    default: launch_read<FourBit>(p, row_dtype, rows, s); break;
+  }
+  return launch_status(who);
+}

@@ -1,0 +1,97 @@
+// The 4-bit latent cache (MLA_FP4_E2M1): how a page holds its rows, and one lane's share
+// of a row in and out of that form.
+//
+// A row's 512 latents are E2M1 codes (sign, two exponent bits, one mantissa bit: 0, 1/2, 1,
+// 3/2, 2, 3, 4, 6) times a power of two 2^e per 16 of them, -8 <= e <= 6; its 64 rotated key
+// values are bf16.  The range of e is chosen so that every latent value is an E4M3 number
+// (6 2^6 = 384, 2^-1 2^-8 = 2^-9, E4M3's smallest): the tensor cores' 8-bit products take a
+// row without another rounding.  e is the smallest with which the block's largest magnitude
+// is at most 7 2^e: what lies above 6 2^e is off by no more than 2^e, as between 4 and 6.
+// (Root-mean-square error of N(0, 1) values 0.110 of their size; 0.113 with 6 2^e as the
+// limit, 0.118 with 8 2^e; 0.112 with one e per 32.)
+//
+// A page of R rows is three planes, 400 R bytes in all, so that the rows of a tile are three
+// contiguous copies:
+//   codes  [R][256]  byte i of a row: values 2 i (low four bits) and 2 i + 1
+//   keys   [R][128]  16-byte piece c of row r stands at piece c ^ (r & 7): as the tensor core
+//                    wants it in shared memory (128-byte swizzle)
+//   exps   [R][16]   byte i: e + 8 of blocks 2 i (low four bits) and 2 i + 1
+#pragma once
+
+#include <cuda_fp4.h>
+
+#include "mla_paged.cuh"
+#include "mla_split.cuh"
+
+namespace mla {
+
+constexpr int kQ4Block = 16;                       // values that share an exponent
+constexpr int kQ4CodeBytes = kDc / 2;              // 256
+constexpr int kQ4KeyBytes = 2 * kDr;               // 128
+constexpr int kQ4ExpBytes = kDc / kQ4Block / 2;    // 16
+constexpr int kQ4RowBytes = kQ4CodeBytes + kQ4KeyBytes + kQ4ExpBytes;   // 400
+constexpr int kQ4ExpMin = -8, kQ4ExpMax = 6;
+
+// The planes of page `id` of a pool (const or not).
+template <typename Byte>
+struct Q4Page {
+  Byte *codes, *keys, *exps;
+  __device__ __forceinline__ Q4Page(Byte* pool, int id, int page_shift) {
+    codes = pool + (static_cast<size_t>(id) << page_shift) * kQ4RowBytes;
+    keys = codes + (static_cast<size_t>(kQ4CodeBytes) << page_shift);
+    exps = keys + (static_cast<size_t>(kQ4KeyBytes) << page_shift);
+  }
+};
+
+// Byte offset of key pair `pair` of row r in the keys' plane.
+__device__ __forceinline__ uint32_t q4_key_at(int r, int pair) {
+  return static_cast<uint32_t>(r * kQ4KeyBytes + ((((pair >> 2) ^ r) & 7) << 4) + ((pair & 3) << 2));
+}
+
+// 2^e for the four bits that hold e + 8 (15 is never written; it reads as 14 does).
+__device__ __forceinline__ float q4_unit(uint32_t bits) {
+  return __uint_as_float((min(bits & 15u, 14u) + 127 + kQ4ExpMin) << 23);
+}
+
+// Eight codes as loaded, to values in units of 2^e.
+__device__ __forceinline__ void q4_values(uint32_t codes, float unit, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
+        static_cast<__nv_fp4x2_storage_t>(codes >> (8 * i)), __NV_E2M1);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x * unit;
+    v[2 * i + 1] = f.y * unit;
+  }
+}
+
+// A lane's values of one row (8 l .., 256 + 8 l .. and the key pair l) as loaded.
+struct Q4Lane {
+  uint32_t code[2], key;
+  uint8_t exp[2];
+  __device__ __forceinline__ void load(const Q4Page<const uint8_t>& page, int r, int lane) {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(page.codes + r * kQ4CodeBytes);
+    code[0] = c[lane];
+    code[1] = c[32 + lane];
+    exp[0] = page.exps[r * kQ4ExpBytes + (lane >> 2)];
+    exp[1] = page.exps[r * kQ4ExpBytes + 8 + (lane >> 2)];
+    key = *reinterpret_cast<const uint32_t*>(page.keys + q4_key_at(r, lane));
+  }
+  __device__ __forceinline__ void zero() {
+    code[0] = code[1] = key = 0;
+    exp[0] = exp[1] = 0;
+  }
+  // Latents 8 l .. (i = 0) or 256 + 8 l .. (i = 1).
+  __device__ __forceinline__ void values(int i, int lane, float* v) const {
+    q4_values(code[i], q4_unit(exp[i] >> (lane & 2 ? 4 : 0)), v);
+  }
+  __device__ __forceinline__ float2 pair() const {
+    return make_float2(__uint_as_float(key << 16), __uint_as_float(key & 0xffff0000u));
+  }
+};
+
+// The split over a 4-bit pool (mla_q4attn.cu).
+mla_status launch_split_q4(const SplitParams& p, const void* cache, cudaStream_t stream,
+                           const char* who);
+
+}  // namespace mla

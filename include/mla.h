@@ -76,7 +76,12 @@ typedef enum mla_status {
   MLA_ERR_CUDA = 4           /* a CUDA runtime call or kernel launch failed */
 } mla_status;
 
-typedef enum mla_dtype { MLA_F32 = 0, MLA_BF16 = 1, MLA_FP8_E4M3 = 2 } mla_dtype;
+typedef enum mla_dtype {
+  MLA_F32 = 0,
+  MLA_BF16 = 1,
+  MLA_FP8_E4M3 = 2,
+  MLA_FP4_E2M1 = 3   /* the paged cache only: see "4-bit pools" */
+} mla_dtype;
 
 /* Problem sizes shared by the three calls. */
 typedef struct mla_dims {
@@ -465,11 +470,28 @@ mla_status mla_decode_step_multi(const mla_dims* dims, int32_t q_len, const void
  * before it has finished writing, except the attention calls, which write only their
  * outputs and workspace.
  */
+/*
+ * 4-bit pools (MLA_FP4_E2M1).  The paged calls below take a pool whose latents are kept in
+ * four bits; the calls on a dense cache do not.  A row's d_c latents are E2M1 numbers (0,
+ * 1/2, 1, 3/2, 2, 3, 4, 6, with a sign) times a power of two 2^e per 16 consecutive values,
+ * -8 <= e <= 6, its d_rope rotated key values are bf16: 400 bytes, against 576 in E4M3 and
+ * 1152 in bf16.  As an E4M3 cache, it has no scale beyond that: magnitudes above 384
+ * saturate, and below 2^-8 a block's values are multiples of 2^-9.  (A cache of another
+ * magnitude is scaled by the caller, in W_UK and W_UV.)  Every latent value that a pool can
+ * hold is an E4M3 number.  mla_cache_append_paged quantises rows into it,
+ * mla_cache_read_paged reads them back, and the attention, index and selection calls take
+ * those values as the cache's.
+ * The pool is num_pages * page_size * 400 bytes (mla_pool_bytes), 16-byte aligned; where a
+ * page keeps which bit is private to the library.  A page of zero bytes holds rows of zeros.
+ */
 typedef struct mla_paging {
   int32_t page_size;      /* rows per page: 16, 32, 64, 128 or 256 */
   int32_t num_pages;      /* pages in the pool                     */
   int32_t table_stride;   /* block-table entries per sequence      */
 } mla_paging;
+
+/* Bytes of a pool of these pages, in the dims' type; 0: invalid arguments. */
+size_t mla_pool_bytes(const mla_dims* dims, const mla_paging* paging);
 
 /*
  * mla_pages_extend -- block tables and slot maps of one step, built on the GPU.
@@ -535,10 +557,14 @@ mla_status mla_pages_release(int32_t batch, const mla_paging* paging, const int3
  *  mla_cache_append's: adjacent pairs, angle positions[t] rope_base^(-2i/d_rope),
  *  reduced to a fraction of a turn in 64-bit fixed point.)  fp32 arithmetic;
  * each value is rounded once to the cache's type (MLA_FP8_E4M3: to nearest even,
- * saturating at +-448).
+ * saturating at +-448).  MLA_FP4_E2M1: each block of 16 latents takes the smallest e in
+ * [-8, 6] with which its largest magnitude is at most 7 2^e, and each value x the E2M1
+ * number nearest to x 2^-e (ties to the even code; beyond 6 it is 6), so that no value
+ * within +-448 is off by more than 2^e; a block with an infinity or a NaN takes e = 6, and
+ * the NaN becomes 384.
  *
- * rows [num_rows, d_c + d_rope] row_dtype: MLA_F32, or MLA_BF16 with a bf16 or
- * FP8 cache; positions [num_rows] int32; slots [num_rows] int64 (both as
+ * rows [num_rows, d_c + d_rope] row_dtype: MLA_F32, or MLA_BF16 with a bf16,
+ * FP8 or 4-bit cache; positions [num_rows] int32; slots [num_rows] int64 (both as
  * mla_pages_extend writes them).  slots[t] = -1: no row.  Any other slot outside
  * the pool sets MLA_DEV_PAGE_OUT_OF_RANGE, a negative position
  * MLA_DEV_LENGTH_OUT_OF_RANGE; such a row is not written.  A slot named twice
@@ -550,6 +576,29 @@ mla_status mla_cache_append_paged(const mla_dims* dims, const mla_paging* paging
                                   const int32_t* positions, const int64_t* slots,
                                   double rope_base, void* cache, int32_t* dev_status,
                                   void* stream);
+
+/*
+ * mla_cache_read_paged -- cached rows as one packed block of rows.
+ *
+ *   rows[t, :] = row first_rows[b] + (t - row_starts[b]) of sequence b, for
+ *                row_starts[b] <= t < row_starts[b + 1]
+ * -- what a prefill over a cached prefix, or a copy into another pool, needs; the key as it
+ * is cached (rotated).  Each value is the cache's, rounded once to row_dtype (exact for
+ * MLA_F32, and for MLA_BF16 from a bf16, FP8 or 4-bit pool).
+ *
+ * row_starts [B + 1] int32, ascending from row_starts[0] = 0; first_rows [B] int32, or NULL:
+ * from each sequence's first row; lengths [B] int32: rows of each sequence; num_rows: rows
+ * that `rows` has room for, of which those from row_starts[B] on are left as they were.  A
+ * row before a sequence's first or past its length (MLA_DEV_LENGTH_OUT_OF_RANGE), or in a
+ * page outside the pool (MLA_DEV_PAGE_OUT_OF_RANGE), is zeros.  Any pool type; row_dtype
+ * MLA_F32 or MLA_BF16.  num_rows = 0 does nothing.
+ */
+mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
+                                const void* cache, const int32_t* block_table,
+                                const int32_t* lengths, const int32_t* row_starts,
+                                const int32_t* first_rows, int32_t num_rows,
+                                int32_t row_dtype, void* rows, int32_t* dev_status,
+                                void* stream);
 
 /*
  * mla_decode_attn_paged -- mla_decode_attn_multi over a paged cache.
@@ -564,7 +613,7 @@ mla_status mla_cache_append_paged(const mla_dims* dims, const mla_paging* paging
  *   MLA_F32   as in the dense calls (every cache type).  With a bf16 cache the
  *             query and P enter the tensor cores as hi + lo bf16 pairs at every
  *             head count.
- *   MLA_BF16  bf16 queries and outputs (bf16 and FP8 caches), as a serving
+ *   MLA_BF16  bf16 queries and outputs (bf16, FP8 and 4-bit caches), as a serving
  *             engine keeps them.  The query enters as it is.  From 32 (bf16 cache) or
  *             48 (FP8) query rows heads * q_len per sequence on, two CTAs on a pair of
  *             SMs take up to 128 of them, and P is one bf16 part (at most 2^-8
