@@ -2294,7 +2294,8 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   // that full sequences would need, so that shares may shrink with the lengths.
   const long long sets = pairs ? d->batch / opts.q_len : d->batch;
   const long long ctas = pairs ? 2ll * pair_groups(d->heads * opts.q_len) : groups;
-  if (opts.paged && !opts.late && (pairs || d->dtype == MLA_FP8_E4M3) && requested <= 0 &&
+  if (opts.paged && !opts.late &&
+      (pairs || d->dtype == MLA_FP8_E4M3 || d->dtype == MLA_FP4_E2M1) && requested <= 0 &&
       form != 2 && sets <= kShareSets && ctas <= sms) {
     const long long seq = (S + kTileRows - 1) / kTileRows, runs = sms / ctas;
     const long long each = (sets * seq + runs - 1) / runs, half = (each + 1) / 2;
@@ -2342,13 +2343,13 @@ int chunk_rows(const mla_dims* d, int requested, int* splits_out, const PlanOpts
   return pl.chunk;
 }
 
-// Partial outputs, their log-sum-exps, (FP8 cache) the query images and (paged) the
+// Partial outputs, their log-sum-exps, (FP8 and 4-bit caches) the query images and (paged) the
 // numbers of partials.
 size_t workspace_bytes(const mla_dims* d, int splits, bool paged = false) {
   const size_t n = size_t(d->batch) * splits * d->heads;
   const size_t o_bytes = (n * kDc * sizeof(float) + 255) / 256 * 256;
   const size_t lse_bytes = (n * sizeof(float) + 255) / 256 * 256;
-  const size_t img = d->dtype == MLA_FP8_E4M3
+  const size_t img = d->dtype == MLA_FP8_E4M3 || d->dtype == MLA_FP4_E2M1
                          ? (size_t(d->batch) * (d->heads / kHeadGroup) * kFp8QImage + 255) / 256 * 256
                          : 0;
   const size_t pieces = paged && d->dtype != MLA_F32
@@ -2528,7 +2529,7 @@ static mla_status prepare(const char* who, const mla_dims* dims, int q_len, cons
   const size_t n = size_t(dims->batch) * splits * dims->heads;
   p->part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                          (n * kDc * sizeof(float) + 255) / 256 * 256);
-  p->q_img = dims->dtype == MLA_FP8_E4M3
+  p->q_img = dims->dtype == MLA_FP8_E4M3 || dims->dtype == MLA_FP4_E2M1
                  ? reinterpret_cast<uint8_t*>(p->part_lse) + (n * sizeof(float) + 255) / 256 * 256
                  : nullptr;
   p->status = dev_status;
@@ -2589,7 +2590,7 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
   if (pairs)
     return launch_split_pair(p, cache, dims->dtype == MLA_FP8_E4M3, s, who);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
-  if (dims->dtype == MLA_FP4_E2M1) return launch_split_q4(p, cache, s, who);
+  if (dims->dtype == MLA_FP4_E2M1) return launch_split_q4(p, s, who);
   if (dims->dtype == MLA_BF16) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) {
@@ -2861,13 +2862,14 @@ mla_status mla::attn_queries(const char* who, const mla_dims* dims, const mla_pa
                              int32_t io_dtype, const void* q_abs, const void* q_pe,
                              const int32_t* lengths, int32_t num_splits, void* workspace,
                              size_t ws_bytes, void* stream) {
-  if (dims->dtype != MLA_FP8_E4M3) return MLA_OK;
+  if (dims->dtype != MLA_FP8_E4M3 && dims->dtype != MLA_FP4_E2M1) return MLA_OK;
   const PagedView view{paging, lengths, io_dtype, true};   // the table is not read here
   SplitParams p;
   const mla_status st = prepare(who, dims, 1, q_abs, q_pe, nullptr, lengths, 1.f, num_splits,
                                 workspace, ws_bytes, nullptr, &p, &view);
   if (st != MLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dims->dtype == MLA_FP4_E2M1) return launch_q4_queries(p, s, who);
   return pair_form(dims, plan_opts(dims, 1, &view)) ? launch_pair_queries(p, s, who)
                                                     : launch_fp8_queries(p, s, who);
 }

@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t q4_key_at(int r, int pair) {
 
 // 2^e for the four bits that hold e + 8 (15 is never written; it reads as 14 does).
 __device__ __forceinline__ float q4_unit(uint32_t bits) {
-  return __uint_as_float((min(bits & 15u, 14u) + 127 + kQ4ExpMin) << 23);
+  return __uint_as_float((min(bits & 15u, 14u) + static_cast<uint32_t>(127 + kQ4ExpMin)) << 23);
 }
 
 // Eight codes as loaded, to values in units of 2^e.
@@ -90,8 +90,9 @@ struct Q4Lane {
   }
 };
 
-// The split over a 4-bit pool (mla_q4attn.cu).
-mla_status launch_split_q4(const SplitParams& p, const void* cache, cudaStream_t stream,
-                           const char* who);
+// The split over a 4-bit pool (mla_q4attn.cu), and the kernel that makes the queries' images,
+// which it runs first unless p.late is set.
+mla_status launch_split_q4(const SplitParams& p, cudaStream_t stream, const char* who);
+mla_status launch_q4_queries(const SplitParams& p, cudaStream_t stream, const char* who);
 
 }  // namespace mla

@@ -1,101 +1,808 @@
-// The split kernel over a 4-bit pool.
+// The split kernel over a 4-bit pool, 16 heads per CTA.
+//
+// Per head the score of row t is q_abs . c_t + q_pe . k_t over sqrt(d_h + d_R), an online
+// softmax over the chunk's rows, and the normalised latent output with its log-sum-exp
+// ("Multi-Head Latent Attention" 3.3, 3.6).  c_t are the pool's values: E2M1 codes times a
+// power of two per 16, each of them an E4M3 number (mla_q4.cuh).
+//
+// So a tile of 128 rows (50 KB) is brought into shared memory as it is stored, and its codes
+// are turned into E4M3 bytes there, once, by warps of their own; both products then run on
+// the tensor cores as in the E4M3 cache's kernel (kind::f8f6f4, fp32 accumulators), and the
+// keys, stored as the tensor core wants them, as kind::f16:
+//   scores  S[128 rows x 16 parts] = C[128 x 512] . Q^T,  Sk[128 x 16] = K[128 x 64] . Qk^T
+//   output  O^T[128 latent x 48] += C^T[128 x 128 rows] . P^T   per 128-column block
+// A bf16 query is two E4M3 parts (weights 1, 1/16; exact to 2^-21 of the head's largest
+// value) in units of a power of two per head, an fp32 one four (and its key part a bf16 hi
+// and lo); P is three parts (weights 1, 1/16, 1/256).
+//
+// From codes to E4M3: a byte permute looks the eight magnitudes of a block's exponent up in
+// two registers, four codes at a time (the selector is the codes themselves), and the signs
+// are put on by another: nine operations for eight values, no conversion (which would run at
+// an eighth of the rate) and no multiplication.
+//
+// Warp roles (480 threads, one CTA per SM):
+//   warps 0-7    softmax (one tile row per thread, heads 0-7 in warps 0-3, 8-15 in 4-7),
+//                P, epilogue
+//   warp 8       copies of rows (and TMEM allocation)
+//   warp 9       score MMAs of each tile (20 instructions)
+//   warp 10      the query image's copy, then the PV MMAs of each tile (16)
+//   warps 11-14  codes to E4M3
 #include "mla_q4.cuh"
 
 namespace mla {
 namespace {
 
-// One CTA per (head, chunk, sequence), eight warps, a row per warp at a time: the form of
-// split_f32_paged_kernel with a lane's values of a row as Q4Lane holds them.
-constexpr int kWarps = 8;
+constexpr int kRowsT = 128;                   // rows per tile (the MMA's M)
+constexpr int kBox = kRowsT * 128;            // 128 latent columns of a tile: 16 KB
+constexpr int kTile = 4 * kBox;               // 64 KB of E4M3
+constexpr int kKeyTile = kRowsT * kQ4KeyBytes;   // 16 KB of bf16 keys
+constexpr int kSoft = 256, kDecode = 128;
+constexpr int kThreads = kSoft + 3 * 32 + kDecode;
+constexpr int kPParts = 3;
+constexpr int kHalf = kHeadGroup / 2;         // heads per softmax warp group
+constexpr int kPN = kPParts * kHeadGroup;     // P rows of the PV MMA (part-major)
+constexpr int kPBuf = kPN * 128;              // 6 KB: 48 rows of 128 tile rows
+constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64, O^T at 128..319, Sk[2] at 320 / 352
+constexpr uint32_t kOCol = 128, kKCol = 320;
+constexpr float kRescaleLog2 = 8.f;
 
-__global__ void __launch_bounds__(32 * kWarps) split_q4_kernel(const SplitParams p) {
-  __shared__ float wm[kWarps], wl[kWarps], wo[kWarps][kDc];
-  const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (p.late) pdl_wait();
-  const int len = clamp_length(p, b, tid == 0 && h == 0 && j == 0);
-  const int r0 = j * p.chunk;
-  pdl_wait();   // the queries, and the readers of the workspace and of o_c
-  if (r0 >= len) {
-    if (p.direct) write_no_rows(p, size_t(b) * p.H + h, 1, tid, 32 * kWarps);
-    return;
+// The query of one (sequence, 16-head group) as shared memory holds it: four 128-column
+// boxes of (parts x 16) rows x 128 bytes, the key part's (hi, or hi and lo) x 16 rows x 128
+// bytes, both 128-byte swizzled, and the 16 scales.
+template <bool kF32>
+struct Q4Plan {
+  static constexpr int kQParts = kF32 ? 4 : 2, kKParts = kF32 ? 2 : 1;
+  static constexpr int kQN = kQParts * kHeadGroup, kKN = kKParts * kHeadGroup;
+  static constexpr int kQBox = kQN * 128;
+  static constexpr int kQKeys = 4 * kQBox;                  // offset of the key part
+  static constexpr int kQBytes = kQKeys + kKN * 128;        // of the scales
+  static_assert(size_t(kQBytes) + 64 <= kFp8QImage, "query image in the workspace");
+  // Rows arrive in slots, whose length is what room is left.
+  static constexpr int kSlotRows = kF32 ? 16 : 32, kSlots = kF32 ? 3 : 4;
+  static constexpr int kSlotCodes = kSlotRows * kQ4CodeBytes;
+  static constexpr int kSlotBytes = kSlotRows * (kQ4CodeBytes + kQ4ExpBytes);
+  static constexpr int kOffTile = 0;
+  static constexpr int kOffKeys = kOffTile + 2 * kTile;
+  static constexpr int kOffQ = kOffKeys + 2 * kKeyTile;
+  static constexpr int kOffP = kOffQ + kQBytes;
+  static constexpr int kOffRaw = kOffP + 2 * kPBuf;
+  static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;   // [16] magnitudes by exponent
+  static constexpr int kOffRed = kOffTable + 16 * 8;                // [2][16 heads][4 warps] maxima
+  static constexpr int kOffLsum = kOffRed + 2 * kHeadGroup * 4 * 4;
+  static constexpr int kOffBar = kOffLsum + kHeadGroup * 4 * 4;
+  static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots,   // rows landed / decoded
+                       KEYFULL = RAWEMPTY + kSlots,   // [2] keys of the tile landed
+                       CFULL = KEYFULL + 2,           // [2] tile decoded
+                       SFULL = CFULL + 2,             // [2] scores of the tile (keys free again)
+                       SFREE = SFULL + 2,             // [2] softmax read them
+                       PFULL = SFREE + 2,             // [2] P of the tile written
+                       ODONE = PFULL + 2,             // [2] PV of the tile finished (tile free)
+                       QREADY = ODONE + 2, DONE = QREADY + 1, kBars = DONE + 1;
+  static constexpr int kOffSlot = kOffBar + 8 * kBars;
+  static constexpr int kOffAbort = kOffSlot + 16;
+  static constexpr int kOffShare = kOffAbort + 16;   // TileShare of the CTA
+  static constexpr size_t kSmem = 1024 + kOffShare + 32;
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kOffQ % 1024 == 0 && kQKeys % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  static_assert(kOffRaw % 128 == 0 && kSlotBytes % 16 == 0 && kOffBar % 8 == 0, "alignment");
+  static_assert(kBars <= 32, "a barrier per lane");
+};
+
+__device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f8f6f4 with E4M3 A and B and fp32 accumulators; a_mn selects an MN-major A.
+constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void bulk_g2s_elected(uint32_t dst, const void* src, uint32_t bytes,
+                                                 uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
   }
-  const int r1 = min(r0 + p.chunk, len);
+}
+// The same by a whole warp, which leaves it converged.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  q4_wait(bar, parity, abort);
+  __syncwarp();
+}
+
+__device__ __forceinline__ uint16_t to_e4m3x2(float x0, float x1) {
+  return static_cast<uint16_t>(
+      __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
+  return __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3)));
+}
+// Byte offset of K index k (< 128) in row n of a K-major box of 128-byte rows with the
+// 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
+  return static_cast<uint32_t>(n * 128 + ((((k >> 4) ^ n) & 7) << 4) + (k & 15));
+}
+
+// Where the rows of a page that does not exist come from.
+__device__ __align__(128) uint8_t g_q4_zeros[32 * kQ4CodeBytes];
+
+// Eight codes as E4M3 bytes; (lo, hi): the E4M3 magnitudes of codes 0-3 and 4-7.
+__device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
+  const uint32_t sel = w & 0x77777777u, odd = w << 4;
+  const uint32_t m0 = __byte_perm(mag.x, mag.y, sel), m1 = __byte_perm(mag.x, mag.y, sel >> 16);
+  const uint32_t s0 = __byte_perm(odd, w, 0x5140), s1 = __byte_perm(odd, w, 0x7362);
+  return make_uint2(m0 | (s0 & 0x80808080u), m1 | (s1 & 0x80808080u));
+}
+
+// The query image of one (query group b, head h): q_abs (512 values) becomes sigma (a1 + a2 /
+// 16 + ...), a_i E4M3 and sigma a power of two that puts max |q_abs| / sigma in [128, 256);
+// q_pe a bf16 value, or hi and lo.  Part i goes to row 16 i + (h mod 16) of the group's image.
+// grid (H, B), 160 threads: thread t < 128 converts values 4 t .., thread 128 + u keys 4 u ..
+template <bool kF32>
+__global__ void __launch_bounds__(160) q4_query_kernel(const SplitParams p) {
+  using L = Q4Plan<kF32>;
+  __shared__ float wmax[4];
+  pdl_launch_dependents();   // the split may begin its set-up and cache stream
+  const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, lane = t & 31;
+  const int hh = h % kHeadGroup;
+  uint8_t* img = p.q_img + (size_t(b) * (p.H / kHeadGroup) + h / kHeadGroup) * kFp8QImage;
+  pdl_wait();   // the queries come from the kernel before, and one may still read the image
   const size_t bh = size_t(b) * p.H + h;
-  float q[16];
-  float2 qk;
-  if (p.io_bf16) {
-    const __nv_bfloat16* qa = static_cast<const __nv_bfloat16*>(p.q_abs) + bh * kDc;
-    for (int i = 0; i < 2; ++i)
-      for (int k = 0; k < 8; ++k) q[8 * i + k] = __bfloat162float(qa[256 * i + 8 * lane + k]);
-    qk = load_pair(static_cast<const __nv_bfloat16*>(p.q_pe) + bh * kDr + 2 * lane);
-  } else {
-    const float* qa = static_cast<const float*>(p.q_abs) + bh * kDc;
-    for (int i = 0; i < 2; ++i)
-      for (int k = 0; k < 8; ++k) q[8 * i + k] = qa[256 * i + 8 * lane + k];
-    qk = load_pair(static_cast<const float*>(p.q_pe) + bh * kDr + 2 * lane);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const size_t at = t < 128 ? bh * kDc + 4 * t : bh * kDr + 4 * (t - 128);
+  if (t < 144) {
+    const void* src = t < 128 ? p.q_abs : p.q_pe;
+    if (kF32) {
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+    } else {
+      const uint2 q2 = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src) + at);
+      v = make_float4(__uint_as_float(q2.x << 16), __uint_as_float(q2.x & 0xffff0000u),
+                      __uint_as_float(q2.y << 16), __uint_as_float(q2.y & 0xffff0000u));
+    }
   }
-  const int seq = cache_seq(p, b), mask = (1 << p.page_shift) - 1;
-  float m = -INFINITY, l = 0.f, acc[16];
+  float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int t = r0 + warp; t < r1; t += kWarps) {
-    const int id = page_of(p, seq, t);   // rows of a page that does not exist read as zeros
-    Q4Lane x;
-    if (id >= 0)
-      x.load(Q4Page<const uint8_t>(static_cast<const uint8_t*>(p.cache), id, p.page_shift), t & mask, lane);
-    else
-      x.zero();
-    float c[16];
-    x.values(0, lane, c);
-    x.values(1, lane, c + 8);
-    const float2 ck = x.pair();
-    float s = fmaf(qk.y, ck.y, qk.x * ck.x);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(q[i], c[i], s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), alpha = exp2f(m - mn), w = exp2f(s - mn);
-    l = l * alpha + w;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, c[i], acc[i] * alpha);
-    m = mn;
-  }
-  if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) wo[warp][256 * (i >> 3) + 8 * lane + (i & 7)] = acc[i];
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  if (lane == 0 && t < 128) wmax[t >> 5] = mx;
   __syncthreads();
-  float M = -INFINITY, L = 0.f, f[kWarps];
+  mx = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  int ex = 0;
+  frexpf(mx, &ex);   // mx = f 2^ex, f in [0.5, 1)
+  ex = max(ex, -100);   // keeps 1 / sg finite; smaller queries score as zero to 2^-100
+  const float sg = mx > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
+  const float inv = 1.f / sg;   // exact: a power of two
+  if (t == 0) reinterpret_cast<float*>(img + L::kQBytes)[hh] = sg;
+  if (t < 128) {
+    float x0 = v.x * inv, x1 = v.y * inv, x2 = v.z * inv, x3 = v.w * inv;
+    uint8_t* bx = img + (t >> 5) * L::kQBox;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w]);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = wm[w] == -INFINITY ? 0.f : exp2f(wm[w] - M);
-    L += f[w] * wl[w];
+    for (int part = 0; part < L::kQParts; ++part) {
+      const uint16_t lo = to_e4m3x2(x0, x1), hi = to_e4m3x2(x2, x3);
+      *reinterpret_cast<uint32_t*>(bx + sw128_byte(kHeadGroup * part + hh, (4 * t) & 127)) =
+          static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+      const float2 f01 = from_e4m3x2(lo), f23 = from_e4m3x2(hi);
+      // the residuals of a rounding are exact
+      x0 = (x0 - f01.x) * 16.f;
+      x1 = (x1 - f01.y) * 16.f;
+      x2 = (x2 - f23.x) * 16.f;
+      x3 = (x3 - f23.y) * 16.f;
+    }
+  } else if (t < 144) {
+    uint32_t hi0, lo0, hi1, lo1;
+    split_bf16(v.x, v.y, hi0, lo0);
+    split_bf16(v.z, v.w, hi1, lo1);
+    uint8_t* to = img + L::kQKeys;
+    const int k = 8 * (t - 128);   // bytes
+    *reinterpret_cast<uint2*>(to + sw128_byte(hh, k)) = make_uint2(hi0, hi1);
+    if (kF32) *reinterpret_cast<uint2*>(to + sw128_byte(kHeadGroup + hh, k)) = make_uint2(lo0, lo1);
   }
-  const size_t base = bh * p.splits + j;
-  for (int c = tid; c < kDc; c += 32 * kWarps) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], wo[w][c], v);
-    if (p.direct && p.io_bf16)
-      reinterpret_cast<__nv_bfloat16*>(p.part_o)[base * kDc + c] = __float2bfloat16_rn(v / L);
-    else
-      p.part_o[base * kDc + c] = v / L;
+}
+
+// kShare: one CTA per SM takes an equal run of all query groups' tiles (take_share), one item
+// per query group it meets, streamed back to back; otherwise a CTA has one item, its chunk.
+template <bool kF32, bool kShare>
+__global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams p) {
+  using L = Q4Plan<kF32>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + L::kOffBar;
+  float* red = reinterpret_cast<float*>(smem + L::kOffRed);
+  float* lsum = reinterpret_cast<float*>(smem + L::kOffLsum);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+  uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
+  auto bar = [&](int i) { return bars + 8 * i; };
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
+  const int groups = p.H / kHeadGroup;
+  const int g = kShare ? blockIdx.x % groups : blockIdx.x, h0 = g * kHeadGroup;
+  TileItem first{0, 0, 0, 0, 0};   // the CTA's first item (none: T = 0)
+  int T = 0, row_end = 0;  // tiles of the CTA; the row behind its chunk
+  TileShare share{};
+  if (!kShare) {
+    const int j = blockIdx.y, b = blockIdx.z;
+    if (p.late) pdl_wait();
+    const int len = clamp_length(p, b, tid == 0 && g == 0 && j == 0);
+    const int r0 = j * p.chunk;
+    if (r0 >= len) {   // chunk past the end of this sequence: nothing to do
+      if (p.direct || r0 == 0) pdl_wait();   // no row at all: see launch_pdl
+      if (p.direct) write_no_rows(p, size_t(b) * p.H + h0, kHeadGroup, tid, kThreads);
+      return;
+    }
+    row_end = min(r0 + p.chunk, len);
+    T = (row_end - r0 + kRowsT - 1) / kRowsT;
+    first = TileItem{b, j, r0, T, len};
   }
-  if (tid == 0 && p.part_lse) p.part_lse[base] = (M + log2f(L)) * kLn2;
+  auto begin_share = [&] {
+    T = uniform(share.tiles);
+    first = first_item<false>(p, share, blockIdx.x / groups);
+  };
+  auto item_after = [&](const TileItem& it, int t) { return next_item<false>(p, it, T - t); };
+
+  // A tile is 128 / piece pieces of rows of one page each, at most a slot; lane i knows the
+  // page of piece i (-1: outside the pool, -2: past the sequence's end).
+  const int piece = min(1 << p.page_shift, L::kSlotRows);
+  const uint8_t* pool = static_cast<const uint8_t*>(p.cache);
+  const uint64_t pol = l2_evict_first_policy();
+  auto piece_page = [&](const TileItem& it, int i) {
+    const int r = it.r0 + i * kRowsT + lane * piece;
+    return lane * piece < kRowsT && r < it.len ? page_of(p, cache_seq(p, it.v), r) : -2;
+  };
+  // Copies `bytes` bytes of each of the rows of pieces from .. to - 1 of a tile whose first row
+  // is r0, from a plane at `plane` bytes a row of the page, to dst on.
+  auto copy_rows = [&](int pages, int r0, int from, int to, int plane, int bytes, uint32_t dst,
+                       uint32_t full) {
+#pragma unroll 1
+    for (int i = from; i < to; ++i) {
+      const int id = __shfl_sync(0xffffffffu, pages, i);
+      if (id == -2) break;
+      const int r = (r0 + i * piece) & ((1 << p.page_shift) - 1);
+      const uint8_t* src = id < 0 ? g_q4_zeros
+                                  : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
+                                        (static_cast<size_t>(plane) << p.page_shift) + r * bytes;
+      bulk_g2s_elected(dst + (i - from) * piece * bytes, src, piece * bytes, full, pol);
+    }
+  };
+  // Slot s of tile t of the CTA, whose pieces' pages the lanes hold.
+  constexpr int kTileSlots = kRowsT / L::kSlotRows;
+  auto issue_slot = [&](int pages, int r0, int n) {   // n: slots issued before
+    const int at = n % L::kSlots, per = L::kSlotRows / piece, from = n % kTileSlots * per;
+    if (n >= L::kSlots)
+      warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
+    const uint32_t live = __ballot_sync(0xffffffffu, lane >= from && lane < from + per && pages != -2);
+    const uint32_t full = bar(L::RAWFULL + at), dst = sbase + L::kOffRaw + at * L::kSlotBytes;
+    expect_tx_elected(full, __popc(live) * piece * (kQ4CodeBytes + kQ4ExpBytes));
+    copy_rows(pages, r0, from, from + per, 0, kQ4CodeBytes, dst, full);
+    copy_rows(pages, r0, from, from + per, kQ4CodeBytes + kQ4KeyBytes, kQ4ExpBytes,
+              dst + L::kSlotCodes, full);
+  };
+  auto issue_keys = [&](int pages, int r0, int t) {
+    const int bf = t & 1;
+    if (t >= 2) warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
+    const uint32_t live = __ballot_sync(0xffffffffu, pages != -2);
+    expect_tx_elected(bar(L::KEYFULL + bf), __popc(live) * piece * kQ4KeyBytes);
+    copy_rows(pages, r0, 0, kRowsT / piece, kQ4CodeBytes, kQ4KeyBytes,
+              sbase + L::kOffKeys + bf * kKeyTile, bar(L::KEYFULL + bf));
+  };
+  // The query image of group v, by one thread.  (The scales stay behind: of a share this copy
+  // may run ahead of the softmax, which reads them from global memory.)
+  auto load_query = [&](int v) {
+    const uint8_t* img = p.q_img + (size_t(v) * groups + g) * kFp8QImage;
+    mbar_arrive_expect_tx(bar(L::QREADY), L::kQBytes);
+    bulk_g2s(sbase + L::kOffQ, img, L::kQBytes, bar(L::QREADY));
+  };
+  // The producer's place: its next tile is tile i of `it`.
+  TileItem it;
+  int i = 0, pages = -2, slots = 0;   // slots issued
+  if (warp == 8) {
+    if (kShare) {
+      share = take_share<false>(p, blockIdx.x / groups, gridDim.x / groups, lane, blockIdx.x == 0);
+      if (lane == 0) *reinterpret_cast<TileShare*>(smem + L::kOffShare) = share;
+      if (share.tiles > 0)
+        begin_share();
+      else
+        T = 0;
+    }
+    if (T > 0) {
+      it = first;
+      pages = piece_page(it, 0);
+    }
+    if (lane < L::kBars)
+      // counts: decoded slots and tiles four warps; S read and P written eight; else one
+      mbar_init(bar(lane), lane >= L::SFREE && lane < L::ODONE ? 8
+                           : (lane >= L::RAWEMPTY && lane < L::KEYFULL) ||
+                                     (lane >= L::CFULL && lane < L::SFULL)
+                               ? kDecode / 32
+                               : 1);
+    if (lane == 0) *abort_flag = 0;
+    fence_mbarrier_init();
+    __syncwarp();
+    if (T > 0) {   // the stream starts before the CTA's barrier
+      for (int s = 0; s < min(L::kSlots, kTileSlots); ++s) issue_slot(pages, it.r0, slots++);
+      if (L::kSlots >= kTileSlots) issue_keys(pages, it.r0, 0);
+    }
+    if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
+  } else if (warp == 11 && lane < 16) {
+    // Magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^(lane - 8) as E4M3 (15 as 14).
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float u = q4_unit(lane);
+      const float2 x = k == 0   ? make_float2(0.f, 0.5f)
+                       : k == 1 ? make_float2(1.f, 1.5f)
+                       : k == 2 ? make_float2(2.f, 3.f)
+                                : make_float2(4.f, 6.f);
+      w[k] = to_e4m3x2(x.x * u, x.y * u);
+    }
+    reinterpret_cast<uint2*>(smem + L::kOffTable)[lane] =
+        make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (kShare) {
+    share = *reinterpret_cast<const TileShare*>(smem + L::kOffShare);
+    if (share.tiles <= 0) {   // more CTAs than tiles
+      pdl_wait();
+      return;
+    }
+    if (warp != 8) begin_share();
+  }
+  const uint32_t tmem = *slot_ptr;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ rows
+    int keys = L::kSlots >= kTileSlots ? 1 : 0;   // tiles whose keys are on their way
+    for (int t = 0; t < T; ++t) {
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      for (; slots < (t + 1) * kTileSlots; ++slots) issue_slot(pages, it.r0 + i * kRowsT, slots);
+      if (keys == t) {
+        issue_keys(pages, it.r0 + i * kRowsT, t);
+        ++keys;
+      }
+      if (kShare && i == 0 && t > 0) {
+        // A new item's query, once the last score MMA of the one before has read its own.
+        warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        if (lane == 0) {
+          pdl_wait();
+          load_query(it.v);
+        }
+        __syncwarp();
+      }
+      if (t + 1 >= T) break;
+      if (++i == it.tiles) {
+        it = item_after(it, t + 1);
+        i = 0;
+      }
+      pages = piece_page(it, i);
+    }
+    // Copies still in flight land before the CTA may leave (bounded waits).
+    for (int n = max(0, slots - L::kSlots); n < slots; ++n)
+      if (!mbar_wait_bounded(bar(L::RAWFULL + n % L::kSlots), (n / L::kSlots) & 1)) *abort_flag = 1;
+    for (int t = max(0, keys - 2); t < keys; ++t)
+      if (!mbar_wait_bounded(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
+  } else if (warp > 10) {
+    // ------------------------------------------------------------ codes to E4M3
+    // Thread d of 128: 16 bytes of codes (32 values, one byte of exponents) of rows d / 16,
+    // 8 + d / 16, ... of a slot: a warp reads two whole rows.  Of the two 16-byte pieces a
+    // thread writes, odd boxes' threads write the second first: eight threads of one row then
+    // meet eight different pieces of the banks.
+    const int d = tid - (kSoft + 3 * 32), c = d & 15, r = d >> 4;
+    const uint2* table = reinterpret_cast<const uint2*>(smem + L::kOffTable);
+    const int box = c >> 2, swap = box & 1;
+    int n = 0;
+    for (int t = 0; t < T; ++t) {
+      uint8_t* tile = smem + L::kOffTile + (t & 1) * kTile + box * kBox;
+      if (t >= 2) {
+        warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+        tc_fence_after();
+      }
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+#pragma unroll 1
+      for (int s = 0; s < kTileSlots; ++s, ++n) {
+        const int at = n % L::kSlots;
+        warp_wait(bar(L::RAWFULL + at), (n / L::kSlots) & 1, abort_flag);
+        const uint8_t* raw = smem + L::kOffRaw + at * L::kSlotBytes;
+        constexpr int kEach = L::kSlotRows / 8;
+        uint4 w[kEach];
+        uint32_t e[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          w[k] = *reinterpret_cast<const uint4*>(raw + (8 * k + r) * kQ4CodeBytes + 16 * c);
+          e[k] = raw[L::kSlotCodes + (8 * k + r) * kQ4ExpBytes + c];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + at));
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const uint2 m0 = table[e[k] & 15], m1 = table[e[k] >> 4];
+          const uint2 a = decode8(w[k].x, m0), b = decode8(w[k].y, m0);
+          const uint2 x = decode8(w[k].z, m1), y = decode8(w[k].w, m1);
+          const uint4 v0 = make_uint4(a.x, a.y, b.x, b.y), v1 = make_uint4(x.x, x.y, y.x, y.y);
+          const int row = L::kSlotRows * s + 8 * k + r, u = 2 * (c & 3) + swap;
+          *reinterpret_cast<uint4*>(tile + sw128(row, u)) = swap ? v1 : v0;
+          *reinterpret_cast<uint4*>(tile + sw128(row, u ^ 1)) = swap ? v0 : v1;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::CFULL + (t & 1)));
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ score MMAs
+    // The whole warp runs along, converged at every MMA; boxes are not unrolled (code
+    // that runs once a tile is fetched anew each time).
+    constexpr uint32_t idesc_s = idesc_e4m3(128, L::kQN, 0);
+    constexpr uint32_t idesc_k = umma_idesc_bf16(128, L::kKN, 0, 0);
+    const uint64_t a0 = umma_desc_sw128(sbase + L::kOffTile, 16, 1024);
+    const uint64_t k0 = umma_desc_sw128(sbase + L::kOffKeys, 16, 1024);
+    const uint64_t q0 = umma_desc_sw128(sbase + L::kOffQ, 16, 1024);
+    TileItem cur = first;
+    int left = 0, n = 0;   // tiles left of the item; items begun
+    for (int t = 0; t < T; ++t) {
+      const int bf = t & 1;
+      if (left == 0) {
+        if (t > 0) cur = item_after(cur, t);
+        left = cur.tiles;
+        warp_wait(bar(L::QREADY), n & 1, abort_flag);
+        if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
+          // The run with a query group's first tile says how many runs it spans.  (Not
+          // before a query is here, fetched behind the PDL wait: the combine of the call
+          // before may still be reading its own counts.)
+          p.pieces[cur.v] = count_pieces(cur, share.first + t, share.each);
+        }
+        ++n;
+      }
+      --left;
+      if (t >= 2) warp_wait(bar(L::SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
+      warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)   // 16 key values (32 bytes) a step
+        umma_bf16_elected(tmem + kKCol + 32 * bf, k0 + ((bf * kKeyTile) >> 4) + 2 * k,
+                          q0 + (L::kQKeys >> 4) + 2 * k, idesc_k, k > 0 ? 1u : 0u);
+      warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m) {
+        const uint64_t a = a0 + static_cast<uint64_t>((bf * kTile + m * kBox) >> 4);
+        const uint64_t q = q0 + static_cast<uint64_t>((m * L::kQBox) >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)   // 32 columns a step
+          umma_e4m3(tmem + 64 * bf, a + 2 * k, q + 2 * k, idesc_s, k > 0 ? 1u : (m > 0 ? 1u : 0u));
+      }
+      umma_commit_elected(bar(L::SFULL + bf));
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ query image, PV MMAs
+    if (lane == 0) {
+      pdl_wait();   // the image is written by the kernel before
+      load_query(first.v);
+    }
+    __syncwarp();
+    constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
+    const uint64_t p0 = umma_desc_sw128(sbase + L::kOffP, 16, 1024);
+    const uint64_t c0 = umma_desc_sw128(sbase + L::kOffTile, kBox, 1024);
+    TileItem cur = first;
+    int done = 0;   // tiles of the item accumulated
+    for (int t = 0; t < T; ++t, ++done) {
+      const int bf = t & 1;
+      if (kShare && done == cur.tiles) {
+        cur = item_after(cur, t);
+        done = 0;
+      }
+      warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+      const uint64_t pd = p0 + static_cast<uint64_t>((bf * kPBuf) >> 4);
+#pragma unroll 1
+      for (int mb = 0; mb < 4; ++mb) {
+        // C^T block mb: latent columns 128 mb.. (MN-major, one 128-byte
+        // span), K = tile rows in 8-row groups 1024 B apart
+        const uint64_t c = c0 + static_cast<uint64_t>((bf * kTile + mb * kBox) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
+          umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
+                    idesc_o, ks > 0 ? 1u : (done > 0 ? 1u : 0u));
+      }
+      umma_commit_elected(bar(L::ODONE + bf));
+    }
+    umma_commit_elected(bar(L::DONE));
+    mbar_wait_bounded(bar(L::DONE), 0);
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int gp = warp >> 2, wq = warp & 3;
+    const int hb = kHalf * gp;                          // first head of this group
+    const int row = 32 * wq + lane;                     // tile row held by this thread
+    const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
+    TileItem cur = first;
+    float qsig[kHalf];
+    auto read_scales = [&] {   // of the item
+      const float4* sg = reinterpret_cast<const float4*>(
+          p.q_img + (size_t(cur.v) * groups + g) * kFp8QImage + L::kQBytes + 4 * hb);
+      const float4 s0 = __ldcg(sg), s1 = __ldcg(sg + 1);
+      const float s[kHalf] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+      for (int h = 0; h < kHalf; ++h) qsig[h] = s[h] * p.scale_log2;
+    };
+    pdl_wait();   // the scales come with the query image
+    read_scales();
+    for (int t0 = 0; t0 < T;) {   // items; t0: the item's first tile among the CTA's
+      const int tiles = cur.tiles;
+      // Rows past the item's last (of a sequence, or of a chunk) get P = 0.  What they hold
+      // is finite whatever their bytes are, but for the keys, whose scores are not looked at.
+      const int end = kShare ? cur.len : row_end;
+      const int last_valid = min(end - (cur.r0 + (tiles - 1) * kRowsT), kRowsT);
+      float m[kHalf], l[kHalf];
+#pragma unroll
+      for (int h = 0; h < kHalf; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      for (int t = t0; t < t0 + tiles; ++t) {
+        const int sb = t & 1;
+        const int valid = t == t0 + tiles - 1 ? last_valid : kRowsT;
+        warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
+        tc_fence_after();
+        float sc[kHalf], tt[kHalf];
+        {
+          uint32_t s[L::kQParts][8], sk[L::kKParts][8];
+#pragma unroll
+          for (int i = 0; i < L::kQParts; ++i)
+            tmem_ld8_nowait(tmem + lane_base + 64 * sb + kHeadGroup * i + hb, s[i]);
+#pragma unroll
+          for (int i = 0; i < L::kKParts; ++i)
+            tmem_ld8_nowait(tmem + lane_base + kKCol + 32 * sb + kHeadGroup * i + hb, sk[i]);
+          tmem_wait_ld();
+          const bool rv = row < valid;
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {
+            float x = __uint_as_float(s[L::kQParts - 1][h]);
+#pragma unroll
+            for (int i = L::kQParts - 2; i >= 0; --i) x = fmaf(x, 0.0625f, __uint_as_float(s[i][h]));
+            float k = __uint_as_float(sk[0][h]);
+            if (kF32) k += __uint_as_float(sk[L::kKParts - 1][h]);
+            sc[h] = rv ? fmaf(x, qsig[h], k * p.scale_log2) : -INFINITY;
+            tt[h] = sc[h];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::SFREE + sb));
+        // tile maximum per head: warp, then the group's four warps
+#pragma unroll
+        for (int h = 0; h < kHalf; ++h)
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
+        float* rd = red + sb * kHeadGroup * 4;
+        if (lane < kHalf) {
+          float v = tt[0];
+#pragma unroll
+          for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
+          rd[(hb + lane) * 4 + wq] = v;
+        }
+        named_bar_sync(1, kSoft);
+        bool need = false;
+        float tmax[kHalf];
+#pragma unroll
+        for (int h = 0; h < kHalf; ++h) {
+          const float4 q4 = *reinterpret_cast<const float4*>(rd + (hb + h) * 4);
+          tmax[h] = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
+          need |= tmax[h] > m[h] + kRescaleLog2;
+        }
+        if (need) {
+          // Move this group's reference maxima; rescale its row sums and the O^T
+          // columns it owns (in TMEM, after the previous PV finished).
+          float alpha[kHalf];
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {
+            const float mn = fmaxf(m[h], tmax[h]);
+            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= alpha[h];
+          }
+          if (t > t0) {
+            warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+              for (int part = 0; part < kPParts; ++part) {
+                const uint32_t col = kOCol + kPN * mb + kHeadGroup * part + hb;
+                uint32_t r[8];
+                float o[8];
+                tmem_ld8_nowait(tmem + lane_base + col, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < kHalf; ++h) o[h] = __uint_as_float(r[h]) * alpha[h];
+                tmem_st8(tmem + lane_base + col, o);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // p in [0, 2^8] as three E4M3 parts, two heads per conversion; the row
+        // sum takes the value the PV uses.
+        uint16_t pp[kPParts][kHalf / 2];
+#pragma unroll
+        for (int h2 = 0; h2 < kHalf / 2; ++h2) {
+          float v0, v1;
+          {
+            const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
+            const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
+            v0 = ex2(sc[2 * h2] - mu0);
+            v1 = ex2(sc[2 * h2 + 1] - mu1);
+          }
+          float used0 = 0.f, used1 = 0.f, wgt = 1.f;
+#pragma unroll
+          for (int part = 0; part < kPParts; ++part) {
+            pp[part][h2] = to_e4m3x2(v0, v1);
+            const float2 f = from_e4m3x2(pp[part][h2]);
+            used0 += f.x * wgt;
+            used1 += f.y * wgt;
+            v0 = (v0 - f.x) * 16.f;
+            v1 = (v1 - f.y) * 16.f;
+            wgt *= 0.0625f;
+          }
+          l[2 * h2] += used0;
+          l[2 * h2 + 1] += used1;
+        }
+        // P^T buffer sb was last read by the PV of tile t-2.
+        if (t >= 2) warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
+        {
+          // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
+          // 16 part + n is part `part` of head n; the K index is the tile row.
+          uint8_t* pbuf = smem + L::kOffP + sb * kPBuf;
+#pragma unroll
+          for (int part = 0; part < kPParts; ++part)
+#pragma unroll
+            for (int h2 = 0; h2 < kHalf / 2; ++h2) {
+              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2, row)] = pp[part][h2] & 0xFF;
+              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2 + 1, row)] = pp[part][h2] >> 8;
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::PFULL + sb));
+      }
+      t0 += tiles;
+      // The combine may start launching: it waits for this grid anyway.
+      if (tid == 0 && t0 == T) pdl_launch_dependents();
+      // Softmax denominators over the chunk's rows.
+#pragma unroll
+      for (int h = 0; h < kHalf; ++h)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+      if (lane < kHalf) {
+        float v = l[0];
+#pragma unroll
+        for (int h = 1; h < kHalf; ++h) v = lane == h ? l[h] : v;
+        lsum[(hb + lane) * 4 + wq] = v;
+      }
+      const TileItem out = cur;
+      if (kShare && t0 < T) {   // fetched while the last PV runs
+        cur = item_after(cur, t0);
+        read_scales();
+      }
+      // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
+      warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      tc_fence_after();
+      named_bar_sync(1, kSoft);
+      if (!*abort_flag) {
+        const size_t base = (size_t(out.v) * p.H + h0) * p.splits + out.j;
+        // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
+        // here, 1 <= L <= 2^8 x rows), branch-free; lane h of the first warp of
+        // each group writes head h's log-sum-exp.
+        float inv[kHalf], Lme = 0.f, mme = 0.f;
+#pragma unroll
+        for (int h = 0; h < kHalf; ++h) {
+          const float4 q4 = *reinterpret_cast<const float4*>(lsum + (hb + h) * 4);
+          const float L_ = (q4.x + q4.y) + (q4.z + q4.w);
+          inv[h] = L_ > 0.f ? __fdividef(1.f, L_) : 0.f;
+          Lme = lane == h ? L_ : Lme;
+          mme = lane == h ? m[h] : mme;
+        }
+        if (wq == 0 && lane < kHalf && p.part_lse)
+          p.part_lse[base + size_t(hb + lane) * p.splits] =
+              Lme > 0.f ? (mme + log2f(Lme)) * kLn2 : -INFINITY;
+        float* row0 = p.part_o + (base + size_t(hb) * p.splits) * kDc + 32 * wq + lane;
+        const size_t head_stride = size_t(p.splits) * kDc;
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          uint32_t o1[8], o2[8], o3[8];
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + hb, o1);
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + kHeadGroup + hb, o2);
+          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + 2 * kHeadGroup + hb, o3);
+          tmem_wait_ld();
+          float* at = row0 + 128 * mb;
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h, at += head_stride) {
+            const float v = (__uint_as_float(o1[h]) + (__uint_as_float(o2[h]) * 0.0625f +
+                                                       __uint_as_float(o3[h]) * 0.00390625f)) *
+                            inv[h];
+            if (p.direct && p.io_bf16)
+              reinterpret_cast<__nv_bfloat16*>(p.part_o)[at - p.part_o] = __float2bfloat16_rn(v);
+            else
+              *at = v;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && *abort_flag) report(p.status, MLA_DEV_PIPELINE_TIMEOUT);
+}
+
+template <bool kF32, bool kShare>
+mla_status launch_q4(const SplitParams& p, cudaStream_t stream, const char* who) {
+  using L = Q4Plan<kF32>;
+  static DeviceFlags attr_done;
+  const int dev = current_device();
+  if (!attr_done.test(dev)) {
+    if (cudaFuncSetAttribute(split_q4_kernel<kF32, kShare>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      set_error("%s: cannot reserve %zu bytes of shared memory", who, L::kSmem);
+      return MLA_ERR_CUDA;
+    }
+    attr_done.set(dev);
+  }
+  const int groups = p.H / kHeadGroup;
+  const dim3 grid = kShare ? dim3(share_runs(groups) * groups) : dim3(groups, p.splits, p.B);
+  launch_pdl(split_q4_kernel<kF32, kShare>, grid, dim3(kThreads), L::kSmem, stream, p);
+  return launch_status(who);
 }
 
 }  // namespace
 
-mla_status launch_split_q4(const SplitParams& p, const void* cache, cudaStream_t stream,
-                           const char* who) {
-  launch_pdl(split_q4_kernel, dim3(p.H, p.splits, p.B), dim3(32 * kWarps), 0, stream, p);
+mla_status launch_q4_queries(const SplitParams& p, cudaStream_t stream, const char* who) {
+  launch_pdl(p.io_bf16 ? q4_query_kernel<false> : q4_query_kernel<true>, dim3(p.H, p.B), dim3(160),
+             0, stream, p);
   return launch_status(who);
+}
+
+mla_status launch_split_q4(const SplitParams& p, cudaStream_t stream, const char* who) {
+  if (!p.late) {
+    const mla_status st = launch_q4_queries(p, stream, who);
+    if (st != MLA_OK) return st;
+  }
+  if (p.pieces)
+    return p.io_bf16 ? launch_q4<false, true>(p, stream, who) : launch_q4<true, true>(p, stream, who);
+  return p.io_bf16 ? launch_q4<false, false>(p, stream, who) : launch_q4<true, false>(p, stream, who);
 }
 
 }  // namespace mla
