@@ -71,12 +71,12 @@ __global__ void __launch_bounds__(32 * kWarps)
         code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
                     make_float2(v[2 * k] * inv, v[2 * k + 1] * inv), __NV_E2M1,
                     cudaRoundNearest)) << (8 * k);
-      reinterpret_cast<uint32_t*>(page.codes + r * kQ4CodeBytes)[32 * i + lane] = code;
+      reinterpret_cast<uint32_t*>(page.codes(r))[32 * i + lane] = code;
       uint32_t word = (lane & 1) ? 0u : e8 << (4 * ((lane >> 1) & 7));
 #pragma unroll
       for (int off = 2; off < 16; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
       if ((lane & 15) == 0)
-        reinterpret_cast<uint32_t*>(page.exps + r * kQ4ExpBytes)[2 * i + (lane >> 4)] = word;
+        reinterpret_cast<uint32_t*>(page.exps(r))[2 * i + (lane >> 4)] = word;
     }
     const float2 k = rotated(pair[u], pos[u], turn);
     *reinterpret_cast<uint32_t*>(page.keys + q4_key_at(r, lane)) = pack_bf16(k.x, k.y);

@@ -10,12 +10,12 @@
 // (Root-mean-square error of N(0, 1) values 0.110 of their size; 0.113 with 6 2^e as the
 // limit, 0.118 with 8 2^e; 0.112 with one e per 32.)
 //
-// A page of R rows is three planes, 400 R bytes in all, so that the rows of a tile are three
+// A page of R rows is two planes, 400 R bytes in all, so that the rows of a tile are two
 // contiguous copies:
-//   codes  [R][256]  byte i of a row: values 2 i (low four bits) and 2 i + 1
-//   keys   [R][128]  16-byte piece c of row r stands at piece c ^ (r & 7): as the tensor core
-//                    wants it in shared memory (128-byte swizzle)
-//   exps   [R][16]   byte i: e + 8 of blocks 2 i (low four bits) and 2 i + 1
+//   latents [R][272]  256 bytes of codes, byte i: values 2 i (low four bits) and 2 i + 1, then
+//                     16 of exponents, byte i: e + 8 of blocks 2 i (low four bits) and 2 i + 1
+//   keys    [R][128]  16-byte piece c of row r stands at piece c ^ (r & 7): as the tensor core
+//                     wants it in shared memory (128-byte swizzle)
 #pragma once
 
 #include <cuda_fp4.h>
@@ -29,18 +29,20 @@ constexpr int kQ4Block = 16;                       // values that share an expon
 constexpr int kQ4CodeBytes = kDc / 2;              // 256
 constexpr int kQ4KeyBytes = 2 * kDr;               // 128
 constexpr int kQ4ExpBytes = kDc / kQ4Block / 2;    // 16
-constexpr int kQ4RowBytes = kQ4CodeBytes + kQ4KeyBytes + kQ4ExpBytes;   // 400
+constexpr int kQ4LatBytes = kQ4CodeBytes + kQ4ExpBytes;                 // 272
+constexpr int kQ4RowBytes = kQ4LatBytes + kQ4KeyBytes;                  // 400
 constexpr int kQ4ExpMin = -8, kQ4ExpMax = 6;
 
 // The planes of page `id` of a pool (const or not).
 template <typename Byte>
 struct Q4Page {
-  Byte *codes, *keys, *exps;
+  Byte *latents, *keys;
   __device__ __forceinline__ Q4Page(Byte* pool, int id, int page_shift) {
-    codes = pool + (static_cast<size_t>(id) << page_shift) * kQ4RowBytes;
-    keys = codes + (static_cast<size_t>(kQ4CodeBytes) << page_shift);
-    exps = keys + (static_cast<size_t>(kQ4KeyBytes) << page_shift);
+    latents = pool + (static_cast<size_t>(id) << page_shift) * kQ4RowBytes;
+    keys = latents + (static_cast<size_t>(kQ4LatBytes) << page_shift);
   }
+  __device__ __forceinline__ Byte* codes(int r) const { return latents + r * kQ4LatBytes; }
+  __device__ __forceinline__ Byte* exps(int r) const { return codes(r) + kQ4CodeBytes; }
 };
 
 // Byte offset of key pair `pair` of row r in the keys' plane.
@@ -70,11 +72,11 @@ struct Q4Lane {
   uint32_t code[2], key;
   uint8_t exp[2];
   __device__ __forceinline__ void load(const Q4Page<const uint8_t>& page, int r, int lane) {
-    const uint32_t* c = reinterpret_cast<const uint32_t*>(page.codes + r * kQ4CodeBytes);
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(page.codes(r));
     code[0] = c[lane];
     code[1] = c[32 + lane];
-    exp[0] = page.exps[r * kQ4ExpBytes + (lane >> 2)];
-    exp[1] = page.exps[r * kQ4ExpBytes + 8 + (lane >> 2)];
+    exp[0] = page.exps(r)[lane >> 2];
+    exp[1] = page.exps(r)[8 + (lane >> 2)];
     key = *reinterpret_cast<const uint32_t*>(page.keys + q4_key_at(r, lane));
   }
   __device__ __forceinline__ void zero() {

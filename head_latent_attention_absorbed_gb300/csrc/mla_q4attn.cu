@@ -20,13 +20,16 @@
 // are put on by another: nine operations for eight values, no conversion (which would run at
 // an eighth of the rate) and no multiplication.
 //
-// Warp roles (480 threads, one CTA per SM):
+// Warp roles (512 threads, one CTA per SM):
 //   warps 0-7    softmax (one tile row per thread, heads 0-7 in warps 0-3, 8-15 in 4-7),
 //                P, epilogue
-//   warp 8       copies of rows (and TMEM allocation)
+//   warp 8       copies of codes and exponents (and TMEM allocation)
 //   warp 9       score MMAs of each tile (20 instructions)
-//   warp 10      the query image's copy, then the PV MMAs of each tile (16)
+//   warp 10      the first query image's copy, then the PV MMAs of each tile (16)
 //   warps 11-14  codes to E4M3
+//   warp 15      copies of keys, and of the later items' query images
+// (A copy takes its warp some 450 cycles among the others' work: one warp for all of a
+// tile's, and exponents in a plane of their own, took 6600 cycles a tile.)
 #include "mla_q4.cuh"
 
 namespace mla {
@@ -37,7 +40,7 @@ constexpr int kBox = kRowsT * 128;            // 128 latent columns of a tile: 1
 constexpr int kTile = 4 * kBox;               // 64 KB of E4M3
 constexpr int kKeyTile = kRowsT * kQ4KeyBytes;   // 16 KB of bf16 keys
 constexpr int kSoft = 256, kDecode = 128;
-constexpr int kThreads = kSoft + 3 * 32 + kDecode;
+constexpr int kThreads = kSoft + 3 * 32 + kDecode + 32;
 constexpr int kPParts = 3;
 constexpr int kHalf = kHeadGroup / 2;         // heads per softmax warp group
 constexpr int kPN = kPParts * kHeadGroup;     // P rows of the PV MMA (part-major)
@@ -59,8 +62,7 @@ struct Q4Plan {
   static_assert(size_t(kQBytes) + 64 <= kFp8QImage, "query image in the workspace");
   // Rows arrive in slots, whose length is what room is left.
   static constexpr int kSlotRows = kF32 ? 16 : 32, kSlots = kF32 ? 3 : 4;
-  static constexpr int kSlotCodes = kSlotRows * kQ4CodeBytes;
-  static constexpr int kSlotBytes = kSlotRows * (kQ4CodeBytes + kQ4ExpBytes);
+  static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kOffTile = 0;
   static constexpr int kOffKeys = kOffTile + 2 * kTile;
   static constexpr int kOffQ = kOffKeys + 2 * kKeyTile;
@@ -145,7 +147,7 @@ __device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
 }
 
 // Where the rows of a page that does not exist come from.
-__device__ __align__(128) uint8_t g_q4_zeros[32 * kQ4CodeBytes];
+__device__ __align__(128) uint8_t g_q4_zeros[kRowsT * kQ4LatBytes];
 
 // Eight codes as E4M3 bytes; (lo, hi): the E4M3 magnitudes of codes 0-3 and 4-7.
 __device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
@@ -262,50 +264,56 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
   };
   auto item_after = [&](const TileItem& it, int t) { return next_item<false>(p, it, T - t); };
 
-  // A tile is 128 / piece pieces of rows of one page each, at most a slot; lane i knows the
-  // page of piece i (-1: outside the pool, -2: past the sequence's end).
-  const int piece = min(1 << p.page_shift, L::kSlotRows);
+  // A tile is 128 / piece pieces of rows of one page each (for the copies of latents at most a
+  // slot); lane i knows the page of piece i, looked up a tile ahead: -1, outside the pool, or
+  // -2, past the sequence's end.
   const uint8_t* pool = static_cast<const uint8_t*>(p.cache);
   const uint64_t pol = l2_evict_first_policy();
-  auto piece_page = [&](const TileItem& it, int i) {
+  auto piece_page = [&](const TileItem& it, int i, int piece) {
     const int r = it.r0 + i * kRowsT + lane * piece;
-    return lane * piece < kRowsT && r < it.len ? page_of(p, cache_seq(p, it.v), r) : -2;
+    if (lane * piece >= kRowsT || r >= it.len) return -2;
+    const int id = p.table[static_cast<size_t>(cache_seq(p, it.v)) * p.table_stride + (r >> p.page_shift)];
+    return id < 0 ? -1 : id;
   };
-  // Copies `bytes` bytes of each of the rows of pieces from .. to - 1 of a tile whose first row
-  // is r0, from a plane at `plane` bytes a row of the page, to dst on.
-  auto copy_rows = [&](int pages, int r0, int from, int to, int plane, int bytes, uint32_t dst,
-                       uint32_t full) {
+  // Where lane i's piece comes from, in the plane at `plane` bytes a row of the page and of
+  // `bytes` bytes a row; r0: the tile's first row.
+  auto piece_source = [&](int id, int r0, int piece, int plane, int bytes) {
+    if (id >= p.num_pages) id = -1;
+    if (id == -1) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+    const int r = (r0 + lane * piece) & ((1 << p.page_shift) - 1);
+    return id < 0 ? g_q4_zeros
+                  : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
+                        (static_cast<size_t>(plane) << p.page_shift) + r * bytes;
+  };
+  // Copies pieces from .. to - 1, the first `live` of which lie in the sequence, to dst on.
+  auto copy_pieces = [&](const uint8_t* src, int from, int to, int live, uint32_t bytes,
+                         uint32_t dst, uint32_t full) {
+    const int n = max(min(to, live) - from, 0);
+    expect_tx_elected(full, n * bytes);
 #pragma unroll 1
-    for (int i = from; i < to; ++i) {
-      const int id = __shfl_sync(0xffffffffu, pages, i);
-      if (id == -2) break;
-      const int r = (r0 + i * piece) & ((1 << p.page_shift) - 1);
-      const uint8_t* src = id < 0 ? g_q4_zeros
-                                  : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
-                                        (static_cast<size_t>(plane) << p.page_shift) + r * bytes;
-      bulk_g2s_elected(dst + (i - from) * piece * bytes, src, piece * bytes, full, pol);
-    }
+    for (int i = 0; i < n; ++i)
+      bulk_g2s_elected(dst + i * bytes,
+                       reinterpret_cast<const uint8_t*>(__shfl_sync(
+                           0xffffffffu, reinterpret_cast<unsigned long long>(src), from + i)),
+                       bytes, full, pol);
   };
-  // Slot s of tile t of the CTA, whose pieces' pages the lanes hold.
+  const int lat_piece = min(1 << p.page_shift, L::kSlotRows);
+  const int key_piece = min(1 << p.page_shift, kRowsT);
   constexpr int kTileSlots = kRowsT / L::kSlotRows;
-  auto issue_slot = [&](int pages, int r0, int n) {   // n: slots issued before
-    const int at = n % L::kSlots, per = L::kSlotRows / piece, from = n % kTileSlots * per;
+  // Slot n of the CTA, of the tile whose pieces come from `src`.
+  auto issue_slot = [&](const uint8_t* src, int live, int n) {
+    const int at = n % L::kSlots, per = L::kSlotRows / lat_piece, from = n % kTileSlots * per;
     if (n >= L::kSlots)
       warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
-    const uint32_t live = __ballot_sync(0xffffffffu, lane >= from && lane < from + per && pages != -2);
-    const uint32_t full = bar(L::RAWFULL + at), dst = sbase + L::kOffRaw + at * L::kSlotBytes;
-    expect_tx_elected(full, __popc(live) * piece * (kQ4CodeBytes + kQ4ExpBytes));
-    copy_rows(pages, r0, from, from + per, 0, kQ4CodeBytes, dst, full);
-    copy_rows(pages, r0, from, from + per, kQ4CodeBytes + kQ4KeyBytes, kQ4ExpBytes,
-              dst + L::kSlotCodes, full);
+    copy_pieces(src, from, from + per, live, lat_piece * kQ4LatBytes,
+                sbase + L::kOffRaw + at * L::kSlotBytes, bar(L::RAWFULL + at));
   };
-  auto issue_keys = [&](int pages, int r0, int t) {
+  auto issue_keys = [&](int id, int r0, int t) {
     const int bf = t & 1;
+    const uint8_t* src = piece_source(id, r0, key_piece, kQ4LatBytes, kQ4KeyBytes);
     if (t >= 2) warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
-    const uint32_t live = __ballot_sync(0xffffffffu, pages != -2);
-    expect_tx_elected(bar(L::KEYFULL + bf), __popc(live) * piece * kQ4KeyBytes);
-    copy_rows(pages, r0, 0, kRowsT / piece, kQ4CodeBytes, kQ4KeyBytes,
-              sbase + L::kOffKeys + bf * kKeyTile, bar(L::KEYFULL + bf));
+    copy_pieces(src, 0, kRowsT / key_piece, __popc(__ballot_sync(0xffffffffu, id != -2)),
+                key_piece * kQ4KeyBytes, sbase + L::kOffKeys + bf * kKeyTile, bar(L::KEYFULL + bf));
   };
   // The query image of group v, by one thread.  (The scales stay behind: of a share this copy
   // may run ahead of the softmax, which reads them from global memory.)
@@ -314,9 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     mbar_arrive_expect_tx(bar(L::QREADY), L::kQBytes);
     bulk_g2s(sbase + L::kOffQ, img, L::kQBytes, bar(L::QREADY));
   };
-  // The producer's place: its next tile is tile i of `it`.
-  TileItem it;
-  int i = 0, pages = -2, slots = 0;   // slots issued
+  int slots = 0;   // slots issued (warp 8)
   if (warp == 8) {
     if (kShare) {
       share = take_share<false>(p, blockIdx.x / groups, gridDim.x / groups, lane, blockIdx.x == 0);
@@ -326,9 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       else
         T = 0;
     }
+    int id = -2, key_id = -2;
     if (T > 0) {
-      it = first;
-      pages = piece_page(it, 0);
+      id = piece_page(first, 0, lat_piece);
+      key_id = piece_page(first, 0, key_piece);
     }
     if (lane < L::kBars)
       // counts: decoded slots and tiles four warps; S read and P written eight; else one
@@ -341,8 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     fence_mbarrier_init();
     __syncwarp();
     if (T > 0) {   // the stream starts before the CTA's barrier
-      for (int s = 0; s < min(L::kSlots, kTileSlots); ++s) issue_slot(pages, it.r0, slots++);
-      if (L::kSlots >= kTileSlots) issue_keys(pages, it.r0, 0);
+      const uint8_t* src = piece_source(id, first.r0, lat_piece, 0, kQ4LatBytes);
+      const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
+      for (; slots < min(L::kSlots, kTileSlots); ++slots) issue_slot(src, live, slots);
+      issue_keys(key_id, first.r0, 0);
     }
     if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
   } else if (warp == 11 && lane < 16) {
@@ -373,36 +382,51 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
   }
   const uint32_t tmem = *slot_ptr;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ rows
-    int keys = L::kSlots >= kTileSlots ? 1 : 0;   // tiles whose keys are on their way
+  // Runs the tiles of the CTA, each with its pieces' pages: f(id, first row, t, first of a
+  // later item, that item); false: given up.
+  auto for_tiles = [&](int piece, auto&& f) {
+    TileItem it = first;
+    int i = 0, id = piece_page(it, 0, piece);
     for (int t = 0; t < T; ++t) {
-      if (__any_sync(0xffffffffu, *abort_flag)) break;
-      for (; slots < (t + 1) * kTileSlots; ++slots) issue_slot(pages, it.r0 + i * kRowsT, slots);
-      if (keys == t) {
-        issue_keys(pages, it.r0 + i * kRowsT, t);
-        ++keys;
-      }
-      if (kShare && i == 0 && t > 0) {
-        // A new item's query, once the last score MMA of the one before has read its own.
-        warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        if (lane == 0) {
-          pdl_wait();
-          load_query(it.v);
+      if (__any_sync(0xffffffffu, *abort_flag)) return;
+      const TileItem now = it;
+      const int at = i, now_id = id;
+      if (t + 1 < T) {
+        if (++i == it.tiles) {
+          it = item_after(it, t + 1);
+          i = 0;
         }
-        __syncwarp();
+        id = piece_page(it, i, piece);
       }
-      if (t + 1 >= T) break;
-      if (++i == it.tiles) {
-        it = item_after(it, t + 1);
-        i = 0;
-      }
-      pages = piece_page(it, i);
+      f(now_id, now.r0 + at * kRowsT, t, at == 0 && t > 0, now);
     }
+  };
+  if (warp == 8) {
+    // ------------------------------------------------------------ codes and exponents
+    for_tiles(lat_piece, [&](int id, int r0, int t, bool, const TileItem&) {
+      const uint8_t* src = piece_source(id, r0, lat_piece, 0, kQ4LatBytes);
+      const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
+      for (; slots < (t + 1) * kTileSlots; ++slots) issue_slot(src, live, slots);
+    });
     // Copies still in flight land before the CTA may leave (bounded waits).
     for (int n = max(0, slots - L::kSlots); n < slots; ++n)
       if (!mbar_wait_bounded(bar(L::RAWFULL + n % L::kSlots), (n / L::kSlots) & 1)) *abort_flag = 1;
+  } else if (warp == 15) {
+    // ------------------------------------------------------------ keys, later queries
+    int keys = T > 0 ? 1 : 0;   // tiles whose keys are on their way (the first from warp 8)
+    for_tiles(key_piece, [&](int id, int r0, int t, bool later, const TileItem& now) {
+      if (t > 0) issue_keys(id, r0, t);
+      keys = t + 1;
+      if (kShare && later) {
+        // A new item's query, once the last score MMA of the one before has read its own.
+        warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        if (!__any_sync(0xffffffffu, *abort_flag) && lane == 0) {
+          pdl_wait();
+          load_query(now.v);
+        }
+        __syncwarp();
+      }
+    });
     for (int t = max(0, keys - 2); t < keys; ++t)
       if (!mbar_wait_bounded(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
   } else if (warp > 10) {
@@ -432,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         uint32_t e[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-          w[k] = *reinterpret_cast<const uint4*>(raw + (8 * k + r) * kQ4CodeBytes + 16 * c);
-          e[k] = raw[L::kSlotCodes + (8 * k + r) * kQ4ExpBytes + c];
+          w[k] = *reinterpret_cast<const uint4*>(raw + (8 * k + r) * kQ4LatBytes + 16 * c);
+          e[k] = raw[(8 * k + r) * kQ4LatBytes + kQ4CodeBytes + c];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + at));

@@ -65,15 +65,16 @@ def pack(code, e, key):
     at = np.arange(8)[None, :] ^ (np.arange(R)[:, None] & 7)
     moved = np.empty_like(k)
     np.put_along_axis(moved, np.broadcast_to(at[None, :, :, None], k.shape), k, 2)
-    return np.concatenate([c.reshape(n, -1), moved.reshape(n, -1), x.reshape(n, -1)], 1)
+    return np.concatenate([np.concatenate([c, x], -1).reshape(n, -1), moved.reshape(n, -1)], 1)
 
 
 def unpack(pool, page):
     """pack()'s arguments of a pool's bytes."""
     n = pool.size // (page * ROW_BYTES)
     p = np.asarray(pool, np.uint8).reshape(n, page * ROW_BYTES)
-    c, k, x = np.split(p, [page * 256, page * 384], 1)
-    c, k, x = c.reshape(n, page, 256), k.reshape(n, page, 8, 16), x.reshape(n, page, 16)
+    c, k = np.split(p, [page * 272], 1)
+    c, k = c.reshape(n, page, 272), k.reshape(n, page, 8, 16)
+    c, x = c[..., :256], c[..., 256:]
     code = np.stack([c & 15, c >> 4], -1).reshape(n, page, D_C).astype(np.int64)
     e = np.stack([x & 15, x >> 4], -1).reshape(n, page, D_C // BLOCK).astype(np.int64) + E_MIN
     at = np.arange(8)[None, :] ^ (np.arange(page)[:, None] & 7)

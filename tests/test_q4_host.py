@@ -64,11 +64,11 @@ def test_pack_and_unpack(page):
     assert pool.shape == (3, page * 400)
     for a, b in zip(F.unpack(pool, page), (code, e, key)):
         assert (a == b).all()
-    # rows by their own bytes: codes, then keys, then exponents
+    # rows by their own bytes: codes and exponents, then keys
     flat = pool[1]
-    assert flat[5 * 256 + 7] == code[1, 5, 14] | code[1, 5, 15] << 4
-    assert flat[page * 384 + 5 * 16 + 3] == (e[1, 5, 6] + 8) | (e[1, 5, 7] + 8) << 4
-    piece = flat[page * 256 + 5 * 128:][:128].reshape(8, 16)[2 ^ 5]
+    assert flat[5 * 272 + 7] == code[1, 5, 14] | code[1, 5, 15] << 4
+    assert flat[5 * 272 + 256 + 3] == (e[1, 5, 6] + 8) | (e[1, 5, 7] + 8) << 4
+    piece = flat[page * 272 + 5 * 128:][:128].reshape(8, 16)[2 ^ 5]
     assert (piece.view(np.uint16) == key[1, 5, 16:24]).all()
 
 
