@@ -12,8 +12,10 @@
 //
 // A page of R rows is two planes, 400 R bytes in all, so that the rows of a tile are two
 // contiguous copies:
-//   latents [R][272]  256 bytes of codes, byte i: values 2 i (low four bits) and 2 i + 1, then
-//                     16 of exponents, byte i: e + 8 of blocks 2 i (low four bits) and 2 i + 1
+//   latents [R][272]  256 bytes of codes, a 32-bit word for eight values: the magnitude of
+//                     value k in bits 4 k .. 4 k + 2, the signs of values 0-3 in bits 7, 15,
+//                     23, 31 and of 4-7 in bits 3, 11, 19, 27 (where a reader wants them);
+//                     then 16 of exponents, byte i: e + 8 of blocks 2 i (low four bits), 2 i + 1
 //   keys    [R][128]  16-byte piece c of row r stands at piece c ^ (r & 7): as the tensor core
 //                     wants it in shared memory (128-byte swizzle)
 #pragma once
@@ -55,8 +57,20 @@ __device__ __forceinline__ float q4_unit(uint32_t bits) {
   return __uint_as_float((min(bits & 15u, 14u) + static_cast<uint32_t>(127 + kQ4ExpMin)) << 23);
 }
 
+// Eight codes, value k in bits 4 k .. 4 k + 3, as a page holds them, and back.
+__device__ __forceinline__ uint32_t q4_page_word(uint32_t w) {
+  const uint32_t odd = w << 4;
+  return (w & 0x77777777u) | (__byte_perm(odd, w, 0x5140) & 0x80808080u) |
+         (__byte_perm(odd, w, 0x7362) & 0x80808080u) >> 4;
+}
+__device__ __forceinline__ uint32_t q4_codes(uint32_t w) {
+  const uint32_t low = w & 0x80808080u, high = (w << 4) & 0x80808080u;
+  return (w & 0x77777777u) | __byte_perm(low, high, 0x6420) >> 4 | __byte_perm(low, high, 0x7531);
+}
+
 // Eight codes as loaded, to values in units of 2^e.
-__device__ __forceinline__ void q4_values(uint32_t codes, float unit, float* v) {
+__device__ __forceinline__ void q4_values(uint32_t word, float unit, float* v) {
+  const uint32_t codes = q4_codes(word);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(

@@ -10,24 +10,27 @@
 // the tensor cores as in the E4M3 cache's kernel (kind::f8f6f4, fp32 accumulators), and the
 // keys, stored as the tensor core wants them, as kind::f16:
 //   scores  S[128 rows x 16 parts] = C[128 x 512] . Q^T,  Sk[128 x 16] = K[128 x 64] . Qk^T
-//   output  O^T[128 latent x 48] += C^T[128 x 128 rows] . P^T   per 128-column block
+//   output  O^T[128 latent x 16 parts] += C^T[128 x 128 rows] . P^T   per 128-column block
 // A bf16 query is two E4M3 parts (weights 1, 1/16; exact to 2^-21 of the head's largest
-// value) in units of a power of two per head, an fp32 one four (and its key part a bf16 hi
-// and lo); P is three parts (weights 1, 1/16, 1/256).
+// value) in units of a power of two per head, and P two parts (at most 2^-8 relative, less in
+// the weighted sum than the bf16 output's own rounding); an fp32 query is four parts, its key
+// part a bf16 hi and lo, and P three.  With two parts of P the softmax's reference stays 2^5
+// below the running maximum, so that the smallest step is 2^-19 of the largest weight, and O
+// is rescaled when a maximum passes it by 2^3.5.
 //
 // From codes to E4M3: a byte permute looks the eight magnitudes of a block's exponent up in
 // two registers, four codes at a time (the selector is the codes themselves), and the signs
-// are put on by another: nine operations for eight values, no conversion (which would run at
-// an eighth of the rate) and no multiplication.
+// lie where the bytes want them: seven operations for eight values, no conversion (which
+// would run at an eighth of the rate) and no multiplication.
 //
-// Warp roles (512 threads, one CTA per SM):
+// Warp roles (640 threads, one CTA per SM):
 //   warps 0-7    softmax (one tile row per thread, heads 0-7 in warps 0-3, 8-15 in 4-7),
 //                P, epilogue
 //   warp 8       copies of codes and exponents (and TMEM allocation)
 //   warp 9       score MMAs of each tile (20 instructions)
 //   warp 10      the first query image's copy, then the PV MMAs of each tile (16)
-//   warps 11-14  codes to E4M3
-//   warp 15      copies of keys, and of the later items' query images
+//   warp 11      copies of keys, and of the later items' query images
+//   warps 12-19  codes to E4M3, two teams of four warps in turn
 // (A copy takes its warp some 450 cycles among the others' work: one warp for all of a
 // tile's, and exponents in a plane of their own, took 6600 cycles a tile.)
 #include "mla_q4.cuh"
@@ -39,15 +42,12 @@ constexpr int kRowsT = 128;                   // rows per tile (the MMA's M)
 constexpr int kBox = kRowsT * 128;            // 128 latent columns of a tile: 16 KB
 constexpr int kTile = 4 * kBox;               // 64 KB of E4M3
 constexpr int kKeyTile = kRowsT * kQ4KeyBytes;   // 16 KB of bf16 keys
-constexpr int kSoft = 256, kDecode = 128;
-constexpr int kThreads = kSoft + 3 * 32 + kDecode + 32;
-constexpr int kPParts = 3;
+constexpr int kSoft = 256;
+constexpr int kTeam = 128, kTeams = 2;        // threads of a decoding team, and teams
+constexpr int kThreads = kSoft + 4 * 32 + kTeams * kTeam;
 constexpr int kHalf = kHeadGroup / 2;         // heads per softmax warp group
-constexpr int kPN = kPParts * kHeadGroup;     // P rows of the PV MMA (part-major)
-constexpr int kPBuf = kPN * 128;              // 6 KB: 48 rows of 128 tile rows
-constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64, O^T at 128..319, Sk[2] at 320 / 352
+constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64, O^T from 128 to 319, Sk[2] at 320 / 352
 constexpr uint32_t kOCol = 128, kKCol = 320;
-constexpr float kRescaleLog2 = 8.f;
 
 // The query of one (sequence, 16-head group) as shared memory holds it: four 128-column
 // boxes of (parts x 16) rows x 128 bytes, the key part's (hi, or hi and lo) x 16 rows x 128
@@ -55,13 +55,22 @@ constexpr float kRescaleLog2 = 8.f;
 template <bool kF32>
 struct Q4Plan {
   static constexpr int kQParts = kF32 ? 4 : 2, kKParts = kF32 ? 2 : 1;
+  static constexpr int kPParts = kF32 ? 3 : 2;
+  static constexpr int kPN = kPParts * kHeadGroup;   // P rows of the PV MMA (part-major)
+  static constexpr int kPBuf = kPN * 128;            // of 128 tile rows
+  // Reference of the softmax below the running maximum, and how far above the reference a
+  // score may lie (log2): weights stay below E4M3's 448.
+  static constexpr float kBias = kF32 ? 0.f : 5.f, kTop = kF32 ? 8.f : 8.5f;
   static constexpr int kQN = kQParts * kHeadGroup, kKN = kKParts * kHeadGroup;
   static constexpr int kQBox = kQN * 128;
   static constexpr int kQKeys = 4 * kQBox;                  // offset of the key part
   static constexpr int kQBytes = kQKeys + kKN * 128;        // of the scales
   static_assert(size_t(kQBytes) + 64 <= kFp8QImage, "query image in the workspace");
-  // Rows arrive in slots, whose length is what room is left.
-  static constexpr int kSlotRows = kF32 ? 16 : 32, kSlots = kF32 ? 3 : 4;
+  // Rows arrive in slots, whose length is what room is left.  Their number is a multiple of
+  // the teams that decode them in turn: each team then meets every phase of its slots (a
+  // parity wait that skips one passes too early).
+  static constexpr int kSlotRows = kF32 ? 16 : 32, kSlots = 4;
+  static_assert(kSlots % kTeams == 0 && (kRowsT / kSlotRows) % kTeams == 0, "slots by team");
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kOffTile = 0;
   static constexpr int kOffKeys = kOffTile + 2 * kTile;
@@ -69,12 +78,12 @@ struct Q4Plan {
   static constexpr int kOffP = kOffQ + kQBytes;
   static constexpr int kOffRaw = kOffP + 2 * kPBuf;
   static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;   // [16] magnitudes by exponent
-  static constexpr int kOffRed = kOffTable + 16 * 8;                // [2][16 heads][4 warps] maxima
-  static constexpr int kOffLsum = kOffRed + 2 * kHeadGroup * 4 * 4;
+  static constexpr int kOffRed = kOffTable + 16 * 8;                // [16 heads][4 warps] maxima
+  static constexpr int kOffLsum = kOffRed + kHeadGroup * 4 * 4;
   static constexpr int kOffBar = kOffLsum + kHeadGroup * 4 * 4;
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots,   // rows landed / decoded
                        KEYFULL = RAWEMPTY + kSlots,   // [2] keys of the tile landed
-                       CFULL = KEYFULL + 2,           // [2] tile decoded
+                       CFULL = KEYFULL + 2,           // [2] tile decoded (both teams)
                        SFULL = CFULL + 2,             // [2] scores of the tile (keys free again)
                        SFREE = SFULL + 2,             // [2] softmax read them
                        PFULL = SFREE + 2,             // [2] P of the tile written
@@ -149,12 +158,22 @@ __device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
 // Where the rows of a page that does not exist come from.
 __device__ __align__(128) uint8_t g_q4_zeros[kRowsT * kQ4LatBytes];
 
-// Eight codes as E4M3 bytes; (lo, hi): the E4M3 magnitudes of codes 0-3 and 4-7.
+// Eight codes as E4M3 bytes; mag: the E4M3 magnitudes of codes 0-3 and 4-7.
 __device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
-  const uint32_t sel = w & 0x77777777u, odd = w << 4;
-  const uint32_t m0 = __byte_perm(mag.x, mag.y, sel), m1 = __byte_perm(mag.x, mag.y, sel >> 16);
-  const uint32_t s0 = __byte_perm(odd, w, 0x5140), s1 = __byte_perm(odd, w, 0x7362);
-  return make_uint2(m0 | (s0 & 0x80808080u), m1 | (s1 & 0x80808080u));
+  const uint32_t sel = w & 0x77777777u;
+  return make_uint2(__byte_perm(mag.x, mag.y, sel) | (w & 0x80808080u),
+                    __byte_perm(mag.x, mag.y, sel >> 16) | ((w << 4) & 0x80808080u));
+}
+// Whether `x` holds for any of `count` threads (named barrier `bar`).
+__device__ __forceinline__ bool any_of(bool x, int bar, int count) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(bar), "r"(count)
+      : "memory");
+  return r != 0;
 }
 
 // The query image of one (query group b, head h): q_abs (512 values) becomes sigma (a1 + a2 /
@@ -301,19 +320,26 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
   const int key_piece = min(1 << p.page_shift, kRowsT);
   constexpr int kTileSlots = kRowsT / L::kSlotRows;
   // Slot n of the CTA, of the tile whose pieces come from `src`.
-  auto issue_slot = [&](const uint8_t* src, int live, int n) {
+  auto issue_slot = [&](const uint8_t* src, int live, int n) {   // false: given up
     const int at = n % L::kSlots, per = L::kSlotRows / lat_piece, from = n % kTileSlots * per;
-    if (n >= L::kSlots)
+    if (n >= L::kSlots) {
       warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    }
     copy_pieces(src, from, from + per, live, lat_piece * kQ4LatBytes,
                 sbase + L::kOffRaw + at * L::kSlotBytes, bar(L::RAWFULL + at));
+    return true;
   };
-  auto issue_keys = [&](int id, int r0, int t) {
+  auto issue_keys = [&](int id, int r0, int t) {   // false: given up
     const int bf = t & 1;
     const uint8_t* src = piece_source(id, r0, key_piece, kQ4LatBytes, kQ4KeyBytes);
-    if (t >= 2) warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
+    if (t >= 2) {
+      warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
+      if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    }
     copy_pieces(src, 0, kRowsT / key_piece, __popc(__ballot_sync(0xffffffffu, id != -2)),
                 key_piece * kQ4KeyBytes, sbase + L::kOffKeys + bf * kKeyTile, bar(L::KEYFULL + bf));
+    return true;
   };
   // The query image of group v, by one thread.  (The scales stay behind: of a share this copy
   // may run ahead of the softmax, which reads them from global memory.)
@@ -338,12 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       key_id = piece_page(first, 0, key_piece);
     }
     if (lane < L::kBars)
-      // counts: decoded slots and tiles four warps; S read and P written eight; else one
-      mbar_init(bar(lane), lane >= L::SFREE && lane < L::ODONE ? 8
-                           : (lane >= L::RAWEMPTY && lane < L::KEYFULL) ||
-                                     (lane >= L::CFULL && lane < L::SFULL)
-                               ? kDecode / 32
-                               : 1);
+      // counts: slots decoded by four warps, tiles by eight; S read and P written eight
+      mbar_init(bar(lane), (lane >= L::SFREE && lane < L::ODONE) ||
+                                   (lane >= L::CFULL && lane < L::SFULL)
+                               ? 8
+                           : lane >= L::RAWEMPTY && lane < L::KEYFULL ? kTeam / 32
+                                                                      : 1);
     if (lane == 0) *abort_flag = 0;
     fence_mbarrier_init();
     __syncwarp();
@@ -354,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       issue_keys(key_id, first.r0, 0);
     }
     if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
-  } else if (warp == 11 && lane < 16) {
+  } else if (warp == 12 && lane < 16) {
     // Magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^(lane - 8) as E4M3 (15 as 14).
     uint32_t w[4];
 #pragma unroll
@@ -406,17 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     for_tiles(lat_piece, [&](int id, int r0, int t, bool, const TileItem&) {
       const uint8_t* src = piece_source(id, r0, lat_piece, 0, kQ4LatBytes);
       const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
-      for (; slots < (t + 1) * kTileSlots; ++slots) issue_slot(src, live, slots);
+      while (slots < (t + 1) * kTileSlots && issue_slot(src, live, slots)) ++slots;
     });
     // Copies still in flight land before the CTA may leave (bounded waits).
     for (int n = max(0, slots - L::kSlots); n < slots; ++n)
       if (!mbar_wait_bounded(bar(L::RAWFULL + n % L::kSlots), (n / L::kSlots) & 1)) *abort_flag = 1;
-  } else if (warp == 15) {
+  } else if (warp == 11) {
     // ------------------------------------------------------------ keys, later queries
     int keys = T > 0 ? 1 : 0;   // tiles whose keys are on their way (the first from warp 8)
     for_tiles(key_piece, [&](int id, int r0, int t, bool later, const TileItem& now) {
-      if (t > 0) issue_keys(id, r0, t);
-      keys = t + 1;
+      if (t > 0 && issue_keys(id, r0, t)) keys = t + 1;
       if (kShare && later) {
         // A new item's query, once the last score MMA of the one before has read its own.
         warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
@@ -429,47 +454,53 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     });
     for (int t = max(0, keys - 2); t < keys; ++t)
       if (!mbar_wait_bounded(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
-  } else if (warp > 10) {
+  } else if (warp > 11) {
     // ------------------------------------------------------------ codes to E4M3
-    // Thread d of 128: 16 bytes of codes (32 values, one byte of exponents) of rows d / 16,
-    // 8 + d / 16, ... of a slot: a warp reads two whole rows.  Of the two 16-byte pieces a
-    // thread writes, odd boxes' threads write the second first: eight threads of one row then
-    // meet eight different pieces of the banks.
-    const int d = tid - (kSoft + 3 * 32), c = d & 15, r = d >> 4;
-    const uint2* table = reinterpret_cast<const uint2*>(smem + L::kOffTable);
-    const int box = c >> 2, swap = box & 1;
-    int n = 0;
+    // Teams take slots in turn.  Thread d of a team: 16 bytes of codes (32 values, one byte of
+    // exponents) of rows d / 16, 8 + d / 16, ... of a slot, so that a warp reads two whole
+    // rows.  They are read and written as halves, of which odd boxes' threads take the second
+    // first: eight threads of one row then write to eight different pieces of the banks.
+    const int team = (warp - 12) >> 2, d = (tid - kSoft) & (kTeam - 1), c = d & 15, r = d >> 4;
+    const int swap = (c >> 2) & 1;
+    const uint8_t* from = smem + L::kOffRaw + r * kQ4LatBytes;
+    const uint8_t* table = smem + L::kOffTable;
+    uint8_t* to = smem + L::kOffTile + (c >> 2) * kBox;
+    // (a slot's first row is a multiple of eight: the swizzle goes by r)
+    const uint32_t to0 = sw128(r, 2 * (c & 3) + swap), to1 = sw128(r, 2 * (c & 3) + 1 - swap);
+    const int at0 = 16 * c + 8 * swap, at1 = 16 * c + 8 - 8 * swap, sh0 = 4 * swap, sh1 = 4 - 4 * swap;
+    int n = team;
     for (int t = 0; t < T; ++t) {
-      uint8_t* tile = smem + L::kOffTile + (t & 1) * kTile + box * kBox;
+      uint8_t* tile = to + (t & 1) * kTile;
       if (t >= 2) {
         warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
         tc_fence_after();
       }
       if (__any_sync(0xffffffffu, *abort_flag)) break;
 #pragma unroll 1
-      for (int s = 0; s < kTileSlots; ++s, ++n) {
-        const int at = n % L::kSlots;
-        warp_wait(bar(L::RAWFULL + at), (n / L::kSlots) & 1, abort_flag);
-        const uint8_t* raw = smem + L::kOffRaw + at * L::kSlotBytes;
+      for (int s = team; s < kTileSlots; s += kTeams, n += kTeams) {
+        const int slot = n % L::kSlots;
+        warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
+        const uint8_t* raw = from + slot * L::kSlotBytes;
         constexpr int kEach = L::kSlotRows / 8;
-        uint4 w[kEach];
+        uint2 w0[kEach], w1[kEach];
         uint32_t e[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-          w[k] = *reinterpret_cast<const uint4*>(raw + (8 * k + r) * kQ4LatBytes + 16 * c);
-          e[k] = raw[(8 * k + r) * kQ4LatBytes + kQ4CodeBytes + c];
+          e[k] = raw[8 * k * kQ4LatBytes + kQ4CodeBytes + c];
+          w0[k] = *reinterpret_cast<const uint2*>(raw + 8 * k * kQ4LatBytes + at0);
+          w1[k] = *reinterpret_cast<const uint2*>(raw + 8 * k * kQ4LatBytes + at1);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + at));
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+        uint8_t* rows = tile + s * L::kSlotRows * 128;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-          const uint2 m0 = table[e[k] & 15], m1 = table[e[k] >> 4];
-          const uint2 a = decode8(w[k].x, m0), b = decode8(w[k].y, m0);
-          const uint2 x = decode8(w[k].z, m1), y = decode8(w[k].w, m1);
-          const uint4 v0 = make_uint4(a.x, a.y, b.x, b.y), v1 = make_uint4(x.x, x.y, y.x, y.y);
-          const int row = L::kSlotRows * s + 8 * k + r, u = 2 * (c & 3) + swap;
-          *reinterpret_cast<uint4*>(tile + sw128(row, u)) = swap ? v1 : v0;
-          *reinterpret_cast<uint4*>(tile + sw128(row, u ^ 1)) = swap ? v0 : v1;
+          const uint2 m0 = *reinterpret_cast<const uint2*>(table + ((e[k] >> sh0) & 15) * 8);
+          const uint2 m1 = *reinterpret_cast<const uint2*>(table + ((e[k] >> sh1) & 15) * 8);
+          const uint2 a = decode8(w0[k].x, m0), b = decode8(w0[k].y, m0);
+          *reinterpret_cast<uint4*>(rows + 1024 * k + to0) = make_uint4(a.x, a.y, b.x, b.y);
+          const uint2 x = decode8(w1[k].x, m1), y = decode8(w1[k].y, m1);
+          *reinterpret_cast<uint4*>(rows + 1024 * k + to1) = make_uint4(x.x, x.y, y.x, y.y);
         }
       }
       fence_proxy_async_smem();
@@ -530,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       load_query(first.v);
     }
     __syncwarp();
-    constexpr uint32_t idesc_o = idesc_e4m3(128, kPN, 1);
+    constexpr uint32_t idesc_o = idesc_e4m3(128, L::kPN, 1);
     const uint64_t p0 = umma_desc_sw128(sbase + L::kOffP, 16, 1024);
     const uint64_t c0 = umma_desc_sw128(sbase + L::kOffTile, kBox, 1024);
     TileItem cur = first;
@@ -544,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
-      const uint64_t pd = p0 + static_cast<uint64_t>((bf * kPBuf) >> 4);
+      const uint64_t pd = p0 + static_cast<uint64_t>((bf * L::kPBuf) >> 4);
 #pragma unroll 1
       for (int mb = 0; mb < 4; ++mb) {
         // C^T block mb: latent columns 128 mb.. (MN-major, one 128-byte
@@ -552,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const uint64_t c = c0 + static_cast<uint64_t>((bf * kTile + mb * kBox) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
-          umma_e4m3(tmem + kOCol + kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
+          umma_e4m3(tmem + kOCol + L::kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
                     idesc_o, ks > 0 ? 1u : (done > 0 ? 1u : 0u));
       }
       umma_commit_elected(bar(L::ODONE + bf));
@@ -594,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const int valid = t == t0 + tiles - 1 ? last_valid : kRowsT;
         warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
         tc_fence_after();
-        float sc[kHalf], tt[kHalf];
+        float sc[kHalf];
         {
           uint32_t s[L::kQParts][8], sk[L::kKParts][8];
 #pragma unroll
@@ -613,41 +644,39 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             float k = __uint_as_float(sk[0][h]);
             if (kF32) k += __uint_as_float(sk[L::kKParts - 1][h]);
             sc[h] = rv ? fmaf(x, qsig[h], k * p.scale_log2) : -INFINITY;
-            tt[h] = sc[h];
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::SFREE + sb));
-        // tile maximum per head: warp, then the group's four warps
-#pragma unroll
-        for (int h = 0; h < kHalf; ++h)
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1)
-            tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
-        float* rd = red + sb * kHeadGroup * 4;
-        if (lane < kHalf) {
-          float v = tt[0];
-#pragma unroll
-          for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
-          rd[(hb + lane) * 4 + wq] = v;
-        }
-        named_bar_sync(1, kSoft);
         bool need = false;
-        float tmax[kHalf];
 #pragma unroll
-        for (int h = 0; h < kHalf; ++h) {
-          const float4 q4 = *reinterpret_cast<const float4*>(rd + (hb + h) * 4);
-          tmax[h] = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
-          need |= tmax[h] > m[h] + kRescaleLog2;
-        }
-        if (need) {
-          // Move this group's reference maxima; rescale its row sums and the O^T
-          // columns it owns (in TMEM, after the previous PV finished).
+        for (int h = 0; h < kHalf; ++h) need |= sc[h] > m[h] + L::kTop;
+        if (any_of(need, 1 + gp, kSoft / 2)) {
+          // Some score is too far above its head's reference: the tile's maxima (warp, then
+          // the group's four warps) move the references of this group's heads; rescale its row
+          // sums and the O^T columns it owns (in TMEM, after the previous PV finished).
+          float tt[kHalf];
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {
+            tt[h] = sc[h];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+              tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
+          }
+          if (lane < kHalf) {
+            float v = tt[0];
+#pragma unroll
+            for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
+            red[(hb + lane) * 4 + wq] = v;
+          }
+          named_bar_sync(3 + gp, kSoft / 2);
           float alpha[kHalf];
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
-            const float mn = fmaxf(m[h], tmax[h]);
+            const float4 q4 = *reinterpret_cast<const float4*>(red + (hb + h) * 4);
+            const float mn =
+                fmaxf(m[h], fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
             alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
             m[h] = mn;
             l[h] *= alpha[h];
@@ -658,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-              for (int part = 0; part < kPParts; ++part) {
-                const uint32_t col = kOCol + kPN * mb + kHeadGroup * part + hb;
+              for (int part = 0; part < L::kPParts; ++part) {
+                const uint32_t col = kOCol + L::kPN * mb + kHeadGroup * part + hb;
                 uint32_t r[8];
                 float o[8];
                 tmem_ld8_nowait(tmem + lane_base + col, r);
@@ -672,40 +701,41 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             tmem_wait_st();
           }
         }
-        // p in [0, 2^8] as three E4M3 parts, two heads per conversion; the row
-        // sum takes the value the PV uses.
-        uint16_t pp[kPParts][kHalf / 2];
+        // p as E4M3 parts, two heads per conversion.  Of three parts the row sum takes the
+        // value that the PV uses.
+        uint16_t pp[L::kPParts][kHalf / 2];
 #pragma unroll
         for (int h2 = 0; h2 < kHalf / 2; ++h2) {
-          float v0, v1;
-          {
-            const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
-            const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
-            v0 = ex2(sc[2 * h2] - mu0);
-            v1 = ex2(sc[2 * h2 + 1] - mu1);
+          const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
+          const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
+          float v0 = ex2(sc[2 * h2] - mu0), v1 = ex2(sc[2 * h2 + 1] - mu1);
+          if (!kF32) {
+            l[2 * h2] += v0;
+            l[2 * h2 + 1] += v1;
           }
-          float used0 = 0.f, used1 = 0.f, wgt = 1.f;
+          float wgt = 1.f;
 #pragma unroll
-          for (int part = 0; part < kPParts; ++part) {
+          for (int part = 0; part < L::kPParts; ++part) {
             pp[part][h2] = to_e4m3x2(v0, v1);
+            if (!kF32 && part == L::kPParts - 1) break;
             const float2 f = from_e4m3x2(pp[part][h2]);
-            used0 += f.x * wgt;
-            used1 += f.y * wgt;
+            if (kF32) {
+              l[2 * h2] = fmaf(f.x, wgt, l[2 * h2]);
+              l[2 * h2 + 1] = fmaf(f.y, wgt, l[2 * h2 + 1]);
+            }
             v0 = (v0 - f.x) * 16.f;
             v1 = (v1 - f.y) * 16.f;
             wgt *= 0.0625f;
           }
-          l[2 * h2] += used0;
-          l[2 * h2 + 1] += used1;
         }
         // P^T buffer sb was last read by the PV of tile t-2.
         if (t >= 2) warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
         {
           // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
           // 16 part + n is part `part` of head n; the K index is the tile row.
-          uint8_t* pbuf = smem + L::kOffP + sb * kPBuf;
+          uint8_t* pbuf = smem + L::kOffP + sb * L::kPBuf;
 #pragma unroll
-          for (int part = 0; part < kPParts; ++part)
+          for (int part = 0; part < L::kPParts; ++part)
 #pragma unroll
             for (int h2 = 0; h2 < kHalf / 2; ++h2) {
               pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2, row)] = pp[part][h2] & 0xFF;
@@ -739,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
       warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
-      named_bar_sync(1, kSoft);
+      named_bar_sync(3 + gp, kSoft / 2);
       if (!*abort_flag) {
         const size_t base = (size_t(out.v) * p.H + h0) * p.splits + out.j;
         // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
@@ -761,17 +791,18 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const size_t head_stride = size_t(p.splits) * kDc;
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
-          uint32_t o1[8], o2[8], o3[8];
-          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + hb, o1);
-          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + kHeadGroup + hb, o2);
-          tmem_ld8_nowait(tmem + lane_base + kOCol + kPN * mb + 2 * kHeadGroup + hb, o3);
+          uint32_t o[L::kPParts][8];
+#pragma unroll
+          for (int i = 0; i < L::kPParts; ++i)
+            tmem_ld8_nowait(tmem + lane_base + kOCol + L::kPN * mb + kHeadGroup * i + hb, o[i]);
           tmem_wait_ld();
           float* at = row0 + 128 * mb;
 #pragma unroll
           for (int h = 0; h < kHalf; ++h, at += head_stride) {
-            const float v = (__uint_as_float(o1[h]) + (__uint_as_float(o2[h]) * 0.0625f +
-                                                       __uint_as_float(o3[h]) * 0.00390625f)) *
-                            inv[h];
+            float v = __uint_as_float(o[L::kPParts - 1][h]);
+#pragma unroll
+            for (int i = L::kPParts - 2; i >= 0; --i) v = fmaf(v, 0.0625f, __uint_as_float(o[i][h]));
+            v *= inv[h];
             if (p.direct && p.io_bf16)
               reinterpret_cast<__nv_bfloat16*>(p.part_o)[at - p.part_o] = __float2bfloat16_rn(v);
             else

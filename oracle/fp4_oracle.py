@@ -11,6 +11,9 @@ import numpy as np
 D_C, D_R, BLOCK = 512, 64, 16
 ROW_BYTES = 400
 E_MIN, E_MAX = -8, 6
+# bits of a 32-bit word of eight codes: their magnitudes' lowest, and their signs
+MAG = np.arange(0, 32, 4, dtype=np.uint64)
+SIGN = np.array([7, 15, 23, 31, 3, 11, 19, 27], np.uint64)
 GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 
@@ -58,7 +61,9 @@ def pack(code, e, key):
     """Pages [n, R] of codes [n, R, 512], exponents [n, R, 32] (-8 .. 7: 7 is no exponent and
     reads as 6) and key bits [n, R, 64] uint16 as the pool's bytes [n, R * 400]."""
     n, R = code.shape[:2]
-    c = (code[..., 0::2] | code[..., 1::2] << 4).astype(np.uint8)
+    w = np.asarray(code, np.uint64).reshape(n, R, D_C // 8, 8)
+    word = ((w & np.uint64(7)) << MAG).sum(-1) | ((w >> np.uint64(3)) << SIGN).sum(-1)
+    c = word.astype("<u4").view(np.uint8).reshape(n, R, D_C // 2)
     u = (np.asarray(e) - E_MIN)
     x = (u[..., 0::2] | u[..., 1::2] << 4).astype(np.uint8)
     k = np.ascontiguousarray(key).view(np.uint8).reshape(n, R, 8, 16)
@@ -75,7 +80,8 @@ def unpack(pool, page):
     c, k = np.split(p, [page * 272], 1)
     c, k = c.reshape(n, page, 272), k.reshape(n, page, 8, 16)
     c, x = c[..., :256], c[..., 256:]
-    code = np.stack([c & 15, c >> 4], -1).reshape(n, page, D_C).astype(np.int64)
+    w = np.ascontiguousarray(c).view("<u4").astype(np.uint64)[..., None]
+    code = ((w >> MAG & np.uint64(7)) | (w >> SIGN & np.uint64(1)) << np.uint64(3)).reshape(n, page, D_C).astype(np.int64)
     e = np.stack([x & 15, x >> 4], -1).reshape(n, page, D_C // BLOCK).astype(np.int64) + E_MIN
     at = np.arange(8)[None, :] ^ (np.arange(page)[:, None] & 7)
     key = np.take_along_axis(k, np.broadcast_to(at[None, :, :, None], k.shape), 2)

@@ -59,14 +59,14 @@ def make_pool(rng, lengths, page, extra_pages=3, width=None, gain=None):
 def bounds(q, rows, p, z, io, heads, q_len):
     """Elementwise bounds of |o - exact| and |lse - exact| for one token.
 
-    Every cached value is exact in the tensor cores' operands.  Up to 32 query rows a
-    sequence, and fp32 queries: the E4M3 cache's bounds (a query within 2^-16 of the head's
-    largest value, weights within 2^-12 and 2^-18 of the largest one).  More bf16 rows may
-    run as SM pairs, whose weights are an E4M3 part and its E5M2 remainder (2^-7, 2^-19):
-    the larger of the two.
+    Every cached value is exact in the tensor cores' operands.  fp32 queries: the E4M3
+    cache's bounds (a query within 2^-16 of the head's largest value, weights within 2^-12
+    and 2^-18 of the largest one).  bf16 queries: weights are two E4M3 parts (half a step
+    is 2^-4 of each: 2^-8, and 2^-19 of the largest weight) or, in SM pairs, a part and its
+    E5M2 remainder (2^-7, 2^-19); queries within 2^-17 of the head's largest value.
     """
     one = attention_bounds(q, rows, p, z, "fp8", torch.float32, heads, q_len)
-    if io == torch.float32 or heads * q_len < 32:
+    if io == torch.float32:
         return one
     two = attention_bounds(q, rows, p, z, "fp8", io, max(heads, 48), q_len)
     return np.maximum(one[0], two[0]), np.maximum(one[1], two[1])
