@@ -456,18 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (!mbar_wait_bounded(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1)) *abort_flag = 1;
   } else if (warp > 11) {
     // ------------------------------------------------------------ codes to E4M3
-    // Teams take slots in turn.  Thread d of a team: 16 bytes of codes (32 values, one byte of
-    // exponents) of rows d / 16, 8 + d / 16, ... of a slot, so that a warp reads two whole
-    // rows.  They are read and written as halves, of which odd boxes' threads take the second
-    // first: eight threads of one row then write to eight different pieces of the banks.
-    const int team = (warp - 12) >> 2, d = (tid - kSoft) & (kTeam - 1), c = d & 15, r = d >> 4;
-    const int swap = (c >> 2) & 1;
-    const uint8_t* from = smem + L::kOffRaw + r * kQ4LatBytes;
+    // Teams take slots in turn; warp m of a team decodes box m of a slot, a row (or, of slots
+    // of 16 rows, half of one) per lane: rows are 17 times 16 bytes apart, so eight lanes read
+    // from eight different pieces of the banks, and the swizzle has them write so too.
+    const int team = (warp - 12) >> 2, m = (warp - 12) & 3;
+    const int r = lane % L::kSlotRows, part = lane / L::kSlotRows;
+    constexpr int kEach = L::kSlotRows / 8;   // 16-byte pieces of codes (32 values) a lane
+    const uint8_t* from = smem + L::kOffRaw + r * kQ4LatBytes + 64 * m + 16 * kEach * part;
+    const uint8_t* exps = smem + L::kOffRaw + r * kQ4LatBytes + kQ4CodeBytes + 4 * m;
     const uint8_t* table = smem + L::kOffTable;
-    uint8_t* to = smem + L::kOffTile + (c >> 2) * kBox;
-    // (a slot's first row is a multiple of eight: the swizzle goes by r)
-    const uint32_t to0 = sw128(r, 2 * (c & 3) + swap), to1 = sw128(r, 2 * (c & 3) + 1 - swap);
-    const int at0 = 16 * c + 8 * swap, at1 = 16 * c + 8 - 8 * swap, sh0 = 4 * swap, sh1 = 4 - 4 * swap;
+    uint8_t* to = smem + L::kOffTile + m * kBox + r * 128;
+    const uint32_t swz = (r & 7) << 4, unit0 = 2 * kEach * part;
     int n = team;
     for (int t = 0; t < T; ++t) {
       uint8_t* tile = to + (t & 1) * kTile;
@@ -480,28 +479,40 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       for (int s = team; s < kTileSlots; s += kTeams, n += kTeams) {
         const int slot = n % L::kSlots;
         warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
-        const uint8_t* raw = from + slot * L::kSlotBytes;
-        constexpr int kEach = L::kSlotRows / 8;
-        uint2 w0[kEach], w1[kEach];
-        uint32_t e[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          e[k] = raw[8 * k * kQ4LatBytes + kQ4CodeBytes + c];
-          w0[k] = *reinterpret_cast<const uint2*>(raw + 8 * k * kQ4LatBytes + at0);
-          w1[k] = *reinterpret_cast<const uint2*>(raw + 8 * k * kQ4LatBytes + at1);
-        }
+        const uint8_t* src = from + slot * L::kSlotBytes;
+        uint32_t e = *reinterpret_cast<const uint32_t*>(exps + slot * L::kSlotBytes);
+        if (kEach < 4) e >>= 8 * kEach * part;
+        uint4 w = *reinterpret_cast<const uint4*>(src);
+        uint8_t* row = tile + s * L::kSlotRows * 128;
+        // From e = -5 on (bits 3) every magnitude is a normal E4M3 number, whose exponent field
+        // grows with e; a slot with smaller ones (or the bits 15) looks them up.
+        constexpr uint32_t kMine = kEach == 4 ? 0x0f0f0f0fu : 0x0f0fu;
+        const uint32_t low = e & kMine, high = (e >> 4) & kMine;
+        const uint32_t odd = __vcmpltu4(low, 0x03030303u) | __vcmpltu4(high, 0x03030303u) |
+                             __vcmpeq4(low, 0x0f0f0f0fu) | __vcmpeq4(high, 0x0f0f0f0fu);
+        // (Not unrolled: a loop that stays in the instruction cache.)
+        auto decode = [&](auto&& magnitudes) {
+#pragma unroll 1
+          for (int k = 0; k < kEach; ++k) {
+            const uint2 m0 = magnitudes(e & 15), m1 = magnitudes((e >> 4) & 15);
+            e >>= 8;
+            const uint4 v = w;
+            if (k + 1 < kEach) w = *reinterpret_cast<const uint4*>(src + 16 * (k + 1));
+            const uint32_t at = ((unit0 + 2 * k) << 4) ^ swz;
+            const uint2 a = decode8(v.x, m0), b = decode8(v.y, m0);
+            *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
+            const uint2 x = decode8(v.z, m1), y = decode8(v.w, m1);
+            *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
+          }
+        };
+        if (__any_sync(0xffffffffu, (odd & kMine) != 0))
+          decode([&](uint32_t x) { return *reinterpret_cast<const uint2*>(table + 8 * x); });
+        else
+          decode([&](uint32_t x) {
+            return make_uint2(x * 0x08080800u - 0x04081000u, x * 0x08080808u + 0x0c080400u);
+          });
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
-        uint8_t* rows = tile + s * L::kSlotRows * 128;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const uint2 m0 = *reinterpret_cast<const uint2*>(table + ((e[k] >> sh0) & 15) * 8);
-          const uint2 m1 = *reinterpret_cast<const uint2*>(table + ((e[k] >> sh1) & 15) * 8);
-          const uint2 a = decode8(w0[k].x, m0), b = decode8(w0[k].y, m0);
-          *reinterpret_cast<uint4*>(rows + 1024 * k + to0) = make_uint4(a.x, a.y, b.x, b.y);
-          const uint2 x = decode8(w1[k].x, m1), y = decode8(w1[k].y, m1);
-          *reinterpret_cast<uint4*>(rows + 1024 * k + to1) = make_uint4(x.x, x.y, y.x, y.y);
-        }
       }
       fence_proxy_async_smem();
       __syncwarp();
