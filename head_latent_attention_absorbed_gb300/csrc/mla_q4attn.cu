@@ -176,14 +176,14 @@ __device__ __forceinline__ bool any_of(bool x, int bar, int count) {
   return r != 0;
 }
 
-// The query image of one (query group b, head h): q_abs (512 values) becomes sigma (a1 + a2 /
-// 16 + ...), a_i E4M3 and sigma a power of two that puts max |q_abs| / sigma in [128, 256);
-// q_pe a bf16 value, or hi and lo.  Part i goes to row 16 i + (h mod 16) of the group's image.
+// The query image of one (query group b, head h), in units of sigma, a power of two that puts
+// the largest magnitude of q_abs and q_pe in [128, 256): q_abs (512 values) becomes a1 + a2 /
+// 16 + ..., a_i E4M3, q_pe a bf16 value, or hi and lo.  Part i goes to row 16 i + (h mod 16) of the group's image.
 // grid (H, B), 160 threads: thread t < 128 converts values 4 t .., thread 128 + u keys 4 u ..
 template <bool kF32>
 __global__ void __launch_bounds__(160) q4_query_kernel(const SplitParams p) {
   using L = Q4Plan<kF32>;
-  __shared__ float wmax[4];
+  __shared__ float wmax[5];
   pdl_launch_dependents();   // the split may begin its set-up and cache stream
   const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, lane = t & 31;
   const int hh = h % kHeadGroup;
@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(160) q4_query_kernel(const SplitParams p) {
   float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if (lane == 0 && t < 128) wmax[t >> 5] = mx;
+  if (lane == 0) wmax[t >> 5] = mx;
   __syncthreads();
-  mx = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+  mx = fmaxf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), wmax[4]);
   int ex = 0;
   frexpf(mx, &ex);   // mx = f 2^ex, f in [0.5, 1)
   ex = max(ex, -100);   // keeps 1 / sg finite; smaller queries score as zero to 2^-100
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(160) q4_query_kernel(const SplitParams p) {
     }
   } else if (t < 144) {
     uint32_t hi0, lo0, hi1, lo1;
-    split_bf16(v.x, v.y, hi0, lo0);
-    split_bf16(v.z, v.w, hi1, lo1);
+    split_bf16(v.x * inv, v.y * inv, hi0, lo0);
+    split_bf16(v.z * inv, v.w * inv, hi1, lo1);
     uint8_t* to = img + L::kQKeys;
     const int k = 8 * (t - 128);   // bytes
     *reinterpret_cast<uint2*>(to + sw128_byte(hh, k)) = make_uint2(hi0, hi1);
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const int valid = t == t0 + tiles - 1 ? last_valid : kRowsT;
         warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
         tc_fence_after();
-        float sc[kHalf];
+        float x[kHalf];   // scores in units of the head's scale
         {
           uint32_t s[L::kQParts][8], sk[L::kKParts][8];
 #pragma unroll
@@ -646,23 +646,31 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
           for (int i = 0; i < L::kKParts; ++i)
             tmem_ld8_nowait(tmem + lane_base + kKCol + 32 * sb + kHeadGroup * i + hb, sk[i]);
           tmem_wait_ld();
-          const bool rv = row < valid;
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
-            float x = __uint_as_float(s[L::kQParts - 1][h]);
+            x[h] = __uint_as_float(s[L::kQParts - 1][h]);
 #pragma unroll
-            for (int i = L::kQParts - 2; i >= 0; --i) x = fmaf(x, 0.0625f, __uint_as_float(s[i][h]));
-            float k = __uint_as_float(sk[0][h]);
-            if (kF32) k += __uint_as_float(sk[L::kKParts - 1][h]);
-            sc[h] = rv ? fmaf(x, qsig[h], k * p.scale_log2) : -INFINITY;
+            for (int i = L::kQParts - 2; i >= 0; --i)
+              x[h] = fmaf(x[h], 0.0625f, __uint_as_float(s[i][h]));
+#pragma unroll
+            for (int i = 0; i < L::kKParts; ++i) x[h] += __uint_as_float(sk[i][h]);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::SFREE + sb));
+        float d[kHalf];   // and above the head's reference
+        auto above = [&] {
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) d[h] = fmaf(x[h], qsig[h], -m[h]);
+          if (row >= valid)
+#pragma unroll
+            for (int h = 0; h < kHalf; ++h) d[h] = -INFINITY;
+        };
+        above();
         bool need = false;
 #pragma unroll
-        for (int h = 0; h < kHalf; ++h) need |= sc[h] > m[h] + L::kTop;
+        for (int h = 0; h < kHalf; ++h) need |= d[h] > L::kTop;
         if (any_of(need, 1 + gp, kSoft / 2)) {
           // Some score is too far above its head's reference: the tile's maxima (warp, then
           // the group's four warps) move the references of this group's heads; rescale its row
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
           float tt[kHalf];
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
-            tt[h] = sc[h];
+            tt[h] = row < valid ? x[h] * qsig[h] : -INFINITY;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
               tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
@@ -686,8 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
             const float4 q4 = *reinterpret_cast<const float4*>(red + (hb + h) * 4);
-            const float mn =
-                fmaxf(m[h], fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
+            // (finite even where every score is -infinity)
+            const float mn = fmaxf(fmaxf(m[h], -1e30f),
+                                   fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
             alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
             m[h] = mn;
             l[h] *= alpha[h];
@@ -711,32 +720,36 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             }
             tmem_wait_st();
           }
+          above();
         }
         // p as E4M3 parts, two heads per conversion.  Of three parts the row sum takes the
         // value that the PV uses.
         uint16_t pp[L::kPParts][kHalf / 2];
 #pragma unroll
         for (int h2 = 0; h2 < kHalf / 2; ++h2) {
-          const float mu0 = m[2 * h2] == -INFINITY ? 0.f : m[2 * h2];
-          const float mu1 = m[2 * h2 + 1] == -INFINITY ? 0.f : m[2 * h2 + 1];
-          float v0 = ex2(sc[2 * h2] - mu0), v1 = ex2(sc[2 * h2 + 1] - mu1);
-          if (!kF32) {
+          float v0 = ex2(d[2 * h2]), v1 = ex2(d[2 * h2 + 1]);
+          if constexpr (!kF32) {
             l[2 * h2] += v0;
             l[2 * h2 + 1] += v1;
-          }
-          float wgt = 1.f;
+            // By way of fp16 (2^-11 relative, a quarter of what two parts keep): two values
+            // an instruction, and the remainder of a rounding is exact there.
+            const __half2 v = __floats2half2_rn(v0, v1);
+            pp[0][h2] = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(pp[0][h2], __NV_E4M3));
+            const __half2 r = __hfma2(f, __float2half2_rn(-16.f), __hmul2(v, __float2half2_rn(16.f)));
+            pp[1][h2] = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+          } else {
+            float wgt = 1.f;
 #pragma unroll
-          for (int part = 0; part < L::kPParts; ++part) {
-            pp[part][h2] = to_e4m3x2(v0, v1);
-            if (!kF32 && part == L::kPParts - 1) break;
-            const float2 f = from_e4m3x2(pp[part][h2]);
-            if (kF32) {
+            for (int part = 0; part < L::kPParts; ++part) {
+              pp[part][h2] = to_e4m3x2(v0, v1);
+              const float2 f = from_e4m3x2(pp[part][h2]);
               l[2 * h2] = fmaf(f.x, wgt, l[2 * h2]);
               l[2 * h2 + 1] = fmaf(f.y, wgt, l[2 * h2 + 1]);
+              v0 = (v0 - f.x) * 16.f;
+              v1 = (v1 - f.y) * 16.f;
+              wgt *= 0.0625f;
             }
-            v0 = (v0 - f.x) * 16.f;
-            v1 = (v1 - f.y) * 16.f;
-            wgt *= 0.0625f;
           }
         }
         // P^T buffer sb was last read by the PV of tile t-2.
