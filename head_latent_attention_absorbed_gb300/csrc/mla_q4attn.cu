@@ -99,13 +99,30 @@ struct Q4Plan {
   static_assert(kBars <= 32, "a barrier per lane");
 };
 
-__device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Four K steps of a product, `sa` and `sb` (16-byte units) apart, by one elected thread of the
+// converged warp; the first replaces what D holds unless `accumulate`.  (One at a time, with an
+// election each, a step took its warp some 90 cycles among the others' work.)
+template <bool kE4m3, int kSa, int kSb>
+__device__ __forceinline__ void umma_x4(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+#define MLA_Q4_STEPS(KIND)                                                                    \
+  asm volatile(                                                                               \
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"               \
+      "setp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                               \
+      "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n\t"                   \
+      "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"                                          \
+      "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                     \
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"                                            \
+      "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                     \
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"                                            \
+      "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t}" ::"r"(tmem_d),     \
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(kSa), "n"(kSb)                         \
+      : "memory")
+  if constexpr (kE4m3)
+    MLA_Q4_STEPS("f8f6f4");
+  else
+    MLA_Q4_STEPS("f16");
+#undef MLA_Q4_STEPS
 }
 // kind::f8f6f4 with E4M3 A and B and fp32 accumulators; a_mn selects an MN-major A.
 constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
@@ -364,10 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       key_id = piece_page(first, 0, key_piece);
     }
     if (lane < L::kBars)
-      // counts: slots decoded by four warps, tiles by eight; S read and P written eight
-      mbar_init(bar(lane), (lane >= L::SFREE && lane < L::ODONE) ||
-                                   (lane >= L::CFULL && lane < L::SFULL)
-                               ? 8
+      // counts: slots decoded by a team's warps, tiles by all teams'; S read and P written by
+      // the softmax warps
+      mbar_init(bar(lane), lane >= L::SFREE && lane < L::ODONE      ? kSoft / 32
+                           : lane >= L::CFULL && lane < L::SFULL    ? kTeams * kTeam / 32
                            : lane >= L::RAWEMPTY && lane < L::KEYFULL ? kTeam / 32
                                                                       : 1);
     if (lane == 0) *abort_flag = 0;
@@ -406,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     }
     if (warp != 8) begin_share();
   }
-  const uint32_t tmem = *slot_ptr;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot_ptr, 0);   // uniform to the compiler
 
   // Runs the tiles of the CTA, each with its pieces' pages: f(id, first row, t, first of a
   // later item, that item); false: given up.
@@ -548,10 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k)   // 16 key values (32 bytes) a step
-        umma_bf16_elected(tmem + kKCol + 32 * bf, k0 + ((bf * kKeyTile) >> 4) + 2 * k,
-                          q0 + (L::kQKeys >> 4) + 2 * k, idesc_k, k > 0 ? 1u : 0u);
+      // 16 key values (32 bytes) a step
+      umma_x4<false, 2, 2>(tmem + kKCol + 32 * bf, k0 + ((bf * kKeyTile) >> 4),
+                           q0 + (L::kQKeys >> 4), idesc_k, 0);
       warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
@@ -559,9 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       for (int m = 0; m < 4; ++m) {
         const uint64_t a = a0 + static_cast<uint64_t>((bf * kTile + m * kBox) >> 4);
         const uint64_t q = q0 + static_cast<uint64_t>((m * L::kQBox) >> 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)   // 32 columns a step
-          umma_e4m3(tmem + 64 * bf, a + 2 * k, q + 2 * k, idesc_s, k > 0 ? 1u : (m > 0 ? 1u : 0u));
+        umma_x4<true, 2, 2>(tmem + 64 * bf, a, q, idesc_s, m > 0 ? 1u : 0u);   // 32 columns a step
       }
       umma_commit_elected(bar(L::SFULL + bf));
     }
@@ -592,10 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         // C^T block mb: latent columns 128 mb.. (MN-major, one 128-byte
         // span), K = tile rows in 8-row groups 1024 B apart
         const uint64_t c = c0 + static_cast<uint64_t>((bf * kTile + mb * kBox) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)   // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
-          umma_e4m3(tmem + kOCol + L::kPN * mb, c + ((ks * 4096) >> 4), pd + ((ks * 32) >> 4),
-                    idesc_o, ks > 0 ? 1u : (done > 0 ? 1u : 0u));
+        // 32 tile rows per step: 4096 B of C^T, 32 B of P^T
+        umma_x4<true, 4096 / 16, 32 / 16>(tmem + kOCol + L::kPN * mb, c, pd, idesc_o,
+                                          done > 0 ? 1u : 0u);
       }
       umma_commit_elected(bar(L::ODONE + bf));
     }
