@@ -2087,7 +2087,7 @@ struct PlanOpts {
 // 65536, 16 rows 58 / 61, 32 68 / 65, 64 105 / 68; 64 sequences of 512 to 8192, 32 rows
 // 99 / 76, 128 268 / 89.  E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48 22.9 / 17.1; 4 x 65536,
 // 32 rows 61 / 53, 48 88 / 56.
-constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48;
+constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48, kPairMinFp4 = 32;
 // Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
 // 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
@@ -2102,9 +2102,10 @@ constexpr int kShareMinTiles = 5;
 // 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82.
 constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
-  return o.paged && o.io == MLA_BF16 && (d->dtype == MLA_BF16 || d->dtype == MLA_FP8_E4M3) &&
-         g_split_parts.load() != 2 &&
-         d->heads * o.q_len >= (d->dtype == MLA_BF16 ? kPairMinBf16 : kPairMinFp8);
+  return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
+         d->heads * o.q_len >= (d->dtype == MLA_BF16       ? kPairMinBf16
+                                : d->dtype == MLA_FP8_E4M3 ? kPairMinFp8
+                                                           : kPairMinFp4);
 }
 int tc_heads_per_cta(const mla_dims* d, const PlanOpts& o = {}) {
   if (pair_form(d, o)) return 64;
@@ -2587,6 +2588,7 @@ static mla_status decode_split(const char* who, const mla_dims* dims, int q_len,
     p.part_lse = direct_lse;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pairs && dims->dtype == MLA_FP4_E2M1) return launch_split_q4_pair(p, s, who);
   if (pairs)
     return launch_split_pair(p, cache, dims->dtype == MLA_FP8_E4M3, s, who);
   if (dims->dtype == MLA_FP8_E4M3) return launch_split_fp8(p, cache, s, who);
@@ -2869,9 +2871,8 @@ mla_status mla::attn_queries(const char* who, const mla_dims* dims, const mla_pa
                                 workspace, ws_bytes, nullptr, &p, &view);
   if (st != MLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dims->dtype == MLA_FP4_E2M1) return launch_q4_queries(p, s, who);
-  return pair_form(dims, plan_opts(dims, 1, &view)) ? launch_pair_queries(p, s, who)
-                                                    : launch_fp8_queries(p, s, who);
+  if (pair_form(dims, plan_opts(dims, 1, &view))) return launch_pair_queries(p, s, who);
+  return dims->dtype == MLA_FP4_E2M1 ? launch_q4_queries(p, s, who) : launch_fp8_queries(p, s, who);
 }
 
 mla_status mla::attn_selected(const char* who, const mla_dims* dims, const mla_paging* paging,

@@ -106,9 +106,79 @@ struct Q4Lane {
   }
 };
 
+// ------------------------------------------------------------- codes to E4M3
+__device__ __forceinline__ uint16_t to_e4m3x2(float x0, float x1) {
+  return static_cast<uint16_t>(
+      __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3));
+}
+// Eight codes as E4M3 bytes; mag: the E4M3 magnitudes of codes 0-3 and 4-7.
+__device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
+  const uint32_t sel = w & 0x77777777u;
+  return make_uint2(__byte_perm(mag.x, mag.y, sel) | (w & 0x80808080u),
+                    __byte_perm(mag.x, mag.y, sel >> 16) | ((w << 4) & 0x80808080u));
+}
+// Table of magnitudes by exponent bits, for q4_decode (16 entries of 8 bytes, by 16 lanes):
+// 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^(lane - 8) as E4M3 (15 as 14).
+__device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
+  const float u = q4_unit(lane);
+  reinterpret_cast<uint2*>(table)[lane] =
+      make_uint2(to_e4m3x2(0.f, 0.5f * u) | to_e4m3x2(u, 1.5f * u) << 16,
+                 to_e4m3x2(2.f * u, 3.f * u) | to_e4m3x2(4.f * u, 6.f * u) << 16);
+}
+
+// kEach times 32 codes of one row, from src (16 bytes each), as E4M3 into the row's 16-byte
+// units unit0 .. of a box of 128-byte rows (swz: 16 (row mod 8), the 128-byte swizzle); e: their
+// exponents, a byte for two blocks.  By a whole warp, a row or part of one per lane.
+template <int kEach>
+__device__ __forceinline__ void q4_decode(const uint8_t* src, uint32_t e, uint8_t* row,
+                                          uint32_t unit0, uint32_t swz, const uint8_t* table) {
+  uint4 w = *reinterpret_cast<const uint4*>(src);
+  // From e = -5 on (bits 3) every magnitude is a normal E4M3 number, whose exponent field grows
+  // with e; where a lane has smaller ones (or the bits 15) the warp looks them up.
+  constexpr uint32_t kMine = kEach == 4 ? 0x0f0f0f0fu : kEach == 2 ? 0x0f0fu : 0x0fu;
+  const uint32_t low = e & kMine, high = (e >> 4) & kMine;
+  const uint32_t odd = __vcmpltu4(low, 0x03030303u) | __vcmpltu4(high, 0x03030303u) |
+                       __vcmpeq4(low, 0x0f0f0f0fu) | __vcmpeq4(high, 0x0f0f0f0fu);
+  // (Not unrolled: a loop that stays in the instruction cache.)
+  auto decode = [&](auto&& magnitudes) {
+#pragma unroll 1
+    for (int k = 0; k < kEach; ++k) {
+      const uint2 m0 = magnitudes(e & 15), m1 = magnitudes((e >> 4) & 15);
+      e >>= 8;
+      const uint4 v = w;
+      if (k + 1 < kEach) w = *reinterpret_cast<const uint4*>(src + 16 * (k + 1));
+      const uint32_t at = ((unit0 + 2 * k) << 4) ^ swz;
+      const uint2 a = decode8(v.x, m0), b = decode8(v.y, m0);
+      *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
+      const uint2 x = decode8(v.z, m1), y = decode8(v.w, m1);
+      *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
+    }
+  };
+  if (__any_sync(0xffffffffu, (odd & kMine) != 0))
+    decode([&](uint32_t x) { return *reinterpret_cast<const uint2*>(table + 8 * x); });
+  else
+    decode([&](uint32_t x) {
+      return make_uint2(x * 0x08080800u - 0x04081000u, x * 0x08080808u + 0x0c080400u);
+    });
+}
+
+__device__ __forceinline__ void bulk_g2s_elected(uint32_t dst, const void* src, uint32_t bytes,
+                                                 uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+
 // The split over a 4-bit pool (mla_q4attn.cu), and the kernel that makes the queries' images,
 // which it runs first unless p.late is set.
 mla_status launch_split_q4(const SplitParams& p, cudaStream_t stream, const char* who);
 mla_status launch_q4_queries(const SplitParams& p, cudaStream_t stream, const char* who);
+// The same for bf16 queries of many heads as SM pairs (mla_q4pair.cu), with the query codes of
+// an E4M3 cache's pairs (launch_pair_queries).
+mla_status launch_split_q4_pair(const SplitParams& p, cudaStream_t stream, const char* who);
 
 }  // namespace mla

@@ -129,16 +129,6 @@ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void bulk_g2s_elected(uint32_t dst, const void* src, uint32_t bytes,
-                                                 uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;\n\t}" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
@@ -158,10 +148,6 @@ __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
 }
 
-__device__ __forceinline__ uint16_t to_e4m3x2(float x0, float x1) {
-  return static_cast<uint16_t>(
-      __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3));
-}
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
   return __half22float2(
       __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3)));
@@ -175,12 +161,6 @@ __device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
 // Where the rows of a page that does not exist come from.
 __device__ __align__(128) uint8_t g_q4_zeros[kRowsT * kQ4LatBytes];
 
-// Eight codes as E4M3 bytes; mag: the E4M3 magnitudes of codes 0-3 and 4-7.
-__device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
-  const uint32_t sel = w & 0x77777777u;
-  return make_uint2(__byte_perm(mag.x, mag.y, sel) | (w & 0x80808080u),
-                    __byte_perm(mag.x, mag.y, sel >> 16) | ((w << 4) & 0x80808080u));
-}
 // Whether `x` holds for any of `count` threads (named barrier `bar`).
 __device__ __forceinline__ bool any_of(bool x, int bar, int count) {
   uint32_t r;
@@ -398,19 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     }
     if (!kShare || T > 0) tmem_alloc(smem_u32(slot_ptr), kTmemCols);
   } else if (warp == 12 && lane < 16) {
-    // Magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^(lane - 8) as E4M3 (15 as 14).
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float u = q4_unit(lane);
-      const float2 x = k == 0   ? make_float2(0.f, 0.5f)
-                       : k == 1 ? make_float2(1.f, 1.5f)
-                       : k == 2 ? make_float2(2.f, 3.f)
-                                : make_float2(4.f, 6.f);
-      w[k] = to_e4m3x2(x.x * u, x.y * u);
-    }
-    reinterpret_cast<uint2*>(smem + L::kOffTable)[lane] =
-        make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    q4_table(smem + L::kOffTable, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -499,35 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const uint8_t* src = from + slot * L::kSlotBytes;
         uint32_t e = *reinterpret_cast<const uint32_t*>(exps + slot * L::kSlotBytes);
         if (kEach < 4) e >>= 8 * kEach * part;
-        uint4 w = *reinterpret_cast<const uint4*>(src);
         uint8_t* row = tile + s * L::kSlotRows * 128;
-        // From e = -5 on (bits 3) every magnitude is a normal E4M3 number, whose exponent field
-        // grows with e; a slot with smaller ones (or the bits 15) looks them up.
-        constexpr uint32_t kMine = kEach == 4 ? 0x0f0f0f0fu : 0x0f0fu;
-        const uint32_t low = e & kMine, high = (e >> 4) & kMine;
-        const uint32_t odd = __vcmpltu4(low, 0x03030303u) | __vcmpltu4(high, 0x03030303u) |
-                             __vcmpeq4(low, 0x0f0f0f0fu) | __vcmpeq4(high, 0x0f0f0f0fu);
-        // (Not unrolled: a loop that stays in the instruction cache.)
-        auto decode = [&](auto&& magnitudes) {
-#pragma unroll 1
-          for (int k = 0; k < kEach; ++k) {
-            const uint2 m0 = magnitudes(e & 15), m1 = magnitudes((e >> 4) & 15);
-            e >>= 8;
-            const uint4 v = w;
-            if (k + 1 < kEach) w = *reinterpret_cast<const uint4*>(src + 16 * (k + 1));
-            const uint32_t at = ((unit0 + 2 * k) << 4) ^ swz;
-            const uint2 a = decode8(v.x, m0), b = decode8(v.y, m0);
-            *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
-            const uint2 x = decode8(v.z, m1), y = decode8(v.w, m1);
-            *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
-          }
-        };
-        if (__any_sync(0xffffffffu, (odd & kMine) != 0))
-          decode([&](uint32_t x) { return *reinterpret_cast<const uint2*>(table + 8 * x); });
-        else
-          decode([&](uint32_t x) {
-            return make_uint2(x * 0x08080800u - 0x04081000u, x * 0x08080808u + 0x0c080400u);
-          });
+        q4_decode<kEach>(src, e, row, unit0, swz, table);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
       }

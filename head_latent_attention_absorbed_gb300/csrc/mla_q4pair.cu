@@ -1,0 +1,728 @@
+// The split over a 4-bit pool for bf16 queries of many heads: a pair of SMs takes up to 128
+// query rows (heads, and the tokens of a multi-token step) of one sequence.
+//
+// The products, their split over the pair and the softmax are those of mla_pair.cu with an
+// E4M3 cache: heads are the M of the MMAs, CTA i of the pair holds 64 of them, and of every
+// other operand half:
+//   scores  S0[128 heads x 128 rows] = Q[128 x 512] . C^T, S1 = Qk[128 x 64] . K^T
+//                                                       CTA i: rows 64 i ..
+//   output  O[128 x 512] += P[128 x 128 rows] . C[128 x 512]
+//                                                       CTA i: 256 of the latent columns
+// Queries are two E4M3 parts in units of a power of two per head (their keys' part bf16, and
+// so S1 has no unit), P an E4M3 part and its E5M2 remainder.
+//
+// What differs is where the operands come from.  A tile of 128 rows (35 KB of codes and
+// exponents) lands in both CTAs as it is stored, and eight warps turn it into E4M3 boxes of 64
+// rows x 128 columns: four each own a score box (the CTA's 64 rows), four an output unit (all
+// 128 rows x its 256 columns), so that each warp waits for one operand to be free and hands one
+// over.  (A box that is both is decoded twice: one copy would tie the scores of a tile to the
+// output product of the tile before.)  Of the keys, stored as the tensor core wants them, each
+// CTA copies its 64 rows.  Nothing needs cleaning behind a sequence's end: whatever bits a row
+// holds, its latents are finite, and its scores are not looked at.
+//
+// Tensor memory per CTA as in mla_pair.cu: S0 and S1, two buffers of 64 columns each, and O.
+//
+// Warps (1024 threads): 0-15 softmax and epilogue; 16 copies of rows; 17 keys and the first
+// query; 18 score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue
+// for the pair); 22 the later items' queries; 24-27 score boxes, 28-31 output units.
+#include <cuda_fp8.h>
+#include <cudaTypedefs.h>
+
+#include "mla_pair.cuh"
+#include "mla_q4.cuh"
+
+namespace mla {
+namespace {
+
+struct Q4Pair {
+  static constexpr int kSoftWarps = 16, kSoft = 32 * kSoftWarps, kThreads = 1024;
+  static constexpr int kSlices = kSoftWarps / 4, kCols = 64 / kSlices;
+  static constexpr int kParts = 2;
+  static constexpr int kQKeys = kParts * 4 * kPBox;     // offset of the query's key part
+  static constexpr int kQBytes = kQKeys + kPBox;
+  static constexpr int kSlotRows = 32, kSlots = 4;      // a tile's rows
+  static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
+  static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffS = kOffQ + kQBytes;         // [4] score boxes
+  static constexpr int kOffV = kOffS + 4 * kPBox;       // [row half][O tile] output units
+  static constexpr int kOffK = kOffV + 4 * kPBox;       // [2] keys
+  static constexpr int kOffP = kOffK + 2 * kKeyBytes;
+  static constexpr int kOffRaw = kOffP + kPBufBytes;
+  static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;
+  static constexpr int kOffRed = kOffTable + 128;       // [2][2 kSlices][64] maxima
+  static constexpr int kOffSum = kOffRed + 2 * 2 * kSlices * kPHeads * 4;   // row sums
+  static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
+  // Rows landed / decoded and keys landed (this CTA's); score boxes and output units handed
+  // over / free; keys handed over; S, P, O and the query as in mla_pair.cu.
+  static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots, KEYFULL = RAWEMPTY + kSlots,
+                       FULLS = KEYFULL + 2, EMPTYS = FULLS + 4, FULLV = EMPTYS + 4,
+                       EMPTYV = FULLV + 4, KREADY = EMPTYV + 4, SREADY = KREADY + 2,
+                       SFREE = SREADY + 2, PREADY = SFREE + 2, PVDONE = PREADY + 2,
+                       QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
+  static constexpr int kOffSlot = kOffBar + 8 * kBars;
+  static constexpr int kOffAbort = kOffSlot + 8;
+  static constexpr int kOffShare = kOffAbort + 8;       // TileShare of the pair
+  static constexpr size_t kSmem = 1024 + kOffShare + 24;
+  static constexpr uint32_t kOCol = 256;
+  // Reference of the softmax below the running maximum, and how far a maximum may pass it
+  // before O is rescaled (log2): weights stay in [0, 2^8.5].
+  static constexpr float kBias = 3.f, kGrow = 5.5f;
+  static constexpr int kStageRow = kDc * 4 + 16;        // epilogue staging, over the operands
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kOffRed >= kPHeads * kStageRow, "epilogue staging");
+  static_assert(kPBufBytes == kSoftWarps * 32 * 32, "an item's output through P");
+  static_assert(kOffS % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  static_assert(kOffRaw % 16 == 0 && kOffBar % 8 == 0, "alignment");
+};
+
+// 8 columns of this thread's lane, loaded (one statement, as tmem_ld16).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Where the rows of a page that does not exist come from.
+__device__ __align__(128) uint8_t g_q4_pair_zeros[Q4Pair::kSlotBytes];
+static_assert(Q4Pair::kKeyBytes <= Q4Pair::kSlotBytes, "zeros for either plane");
+
+// kShare: one pair per two SMs takes an equal run of all sequences' tiles (take_share), an
+// item per sequence it meets; otherwise a pair has one item, its chunk.
+template <bool kShare>
+__global__ void __launch_bounds__(Q4Pair::kThreads, 1)
+    split_q4_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                         const __grid_constant__ CUtensorMap tmap_qpe, const SplitParams p,
+                         const float* __restrict__ sigma) {
+  using L = Q4Pair;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem), bars = sbase + L::kOffBar;
+  float* red = reinterpret_cast<float*>(smem + L::kOffRed);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+  uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
+  // Query rows (tokens x heads) of the sequence, dealt evenly to its CTAs: this CTA's are
+  // flat0 .. flat0 + mine - 1 of all; rows past them up to 64 are computed as well and dropped.
+  const int all = p.q_len * p.H, parts = kShare ? 2 * pair_groups(all) : gridDim.x;
+  const int dealt = (all + parts - 1) / parts, part = kShare ? blockIdx.x % parts : blockIdx.x;
+  const int first = part * dealt, mine = min(dealt, all - first);
+  const int rank = uniform(static_cast<int>(cluster_ctarank()));
+  const bool leader = rank == 0;
+  if (p.late) pdl_wait();
+  // Rows of a sequence, all of which its last token attends, count.
+  TileItem item0{0, 0, 0, 0, 0};   // the pair's first item (none: T = 0)
+  int T = 0;        // tiles of the pair
+  TileShare share{};
+  if (!kShare) {
+    const int j = blockIdx.y, seq = blockIdx.z;
+    const int len =
+        clamp_length(p, (seq + 1) * p.q_len - 1, tid == 0 && blockIdx.x == 0 && j == 0);
+    const int r0 = j * p.chunk;
+    if (r0 >= len) {   // both CTAs of the pair: the chunk lies past the sequence
+      if (p.direct || r0 == 0) pdl_wait();   // no row at all: see launch_pdl
+      if (p.direct) write_no_rows(p, seq * all + first, mine, tid, L::kThreads);
+      return;
+    }
+    T = (min(r0 + p.chunk, len) - r0 + kTileRows - 1) / kTileRows;
+    item0 = TileItem{seq, j, r0, T, len};
+  }
+  auto item_after = [&](const TileItem& it, int t) { return next_item<true>(p, it, T - t); };
+  const uint32_t lead = mapa_shared(bars, 0);   // the even CTA's barriers
+  auto bar = [&](int i) { return bars + 8 * i; };
+  auto lbar = [&](int i) { return lead + 8 * i; };
+  constexpr int kWarpRows = L::kSoftWarps, kWarpKeys = kWarpRows + 1, kWarpScore = kWarpRows + 2,
+                kWarpOut = kWarpRows + 4, kWarpQuery = kWarpRows + 6, kWarpBox = kWarpRows + 8,
+                kWarpUnit = kWarpBox + 4;
+
+  if (tid == L::kSoft) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar(L::RAWFULL + i), 1);
+      // decoded by the units' two warps of that row half, of the CTA's own half by the boxes' too
+      mbar_init(bar(L::RAWEMPTY + i), (i >> 1) == rank ? 6 : 2);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(L::FULLS + i), 2);   // a warp of each CTA
+      mbar_init(bar(L::EMPTYS + i), 1);
+      mbar_init(bar(L::FULLV + i), 2);
+      mbar_init(bar(L::EMPTYV + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(L::KEYFULL + i), 1);
+      mbar_init(bar(L::KREADY + i), 2);                 // both CTAs' keys
+      mbar_init(bar(L::SREADY + i), 2);                 // one commit per issuer
+      mbar_init(bar(L::SFREE + i), 2 * L::kSoftWarps);  // both CTAs' softmax warps
+      mbar_init(bar(L::PREADY + i), 2 * L::kSoftWarps);
+      mbar_init(bar(L::PVDONE + i), 2);
+    }
+    mbar_init(bar(L::QFULL), 1);
+    mbar_init(bar(L::QFREE), 2);   // one commit per score issuer
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_qpe);
+  }
+  if (warp == kWarpBox && lane < 16) q4_table(smem + L::kOffTable, lane);
+  if (kShare && warp == kWarpRows) {
+    __syncwarp();
+    share = take_share<true>(p, blockIdx.x / parts, gridDim.x / parts, lane, blockIdx.x == 0);
+    if (lane == 0) *reinterpret_cast<TileShare*>(smem + L::kOffShare) = share;
+  }
+  if (warp == kWarpScore) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot_ptr)),
+                 "r"(kPTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the barriers of both CTAs exist
+  tc_fence_after();
+  const uint32_t tmem = uniform(static_cast<int>(*slot_ptr));
+  if (kShare) {
+    share = *reinterpret_cast<const TileShare*>(smem + L::kOffShare);
+    T = uniform(max(share.tiles, 0));   // none: more pairs than tiles
+    if (T > 0)
+      item0 = first_item<true>(p, share, blockIdx.x / parts);
+    else
+      pdl_wait();
+  }
+  // This CTA's half of the queries of sequence v, by a whole warp after its PDL wait.
+  auto load_query = [&](int v) {
+    const uint64_t stream = l2_evict_first_policy();
+    const int flat0 = v * all + first;
+    if (leader) expect_tx_elected(bar(L::QFULL), 2 * L::kQBytes);
+#pragma unroll 1
+    for (int i = 0; i < L::kParts * 4; ++i)
+      tma_load_pair(sbase + L::kOffQ + i * kPBox, &tmap_q, 128 * (i & 3),
+                    (i >> 2) * p.B * p.H + flat0, lbar(L::QFULL), stream);
+    tma_load_pair(sbase + L::kOffQ + L::kQKeys, &tmap_qpe, 0, flat0, lbar(L::QFULL), stream);
+  };
+  // Runs the pair's tiles, item by item: f(item, tile i of it, tile t of all) -> false: given up.
+  auto for_tiles = [&](auto&& f) {
+    TileItem it = item0;
+    for (int t = 0, i = 0; t < T; ++t) {
+      if (!f(it, i, t)) return;
+      if (++i == it.tiles && t + 1 < T) {
+        it = item_after(it, t + 1);
+        i = 0;
+      }
+    }
+  };
+  auto given_up = [&] { return __any_sync(0xffffffffu, *abort_flag) != 0; };
+
+  if (warp == kWarpRows || warp == kWarpKeys) {
+    // ------------------------------------------------------------ rows, keys
+    // Pieces of one page each: of a slot's 32 rows, or of the CTA's 64 keys.
+    const bool rows = warp == kWarpRows;
+    const uint8_t* pool = static_cast<const uint8_t*>(p.cache);
+    const uint64_t pol = l2_evict_first_policy();
+    const int piece = min(1 << p.page_shift, rows ? L::kSlotRows : 64);
+    const int span = rows ? kTileRows : 64, row0 = rows ? 0 : 64 * rank;
+    // Lane i: the page of piece i of a tile, or -1 (outside the pool), -2 (past the end).
+    auto piece_page = [&](const TileItem& it, int i) {
+      const int r = it.r0 + i * kTileRows + row0 + lane * piece;
+      if (lane * piece >= span || r >= it.len) return -2;
+      const int id = p.table[static_cast<size_t>(it.v) * p.table_stride + (r >> p.page_shift)];
+      return id < 0 ? -1 : id;
+    };
+    // Copies pieces from .. to - 1, of which those below `live` lie in the sequence.
+    auto copy_pieces = [&](const uint8_t* src, int from, int to, int live, uint32_t bytes,
+                           uint32_t dst, uint32_t full) {
+      const int n = max(min(to, live) - from, 0);
+      expect_tx_elected(full, n * bytes);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i)
+        bulk_g2s_elected(dst + i * bytes,
+                         reinterpret_cast<const uint8_t*>(__shfl_sync(
+                             0xffffffffu, reinterpret_cast<unsigned long long>(src), from + i)),
+                         bytes, full, pol);
+    };
+    if (warp == kWarpKeys) {
+      pdl_wait();   // the query comes from the kernel before
+      if (T > 0) load_query(item0.v);
+    }
+    const int bytes = rows ? kQ4LatBytes : kQ4KeyBytes, plane = rows ? 0 : kQ4LatBytes;
+    int ahead = T > 0 ? piece_page(item0, 0) : -2;   // the next tile's, looked up early
+    int landed = 0;                                  // tiles whose keys were handed over
+    // Hands the keys of tile t over once they have landed: the even CTA's MMAs read both.
+    auto hand_over = [&](int t) {
+      warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
+      if (lane == 0) arrive_cluster(lbar(L::KREADY + (t & 1)));
+      landed = t + 1;
+    };
+    int issued = 0;
+    for_tiles([&](const TileItem& it, int i, int t) {
+      if (given_up()) return false;
+      int id = ahead;
+      if (t + 1 < T) {
+        if (i + 1 < it.tiles)
+          ahead = piece_page(it, i + 1);
+        else
+          ahead = piece_page(item_after(it, t + 1), 0);
+      }
+      if (id >= p.num_pages) id = -1;
+      if (id == -1) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+      const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
+      const int r = (it.r0 + row0 + lane * piece) & ((1 << p.page_shift) - 1);
+      const int in_page = (r + i * kTileRows) & ((1 << p.page_shift) - 1);
+      const uint8_t* src =
+          id < 0 ? g_q4_pair_zeros
+                 : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
+                       (static_cast<size_t>(plane) << p.page_shift) + in_page * bytes;
+      if (rows) {
+        // The CTA's own half first: its scores start a tile.
+        const int per = L::kSlotRows / piece;
+#pragma unroll 1
+        for (int k = 0; k < L::kSlots; ++k) {
+          const int s = k ^ (rank << 1);
+          if (t > 0) {
+            warp_wait(bar(L::RAWEMPTY + s), (t - 1) & 1, abort_flag);
+            if (given_up()) return false;
+          }
+          copy_pieces(src, s * per, (s + 1) * per, live, piece * bytes,
+                      sbase + L::kOffRaw + s * L::kSlotBytes, bar(L::RAWFULL + s));
+        }
+      } else {
+        if (t >= 2) {   // the scores of tile t - 2 have read this buffer
+          warp_wait(bar(L::SREADY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+          if (given_up()) return false;
+        }
+        copy_pieces(src, 0, 64 / piece, live, piece * bytes,
+                    sbase + L::kOffK + (t & 1) * L::kKeyBytes, bar(L::KEYFULL + (t & 1)));
+        issued = t + 1;
+        if (t > 0) hand_over(t - 1);
+      }
+      return true;
+    });
+    if (!rows && landed < issued) hand_over(issued - 1);
+  } else if (warp >= kWarpBox) {
+    // ------------------------------------------------------------ codes to E4M3
+    // Warp m of the first four: score box m, columns 128 m .. of the CTA's 64 rows; warp u of
+    // the others: output unit u, row half u >> 1, columns 256 (u & 1) + 128 rank ..  A lane
+    // takes a row of each of the half's two slots: rows are 17 times 16 bytes apart, so eight
+    // lanes read from eight different pieces of the banks, and the swizzle has them write so.
+    const bool unit = warp >= kWarpUnit;
+    const int u = (warp - kWarpBox) & 3;
+    const int half = unit ? u >> 1 : rank, box = unit ? 2 * (u & 1) + rank : u;
+    const int empty = (unit ? L::EMPTYV : L::EMPTYS) + u, full = (unit ? L::FULLV : L::FULLS) + u;
+    uint8_t* to = smem + (unit ? L::kOffV : L::kOffS) + u * kPBox + lane * 128;
+    const uint8_t* from = smem + L::kOffRaw + 2 * half * L::kSlotBytes + lane * kQ4LatBytes;
+    const uint32_t swz = (lane & 7) << 4;
+    for (int t = 0; t < T; ++t) {
+      if (t > 0) {
+        warp_wait(bar(empty), (t - 1) & 1, abort_flag);
+        tc_fence_after();
+      }
+      if (given_up()) break;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int s = 2 * half + k;
+        warp_wait(bar(L::RAWFULL + s), t & 1, abort_flag);
+        const uint8_t* raw = from + k * L::kSlotBytes;
+        q4_decode<4>(raw + 64 * box,
+                     *reinterpret_cast<const uint32_t*>(raw + kQ4CodeBytes + 4 * box),
+                     to + k * (L::kSlotRows * 128), 0, swz, smem + L::kOffTable);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + s));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lbar(full));
+    }
+  } else if (kShare && warp == kWarpQuery) {
+    // ------------------------------------------------------------ the later items' queries
+    // Each once the scores of the item before are done, which read the query it replaces.
+    TileItem it = item0;
+    for (int t = it.tiles, n = 0; 0 < t && t < T; t += it.tiles, ++n) {
+      it = item_after(it, t);
+      warp_wait(bar(L::QFREE), n & 1, abort_flag);
+      if (given_up()) break;
+      pdl_wait();
+      load_query(it.v);
+    }
+  } else if (warp == kWarpScore || warp == kWarpScore + 1) {
+    // ------------------------------------------------------------ score MMAs (even CTA)
+    // The whole warp runs along, converged at every MMA and commit.  Not unrolled over boxes:
+    // code that runs once a tile is fetched anew each time.
+    if (leader) {
+      const bool keys = warp != kWarpScore;
+      constexpr uint32_t idesc = (1u << 4) | (128u >> 3 << 17) | (128u >> 4 << 24);   // E4M3
+      constexpr uint32_t idesc_k = idesc | (1u << 7) | (1u << 10);                    // bf16
+      const uint64_t q0 = umma_desc_sw128(sbase + L::kOffQ, 16, 1024);
+      const uint64_t s0 = umma_desc_sw128(sbase + L::kOffS, 16, 1024);
+      const uint64_t qk0 = umma_desc_sw128(sbase + L::kOffQ + L::kQKeys, 16, 1024);
+      const uint64_t k0 = umma_desc_sw128(sbase + L::kOffK, 16, 1024);
+      int n = 0;   // items begun
+      for_tiles([&](const TileItem& it, int i, int t) {
+        const int sb = t & 1;
+        if (i == 0) {
+          warp_wait(bar(L::QFULL), n & 1, abort_flag);
+          ++n;
+          if (kShare && !keys && blockIdx.x % parts == 0 && it.r0 == 0)
+            // The run with a sequence's first tile says how many runs it spans.  (Not before a
+            // query is here, fetched behind the PDL wait: the combine of the call before may
+            // still be reading its own counts.)
+            for (int q = lane; q < p.q_len; q += 32)
+              p.pieces[it.v * p.q_len + q] = count_pieces(it, share.first + t, share.each);
+        }
+        if (t >= 2) warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
+        if (given_up()) return false;
+        if (keys) {
+          warp_wait(bar(L::KREADY + sb), (t >> 1) & 1, abort_flag);
+          if (given_up()) return false;
+          tc_fence_after();
+          const uint64_t b = k0 + static_cast<uint64_t>(sb * (L::kKeyBytes >> 4));
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_pair<false>(tmem + 128 + 64 * sb, qk0 + 2 * ks, b + 2 * ks, idesc_k, ks > 0);
+        } else {
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            warp_wait(bar(L::FULLS + m), t & 1, abort_flag);
+            if (given_up()) return false;
+            tc_fence_after();
+            const uint64_t b = s0 + static_cast<uint64_t>(m * (kPBox >> 4));
+#pragma unroll
+            for (int part = 0; part < L::kParts; ++part) {
+              const uint64_t a = q0 + static_cast<uint64_t>((part * 4 + m) * (kPBox >> 4));
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)   // 32 bytes of K a step
+                mma_pair<true>(tmem + 64 * sb, a + 2 * ks, b + 2 * ks, idesc,
+                               part > 0 || ks > 0 ? 1u : (m > 0 ? 1u : 0u));
+            }
+            commit_pair(bar(L::EMPTYS + m));
+          }
+        }
+        commit_pair(bar(L::SREADY + sb));
+        if (kShare && i + 1 == it.tiles && t + 1 < T) commit_pair(bar(L::QFREE));
+        return true;
+      });
+    }
+  } else if (warp == kWarpOut || warp == kWarpOut + 1) {
+    // ------------------------------------------------------------ output MMAs (even CTA)
+    // Issuer jj takes the units of O tile jj.
+    if (leader) {
+      const int jj = warp - kWarpOut;
+      constexpr uint32_t idesc =
+          (1u << 4) | (1u << 16) | (256u >> 3 << 17) | (128u >> 4 << 24);
+      const uint64_t p0 = umma_desc_sw128(sbase + L::kOffP, 16, 1024);
+      const uint64_t v0 = umma_desc_sw128(sbase + L::kOffV, kPBox, 1024);   // rows (K) by eights
+      const uint32_t d = tmem + L::kOCol + 128 * jj;
+      for_tiles([&](const TileItem&, int i, int t) {
+        const int pb = t & 1;
+        warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
+        if (given_up()) return false;
+#pragma unroll 1
+        for (int kh = 0; kh < 2; ++kh) {
+          const int u = 2 * kh + jj;
+          warp_wait(bar(L::FULLV + u), t & 1, abort_flag);
+          if (given_up()) return false;
+          tc_fence_after();
+          const uint64_t b = v0 + static_cast<uint64_t>(u * (kPBox >> 4));
+          // 64 rows: two steps of 32 (4 KB; 32 bytes of each part's row, the half at byte 64 kh)
+#pragma unroll
+          for (int part = 0; part < L::kParts; ++part) {
+            const uint64_t a = p0 + ((part * kPBox + 64 * kh) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+              mma_pair<true>(d, a + 2 * ks, b + ks * (4096 >> 4),
+                             idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
+                             part > 0 || ks > 0 ? 1u : (i > 0 || kh > 0 ? 1u : 0u));
+          }
+          commit_pair(bar(L::EMPTYV + u));
+        }
+        commit_pair(bar(L::PVDONE + pb));
+        return true;
+      });
+    }
+  } else if (warp < L::kSoftWarps) {
+    // ------------------------------------------------------------ softmax
+    // Warp w: lanes 32 (w & 3) .. of tensor memory, so head 32 (w & 1) + lane of the
+    // tile's row half (w >> 1) & 1, and the column slice w >> 2 of those 64 rows.
+    constexpr int kCols = L::kCols, kSlices = L::kSlices;
+    const int qd = warp & 3, hh = warp >> 2;
+    const int head = 32 * (qd & 1) + lane, row0 = 64 * (qd >> 1) + kCols * hh;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qd) << 16);
+    const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
+    const int back = p.q_len - 1 - (first + min(head, mine - 1)) / p.H;   // tokens behind its own
+    const float scale = p.scale_log2;
+    TileItem it = item0;
+    for (int t0 = 0; t0 < T;) {   // items; t0: the item's first tile among the pair's
+      const int flat0 = it.v * all + first, tiles = it.tiles;
+      float unit = 0.f;   // the head's, of the query's codes
+      // Rows from this thread's first on that its head's token attends: one before the last
+      // token sees fewer.
+      const int limit = min(tiles * kTileRows, it.len - back - it.r0) - row0 + t0 * kTileRows;
+      float m = -INFINITY, l = 0.f;
+      // A wait that gives up leaves the loop running (every later wait then returns at
+      // once), so that all softmax warps meet at the same barriers.
+      for (int t = t0; t < t0 + tiles; ++t) {
+        const int sb = t & 1;
+        warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
+        // written by the kernel before, known complete once the first scores are
+        if (t == t0) unit = __ldcg(sigma + flat0 + min(head, mine - 1));
+        tc_fence_after();
+        float x[kCols], y[kCols];
+        const uint32_t s_at = lanes + 64 * sb + kCols * hh;
+        tmem_ld16(s_at, reinterpret_cast<uint32_t*>(x));
+        tmem_ld16(s_at + 128, reinterpret_cast<uint32_t*>(y));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lbar(L::SFREE + sb));
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) x[i] = fmaf(x[i], unit, y[i]);
+        if (__any_sync(0xffffffffu, t * kTileRows + kCols > limit)) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (t * kTileRows + i >= limit) x[i] = -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
+        float* rd = red + sb * 2 * kSlices * kPHeads;
+        rd[part_of * kPHeads + head] = mx;
+        named_bar_sync(1, L::kSoft);
+        mx = rd[head];
+#pragma unroll
+        for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, rd[i * kPHeads + head]);
+        mx = mx * scale - L::kBias;
+        if (__any_sync(0xffffffffu, mx > m + L::kGrow)) {
+          // Move the references of the warp's heads (the four warps of the same heads
+          // decide alike); rescale the sum and this warp's share of O.
+          const float mn = fmaxf(m, mx);
+          const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
+          m = mn;
+          l *= alpha;
+          if (t > t0) {
+            warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 16 / kSlices; ++c) {   // this warp's slice of O's 256 columns
+              const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 16 * c;
+              float o[16];
+              tmem_ld16(at, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st8(at, o);
+              tmem_st8(at + 8, o + 8);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          x[i] = ex2(fmaf(x[i], scale, -ref));
+          l += x[i];
+        }
+        // P was last read by the output MMAs of tile t - 1.
+        if (t >= 1) warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        {
+          // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
+          uint8_t* pb = smem + L::kOffP;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a = 0, b = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float y0 = x[4 * w + 2 * e], y1 = x[4 * w + 2 * e + 1];
+              const uint32_t f1 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+              const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                  static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3)));
+              const uint32_t f2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - g.x, y1 - g.y),
+                                                           __NV_SATFINITE, __NV_E5M2);
+              a |= f1 << (16 * e);
+              b |= f2 << (16 * e);
+            }
+            hi[w] = a;
+            lo[w] = b;
+          }
+          const uint32_t at = sw128(head, row0 / 16);
+          *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(pb + kPBox + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lbar(L::PREADY + sb));
+      }
+      t0 += tiles;
+      if (tid == 0 && t0 == T) pdl_launch_dependents();   // the combine waits for this grid anyway
+      // The row sums of a head's threads, its log-sum-exp, and O / sum through shared memory
+      // (over operands that nothing reads any more) to whole rows.
+      float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
+      sums[part_of * kPHeads + head] = l;
+      warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      tc_fence_after();
+      named_bar_sync(1, L::kSoft);
+      if (!*abort_flag) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * kSlices; ++i) sum += sums[i * kPHeads + head];
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const bool whole = kShare ? whole_set(it) : p.direct != 0;   // the result itself
+        const size_t stride = whole ? 1 : p.splits;
+        const size_t row = static_cast<size_t>(flat0) * stride + (whole ? 0 : it.j);   // the first's
+        float* o_to = kShare && whole ? static_cast<float*>(p.out) : p.part_o;
+        float* lse_to = kShare && whole ? p.out_lse : p.part_lse;
+        // Four values of row h, column x (results are bf16, partials fp32).
+        auto put = [&](int h, int x, float4 o) {
+          const size_t at = (row + static_cast<size_t>(h) * stride) * kDc + x;
+          if (whole)
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(o_to) + at) =
+                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+          else
+            *reinterpret_cast<float4*>(o_to + at) = o;
+        };
+        if (part_of == 0 && head < mine && lse_to)
+          lse_to[row + static_cast<size_t>(head) * stride] =
+              sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        // This warp's slice of O's columns: in tile jj = col0 / 128 the lane's 128 columns are
+        // latents 256 jj + 128 (qd >> 1) ..
+        const int col0 = 256 / kSlices * hh;
+        const int latent = 256 * (col0 >> 7) + 128 * (qd >> 1) + (col0 & 127);
+        if (kShare && t0 < T) {
+          // The next item's operands are on their way to where the last one stages: each warp
+          // turns its 32 heads' columns over in its part of P, 8 at a time, and writes 32 bytes
+          // of sixteen rows at once.  (P of the next tile is written behind the barrier of its
+          // maxima.)
+          float4* mine4 = reinterpret_cast<float4*>(smem + L::kOffP) + 64 * warp;
+          const int h0 = 32 * (qd & 1);
+#pragma unroll 1
+          for (int c = 0; c < 32 / kSlices; ++c) {
+            float o[8];
+            tmem_ld8(lanes + L::kOCol + col0 + 8 * c, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mine4[2 * lane + (i ^ (lane >> 2 & 1))] = make_float4(
+                  o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 16 * i + (lane >> 1), q = lane & 1;
+              if (h0 + r < mine)
+                put(h0 + r, latent + 8 * c + 4 * q, mine4[2 * r + (q ^ (r >> 2 & 1))]);
+            }
+            __syncwarp();
+          }
+        } else {
+          float* to = reinterpret_cast<float*>(smem + head * L::kStageRow) + latent;
+#pragma unroll 1
+          for (int c = 0; c < 16 / kSlices; ++c) {
+            float o[16];
+            tmem_ld16(lanes + L::kOCol + col0 + 16 * c, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(to + 16 * c + 4 * i) =
+                  make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
+                              o[4 * i + 3] * inv);
+          }
+          named_bar_sync(1, L::kSoft);
+          for (int h = warp; h < mine; h += L::kSoftWarps) {
+            const float4* src = reinterpret_cast<const float4*>(smem + h * L::kStageRow);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(h, 128 * i + 4 * lane, src[32 * i + lane]);
+          }
+        }
+      }
+      if (kShare && t0 < T) it = item_after(it, t0);
+    }
+  }
+  // A CTA that gave up may have copies in flight: they land long before this.
+  if (*abort_flag) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 5000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the other's MMAs or barriers use it
+  if (warp == kWarpScore) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPTmem)
+                 : "memory");
+  }
+  if (tid == 0 && *abort_flag) report(p.status, MLA_DEV_PIPELINE_TIMEOUT);
+}
+
+template <bool kShare>
+mla_status launch_q4_pair(const CUtensorMap& q, const CUtensorMap& qpe, const SplitParams& p,
+                          cudaStream_t s, const char* who) {
+  using L = Q4Pair;
+  static DeviceFlags attr_done;
+  const int dev = current_device();
+  if (!attr_done.test(dev)) {
+    if (cudaFuncSetAttribute(split_q4_pair_kernel<kShare>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      set_error("%s: cannot reserve %zu bytes of shared memory", who, L::kSmem);
+      return MLA_ERR_CUDA;
+    }
+    attr_done.set(dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  const int ctas = 2 * pair_groups(p.q_len * p.H);   // of a row
+  cfg.gridDim = kShare ? dim3(share_runs(ctas) * ctas) : dim3(ctas, p.splits, p.B / p.q_len);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_overlap_enabled() ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, split_q4_pair_kernel<kShare>, q, qpe, p,
+                     static_cast<const float*>(pair_units(p)));
+  return launch_status(who);
+}
+
+}  // namespace
+
+mla_status launch_split_q4_pair(const SplitParams& p, cudaStream_t stream, const char* who) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) {
+    set_error("%s: cuTensorMapEncodeTiled is not available from the driver", who);
+    return MLA_ERR_CUDA;
+  }
+  // The queries, in boxes of one CTA's 64 heads x 128 bytes (128-byte swizzle).
+  CUresult bad = CUDA_SUCCESS;
+  auto encode = [&](CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, int elt) {
+    const cuuint64_t gdim[2] = {cols, rows}, gstride[1] = {cols * elt};
+    const cuuint32_t box[2] = {cuuint32_t(128 / elt), kPHeads}, estride[2] = {1, 1};
+    const CUresult r = enc(m, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           2, const_cast<void*>(base), gdim, gstride, box, estride,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) bad = r;
+  };
+  const uint64_t rows = static_cast<uint64_t>(p.B) * p.H;
+  CUtensorMap tq, tp;
+  encode(&tq, pair_codes(p), kQ8Row, 2 * rows, 1);
+  encode(&tp, p.q_pe, kDr, rows, 2);
+  if (bad != CUDA_SUCCESS) {
+    set_error("%s: cuTensorMapEncodeTiled failed (%d)", who, int(bad));
+    return MLA_ERR_CUDA;
+  }
+  if (!p.late) {
+    const mla_status st = launch_pair_queries(p, stream, who);
+    if (st != MLA_OK) return st;
+  }
+  return p.pieces ? launch_q4_pair<true>(tq, tp, p, stream, who)
+                  : launch_q4_pair<false>(tq, tp, p, stream, who);
+}
+
+}  // namespace mla
