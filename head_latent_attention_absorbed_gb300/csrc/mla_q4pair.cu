@@ -13,18 +13,22 @@
 //
 // What differs is where the operands come from.  A tile of 128 rows (35 KB of codes and
 // exponents) lands in both CTAs as it is stored, and eight warps turn it into E4M3 boxes of 64
-// rows x 128 columns: four each own a score box (the CTA's 64 rows), four an output unit (all
-// 128 rows x its 256 columns), so that each warp waits for one operand to be free and hands one
-// over.  (A box that is both is decoded twice: one copy would tie the scores of a tile to the
-// output product of the tile before.)  Of the keys, stored as the tensor core wants them, each
-// CTA copies its 64 rows.  Nothing needs cleaning behind a sequence's end: whatever bits a row
-// holds, its latents are finite, and its scores are not looked at.
+// rows x 128 columns: first the four score boxes (the CTA's 64 rows), two warps a box, then the
+// four output units (all 128 rows x its 256 columns).  While the tensor cores take the scores of
+// a tile the warps decode its output units, and during an output product the next tile's scores.
+// (Four warps on the boxes and four on the units, a box or unit each: 193 us for 32 x 16384 rows
+// x 128 heads, the scores of a tile waiting for one warp's whole box.  A box that is both is
+// decoded twice: one copy would tie the scores of a tile to the output product of the one
+// before.)  The CTA's own half of the rows is read by both steps, so it has two buffers.  Of the
+// keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
+// cleaning behind a sequence's end: whatever bits a row holds, its latents are finite, and its
+// scores are not looked at.
 //
 // Tensor memory per CTA as in mla_pair.cu: S0 and S1, two buffers of 64 columns each, and O.
 //
 // Warps (1024 threads): 0-15 softmax and epilogue; 16 copies of rows; 17 keys and the first
 // query; 18 score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue
-// for the pair); 22 the later items' queries; 24-27 score boxes, 28-31 output units.
+// for the pair); 22 the later items' queries; 24-31 codes to E4M3.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
@@ -40,7 +44,9 @@ struct Q4Pair {
   static constexpr int kParts = 2;
   static constexpr int kQKeys = kParts * 4 * kPBox;     // offset of the query's key part
   static constexpr int kQBytes = kQKeys + kPBox;
-  static constexpr int kSlotRows = 32, kSlots = 4;      // a tile's rows
+  // Rows arrive in slots of 32: two tiles' of the CTA's own half, one's of the other half.
+  static constexpr int kSlotRows = 32, kSlots = 6;
+  static constexpr int kPeerSlot = 4;                   // own: 2 (tile & 1) + which 32 rows
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
   static constexpr int kOffQ = 0;
@@ -138,19 +144,18 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
   auto bar = [&](int i) { return bars + 8 * i; };
   auto lbar = [&](int i) { return lead + 8 * i; };
   constexpr int kWarpRows = L::kSoftWarps, kWarpKeys = kWarpRows + 1, kWarpScore = kWarpRows + 2,
-                kWarpOut = kWarpRows + 4, kWarpQuery = kWarpRows + 6, kWarpBox = kWarpRows + 8,
-                kWarpUnit = kWarpBox + 4;
+                kWarpOut = kWarpRows + 4, kWarpQuery = kWarpRows + 6, kWarpDecode = kWarpRows + 8;
 
   if (tid == L::kSoft) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(L::RAWFULL + i), 1);
-      // decoded by the units' two warps of that row half, of the CTA's own half by the boxes' too
-      mbar_init(bar(L::RAWEMPTY + i), (i >> 1) == rank ? 6 : 2);
+      // decoded into the row half's two units, of the CTA's own half into four boxes too
+      mbar_init(bar(L::RAWEMPTY + i), i < L::kPeerSlot ? 6 : 2);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(L::FULLS + i), 2);   // a warp of each CTA
+      mbar_init(bar(L::FULLS + i), 4);   // two warps of each CTA
       mbar_init(bar(L::EMPTYS + i), 1);
-      mbar_init(bar(L::FULLV + i), 2);
+      mbar_init(bar(L::FULLV + i), 4);
       mbar_init(bar(L::EMPTYV + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_qpe);
   }
-  if (warp == kWarpBox && lane < 16) q4_table(smem + L::kOffTable, lane);
+  if (warp == kWarpDecode && lane < 16) q4_table(smem + L::kOffTable, lane);
   if (kShare && warp == kWarpRows) {
     __syncwarp();
     share = take_share<true>(p, blockIdx.x / parts, gridDim.x / parts, lane, blockIdx.x == 0);
@@ -281,14 +286,16 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         // The CTA's own half first: its scores start a tile.
         const int per = L::kSlotRows / piece;
 #pragma unroll 1
-        for (int k = 0; k < L::kSlots; ++k) {
-          const int s = k ^ (rank << 1);
-          if (t > 0) {
-            warp_wait(bar(L::RAWEMPTY + s), (t - 1) & 1, abort_flag);
+        for (int k = 0; k < 4; ++k) {
+          const bool own = k < 2;
+          const int at = (k & 1) + (own ? 2 * (t & 1) : L::kPeerSlot);        // slot
+          const int from = ((k & 1) + 2 * (own ? rank : 1 - rank)) * per;     // the tile's pieces
+          if (t >= (own ? 2 : 1)) {
+            warp_wait(bar(L::RAWEMPTY + at), own ? ((t - 2) >> 1) & 1 : (t - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
-          copy_pieces(src, s * per, (s + 1) * per, live, piece * bytes,
-                      sbase + L::kOffRaw + s * L::kSlotBytes, bar(L::RAWFULL + s));
+          copy_pieces(src, from, from + per, live, piece * bytes,
+                      sbase + L::kOffRaw + at * L::kSlotBytes, bar(L::RAWFULL + at));
         }
       } else {
         if (t >= 2) {   // the scores of tile t - 2 have read this buffer
@@ -303,39 +310,45 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       return true;
     });
     if (!rows && landed < issued) hand_over(issued - 1);
-  } else if (warp >= kWarpBox) {
+  } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
-    // Warp m of the first four: score box m, columns 128 m .. of the CTA's 64 rows; warp u of
-    // the others: output unit u, row half u >> 1, columns 256 (u & 1) + 128 rank ..  A lane
-    // takes a row of each of the half's two slots: rows are 17 times 16 bytes apart, so eight
-    // lanes read from eight different pieces of the banks, and the swizzle has them write so.
-    const bool unit = warp >= kWarpUnit;
-    const int u = (warp - kWarpBox) & 3;
-    const int half = unit ? u >> 1 : rank, box = unit ? 2 * (u & 1) + rank : u;
-    const int empty = (unit ? L::EMPTYV : L::EMPTYS) + u, full = (unit ? L::FULLV : L::FULLS) + u;
-    uint8_t* to = smem + (unit ? L::kOffV : L::kOffS) + u * kPBox + lane * 128;
-    const uint8_t* from = smem + L::kOffRaw + 2 * half * L::kSlotBytes + lane * kQ4LatBytes;
+    // Warp d: 32 rows (slot d >> 2 of a row half) of score box u = d & 3, columns 128 u .. of the
+    // CTA's own half, then of output unit u, row half u >> 1, columns 256 (u & 1) + 128 rank ..
+    // A row per lane: rows are 17 times 16 bytes apart, so eight lanes read from eight different
+    // pieces of the banks, and the swizzle has them write so.
+    const int u = (warp - kWarpDecode) & 3, k = (warp - kWarpDecode) >> 2;
+    const bool own = (u >> 1) == rank;   // the unit's rows
+    const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
+    uint8_t* to = smem + u * kPBox + k * (L::kSlotRows * 128) + lane * 128;
     const uint32_t swz = (lane & 7) << 4;
+    auto decode = [&](int slot, uint32_t parity, int box, uint8_t* dst, int full) {
+      warp_wait(bar(L::RAWFULL + slot), parity, abort_flag);
+      const uint8_t* raw = from + slot * L::kSlotBytes;
+      q4_decode<4>(raw + 64 * box,
+                   *reinterpret_cast<const uint32_t*>(raw + kQ4CodeBytes + 4 * box), dst, 0, swz,
+                   smem + L::kOffTable);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::RAWEMPTY + slot));
+        arrive_cluster(lbar(full));
+      }
+    };
     for (int t = 0; t < T; ++t) {
+      const int slot = 2 * (t & 1) + k;
       if (t > 0) {
-        warp_wait(bar(empty), (t - 1) & 1, abort_flag);
+        warp_wait(bar(L::EMPTYS + u), (t - 1) & 1, abort_flag);
         tc_fence_after();
       }
       if (given_up()) break;
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int s = 2 * half + k;
-        warp_wait(bar(L::RAWFULL + s), t & 1, abort_flag);
-        const uint8_t* raw = from + k * L::kSlotBytes;
-        q4_decode<4>(raw + 64 * box,
-                     *reinterpret_cast<const uint32_t*>(raw + kQ4CodeBytes + 4 * box),
-                     to + k * (L::kSlotRows * 128), 0, swz, smem + L::kOffTable);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + s));
+      decode(slot, (t >> 1) & 1, u, to + L::kOffS, L::FULLS + u);
+      if (t > 0) {
+        warp_wait(bar(L::EMPTYV + u), (t - 1) & 1, abort_flag);
+        tc_fence_after();
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(lbar(full));
+      if (given_up()) break;
+      decode(own ? slot : L::kPeerSlot + k, own ? (t >> 1) & 1 : t & 1, 2 * (u & 1) + rank,
+             to + L::kOffV, L::FULLV + u);
     }
   } else if (kShare && warp == kWarpQuery) {
     // ------------------------------------------------------------ the later items' queries
