@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(32 * kWarps)
                     make_float2(v[2 * k] * inv, v[2 * k + 1] * inv), __NV_E2M1,
                     cudaRoundNearest)) << (8 * k);
       reinterpret_cast<uint32_t*>(page.codes(r))[32 * i + lane] = q4_page_word(code);
-      uint32_t word = (lane & 1) ? 0u : e8 << (4 * ((lane >> 1) & 7));
+      // (e + 5) mod 16
+      uint32_t word = (lane & 1) ? 0u : ((e8 + 13u) & 15u) << (4 * ((lane >> 1) & 7));
 #pragma unroll
       for (int off = 2; off < 16; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
       if ((lane & 15) == 0)

@@ -15,7 +15,9 @@
 //   latents [R][272]  256 bytes of codes, a 32-bit word for eight values: the magnitude of
 //                     value k in bits 4 k .. 4 k + 2, the signs of values 0-3 in bits 7, 15,
 //                     23, 31 and of 4-7 in bits 3, 11, 19, 27 (where a reader wants them);
-//                     then 16 of exponents, byte i: e + 8 of blocks 2 i (low four bits), 2 i + 1
+//                     then 16 of exponents, byte i: (e + 5) mod 16 of blocks 2 i (low four
+//                     bits) and 2 i + 1, so that the exponents with which every magnitude is a
+//                     normal E4M3 number (-5 .. 6) are the bits 0 .. 11
 //   keys    [R][128]  16-byte piece c of row r stands at piece c ^ (r & 7): as the tensor core
 //                     wants it in shared memory (128-byte swizzle)
 #pragma once
@@ -52,9 +54,9 @@ __device__ __forceinline__ uint32_t q4_key_at(int r, int pair) {
   return static_cast<uint32_t>(r * kQ4KeyBytes + ((((pair >> 2) ^ r) & 7) << 4) + ((pair & 3) << 2));
 }
 
-// 2^e for the four bits that hold e + 8 (15 is never written; it reads as 14 does).
+// 2^e for an exponent's four bits (12 is never written; it reads as 11, e = 6, does).
 __device__ __forceinline__ float q4_unit(uint32_t bits) {
-  return __uint_as_float((min(bits & 15u, 14u) + static_cast<uint32_t>(127 + kQ4ExpMin)) << 23);
+  return __uint_as_float((min((bits + 3u) & 15u, 14u) + static_cast<uint32_t>(127 + kQ4ExpMin)) << 23);
 }
 
 // Eight codes, value k in bits 4 k .. 4 k + 3, as a page holds them, and back.
@@ -106,6 +108,49 @@ struct Q4Lane {
   }
 };
 
+// Whether `x` holds for any of `count` threads (named barrier `bar`).
+__device__ __forceinline__ bool any_of(bool x, int bar, int count) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(bar), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+// Waits for a phase, bounded: gives up, raising the CTA's abort flag, after the library's limit.
+// The warp is suspended for up to kSuspendNs at a time: so many warps of these kernels wait that
+// their polling would take issue slots from the others.
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// The same by a whole warp, which leaves it converged (as the .aligned tensor-core
+// instructions after it need).
+__device__ __forceinline__ void q4_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  q4_wait(bar, parity, abort);
+  __syncwarp();
+}
+
 // ------------------------------------------------------------- codes to E4M3
 __device__ __forceinline__ uint16_t to_e4m3x2(float x0, float x1) {
   return static_cast<uint16_t>(
@@ -118,7 +163,7 @@ __device__ __forceinline__ uint2 decode8(uint32_t w, uint2 mag) {
                     __byte_perm(mag.x, mag.y, sel >> 16) | ((w << 4) & 0x80808080u));
 }
 // Table of magnitudes by exponent bits, for q4_decode (16 entries of 8 bytes, by 16 lanes):
-// 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^(lane - 8) as E4M3 (15 as 14).
+// 0, 1/2, 1, 3/2, 2, 3, 4, 6 times 2^e as E4M3.
 __device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
   const float u = q4_unit(lane);
   reinterpret_cast<uint2*>(table)[lane] =
@@ -127,21 +172,20 @@ __device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
 }
 
 // kEach times 32 codes of one row, from src (16 bytes each), as E4M3 into the row's 16-byte
-// units unit0 .. of a box of 128-byte rows (swz: 16 (row mod 8), the 128-byte swizzle); e: their
-// exponents, a byte for two blocks.  By a whole warp, a row or part of one per lane.
-template <int kEach>
+// units unit0 .. of a box of 128-byte rows (swz: 16 (row mod 8), the 128-byte swizzle), and with
+// kTwice into those of another, `other` bytes on, where that is not 0; e: their exponents, a byte
+// for two blocks.  By a whole warp, a row or part of one per lane.
+template <int kEach, bool kTwice = false>
 __device__ __forceinline__ void q4_decode(const uint8_t* src, uint32_t e, uint8_t* row,
-                                          uint32_t unit0, uint32_t swz, const uint8_t* table) {
+                                          uint32_t unit0, uint32_t swz, const uint8_t* table,
+                                          int other = 0) {
   uint4 w = *reinterpret_cast<const uint4*>(src);
-  // From e = -5 on (bits 3) every magnitude is a normal E4M3 number, whose exponent field grows
-  // with e; where a lane has smaller ones (or the bits 15) the warp looks them up.
-  constexpr uint32_t kMine = kEach == 4 ? 0x0f0f0f0fu : kEach == 2 ? 0x0f0fu : 0x0fu;
-  const uint32_t low = e & kMine, high = (e >> 4) & kMine;
-  const uint32_t odd = __vcmpltu4(low, 0x03030303u) | __vcmpltu4(high, 0x03030303u) |
-                       __vcmpeq4(low, 0x0f0f0f0fu) | __vcmpeq4(high, 0x0f0f0f0fu);
-  // (Not unrolled: a loop that stays in the instruction cache.)
+  // Up to the bits 11 every magnitude is a normal E4M3 number, whose exponent field grows with
+  // e; where a lane has others the warp looks them up.
+  constexpr uint32_t kMine = kEach == 4 ? 0x88888888u : kEach == 2 ? 0x8888u : 0x88u;
+  const uint32_t odd = e & (e << 1) & kMine;
   auto decode = [&](auto&& magnitudes) {
-#pragma unroll 1
+#pragma unroll 2
     for (int k = 0; k < kEach; ++k) {
       const uint2 m0 = magnitudes(e & 15), m1 = magnitudes((e >> 4) & 15);
       e >>= 8;
@@ -149,16 +193,22 @@ __device__ __forceinline__ void q4_decode(const uint8_t* src, uint32_t e, uint8_
       if (k + 1 < kEach) w = *reinterpret_cast<const uint4*>(src + 16 * (k + 1));
       const uint32_t at = ((unit0 + 2 * k) << 4) ^ swz;
       const uint2 a = decode8(v.x, m0), b = decode8(v.y, m0);
-      *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
+      const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(row + at) = o0;
       const uint2 x = decode8(v.z, m1), y = decode8(v.w, m1);
-      *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
+      const uint4 o1 = make_uint4(x.x, x.y, y.x, y.y);
+      *reinterpret_cast<uint4*>(row + (at ^ 16)) = o1;
+      if (kTwice && other) {
+        *reinterpret_cast<uint4*>(row + other + at) = o0;
+        *reinterpret_cast<uint4*>(row + other + (at ^ 16)) = o1;
+      }
     }
   };
-  if (__any_sync(0xffffffffu, (odd & kMine) != 0))
+  if (__any_sync(0xffffffffu, odd != 0))
     decode([&](uint32_t x) { return *reinterpret_cast<const uint2*>(table + 8 * x); });
   else
     decode([&](uint32_t x) {
-      return make_uint2(x * 0x08080800u - 0x04081000u, x * 0x08080808u + 0x0c080400u);
+      return make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u);
     });
 }
 

@@ -129,25 +129,6 @@ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-// The same by a whole warp, which leaves it converged.
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  q4_wait(bar, parity, abort);
-  __syncwarp();
-}
-
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
   return __half22float2(
       __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3)));
@@ -160,18 +141,6 @@ __device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
 
 // Where the rows of a page that does not exist come from.
 __device__ __align__(128) uint8_t g_q4_zeros[kRowsT * kQ4LatBytes];
-
-// Whether `x` holds for any of `count` threads (named barrier `bar`).
-__device__ __forceinline__ bool any_of(bool x, int bar, int count) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(bar), "r"(count)
-      : "memory");
-  return r != 0;
-}
 
 // The query image of one (query group b, head h), in units of sigma, a power of two that puts
 // the largest magnitude of q_abs and q_pe in [128, 256): q_abs (512 values) becomes a1 + a2 /
@@ -320,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
   auto issue_slot = [&](const uint8_t* src, int live, int n) {   // false: given up
     const int at = n % L::kSlots, per = L::kSlotRows / lat_piece, from = n % kTileSlots * per;
     if (n >= L::kSlots) {
-      warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     copy_pieces(src, from, from + per, live, lat_piece * kQ4LatBytes,
@@ -331,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     const int bf = t & 1;
     const uint8_t* src = piece_source(id, r0, key_piece, kQ4LatBytes, kQ4KeyBytes);
     if (t >= 2) {
-      warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     copy_pieces(src, 0, kRowsT / key_piece, __popc(__ballot_sync(0xffffffffu, id != -2)),
@@ -429,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (t > 0 && issue_keys(id, r0, t)) keys = t + 1;
       if (kShare && later) {
         // A new item's query, once the last score MMA of the one before has read its own.
-        warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
         if (!__any_sync(0xffffffffu, *abort_flag) && lane == 0) {
           pdl_wait();
           load_query(now.v);
@@ -456,14 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     for (int t = 0; t < T; ++t) {
       uint8_t* tile = to + (t & 1) * kTile;
       if (t >= 2) {
-        warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
         tc_fence_after();
       }
       if (__any_sync(0xffffffffu, *abort_flag)) break;
 #pragma unroll 1
       for (int s = team; s < kTileSlots; s += kTeams, n += kTeams) {
         const int slot = n % L::kSlots;
-        warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
+        q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
         const uint8_t* src = from + slot * L::kSlotBytes;
         uint32_t e = *reinterpret_cast<const uint32_t*>(exps + slot * L::kSlotBytes);
         if (kEach < 4) e >>= 8 * kEach * part;
@@ -492,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (left == 0) {
         if (t > 0) cur = item_after(cur, t);
         left = cur.tiles;
-        warp_wait(bar(L::QREADY), n & 1, abort_flag);
+        q4_warp_wait(bar(L::QREADY), n & 1, abort_flag);
         if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
           // The run with a query group's first tile says how many runs it spans.  (Not
           // before a query is here, fetched behind the PDL wait: the combine of the call
@@ -502,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         ++n;
       }
       --left;
-      if (t >= 2) warp_wait(bar(L::SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
-      warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag);
+      if (t >= 2) q4_warp_wait(bar(L::SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       // 16 key values (32 bytes) a step
       umma_x4<false, 2, 2>(tmem + kKCol + 32 * bf, k0 + ((bf * kKeyTile) >> 4),
                            q0 + (L::kQKeys >> 4), idesc_k, 0);
-      warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -538,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         cur = item_after(cur, t);
         done = 0;
       }
-      warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       const uint64_t pd = p0 + static_cast<uint64_t>((bf * L::kPBuf) >> 4);
@@ -588,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       for (int t = t0; t < t0 + tiles; ++t) {
         const int sb = t & 1;
         const int valid = t == t0 + tiles - 1 ? last_valid : kRowsT;
-        warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
         tc_fence_after();
         float x[kHalf];   // scores in units of the head's scale
         {
@@ -656,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             l[h] *= alpha[h];
           }
           if (t > t0) {
-            warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            q4_warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
@@ -707,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
           }
         }
         // P^T buffer sb was last read by the PV of tile t-2.
-        if (t >= 2) warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
+        if (t >= 2) q4_warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
         {
           // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
           // 16 part + n is part `part` of head n; the K index is the tile row.
@@ -745,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         read_scales();
       }
       // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
-      warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
       named_bar_sync(3 + gp, kSoft / 2);
       if (!*abort_flag) {

@@ -11,16 +11,15 @@
 // Queries are two E4M3 parts in units of a power of two per head (their keys' part bf16, and
 // so S1 has no unit), P an E4M3 part and its E5M2 remainder.
 //
-// What differs is where the operands come from.  A tile of 128 rows (35 KB of codes and
-// exponents) lands in both CTAs as it is stored, and eight warps turn it into E4M3 boxes of 64
-// rows x 128 columns: first the four score boxes (the CTA's 64 rows), two warps a box, then the
-// four output units (all 128 rows x its 256 columns).  While the tensor cores take the scores of
-// a tile the warps decode its output units, and during an output product the next tile's scores.
-// (Four warps on the boxes and four on the units, a box or unit each: 193 us for 32 x 16384 rows
-// x 128 heads, the scores of a tile waiting for one warp's whole box.  A box that is both is
-// decoded twice: one copy would tie the scores of a tile to the output product of the one
-// before.)  The CTA's own half of the rows is read by both steps, so it has two buffers.  Of the
-// keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
+// What differs is where the operands come from.  A tile's codes and exponents pass through both
+// CTAs as they are stored, 32 rows at a time, and eight warps turn them into E4M3 boxes of 64
+// rows x 128 columns: of the CTA's own 64 rows four score boxes, two of which are output units as
+// well (decoded once, written twice), of the other CTA's rows the two other output units.  Score
+// boxes are free again when the scores are done, output units, of which there are two tiles',
+// when their product is.  (With a box or unit per warp and one tile of each, 32 x 16384 rows x
+// 128 heads took 193 us, the scores of a tile waiting for one warp's whole box; with all warps
+// on the boxes and then on the units 172, the units waiting for the output product before.)
+// Of the keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
 // cleaning behind a sequence's end: whatever bits a row holds, its latents are finite, and its
 // scores are not looked at.
 //
@@ -44,26 +43,26 @@ struct Q4Pair {
   static constexpr int kParts = 2;
   static constexpr int kQKeys = kParts * 4 * kPBox;     // offset of the query's key part
   static constexpr int kQBytes = kQKeys + kPBox;
-  // Rows arrive in slots of 32: two tiles' of the CTA's own half, one's of the other half.
-  static constexpr int kSlotRows = 32, kSlots = 6;
-  static constexpr int kPeerSlot = 4;                   // own: 2 (tile & 1) + which 32 rows
+  // Rows arrive in two slots of 32: the CTA's own half of a tile, then the other half.
+  static constexpr int kSlotRows = 32, kSlots = 2;
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
   static constexpr int kOffQ = 0;
   static constexpr int kOffS = kOffQ + kQBytes;         // [4] score boxes
-  static constexpr int kOffV = kOffS + 4 * kPBox;       // [row half][O tile] output units
-  static constexpr int kOffK = kOffV + 4 * kPBox;       // [2] keys
+  static constexpr int kOffV = kOffS + 4 * kPBox;       // [2][row half][O tile] output units
+  static constexpr int kOffK = kOffV + 8 * kPBox;       // [2] keys
   static constexpr int kOffP = kOffK + 2 * kKeyBytes;
   static constexpr int kOffRaw = kOffP + kPBufBytes;
   static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;
-  static constexpr int kOffRed = kOffTable + 128;       // [2][2 kSlices][64] maxima
-  static constexpr int kOffSum = kOffRed + 2 * 2 * kSlices * kPHeads * 4;   // row sums
+  static constexpr int kOffRed = kOffTable + 128;       // [2 kSlices][64] maxima
+  static constexpr int kOffSum = kOffRed + 2 * kSlices * kPHeads * 4;       // row sums
   static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
-  // Rows landed / decoded and keys landed (this CTA's); score boxes and output units handed
-  // over / free; keys handed over; S, P, O and the query as in mla_pair.cu.
+  // Rows landed / decoded and keys landed (this CTA's); score boxes handed over / free; output
+  // units handed over (free with PVDONE); keys handed over; S, P, O and the query as in
+  // mla_pair.cu.
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots, KEYFULL = RAWEMPTY + kSlots,
                        FULLS = KEYFULL + 2, EMPTYS = FULLS + 4, FULLV = EMPTYS + 4,
-                       EMPTYV = FULLV + 4, KREADY = EMPTYV + 4, SREADY = KREADY + 2,
+                       KREADY = FULLV + 8, SREADY = KREADY + 2,
                        SFREE = SREADY + 2, PREADY = SFREE + 2, PVDONE = PREADY + 2,
                        QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
@@ -91,6 +90,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
         "=r"(r[7])
       : "r"(taddr)
       : "memory");
+}
+
+// Asks L2 for `bytes` bytes at `src` (16-byte units).
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // Where the rows of a page that does not exist come from.
@@ -149,14 +153,13 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
   if (tid == L::kSoft) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(L::RAWFULL + i), 1);
-      // decoded into the row half's two units, of the CTA's own half into four boxes too
-      mbar_init(bar(L::RAWEMPTY + i), i < L::kPeerSlot ? 6 : 2);
+      mbar_init(bar(L::RAWEMPTY + i), 8);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(L::FULLS + i), 4);   // two warps of each CTA
       mbar_init(bar(L::EMPTYS + i), 1);
-      mbar_init(bar(L::FULLV + i), 4);
-      mbar_init(bar(L::EMPTYV + i), 1);
+      mbar_init(bar(L::FULLV + i), 6);   // two of the CTA whose rows they are, four of the other
+      mbar_init(bar(L::FULLV + 4 + i), 6);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::KEYFULL + i), 1);
@@ -259,39 +262,50 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     int landed = 0;                                  // tiles whose keys were handed over
     // Hands the keys of tile t over once they have landed: the even CTA's MMAs read both.
     auto hand_over = [&](int t) {
-      warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
       if (lane == 0) arrive_cluster(lbar(L::KREADY + (t & 1)));
       landed = t + 1;
     };
     int issued = 0;
     for_tiles([&](const TileItem& it, int i, int t) {
       if (given_up()) return false;
-      int id = ahead;
+      int id = ahead, r_next = 0;
+      const int mask = (1 << p.page_shift) - 1;
+      ahead = -2;
       if (t + 1 < T) {
-        if (i + 1 < it.tiles)
+        if (i + 1 < it.tiles) {
           ahead = piece_page(it, i + 1);
-        else
-          ahead = piece_page(item_after(it, t + 1), 0);
+        } else {
+          const TileItem then = item_after(it, t + 1);
+          ahead = piece_page(then, 0);
+          r_next = then.r0 + row0 + lane * piece;
+        }
       }
       if (id >= p.num_pages) id = -1;
       if (id == -1) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
       const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
-      const int r = (it.r0 + row0 + lane * piece) & ((1 << p.page_shift) - 1);
-      const int in_page = (r + i * kTileRows) & ((1 << p.page_shift) - 1);
+      const int r = it.r0 + row0 + lane * piece;
+      const int in_page = (r + i * kTileRows) & mask;
       const uint8_t* src =
           id < 0 ? g_q4_pair_zeros
                  : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
                        (static_cast<size_t>(plane) << p.page_shift) + in_page * bytes;
       if (rows) {
-        // The CTA's own half first: its scores start a tile.
+        // The next tile's rows of the CTA's half are asked for ahead: two slots are not enough to
+        // cover the way from HBM.
         const int per = L::kSlotRows / piece;
+        if (ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank) {
+          const int rn = (i + 1 < it.tiles ? r + (i + 1) * kTileRows : r_next) & mask;
+          prefetch_l2(pool + (static_cast<size_t>(ahead) << p.page_shift) * kQ4RowBytes + rn * bytes,
+                      piece * bytes);
+        }
+        // The CTA's own half first: its scores start a tile.
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          const bool own = k < 2;
-          const int at = (k & 1) + (own ? 2 * (t & 1) : L::kPeerSlot);        // slot
-          const int from = ((k & 1) + 2 * (own ? rank : 1 - rank)) * per;     // the tile's pieces
-          if (t >= (own ? 2 : 1)) {
-            warp_wait(bar(L::RAWEMPTY + at), own ? ((t - 2) >> 1) & 1 : (t - 1) & 1, abort_flag);
+          const int at = k & 1, n = 4 * t + k;
+          const int from = (at + 2 * (k < 2 ? rank : 1 - rank)) * per;   // of the tile's pieces
+          if (n >= L::kSlots) {
+            q4_warp_wait(bar(L::RAWEMPTY + at), ((n >> 1) - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
           copy_pieces(src, from, from + per, live, piece * bytes,
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         }
       } else {
         if (t >= 2) {   // the scores of tile t - 2 have read this buffer
-          warp_wait(bar(L::SREADY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+          q4_warp_wait(bar(L::SREADY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
           if (given_up()) return false;
         }
         copy_pieces(src, 0, 64 / piece, live, piece * bytes,
@@ -312,43 +326,55 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     if (!rows && landed < issued) hand_over(issued - 1);
   } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
-    // Warp d: 32 rows (slot d >> 2 of a row half) of score box u = d & 3, columns 128 u .. of the
-    // CTA's own half, then of output unit u, row half u >> 1, columns 256 (u & 1) + 128 rank ..
-    // A row per lane: rows are 17 times 16 bytes apart, so eight lanes read from eight different
-    // pieces of the banks, and the swizzle has them write so.
-    const int u = (warp - kWarpDecode) & 3, k = (warp - kWarpDecode) >> 2;
-    const bool own = (u >> 1) == rank;   // the unit's rows
+    // Warp d, of the CTA's own rows: 64 columns, half d >> 2 of score box u = d & 3, which where
+    // u & 1 is the CTA's rank is output unit (rank, u >> 1) too; of the other's rows: 32 columns,
+    // piece d & 3 of output unit (1 - rank, d >> 2).  A row per lane: rows are 17 times 16 bytes
+    // apart, so eight lanes read from eight different pieces of the banks, and the swizzle has
+    // them write so.
+    const int d = warp - kWarpDecode, u = d & 3, h = d >> 2;
+    const bool both = (u & 1) == rank;
+    const int own_unit = 2 * rank + (u >> 1), peer_unit = 2 * (1 - rank) + h;
+    const int peer_box = 2 * h + rank;
+    const uint8_t* table = smem + L::kOffTable;
     const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
-    uint8_t* to = smem + u * kPBox + k * (L::kSlotRows * 128) + lane * 128;
+    uint8_t* box = smem + L::kOffS + u * kPBox + lane * 128;
+    uint8_t* units = smem + L::kOffV + lane * 128;
     const uint32_t swz = (lane & 7) << 4;
-    auto decode = [&](int slot, uint32_t parity, int box, uint8_t* dst, int full) {
-      warp_wait(bar(L::RAWFULL + slot), parity, abort_flag);
-      const uint8_t* raw = from + slot * L::kSlotBytes;
-      q4_decode<4>(raw + 64 * box,
-                   *reinterpret_cast<const uint32_t*>(raw + kQ4CodeBytes + 4 * box), dst, 0, swz,
-                   smem + L::kOffTable);
+    for (int t = 0; t < T; ++t) {
+      const int buf = 4 * (t & 1);   // its first unit
+      if (t > 0) q4_warp_wait(bar(L::EMPTYS + u), (t - 1) & 1, abort_flag);
+      if (t > 1) q4_warp_wait(bar(L::PVDONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+      tc_fence_after();
+      if (given_up()) break;
+      const int other = both ? static_cast<int>(units - box) + (buf + own_unit) * kPBox : 0;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        q4_warp_wait(bar(L::RAWFULL + k), 0, abort_flag);
+        const uint8_t* raw = from + k * L::kSlotBytes;
+        q4_decode<2, true>(raw + 64 * u + 32 * h,
+                           *reinterpret_cast<const uint16_t*>(raw + kQ4CodeBytes + 4 * u + 2 * h),
+                           box + k * (L::kSlotRows * 128), 4 * h, swz, table, other);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(L::RAWEMPTY + slot));
-        arrive_cluster(lbar(full));
+        arrive_cluster(lbar(L::FULLS + u));
+        if (both) arrive_cluster(lbar(L::FULLV + buf + own_unit));
       }
-    };
-    for (int t = 0; t < T; ++t) {
-      const int slot = 2 * (t & 1) + k;
-      if (t > 0) {
-        warp_wait(bar(L::EMPTYS + u), (t - 1) & 1, abort_flag);
-        tc_fence_after();
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        q4_warp_wait(bar(L::RAWFULL + k), 1, abort_flag);
+        const uint8_t* raw = from + k * L::kSlotBytes;
+        q4_decode<1>(raw + 64 * peer_box + 16 * u, raw[kQ4CodeBytes + 4 * peer_box + u],
+                     units + (buf + peer_unit) * kPBox + k * (L::kSlotRows * 128), 2 * u, swz, table);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
       }
-      if (given_up()) break;
-      decode(slot, (t >> 1) & 1, u, to + L::kOffS, L::FULLS + u);
-      if (t > 0) {
-        warp_wait(bar(L::EMPTYV + u), (t - 1) & 1, abort_flag);
-        tc_fence_after();
-      }
-      if (given_up()) break;
-      decode(own ? slot : L::kPeerSlot + k, own ? (t >> 1) & 1 : t & 1, 2 * (u & 1) + rank,
-             to + L::kOffV, L::FULLV + u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lbar(L::FULLV + buf + peer_unit));
     }
   } else if (kShare && warp == kWarpQuery) {
     // ------------------------------------------------------------ the later items' queries
@@ -356,7 +382,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     TileItem it = item0;
     for (int t = it.tiles, n = 0; 0 < t && t < T; t += it.tiles, ++n) {
       it = item_after(it, t);
-      warp_wait(bar(L::QFREE), n & 1, abort_flag);
+      q4_warp_wait(bar(L::QFREE), n & 1, abort_flag);
       if (given_up()) break;
       pdl_wait();
       load_query(it.v);
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       for_tiles([&](const TileItem& it, int i, int t) {
         const int sb = t & 1;
         if (i == 0) {
-          warp_wait(bar(L::QFULL), n & 1, abort_flag);
+          q4_warp_wait(bar(L::QFULL), n & 1, abort_flag);
           ++n;
           if (kShare && !keys && blockIdx.x % parts == 0 && it.r0 == 0)
             // The run with a sequence's first tile says how many runs it spans.  (Not before a
@@ -386,10 +412,10 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
             for (int q = lane; q < p.q_len; q += 32)
               p.pieces[it.v * p.q_len + q] = count_pieces(it, share.first + t, share.each);
         }
-        if (t >= 2) warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
+        if (t >= 2) q4_warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
         if (given_up()) return false;
         if (keys) {
-          warp_wait(bar(L::KREADY + sb), (t >> 1) & 1, abort_flag);
+          q4_warp_wait(bar(L::KREADY + sb), (t >> 1) & 1, abort_flag);
           if (given_up()) return false;
           tc_fence_after();
           const uint64_t b = k0 + static_cast<uint64_t>(sb * (L::kKeyBytes >> 4));
@@ -399,7 +425,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         } else {
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
-            warp_wait(bar(L::FULLS + m), t & 1, abort_flag);
+            q4_warp_wait(bar(L::FULLS + m), t & 1, abort_flag);
             if (given_up()) return false;
             tc_fence_after();
             const uint64_t b = s0 + static_cast<uint64_t>(m * (kPBox >> 4));
@@ -431,12 +457,12 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       const uint32_t d = tmem + L::kOCol + 128 * jj;
       for_tiles([&](const TileItem&, int i, int t) {
         const int pb = t & 1;
-        warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
         if (given_up()) return false;
 #pragma unroll 1
         for (int kh = 0; kh < 2; ++kh) {
-          const int u = 2 * kh + jj;
-          warp_wait(bar(L::FULLV + u), t & 1, abort_flag);
+          const int u = 4 * pb + 2 * kh + jj;
+          q4_warp_wait(bar(L::FULLV + u), (t >> 1) & 1, abort_flag);
           if (given_up()) return false;
           tc_fence_after();
           const uint64_t b = v0 + static_cast<uint64_t>(u * (kPBox >> 4));
@@ -450,7 +476,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
                              idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
                              part > 0 || ks > 0 ? 1u : (i > 0 || kh > 0 ? 1u : 0u));
           }
-          commit_pair(bar(L::EMPTYV + u));
         }
         commit_pair(bar(L::PVDONE + pb));
         return true;
@@ -474,14 +499,14 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       // Rows from this thread's first on that its head's token attends: one before the last
       // token sees fewer.
       const int limit = min(tiles * kTileRows, it.len - back - it.r0) - row0 + t0 * kTileRows;
-      float m = -INFINITY, l = 0.f;
+      float m = 0.f, l = 0.f;   // m is set by the item's first tile
       // A wait that gives up leaves the loop running (every later wait then returns at
       // once), so that all softmax warps meet at the same barriers.
       for (int t = t0; t < t0 + tiles; ++t) {
         const int sb = t & 1;
-        warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
         // written by the kernel before, known complete once the first scores are
-        if (t == t0) unit = __ldcg(sigma + flat0 + min(head, mine - 1));
+        if (t == t0) unit = __ldcg(sigma + flat0 + min(head, mine - 1)) * scale;
         tc_fence_after();
         float x[kCols], y[kCols];
         const uint32_t s_at = lanes + 64 * sb + kCols * hh;
@@ -490,8 +515,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(lbar(L::SFREE + sb));
+        // Scores above the head's reference.
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) x[i] = fmaf(x[i], unit, y[i]);
+        for (int i = 0; i < kCols; ++i) x[i] = fmaf(x[i], unit, fmaf(y[i], scale, -m));
         if (__any_sync(0xffffffffu, t * kTileRows + kCols > limit)) {
 #pragma unroll
           for (int i = 0; i < kCols; ++i)
@@ -500,22 +526,25 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         float mx = x[0];
 #pragma unroll
         for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
-        float* rd = red + sb * 2 * kSlices * kPHeads;
-        rd[part_of * kPHeads + head] = mx;
-        named_bar_sync(1, L::kSoft);
-        mx = rd[head];
+        // The eight warps of the same heads go by one reference, and decide alike.
+        if (any_of(t == t0 || mx > L::kBias + L::kGrow, 1 + (qd & 1), L::kSoft / 2)) {
+          red[part_of * kPHeads + head] = mx;
+          named_bar_sync(3 + (qd & 1), L::kSoft / 2);
+          mx = red[head];
 #pragma unroll
-        for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, rd[i * kPHeads + head]);
-        mx = mx * scale - L::kBias;
-        if (__any_sync(0xffffffffu, mx > m + L::kGrow)) {
-          // Move the references of the warp's heads (the four warps of the same heads
-          // decide alike); rescale the sum and this warp's share of O.
-          const float mn = fmaxf(m, mx);
-          const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
-          m = mn;
+          for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, red[i * kPHeads + head]);
+          // Move the reference (up, but to wherever the first tile has it; a head whose token
+          // attends none of its rows attends none of the item's); rescale the sum and this
+          // warp's share of O.
+          float up = mx - L::kBias;
+          up = t > t0 ? fmaxf(up, 0.f) : mx == -INFINITY ? 0.f : up;
+          const float alpha = ex2(-up);
+          m += up;
           l *= alpha;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) x[i] -= up;
           if (t > t0) {
-            warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 16 / kSlices; ++c) {   // this warp's slice of O's 256 columns
@@ -530,14 +559,13 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
             tmem_wait_st();
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
-          x[i] = ex2(fmaf(x[i], scale, -ref));
+          x[i] = ex2(x[i]);
           l += x[i];
         }
         // P was last read by the output MMAs of tile t - 1.
-        if (t >= 1) warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        if (t >= 1) q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
         {
           // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
           uint8_t* pb = smem + L::kOffP;
@@ -547,13 +575,13 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
             uint32_t a = 0, b = 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float y0 = x[4 * w + 2 * e], y1 = x[4 * w + 2 * e + 1];
-              const uint32_t f1 =
-                  __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-              const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                  static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3)));
-              const uint32_t f2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - g.x, y1 - g.y),
-                                                           __NV_SATFINITE, __NV_E5M2);
+              // by way of fp16, where the remainder is exact
+              const __half2 y = __floats2half2_rn(x[4 * w + 2 * e], x[4 * w + 2 * e + 1]);
+              const uint32_t f1 = __nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const __half2 g = __half2(
+                  __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(f1), __NV_E4M3));
+              const uint32_t f2 =
+                  __nv_cvt_halfraw2_to_fp8x2(__hsub2(y, g), __NV_SATFINITE, __NV_E5M2);
               a |= f1 << (16 * e);
               b |= f2 << (16 * e);
             }
@@ -575,9 +603,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       // (over operands that nothing reads any more) to whole rows.
       float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
       sums[part_of * kPHeads + head] = l;
-      warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
-      named_bar_sync(1, L::kSoft);
+      named_bar_sync(5, L::kSoft);
       if (!*abort_flag) {
         float sum = 0.f;
 #pragma unroll
@@ -606,10 +634,11 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         const int latent = 256 * (col0 >> 7) + 128 * (qd >> 1) + (col0 & 127);
         if (kShare && t0 < T) {
           // The next item's operands are on their way to where the last one stages: each warp
-          // turns its 32 heads' columns over in its part of P, 8 at a time, and writes 32 bytes
-          // of sixteen rows at once.  (P of the next tile is written behind the barrier of its
-          // maxima.)
-          float4* mine4 = reinterpret_cast<float4*>(smem + L::kOffP) + 64 * warp;
+          // turns its 32 heads' columns over in P, 8 at a time, and writes 32 bytes of sixteen
+          // rows at once.  The eight warps of the same heads keep to those heads' rows of P,
+          // which they write again behind a barrier of their own.
+          float4* mine4 = reinterpret_cast<float4*>(smem + L::kOffP + (warp >> 3) * kPBox +
+                                                    4096 * (warp & 1) + 1024 * (warp >> 1 & 3));
           const int h0 = 32 * (qd & 1);
 #pragma unroll 1
           for (int c = 0; c < 32 / kSlices; ++c) {
@@ -640,7 +669,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
                   make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
                               o[4 * i + 3] * inv);
           }
-          named_bar_sync(1, L::kSoft);
+          named_bar_sync(5, L::kSoft);
           for (int h = warp; h < mine; h += L::kSoftWarps) {
             const float4* src = reinterpret_cast<const float4*>(smem + h * L::kStageRow);
 #pragma unroll

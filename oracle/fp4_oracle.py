@@ -64,7 +64,7 @@ def pack(code, e, key):
     w = np.asarray(code, np.uint64).reshape(n, R, D_C // 8, 8)
     word = ((w & np.uint64(7)) << MAG).sum(-1) | ((w >> np.uint64(3)) << SIGN).sum(-1)
     c = word.astype("<u4").view(np.uint8).reshape(n, R, D_C // 2)
-    u = (np.asarray(e) - E_MIN)
+    u = (np.asarray(e) + 5) & 15
     x = (u[..., 0::2] | u[..., 1::2] << 4).astype(np.uint8)
     k = np.ascontiguousarray(key).view(np.uint8).reshape(n, R, 8, 16)
     at = np.arange(8)[None, :] ^ (np.arange(R)[:, None] & 7)
@@ -82,7 +82,8 @@ def unpack(pool, page):
     c, x = c[..., :256], c[..., 256:]
     w = np.ascontiguousarray(c).view("<u4").astype(np.uint64)[..., None]
     code = ((w >> MAG & np.uint64(7)) | (w >> SIGN & np.uint64(1)) << np.uint64(3)).reshape(n, page, D_C).astype(np.int64)
-    e = np.stack([x & 15, x >> 4], -1).reshape(n, page, D_C // BLOCK).astype(np.int64) + E_MIN
+    e = np.stack([x & 15, x >> 4], -1).reshape(n, page, D_C // BLOCK).astype(np.int64)
+    e = ((e + 3) & 15) - 8
     at = np.arange(8)[None, :] ^ (np.arange(page)[:, None] & 7)
     key = np.take_along_axis(k, np.broadcast_to(at[None, :, :, None], k.shape), 2)
     return code, e, np.ascontiguousarray(key).view(np.uint16).reshape(n, page, D_R)

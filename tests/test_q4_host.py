@@ -69,7 +69,7 @@ def test_pack_and_unpack(page):
     word = int(flat[5 * 272 + 12:][:4].view("<u4")[0])
     bits = [7, 15, 23, 31, 3, 11, 19, 27]
     assert [(word >> 4 * k & 7) | (word >> bits[k] & 1) << 3 for k in range(8)] == code[1, 5, 24:32].tolist()
-    assert flat[5 * 272 + 256 + 3] == (e[1, 5, 6] + 8) | (e[1, 5, 7] + 8) << 4
+    assert flat[5 * 272 + 256 + 3] == ((e[1, 5, 6] + 5) & 15) | ((e[1, 5, 7] + 5) & 15) << 4
     piece = flat[page * 272 + 5 * 128:][:128].reshape(8, 16)[2 ^ 5]
     assert (piece.view(np.uint16) == key[1, 5, 16:24]).all()
 
