@@ -171,46 +171,39 @@ __device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
                  to_e4m3x2(2.f * u, 3.f * u) | to_e4m3x2(4.f * u, 6.f * u) << 16);
 }
 
-// kEach times 32 codes of one row, from src (16 bytes each), as E4M3 into the row's 16-byte
-// units unit0 .. of a box of 128-byte rows (swz: 16 (row mod 8), the 128-byte swizzle), and with
-// kTwice into those of another, `other` bytes on, where that is not 0; e: their exponents, a byte
-// for two blocks.  By a whole warp, a row or part of one per lane.
-template <int kEach, bool kTwice = false>
-__device__ __forceinline__ void q4_decode(const uint8_t* src, uint32_t e, uint8_t* row,
-                                          uint32_t unit0, uint32_t swz, const uint8_t* table,
-                                          int other = 0) {
-  uint4 w = *reinterpret_cast<const uint4*>(src);
+// 32 codes of one row and their two blocks' exponents, as loaded, and as E4M3 in the row's
+// 16-byte units at `at` and at ^ 16 of a box of 128-byte rows (the caller has the 128-byte
+// swizzle in `at`); with `other` != 0 the same `other` bytes on.
+struct Q4Piece {
+  uint4 w;
+  uint32_t e;   // one byte
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* exps) {
+    w = *reinterpret_cast<const uint4*>(codes);
+    e = *exps;
+  }
   // Up to the bits 11 every magnitude is a normal E4M3 number, whose exponent field grows with
-  // e; where a lane has others the warp looks them up.
-  constexpr uint32_t kMine = kEach == 4 ? 0x88888888u : kEach == 2 ? 0x8888u : 0x88u;
-  const uint32_t odd = e & (e << 1) & kMine;
-  auto decode = [&](auto&& magnitudes) {
-#pragma unroll 2
-    for (int k = 0; k < kEach; ++k) {
-      const uint2 m0 = magnitudes(e & 15), m1 = magnitudes((e >> 4) & 15);
-      e >>= 8;
-      const uint4 v = w;
-      if (k + 1 < kEach) w = *reinterpret_cast<const uint4*>(src + 16 * (k + 1));
-      const uint32_t at = ((unit0 + 2 * k) << 4) ^ swz;
-      const uint2 a = decode8(v.x, m0), b = decode8(v.y, m0);
-      const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y);
-      *reinterpret_cast<uint4*>(row + at) = o0;
-      const uint2 x = decode8(v.z, m1), y = decode8(v.w, m1);
-      const uint4 o1 = make_uint4(x.x, x.y, y.x, y.y);
-      *reinterpret_cast<uint4*>(row + (at ^ 16)) = o1;
-      if (kTwice && other) {
-        *reinterpret_cast<uint4*>(row + other + at) = o0;
-        *reinterpret_cast<uint4*>(row + other + (at ^ 16)) = o1;
-      }
+  // e; others are looked up.
+  __device__ __forceinline__ bool plain() const { return (e & (e << 1) & 0x88u) == 0; }
+  template <bool kPlain>
+  __device__ __forceinline__ void store(uint8_t* row, uint32_t at, int other,
+                                        const uint8_t* table) const {
+    auto magnitudes = [&](uint32_t x) {
+      return kPlain ? make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u)
+                    : *reinterpret_cast<const uint2*>(table + 8 * x);
+    };
+    const uint2 m0 = magnitudes(e & 15), m1 = magnitudes(e >> 4);
+    const uint2 a = decode8(w.x, m0), b = decode8(w.y, m0);
+    const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(row + at) = o0;
+    const uint2 x = decode8(w.z, m1), y = decode8(w.w, m1);
+    const uint4 o1 = make_uint4(x.x, x.y, y.x, y.y);
+    *reinterpret_cast<uint4*>(row + (at ^ 16)) = o1;
+    if (other) {
+      *reinterpret_cast<uint4*>(row + other + at) = o0;
+      *reinterpret_cast<uint4*>(row + other + (at ^ 16)) = o1;
     }
-  };
-  if (__any_sync(0xffffffffu, odd != 0))
-    decode([&](uint32_t x) { return *reinterpret_cast<const uint2*>(table + 8 * x); });
-  else
-    decode([&](uint32_t x) {
-      return make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u);
-    });
-}
+  }
+};
 
 __device__ __forceinline__ void bulk_g2s_elected(uint32_t dst, const void* src, uint32_t bytes,
                                                  uint32_t bar, uint64_t policy) {

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     const int r = lane % L::kSlotRows, part = lane / L::kSlotRows;
     constexpr int kEach = L::kSlotRows / 8;   // 16-byte pieces of codes (32 values) a lane
     const uint8_t* from = smem + L::kOffRaw + r * kQ4LatBytes + 64 * m + 16 * kEach * part;
-    const uint8_t* exps = smem + L::kOffRaw + r * kQ4LatBytes + kQ4CodeBytes + 4 * m;
+    const uint8_t* exps = smem + L::kOffRaw + r * kQ4LatBytes + kQ4CodeBytes + 4 * m + kEach * part;
     const uint8_t* table = smem + L::kOffTable;
     uint8_t* to = smem + L::kOffTile + m * kBox + r * 128;
     const uint32_t swz = (r & 7) << 4, unit0 = 2 * kEach * part;
@@ -434,12 +434,25 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const int slot = n % L::kSlots;
         q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
         const uint8_t* src = from + slot * L::kSlotBytes;
-        uint32_t e = *reinterpret_cast<const uint32_t*>(exps + slot * L::kSlotBytes);
-        if (kEach < 4) e >>= 8 * kEach * part;
-        uint8_t* row = tile + s * L::kSlotRows * 128;
-        q4_decode<kEach>(src, e, row, unit0, swz, table);
+        Q4Piece piece[kEach];
+        bool plain = true;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          piece[k].load(src + 16 * k, exps + slot * L::kSlotBytes + k);
+          plain = plain && piece[k].plain();
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+        uint8_t* row = tile + s * L::kSlotRows * 128;
+        if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+          for (int k = 0; k < kEach; ++k)
+            piece[k].template store<true>(row, ((unit0 + 2 * k) << 4) ^ swz, 0, table);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kEach; ++k)
+            piece[k].template store<false>(row, ((unit0 + 2 * k) << 4) ^ swz, 0, table);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();

@@ -92,6 +92,36 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
+// kSteps K steps of a pair's product, `sa` and `sb` (16-byte units) apart, by one elected thread
+// of the converged warp; the first replaces what D holds unless `accumulate`.  (With an election
+// and a predicate for every step the warp that issues the scores' 32 was what a tile waited for:
+// 169 us for 32 x 16384 rows x 128 heads.)
+template <bool kE4m3, int kSteps, int kSa, int kSb>
+__device__ __forceinline__ void mma_pair_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+  static_assert(kSteps == 2 || kSteps == 4, "steps");
+#define MLA_Q4_FIRST(KIND)                                                                    \
+  "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"                   \
+  "setp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                                   \
+  "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], %1, %2, %3, p;\n\t"                       \
+  "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"                                              \
+  "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %3, t;\n\t"
+#define MLA_Q4_MORE(KIND)                                                                     \
+  "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"                                                \
+  "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %3, t;\n\t"
+#define MLA_Q4_ARGS                                                                           \
+  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(kSa), "n"(kSb) : "memory"
+  if constexpr (kE4m3 && kSteps == 4)
+    asm volatile(MLA_Q4_FIRST("f8f6f4") MLA_Q4_MORE("f8f6f4") MLA_Q4_MORE("f8f6f4") "}" MLA_Q4_ARGS);
+  else if constexpr (kE4m3)
+    asm volatile(MLA_Q4_FIRST("f8f6f4") "}" MLA_Q4_ARGS);
+  else
+    asm volatile(MLA_Q4_FIRST("f16") MLA_Q4_MORE("f16") MLA_Q4_MORE("f16") "}" MLA_Q4_ARGS);
+#undef MLA_Q4_FIRST
+#undef MLA_Q4_MORE
+#undef MLA_Q4_ARGS
+}
+
 // Asks L2 for `bytes` bytes at `src` (16-byte units).
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
@@ -156,10 +186,10 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       mbar_init(bar(L::RAWEMPTY + i), 8);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(L::FULLS + i), 4);   // two warps of each CTA
+      mbar_init(bar(L::FULLS + i), 8);   // four warps of each CTA
       mbar_init(bar(L::EMPTYS + i), 1);
-      mbar_init(bar(L::FULLV + i), 6);   // two of the CTA whose rows they are, four of the other
-      mbar_init(bar(L::FULLV + 4 + i), 6);
+      mbar_init(bar(L::FULLV + i), 8);
+      mbar_init(bar(L::FULLV + 4 + i), 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::KEYFULL + i), 1);
@@ -326,51 +356,69 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     if (!rows && landed < issued) hand_over(issued - 1);
   } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
-    // Warp d, of the CTA's own rows: 64 columns, half d >> 2 of score box u = d & 3, which where
-    // u & 1 is the CTA's rank is output unit (rank, u >> 1) too; of the other's rows: 32 columns,
-    // piece d & 3 of output unit (1 - rank, d >> 2).  A row per lane: rows are 17 times 16 bytes
-    // apart, so eight lanes read from eight different pieces of the banks, and the swizzle has
-    // them write so.
-    const int d = warp - kWarpDecode, u = d & 3, h = d >> 2;
-    const bool both = (u & 1) == rank;
-    const int own_unit = 2 * rank + (u >> 1), peer_unit = 2 * (1 - rank) + h;
-    const int peer_box = 2 * h + rank;
+    // Warp d takes 32 columns, piece c = d & 3, of the CTA's own rows in score boxes 2 j and
+    // 2 j + 1, j = d >> 2, of which the one of the CTA's rank's parity is output unit (rank, j)
+    // too; of the other CTA's rows in output unit (1 - rank, j).  A row per lane: rows are 17
+    // times 16 bytes apart, so eight lanes read from eight different pieces of the banks, and
+    // the swizzle has them write so.
+    const int d = warp - kWarpDecode, c = d & 3, j = d >> 2;
+    const int own_unit = 2 * rank + j, peer_unit = 2 * (1 - rank) + j;
     const uint8_t* table = smem + L::kOffTable;
     const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
-    uint8_t* box = smem + L::kOffS + u * kPBox + lane * 128;
+    uint8_t* boxes = smem + L::kOffS + 2 * j * kPBox + lane * 128;
     uint8_t* units = smem + L::kOffV + lane * 128;
-    const uint32_t swz = (lane & 7) << 4;
+    const uint32_t at = (2 * c << 4) ^ ((lane & 7) << 4);
+    // Codes and exponents of piece c of box m.
+    auto codes_at = [&](const uint8_t* raw, int m) { return raw + 64 * m + 16 * c; };
+    auto exps_at = [&](const uint8_t* raw, int m) { return raw + kQ4CodeBytes + 4 * m + c; };
     for (int t = 0; t < T; ++t) {
       const int buf = 4 * (t & 1);   // its first unit
-      if (t > 0) q4_warp_wait(bar(L::EMPTYS + u), (t - 1) & 1, abort_flag);
+      if (t > 0) {
+        q4_warp_wait(bar(L::EMPTYS + 2 * j), (t - 1) & 1, abort_flag);
+        q4_warp_wait(bar(L::EMPTYS + 2 * j + 1), (t - 1) & 1, abort_flag);
+      }
       if (t > 1) q4_warp_wait(bar(L::PVDONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
       tc_fence_after();
       if (given_up()) break;
-      const int other = both ? static_cast<int>(units - box) + (buf + own_unit) * kPBox : 0;
+      const int other = static_cast<int>(units - (boxes + rank * kPBox)) + (buf + own_unit) * kPBox;
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         q4_warp_wait(bar(L::RAWFULL + k), 0, abort_flag);
         const uint8_t* raw = from + k * L::kSlotBytes;
-        q4_decode<2, true>(raw + 64 * u + 32 * h,
-                           *reinterpret_cast<const uint16_t*>(raw + kQ4CodeBytes + 4 * u + 2 * h),
-                           box + k * (L::kSlotRows * 128), 4 * h, swz, table, other);
+        Q4Piece both, box;   // of the box that is a unit too, and of the other
+        both.load(codes_at(raw, 2 * j + rank), exps_at(raw, 2 * j + rank));
+        box.load(codes_at(raw, 2 * j + 1 - rank), exps_at(raw, 2 * j + 1 - rank));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
+        uint8_t* rows = boxes + k * (L::kSlotRows * 128);
+        if (__all_sync(0xffffffffu, both.plain() && box.plain())) {
+          both.store<true>(rows + rank * kPBox, at, other, table);
+          box.store<true>(rows + (1 - rank) * kPBox, at, 0, table);
+        } else {
+          both.store<false>(rows + rank * kPBox, at, other, table);
+          box.store<false>(rows + (1 - rank) * kPBox, at, 0, table);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_cluster(lbar(L::FULLS + u));
-        if (both) arrive_cluster(lbar(L::FULLV + buf + own_unit));
+        arrive_cluster(lbar(L::FULLS + 2 * j));
+        arrive_cluster(lbar(L::FULLS + 2 * j + 1));
+        arrive_cluster(lbar(L::FULLV + buf + own_unit));
       }
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         q4_warp_wait(bar(L::RAWFULL + k), 1, abort_flag);
         const uint8_t* raw = from + k * L::kSlotBytes;
-        q4_decode<1>(raw + 64 * peer_box + 16 * u, raw[kQ4CodeBytes + 4 * peer_box + u],
-                     units + (buf + peer_unit) * kPBox + k * (L::kSlotRows * 128), 2 * u, swz, table);
+        Q4Piece unit;
+        unit.load(codes_at(raw, 2 * j + rank), exps_at(raw, 2 * j + rank));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
+        uint8_t* rows = units + (buf + peer_unit) * kPBox + k * (L::kSlotRows * 128);
+        if (__all_sync(0xffffffffu, unit.plain()))
+          unit.store<true>(rows, at, 0, table);
+        else
+          unit.store<false>(rows, at, 0, table);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -419,9 +467,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           if (given_up()) return false;
           tc_fence_after();
           const uint64_t b = k0 + static_cast<uint64_t>(sb * (L::kKeyBytes >> 4));
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_pair<false>(tmem + 128 + 64 * sb, qk0 + 2 * ks, b + 2 * ks, idesc_k, ks > 0);
+          mma_pair_steps<false, 4, 2, 2>(tmem + 128 + 64 * sb, qk0, b, idesc_k, 0);
         } else {
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
@@ -432,10 +478,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
             for (int part = 0; part < L::kParts; ++part) {
               const uint64_t a = q0 + static_cast<uint64_t>((part * 4 + m) * (kPBox >> 4));
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)   // 32 bytes of K a step
-                mma_pair<true>(tmem + 64 * sb, a + 2 * ks, b + 2 * ks, idesc,
-                               part > 0 || ks > 0 ? 1u : (m > 0 ? 1u : 0u));
+              // 32 bytes of K a step
+              mma_pair_steps<true, 4, 2, 2>(tmem + 64 * sb, a, b, idesc,
+                                            part > 0 ? 1u : (m > 0 ? 1u : 0u));
             }
             commit_pair(bar(L::EMPTYS + m));
           }
@@ -470,11 +515,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
           for (int part = 0; part < L::kParts; ++part) {
             const uint64_t a = p0 + ((part * kPBox + 64 * kh) >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              mma_pair<true>(d, a + 2 * ks, b + ks * (4096 >> 4),
-                             idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
-                             part > 0 || ks > 0 ? 1u : (i > 0 || kh > 0 ? 1u : 0u));
+            mma_pair_steps<true, 2, 2, (4096 >> 4)>(
+                d, a, b, idesc | (part == 1 ? 1u << 7 : 0u),   // the remainder is E5M2
+                part > 0 ? 1u : (i > 0 || kh > 0 ? 1u : 0u));
           }
         }
         commit_pair(bar(L::PVDONE + pb));
