@@ -173,7 +173,7 @@ __device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
 
 // 32 codes of one row and their two blocks' exponents, as loaded, and as E4M3 in the row's
 // 16-byte units at `at` and at ^ 16 of a box of 128-byte rows (the caller has the 128-byte
-// swizzle in `at`); with `other` != 0 the same `other` bytes on.
+// swizzle in `at`).
 struct Q4Piece {
   uint4 w;
   uint32_t e;   // one byte
@@ -185,23 +185,16 @@ struct Q4Piece {
   // e; others are looked up.
   __device__ __forceinline__ bool plain() const { return (e & (e << 1) & 0x88u) == 0; }
   template <bool kPlain>
-  __device__ __forceinline__ void store(uint8_t* row, uint32_t at, int other,
-                                        const uint8_t* table) const {
+  __device__ __forceinline__ void store(uint8_t* row, uint32_t at, const uint8_t* table) const {
     auto magnitudes = [&](uint32_t x) {
       return kPlain ? make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u)
                     : *reinterpret_cast<const uint2*>(table + 8 * x);
     };
     const uint2 m0 = magnitudes(e & 15), m1 = magnitudes(e >> 4);
     const uint2 a = decode8(w.x, m0), b = decode8(w.y, m0);
-    const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4*>(row + at) = o0;
+    *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
     const uint2 x = decode8(w.z, m1), y = decode8(w.w, m1);
-    const uint4 o1 = make_uint4(x.x, x.y, y.x, y.y);
-    *reinterpret_cast<uint4*>(row + (at ^ 16)) = o1;
-    if (other) {
-      *reinterpret_cast<uint4*>(row + other + at) = o0;
-      *reinterpret_cast<uint4*>(row + other + (at ^ 16)) = o1;
-    }
+    *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
   }
 };
 

@@ -447,11 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
           for (int k = 0; k < kEach; ++k)
-            piece[k].template store<true>(row, ((unit0 + 2 * k) << 4) ^ swz, 0, table);
+            piece[k].template store<true>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
         } else {
 #pragma unroll
           for (int k = 0; k < kEach; ++k)
-            piece[k].template store<false>(row, ((unit0 + 2 * k) << 4) ^ swz, 0, table);
+            piece[k].template store<false>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
         }
       }
       fence_proxy_async_smem();

@@ -13,12 +13,16 @@
 //
 // What differs is where the operands come from.  A tile's codes and exponents pass through both
 // CTAs as they are stored, 32 rows at a time, and eight warps turn them into E4M3 boxes of 64
-// rows x 128 columns: of the CTA's own 64 rows four score boxes, two of which are output units as
-// well (decoded once, written twice), of the other CTA's rows the two other output units.  Score
-// boxes are free again when the scores are done, output units, of which there are two tiles',
-// when their product is.  (With a box or unit per warp and one tile of each, 32 x 16384 rows x
-// 128 heads took 193 us, the scores of a tile waiting for one warp's whole box; with all warps
-// on the boxes and then on the units 172, the units waiting for the output product before.)
+// rows x 128 columns.  A tile has four boxes in a CTA.  First they hold the CTA's own 64 rows,
+// for the scores.  The output product wants, at the same place in both CTAs, box 2 jj + h with
+// the rows of half h and the columns of box 2 jj + i in CTA i: where h is the CTA's own half that
+// is what the box holds already, and the other two boxes are decoded again from the other CTA's
+// rows, once the scores are done.  So each value is decoded where it is used, one and a half
+// times in all, and three tiles' boxes fit: the scores of the next tile are decoded while this
+// one's run, its second halves behind the softmax.  (32 x 16384 rows x 128 heads, earlier forms:
+// 193 us with score boxes and output units apart, a tile of each, and a warp for each; 172 with
+// all warps on the one and then the other; 169 with two tiles of units, decoded once and stored
+// twice, where the one tile of score boxes made decoding and the tensor cores take turns.)
 // Of the keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
 // cleaning behind a sequence's end: whatever bits a row holds, its latents are finite, and its
 // scores are not looked at.
@@ -48,21 +52,20 @@ struct Q4Pair {
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffS = kOffQ + kQBytes;         // [4] score boxes
-  static constexpr int kOffV = kOffS + 4 * kPBox;       // [2][row half][O tile] output units
-  static constexpr int kOffK = kOffV + 8 * kPBox;       // [2] keys
+  static constexpr int kTiles = 3;
+  static constexpr int kOffC = kOffQ + kQBytes;         // [3][4] boxes
+  static constexpr int kOffK = kOffC + kTiles * 4 * kPBox;   // [2] keys
   static constexpr int kOffP = kOffK + 2 * kKeyBytes;
   static constexpr int kOffRaw = kOffP + kPBufBytes;
   static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;
   static constexpr int kOffRed = kOffTable + 128;       // [2 kSlices][64] maxima
   static constexpr int kOffSum = kOffRed + 2 * kSlices * kPHeads * 4;       // row sums
   static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
-  // Rows landed / decoded and keys landed (this CTA's); score boxes handed over / free; output
-  // units handed over (free with PVDONE); keys handed over; S, P, O and the query as in
-  // mla_pair.cu.
+  // Rows landed / decoded and keys landed (this CTA's); a tile's boxes decoded for the scores,
+  // for the output, and free; keys handed over; S, P, O and the query as in mla_pair.cu.
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots, KEYFULL = RAWEMPTY + kSlots,
-                       FULLS = KEYFULL + 2, EMPTYS = FULLS + 4, FULLV = EMPTYS + 4,
-                       KREADY = FULLV + 8, SREADY = KREADY + 2,
+                       FULLS = KEYFULL + 2, FULLV = FULLS + kTiles, FREE = FULLV + kTiles,
+                       KREADY = FREE + kTiles, SREADY = KREADY + 2,
                        SFREE = SREADY + 2, PREADY = SFREE + 2, PVDONE = PREADY + 2,
                        QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
@@ -77,7 +80,7 @@ struct Q4Pair {
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kOffRed >= kPHeads * kStageRow, "epilogue staging");
   static_assert(kPBufBytes == kSoftWarps * 32 * 32, "an item's output through P");
-  static_assert(kOffS % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  static_assert(kOffC % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kOffRaw % 16 == 0 && kOffBar % 8 == 0, "alignment");
 };
 
@@ -121,6 +124,11 @@ __device__ __forceinline__ void mma_pair_steps(uint32_t d, uint64_t a, uint64_t 
 #undef MLA_Q4_MORE
 #undef MLA_Q4_ARGS
 }
+
+template <int kN>
+struct Int {
+  static constexpr int value = kN;
+};
 
 // Asks L2 for `bytes` bytes at `src` (16-byte units).
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
@@ -185,11 +193,10 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       mbar_init(bar(L::RAWFULL + i), 1);
       mbar_init(bar(L::RAWEMPTY + i), 8);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(L::FULLS + i), 8);   // four warps of each CTA
-      mbar_init(bar(L::EMPTYS + i), 1);
-      mbar_init(bar(L::FULLV + i), 8);
-      mbar_init(bar(L::FULLV + 4 + i), 8);
+    for (int i = 0; i < L::kTiles; ++i) {
+      mbar_init(bar(L::FULLS + i), 16);   // the decoding warps of both CTAs
+      mbar_init(bar(L::FULLV + i), 16);
+      mbar_init(bar(L::FREE + i), 2);     // one commit per output issuer
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::KEYFULL + i), 1);
@@ -288,60 +295,77 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       if (T > 0) load_query(item0.v);
     }
     const int bytes = rows ? kQ4LatBytes : kQ4KeyBytes, plane = rows ? 0 : kQ4LatBytes;
-    int ahead = T > 0 ? piece_page(item0, 0) : -2;   // the next tile's, looked up early
-    int landed = 0;                                  // tiles whose keys were handed over
-    // Hands the keys of tile t over once they have landed: the even CTA's MMAs read both.
-    auto hand_over = [&](int t) {
-      q4_warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
-      if (lane == 0) arrive_cluster(lbar(L::KREADY + (t & 1)));
-      landed = t + 1;
-    };
-    int issued = 0;
-    for_tiles([&](const TileItem& it, int i, int t) {
-      if (given_up()) return false;
-      int id = ahead, r_next = 0;
-      const int mask = (1 << p.page_shift) - 1;
-      ahead = -2;
-      if (t + 1 < T) {
-        if (i + 1 < it.tiles) {
-          ahead = piece_page(it, i + 1);
-        } else {
-          const TileItem then = item_after(it, t + 1);
-          ahead = piece_page(then, 0);
-          r_next = then.r0 + row0 + lane * piece;
-        }
-      }
+    // Where lane i's piece of tile i of `it` comes from, its page looked up before.
+    const int mask = (1 << p.page_shift) - 1;
+    auto piece_source = [&](int id, int r0) {
       if (id >= p.num_pages) id = -1;
-      if (id == -1) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
-      const int live = __popc(__ballot_sync(0xffffffffu, id != -2));
-      const int r = it.r0 + row0 + lane * piece;
-      const int in_page = (r + i * kTileRows) & mask;
-      const uint8_t* src =
-          id < 0 ? g_q4_pair_zeros
-                 : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
-                       (static_cast<size_t>(plane) << p.page_shift) + in_page * bytes;
-      if (rows) {
-        // The next tile's rows of the CTA's half are asked for ahead: two slots are not enough to
-        // cover the way from HBM.
-        const int per = L::kSlotRows / piece;
-        if (ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank) {
-          const int rn = (i + 1 < it.tiles ? r + (i + 1) * kTileRows : r_next) & mask;
-          prefetch_l2(pool + (static_cast<size_t>(ahead) << p.page_shift) * kQ4RowBytes + rn * bytes,
-                      piece * bytes);
-        }
-        // The CTA's own half first: its scores start a tile.
+      const int r = (r0 + row0 + lane * piece) & mask;
+      return id < 0 ? g_q4_pair_zeros
+                    : pool + (static_cast<size_t>(id) << p.page_shift) * kQ4RowBytes +
+                          (static_cast<size_t>(plane) << p.page_shift) + r * bytes;
+    };
+    auto live_of = [&](int id) { return __popc(__ballot_sync(0xffffffffu, id != -2)); };
+    // The next tile's pages and first row, looked up early.
+    int ahead = T > 0 ? piece_page(item0, 0) : -2, ahead_r0 = item0.r0;
+    auto look_ahead = [&](const TileItem& it, int i, int t) {
+      if (ahead == -1 || ahead >= p.num_pages) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+      ahead = -2;
+      if (t + 1 >= T) return;
+      const bool more = i + 1 < it.tiles;
+      const TileItem then = more ? it : item_after(it, t + 1);
+      ahead = piece_page(then, more ? i + 1 : 0);
+      ahead_r0 = then.r0 + (more ? i + 1 : 0) * kTileRows;
+    };
+    if (rows) {
+      // In the order in which they are decoded: the CTA's own half of a tile, then the other
+      // half of the tile before.
+      const int per = L::kSlotRows / piece;
+      int n = 0;   // slots issued
+      auto issue_half = [&](const uint8_t* src, int live, int half) {   // false: given up
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const int at = k & 1, n = 4 * t + k;
-          const int from = (at + 2 * (k < 2 ? rank : 1 - rank)) * per;   // of the tile's pieces
+        for (int k = 0; k < 2; ++k, ++n) {
+          const int slot = n & 1, from = (2 * half + k) * per;
           if (n >= L::kSlots) {
-            q4_warp_wait(bar(L::RAWEMPTY + at), ((n >> 1) - 1) & 1, abort_flag);
+            q4_warp_wait(bar(L::RAWEMPTY + slot), ((n >> 1) - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
           copy_pieces(src, from, from + per, live, piece * bytes,
-                      sbase + L::kOffRaw + at * L::kSlotBytes, bar(L::RAWFULL + at));
+                      sbase + L::kOffRaw + slot * L::kSlotBytes, bar(L::RAWFULL + slot));
         }
-      } else {
+        return true;
+      };
+      const uint8_t* last = nullptr;   // the tile before's sources
+      int last_live = 0;
+      bool ok = true;
+      for_tiles([&](const TileItem& it, int i, int t) {
+        if (given_up()) return ok = false;
+        const uint8_t* src = piece_source(ahead, ahead_r0);
+        const int live = live_of(ahead);
+        look_ahead(it, i, t);
+        // Two slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
+        // other half has come with the other CTA's by the time it is copied.)
+        if (ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
+          prefetch_l2(piece_source(ahead, ahead_r0), piece * bytes);
+        if (!issue_half(src, live, rank)) return ok = false;
+        if (t > 0 && !issue_half(last, last_live, 1 - rank)) return ok = false;
+        last = src;
+        last_live = live;
+        return true;
+      });
+      if (ok && T > 0) issue_half(last, last_live, 1 - rank);
+    } else {
+      int issued = 0, landed = 0;   // tiles whose keys are on their way, and handed over
+      // Hands the keys of tile t over once they have landed: the even CTA's MMAs read both.
+      auto hand_over = [&](int t) {
+        q4_warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
+        if (lane == 0) arrive_cluster(lbar(L::KREADY + (t & 1)));
+        landed = t + 1;
+      };
+      for_tiles([&](const TileItem& it, int i, int t) {
+        if (given_up()) return false;
+        const uint8_t* src = piece_source(ahead, ahead_r0);
+        const int live = live_of(ahead);
+        look_ahead(it, i, t);
         if (t >= 2) {   // the scores of tile t - 2 have read this buffer
           q4_warp_wait(bar(L::SREADY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
           if (given_up()) return false;
@@ -350,79 +374,76 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
                     sbase + L::kOffK + (t & 1) * L::kKeyBytes, bar(L::KEYFULL + (t & 1)));
         issued = t + 1;
         if (t > 0) hand_over(t - 1);
-      }
-      return true;
-    });
-    if (!rows && landed < issued) hand_over(issued - 1);
+        return true;
+      });
+      if (landed < issued) hand_over(issued - 1);
+    }
   } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
-    // Warp d takes 32 columns, piece c = d & 3, of the CTA's own rows in score boxes 2 j and
-    // 2 j + 1, j = d >> 2, of which the one of the CTA's rank's parity is output unit (rank, j)
-    // too; of the other CTA's rows in output unit (1 - rank, j).  A row per lane: rows are 17
-    // times 16 bytes apart, so eight lanes read from eight different pieces of the banks, and
-    // the swizzle has them write so.
+    // Warp d takes 32 columns, piece c = d & 3: of the CTA's own rows in boxes 2 j and 2 j + 1,
+    // j = d >> 2, then, one tile behind, of the other CTA's rows in box 2 j + 1 - rank, the
+    // columns of box 2 j + rank.  A row per lane: rows are 17 times 16 bytes apart, so eight
+    // lanes read from eight different pieces of the banks, and the swizzle has them write so.
     const int d = warp - kWarpDecode, c = d & 3, j = d >> 2;
-    const int own_unit = 2 * rank + j, peer_unit = 2 * (1 - rank) + j;
     const uint8_t* table = smem + L::kOffTable;
     const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
-    uint8_t* boxes = smem + L::kOffS + 2 * j * kPBox + lane * 128;
-    uint8_t* units = smem + L::kOffV + lane * 128;
+    uint8_t* boxes = smem + L::kOffC + 2 * j * kPBox + lane * 128;
     const uint32_t at = (2 * c << 4) ^ ((lane & 7) << 4);
-    // Codes and exponents of piece c of box m.
-    auto codes_at = [&](const uint8_t* raw, int m) { return raw + 64 * m + 16 * c; };
-    auto exps_at = [&](const uint8_t* raw, int m) { return raw + kQ4CodeBytes + 4 * m + c; };
-    for (int t = 0; t < T; ++t) {
-      const int buf = 4 * (t & 1);   // its first unit
-      if (t > 0) {
-        q4_warp_wait(bar(L::EMPTYS + 2 * j), (t - 1) & 1, abort_flag);
-        q4_warp_wait(bar(L::EMPTYS + 2 * j + 1), (t - 1) & 1, abort_flag);
+    int n = 0;   // slots taken
+    // The next slot's piece c of boxes m .. m + kBoxes - 1, into boxes from `to` on.
+    auto decode_slot = [&](auto boxes_of, int m, uint8_t* to) {
+      constexpr int kBoxes = decltype(boxes_of)::value;
+      const int slot = n & 1;
+      q4_warp_wait(bar(L::RAWFULL + slot), (n >> 1) & 1, abort_flag);
+      ++n;
+      const uint8_t* raw = from + slot * L::kSlotBytes;
+      Q4Piece piece[kBoxes];
+      bool plain = true;
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) {
+        piece[i].load(raw + 64 * (m + i) + 16 * c, raw + kQ4CodeBytes + 4 * (m + i) + c);
+        plain = plain && piece[i].plain();
       }
-      if (t > 1) q4_warp_wait(bar(L::PVDONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
-      tc_fence_after();
-      if (given_up()) break;
-      const int other = static_cast<int>(units - (boxes + rank * kPBox)) + (buf + own_unit) * kPBox;
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        q4_warp_wait(bar(L::RAWFULL + k), 0, abort_flag);
-        const uint8_t* raw = from + k * L::kSlotBytes;
-        Q4Piece both, box;   // of the box that is a unit too, and of the other
-        both.load(codes_at(raw, 2 * j + rank), exps_at(raw, 2 * j + rank));
-        box.load(codes_at(raw, 2 * j + 1 - rank), exps_at(raw, 2 * j + 1 - rank));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
-        uint8_t* rows = boxes + k * (L::kSlotRows * 128);
-        if (__all_sync(0xffffffffu, both.plain() && box.plain())) {
-          both.store<true>(rows + rank * kPBox, at, other, table);
-          box.store<true>(rows + (1 - rank) * kPBox, at, 0, table);
-        } else {
-          both.store<false>(rows + rank * kPBox, at, other, table);
-          box.store<false>(rows + (1 - rank) * kPBox, at, 0, table);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+      if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) piece[i].template store<true>(to + i * kPBox, at, table);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) piece[i].template store<false>(to + i * kPBox, at, table);
+      }
+    };
+    auto hand_over = [&](int full) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lbar(full));
+    };
+    for (int t = 0; t <= T; ++t) {
+      const int buf = t % L::kTiles;
+      if (t < T) {   // the scores' boxes of tile t
+        if (t >= L::kTiles) {
+          q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
+          tc_fence_after();
         }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        arrive_cluster(lbar(L::FULLS + 2 * j));
-        arrive_cluster(lbar(L::FULLS + 2 * j + 1));
-        arrive_cluster(lbar(L::FULLV + buf + own_unit));
-      }
+        if (given_up()) break;
+        uint8_t* to = boxes + buf * 4 * kPBox;
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        q4_warp_wait(bar(L::RAWFULL + k), 1, abort_flag);
-        const uint8_t* raw = from + k * L::kSlotBytes;
-        Q4Piece unit;
-        unit.load(codes_at(raw, 2 * j + rank), exps_at(raw, 2 * j + rank));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
-        uint8_t* rows = units + (buf + peer_unit) * kPBox + k * (L::kSlotRows * 128);
-        if (__all_sync(0xffffffffu, unit.plain()))
-          unit.store<true>(rows, at, 0, table);
-        else
-          unit.store<false>(rows, at, 0, table);
+        for (int k = 0; k < 2; ++k)
+          decode_slot(Int<2>{}, 2 * j, to + k * (L::kSlotRows * 128));
+        hand_over(L::FULLS + buf);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(lbar(L::FULLV + buf + peer_unit));
+      if (t > 0) {   // the output's of tile t - 1, once its scores are done
+        const int last = (t - 1) % L::kTiles;
+        q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+        tc_fence_after();
+        if (given_up()) break;
+        uint8_t* to = boxes + (last * 4 + 1 - rank) * kPBox;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k)
+          decode_slot(Int<1>{}, 2 * j + rank, to + k * (L::kSlotRows * 128));
+        hand_over(L::FULLV + last);
+      }
     }
   } else if (kShare && warp == kWarpQuery) {
     // ------------------------------------------------------------ the later items' queries
@@ -444,7 +465,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       constexpr uint32_t idesc = (1u << 4) | (128u >> 3 << 17) | (128u >> 4 << 24);   // E4M3
       constexpr uint32_t idesc_k = idesc | (1u << 7) | (1u << 10);                    // bf16
       const uint64_t q0 = umma_desc_sw128(sbase + L::kOffQ, 16, 1024);
-      const uint64_t s0 = umma_desc_sw128(sbase + L::kOffS, 16, 1024);
+      const uint64_t c0 = umma_desc_sw128(sbase + L::kOffC, 16, 1024);
       const uint64_t qk0 = umma_desc_sw128(sbase + L::kOffQ + L::kQKeys, 16, 1024);
       const uint64_t k0 = umma_desc_sw128(sbase + L::kOffK, 16, 1024);
       int n = 0;   // items begun
@@ -469,12 +490,13 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           const uint64_t b = k0 + static_cast<uint64_t>(sb * (L::kKeyBytes >> 4));
           mma_pair_steps<false, 4, 2, 2>(tmem + 128 + 64 * sb, qk0, b, idesc_k, 0);
         } else {
+          const int buf = t % L::kTiles;
+          q4_warp_wait(bar(L::FULLS + buf), (t / L::kTiles) & 1, abort_flag);
+          if (given_up()) return false;
+          tc_fence_after();
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
-            q4_warp_wait(bar(L::FULLS + m), t & 1, abort_flag);
-            if (given_up()) return false;
-            tc_fence_after();
-            const uint64_t b = s0 + static_cast<uint64_t>(m * (kPBox >> 4));
+            const uint64_t b = c0 + static_cast<uint64_t>((4 * buf + m) * (kPBox >> 4));
 #pragma unroll
             for (int part = 0; part < L::kParts; ++part) {
               const uint64_t a = q0 + static_cast<uint64_t>((part * 4 + m) * (kPBox >> 4));
@@ -482,7 +504,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
               mma_pair_steps<true, 4, 2, 2>(tmem + 64 * sb, a, b, idesc,
                                             part > 0 ? 1u : (m > 0 ? 1u : 0u));
             }
-            commit_pair(bar(L::EMPTYS + m));
           }
         }
         commit_pair(bar(L::SREADY + sb));
@@ -498,19 +519,18 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       constexpr uint32_t idesc =
           (1u << 4) | (1u << 16) | (256u >> 3 << 17) | (128u >> 4 << 24);
       const uint64_t p0 = umma_desc_sw128(sbase + L::kOffP, 16, 1024);
-      const uint64_t v0 = umma_desc_sw128(sbase + L::kOffV, kPBox, 1024);   // rows (K) by eights
+      const uint64_t v0 = umma_desc_sw128(sbase + L::kOffC, kPBox, 1024);   // rows (K) by eights
       const uint32_t d = tmem + L::kOCol + 128 * jj;
       for_tiles([&](const TileItem&, int i, int t) {
         const int pb = t & 1;
         q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
+        const int buf = t % L::kTiles;
+        q4_warp_wait(bar(L::FULLV + buf), (t / L::kTiles) & 1, abort_flag);
         if (given_up()) return false;
+        tc_fence_after();
 #pragma unroll 1
         for (int kh = 0; kh < 2; ++kh) {
-          const int u = 4 * pb + 2 * kh + jj;
-          q4_warp_wait(bar(L::FULLV + u), (t >> 1) & 1, abort_flag);
-          if (given_up()) return false;
-          tc_fence_after();
-          const uint64_t b = v0 + static_cast<uint64_t>(u * (kPBox >> 4));
+          const uint64_t b = v0 + static_cast<uint64_t>((4 * buf + 2 * jj + kh) * (kPBox >> 4));
           // 64 rows: two steps of 32 (4 KB; 32 bytes of each part's row, the half at byte 64 kh)
 #pragma unroll
           for (int part = 0; part < L::kParts; ++part) {
@@ -521,6 +541,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           }
         }
         commit_pair(bar(L::PVDONE + pb));
+        commit_pair(bar(L::FREE + buf));
         return true;
       });
     }
