@@ -47,15 +47,16 @@ struct Q4Pair {
   static constexpr int kParts = 2;
   static constexpr int kQKeys = kParts * 4 * kPBox;     // offset of the query's key part
   static constexpr int kQBytes = kQKeys + kPBox;
-  // Rows arrive in two slots of 32: the CTA's own half of a tile, then the other half.
-  static constexpr int kSlotRows = 32, kSlots = 2;
+  // Rows arrive in slots of 32: the CTA's own half of a tile, then the other half of the one
+  // before.  (With two slots and two tiles' keys 145 us for 32 x 16384 rows x 128 heads.)
+  static constexpr int kSlotRows = 32, kSlots = 3;
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
   static constexpr int kOffQ = 0;
   static constexpr int kTiles = 3;
   static constexpr int kOffC = kOffQ + kQBytes;         // [3][4] boxes
-  static constexpr int kOffK = kOffC + kTiles * 4 * kPBox;   // [2] keys
-  static constexpr int kOffP = kOffK + 2 * kKeyBytes;
+  static constexpr int kOffK = kOffC + kTiles * 4 * kPBox;   // keys
+  static constexpr int kOffP = kOffK + kKeyBytes;
   static constexpr int kOffRaw = kOffP + kPBufBytes;
   static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;
   static constexpr int kOffRed = kOffTable + 128;       // [2 kSlices][64] maxima
@@ -64,8 +65,8 @@ struct Q4Pair {
   // Rows landed / decoded and keys landed (this CTA's); a tile's boxes decoded for the scores,
   // for the output, and free; keys handed over; S, P, O and the query as in mla_pair.cu.
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots, KEYFULL = RAWEMPTY + kSlots,
-                       FULLS = KEYFULL + 2, FULLV = FULLS + kTiles, FREE = FULLV + kTiles,
-                       KREADY = FREE + kTiles, SREADY = KREADY + 2,
+                       FULLS = KEYFULL + 1, FULLV = FULLS + kTiles, FREE = FULLV + kTiles,
+                       KREADY = FREE + kTiles, SREADY = KREADY + 1,
                        SFREE = SREADY + 2, PREADY = SFREE + 2, PVDONE = PREADY + 2,
                        QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
@@ -199,13 +200,13 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       mbar_init(bar(L::FREE + i), 2);     // one commit per output issuer
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(L::KEYFULL + i), 1);
-      mbar_init(bar(L::KREADY + i), 2);                 // both CTAs' keys
       mbar_init(bar(L::SREADY + i), 2);                 // one commit per issuer
       mbar_init(bar(L::SFREE + i), 2 * L::kSoftWarps);  // both CTAs' softmax warps
       mbar_init(bar(L::PREADY + i), 2 * L::kSoftWarps);
       mbar_init(bar(L::PVDONE + i), 2);
     }
+    mbar_init(bar(L::KEYFULL), 1);
+    mbar_init(bar(L::KREADY), 2);   // both CTAs' keys
     mbar_init(bar(L::QFULL), 1);
     mbar_init(bar(L::QFREE), 2);   // one commit per score issuer
     *abort_flag = 0;
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       auto issue_half = [&](const uint8_t* src, int live, int half) {   // false: given up
 #pragma unroll 1
         for (int k = 0; k < 2; ++k, ++n) {
-          const int slot = n & 1, from = (2 * half + k) * per;
+          const int slot = n % L::kSlots, from = (2 * half + k) * per;
           if (n >= L::kSlots) {
-            q4_warp_wait(bar(L::RAWEMPTY + slot), ((n >> 1) - 1) & 1, abort_flag);
+            q4_warp_wait(bar(L::RAWEMPTY + slot), (n / L::kSlots - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
           copy_pieces(src, from, from + per, live, piece * bytes,
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         const uint8_t* src = piece_source(ahead, ahead_r0);
         const int live = live_of(ahead);
         look_ahead(it, i, t);
-        // Two slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
+        // The slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
         // other half has come with the other CTA's by the time it is copied.)
         if (ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
           prefetch_l2(piece_source(ahead, ahead_r0), piece * bytes);
@@ -354,29 +355,21 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       });
       if (ok && T > 0) issue_half(last, last_live, 1 - rank);
     } else {
-      int issued = 0, landed = 0;   // tiles whose keys are on their way, and handed over
-      // Hands the keys of tile t over once they have landed: the even CTA's MMAs read both.
-      auto hand_over = [&](int t) {
-        q4_warp_wait(bar(L::KEYFULL + (t & 1)), (t >> 1) & 1, abort_flag);
-        if (lane == 0) arrive_cluster(lbar(L::KREADY + (t & 1)));
-        landed = t + 1;
-      };
       for_tiles([&](const TileItem& it, int i, int t) {
         if (given_up()) return false;
         const uint8_t* src = piece_source(ahead, ahead_r0);
         const int live = live_of(ahead);
         look_ahead(it, i, t);
-        if (t >= 2) {   // the scores of tile t - 2 have read this buffer
-          q4_warp_wait(bar(L::SREADY + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
+        if (t > 0) {   // the scores of the tile before have read them
+          q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
           if (given_up()) return false;
         }
-        copy_pieces(src, 0, 64 / piece, live, piece * bytes,
-                    sbase + L::kOffK + (t & 1) * L::kKeyBytes, bar(L::KEYFULL + (t & 1)));
-        issued = t + 1;
-        if (t > 0) hand_over(t - 1);
+        copy_pieces(src, 0, 64 / piece, live, piece * bytes, sbase + L::kOffK, bar(L::KEYFULL));
+        // Handed over once they have landed: the even CTA's MMAs read both CTAs'.
+        q4_warp_wait(bar(L::KEYFULL), t & 1, abort_flag);
+        if (lane == 0) arrive_cluster(lbar(L::KREADY));
         return true;
       });
-      if (landed < issued) hand_over(issued - 1);
     }
   } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
@@ -393,8 +386,8 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     // The next slot's piece c of boxes m .. m + kBoxes - 1, into boxes from `to` on.
     auto decode_slot = [&](auto boxes_of, int m, uint8_t* to) {
       constexpr int kBoxes = decltype(boxes_of)::value;
-      const int slot = n & 1;
-      q4_warp_wait(bar(L::RAWFULL + slot), (n >> 1) & 1, abort_flag);
+      const int slot = n % L::kSlots;
+      q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
       ++n;
       const uint8_t* raw = from + slot * L::kSlotBytes;
       Q4Piece piece[kBoxes];
@@ -484,11 +477,10 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         if (t >= 2) q4_warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
         if (given_up()) return false;
         if (keys) {
-          q4_warp_wait(bar(L::KREADY + sb), (t >> 1) & 1, abort_flag);
+          q4_warp_wait(bar(L::KREADY), t & 1, abort_flag);
           if (given_up()) return false;
           tc_fence_after();
-          const uint64_t b = k0 + static_cast<uint64_t>(sb * (L::kKeyBytes >> 4));
-          mma_pair_steps<false, 4, 2, 2>(tmem + 128 + 64 * sb, qk0, b, idesc_k, 0);
+          mma_pair_steps<false, 4, 2, 2>(tmem + 128 + 64 * sb, qk0, k0, idesc_k, 0);
         } else {
           const int buf = t % L::kTiles;
           q4_warp_wait(bar(L::FULLS + buf), (t / L::kTiles) & 1, abort_flag);
