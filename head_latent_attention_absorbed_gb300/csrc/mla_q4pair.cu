@@ -29,9 +29,10 @@
 //
 // Tensor memory per CTA as in mla_pair.cu: S0 and S1, two buffers of 64 columns each, and O.
 //
-// Warps (1024 threads): 0-15 softmax and epilogue; 16 copies of rows; 17 keys and the first
-// query; 18 score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue
-// for the pair); 22 the later items' queries; 24-31 codes to E4M3.
+// Warps (1024 threads): 0-15 softmax and epilogue; 16, 22 and 23 copies of rows, a slot each (one
+// warp took 4200 cycles for a tile's four copies and what leads to them); 17 keys and queries; 18
+// score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue for the pair);
+// 24-31 codes to E4M3.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
   auto bar = [&](int i) { return bars + 8 * i; };
   auto lbar = [&](int i) { return lead + 8 * i; };
   constexpr int kWarpRows = L::kSoftWarps, kWarpKeys = kWarpRows + 1, kWarpScore = kWarpRows + 2,
-                kWarpOut = kWarpRows + 4, kWarpQuery = kWarpRows + 6, kWarpDecode = kWarpRows + 8;
+                kWarpOut = kWarpRows + 4, kWarpRows2 = kWarpRows + 6, kWarpDecode = kWarpRows + 8;
+  static_assert(L::kSlots == 3, "a warp for each slot of rows");
 
   if (tid == L::kSoft) {
     for (int i = 0; i < L::kSlots; ++i) {
@@ -264,10 +266,10 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
   };
   auto given_up = [&] { return __any_sync(0xffffffffu, *abort_flag) != 0; };
 
-  if (warp == kWarpRows || warp == kWarpKeys) {
+  if (warp == kWarpRows || warp == kWarpKeys || warp == kWarpRows2 || warp == kWarpRows2 + 1) {
     // ------------------------------------------------------------ rows, keys
     // Pieces of one page each: of a slot's 32 rows, or of the CTA's 64 keys.
-    const bool rows = warp == kWarpRows;
+    const bool rows = warp != kWarpKeys;
     const uint8_t* pool = static_cast<const uint8_t*>(p.cache);
     const uint64_t pol = l2_evict_first_policy();
     const int piece = min(1 << p.page_shift, rows ? L::kSlotRows : 64);
@@ -320,41 +322,47 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     if (rows) {
       // In the order in which they are decoded: the CTA's own half of a tile, then the other
       // half of the tile before.
-      const int per = L::kSlotRows / piece;
-      int n = 0;   // slots issued
+      const int per = L::kSlotRows / piece, slot = warp == kWarpRows ? 0 : warp - kWarpRows2 + 1;
+      int next = slot, used = 0;   // halves' 32 rows until this warp's next; times its slot was used
       auto issue_half = [&](const uint8_t* src, int live, int half) {   // false: given up
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k, ++n) {
-          const int slot = n % L::kSlots, from = (2 * half + k) * per;
-          if (n >= L::kSlots) {
-            q4_warp_wait(bar(L::RAWEMPTY + slot), (n / L::kSlots - 1) & 1, abort_flag);
+        for (int k = 0; k < 2; ++k) {
+          if (next-- > 0) continue;
+          next = L::kSlots - 1;
+          const int from = (2 * half + k) * per;
+          if (used > 0) {
+            q4_warp_wait(bar(L::RAWEMPTY + slot), (used - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
+          ++used;
           copy_pieces(src, from, from + per, live, piece * bytes,
                       sbase + L::kOffRaw + slot * L::kSlotBytes, bar(L::RAWFULL + slot));
         }
         return true;
       };
-      const uint8_t* last = nullptr;   // the tile before's sources
+      // A tile's sources, the one before's and the next one's.
+      const uint8_t *src = piece_source(ahead, ahead_r0), *last = nullptr;
       int last_live = 0;
       bool ok = true;
       for_tiles([&](const TileItem& it, int i, int t) {
         if (given_up()) return ok = false;
-        const uint8_t* src = piece_source(ahead, ahead_r0);
         const int live = live_of(ahead);
         look_ahead(it, i, t);
+        const uint8_t* then = piece_source(ahead, ahead_r0);
         // The slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
         // other half has come with the other CTA's by the time it is copied.)
-        if (ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
-          prefetch_l2(piece_source(ahead, ahead_r0), piece * bytes);
+        if (slot == 0 && ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
+          prefetch_l2(then, piece * bytes);
         if (!issue_half(src, live, rank)) return ok = false;
         if (t > 0 && !issue_half(last, last_live, 1 - rank)) return ok = false;
         last = src;
         last_live = live;
+        src = then;
         return true;
       });
       if (ok && T > 0) issue_half(last, last_live, 1 - rank);
     } else {
+      int queries = 0;   // later items' queries fetched
       for_tiles([&](const TileItem& it, int i, int t) {
         if (given_up()) return false;
         const uint8_t* src = piece_source(ahead, ahead_r0);
@@ -365,6 +373,14 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           if (given_up()) return false;
         }
         copy_pieces(src, 0, 64 / piece, live, piece * bytes, sbase + L::kOffK, bar(L::KEYFULL));
+        if (kShare && i == 0 && t > 0) {
+          // A later item's query, once the scores of the item before are done, which read the one
+          // that it replaces.
+          q4_warp_wait(bar(L::QFREE), queries & 1, abort_flag);
+          if (given_up()) return false;
+          ++queries;
+          load_query(it.v);
+        }
         // Handed over once they have landed: the even CTA's MMAs read both CTAs'.
         q4_warp_wait(bar(L::KEYFULL), t & 1, abort_flag);
         if (lane == 0) arrive_cluster(lbar(L::KREADY));
@@ -437,17 +453,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           decode_slot(Int<1>{}, 2 * j + rank, to + k * (L::kSlotRows * 128));
         hand_over(L::FULLV + last);
       }
-    }
-  } else if (kShare && warp == kWarpQuery) {
-    // ------------------------------------------------------------ the later items' queries
-    // Each once the scores of the item before are done, which read the query it replaces.
-    TileItem it = item0;
-    for (int t = it.tiles, n = 0; 0 < t && t < T; t += it.tiles, ++n) {
-      it = item_after(it, t);
-      q4_warp_wait(bar(L::QFREE), n & 1, abort_flag);
-      if (given_up()) break;
-      pdl_wait();
-      load_query(it.v);
     }
   } else if (warp == kWarpScore || warp == kWarpScore + 1) {
     // ------------------------------------------------------------ score MMAs (even CTA)
