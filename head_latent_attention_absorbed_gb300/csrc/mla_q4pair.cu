@@ -399,29 +399,38 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     uint8_t* boxes = smem + L::kOffC + 2 * j * kPBox + lane * 128;
     const uint32_t at = (2 * c << 4) ^ ((lane & 7) << 4);
     int n = 0;   // slots taken
-    // The next slot's piece c of boxes m .. m + kBoxes - 1, into boxes from `to` on.
-    auto decode_slot = [&](auto boxes_of, int m, uint8_t* to) {
+    // The next two slots' (a half's 64 rows) piece c of boxes m .. m + kBoxes - 1, into boxes from
+    // `to` on: all loaded, and the slots given back, before the first is stored.
+    auto decode_half = [&](auto boxes_of, int m, uint8_t* to) {
       constexpr int kBoxes = decltype(boxes_of)::value;
-      const int slot = n % L::kSlots;
-      q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
-      ++n;
-      const uint8_t* raw = from + slot * L::kSlotBytes;
-      Q4Piece piece[kBoxes];
+      Q4Piece piece[2][kBoxes];
       bool plain = true;
 #pragma unroll
-      for (int i = 0; i < kBoxes; ++i) {
-        piece[i].load(raw + 64 * (m + i) + 16 * c, raw + kQ4CodeBytes + 4 * (m + i) + c);
-        plain = plain && piece[i].plain();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
-      if (__all_sync(0xffffffffu, plain)) {
+      for (int k = 0; k < 2; ++k) {
+        const int slot = n % L::kSlots;
+        q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
+        ++n;
+        const uint8_t* raw = from + slot * L::kSlotBytes;
 #pragma unroll
-        for (int i = 0; i < kBoxes; ++i) piece[i].template store<true>(to + i * kPBox, at, table);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i) piece[i].template store<false>(to + i * kPBox, at, table);
+        for (int i = 0; i < kBoxes; ++i) {
+          piece[k][i].load(raw + 64 * (m + i) + 16 * c, raw + kQ4CodeBytes + 4 * (m + i) + c);
+          plain = plain && piece[k][i].plain();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
       }
+      auto store = [&](auto is_plain) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i)
+            piece[k][i].template store<decltype(is_plain)::value != 0>(
+                to + i * kPBox + k * (L::kSlotRows * 128), at, table);
+      };
+      if (__all_sync(0xffffffffu, plain))
+        store(Int<1>{});
+      else
+        store(Int<0>{});
     };
     auto hand_over = [&](int full) {
       fence_proxy_async_smem();
@@ -436,10 +445,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           tc_fence_after();
         }
         if (given_up()) break;
-        uint8_t* to = boxes + buf * 4 * kPBox;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k)
-          decode_slot(Int<2>{}, 2 * j, to + k * (L::kSlotRows * 128));
+        decode_half(Int<2>{}, 2 * j, boxes + buf * 4 * kPBox);
         hand_over(L::FULLS + buf);
       }
       if (t > 0) {   // the output's of tile t - 1, once its scores are done
@@ -447,10 +453,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
         tc_fence_after();
         if (given_up()) break;
-        uint8_t* to = boxes + (last * 4 + 1 - rank) * kPBox;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k)
-          decode_slot(Int<1>{}, 2 * j + rank, to + k * (L::kSlotRows * 128));
+        decode_half(Int<1>{}, 2 * j + rank, boxes + (last * 4 + 1 - rank) * kPBox);
         hand_over(L::FULLV + last);
       }
     }
