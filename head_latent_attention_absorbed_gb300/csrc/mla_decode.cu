@@ -2086,21 +2086,25 @@ struct PlanOpts {
 // 4096 rows, 16 query rows 13.7 / 15.0, 32 17.7 / 15.7, 48 26.3 / 16.2, 64 24.5 / 17.1; 4 x
 // 65536, 16 rows 58 / 61, 32 68 / 65, 64 105 / 68; 64 sequences of 512 to 8192, 32 rows
 // 99 / 76, 128 268 / 89.  E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48 22.9 / 17.1; 4 x 65536,
-// 32 rows 61 / 53, 48 88 / 56.
-constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48, kPairMinFp4 = 32;
+// 32 rows 61 / 53, 48 88 / 56.  4-bit, 8 x 4096, 32 rows 16.6 / 19.6, 64 25.9 / 20.7; 64
+// sequences of 512 to 8192, 32 rows 75 / 84, 128 264 / 102.
+constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48, kPairMinFp4 = 48;
 // Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
 // 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
 // full, 256 x 2048 75 / 73, 64 x 4096 40.8 / 40.9, 32 x 4096 (6.7) 24.6 / 25.4, 16 x 4096
-// (3.4) 16.1 / 18.6.
+// (3.4) 16.1 / 18.6.  4-bit: 512 to 8192 rows, 64 sequences 53 / 43, 16 23.3 / 19.3; all full,
+// 256 x 2048 74 / 74, 64 x 4096 40.0 / 40.6, 32 x 4096 24.6 / 25.9, 16 x 2048 12.9 / 14.9.
 constexpr int kShareMinTiles = 5;
 // The same for SM pairs: tiles per pair (bf16, E4M3), and sequences per pair up to which
 // (more are balanced as they are, with one chunk each and no combine).  64 heads, chunks /
 // shares: bf16, 512 to 8192 rows, 16 sequences (13.5 tiles) 34.1 / 29.1, 76 114 / 93, 152
 // 204 / 166, 200 245 / 214, 256 of 100 to 2048 95 / 106; 512 to 4096, 16 (6.7) 22.6 / 23.9,
 // 24 (10.1) 27.6 / 28.0; all full, 16 x 8192 40.7 / 44.4, 76 x 8192 127 / 136; E4M3, 32 of
-// 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82.
-constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairSets = 3;
+// 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82; 4-bit, 16 of
+// 512 to 8192 (13.5) 42.0 / 34.4, 32 x 2048 x 128 heads (6.7) 33.2 / 39.6.
+constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairTilesFp4 = 13,
+              kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {
   return o.paged && o.io == MLA_BF16 && d->dtype != MLA_F32 && g_split_parts.load() != 2 &&
          d->heads * o.q_len >= (d->dtype == MLA_BF16       ? kPairMinBf16
@@ -2291,7 +2295,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
   }
   const bool np_one_wave = per_split * np_splits <= slots;
   const int form = g_split_form.load();
-  // Equal shares of a paged call's tiles (E4M3, and SM pairs): room for twice the partials
+  // Equal shares of a paged call's tiles (E4M3, 4-bit, and SM pairs): room for twice the partials
   // that full sequences would need, so that shares may shrink with the lengths.
   const long long sets = pairs ? d->batch / opts.q_len : d->batch;
   const long long ctas = pairs ? 2ll * pair_groups(d->heads * opts.q_len) : groups;
@@ -2302,7 +2306,9 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
     const long long each = (sets * seq + runs - 1) / runs, half = (each + 1) / 2;
     const bool pays =
         !pairs ? each >= kShareMinTiles
-               : each >= (d->dtype == MLA_BF16 ? kSharePairTilesBf16 : kSharePairTilesFp8) &&
+               : each >= (d->dtype == MLA_BF16       ? kSharePairTilesBf16
+                         : d->dtype == MLA_FP8_E4M3 ? kSharePairTilesFp8
+                                                    : kSharePairTilesFp4) &&
                      sets <= kSharePairSets * runs;
     if (sets * seq < (1ll << 30) && (form == 1 || pays))
       return {np_chunk, static_cast<int>((seq + half - 1) / half + 1), false, true};

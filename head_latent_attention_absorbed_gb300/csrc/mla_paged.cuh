@@ -141,9 +141,13 @@ __device__ __forceinline__ void store_pair(__nv_fp8_storage_t* dst, float x, flo
       __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The turns of each pair per position (see append_paged_kernel).
-inline RopeTurns rope_turns(double rope_base) {
-  RopeTurns turns;
+// The turns of each pair per position (see append_paged_kernel); a thread keeps the last base's,
+// whose powers take longer than the rest of a call.
+inline const RopeTurns& rope_turns(double rope_base) {
+  thread_local double base = 0.0;
+  thread_local RopeTurns turns;
+  if (base == rope_base) return turns;
+  base = rope_base;
   for (int i = 0; i < kDr / 2; ++i) {
     const double t = pow(rope_base, -2.0 * i / kDr) / 6.283185307179586476925;
     // the fraction of a turn per position; a base below 1 has whole turns to drop

@@ -825,7 +825,7 @@ extern "C" mla_status mla_cache_append_paged(const mla_dims* dims, const mla_pag
   if (dims->dtype == MLA_FP4_E2M1)
     return append_q4(who, paging, num_rows, row_dtype == MLA_F32, rows, positions, slots, rope_base,
                      cache, dev_status, static_cast<cudaStream_t>(stream));
-  const RopeTurns turns = rope_turns(rope_base);
+  const RopeTurns& turns = rope_turns(rope_base);
   const dim3 grid((num_rows + kAppendRows - 1) / kAppendRows);
   const int64_t pool = static_cast<int64_t>(paging->num_pages) * paging->page_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,15 +1,21 @@
 // Rows into a 4-bit pool and out of any: the 4-bit form of mla_cache_append_paged,
 // mla_cache_read_paged for every pool, and the page index over 4-bit pages.
+#include <type_traits>
+
 #include "mla_q4.cuh"
 
 namespace mla {
 namespace {
 
+constexpr int kWarps = 8;
+
 // ------------------------------------------------------------- rows into slots
 // Bound by HBM: 576 values read, 400 bytes written per row.  A warp moves a row, as in
-// append_paged_kernel; two lanes share a block of 16 latents, so its largest magnitude is one
-// exchange, and the exponents of a row's blocks are gathered into words over half a warp.
-constexpr int kWarps = 8, kEach = 4, kRows = kWarps * kEach;
+// append_paged_kernel, kAppendEach rows' loads in flight; two lanes share a block of 16 latents,
+// so its largest magnitude is one exchange, and the exponents of a row's blocks are gathered into
+// words over half a warp.  62281 bf16 rows 20.4 us, 0.70 of the measured copy bandwidth.  (A grid
+// that the SMs hold at once, each warp with its next row's loads out while it writes one: 26.7.)
+constexpr int kAppendEach = 4, kAppendRows = kWarps * kAppendEach;
 
 // e + 8 of the block whose largest magnitude has these fp32 bits (NaN counts above infinity:
 // both take the largest e).
@@ -25,13 +31,13 @@ __global__ void __launch_bounds__(32 * kWarps)
                      const __grid_constant__ RopeTurns turns, int32_t* status, int n,
                      int64_t pool_rows, int page_shift) {
   const int lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * kRows + (threadIdx.x >> 5);
-  int64_t slot[kEach];
-  int pos[kEach];
-  Raw8<In> raw[kEach][2];
-  float2 pair[kEach];
+  const int r0 = blockIdx.x * kAppendRows + (threadIdx.x >> 5);
+  int64_t slot[kAppendEach];
+  int pos[kAppendEach];
+  Raw8<In> raw[kAppendEach][2];
+  float2 pair[kAppendEach];
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
+  for (int u = 0; u < kAppendEach; ++u) {
     const int r = r0 + u * kWarps;
     slot[u] = -1;
     pos[u] = 0;
@@ -46,7 +52,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   const uint64_t turn = turns.t[lane];
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
+  for (int u = 0; u < kAppendEach; ++u) {
     if (slot[u] < 0 || slot[u] >= pool_rows || pos[u] < 0) {
       if (lane == 0 && slot[u] != -1)
         report(status, slot[u] < 0 || slot[u] >= pool_rows ? MLA_DEV_PAGE_OUT_OF_RANGE
@@ -85,8 +91,14 @@ __global__ void __launch_bounds__(32 * kWarps)
 }
 
 // ------------------------------------------------------------- rows out of pages
-// Bound by HBM: a row read, 576 values written.  A warp takes kEach consecutive rows of the
-// packed output, whose sequence its lanes find together (32 steps of the row starts a round).
+// Bound by HBM: a row read, 576 values written.  A warp takes up to 32 consecutive rows of the
+// packed output.  Its lanes find the first one's sequence together (32 steps of the row starts a
+// round), then each one row's page, so that a run of rows costs one chain of dependent loads; then
+// the warp moves them, a few rows' loads out while as many are written: four, or two of the wide
+// rows, whose registers would halve the warps.  4 x 16384 rows to bf16, 4-bit 20.1 us (0.75 of the
+// measured copy bandwidth; 22.9 with four rows a warp, each row's page looked up on its way), bf16
+// 27.9, fp32 to fp32 53.2 us (0.84).
+constexpr int kReadMost = 32;
 struct ReadParams {
   const void* pool;
   const int32_t *table, *lengths, *starts, *first;   // first may be NULL: zeros
@@ -155,53 +167,76 @@ struct RowLane<FourBit> : Q4Lane {
   }
 };
 
+template <typename T>
+constexpr int kReadEach = std::is_same_v<T, float> || std::is_same_v<T, __nv_bfloat16> ? 2 : 4;
+
 template <typename T, typename Out>
-__global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const ReadParams p, Out* rows) {
+__global__ void __launch_bounds__(32 * kWarps)
+    cache_read_kernel(const ReadParams p, Out* rows, int span) {
   const int lane = threadIdx.x & 31;
-  const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kEach;
+  const long long first = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * span;
   const int end = min(p.starts[p.B], p.num_rows);
-  if (t0 >= end) return;
-  int b = warp_search(p.starts, p.B, t0, lane);
-  int next = p.starts[b + 1], start = p.starts[b];
-  RowLane<T> in[kEach];
-  bool have[kEach];
-#pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    const int t = t0 + u;
-    have[u] = false;
-    if (t >= end) continue;
-    if (t >= next) {   // empty sequences are passed over
-      b = warp_search(p.starts, p.B, t, lane);
-      start = p.starts[b];
-      next = p.starts[b + 1];
-    }
-    const long long pos = static_cast<long long>(t) - start + (p.first ? p.first[b] : 0);
+  if (first >= end) return;
+  const int t0 = static_cast<int>(first), n = min(span, end - t0);
+  // Lane i: row t0 + i, page * page_size + row of the page, or -1 (there is none: zeros).
+  const int b0 = warp_search(p.starts, p.B, t0, lane);
+  long long slot = -1;
+  if (lane < n) {
+    const int t = t0 + lane;
+    // From there on in doubling steps (most often none or one sequence further), then halved.
+    int b = b0, step = 1;
+    for (; b + step < p.B && p.starts[b + step] <= t; step <<= 1) b += step;
+    for (step >>= 1; step > 0; step >>= 1)
+      if (b + step < p.B && p.starts[b + step] <= t) b += step;
+    const long long pos = static_cast<long long>(t) - p.starts[b] + (p.first ? p.first[b] : 0);
     if (pos < 0 || pos >= p.lengths[b] ||
         pos >= static_cast<long long>(p.table_stride) << p.page_shift) {
-      if (lane == 0) report(p.status, MLA_DEV_LENGTH_OUT_OF_RANGE);
-      continue;
+      report(p.status, MLA_DEV_LENGTH_OUT_OF_RANGE);
+    } else {
+      const int id = p.table[static_cast<size_t>(b) * p.table_stride + (pos >> p.page_shift)];
+      if (id < 0 || id >= p.num_pages)
+        report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
+      else
+        slot = (static_cast<long long>(id) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
     }
-    const int id = p.table[static_cast<size_t>(b) * p.table_stride + (pos >> p.page_shift)];
-    if (id < 0 || id >= p.num_pages) {
-      if (lane == 0) report(p.status, MLA_DEV_PAGE_OUT_OF_RANGE);
-      continue;
-    }
-    have[u] = true;
-    in[u].load(p.pool, id, static_cast<int>(pos) & ((1 << p.page_shift) - 1), p.page_shift, lane);
   }
+  constexpr int kEach = kReadEach<T>;
+  RowLane<T> next[kEach];
+  long long next_slot[kEach];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    if (t0 + u >= end) break;
-    Out* row = rows + static_cast<size_t>(t0 + u) * kRow;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float2 k = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (have[u]) in[u].values(i, lane, v);
-      store8(row + 256 * i + 8 * lane, v);
+    for (int u = 0; u < kEach; ++u) {
+      next_slot[u] = __shfl_sync(0xffffffffu, slot, (i0 + u) & 31);
+      if (i0 + u < n && next_slot[u] >= 0)
+        next[u].load(p.pool, static_cast<int>(next_slot[u] >> p.page_shift),
+                     static_cast<int>(next_slot[u]) & ((1 << p.page_shift) - 1), p.page_shift, lane);
     }
-    if (have[u]) k = in[u].pair();
-    store_pair(row + kDc + 2 * lane, k.x, k.y);
+  };
+  load(0);
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kEach) {
+    RowLane<T> in[kEach];
+    bool have[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      in[u] = next[u];
+      have[u] = next_slot[u] >= 0;
+    }
+    if (i0 + kEach < n) load(i0 + kEach);
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      if (i0 + u >= n) break;
+      Out* row = rows + static_cast<size_t>(t0 + i0 + u) * kRow;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float2 k = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (have[u]) in[u].values(i, lane, v);
+        store8(row + 256 * i + 8 * lane, v);
+      }
+      if (have[u]) k = in[u].pair();
+      store_pair(row + kDc + 2 * lane, k.x, k.y);
+    }
   }
 }
 
@@ -309,13 +344,28 @@ __global__ void __launch_bounds__(32 * kWarps)
     scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
 }
 
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  return sms > 0 ? sms : 1;
+}
+
 template <typename T>
 void launch_read(const ReadParams& p, int32_t out_dtype, void* rows, cudaStream_t s) {
-  const dim3 grid((p.num_rows + kRows - 1) / kRows), block(32 * kWarps);
+  constexpr int kEach = kReadEach<T>;
+  // As many rows a warp as leave every SM some 24 warps.
+  const long long warps = 24ll * sm_count();
+  const long long even = (p.num_rows + warps - 1) / warps;
+  const int span = static_cast<int>(
+      even > kReadMost ? kReadMost : (even + kEach - 1) / kEach * kEach);
+  const long long per_cta = static_cast<long long>(span) * kWarps;
+  const dim3 grid(static_cast<unsigned>((p.num_rows + per_cta - 1) / per_cta)), block(32 * kWarps);
   if (out_dtype == MLA_F32)
-    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<float*>(rows));
+    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<float*>(rows), span);
   else
-    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<__nv_bfloat16*>(rows));
+    cache_read_kernel<T><<<grid, block, 0, s>>>(p, static_cast<__nv_bfloat16*>(rows), span);
 }
 
 }  // namespace
@@ -323,7 +373,7 @@ void launch_read(const ReadParams& p, int32_t out_dtype, void* rows, cudaStream_
 mla_status append_q4(const char* who, const mla_paging* paging, int num_rows, bool f32_rows,
                      const void* rows, const int32_t* positions, const int64_t* slots,
                      double rope_base, void* cache, int32_t* status, cudaStream_t s) {
-  const dim3 grid((num_rows + kRows - 1) / kRows);
+  const dim3 grid((num_rows - 1) / kAppendRows + 1);
   const int64_t pool = static_cast<int64_t>(paging->num_pages) * paging->page_size;
   auto go = [&](auto* in) {
     append_q4_kernel<<<grid, 32 * kWarps, 0, s>>>(in, positions, slots,
