@@ -12,27 +12,28 @@
 // so S1 has no unit), P an E4M3 part and its E5M2 remainder.
 //
 // What differs is where the operands come from.  A tile's codes and exponents pass through both
-// CTAs as they are stored, 32 rows at a time, and eight warps turn them into E4M3 boxes of 64
-// rows x 128 columns.  A tile has four boxes in a CTA.  First they hold the CTA's own 64 rows,
-// for the scores.  The output product wants, at the same place in both CTAs, box 2 jj + h with
-// the rows of half h and the columns of box 2 jj + i in CTA i: where h is the CTA's own half that
-// is what the box holds already, and the other two boxes are decoded again from the other CTA's
-// rows, once the scores are done.  So each value is decoded where it is used, one and a half
-// times in all, and three tiles' boxes fit: the scores of the next tile are decoded while this
-// one's run, its second halves behind the softmax.  (32 x 16384 rows x 128 heads, earlier forms:
-// 193 us with score boxes and output units apart, a tile of each, and a warp for each; 172 with
-// all warps on the one and then the other; 169 with two tiles of units, decoded once and stored
-// twice, where the one tile of score boxes made decoding and the tensor cores take turns.)
+// CTAs as they are stored, 32 rows at a time, and become E4M3 boxes of 64 rows x 128 columns.  A
+// tile has four boxes in a CTA.  First they hold the CTA's own 64 rows, for the scores.  The
+// output product wants, at the same place in both CTAs, box 2 jj + h with the rows of half h and
+// the columns of box 2 jj + i in CTA i: where h is the CTA's own half that is what the box holds
+// already, and the other two boxes are decoded again from the other CTA's rows, once the scores
+// are done.  So each value is decoded where it is used, one and a half times in all, and three
+// tiles' boxes fit.  Eight warps decode the scores' boxes, a tile or two ahead; the second halves
+// are the softmax warps', behind their P, which would otherwise wait for the next scores.
+// (32 x 16384 rows x 128 heads, earlier forms: 193 us with score boxes and output units apart, a
+// tile of each, and a warp for each; 172 with all warps on the one and then the other; 169 with
+// two tiles of units, decoded once and stored twice, where the one tile of score boxes made
+// decoding and the tensor cores take turns; 137 with all of it on the eight warps, 124 now.)
 // Of the keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
 // cleaning behind a sequence's end: whatever bits a row holds, its latents are finite, and its
 // scores are not looked at.
 //
 // Tensor memory per CTA as in mla_pair.cu: S0 and S1, two buffers of 64 columns each, and O.
 //
-// Warps (1024 threads): 0-15 softmax and epilogue; 16, 22 and 23 copies of rows, a slot each (one
-// warp took 4200 cycles for a tile's four copies and what leads to them); 17 keys and queries; 18
-// score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue for the pair);
-// 24-31 codes to E4M3.
+// Warps (1024 threads): 0-15 softmax, second halves of the boxes, epilogue; 16, 22 and 23 copies
+// of rows (one warp took 4200 cycles for a tile's four copies and what leads to them); 17 keys and
+// queries; 18 score MMAs and 19 those of the keys, 20 and 21 output MMAs (the even CTA's issue for
+// the pair); 24-31 the scores' boxes.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
@@ -48,9 +49,8 @@ struct Q4Pair {
   static constexpr int kParts = 2;
   static constexpr int kQKeys = kParts * 4 * kPBox;     // offset of the query's key part
   static constexpr int kQBytes = kQKeys + kPBox;
-  // Rows arrive in slots of 32: the CTA's own half of a tile, then the other half of the one
-  // before.  (With two slots and two tiles' keys 145 us for 32 x 16384 rows x 128 heads.)
-  static constexpr int kSlotRows = 32, kSlots = 3;
+  // Rows arrive in slots of 32: two for the CTA's own half of a tile, two for the other half.
+  static constexpr int kSlotRows = 32, kSlots = 4;
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kKeyBytes = 64 * kQ4KeyBytes;
   static constexpr int kOffQ = 0;
@@ -60,28 +60,31 @@ struct Q4Pair {
   static constexpr int kOffP = kOffK + kKeyBytes;
   static constexpr int kOffRaw = kOffP + kPBufBytes;
   static constexpr int kOffTable = kOffRaw + kSlots * kSlotBytes;
-  static constexpr int kOffRed = kOffTable + 128;       // [2 kSlices][64] maxima
-  static constexpr int kOffSum = kOffRed + 2 * kSlices * kPHeads * 4;       // row sums
-  static constexpr int kOffBar = kOffSum + 2 * kSlices * kPHeads * 4;
+  static constexpr int kOffBar = kOffTable + 128;
   // Rows landed / decoded and keys landed (this CTA's); a tile's boxes decoded for the scores,
-  // for the output, and free; keys handed over; S, P, O and the query as in mla_pair.cu.
+  // and free; keys handed over; S, P (with the boxes' second halves), O and the query as in
+  // mla_pair.cu.
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + kSlots, KEYFULL = RAWEMPTY + kSlots,
-                       FULLS = KEYFULL + 1, FULLV = FULLS + kTiles, FREE = FULLV + kTiles,
+                       FULLS = KEYFULL + 1, FREE = FULLS + kTiles,
                        KREADY = FREE + kTiles, SREADY = KREADY + 1,
                        SFREE = SREADY + 2, PREADY = SFREE + 2, PVDONE = PREADY + 2,
                        QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffSlot + 8;
   static constexpr int kOffShare = kOffAbort + 8;       // TileShare of the pair
-  static constexpr size_t kSmem = 1024 + kOffShare + 24;
+  static constexpr size_t kSmem = kOffShare + 24;
   static constexpr uint32_t kOCol = 256;
   // Reference of the softmax below the running maximum, and how far a maximum may pass it
   // before O is rescaled (log2): weights stay in [0, 2^8.5].
   static constexpr float kBias = 3.f, kGrow = 5.5f;
   static constexpr int kStageRow = kDc * 4 + 16;        // epilogue staging, over the operands
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kOffRed >= kPHeads * kStageRow, "epilogue staging");
+  static_assert(kOffRaw >= kPHeads * kStageRow, "epilogue staging");
+  // What the softmax warps exchange (maxima, sums, an item's output) goes through P when nothing
+  // reads it; the eight warps of the same heads keep to those heads' rows of it: 32 rows of each
+  // part, part 0 first.
   static_assert(kPBufBytes == kSoftWarps * 32 * 32, "an item's output through P");
+  static_assert(2 * kSlices * 32 * 4 <= 4096, "the maxima of 32 heads through P");
   static_assert(kOffC % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kOffRaw % 16 == 0 && kOffBar % 8 == 0, "alignment");
 };
@@ -149,11 +152,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
                          const __grid_constant__ CUtensorMap tmap_qpe, const SplitParams p,
                          const float* __restrict__ sigma) {
   using L = Q4Pair;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t q4_pair_smem[];
+  uint8_t* smem = q4_pair_smem;
   const uint32_t sbase = smem_u32(smem), bars = sbase + L::kOffBar;
-  float* red = reinterpret_cast<float*>(smem + L::kOffRed);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -189,7 +190,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
   auto lbar = [&](int i) { return lead + 8 * i; };
   constexpr int kWarpRows = L::kSoftWarps, kWarpKeys = kWarpRows + 1, kWarpScore = kWarpRows + 2,
                 kWarpOut = kWarpRows + 4, kWarpRows2 = kWarpRows + 6, kWarpDecode = kWarpRows + 8;
-  static_assert(L::kSlots == 3, "a warp for each slot of rows");
 
   if (tid == L::kSoft) {
     for (int i = 0; i < L::kSlots; ++i) {
@@ -198,7 +198,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     }
     for (int i = 0; i < L::kTiles; ++i) {
       mbar_init(bar(L::FULLS + i), 16);   // the decoding warps of both CTAs
-      mbar_init(bar(L::FULLV + i), 16);
       mbar_init(bar(L::FREE + i), 2);     // one commit per output issuer
     }
     for (int i = 0; i < 2; ++i) {
@@ -320,47 +319,34 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       ahead_r0 = then.r0 + (more ? i + 1 : 0) * kTileRows;
     };
     if (rows) {
-      // In the order in which they are decoded: the CTA's own half of a tile, then the other
-      // half of the tile before.
-      const int per = L::kSlotRows / piece, slot = warp == kWarpRows ? 0 : warp - kWarpRows2 + 1;
-      int next = slot, used = 0;   // halves' 32 rows until this warp's next; times its slot was used
-      auto issue_half = [&](const uint8_t* src, int live, int half) {   // false: given up
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          if (next-- > 0) continue;
-          next = L::kSlots - 1;
-          const int from = (2 * half + k) * per;
-          if (used > 0) {
-            q4_warp_wait(bar(L::RAWEMPTY + slot), (used - 1) & 1, abort_flag);
-            if (given_up()) return false;
-          }
-          ++used;
-          copy_pieces(src, from, from + per, live, piece * bytes,
-                      sbase + L::kOffRaw + slot * L::kSlotBytes, bar(L::RAWFULL + slot));
-        }
-        return true;
-      };
-      // A tile's sources, the one before's and the next one's.
-      const uint8_t *src = piece_source(ahead, ahead_r0), *last = nullptr;
-      int last_live = 0;
-      bool ok = true;
+      // Two warps for the slots of the CTA's own half, one for both of the other half.
+      const bool own = warp != kWarpRows2 + 1;
+      const int k0 = own && warp != kWarpRows ? 1 : 0, k1 = own ? k0 + 1 : 2;
+      const int per = L::kSlotRows / piece, half = own ? rank : 1 - rank;
+      // A tile's sources, and the next one's.
+      const uint8_t* src = piece_source(ahead, ahead_r0);
       for_tiles([&](const TileItem& it, int i, int t) {
-        if (given_up()) return ok = false;
+        if (given_up()) return false;
         const int live = live_of(ahead);
         look_ahead(it, i, t);
         const uint8_t* then = piece_source(ahead, ahead_r0);
         // The slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
         // other half has come with the other CTA's by the time it is copied.)
-        if (slot == 0 && ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
+        if (warp == kWarpRows && ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
           prefetch_l2(then, piece * bytes);
-        if (!issue_half(src, live, rank)) return ok = false;
-        if (t > 0 && !issue_half(last, last_live, 1 - rank)) return ok = false;
-        last = src;
-        last_live = live;
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) {
+          const int slot = (own ? 0 : 2) + k, from = (2 * half + k) * per;
+          if (t > 0) {
+            q4_warp_wait(bar(L::RAWEMPTY + slot), (t - 1) & 1, abort_flag);
+            if (given_up()) return false;
+          }
+          copy_pieces(src, from, from + per, live, piece * bytes,
+                      sbase + L::kOffRaw + slot * L::kSlotBytes, bar(L::RAWFULL + slot));
+        }
         src = then;
         return true;
       });
-      if (ok && T > 0) issue_half(last, last_live, 1 - rank);
     } else {
       int queries = 0;   // later items' queries fetched
       for_tiles([&](const TileItem& it, int i, int t) {
@@ -389,41 +375,43 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     }
   } else if (warp >= kWarpDecode) {
     // ------------------------------------------------------------ codes to E4M3
-    // Warp d takes 32 columns, piece c = d & 3: of the CTA's own rows in boxes 2 j and 2 j + 1,
-    // j = d >> 2, then, one tile behind, of the other CTA's rows in box 2 j + 1 - rank, the
-    // columns of box 2 j + rank.  A row per lane: rows are 17 times 16 bytes apart, so eight
-    // lanes read from eight different pieces of the banks, and the swizzle has them write so.
+    // Warp d takes 32 columns, piece c = d & 3, of the CTA's own rows in boxes 2 j and 2 j + 1,
+    // j = d >> 2.  A row per lane: rows are 17 times 16 bytes apart, so eight lanes read from
+    // eight different pieces of the banks, and the swizzle has them write so.  All is loaded, and
+    // the slots given back, before the first is stored.
     const int d = warp - kWarpDecode, c = d & 3, j = d >> 2;
     const uint8_t* table = smem + L::kOffTable;
     const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
     uint8_t* boxes = smem + L::kOffC + 2 * j * kPBox + lane * 128;
     const uint32_t at = (2 * c << 4) ^ ((lane & 7) << 4);
-    int n = 0;   // slots taken
-    // The next two slots' (a half's 64 rows) piece c of boxes m .. m + kBoxes - 1, into boxes from
-    // `to` on: all loaded, and the slots given back, before the first is stored.
-    auto decode_half = [&](auto boxes_of, int m, uint8_t* to) {
-      constexpr int kBoxes = decltype(boxes_of)::value;
-      Q4Piece piece[2][kBoxes];
+    for (int t = 0; t < T; ++t) {
+      const int buf = t % L::kTiles;
+      if (t >= L::kTiles) {
+        q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
+        tc_fence_after();
+      }
+      if (given_up()) break;
+      Q4Piece piece[2][2];
       bool plain = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int slot = n % L::kSlots;
-        q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
-        ++n;
-        const uint8_t* raw = from + slot * L::kSlotBytes;
+        q4_warp_wait(bar(L::RAWFULL + k), t & 1, abort_flag);
+        const uint8_t* raw = from + k * L::kSlotBytes;
 #pragma unroll
-        for (int i = 0; i < kBoxes; ++i) {
-          piece[k][i].load(raw + 64 * (m + i) + 16 * c, raw + kQ4CodeBytes + 4 * (m + i) + c);
+        for (int i = 0; i < 2; ++i) {
+          const int m = 2 * j + i;
+          piece[k][i].load(raw + 64 * m + 16 * c, raw + kQ4CodeBytes + 4 * m + c);
           plain = plain && piece[k][i].plain();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
       }
+      uint8_t* to = boxes + buf * 4 * kPBox;
       auto store = [&](auto is_plain) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < kBoxes; ++i)
+          for (int i = 0; i < 2; ++i)
             piece[k][i].template store<decltype(is_plain)::value != 0>(
                 to + i * kPBox + k * (L::kSlotRows * 128), at, table);
       };
@@ -431,31 +419,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         store(Int<1>{});
       else
         store(Int<0>{});
-    };
-    auto hand_over = [&](int full) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_cluster(lbar(full));
-    };
-    for (int t = 0; t <= T; ++t) {
-      const int buf = t % L::kTiles;
-      if (t < T) {   // the scores' boxes of tile t
-        if (t >= L::kTiles) {
-          q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
-          tc_fence_after();
-        }
-        if (given_up()) break;
-        decode_half(Int<2>{}, 2 * j, boxes + buf * 4 * kPBox);
-        hand_over(L::FULLS + buf);
-      }
-      if (t > 0) {   // the output's of tile t - 1, once its scores are done
-        const int last = (t - 1) % L::kTiles;
-        q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-        tc_fence_after();
-        if (given_up()) break;
-        decode_half(Int<1>{}, 2 * j + rank, boxes + (last * 4 + 1 - rank) * kPBox);
-        hand_over(L::FULLV + last);
-      }
+      if (lane == 0) arrive_cluster(lbar(L::FULLS + buf));
     }
   } else if (warp == kWarpScore || warp == kWarpScore + 1) {
     // ------------------------------------------------------------ score MMAs (even CTA)
@@ -523,9 +489,8 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       const uint32_t d = tmem + L::kOCol + 128 * jj;
       for_tiles([&](const TileItem&, int i, int t) {
         const int pb = t & 1;
-        q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
         const int buf = t % L::kTiles;
-        q4_warp_wait(bar(L::FULLV + buf), (t / L::kTiles) & 1, abort_flag);
+        q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
         if (given_up()) return false;
         tc_fence_after();
 #pragma unroll 1
@@ -554,6 +519,16 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     const int head = 32 * (qd & 1) + lane, row0 = 64 * (qd >> 1) + kCols * hh;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qd) << 16);
     const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
+    // The rows of P of the warp's heads: 32 of each part.
+    uint8_t* mine_p = smem + L::kOffP + 4096 * (qd & 1);
+    float* red = reinterpret_cast<float*>(mine_p);   // [2 kSlices][32 heads]
+    // A tile's boxes again: 32 of the other CTA's rows (slot), 32 columns (piece c) of box 2 j +
+    // rank, into box 2 j + 1 - rank; a row per lane, as the decoding warps.
+    const int slot = 2 + (warp >> 3), c = warp & 3, j = (warp >> 2) & 1;
+    const uint8_t* raw = smem + L::kOffRaw + slot * L::kSlotBytes + lane * kQ4LatBytes;
+    uint8_t* box = smem + L::kOffC + (2 * j + 1 - rank) * kPBox +
+                   (warp >> 3) * (L::kSlotRows * 128) + lane * 128;
+    const uint32_t box_at = (2 * c << 4) ^ ((lane & 7) << 4);
     const int back = p.q_len - 1 - (first + min(head, mine - 1)) / p.H;   // tokens behind its own
     const float scale = p.scale_log2;
     TileItem it = item0;
@@ -592,11 +567,16 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
         // The eight warps of the same heads go by one reference, and decide alike.
         if (any_of(t == t0 || mx > L::kBias + L::kGrow, 1 + (qd & 1), L::kSoft / 2)) {
-          red[part_of * kPHeads + head] = mx;
+          if (t > t0) {   // P and O: the output product of the tile before is done
+            q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+          }
+          red[part_of * 32 + lane] = mx;
           named_bar_sync(3 + (qd & 1), L::kSoft / 2);
-          mx = red[head];
+          mx = red[lane];
 #pragma unroll
-          for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, red[i * kPHeads + head]);
+          for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, red[i * 32 + lane]);
+          named_bar_sync(3 + (qd & 1), L::kSoft / 2);   // read before any P is written
           // Move the reference (up, but to wherever the first tile has it; a head whose token
           // attends none of its rows attends none of the item's); rescale the sum and this
           // warp's share of O.
@@ -608,8 +588,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] -= up;
           if (t > t0) {
-            q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 16 / kSlices; ++c) {   // this warp's slice of O's 256 columns
               const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 16 * c;
@@ -656,6 +634,20 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           *reinterpret_cast<uint4*>(pb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(pb + kPBox + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        {
+          // The scores of this tile are done: its boxes' second halves.
+          q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag);
+          Q4Piece piece;
+          const int m = 2 * j + rank;
+          piece.load(raw + 64 * m + 16 * c, raw + kQ4CodeBytes + 4 * m + c);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+          uint8_t* to = box + t % L::kTiles * 4 * kPBox;
+          if (__all_sync(0xffffffffu, piece.plain()))
+            piece.store<true>(to, box_at, smem + L::kOffTable);
+          else
+            piece.store<false>(to, box_at, smem + L::kOffTable);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -665,15 +657,15 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       if (tid == 0 && t0 == T) pdl_launch_dependents();   // the combine waits for this grid anyway
       // The row sums of a head's threads, its log-sum-exp, and O / sum through shared memory
       // (over operands that nothing reads any more) to whole rows.
-      float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
-      sums[part_of * kPHeads + head] = l;
       q4_warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
+      red[part_of * 32 + lane] = l;
       named_bar_sync(5, L::kSoft);
-      if (!*abort_flag) {
-        float sum = 0.f;
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * kSlices; ++i) sum += sums[i * kPHeads + head];
+      for (int i = 0; i < 2 * kSlices; ++i) sum += red[i * 32 + lane];
+      named_bar_sync(5, L::kSoft);   // read before P is written again
+      if (!*abort_flag) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const bool whole = kShare ? whole_set(it) : p.direct != 0;   // the result itself
         const size_t stride = whole ? 1 : p.splits;
