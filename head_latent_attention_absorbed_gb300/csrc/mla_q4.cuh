@@ -185,16 +185,23 @@ struct Q4Piece {
   // e; others are looked up.
   __device__ __forceinline__ bool plain() const { return (e & (e << 1) & 0x88u) == 0; }
   template <bool kPlain>
-  __device__ __forceinline__ void store(uint8_t* row, uint32_t at, const uint8_t* table) const {
+  __device__ __forceinline__ void decode(uint4& lo, uint4& hi, const uint8_t* table) const {
     auto magnitudes = [&](uint32_t x) {
       return kPlain ? make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u)
                     : *reinterpret_cast<const uint2*>(table + 8 * x);
     };
     const uint2 m0 = magnitudes(e & 15), m1 = magnitudes(e >> 4);
     const uint2 a = decode8(w.x, m0), b = decode8(w.y, m0);
-    *reinterpret_cast<uint4*>(row + at) = make_uint4(a.x, a.y, b.x, b.y);
+    lo = make_uint4(a.x, a.y, b.x, b.y);
     const uint2 x = decode8(w.z, m1), y = decode8(w.w, m1);
-    *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(x.x, x.y, y.x, y.y);
+    hi = make_uint4(x.x, x.y, y.x, y.y);
+  }
+  template <bool kPlain>
+  __device__ __forceinline__ void store(uint8_t* row, uint32_t at, const uint8_t* table) const {
+    uint4 lo, hi;
+    decode<kPlain>(lo, hi, table);
+    *reinterpret_cast<uint4*>(row + at) = lo;
+    *reinterpret_cast<uint4*>(row + (at ^ 16)) = hi;
   }
 };
 

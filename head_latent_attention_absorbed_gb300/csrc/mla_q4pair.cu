@@ -377,8 +377,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     // ------------------------------------------------------------ codes to E4M3
     // Warp d takes 32 columns, piece c = d & 3, of the CTA's own rows in boxes 2 j and 2 j + 1,
     // j = d >> 2.  A row per lane: rows are 17 times 16 bytes apart, so eight lanes read from
-    // eight different pieces of the banks, and the swizzle has them write so.  All is loaded, and
-    // the slots given back, before the first is stored.
+    // eight different pieces of the banks, and the swizzle has them write so.  All is decoded into
+    // registers before the wait for the boxes: a tile's way through them, from here to the end of
+    // its output product, is what bounds the kernel.
     const int d = warp - kWarpDecode, c = d & 3, j = d >> 2;
     const uint8_t* table = smem + L::kOffTable;
     const uint8_t* from = smem + L::kOffRaw + lane * kQ4LatBytes;
@@ -386,10 +387,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     const uint32_t at = (2 * c << 4) ^ ((lane & 7) << 4);
     for (int t = 0; t < T; ++t) {
       const int buf = t % L::kTiles;
-      if (t >= L::kTiles) {
-        q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
-        tc_fence_after();
-      }
       if (given_up()) break;
       Q4Piece piece[2][2];
       bool plain = true;
@@ -406,19 +403,32 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
       }
-      uint8_t* to = boxes + buf * 4 * kPBox;
-      auto store = [&](auto is_plain) {
+      uint4 e4m3[2][2][2];
+      auto decode = [&](auto is_plain) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            piece[k][i].template store<decltype(is_plain)::value != 0>(
-                to + i * kPBox + k * (L::kSlotRows * 128), at, table);
+            piece[k][i].template decode<decltype(is_plain)::value != 0>(e4m3[k][i][0],
+                                                                        e4m3[k][i][1], table);
       };
       if (__all_sync(0xffffffffu, plain))
-        store(Int<1>{});
+        decode(Int<1>{});
       else
-        store(Int<0>{});
+        decode(Int<0>{});
+      if (t >= L::kTiles) {
+        q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
+        tc_fence_after();
+      }
+      uint8_t* to = boxes + buf * 4 * kPBox;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint8_t* row = to + i * kPBox + k * (L::kSlotRows * 128);
+          *reinterpret_cast<uint4*>(row + at) = e4m3[k][i][0];
+          *reinterpret_cast<uint4*>(row + (at ^ 16)) = e4m3[k][i][1];
+        }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_cluster(lbar(L::FULLS + buf));
@@ -601,6 +611,11 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
             tmem_wait_st();
           }
         }
+        // The scores of this tile are done: its boxes' second halves, loaded.
+        q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag);
+        Q4Piece piece;
+        const int box_m = 2 * j + rank;
+        piece.load(raw + 64 * box_m + 16 * c, raw + kQ4CodeBytes + 4 * box_m + c);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
           x[i] = ex2(x[i]);
@@ -635,11 +650,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           *reinterpret_cast<uint4*>(pb + kPBox + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         {
-          // The scores of this tile are done: its boxes' second halves.
-          q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag);
-          Q4Piece piece;
-          const int m = 2 * j + rank;
-          piece.load(raw + 64 * m + 16 * c, raw + kQ4CodeBytes + 4 * m + c);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
           uint8_t* to = box + t % L::kTiles * 4 * kPBox;
