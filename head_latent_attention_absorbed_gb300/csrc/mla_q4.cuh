@@ -171,26 +171,27 @@ __device__ __forceinline__ void q4_table(uint8_t* table, int lane) {
                  to_e4m3x2(2.f * u, 3.f * u) | to_e4m3x2(4.f * u, 6.f * u) << 16);
 }
 
+// Up to the bits 11 every magnitude is a normal E4M3 number, whose exponent field grows with
+// the bits; others are looked up.  true: all of e's eight (zeros are) are such.
+__device__ __forceinline__ bool q4_plain(uint32_t e) { return (e & (e << 1) & 0x88888888u) == 0; }
+
 // 32 codes of one row and their two blocks' exponents, as loaded, and as E4M3 in the row's
 // 16-byte units at `at` and at ^ 16 of a box of 128-byte rows (the caller has the 128-byte
 // swizzle in `at`).
 struct Q4Piece {
   uint4 w;
-  uint32_t e;   // one byte
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* exps) {
+  uint32_t e;   // in the low byte
+  __device__ __forceinline__ void load(const uint8_t* codes, uint32_t exps) {
     w = *reinterpret_cast<const uint4*>(codes);
-    e = *exps;
+    e = exps;
   }
-  // Up to the bits 11 every magnitude is a normal E4M3 number, whose exponent field grows with
-  // e; others are looked up.
-  __device__ __forceinline__ bool plain() const { return (e & (e << 1) & 0x88u) == 0; }
   template <bool kPlain>
   __device__ __forceinline__ void decode(uint4& lo, uint4& hi, const uint8_t* table) const {
     auto magnitudes = [&](uint32_t x) {
       return kPlain ? make_uint2(x * 0x08080800u + 0x14100800u, x * 0x08080808u + 0x24201c18u)
                     : *reinterpret_cast<const uint2*>(table + 8 * x);
     };
-    const uint2 m0 = magnitudes(e & 15), m1 = magnitudes(e >> 4);
+    const uint2 m0 = magnitudes(e & 15), m1 = magnitudes(e >> 4 & 15);
     const uint2 a = decode8(w.x, m0), b = decode8(w.y, m0);
     lo = make_uint4(a.x, a.y, b.x, b.y);
     const uint2 x = decode8(w.z, m1), y = decode8(w.w, m1);

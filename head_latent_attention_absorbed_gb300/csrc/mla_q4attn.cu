@@ -33,6 +33,8 @@
 //   warps 12-19  codes to E4M3, two teams of four warps in turn
 // (A copy takes its warp some 450 cycles among the others' work: one warp for all of a
 // tile's, and exponents in a plane of their own, took 6600 cycles a tile.)
+#include <type_traits>
+
 #include "mla_q4.cuh"
 
 namespace mla {
@@ -418,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     constexpr int kEach = L::kSlotRows / 8;   // 16-byte pieces of codes (32 values) a lane
     const uint8_t* from = smem + L::kOffRaw + r * kQ4LatBytes + 64 * m + 16 * kEach * part;
     const uint8_t* exps = smem + L::kOffRaw + r * kQ4LatBytes + kQ4CodeBytes + 4 * m + kEach * part;
+    using Exps = std::conditional_t<kEach == 4, uint32_t, uint16_t>;   // a byte per piece
+    static_assert(sizeof(Exps) == kEach, "a byte of exponents per piece");
     const uint8_t* table = smem + L::kOffTable;
     uint8_t* to = smem + L::kOffTile + m * kBox + r * 128;
     const uint32_t swz = (r & 7) << 4, unit0 = 2 * kEach * part;
@@ -434,13 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         const int slot = n % L::kSlots;
         q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
         const uint8_t* src = from + slot * L::kSlotBytes;
+        // (Exponents by bytes: four loads that meet in the same banks for one.)
+        const uint32_t e = *reinterpret_cast<const Exps*>(exps + slot * L::kSlotBytes);
         Q4Piece piece[kEach];
-        bool plain = true;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          piece[k].load(src + 16 * k, exps + slot * L::kSlotBytes + k);
-          plain = plain && piece[k].plain();
-        }
+        for (int k = 0; k < kEach; ++k) piece[k].load(src + 16 * k, e >> 8 * k);
+        const bool plain = q4_plain(e);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
         uint8_t* row = tile + s * L::kSlotRows * 128;

@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int m = 2 * j + i;
-          piece[k][i].load(raw + 64 * m + 16 * c, raw + kQ4CodeBytes + 4 * m + c);
-          plain = plain && piece[k][i].plain();
+          piece[k][i].load(raw + 64 * m + 16 * c, raw[kQ4CodeBytes + 4 * m + c]);
+          plain = plain && q4_plain(piece[k][i].e);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + k));
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag);
         Q4Piece piece;
         const int box_m = 2 * j + rank;
-        piece.load(raw + 64 * box_m + 16 * c, raw + kQ4CodeBytes + 4 * box_m + c);
+        piece.load(raw + 64 * box_m + 16 * c, raw[kQ4CodeBytes + 4 * box_m + c]);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
           x[i] = ex2(x[i]);
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
           uint8_t* to = box + t % L::kTiles * 4 * kPBox;
-          if (__all_sync(0xffffffffu, piece.plain()))
+          if (__all_sync(0xffffffffu, q4_plain(piece.e)))
             piece.store<true>(to, box_at, smem + L::kOffTable);
           else
             piece.store<false>(to, box_at, smem + L::kOffTable);
