@@ -72,7 +72,9 @@ struct Q4Plan {
   // the teams that decode them in turn: each team then meets every phase of its slots (a
   // parity wait that skips one passes too early).
   static constexpr int kSlotRows = kF32 ? 16 : 32, kSlots = 4;
-  static_assert(kSlots % kTeams == 0 && (kRowsT / kSlotRows) % kTeams == 0, "slots by team");
+  static_assert(kSlots % kTeams == 0 && (kRowsT / kSlotRows) % kTeams == 0 &&
+                    kRowsT / kSlotRows >= 2 * kTeams && kSlots >= 2 * kTeams,
+                "slots by team");
   static constexpr int kSlotBytes = kSlotRows * kQ4LatBytes;
   static constexpr int kOffTile = 0;
   static constexpr int kOffKeys = kOffTile + 2 * kTile;
@@ -425,37 +427,66 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     const uint8_t* table = smem + L::kOffTable;
     uint8_t* to = smem + L::kOffTile + m * kBox + r * 128;
     const uint32_t swz = (r & 7) << 4, unit0 = 2 * kEach * part;
+    // Slot n's codes, and the slot given back; true: of plain exponents.  (Exponents by bytes:
+    // four loads that meet in the same banks for one.)
+    auto load = [&](Q4Piece (&piece)[kEach], int n) {
+      const int slot = n % L::kSlots;
+      q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
+      const uint32_t e = *reinterpret_cast<const Exps*>(exps + slot * L::kSlotBytes);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        piece[k].load(from + slot * L::kSlotBytes + 16 * k, e >> 8 * k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
+      return __all_sync(0xffffffffu, q4_plain(e)) != 0;
+    };
+    auto store = [&](const Q4Piece (&piece)[kEach], bool plain, uint8_t* row) {
+      if (plain) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          piece[k].template store<true>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          piece[k].template store<false>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
+      }
+    };
     int n = team;
     for (int t = 0; t < T; ++t) {
-      uint8_t* tile = to + (t & 1) * kTile;
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      // A tile's way through its buffer, from here to the end of its output product, is part of
+      // what bounds the kernel: the team's first slot is decoded, and the second read, before the
+      // wait for the buffer.
+      Q4Piece piece[kEach];
+      uint4 e4m3[kEach][2];
+      if (load(piece, n)) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          piece[k].template decode<true>(e4m3[k][0], e4m3[k][1], table);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          piece[k].template decode<false>(e4m3[k][0], e4m3[k][1], table);
+      }
+      n += kTeams;
+      bool plain = load(piece, n);
+      n += kTeams;
       if (t >= 2) {
         q4_warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
         tc_fence_after();
       }
-      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      uint8_t* rows = to + (t & 1) * kTile + team * L::kSlotRows * 128;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        *reinterpret_cast<uint4*>(rows + (((unit0 + 2 * k) << 4) ^ swz)) = e4m3[k][0];
+        *reinterpret_cast<uint4*>(rows + (((unit0 + 2 * k + 1) << 4) ^ swz)) = e4m3[k][1];
+      }
+      constexpr int kStep = kTeams * L::kSlotRows * 128;
+      store(piece, plain, rows += kStep);
 #pragma unroll 1
-      for (int s = team; s < kTileSlots; s += kTeams, n += kTeams) {
-        const int slot = n % L::kSlots;
-        q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
-        const uint8_t* src = from + slot * L::kSlotBytes;
-        // (Exponents by bytes: four loads that meet in the same banks for one.)
-        const uint32_t e = *reinterpret_cast<const Exps*>(exps + slot * L::kSlotBytes);
-        Q4Piece piece[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) piece[k].load(src + 16 * k, e >> 8 * k);
-        const bool plain = q4_plain(e);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::RAWEMPTY + slot));
-        uint8_t* row = tile + s * L::kSlotRows * 128;
-        if (__all_sync(0xffffffffu, plain)) {
-#pragma unroll
-          for (int k = 0; k < kEach; ++k)
-            piece[k].template store<true>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
-        } else {
-#pragma unroll
-          for (int k = 0; k < kEach; ++k)
-            piece[k].template store<false>(row, ((unit0 + 2 * k) << 4) ^ swz, table);
-        }
+      for (int s = 2 * kTeams; s < kTileSlots; s += kTeams, n += kTeams) {
+        plain = load(piece, n);
+        store(piece, plain, rows += kStep);
       }
       fence_proxy_async_smem();
       __syncwarp();
