@@ -2101,8 +2101,10 @@ constexpr int kShareMinTiles = 5;
 // shares: bf16, 512 to 8192 rows, 16 sequences (13.5 tiles) 34.1 / 29.1, 76 114 / 93, 152
 // 204 / 166, 200 245 / 214, 256 of 100 to 2048 95 / 106; 512 to 4096, 16 (6.7) 22.6 / 23.9,
 // 24 (10.1) 27.6 / 28.0; all full, 16 x 8192 40.7 / 44.4, 76 x 8192 127 / 136; E4M3, 32 of
-// 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82; 4-bit, 16 of
-// 512 to 8192 (13.5) 42.0 / 34.4, 32 x 2048 x 128 heads (6.7) 33.2 / 39.6.
+// 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82; 4-bit of
+// 128 heads, 512 to 8192, 16 (13.5) 40.5 / 36.4, 48 87 / 72, 76 115 / 106, 152 210 / 186; all
+// full, 16 x 8192 42.2 / 47.3, 76 x 4096 68 / 81, 32 x 2048 (6.7) 30.7 / 37.5; one of 32768
+// among 32 of 2048 217 / 123.
 constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairTilesFp4 = 13,
               kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {

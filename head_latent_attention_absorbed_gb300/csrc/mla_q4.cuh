@@ -99,9 +99,19 @@ struct Q4Lane {
     code[0] = code[1] = key = 0;
     exp[0] = exp[1] = 0;
   }
-  // Latents 8 l .. (i = 0) or 256 + 8 l .. (i = 1).
-  __device__ __forceinline__ void values(int i, int lane, float* v) const {
-    q4_values(code[i], q4_unit(exp[i] >> (lane & 2 ? 4 : 0)), v);
+  // Latents 8 l .. (i = 0) or 256 + 8 l .. (i = 1), times a power of two.
+  __device__ __forceinline__ void values(int i, int lane, float* v, float times = 1.f) const {
+    q4_values(code[i], q4_unit(exp[i] >> (lane & 2 ? 4 : 0)) * times, v);
+  }
+  // The power of two above their magnitudes, of 2^high; -100: they are all zero.
+  __device__ __forceinline__ int high(int i, int lane) const {
+    const uint32_t w = code[i];
+    const int e = min(((exp[i] >> (lane & 2 ? 4 : 0)) + 3) & 15, 14) + kQ4ExpMin;   // as q4_unit
+    return (w & (w << 1) & 0x44444444u) ? e + 3   // 4 and 6
+           : (w & 0x44444444u)          ? e + 2   // 2 and 3
+           : (w & 0x22222222u)          ? e + 1   // 1 and 1.5
+           : (w & 0x11111111u)          ? e       // 0.5
+                                        : -100;
   }
   __device__ __forceinline__ float2 pair() const {
     return make_float2(__uint_as_float(key << 16), __uint_as_float(key & 0xffff0000u));
