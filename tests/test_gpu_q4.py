@@ -285,6 +285,42 @@ def test_index(cuda_lib, page):
     assert (codes.cpu().numpy() == want_c).all() and (scales.cpu().numpy() == want_s).all()
 
 
+def test_index_of_every_value(cuda_lib):
+    """A page's unit comes from its largest value: each that a pool can hold, alone and beside
+    smaller ones, under smaller and larger keys, and a page with an infinite key (zeros)."""
+    mla = cuda_lib
+    rng = np.random.RandomState(3)
+    page, each = 16, [(c, e) for c in [*range(1, 8), *range(9, 16)] for e in range(-8, 7)]
+    pages = 4 * len(each) + 2
+    code = np.zeros((pages, page, D_C), np.int64)
+    exp = rng.randint(-8, 7, (pages, page, 32))
+    key = np.zeros((pages, page, 64), np.float32)
+    for i, (c, e) in enumerate(each):
+        for k in range(4):
+            p, r, col = 4 * i + k, rng.randint(page), rng.randint(D_C)
+            if k == 1:                           # smaller ones beside it
+                code[p], exp[p] = rng.randint(0, 2, (page, D_C)), -8
+            code[p, r, col], exp[p, r, col // 16] = c, e
+            if k >= 2:
+                key[p, rng.randint(page), rng.randint(64)] = 2.0 ** (-20 if k == 2 else 12) * 1.5
+    key[-1, 3, 5] = np.inf
+    code[-1] = rng.randint(0, 16, (page, D_C))
+    pool = F.pack(code, exp, _q4.bf16_bits(key))
+    val = _q4.values(pool, page)
+    d, pg = mla.dims(1, 16, pages * page, mla.MLA_FP4_E2M1), mla.paging(page, pages, pages)
+    codes = torch.full((pages, ROW), 77, dtype=torch.int8, device="cuda")
+    scales, status = torch.full((pages,), 7.0, device="cuda"), status_word()
+    mla.page_index(d, pg, torch.from_numpy(pool).cuda(), i32([np.arange(pages)]), i32([0]),
+                   i32([pages * page]), pages * page, codes, scales, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    got_c, got_s = codes.cpu().numpy(), scales.cpu().numpy()
+    for p in range(pages - 1):
+        want_c, want_s = PO.page_index(val[p])
+        assert got_s[p] == want_s and (got_c[p] == want_c).all(), p
+    assert got_s[-1] == 0 and (got_c[-1] == 0).all()
+
+
 def test_index_reports(cuda_lib):
     mla = cuda_lib
     pool, table, pages = _q4.make_pool(np.random.RandomState(0), [40, 20], 16)
@@ -706,3 +742,87 @@ def test_serving_loop(cuda_lib):
         torch.cuda.synchronize()
         assert int(status.item()) == 0
         _q4.check_attention(o, lse, q_abs, q_pe, host, page, sel.cpu(), sel_len.cpu().numpy(), 1, BF16)
+
+
+@pytest.mark.parametrize("form", [0, 1])
+@pytest.mark.parametrize("io,heads", [(BF16, 16), (F32, 32), (BF16, 128)])
+def test_calls_at_once(cuda_lib, io, heads, form):
+    """Two calls on two streams, of one pool and each its own workspace, while a third stream
+    writes and reads other pages of the pool: each gives what it gives alone."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(form)
+    try:
+        calls = [Call(mla, np.minimum(share_lengths("ragged", 20), 900) + 1, 64, io, heads, seed=9,
+                      s_max=7000, extra_pages=40, width=110) for _ in range(2)]
+        calls[1].q_abs = calls[1].q_abs.flip(0).contiguous()
+        calls[1].dev.update(pool=calls[0].dev["pool"], q_abs=calls[1].q_abs.cuda())
+        alone = []
+        for c in calls:
+            c.run().check(tokens=[0, 7, 19])
+            alone.append((c.o.clone(), c.lse.clone()))
+        free = sorted(set(range(calls[0].pages)) - set(calls[0].table[calls[0].table >= 0].tolist()))[:40]
+        rng = np.random.RandomState(10)
+        rows = torch.from_numpy(rng.randn(64 * len(free), ROW).astype(np.float32)).cuda()
+        slots = (torch.tensor(free).repeat_interleave(64) * 64 + torch.arange(64).repeat(len(free))).cuda()
+        table, zero = i32([free]), torch.zeros(len(slots), dtype=torch.int32, device="cuda")
+        d = mla.dims(1, 16, len(slots), mla.MLA_FP4_E2M1)
+        pg = mla.paging(64, calls[0].pages, len(free))
+        out = torch.empty_like(rows)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for c, s in zip(calls, streams):
+                with torch.cuda.stream(s):
+                    c.run()
+            with torch.cuda.stream(streams[2]):
+                mla.cache_append_paged(d, pg, rows, zero, slots, calls[0].dev["pool"])
+                mla.cache_read_paged(d, pg, calls[0].dev["pool"], table, i32_at(len(slots)),
+                                     i32_at(0, len(slots)), out)
+        torch.cuda.synchronize()
+        for c, (o, lse) in zip(calls, alone):
+            assert int(c.status.item()) == 0
+            assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+        x = f64(rows)
+        e = F.exponents(x[:, :D_C])
+        assert (f64(out)[:, :D_C] == F.latents(F.codes(x[:, :D_C], e), e)).all()
+    finally:
+        mla.load().mla_test_set_split_form(0)
+
+
+_KEPT = {}
+
+
+def i32_at(*x):
+    """Small constants on the GPU, made once: streams that run at once do not wait for copies."""
+    if x not in _KEPT:
+        _KEPT[x] = i32(list(x))
+    return _KEPT[x]
+
+
+@pytest.mark.parametrize("io,heads,q_len", [(BF16, 16, 1), (F32, 16, 3), (BF16, 64, 2)])
+def test_many_short_sequences(cuda_lib, io, heads, q_len):
+    """More sequences than are ever cut into shares, most of a page or less, some of none."""
+    B = 1500
+    c = Call(cuda_lib, np.arange(B) * 7 % 41, 16, io, heads, q_len, seed=11)
+    c.run().check(status=cuda_lib.MLA_DEV_LENGTH_OUT_OF_RANGE,       # those of none are reported
+                  tokens=[0, 1, 5 * q_len, 41 * q_len - 1, 700 * q_len, B * q_len - 1])
+    empty = torch.from_numpy(np.arange(B) * 7 % 41 == 0).cuda().repeat_interleave(q_len)
+    assert (c.o[empty] == 0).all() and torch.isneginf(c.lse[empty]).all()
+    assert torch.isfinite(c.o.float()).all()
+
+
+def test_read_with_starts_in_no_order(cuda_lib):
+    """Row starts that do not ascend: rows that belong to nobody may be anything, but nothing
+    behind the last start, or the block's end, is written."""
+    mla = cuda_lib
+    rng = np.random.RandomState(12)
+    pool, t, pages = _q4.make_pool(rng, [40, 25, 60], 16)
+    d, pg = mla.dims(3, 16, 64, mla.MLA_FP4_E2M1), mla.paging(16, pages, t.shape[1])
+    for starts, end in (([0, 90, 20, 70], 70), ([50, 10, 3, 0], 0), ([0, -5, 1 << 30, 100], 80),
+                        ([-(1 << 31), (1 << 31) - 1, 5, -3], 0)):
+        out = torch.full((100, ROW), 3.0, device="cuda")
+        mla.cache_read_paged(d, pg, pool.cuda(), t.cuda(), i32([40, 25, 60]),
+                             torch.tensor(starts, dtype=torch.int32, device="cuda"), out[:80],
+                             dev_status=status_word())
+        torch.cuda.synchronize()
+        assert (out[end:] == 3).all()
