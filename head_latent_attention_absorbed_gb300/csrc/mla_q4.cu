@@ -10,22 +10,82 @@ namespace {
 constexpr int kWarps = 8;
 
 // ------------------------------------------------------------- rows into slots
-// Bound by HBM: 576 values read, 400 bytes written per row.  A warp moves a row, as in
-// append_paged_kernel, kAppendEach rows' loads in flight; two lanes share a block of 16 latents,
-// so its largest magnitude is one exchange, and the exponents of a row's blocks are gathered into
-// words over half a warp.  62281 bf16 rows 20.4 us, 0.70 of the measured copy bandwidth.  (A grid
-// that the SMs hold at once, each warp with its next row's loads out while it writes one: 26.7.)
-constexpr int kAppendEach = 4, kAppendRows = kWarps * kAppendEach;
+// 576 values read, 400 bytes written per row: bound by HBM for fp32 rows, and for bf16 rows as much
+// by the instructions that quantise them.  A warp moves a row, as in append_paged_kernel,
+// kAppendEach rows' loads in flight; two lanes share a block of 16 latents, so its largest
+// magnitude is one exchange, and four a byte of exponents.  62281 rows: bf16 18.0 us, 0.79 of the
+// measured copy bandwidth, fp32 26.3, 0.94.  (Four rows a warp and eight warps a CTA, whose last
+// wave is long: fp32 30.4, 1000 bf16 rows 2.9 for 1.9.  bf16 values widened before they are
+// compared and scaled: 19.1.  A grid that the SMs hold at once, each warp with its next row's
+// loads out while it writes one: 26.7.)
+constexpr int kAppendEach = 2, kAppendWarps = 4, kAppendRows = kAppendWarps * kAppendEach;
 
-// e + 8 of the block whose largest magnitude has these fp32 bits (NaN counts above infinity:
-// both take the largest e).
-__device__ __forceinline__ uint32_t q4_exponent(uint32_t top) {
-  const int e = static_cast<int>(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 2 : 1);
-  return static_cast<uint32_t>(min(max(e, kQ4ExpMin), kQ4ExpMax) - kQ4ExpMin);
+// Eight values times 2^-e (exact), as codes: to nearest even, saturating at 6.
+__device__ __forceinline__ uint32_t q4_encode(const float* y) {
+  uint32_t code = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(y[2 * k], y[2 * k + 1]),
+                                                           __NV_E2M1, cudaRoundNearest)) << (8 * k);
+  return q4_page_word(code);
+}
+// A lane's 2 x 8 values of a row, of two blocks that it shares with its neighbour: their codes as
+// a page holds them, and (e + 5) mod 16 in a byte for each block.  A block's e is two below the
+// exponent of its largest magnitude, or one where the mantissa is above 7/4, between -8 and 6; as
+// integers, NaN counts above infinity, and both take the largest e.  (bf16: both blocks' magnitudes
+// and exponents in halves of a word.)
+__device__ __forceinline__ uint32_t q4_quantise(const Raw8bf16 (&x)[2], uint32_t* codes) {
+  constexpr uint32_t kAbs = 0x7fff7fffu, kOne = 0x00010001u;
+  uint32_t m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    m[i] = __vmaxu2(__vmaxu2(x[i].q.x & kAbs, x[i].q.y & kAbs),
+                    __vmaxu2(x[i].q.z & kAbs, x[i].q.w & kAbs));
+  uint32_t top = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const uint32_t e = (top + 0x1f * kOne) >> 7 & 0x1ff * kOne;   // 129 above the block's
+  constexpr uint32_t kLow = 129 + kQ4ExpMin, kSpan = kQ4ExpMax - kQ4ExpMin;
+  const uint32_t e8 = __vminu2(__vmaxu2(e, kLow * kOne) - kLow * kOne, kSpan * kOne);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t inv = (127 - kQ4ExpMin - (i == 0 ? e8 & 0xffffu : e8 >> 16)) * (kOne << 7);
+    const uint32_t w[4] = {x[i].q.x, x[i].q.y, x[i].q.z, x[i].q.w};
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&inv));
+      y[2 * k] = __low2float(p);
+      y[2 * k + 1] = __high2float(p);
+    }
+    codes[i] = q4_encode(y);
+  }
+  const uint32_t bits = (e8 + 13 * kOne) & 0xf * kOne;
+  return bits | bits >> 8;
+}
+__device__ __forceinline__ uint32_t q4_quantise(const Raw8f32 (&x)[2], uint32_t* codes) {
+  uint32_t exps = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float v[8];
+    x[i].values(v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const int e = static_cast<int>((top + 0x1fffffu) >> 23) - 129;
+    const int e8 = min(max(e, kQ4ExpMin), kQ4ExpMax) - kQ4ExpMin;
+    const float inv = __uint_as_float((127 - kQ4ExpMin - e8) << 23);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= inv;
+    codes[i] = q4_encode(v);
+    exps |= static_cast<uint32_t>((e8 + 13) & 15) << (8 * i);
+  }
+  return exps;
 }
 
 template <typename In>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kAppendWarps)
     append_q4_kernel(const In* __restrict__ rows, const int32_t* __restrict__ positions,
                      const int64_t* __restrict__ slots, uint8_t* __restrict__ pool,
                      const __grid_constant__ RopeTurns turns, int32_t* status, int n,
@@ -34,11 +94,11 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int r0 = blockIdx.x * kAppendRows + (threadIdx.x >> 5);
   int64_t slot[kAppendEach];
   int pos[kAppendEach];
-  Raw8<In> raw[kAppendEach][2];
+  std::conditional_t<std::is_same_v<In, float>, Raw8f32, Raw8bf16> raw[kAppendEach][2];
   float2 pair[kAppendEach];
 #pragma unroll
   for (int u = 0; u < kAppendEach; ++u) {
-    const int r = r0 + u * kWarps;
+    const int r = r0 + u * kAppendWarps;
     slot[u] = -1;
     pos[u] = 0;
     if (r < n) {
@@ -61,30 +121,15 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     const Q4Page<uint8_t> page(pool, static_cast<int>(slot[u] >> page_shift), page_shift);
     const int r = static_cast<int>(slot[u]) & ((1 << page_shift) - 1);
+    uint32_t codes[2], exps = q4_quantise(raw[u], codes);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float v[8];
-      raw[u][i].values(v);
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      const uint32_t e8 = q4_exponent(top);
-      const float inv = __uint_as_float((127 - kQ4ExpMin - e8) << 23);   // 2^-e: exact products
-      uint32_t code = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)   // to nearest even, saturating at 6
-        code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
-                    make_float2(v[2 * k] * inv, v[2 * k + 1] * inv), __NV_E2M1,
-                    cudaRoundNearest)) << (8 * k);
-      reinterpret_cast<uint32_t*>(page.codes(r))[32 * i + lane] = q4_page_word(code);
-      // (e + 5) mod 16
-      uint32_t word = (lane & 1) ? 0u : ((e8 + 13u) & 15u) << (4 * ((lane >> 1) & 7));
-#pragma unroll
-      for (int off = 2; off < 16; off <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, off);
-      if ((lane & 15) == 0)
-        reinterpret_cast<uint32_t*>(page.exps(r))[2 * i + (lane >> 4)] = word;
-    }
+    for (int i = 0; i < 2; ++i)
+      reinterpret_cast<uint32_t*>(page.codes(r))[32 * i + lane] = codes[i];
+    // Four lanes share a byte of exponents, two blocks', in each half of the row.
+    exps <<= 2 * (lane & 2);
+    exps |= __shfl_xor_sync(0xffffffffu, exps, 2);
+    if ((lane & 2) == 0)
+      page.exps(r)[8 * (lane & 1) + (lane >> 2)] = static_cast<uint8_t>(exps >> (8 * (lane & 1)));
     const float2 k = rotated(pair[u], pos[u], turn);
     *reinterpret_cast<uint32_t*>(page.keys + q4_key_at(r, lane)) = pack_bf16(k.x, k.y);
   }
@@ -395,7 +440,7 @@ mla_status append_q4(const char* who, const mla_paging* paging, int num_rows, bo
   const dim3 grid((num_rows - 1) / kAppendRows + 1);
   const int64_t pool = static_cast<int64_t>(paging->num_pages) * paging->page_size;
   auto go = [&](auto* in) {
-    append_q4_kernel<<<grid, 32 * kWarps, 0, s>>>(in, positions, slots,
+    append_q4_kernel<<<grid, 32 * kAppendWarps, 0, s>>>(in, positions, slots,
                                                   static_cast<uint8_t*>(cache), rope_turns(rope_base),
                                                   status, num_rows, pool, page_shift_of(paging));
   };
