@@ -2069,7 +2069,7 @@ __global__ void __launch_bounds__(128)
 
 // ------------------------------------------------------------------------- host side
 // Heads per CTA of the decode kernel: for a dense bf16 cache 64 or 32 where the head count
-// is a multiple, else 16 (the FP8 kernel always takes 16).
+// is a multiple, else 16 (the FP8 and 4-bit kernels always take 16).
 // A paged call's choice goes by its query type: bf16 queries are one part as they stand and
 // run as SM pairs (64 heads per CTA) from the sizes below; fp32 queries and outputs keep the
 // hi + lo pairs at every head count.
@@ -2089,7 +2089,7 @@ struct PlanOpts {
 // 32 rows 61 / 53, 48 88 / 56.  4-bit, 8 x 4096, 32 rows 16.6 / 19.6, 64 25.9 / 20.7; 64
 // sequences of 512 to 8192, 32 rows 75 / 84, 128 264 / 102.
 constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48, kPairMinFp4 = 48;
-// Tiles per CTA, were all sequences full, from which a paged FP8 cache is cut into equal
+// Tiles per CTA, were all sequences full, from which a paged FP8 or 4-bit cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
 // 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
 // full, 256 x 2048 75 / 73, 64 x 4096 40.8 / 40.9, 32 x 4096 (6.7) 24.6 / 25.4, 16 x 4096
@@ -2186,7 +2186,7 @@ namespace {
 //  - One CTA per chunk.  With `requested` = 0 the count minimises a makespan
 //    estimate (in units of cache rows): waves of CTAs over the SMs times (rows
 //    per chunk + a fixed per-CTA cost), plus the combine's cost per chunk.  The
-//    bf16 and FP8 kernels run one CTA per SM and work in 128-row tiles, and a
+//    bf16, FP8 and 4-bit kernels run one CTA per SM and work in 128-row tiles, and a
 //    chunk's partial last tile costs about what a full one does (measured: 16
 //    chunks of 256 rows beat 19 of 216 on 8 x 4096 rows), so for them a chunk's
 //    rows count rounded up to whole tiles.  Chunks are multiples of
@@ -2244,7 +2244,7 @@ SplitPlan plan_split_compute(const mla_dims* d, int requested, const PlanOpts& o
                              long long sms) {
   const int S = d->s_max;
   const bool pair = opts.pair;
-  const bool tiled = d->dtype != MLA_F32;   // bf16 and FP8 kernels: one CTA per SM
+  const bool tiled = d->dtype != MLA_F32;   // bf16, FP8 and 4-bit kernels: one CTA per SM
   const int np_align = opts.paged && tiled ? kTileRows : kChunkAlign;
   const int max_splits = (S + np_align - 1) / np_align;
   const long long groups = d->dtype == MLA_F32 ? d->heads : d->heads / tc_heads_per_cta(d, opts);

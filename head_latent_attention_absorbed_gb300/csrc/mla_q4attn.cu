@@ -33,6 +33,17 @@
 //   warps 12-19  codes to E4M3, two teams of four warps in turn
 // (A copy takes its warp some 450 cycles among the others' work: one warp for all of a
 // tile's, and exponents in a plane of their own, took 6600 cycles a tile.)
+//
+// What bounds it: a tile's way through its two buffers (codes to E4M3 0.6 us beyond what is done
+// before the wait for the buffer, score MMAs 0.6, softmax 1.1, output MMAs 0.9 and what lies
+// between), and the decoding warps, busy for nine tenths of a tile's 1.9 us, on a shared memory
+// that the tensor cores' reads (1440 of 3600 cycles), theirs (1300) and copies (400) keep busy; HBM
+// would allow 1.15.
+// 64 sequences of 512 to 8192 rows 41.4 us (2.7 TB/s of cache), 4 x 65536 rows 37.4, with an E4M3
+// cache, whose rows are longer and need no decoding, 43.4 and 38.8.  Not kept (us of those two):
+// four teams on 72 registers 44.7 / 40.6, the scores' operand in tensor memory, where the decoding
+// warps put it too, 42.5 / 38.8, boxes handed over one by one 41.5 / 37.7, all of a tile decoded
+// before the wait for its buffer 42.4 / 38.7.
 #include <type_traits>
 
 #include "mla_q4.cuh"

@@ -19,7 +19,7 @@ struct SplitParams {
   int tpc;                  // bf16 kernel, 32 columns: query groups per CTA (2: two tokens
                             // x 16 heads; 1: 32 heads of one token)
   float scale_log2;         // softmax_scale * log2(e)
-  uint8_t* q_img;           // FP8: the query's E4M3 image per (sequence, head group)
+  uint8_t* q_img;           // FP8 and 4-bit: the query's E4M3 image per (sequence, head group)
   int fill_early;           // bf16 kernel: issue tile 0's first boxes before the length
                             // is known (a one-wave grid)
   int persist;              // bf16 kernel, 16 heads per CTA: a persistent grid whose CTAs

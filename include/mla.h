@@ -34,6 +34,9 @@
  *    MLA_FP8_E4M3 the cache elements are one-byte FP8 E4M3 numbers, used as
  *    they are (no scale; "Multi-Head Latent Attention" 3.1: an element takes
  *    1-4 bytes, FP8 to FP32), and q_nope, q_rope and the weights are bf16.
+ *    MLA_FP4_E2M1 is a type of the paged cache alone ("4-bit pools" below):
+ *    the calls that take no paged cache refuse it, so the steps before and
+ *    after the attention are called with the dims of their own element type.
  *    Every result -- the absorbed query q_abs, the rotated q_pe, o_c, lse,
  *    the output o -- and the workspace are fp32 in every case (the bf16
  *    decode kernel feeds the fp32 query and the softmax weights to the
@@ -55,7 +58,7 @@
  *    inputs.  mla_absorb_q on its own starts as usual.
  *  - Supported sizes: d_c = 512, d_rope = 64, d_nope = 128, d_v = 128;
  *    batch >= 1; s_max >= 1; heads >= 1 (a multiple of 16 for MLA_BF16 and
- *    MLA_FP8_E4M3).
+ *    MLA_FP8_E4M3 and MLA_FP4_E2M1).
  *    Anything else returns MLA_ERR_UNSUPPORTED.
  */
 #ifndef MLA_GB300_H
@@ -615,11 +618,14 @@ mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
  *             head count.
  *   MLA_BF16  bf16 queries and outputs (bf16, FP8 and 4-bit caches), as a serving
  *             engine keeps them.  The query enters as it is.  From 32 (bf16 cache) or
- *             48 (FP8) query rows heads * q_len per sequence on, two CTAs on a pair of
- *             SMs take up to 128 of them, and P is one bf16 part (at most 2^-8
+ *             48 (FP8, 4-bit) query rows heads * q_len per sequence on, two CTAs on a pair
+ *             of SMs take up to 128 of them, and P is one bf16 part (at most 2^-8
  *             relative: less in the weighted sum than the output's own rounding), or
- *             with an FP8 cache an E4M3 part and its E5M2 remainder (2^-7); with fewer
- *             rows P is as for MLA_F32.  mla_set_split_parts(2) asks for that always.
+ *             with an FP8 or 4-bit cache an E4M3 part and its E5M2 remainder (2^-7); with
+ *             fewer rows P is as for MLA_F32, but over a 4-bit cache two E4M3 parts (2^-8,
+ *             and never finer than 2^-19 of the largest weight).  mla_set_split_parts(2)
+ *             asks for the form of fewer rows always.
+ * Over a 4-bit cache an fp32 query is four E4M3 parts and P three, as over an FP8 cache.
  * lse is fp32, accumulation fp32.
  *
  * q_abs [B*q_len, H, d_c], q_pe [B*q_len, H, d_rope], o_c [B*q_len, H, d_c]
@@ -629,7 +635,7 @@ mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
  * mla_paged_num_splits gives the chunk count used (0: invalid arguments).
  *
  * num_splits = 0 lets the library cut the rows.  For bf16 queries of 32 or more
- * rows and for FP8 caches, batches with enough rows are then cut into equal runs
+ * rows and for FP8 and 4-bit caches, batches with enough rows are then cut into equal runs
  * of 128-row tiles over all sequences, by the lengths that the kernels read: a
  * ragged batch keeps every SM busy to the end (mla_paged_num_splits gives the
  * most pieces that the workspace has room for).  Where a sequence is cut then
