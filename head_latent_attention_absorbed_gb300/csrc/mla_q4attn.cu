@@ -35,15 +35,15 @@
 // tile's, and exponents in a plane of their own, took 6600 cycles a tile.)
 //
 // What bounds it: a tile's way through its two buffers (codes to E4M3 0.6 us beyond what is done
-// before the wait for the buffer, score MMAs 0.6, softmax 1.1, output MMAs 0.9 and what lies
-// between), and the decoding warps, busy for nine tenths of a tile's 1.9 us, on a shared memory
-// that the tensor cores' reads (1440 of 3600 cycles), theirs (1300) and copies (400) keep busy; HBM
-// would allow 1.15.
-// 64 sequences of 512 to 8192 rows 41.4 us (2.7 TB/s of cache), 4 x 65536 rows 37.4, with an E4M3
-// cache, whose rows are longer and need no decoding, 43.4 and 38.8.  Not kept (us of those two):
-// four teams on 72 registers 44.7 / 40.6, the scores' operand in tensor memory, where the decoding
-// warps put it too, 42.5 / 38.8, boxes handed over one by one 41.5 / 37.7, all of a tile decoded
-// before the wait for its buffer 42.4 / 38.7.
+// before the wait for the buffer, score MMAs 0.6, softmax 0.9, output MMAs 0.9 and what lies
+// between), and the decoding warps, busy for nine tenths of a tile's 1.8 us, on a shared memory
+// that the tensor cores' reads (1440 of 3500 cycles), the threads' (1200) and copies (400) keep
+// busy; HBM would allow 1.15.
+// 64 sequences of 512 to 8192 rows 40.1 us (2.8 TB/s of cache), 4 x 65536 rows 36.5, with an E4M3
+// cache, whose rows are longer and need no decoding, 43.4 and 38.8.  Not kept (us of those two,
+// when they took 41.4 and 37.4): four teams on 72 registers 44.7 / 40.6, the scores' operand in
+// tensor memory, where the decoding warps put it too, 42.1 / 38.3, boxes handed over one by one
+// 41.5 / 37.7, all of a tile decoded before the wait for its buffer 42.4 / 38.7.
 #include <type_traits>
 
 #include "mla_q4.cuh"
@@ -737,14 +737,21 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         if (t >= 2) q4_warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
         {
           // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
-          // 16 part + n is part `part` of head n; the K index is the tile row.
+          // 16 part + n is part `part` of head n; the K index is the tile row.  Four
+          // heads of four rows are turned over among four lanes, to four rows of a head
+          // a word.  (Stored byte by byte: 64 sequences of 512 to 8192 rows 41.3 us, 256
+          // of 2048 73.5; 40.0 and 68.5 so.)
           uint8_t* pbuf = smem + L::kOffP + sb * L::kPBuf;
+          const uint32_t s1 = lane & 1 ? 0x3715u : 0x6240u, s2 = lane & 2 ? 0x3276u : 0x5410u;
 #pragma unroll
           for (int part = 0; part < L::kPParts; ++part)
 #pragma unroll
-            for (int h2 = 0; h2 < kHalf / 2; ++h2) {
-              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2, row)] = pp[part][h2] & 0xFF;
-              pbuf[sw128_byte(kHeadGroup * part + hb + 2 * h2 + 1, row)] = pp[part][h2] >> 8;
+            for (int h4 = 0; h4 < kHalf / 4; ++h4) {
+              uint32_t w = pp[part][2 * h4] | static_cast<uint32_t>(pp[part][2 * h4 + 1]) << 16;
+              w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), s1);
+              w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 2), s2);
+              *reinterpret_cast<uint32_t*>(
+                  pbuf + sw128_byte(kHeadGroup * part + hb + 4 * h4 + (lane & 3), row & ~3)) = w;
             }
         }
         fence_proxy_async_smem();
