@@ -144,11 +144,6 @@ struct Int {
   static constexpr int value = kN;
 };
 
-// Asks L2 for `bytes` bytes at `src` (16-byte units).
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // Where the rows of a page that does not exist come from.
 __device__ __align__(128) uint8_t g_q4_pair_zeros[Q4Pair::kSlotBytes];
 static_assert(Q4Pair::kKeyBytes <= Q4Pair::kSlotBytes, "zeros for either plane");
@@ -328,21 +323,16 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       ahead_r0 = then.r0 + (more ? i + 1 : 0) * kTileRows;
     };
     if (rows) {
-      // Two warps for the slots of the CTA's own half, one for both of the other half.
+      // Two warps for the slots of the CTA's own half, one for both of the other half.  (L2 asked
+      // for a tile's rows one tile before: 126 us against 125 for 32 x 16384 rows x 128 heads.)
       const bool own = warp != kWarpRows2 + 1;
       const int k0 = own && warp != kWarpRows ? 1 : 0, k1 = own ? k0 + 1 : 2;
       const int per = L::kSlotRows / piece, half = own ? rank : 1 - rank;
-      // A tile's sources, and the next one's.
-      const uint8_t* src = piece_source(ahead, ahead_r0);
       for_tiles([&](const TileItem& it, int i, int t) {
         if (given_up()) return false;
+        const uint8_t* src = piece_source(ahead, ahead_r0);
         const int live = live_of(ahead);
         look_ahead(it, i, t);
-        const uint8_t* then = piece_source(ahead, ahead_r0);
-        // The slots do not cover the way from HBM: L2 is asked for the next tile's own half.  (The
-        // other half has come with the other CTA's by the time it is copied.)
-        if (warp == kWarpRows && ahead >= 0 && ahead < p.num_pages && lane / (2 * per) == rank)
-          prefetch_l2(then, piece * bytes);
 #pragma unroll 1
         for (int k = k0; k < k1; ++k) {
           const int slot = (own ? 0 : 2) + k, from = (2 * half + k) * per;
@@ -353,7 +343,6 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           copy_pieces(src, from, from + per, live, piece * bytes,
                       sbase + L::kOffRaw + slot * L::kSlotBytes, bar(L::RAWFULL + slot));
         }
-        src = then;
         return true;
       });
     } else {
