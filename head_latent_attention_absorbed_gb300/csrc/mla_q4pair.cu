@@ -23,7 +23,7 @@
 // (32 x 16384 rows x 128 heads, earlier forms: 193 us with score boxes and output units apart, a
 // tile of each, and a warp for each; 172 with all warps on the one and then the other; 169 with
 // two tiles of units, decoded once and stored twice, where the one tile of score boxes made
-// decoding and the tensor cores take turns; 137 with all of it on the eight warps, 124 now.)
+// decoding and the tensor cores take turns; 137 with all of it on the eight warps.)
 // Of the keys, stored as the tensor core wants them, each CTA copies its 64 rows.  Nothing needs
 // cleaning behind a sequence's end: whatever bits a row holds, its latents are finite, and its
 // scores are not looked at.
@@ -40,7 +40,7 @@
 // tile's 2.0 us; and shared memory, of whose 3800 cycles in that time the tensor cores' reads take
 // 1900 (both parts of Q and of P against every row), codes, boxes and copies some 1300.  The
 // operations alone would take 1.4 us.
-// 32 x 16384 rows x 128 heads 124 us (1.68 TB/s of cache; E4M3 cache 104, bf16 128), 64 sequences
+// 32 x 16384 rows x 128 heads 123 us (1.70 TB/s of cache; E4M3 cache 105, bf16 129), 64 sequences
 // of 512 to 8192 rows 98.  A change of item takes 5 to 6 us, of which 4.8 are its result's way
 // through P; stored straight from registers, or 128 bytes of a row at a time, it takes no less.
 #include <cuda_fp8.h>
