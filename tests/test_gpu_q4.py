@@ -826,3 +826,29 @@ def test_read_with_starts_in_no_order(cuda_lib):
                              dev_status=status_word())
         torch.cuda.synchronize()
         assert (out[end:] == 3).all()
+
+
+@pytest.mark.parametrize("io,heads", [(BF16, 16), (F32, 16), (BF16, 128)])
+def test_plain_launches_and_the_other_form(cuda_lib, io, heads):
+    """Launches without overlap give the same bits; SM pairs asked for two parts run as CTAs of
+    16 heads, within the same bounds."""
+    mla = cuda_lib
+    c = Call(mla, [1, 640, 257, 2000], 64, io, heads, seed=13, s_max=2100, width=40)
+    c.run().check()
+    o, lse = c.o.clone(), c.lse.clone()
+    mla.set_launch_overlap(False)
+    try:
+        c.o.fill_(7)
+        c.run()
+        torch.cuda.synchronize()
+    finally:
+        mla.set_launch_overlap(True)
+    assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+    mla.set_split_parts(2)
+    try:
+        n = mla.paged_workspace_bytes(c.d, c.pg, io)
+        c.ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        c.o.fill_(7)
+        c.run().check()
+    finally:
+        mla.set_split_parts(0)
