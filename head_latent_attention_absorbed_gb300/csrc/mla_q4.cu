@@ -286,12 +286,14 @@ __global__ void __launch_bounds__(32 * kWarps)
 }
 
 // ------------------------------------------------------------- the page index
-// page_index_kernel's definition over 4-bit pages; a CTA per touched page, which looks at it
-// twice: its largest magnitude, of which the power of two above it is all that counts (and of
+// page_index_kernel's definition over 4-bit pages.  Items are the pages that each request's max_new
+// rows could touch; a CTA walks its share of them, looked up 32 at a time, and looks at a page that
+// was touched twice: its largest magnitude, of which the power of two above it is all that counts (and of
 // codes, their highest bits), then the sums.  A warp reads four of the page's rows together.
-// One touched page of 64 rows for each of 4 sequences 5.2 us, which is the way from the lengths
-// to the table to the rows and back; all 4096 pages of 4 x 65536 rows 64 us (1.6 TB/s: bound by
-// the codes' conversions and additions, a row at a time and both looks by value 80).
+// One touched page of 64 rows for each of 4 sequences 5.7 us, which is the way from the lengths
+// to the table to the rows and back; one for each of 256 that could have touched 32 9.2 (a CTA for
+// every page that could be touched: 16); all 4096 pages of 4 x 65536 rows 69 us (1.5 TB/s: bound
+// by the codes' conversions and additions; a CTA a page 64).
 // A latent is a multiple of 2^-9 and at most 384, so the maximum is a maximum of exact values.
 constexpr float kQ4Tiny = 1e-30f;
 constexpr int kIndexRows = 4;
@@ -299,113 +301,140 @@ __global__ void __launch_bounds__(32 * kWarps)
     page_index_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ table,
                          const int32_t* __restrict__ first_rows, const int32_t* __restrict__ lengths,
                          int8_t* codes, float* scales, int32_t* status, int page_shift,
-                         int table_stride, int num_pages, int max_new, int most) {
+                         int table_stride, int num_pages, int max_new, int most, int items) {
   __shared__ float tops[kWarps];
   __shared__ int sums[kWarps][kRow];
   __shared__ int peaks[kWarps];
-  const int b = static_cast<int>(blockIdx.x / most), jj = static_cast<int>(blockIdx.x % most);
+  __shared__ int ids[32], rows_of[32];
+  __shared__ uint32_t found;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int first = first_rows[b], len = lengths[b];
-  const bool bad = first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
-  if (tid == 0 && jj == 0 && (bad || static_cast<long long>(len) - first > max_new))
-    report(status, MLA_DEV_LENGTH_OUT_OF_RANGE);
-  const long long j = static_cast<long long>(first >> page_shift) + jj;
-  if (bad || first >= len || (j << page_shift) >= len) return;
-  const int n = static_cast<int>(min(1ll << page_shift, len - (j << page_shift)));
-  const int id = table[static_cast<size_t>(b) * table_stride + j];
-  if (id < 0 || id >= num_pages) {
-    if (tid == 0) report(status, MLA_DEV_PAGE_OUT_OF_RANGE);
-    return;
-  }
-  const Q4Page<const uint8_t> page(pool, id, page_shift);
-  constexpr int kBatch = kWarps * kIndexRows;
-  Q4Lane x[kIndexRows];   // rows r0 + warp, r0 + kWarps + warp, ..
-  auto load = [&](int r0) {
+  // One page of n rows, by the whole CTA.
+  auto page = [&](int id, int n) {
+    const Q4Page<const uint8_t> at(pool, id, page_shift);
+    constexpr int kBatch = kWarps * kIndexRows;
+    Q4Lane x[kIndexRows];   // rows r0 + warp, r0 + kWarps + warp, ..
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < kIndexRows; ++u) {
-      const int r = r0 + kWarps * u + warp;
-      if (r < n)
-        x[u].load(page, r, lane);
-      else
-        x[u].zero();   // adds nothing
-    }
-  };
-  float top = 0.f;
-  int high = -100;   // latents are below 2^high
-  for (int r0 = 0; r0 < n; r0 += kBatch) {
-    load(r0);
-#pragma unroll
-    for (int u = 0; u < kIndexRows; ++u) {
-      if (r0 + kWarps * u >= n) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) high = max(high, x[u].high(i, lane));
-      const float2 k = x[u].pair();
-      top = fmaxf(top, fmaxf(fabsf(k.x), fabsf(k.y)));
-    }
-  }
-  if (high > -100) top = fmaxf(top, ldexpf(0.5f, high));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
-  int ex = 0;
-  frexpf(top, &ex);   // top = m 2^ex, m in [0.5, 1)
-  const float unit = ldexpf(1.f, 20 - ex);
-  const bool live = top >= kQ4Tiny && top <= 3.0e38f;
-  constexpr float kMagic = 12582912.f;   // 1.5 2^23: the sum's low bits are the rounded integer
-  uint32_t sum[18], rows = 0;   // rows: those added, each with kMagic's bits
-#pragma unroll
-  for (int i = 0; i < 18; ++i) sum[i] = 0;
-  for (int r0 = 0; r0 < n; r0 += kBatch) {
-    if (n > kBatch) load(r0);
-#pragma unroll
-    for (int u = 0; u < kIndexRows; ++u) {
-      if (r0 + kWarps * u >= n) break;
-      ++rows;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v[8];
-        x[u].values(i, lane, v, unit);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[8 * i + k] += __float_as_uint(v[k] + kMagic);
+      for (int u = 0; u < kIndexRows; ++u) {
+        const int r = r0 + kWarps * u + warp;
+        if (r < n)
+          x[u].load(at, r, lane);
+        else
+          x[u].zero();   // adds nothing
       }
-      const float2 k = x[u].pair();
-      sum[16] += __float_as_uint(fmaf(k.x, unit, kMagic));
-      sum[17] += __float_as_uint(fmaf(k.y, unit, kMagic));
+    };
+    float top = 0.f;
+    int high = -100;   // latents are below 2^high
+    for (int r0 = 0; r0 < n; r0 += kBatch) {
+      load(r0);
+#pragma unroll
+      for (int u = 0; u < kIndexRows; ++u) {
+        if (r0 + kWarps * u >= n) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) high = max(high, x[u].high(i, lane));
+        const float2 k = x[u].pair();
+        top = fmaxf(top, fmaxf(fabsf(k.x), fabsf(k.y)));
+      }
     }
+    if (high > -100) top = fmaxf(top, ldexpf(0.5f, high));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+    int ex = 0;
+    frexpf(top, &ex);   // top = m 2^ex, m in [0.5, 1)
+    const float unit = ldexpf(1.f, 20 - ex);
+    const bool live = top >= kQ4Tiny && top <= 3.0e38f;
+    constexpr float kMagic = 12582912.f;   // 1.5 2^23: the sum's low bits are the rounded integer
+    uint32_t sum[18], rows = 0;   // rows: those added, each with kMagic's bits
+#pragma unroll
+    for (int i = 0; i < 18; ++i) sum[i] = 0;
+    for (int r0 = 0; r0 < n; r0 += kBatch) {
+      if (n > kBatch) load(r0);
+#pragma unroll
+      for (int u = 0; u < kIndexRows; ++u) {
+        if (r0 + kWarps * u >= n) break;
+        ++rows;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v[8];
+          x[u].values(i, lane, v, unit);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[8 * i + k] += __float_as_uint(v[k] + kMagic);
+        }
+        const float2 k = x[u].pair();
+        sum[16] += __float_as_uint(fmaf(k.x, unit, kMagic));
+        sum[17] += __float_as_uint(fmaf(k.y, unit, kMagic));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 18; ++i)
+      sums[warp][i < 16 ? 256 * (i >> 3) + 8 * lane + (i & 7) : kDc + 2 * lane + (i & 1)] =
+          static_cast<int>(sum[i] - rows * __float_as_uint(kMagic));
+    __syncthreads();
+    int total[3] = {0, 0, 0}, peak = 0;   // of columns tid, tid + 256 and tid + 512
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = tid + 32 * kWarps * i;
+      if (c < kRow)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) total[i] += sums[w][c];
+      peak = max(peak, abs(total[i]));
+    }
+    peak = __reduce_max_sync(0xffffffffu, peak);
+    if (lane == 0) peaks[warp] = peak;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) peak = max(peak, peaks[w]);
+    const bool good = live && peak > 0;
+    const float pf = static_cast<float>(peak), inv = good ? __frcp_rn(pf) * 127.f : 0.f;
+    int8_t* out = codes + static_cast<size_t>(id) * kRow;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = tid + 32 * kWarps * i;
+      if (c < kRow)
+        out[c] = good ? static_cast<int8_t>(__float2int_rn(static_cast<float>(total[i]) * inv)) : 0;
+    }
+    if (tid == 0)
+      scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
+    __syncthreads();   // before the next page's sums
+  };
+  for (long long base = blockIdx.x; base < items; base += 32ll * gridDim.x) {
+    // Lane l of the first warp looks item base + l * gridDim.x up.
+    if (warp == 0) {
+      const long long item = base + static_cast<long long>(lane) * gridDim.x;
+      int id = -1, n = 0;
+      if (item < items) {
+        const int b = static_cast<int>(item) / most, jj = static_cast<int>(item) % most;
+        const int first = first_rows[b], len = lengths[b];
+        const bool bad =
+            first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
+        if (jj == 0 && (bad || static_cast<long long>(len) - first > max_new))
+          report(status, MLA_DEV_LENGTH_OUT_OF_RANGE);
+        const long long j = static_cast<long long>(first >> page_shift) + jj;
+        if (!bad && first < len && (j << page_shift) < len) {
+          n = static_cast<int>(min(1ll << page_shift, len - (j << page_shift)));
+          id = table[static_cast<size_t>(b) * table_stride + j];
+          if (id < 0 || id >= num_pages) {
+            report(status, MLA_DEV_PAGE_OUT_OF_RANGE);
+            id = -1;
+          }
+        }
+      }
+      ids[lane] = id;
+      rows_of[lane] = n;
+      const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+      if (lane == 0) found = live;
+    }
+    __syncthreads();
+    for (uint32_t todo = found; todo; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      page(ids[l], rows_of[l]);
+    }
+    __syncthreads();   // before the next items are looked up
   }
-#pragma unroll
-  for (int i = 0; i < 18; ++i)
-    sums[warp][i < 16 ? 256 * (i >> 3) + 8 * lane + (i & 7) : kDc + 2 * lane + (i & 1)] =
-        static_cast<int>(sum[i] - rows * __float_as_uint(kMagic));
-  __syncthreads();
-  int total[3] = {0, 0, 0}, peak = 0;   // of columns tid, tid + 256 and tid + 512
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int c = tid + 32 * kWarps * i;
-    if (c < kRow)
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) total[i] += sums[w][c];
-    peak = max(peak, abs(total[i]));
-  }
-  peak = __reduce_max_sync(0xffffffffu, peak);
-  if (lane == 0) peaks[warp] = peak;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) peak = max(peak, peaks[w]);
-  const bool good = live && peak > 0;
-  const float pf = static_cast<float>(peak), inv = good ? __frcp_rn(pf) * 127.f : 0.f;
-  int8_t* out = codes + static_cast<size_t>(id) * kRow;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int c = tid + 32 * kWarps * i;
-    if (c < kRow)
-      out[c] = good ? static_cast<int8_t>(__float2int_rn(static_cast<float>(total[i]) * inv)) : 0;
-  }
-  if (tid == 0)
-    scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
 }
 
 int sm_count() {
@@ -460,9 +489,13 @@ mla_status page_index_q4(const char* who, const mla_paging* paging, int batch, i
     set_error("%s: batch=%d requests of up to %d touched pages exceed 2^31", who, batch, most);
     return MLA_ERR_UNSUPPORTED;
   }
-  page_index_q4_kernel<<<static_cast<unsigned>(items), 32 * kWarps, 0, s>>>(
-      static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes, scales, status,
-      page_shift_of(paging), paging->table_stride, paging->num_pages, max_new, most);
+  // As many as the SMs hold at once, but an odd number: where every request touches its first page
+  // alone, those are `most` items apart, often a power of two, and have to come to different CTAs.
+  const long long most_ctas = 4ll * sm_count() - 1;
+  page_index_q4_kernel<<<static_cast<unsigned>(items < most_ctas ? items : most_ctas), 32 * kWarps, 0,
+                         s>>>(static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes,
+                              scales, status, page_shift_of(paging), paging->table_stride,
+                              paging->num_pages, max_new, most, static_cast<int>(items));
   return launch_status(who);
 }
 

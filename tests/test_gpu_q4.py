@@ -321,6 +321,30 @@ def test_index_of_every_value(cuda_lib):
     assert got_s[-1] == 0 and (got_c[-1] == 0).all()
 
 
+def test_index_of_many_requests(cuda_lib):
+    """More pages that could be touched than the kernel looks up at once, few that are."""
+    mla = cuda_lib
+    rng = np.random.RandomState(5)
+    B, page, width = 700, 16, 34
+    lengths = rng.randint(0, 60, B)
+    pool, table, pages = _q4.make_pool(rng, lengths, page, width=width)
+    val = _q4.values(pool.numpy(), page)
+    first = np.maximum(lengths - rng.randint(0, 3, B), 0)
+    d, pg = mla.dims(B, 16, width * page, mla.MLA_FP4_E2M1), mla.paging(page, pages, width)
+    codes = torch.full((pages, ROW), 77, dtype=torch.int8, device="cuda")
+    scales, status = torch.full((pages,), 7.0, device="cuda"), status_word()
+    mla.page_index(d, pg, pool.cuda(), table.cuda(), i32(first), i32(lengths), width * page, codes, scales,
+                   dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    want_c, want_s = np.full((pages, ROW), 77, np.int8), np.full(pages, 7.0, np.float32)
+    for b, n in enumerate(lengths):
+        for j in range(first[b] // page, -(-int(n) // page)) if first[b] < n else ():
+            i = int(table[b, j])
+            want_c[i], want_s[i] = PO.page_index(val[i][:min(page, n - j * page)])
+    assert (codes.cpu().numpy() == want_c).all() and (scales.cpu().numpy() == want_s).all()
+
+
 def test_index_reports(cuda_lib):
     mla = cuda_lib
     pool, table, pages = _q4.make_pool(np.random.RandomState(0), [40, 20], 16)
