@@ -590,7 +590,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           // warp's share of O.
           float up = mx - L::kBias;
           up = t > t0 ? fmaxf(up, 0.f) : mx == -INFINITY ? 0.f : up;
-          const float alpha = ex2(-up);
+          // (nothing is summed before the first tile, whose reference may go down past what
+          // 2^-up can hold)
+          const float alpha = t > t0 ? ex2(-up) : 0.f;
           m += up;
           l *= alpha;
 #pragma unroll
