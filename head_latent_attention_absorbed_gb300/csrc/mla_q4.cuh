@@ -118,18 +118,6 @@ struct Q4Lane {
   }
 };
 
-// Whether `x` holds for any of `count` threads (named barrier `bar`).
-__device__ __forceinline__ bool any_of(bool x, int bar, int count) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(bar), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
 // Waits for a phase, bounded: gives up, raising the CTA's abort flag, after the library's limit.
 // The warp is suspended for up to kSuspendNs at a time: so many warps of these kernels wait that
 // their polling would take issue slots from the others.

@@ -782,8 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
       q4_warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
-      named_bar_sync(3 + gp, kSoft / 2);
-      if (!*abort_flag) {
+      // (asked for all of the group: the flag may be raised at any time)
+      if (!any_of(*abort_flag, 3 + gp, kSoft / 2)) {
         const size_t base = (size_t(out.v) * p.H + h0) * p.splits + out.j;
         // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
         // here, 1 <= L <= 2^8 x rows), branch-free; lane h of the first warp of

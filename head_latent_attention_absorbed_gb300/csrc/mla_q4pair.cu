@@ -674,8 +674,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 2 * kSlices; ++i) sum += red[i * 32 + lane];
-      named_bar_sync(5, L::kSoft);   // read before P is written again
-      if (!*abort_flag) {
+      // Read before P is written again.  Whether the CTA has given up is asked here for all: some
+      // warp may raise the flag at any time, and the softmax warps meet at a barrier below.
+      if (!any_of(*abort_flag, 5, L::kSoft)) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const bool whole = kShare ? whole_set(it) : p.direct != 0;   // the result itself
         const size_t stride = whole ? 1 : p.splits;
