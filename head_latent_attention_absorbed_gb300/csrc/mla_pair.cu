@@ -643,8 +643,9 @@ __global__ void __launch_bounds__(kShare ? PairPlan<kFp8>::kShareThreads
       sums[part_of * kPHeads + head] = l;
       warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
-      named_bar_sync(1, L::kSoft);
-      if (!*abort_flag) {
+      // Whether the CTA has given up is asked for all: some warp may raise the flag at any time,
+      // and the softmax warps meet at a barrier below.
+      if (!any_of(*abort_flag, 1, L::kSoft)) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * kSlices; ++i) sum += sums[i * kPHeads + head];
