@@ -60,6 +60,9 @@ constexpr int kSoft = 256;
 constexpr int kTeam = 128, kTeams = 2;        // threads of a decoding team, and teams
 constexpr int kThreads = kSoft + 4 * 32 + kTeams * kTeam;
 constexpr int kHalf = kHeadGroup / 2;         // heads per softmax warp group
+// The softmax's reference before a head's first score: finite, so that scores of -infinity have no
+// weight there either, and below any other.
+constexpr float kNoRef = -3e38f;
 constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64, O^T from 128 to 319, Sk[2] at 320 / 352
 constexpr uint32_t kOCol = 128, kKCol = 320;
 
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       float m[kHalf], l[kHalf];
 #pragma unroll
       for (int h = 0; h < kHalf; ++h) {
-        m[h] = -INFINITY;
+        m[h] = kNoRef;
         l[h] = 0.f;
       }
       for (int t = t0; t < t0 + tiles; ++t) {
@@ -676,10 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
             const float4 q4 = *reinterpret_cast<const float4*>(red + (hb + h) * 4);
-            // (finite even where every score is -infinity)
-            const float mn = fmaxf(fmaxf(m[h], -1e30f),
-                                   fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
-            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn);
+            const float mn =
+                fmaxf(m[h], fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
+            alpha[h] = ex2(m[h] - mn);
             m[h] = mn;
             l[h] *= alpha[h];
           }

@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       // Rows from this thread's first on that its head's token attends: one before the last
       // token sees fewer.
       const int limit = min(tiles * kTileRows, it.len - back - it.r0) - row0 + t0 * kTileRows;
-      float m = 0.f, l = 0.f;   // m is set by the item's first tile
+      float m = 0.f, l = 0.f;
+      bool fresh = true;   // no score but -infinity so far: m is set by the first other
       // A wait that gives up leaves the loop running (every later wait then returns at
       // once), so that all softmax warps meet at the same barriers.
       for (int t = t0; t < t0 + tiles; ++t) {
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
         for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
         // The eight warps of the same heads go by one reference, and decide alike.
-        if (any_of(t == t0 || mx > L::kBias + L::kGrow, 1 + (qd & 1), L::kSoft / 2)) {
+        if (any_of(fresh || mx > L::kBias + L::kGrow, 1 + (qd & 1), L::kSoft / 2)) {
           if (t > t0) {   // P and O: the output product of the tile before is done
             q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
@@ -585,14 +586,14 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
           for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, red[i * 32 + lane]);
           named_bar_sync(3 + (qd & 1), L::kSoft / 2);   // read before any P is written
-          // Move the reference (up, but to wherever the first tile has it; a head whose token
-          // attends none of its rows attends none of the item's); rescale the sum and this
-          // warp's share of O.
+          // Move the reference (up, but to wherever its first tile has it); rescale the sum and
+          // this warp's share of O.
           float up = mx - L::kBias;
-          up = t > t0 ? fmaxf(up, 0.f) : mx == -INFINITY ? 0.f : up;
+          up = !fresh ? fmaxf(up, 0.f) : mx == -INFINITY ? 0.f : up;
           // (nothing is summed before the first tile, whose reference may go down past what
           // 2^-up can hold)
-          const float alpha = t > t0 ? ex2(-up) : 0.f;
+          const float alpha = fresh ? 0.f : ex2(-up);
+          fresh = fresh && mx == -INFINITY;
           m += up;
           l *= alpha;
 #pragma unroll

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import _q4
-from _paged import ROW, SCALE, f64
+from _paged import D_C, ROW, SCALE, f64
 from _q4_far import BF16, F32, i32, shifted
 from oracle import paged_oracle as PO
 
@@ -85,3 +85,29 @@ def test_sparse_tokens_and_far_scores(cuda_lib, io, heads, q_len, shift):
     first = c.o.clone()
     run()
     assert torch.equal(first, c.o)
+
+
+@pytest.mark.parametrize("form", [0, 1, "one chunk"])
+@pytest.mark.parametrize("heads", [16, 48, 128])
+def test_infinite_keys(cuda_lib, heads, form):
+    """Rows whose score is -infinity weigh nothing, a whole first tile of them and single ones."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(1 if form == 1 else 0)
+    try:
+        rng = np.random.RandomState(heads)
+        shifts = [np.zeros(400), np.full(300, -200.0), np.zeros(130)]
+        shifts[0][:128] = shifts[0][200] = shifts[0][399] = -np.inf
+        shifts[1][:256] = shifts[2][::2] = -np.inf
+        c = shifted(rng, mla, shifts, heads, BF16, splits=1 if form == "one chunk" else 0).run()
+        for b, s in enumerate(shifts):
+            live = np.isfinite(s)
+            pages = _q4.values(c.pool.numpy(), c.page)[c.table[b, :-(-len(s) // c.page)]]
+            rows = pages.reshape(-1, ROW)[:len(s)][live]
+            q = np.concatenate([f64(c.q_abs), f64(c.q_pe)], 2)[b]
+            want, want_lse, p, z = PO.attend(q, rows, SCALE, D_C)
+            do, dl = _q4.bounds(q, rows, p, z, BF16, heads, 1)
+            do = do + 2.0 ** -8 * (np.abs(want) + do)
+            assert (np.abs(f64(c.o)[b] - want) <= do).all()
+            assert (np.abs(f64(c.lse)[b] - want_lse) <= dl + 2.0 ** -22 * np.abs(want_lse)).all()
+    finally:
+        mla.load().mla_test_set_split_form(0)
