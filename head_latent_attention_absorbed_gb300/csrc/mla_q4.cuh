@@ -204,6 +204,35 @@ struct Q4Piece {
   }
 };
 
+// ------------------------------------------------------------- softmax references
+// A head's weights are 2^(score - reference) and enter the output product as parts of eight bits,
+// which hold a weight to a share of it but for their smallest step: a tile's 128 rows may lose up
+// to d = 2^-7 together (two parts; three 2^-11).  With a reference that only rises with the maximum
+// the many rows that one far above them outweighs are lost so, however much they weigh together.
+// So it also goes down: a look at the sum of a head's weights, tiles apart, finds whether the sum is
+// below four for each tile so far, and then lowers the reference to where the tile at hand has its
+// largest weight.  How many tiles the sum bears until the next look follows from the sum; a move to
+// a tile's maximum, which adds 2^4 or more, bears kBearsTiles.  So each d comes with 1 to 4 of the
+// sum, or with octaves that a move adds to it: over 512 tiles some two d of the sum are lost at
+// most.  Looks are few, and so are moves, by which O is rescaled.  (With the weights of every tile
+// looked at, 32 x 16384 rows x 128 heads whose scores spread by 2 nats take 159 us for 134.)
+constexpr float kNoRef = -3e38f;   // before a head's first score: below any, but finite, so that
+                                   // scores of -infinity have no weight there either
+constexpr float kSpan = 40.f;      // how far below the highest it was a reference may go: the rows
+                                   // of a tile that lies further down count for nothing
+constexpr float kPerTile = 4.f;
+constexpr int kBearsTiles = 16;
+// How low a look lets the reference go; drop: how far it lies below the highest it was, sum: of the
+// weights of the `done` tiles before.
+__device__ __forceinline__ float q4_floor(float sum, int done, float ref, float drop) {
+  return sum < kPerTile * static_cast<float>(done + kBearsTiles) ? ref + (drop - kSpan) : ref;
+}
+// Tiles until the next look.
+__device__ __forceinline__ int q4_bears(float sum, int done, float drop) {
+  if (drop >= kSpan - 1.f) return 1 << 20;
+  return max(static_cast<int>(fminf(sum * (1.f / kPerTile), 1e6f)) - done, kBearsTiles);
+}
+
 __device__ __forceinline__ void bulk_g2s_elected(uint32_t dst, const void* src, uint32_t bytes,
                                                  uint32_t bar, uint64_t policy) {
   asm volatile(

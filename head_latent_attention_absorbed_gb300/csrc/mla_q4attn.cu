@@ -14,9 +14,10 @@
 // A bf16 query is two E4M3 parts (weights 1, 1/16; exact to 2^-21 of the head's largest
 // value) in units of a power of two per head, and P two parts (at most 2^-8 relative, less in
 // the weighted sum than the bf16 output's own rounding); an fp32 query is four parts, its key
-// part a bf16 hi and lo, and P three.  With two parts of P the softmax's reference stays 2^5
-// below the running maximum, so that the smallest step is 2^-19 of the largest weight, and O
-// is rescaled when a maximum passes it by 2^3.5.
+// part a bf16 hi and lo, and P three (2^-12).  The parts' smallest step is 2^-13 (three: 2^-17)
+// of the softmax's reference, which therefore follows the scores up and down (mla_q4.cuh): it lies
+// 2^5 below the largest score of the tile where it last moved, and goes up, rescaling O, when a
+// score passes it by 2^8.5.
 //
 // From codes to E4M3: a byte permute looks the eight magnitudes of a block's exponent up in
 // two registers, four codes at a time (the selector is the codes themselves), and the signs
@@ -60,9 +61,6 @@ constexpr int kSoft = 256;
 constexpr int kTeam = 128, kTeams = 2;        // threads of a decoding team, and teams
 constexpr int kThreads = kSoft + 4 * 32 + kTeams * kTeam;
 constexpr int kHalf = kHeadGroup / 2;         // heads per softmax warp group
-// The softmax's reference before a head's first score: finite, so that scores of -infinity have no
-// weight there either, and below any other.
-constexpr float kNoRef = -3e38f;
 constexpr uint32_t kTmemCols = 512;   // S[2] at 0 / 64, O^T from 128 to 319, Sk[2] at 320 / 352
 constexpr uint32_t kOCol = 128, kKCol = 320;
 
@@ -75,9 +73,10 @@ struct Q4Plan {
   static constexpr int kPParts = kF32 ? 3 : 2;
   static constexpr int kPN = kPParts * kHeadGroup;   // P rows of the PV MMA (part-major)
   static constexpr int kPBuf = kPN * 128;            // of 128 tile rows
-  // Reference of the softmax below the running maximum, and how far above the reference a
-  // score may lie (log2): weights stay below E4M3's 448.
-  static constexpr float kBias = kF32 ? 0.f : 5.f, kTop = kF32 ? 8.f : 8.5f;
+  // Where the softmax's reference goes below a tile's largest score when it moves, and how far
+  // above the reference that score may then lie in later tiles (log2): weights stay below E4M3's
+  // 448.
+  static constexpr float kBias = 5.f, kTop = 8.5f;
   static constexpr int kQN = kQParts * kHeadGroup, kKN = kKParts * kHeadGroup;
   static constexpr int kQBox = kQN * 128;
   static constexpr int kQKeys = 4 * kQBox;                  // offset of the key part
@@ -156,6 +155,28 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
 // 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128_byte(int n, int k) {
   return static_cast<uint32_t>(n * 128 + ((((k >> 4) ^ n) & 7) << 4) + (k & 15));
+}
+
+// Of eight values a lane, over a warp's lanes: lane i's result is that of value i mod 8.  (Halves
+// of the values go to and fro: nine exchanges, where a value at a time would take 40.)
+template <typename Op>
+__device__ __forceinline__ float over_lanes(const float (&v)[kHalf], int lane, Op op) {
+  static_assert(kHalf == 8, "three steps");
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float send = lane & 1 ? v[2 * i] : v[2 * i + 1], keep = lane & 1 ? v[2 * i + 1] : v[2 * i];
+    a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 1));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float send = lane & 2 ? a[2 * i] : a[2 * i + 1], keep = lane & 2 ? a[2 * i + 1] : a[2 * i];
+    b[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+  }
+  const float send = lane & 4 ? b[0] : b[1], keep = lane & 4 ? b[1] : b[0];
+  float r = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+  r = op(r, __shfl_xor_sync(0xffffffffu, r, 8));
+  return op(r, __shfl_xor_sync(0xffffffffu, r, 16));
 }
 
 // Where the rows of a page that does not exist come from.
@@ -611,6 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       const int end = kShare ? cur.len : row_end;
       const int last_valid = min(end - (cur.r0 + (tiles - 1) * kRowsT), kRowsT);
       float m[kHalf], l[kHalf];
+      float ref = kNoRef, drop = 0.f;   // lane h: m[h], and how far it lies below the highest it was
+      int due = t0 + kBearsTiles;       // the next look
 #pragma unroll
       for (int h = 0; h < kHalf; ++h) {
         m[h] = kNoRef;
@@ -653,39 +676,46 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             for (int h = 0; h < kHalf; ++h) d[h] = -INFINITY;
         };
         above();
-        bool need = false;
+        bool need = t == due;
 #pragma unroll
         for (int h = 0; h < kHalf; ++h) need |= d[h] > L::kTop;
         if (any_of(need, 1 + gp, kSoft / 2)) {
-          // Some score is too far above its head's reference: the tile's maxima (warp, then
-          // the group's four warps) move the references of this group's heads; rescale its row
-          // sums and the O^T columns it owns (in TMEM, after the previous PV finished).
-          float tt[kHalf];
-#pragma unroll
-          for (int h = 0; h < kHalf; ++h) {
-            tt[h] = row < valid ? x[h] * qsig[h] : -INFINITY;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-              tt[h] = fmaxf(tt[h], __shfl_xor_sync(0xffffffffu, tt[h], off));
-          }
-          if (lane < kHalf) {
-            float v = tt[0];
-#pragma unroll
-            for (int h = 1; h < kHalf; ++h) v = lane == h ? tt[h] : v;
-            red[(hb + lane) * 4 + wq] = v;
-          }
-          named_bar_sync(3 + gp, kSoft / 2);
+          // Some score is too far above its head's reference, or a look at the sums is due: the
+          // tile's maxima (of a warp, then of the group's four) move the references of this
+          // group's heads, lane h (and h + 8 ..) head h's; rescale its row sums and the O^T columns
+          // it owns (in TMEM, after the previous PV finished).
           float alpha[kHalf];
 #pragma unroll
+          for (int h = 0; h < kHalf; ++h) alpha[h] = row < valid ? x[h] * qsig[h] : -INFINITY;
+          float top = over_lanes(alpha, lane, [](float a, float b) { return fmaxf(a, b); });
+          const int mine = hb + (lane & (kHalf - 1));
+          if (lane < kHalf) red[mine * 4 + wq] = top;
+          if (t == due) {
+            const float sum = over_lanes(l, lane, [](float a, float b) { return a + b; });
+            if (lane < kHalf) lsum[mine * 4 + wq] = sum;
+          }
+          named_bar_sync(3 + gp, kSoft / 2);
+          const float4 t4 = *reinterpret_cast<const float4*>(red + mine * 4);
+          top = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)) - L::kBias;
+          float mn = fmaxf(top, ref), sum = 0.f;
+          if (t == due) {
+            const float4 s4 = *reinterpret_cast<const float4*>(lsum + mine * 4);
+            sum = (s4.x + s4.y) + (s4.z + s4.w);
+            mn = fmaxf(top, q4_floor(sum, t - t0, ref, drop));
+          }
+          const float al = ex2(ref - mn);
+          drop = fmaxf(drop + (ref - mn), 0.f);
+          ref = mn;
+          due = t == due ? t + __reduce_min_sync(0xffffffffu, q4_bears(sum * al, t - t0, drop))
+                         : min(due, t + kBearsTiles);
+          const bool moved = __any_sync(0xffffffffu, al != 1.f);
+#pragma unroll
           for (int h = 0; h < kHalf; ++h) {
-            const float4 q4 = *reinterpret_cast<const float4*>(red + (hb + h) * 4);
-            const float mn =
-                fmaxf(m[h], fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - L::kBias);
-            alpha[h] = ex2(m[h] - mn);
-            m[h] = mn;
+            m[h] = __shfl_sync(0xffffffffu, ref, h);
+            alpha[h] = __shfl_sync(0xffffffffu, al, h);
             l[h] *= alpha[h];
           }
-          if (t > t0) {
+          if (t > t0 && moved) {
             q4_warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
 #pragma unroll
@@ -766,15 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       // The combine may start launching: it waits for this grid anyway.
       if (tid == 0 && t0 == T) pdl_launch_dependents();
       // Softmax denominators over the chunk's rows.
-#pragma unroll
-      for (int h = 0; h < kHalf; ++h)
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-      if (lane < kHalf) {
-        float v = l[0];
-#pragma unroll
-        for (int h = 1; h < kHalf; ++h) v = lane == h ? l[h] : v;
-        lsum[(hb + lane) * 4 + wq] = v;
+      {
+        const float sum = over_lanes(l, lane, [](float a, float b) { return a + b; });
+        if (lane < kHalf) lsum[(hb + lane) * 4 + wq] = sum;
       }
       const TileItem out = cur;
       if (kShare && t0 < T) {   // fetched while the last PV runs
@@ -788,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (!any_of(*abort_flag, 3 + gp, kSoft / 2)) {
         const size_t base = (size_t(out.v) * p.H + h0) * p.splits + out.j;
         // 1/L by the approximate reciprocal (within 2 ulp for the L > 0 reached
-        // here, 1 <= L <= 2^8 x rows), branch-free; lane h of the first warp of
+        // here, at most 2^(kTop + kSpan) x rows), branch-free; lane h of the first warp of
         // each group writes head h's log-sum-exp.
         float inv[kHalf], Lme = 0.f, mme = 0.f;
 #pragma unroll

@@ -622,11 +622,17 @@ mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
  *             of SMs take up to 128 of them, and P is one bf16 part (at most 2^-8
  *             relative: less in the weighted sum than the output's own rounding), or
  *             with an FP8 or 4-bit cache an E4M3 part and its E5M2 remainder (2^-7); with
- *             fewer rows P is as for MLA_F32, but over a 4-bit cache two E4M3 parts (2^-8,
- *             and never finer than 2^-19 of the largest weight).  mla_set_split_parts(2)
- *             asks for the form of fewer rows always.
- * Over a 4-bit cache an fp32 query is four E4M3 parts and P three, as over an FP8 cache.
+ *             fewer rows P is as for MLA_F32, but over a 4-bit cache two E4M3 parts (2^-8).
+ *             mla_set_split_parts(2) asks for the form of fewer rows always.
+ * Over a 4-bit cache an fp32 query is four E4M3 parts and P three (2^-12), as over an FP8 cache.
  * lse is fp32, accumulation fp32.
+ * These shares are of each weight.  The parts also have a smallest step, with which weights far
+ * below the largest one are rounded or lost.  Over an FP8 cache it goes by the largest weight, so
+ * that what it takes adds up with the rows, and so over a 4-bit cache from 48 bf16 query rows on
+ * (2^-17 of the largest weight).  With fewer, or fp32 queries, the parts' unit follows the scores,
+ * up and down: of a piece of up to 65536 rows at most 1/60 of the sum of the weights (fp32 queries:
+ * 1/1200) is lost beyond those shares, whatever the largest weight and however many rows the rest
+ * is spread over.  Rows 2^-40 or more below others may count for nothing.
  *
  * q_abs [B*q_len, H, d_c], q_pe [B*q_len, H, d_rope], o_c [B*q_len, H, d_c]
  * (out) io_dtype; lse [B*q_len, H] fp32 (out, may be NULL); lengths [B] int32;
