@@ -9,7 +9,8 @@
 //   output  O[128 x 512] += P[128 x 128 rows] . C[128 x 512]
 //                                                       CTA i: 256 of the latent columns
 // Queries are two E4M3 parts in units of a power of two per head (their keys' part bf16, and
-// so S1 has no unit), P an E4M3 part and its E5M2 remainder.
+// so S1 has no unit), P an E4M3 part and its E5M2 remainder, whose unit follows the scores up and
+// down (mla_q4.cuh).
 //
 // What differs is where the operands come from.  A tile's codes and exponents pass through both
 // CTAs as they are stored, 32 rows at a time, and become E4M3 boxes of 64 rows x 128 columns.  A
@@ -81,11 +82,12 @@ struct Q4Pair {
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffSlot + 8;
   static constexpr int kOffShare = kOffAbort + 8;       // TileShare of the pair
-  static constexpr size_t kSmem = kOffShare + 24;
+  static constexpr int kOffDrop = kOffShare + 24;       // [64 heads], see the softmax
+  static constexpr size_t kSmem = kOffDrop + 64 * 4;
   static constexpr uint32_t kOCol = 256;
-  // Reference of the softmax below the running maximum, and how far a maximum may pass it
-  // before O is rescaled (log2): weights stay in [0, 2^8.5].
-  static constexpr float kBias = 3.f, kGrow = 5.5f;
+  // Where the softmax's reference goes below a tile's largest score when it moves, and how far
+  // above the reference that score may then lie in later tiles (log2): weights stay in [0, 2^8.5].
+  static constexpr float kBias = 4.f, kTop = 8.5f;
   static constexpr int kStageRow = kDc * 4 + 16;        // epilogue staging, over the operands
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kOffRaw >= kPHeads * kStageRow, "epilogue staging");
@@ -93,7 +95,7 @@ struct Q4Pair {
   // reads it; the eight warps of the same heads keep to those heads' rows of it: 32 rows of each
   // part, part 0 first.
   static_assert(kPBufBytes == kSoftWarps * 32 * 32, "an item's output through P");
-  static_assert(2 * kSlices * 32 * 4 <= 4096, "the maxima of 32 heads through P");
+  static_assert(2 * 2 * kSlices * 32 * 4 <= 4096, "the maxima and sums of 32 heads through P");
   static_assert(kOffC % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kOffRaw % 16 == 0 && kOffBar % 8 == 0, "alignment");
 };
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     const int part_of = kSlices * (qd >> 1) + hh;   // which part of the tile's rows
     // The rows of P of the warp's heads: 32 of each part.
     uint8_t* mine_p = smem + L::kOffP + 4096 * (qd & 1);
-    float* red = reinterpret_cast<float*>(mine_p);   // [2 kSlices][32 heads]
+    float* red = reinterpret_cast<float*>(mine_p);   // [2 kSlices][32 heads], two of them
     // A tile's boxes again: 32 of the other CTA's rows (slot), 32 columns (piece c) of box 2 j +
     // rank, into box 2 j + 1 - rank; a row per lane, as the decoding warps.
     const int slot = 2 + (warp >> 3), c = warp & 3, j = (warp >> 2) & 1;
@@ -537,6 +539,9 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     uint8_t* box = smem + L::kOffC + (2 * j + 1 - rank) * kPBox +
                    (warp >> 3) * (L::kSlotRows * 128) + lane * 128;
     const uint32_t box_at = (2 * c << 4) ^ ((lane & 7) << 4);
+    // How far the head's reference lies below the highest it was: written by the first of the eight
+    // warps, behind the barriers between which all read it.
+    float* drop_at = reinterpret_cast<float*>(smem + L::kOffDrop) + head;
     const int back = p.q_len - 1 - (first + min(head, mine - 1)) / p.H;   // tokens behind its own
     const float scale = p.scale_log2;
     TileItem it = item0;
@@ -548,6 +553,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       const int limit = min(tiles * kTileRows, it.len - back - it.r0) - row0 + t0 * kTileRows;
       float m = 0.f, l = 0.f;
       bool fresh = true;   // no score but -infinity so far: m is set by the first other
+      int due = t0 + kBearsTiles;   // the next look at the sums
       // A wait that gives up leaves the loop running (every later wait then returns at
       // once), so that all softmax warps meet at the same barriers.
       for (int t = t0; t < t0 + tiles; ++t) {
@@ -575,30 +581,44 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
 #pragma unroll
         for (int i = 1; i < kCols; ++i) mx = fmaxf(mx, x[i]);
         // The eight warps of the same heads go by one reference, and decide alike.
-        if (any_of(fresh || mx > L::kBias + L::kGrow, 1 + (qd & 1), L::kSoft / 2)) {
+        if (any_of(fresh || mx > L::kTop || t == due, 1 + (qd & 1), L::kSoft / 2)) {
           if (t > t0) {   // P and O: the output product of the tile before is done
             q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
           }
           red[part_of * 32 + lane] = mx;
+          if (t == due) red[(2 * kSlices + part_of) * 32 + lane] = l;
           named_bar_sync(3 + (qd & 1), L::kSoft / 2);
           mx = red[lane];
 #pragma unroll
           for (int i = 1; i < 2 * kSlices; ++i) mx = fmaxf(mx, red[i * 32 + lane]);
+          const float was = fresh ? 0.f : *drop_at;
+          float low = 0.f, sum = 0.f;
+          if (t == due) {
+#pragma unroll 1
+            for (int i = 0; i < 2 * kSlices; ++i) sum += red[(2 * kSlices + i) * 32 + lane];
+            low = q4_floor(sum, t - t0, 0.f, was);
+          }
           named_bar_sync(3 + (qd & 1), L::kSoft / 2);   // read before any P is written
-          // Move the reference (up, but to wherever its first tile has it); rescale the sum and
-          // this warp's share of O.
+          // Move the reference (up, or down after a look, or to wherever its first tile has it);
+          // rescale the sum and this warp's share of O.
           float up = mx - L::kBias;
-          up = !fresh ? fmaxf(up, 0.f) : mx == -INFINITY ? 0.f : up;
+          up = !fresh ? fmaxf(up, low) : mx == -INFINITY ? 0.f : up;
           // (nothing is summed before the first tile, whose reference may go down past what
           // 2^-up can hold)
           const float alpha = fresh ? 0.f : ex2(-up);
+          const float drop = fresh ? 0.f : fmaxf(was - up, 0.f);
+          if (part_of == 0) *drop_at = drop;
+          due = t == due ? t + __reduce_min_sync(0xffffffffu,
+                                                 head < mine ? q4_bears(sum * alpha, t - t0, drop)
+                                                             : 1 << 20)
+                         : min(due, t + kBearsTiles);
           fresh = fresh && mx == -INFINITY;
           m += up;
           l *= alpha;
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] -= up;
-          if (t > t0) {
+          if (t > t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < 16 / kSlices; ++c) {   // this warp's slice of O's 256 columns
               const uint32_t at = lanes + L::kOCol + 256 / kSlices * hh + 16 * c;

@@ -628,8 +628,7 @@ mla_status mla_cache_read_paged(const mla_dims* dims, const mla_paging* paging,
  * lse is fp32, accumulation fp32.
  * These shares are of each weight.  The parts also have a smallest step, with which weights far
  * below the largest one are rounded or lost.  Over an FP8 cache it goes by the largest weight, so
- * that what it takes adds up with the rows, and so over a 4-bit cache from 48 bf16 query rows on
- * (2^-17 of the largest weight).  With fewer, or fp32 queries, the parts' unit follows the scores,
+ * that what it takes adds up with the rows.  Over a 4-bit cache the parts' unit follows the scores,
  * up and down: of a piece of up to 65536 rows at most 1/60 of the sum of the weights (fp32 queries:
  * 1/1200) is lost beyond those shares, whatever the largest weight and however many rows the rest
  * is spread over.  Rows 2^-40 or more below others may count for nothing.

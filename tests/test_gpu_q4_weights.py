@@ -10,10 +10,12 @@ does not go by the largest weight and hardly grows with the rows:
 
     16 heads a CTA, bf16 queries   two E4M3 parts, 1 and 1/16       r 2^-8,  d 2^-7,  b 5
                     fp32 queries   three, 1, 1/16 and 1/256         r 2^-12, d 2^-11, b 5
+    SM pairs                       an E4M3 part, its E5M2 remainder r 2^-7,  d 2^-7,  b 4
 
-Half a step of a part is 2^-4 of its value, or 2^-10 where that is more.  So e, in units of the
-softmax's reference, is at most 2^-10 / 16 for two parts, 2^-10 / 256 for three: a tile's 128 rows
-lose at most d.  How that adds up, L being the sum
+Half a step of a part is 2^-4 of its value, or 2^-10 (E4M3) and 2^-17 (E5M2) where that is more; an
+E5M2 value's 2^-3 of it.  So e, in units of the softmax's reference, is at most 2^-10 / 16 for two
+E4M3 parts, 2^-10 / 256 for three, and for a part and its remainder, which is then at most 2^-10,
+2^-14 (half of a step of 2^-13): a tile's 128 rows lose at most d.  How that adds up, L being the sum
 of the weights of t tiles, in the same units (a move of the reference scales it and the loss):
   - up to 16 tiles go by after a tile to whose maximum the reference moved, or might have: it added
     2^b or more to L, so they lose at most 16 / 2^b of d times what was added to L;
@@ -37,7 +39,10 @@ pytestmark = pytest.mark.gpu
 
 def weight_error(io, heads, q_len, n):
     """r and f above."""
-    r, d, b = (2.0 ** -12, 2.0 ** -11, 5) if io == F32 else (2.0 ** -8, 2.0 ** -7, 5)
+    if io == F32:
+        r, d, b = 2.0 ** -12, 2.0 ** -11, 5
+    else:
+        r, d, b = (2.0 ** -7, 2.0 ** -7, 4) if heads * q_len >= 48 else (2.0 ** -8, 2.0 ** -7, 5)
     return r, d * (16 / 2 ** b + 0.25 + max(np.log(n / TILE / 16), 0.0) / 4) + n * 2.0 ** -40
 
 
@@ -88,7 +93,7 @@ def problem(mla, n, at, nats, spread, io, heads, q_len=1, splits=1, page=64, see
     return Far(mla, [lat], [key], q_abs, q_pe, page, io, q_len, splits)
 
 
-FORMS = [(F32, 16), (BF16, 16)]
+FORMS = [(F32, 16), (BF16, 16), (BF16, 48), (BF16, 128)]
 
 
 @pytest.mark.parametrize("io,heads", FORMS)
@@ -99,7 +104,7 @@ def test_one_row_outweighs_65536(cuda_lib, io, heads, spread, at):
     check(problem(cuda_lib, 65536, at, (9.0, 14.0), spread, io, heads).run())
 
 
-@pytest.mark.parametrize("io,heads", FORMS + [(F32, 64), (F32, 32)])
+@pytest.mark.parametrize("io,heads", FORMS + [(F32, 64), (BF16, 32), (BF16, 64)])
 @pytest.mark.parametrize("q_len", [1, 2])
 @pytest.mark.parametrize("splits", [0, 3])
 def test_cut_rows(cuda_lib, io, heads, q_len, splits):
