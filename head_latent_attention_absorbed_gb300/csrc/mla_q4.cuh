@@ -118,11 +118,13 @@ struct Q4Lane {
   }
 };
 
-// Waits for a phase, bounded: gives up, raising the CTA's abort flag, after the library's limit.
+// Waits for a phase, bounded: gives up, raising the CTA's abort flag, after `limit_ns` (0: the
+// library's limit; see SplitParams::wait_ns).
 // The warp is suspended for up to kSuspendNs at a time: so many warps of these kernels wait that
 // their polling would take issue slots from the others.
 constexpr uint32_t kSuspendNs = 20000;
-__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                        unsigned long long limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   while (true) {
@@ -136,7 +138,7 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
         : "memory");
     if (ok) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (globaltimer_ns() - t0 > (limit_ns ? limit_ns : kWaitNs)) {
       *abort = 1;
       return false;
     }
@@ -144,8 +146,9 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
 }
 // The same by a whole warp, which leaves it converged (as the .aligned tensor-core
 // instructions after it need).
-__device__ __forceinline__ void q4_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  q4_wait(bar, parity, abort);
+__device__ __forceinline__ void q4_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             unsigned long long limit_ns) {
+  q4_wait(bar, parity, abort, limit_ns);
   __syncwarp();
 }
 

@@ -24,9 +24,9 @@ struct SplitParams {
                             // is known (a one-wave grid)
   int persist;              // bf16 kernel, 16 heads per CTA: a persistent grid whose CTAs
                             // take several chunks each (chunk % 128 == 0)
-  // Test hooks of the bf16 kernel (see mla_test_set_split_hooks), 0 in normal use:
+  // Test hooks of the bf16 and the 4-bit kernels (see mla_test_set_split_hooks), 0 in normal use:
   unsigned long long wait_ns;   // limit of each bounded wait (0: kWaitNs)
-  int stop_after_tiles;         // ring A issues only this many tiles of a chunk (0: all)
+  int stop_after_tiles;         // the copies (bf16: ring A's) stop after this many tiles (0: never)
   int32_t* debug;               // where timed-out CTAs record their first failed wait
   // Paged cache: row r of sequence b is pool row
   // table[b * table_stride + (r >> page_shift)] * 2^page_shift + r % 2^page_shift.

@@ -820,16 +820,17 @@ int32_t mla_built_with_checks(void);
 mla_status mla_debug_bounds_word(int32_t** word);
 
 /*
- * mla_test_set_split_hooks -- test hooks of the bf16 split kernel; not for
- * production use.  The pages have no counterpart: this exists so that a test
- * can make the kernel's bounded waits run out without faulting or hanging the
- * GPU (the overflow-returns-an-error rule of "Transformer and KV Cache Basics",
- * applied to the kernel's own pipeline).
+ * mla_test_set_split_hooks -- test hooks of the bf16 split kernel and of the split
+ * kernels over a 4-bit pool; not for production use.  The pages have no counterpart:
+ * this exists so that a test can make the kernel's bounded waits run out without
+ * faulting or hanging the GPU (the overflow-returns-an-error rule of "Transformer and
+ * KV Cache Basics", applied to the kernel's own pipeline).
  *
- * wait_ns           limit of every bounded wait of the bf16 split kernel in ns
- *                   (0: the default of 2 s).
+ * wait_ns           limit of every bounded wait of these kernels in ns (0: the
+ *                   default of 2 s; copies still in flight are always given that).
  * stop_after_tiles  > 0: the kernel's HBM ring issues only the first
- *                   stop_after_tiles 128-row tiles of each chunk, so a chunk
+ *                   stop_after_tiles 128-row tiles of each chunk (over a 4-bit
+ *                   pool a CTA's first ones of all its tiles), so a chunk
  *                   with more tiles leaves its consumers waiting; they give up
  *                   after wait_ns, set MLA_DEV_PIPELINE_TIMEOUT in dev_status,
  *                   write no partial, let the copies still in flight land, free
