@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     page_index_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ table,
                          const int32_t* __restrict__ first_rows, const int32_t* __restrict__ lengths,
                          int8_t* codes, float* scales, int32_t* status, int page_shift,
-                         int table_stride, int num_pages, int max_new, int most, int items) {
+                         int table_stride, int num_pages, int max_new, int most, int batch) {
+  const long long items = static_cast<long long>(batch) * most;
   __shared__ float tops[kWarps];
   __shared__ int sums[kWarps][kRow];
   __shared__ int peaks[kWarps];
@@ -407,7 +408,9 @@ __global__ void __launch_bounds__(32 * kWarps)
       const long long item = base + static_cast<long long>(lane) * gridDim.x;
       int id = -1, n = 0;
       if (item < items) {
-        const int b = static_cast<int>(item) / most, jj = static_cast<int>(item) % most;
+        const int b = items < (1ll << 31) ? static_cast<int>(item) / most
+                                          : static_cast<int>(item / most);
+        const int jj = static_cast<int>(item - static_cast<long long>(b) * most);
         const int first = first_rows[b], len = lengths[b];
         const bool bad =
             first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
@@ -485,17 +488,13 @@ mla_status page_index_q4(const char* who, const mla_paging* paging, int batch, i
                          const int32_t* lengths, int8_t* codes, float* scales, int32_t* status,
                          cudaStream_t s) {
   const long long items = static_cast<long long>(batch) * most;
-  if (items >= (1ll << 31)) {
-    set_error("%s: batch=%d requests of up to %d touched pages exceed 2^31", who, batch, most);
-    return MLA_ERR_UNSUPPORTED;
-  }
   // As many as the SMs hold at once, but an odd number: where every request touches its first page
   // alone, those are `most` items apart, often a power of two, and have to come to different CTAs.
   const long long most_ctas = 4ll * sm_count() - 1;
   page_index_q4_kernel<<<static_cast<unsigned>(items < most_ctas ? items : most_ctas), 32 * kWarps, 0,
                          s>>>(static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes,
                               scales, status, page_shift_of(paging), paging->table_stride,
-                              paging->num_pages, max_new, most, static_cast<int>(items));
+                              paging->num_pages, max_new, most, batch);
   return launch_status(who);
 }
 
