@@ -287,22 +287,24 @@ __global__ void __launch_bounds__(32 * kWarps)
 
 // ------------------------------------------------------------- the page index
 // page_index_kernel's definition over 4-bit pages.  Items are the pages that each request's max_new
-// rows could touch; a CTA walks its share of them, looked up 32 at a time, and looks at a page that
-// was touched twice: its largest magnitude, of which the power of two above it is all that counts (and of
-// codes, their highest bits), then the sums.  A warp reads four of the page's rows together.
-// One touched page of 64 rows for each of 4 sequences 5.7 us, which is the way from the lengths
-// to the table to the rows and back; one for each of 256 that could have touched 32 9.2 (a CTA for
-// every page that could be touched: 16); all 4096 pages of 4 x 65536 rows 69 us (1.5 TB/s: bound
-// by the codes' conversions and additions; a CTA a page 64).
+// rows could touch.  A CTA looks at a page that was touched twice: its largest magnitude, of which
+// the power of two above it is all that counts (and of codes, their highest bits), then the sums.  A
+// warp reads four of the page's rows together.
+// Up to kEachPerSm items for each SM, a CTA has one (kEach); of more, few of which may have been
+// touched, it walks its share, looked up 32 at a time.  61 x 1024 rows, 1037 items all touched, 18.0
+// us for 20.5 walked; 128 requests that touched one page of 9 4.7 for 3.9, of 32 (4096 items) 6.9 for
+// 4.0; one touched page of 40 rows for each of 4 sequences 4.3, which is the way from the lengths to
+// the table to the rows and back, for 4.6; all 4096 pages of 4 x 65536 rows 64 for 69 (1.5 TB/s: bound
+// by the codes' conversions and additions).
 // A latent is a multiple of 2^-9 and at most 384, so the maximum is a maximum of exact values.
 constexpr float kQ4Tiny = 1e-30f;
-constexpr int kIndexRows = 4;
+constexpr int kIndexRows = 4, kEachPerSm = 8;
+template <bool kEach>
 __global__ void __launch_bounds__(32 * kWarps)
     page_index_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ table,
                          const int32_t* __restrict__ first_rows, const int32_t* __restrict__ lengths,
                          int8_t* codes, float* scales, int32_t* status, int page_shift,
                          int table_stride, int num_pages, int max_new, int most, int batch) {
-  const long long items = static_cast<long long>(batch) * most;
   __shared__ float tops[kWarps];
   __shared__ int sums[kWarps][kRow];
   __shared__ int peaks[kWarps];
@@ -400,43 +402,51 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     if (tid == 0)
       scales[id] = good ? ldexpf(pf * (1.f / 127.f) / static_cast<float>(n), ex - 20) : 0.f;
-    __syncthreads();   // before the next page's sums
   };
-  for (long long base = blockIdx.x; base < items; base += 32ll * gridDim.x) {
-    // Lane l of the first warp looks item base + l * gridDim.x up.
-    if (warp == 0) {
-      const long long item = base + static_cast<long long>(lane) * gridDim.x;
-      int id = -1, n = 0;
-      if (item < items) {
-        const int b = items < (1ll << 31) ? static_cast<int>(item) / most
-                                          : static_cast<int>(item / most);
-        const int jj = static_cast<int>(item - static_cast<long long>(b) * most);
-        const int first = first_rows[b], len = lengths[b];
-        const bool bad =
-            first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
-        if (jj == 0 && (bad || static_cast<long long>(len) - first > max_new))
-          report(status, MLA_DEV_LENGTH_OUT_OF_RANGE);
-        const long long j = static_cast<long long>(first >> page_shift) + jj;
-        if (!bad && first < len && (j << page_shift) < len) {
-          n = static_cast<int>(min(1ll << page_shift, len - (j << page_shift)));
-          id = table[static_cast<size_t>(b) * table_stride + j];
-          if (id < 0 || id >= num_pages) {
-            report(status, MLA_DEV_PAGE_OUT_OF_RANGE);
-            id = -1;
-          }
+  // Page jj of those that request b's new rows could touch, and its rows; -1: there is none.
+  auto look_up = [&](int b, int jj, bool say, int& n) {
+    const int first = first_rows[b], len = lengths[b];
+    const bool bad =
+        first < 0 || len < 0 || len > static_cast<long long>(table_stride) << page_shift;
+    if (say && jj == 0 && (bad || static_cast<long long>(len) - first > max_new))
+      report(status, MLA_DEV_LENGTH_OUT_OF_RANGE);
+    const long long j = static_cast<long long>(first >> page_shift) + jj;
+    if (bad || first >= len || (j << page_shift) >= len) return -1;
+    n = static_cast<int>(min(1ll << page_shift, len - (j << page_shift)));
+    const int id = table[static_cast<size_t>(b) * table_stride + j];
+    if (id >= 0 && id < num_pages) return id;
+    if (say) report(status, MLA_DEV_PAGE_OUT_OF_RANGE);
+    return -1;
+  };
+  if constexpr (kEach) {
+    int n = 0;
+    const int id = look_up(blockIdx.x / most, blockIdx.x % most, tid == 0, n);
+    if (id >= 0) page(id, n);
+  } else {
+    const long long items = static_cast<long long>(batch) * most;
+    for (long long base = blockIdx.x; base < items; base += 32ll * gridDim.x) {
+      // Lane l of the first warp looks item base + l * gridDim.x up.
+      if (warp == 0) {
+        const long long item = base + static_cast<long long>(lane) * gridDim.x;
+        int id = -1, n = 0;
+        if (item < items) {
+          const int b = items < (1ll << 31) ? static_cast<int>(item) / most
+                                            : static_cast<int>(item / most);
+          id = look_up(b, static_cast<int>(item - static_cast<long long>(b) * most), true, n);
         }
+        ids[lane] = id;
+        rows_of[lane] = n;
+        const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+        if (lane == 0) found = live;
       }
-      ids[lane] = id;
-      rows_of[lane] = n;
-      const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
-      if (lane == 0) found = live;
+      __syncthreads();
+      for (uint32_t todo = found; todo; todo &= todo - 1) {
+        const int l = __ffs(todo) - 1;
+        page(ids[l], rows_of[l]);
+        __syncthreads();   // before the next page's sums
+      }
+      __syncthreads();   // before the next items are looked up
     }
-    __syncthreads();
-    for (uint32_t todo = found; todo; todo &= todo - 1) {
-      const int l = __ffs(todo) - 1;
-      page(ids[l], rows_of[l]);
-    }
-    __syncthreads();   // before the next items are looked up
   }
 }
 
@@ -488,13 +498,18 @@ mla_status page_index_q4(const char* who, const mla_paging* paging, int batch, i
                          const int32_t* lengths, int8_t* codes, float* scales, int32_t* status,
                          cudaStream_t s) {
   const long long items = static_cast<long long>(batch) * most;
-  // As many as the SMs hold at once, but an odd number: where every request touches its first page
-  // alone, those are `most` items apart, often a power of two, and have to come to different CTAs.
-  const long long most_ctas = 4ll * sm_count() - 1;
-  page_index_q4_kernel<<<static_cast<unsigned>(items < most_ctas ? items : most_ctas), 32 * kWarps, 0,
-                         s>>>(static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes,
-                              scales, status, page_shift_of(paging), paging->table_stride,
-                              paging->num_pages, max_new, most, batch);
+  auto go = [&](auto kernel, long long ctas) {
+    kernel<<<static_cast<unsigned>(ctas), 32 * kWarps, 0, s>>>(
+        static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes, scales, status,
+        page_shift_of(paging), paging->table_stride, paging->num_pages, max_new, most, batch);
+  };
+  const int sms = sm_count();
+  if (items <= kEachPerSm * static_cast<long long>(sms))
+    go(page_index_q4_kernel<true>, items);
+  else
+    // As many as the SMs hold at once, but an odd number: where every request touches its first page
+    // alone, those are `most` items apart, often a power of two, and have to come to different CTAs.
+    go(page_index_q4_kernel<false>, 4ll * sms - 1);
   return launch_status(who);
 }
 
