@@ -31,7 +31,7 @@ import torch
 
 import _q4
 from _paged import D_C, D_R, SCALE, f64, half_step
-from _q4_far import BF16, F32, TILE, Far
+from _q4_far import BF16, F32, TILE, Far, shifted
 from oracle import paged_oracle as PO
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +130,11 @@ def test_tiles_that_climb_and_fall(cuda_lib, io, heads):
     check(problem(cuda_lib, len(tail), 5 * TILE + 3, (0.0, 10.0), 0.0, io, heads, tail=tail).run())
     check(problem(cuda_lib, len(tail) - 77, 60 * TILE, (0.0, 10.0), 0.0, io, heads, 2, 0,
                   tail=tail[77:]).run())
+
+
+@pytest.mark.parametrize("io,heads", FORMS + [(F32, 32), (BF16, 32), (BF16, 64)])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_ordinary_rows(cuda_lib, io, heads, q_len):
+    """Random rows, no row far from the others: each form within its own bound."""
+    rng = np.random.RandomState(heads + q_len)
+    check(shifted(rng, cuda_lib, [np.zeros(n) for n in (2, 129, 700, 5000)], heads, io, q_len).run())
