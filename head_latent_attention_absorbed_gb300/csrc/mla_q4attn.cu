@@ -108,7 +108,7 @@ struct Q4Plan {
                        ODONE = PFULL + 2,             // [2] PV of the tile finished (tile free)
                        QREADY = ODONE + 2, DONE = QREADY + 1, kBars = DONE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
-  static constexpr int kOffAbort = kOffSlot + 16;
+  static constexpr int kOffAbort = kOffSlot + 16;    // flag, limit of the waits
   static constexpr int kOffShare = kOffAbort + 16;   // TileShare of the CTA
   static constexpr size_t kSmem = 1024 + kOffShare + 32;
   static_assert(kSmem <= 232448, "shared memory");
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
   auto issue_slot = [&](const uint8_t* src, int live, int n) {   // false: given up
     const int at = n % L::kSlots, per = L::kSlotRows / lat_piece, from = n % kTileSlots * per;
     if (n >= L::kSlots) {
-      q4_warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::RAWEMPTY + at), (n / L::kSlots - 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     copy_pieces(src, from, from + per, live, lat_piece * kQ4LatBytes,
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     const int bf = t & 1;
     const uint8_t* src = piece_source(id, r0, key_piece, kQ4LatBytes, kQ4KeyBytes);
     if (t >= 2) {
-      q4_warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::SFULL + bf), ((t - 2) >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     copy_pieces(src, 0, kRowsT / key_piece, __popc(__ballot_sync(0xffffffffu, id != -2)),
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
                            : lane >= L::CFULL && lane < L::SFULL    ? kTeams * kTeam / 32
                            : lane >= L::RAWEMPTY && lane < L::KEYFULL ? kTeam / 32
                                                                       : 1);
-    if (lane == 0) *abort_flag = 0;
+    if (lane == 0) q4_wait_init(p, abort_flag);
     fence_mbarrier_init();
     __syncwarp();
     if (T > 0) {   // the stream starts before the CTA's barrier
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (t > 0 && issue_keys(id, r0, t)) keys = t + 1;
       if (kShare && later) {
         // A new item's query, once the last score MMA of the one before has read its own.
-        q4_warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::SFULL + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
         if (!__any_sync(0xffffffffu, *abort_flag) && lane == 0) {
           pdl_wait();
           load_query(now.v);
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
     // four loads that meet in the same banks for one.)
     auto load = [&](Q4Piece (&piece)[kEach], int n) {
       const int slot = n % L::kSlots;
-      q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::RAWFULL + slot), (n / L::kSlots) & 1, abort_flag);
       const uint32_t e = *reinterpret_cast<const Exps*>(exps + slot * L::kSlotBytes);
 #pragma unroll
       for (int k = 0; k < kEach; ++k)
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       bool plain = load(piece, n);
       n += kTeams;
       if (t >= 2) {
-        q4_warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::ODONE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag);
         tc_fence_after();
       }
       uint8_t* rows = to + (t & 1) * kTile + team * L::kSlotRows * 128;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       if (left == 0) {
         if (t > 0) cur = item_after(cur, t);
         left = cur.tiles;
-        q4_warp_wait(bar(L::QREADY), n & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::QREADY), n & 1, abort_flag);
         if (kShare && g == 0 && lane == 0 && cur.r0 == 0) {
           // The run with a query group's first tile says how many runs it spans.  (Not
           // before a query is here, fetched behind the PDL wait: the combine of the call
@@ -555,14 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         ++n;
       }
       --left;
-      if (t >= 2) q4_warp_wait(bar(L::SFREE + bf), ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
-      q4_warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag, p.wait_ns);
+      if (t >= 2) q4_warp_wait(bar(L::SFREE + bf), ((t - 2) >> 1) & 1, abort_flag);
+      q4_warp_wait(bar(L::KEYFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       // 16 key values (32 bytes) a step
       umma_x4<false, 2, 2>(tmem + kKCol + 32 * bf, k0 + ((bf * kKeyTile) >> 4),
                            q0 + (L::kQKeys >> 4), idesc_k, 0);
-      q4_warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::CFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         cur = item_after(cur, t);
         done = 0;
       }
-      q4_warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::PFULL + bf), (t >> 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       const uint64_t pd = p0 + static_cast<uint64_t>((bf * L::kPBuf) >> 4);
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
       for (int t = t0; t < t0 + tiles; ++t) {
         const int sb = t & 1;
         const int valid = t == t0 + tiles - 1 ? last_valid : kRowsT;
-        q4_warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::SFULL + sb), (t >> 1) & 1, abort_flag);
         tc_fence_after();
         float x[kHalf];   // scores in units of the head's scale
         {
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
             l[h] *= alpha[h];
           }
           if (t > t0 && moved) {
-            q4_warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag, p.wait_ns);
+            q4_warp_wait(bar(L::ODONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
           }
         }
         // P^T buffer sb was last read by the PV of tile t-2.
-        if (t >= 2) q4_warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
+        if (t >= 2) q4_warp_wait(bar(L::ODONE + sb), ((t - 2) >> 1) & 1, abort_flag);
         {
           // P^T (B operand of the PV MMA, K-major, 128-byte swizzle): row
           // 16 part + n is part `part` of head n; the K index is the tile row.  Four
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_q4_kernel(const SplitParams
         read_scales();
       }
       // O^T after the last PV: this thread's latent row is 128 mb + 32 wq + lane.
-      q4_warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::ODONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
       // (asked for all of the group: the flag may be raised at any time)
       if (!any_of(*abort_flag, 3 + gp, kSoft / 2)) {

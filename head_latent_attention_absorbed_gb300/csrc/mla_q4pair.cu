@@ -81,7 +81,7 @@ struct Q4Pair {
                        QFULL = PVDONE + 2, QFREE = QFULL + 1, kBars = QFREE + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kBars;
   static constexpr int kOffAbort = kOffSlot + 8;
-  static constexpr int kOffShare = kOffAbort + 8;       // TileShare of the pair
+  static constexpr int kOffShare = kOffAbort + 8;       // (flag and limit) TileShare of the pair
   static constexpr int kOffDrop = kOffShare + 24;       // [64 heads], see the softmax
   static constexpr size_t kSmem = kOffDrop + 64 * 4;
   static constexpr uint32_t kOCol = 256;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
     mbar_init(bar(L::KREADY), 2);   // both CTAs' keys
     mbar_init(bar(L::QFULL), 1);
     mbar_init(bar(L::QFREE), 2);   // one commit per score issuer
-    *abort_flag = 0;
+    q4_wait_init(p, abort_flag);
     fence_mbarrier_init();
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_qpe);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         for (int k = k0; k < k1; ++k) {
           const int slot = (own ? 0 : 2) + k, from = (2 * half + k) * per;
           if (t > 0) {
-            q4_warp_wait(bar(L::RAWEMPTY + slot), (t - 1) & 1, abort_flag, p.wait_ns);
+            q4_warp_wait(bar(L::RAWEMPTY + slot), (t - 1) & 1, abort_flag);
             if (given_up()) return false;
           }
           copy_pieces(src, from, from + per, live, piece * bytes,
@@ -356,20 +356,20 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         const int live = live_of(ahead);
         look_ahead(it, i, t);
         if (t > 0) {   // the scores of the tile before have read them
-          q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag, p.wait_ns);
+          q4_warp_wait(bar(L::SREADY + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
           if (given_up()) return false;
         }
         copy_pieces(src, 0, 64 / piece, live, piece * bytes, sbase + L::kOffK, bar(L::KEYFULL));
         if (kShare && i == 0 && t > 0) {
           // A later item's query, once the scores of the item before are done, which read the one
           // that it replaces.
-          q4_warp_wait(bar(L::QFREE), queries & 1, abort_flag, p.wait_ns);
+          q4_warp_wait(bar(L::QFREE), queries & 1, abort_flag);
           if (given_up()) return false;
           ++queries;
           load_query(it.v);
         }
         // Handed over once they have landed: the even CTA's MMAs read both CTAs'.
-        q4_warp_wait(bar(L::KEYFULL), t & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::KEYFULL), t & 1, abort_flag);
         if (lane == 0) arrive_cluster(lbar(L::KREADY));
         return true;
       });
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       bool plain = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        q4_warp_wait(bar(L::RAWFULL + k), t & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::RAWFULL + k), t & 1, abort_flag);
         const uint8_t* raw = from + k * L::kSlotBytes;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       else
         decode(Int<0>{});
       if (t >= L::kTiles) {
-        q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::FREE + buf), (t / L::kTiles - 1) & 1, abort_flag);
         tc_fence_after();
       }
       uint8_t* to = boxes + buf * 4 * kPBox;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       for_tiles([&](const TileItem& it, int i, int t) {
         const int sb = t & 1;
         if (i == 0) {
-          q4_warp_wait(bar(L::QFULL), n & 1, abort_flag, p.wait_ns);
+          q4_warp_wait(bar(L::QFULL), n & 1, abort_flag);
           ++n;
           if (kShare && !keys && blockIdx.x % parts == 0 && it.r0 == 0)
             // The run with a sequence's first tile says how many runs it spans.  (Not before a
@@ -459,16 +459,16 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
             for (int q = lane; q < p.q_len; q += 32)
               p.pieces[it.v * p.q_len + q] = count_pieces(it, share.first + t, share.each);
         }
-        if (t >= 2) q4_warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
+        if (t >= 2) q4_warp_wait(bar(L::SFREE + sb), ((t - 2) >> 1) & 1, abort_flag);
         if (given_up()) return false;
         if (keys) {
-          q4_warp_wait(bar(L::KREADY), t & 1, abort_flag, p.wait_ns);
+          q4_warp_wait(bar(L::KREADY), t & 1, abort_flag);
           if (given_up()) return false;
           tc_fence_after();
           mma_pair_steps<false, 4, 2, 2>(tmem + 128 + 64 * sb, qk0, k0, idesc_k, 0);
         } else {
           const int buf = t % L::kTiles;
-          q4_warp_wait(bar(L::FULLS + buf), (t / L::kTiles) & 1, abort_flag, p.wait_ns);
+          q4_warp_wait(bar(L::FULLS + buf), (t / L::kTiles) & 1, abort_flag);
           if (given_up()) return false;
           tc_fence_after();
 #pragma unroll 1
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       for_tiles([&](const TileItem&, int i, int t) {
         const int pb = t & 1;
         const int buf = t % L::kTiles;
-        q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::PREADY + pb), (t >> 1) & 1, abort_flag);
         if (given_up()) return false;
         tc_fence_after();
 #pragma unroll 1
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       // once), so that all softmax warps meet at the same barriers.
       for (int t = t0; t < t0 + tiles; ++t) {
         const int sb = t & 1;
-        q4_warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::SREADY + sb), (t >> 1) & 1, abort_flag);
         // written by the kernel before, known complete once the first scores are
         if (t == t0) unit = __ldcg(sigma + flat0 + min(head, mine - 1)) * scale;
         tc_fence_after();
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
         // The eight warps of the same heads go by one reference, and decide alike.
         if (any_of(fresh || mx > L::kTop || t == due, 1 + (qd & 1), L::kSoft / 2)) {
           if (t > t0) {   // P and O: the output product of the tile before is done
-            q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag, p.wait_ns);
+            q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
             tc_fence_after();
           }
           red[part_of * 32 + lane] = mx;
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           }
         }
         // The scores of this tile are done: its boxes' second halves, loaded.
-        q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag, p.wait_ns);
+        q4_warp_wait(bar(L::RAWFULL + slot), t & 1, abort_flag);
         Q4Piece piece;
         const int box_m = 2 * j + rank;
         piece.load(raw + 64 * box_m + 16 * c, raw[kQ4CodeBytes + 4 * box_m + c]);
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
           l += x[i];
         }
         // P was last read by the output MMAs of tile t - 1.
-        if (t >= 1) q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag, p.wait_ns);
+        if (t >= 1) q4_warp_wait(bar(L::PVDONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
         {
           // A operand, K-major: row `head` of each part's box, 128 bytes of tile rows.
           uint8_t* pb = smem + L::kOffP;
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(Q4Pair::kThreads, 1)
       if (tid == 0 && t0 == T) pdl_launch_dependents();   // the combine waits for this grid anyway
       // The row sums of a head's threads, its log-sum-exp, and O / sum through shared memory
       // (over operands that nothing reads any more) to whole rows.
-      q4_warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag, p.wait_ns);
+      q4_warp_wait(bar(L::PVDONE + ((t0 - 1) & 1)), ((t0 - 1) >> 1) & 1, abort_flag);
       tc_fence_after();
       red[part_of * 32 + lane] = l;
       named_bar_sync(5, L::kSoft);
