@@ -13,9 +13,9 @@ constexpr int kWarps = 8;
 // 576 values read, 400 bytes written per row: bound by HBM for fp32 rows, and for bf16 rows as much
 // by the instructions that quantise them.  A warp moves a row, as in append_paged_kernel,
 // kAppendEach rows' loads in flight; two lanes share a block of 16 latents, so its largest
-// magnitude is one exchange, and four a byte of exponents.  62281 rows: bf16 18.0 us, 0.79 of the
-// measured copy bandwidth, fp32 26.3, 0.94.  (Four rows a warp and eight warps a CTA, whose last
-// wave is long: fp32 30.4, 1000 bf16 rows 2.9 for 1.9.  bf16 values widened before they are
+// magnitude is one exchange, and four a byte of exponents.  62281 rows: bf16 19.0 us, 0.75 of the
+// measured copy bandwidth, fp32 27.0, 0.92.  (When these took 18.0 and 26.3, over one copy of the rows:
+// four rows a warp and eight warps a CTA, whose last wave is long, fp32 30.4, 1000 bf16 rows 2.9 for 1.9.  bf16 values widened before they are
 // compared and scaled: 19.1.  A grid that the SMs hold at once, each warp with its next row's
 // loads out while it writes one: 26.7.)
 constexpr int kAppendEach = 2, kAppendWarps = 4, kAppendRows = kAppendWarps * kAppendEach;
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 // packed output.  Its lanes find the first one's sequence together (32 steps of the row starts a
 // round), then each one row's page, so that a run of rows costs one chain of dependent loads; then
 // the warp moves them, a few rows' loads out while as many are written: four, or two of the wide
-// rows, whose registers would halve the warps.  4 x 16384 rows to bf16, 4-bit 20.1 us (0.75 of the
+// rows, whose registers would halve the warps.  4 x 16384 rows to bf16, 4-bit 20.3 us (0.74 of the
 // measured copy bandwidth; 22.9 with four rows a warp, each row's page looked up on its way), bf16
-// 27.9, fp32 to fp32 53.2 us (0.84).
+// 28.6 (0.78), fp32 to fp32 54.0 (0.82).
 constexpr int kReadMost = 32;
 struct ReadParams {
   const void* pool;
@@ -290,15 +290,16 @@ __global__ void __launch_bounds__(32 * kWarps)
 // rows could touch.  A CTA looks at a page that was touched twice: its largest magnitude, of which
 // the power of two above it is all that counts (and of codes, their highest bits), then the sums.  A
 // warp reads four of the page's rows together.
-// Up to kEachPerSm items for each SM, a CTA has one (kEach); of more, few of which may have been
-// touched, it walks its share, looked up 32 at a time.  61 x 1024 rows, 1037 items all touched, 18.0
-// us for 20.5 walked; 128 requests that touched one page of 9 4.7 for 3.9, of 32 (4096 items) 6.9 for
-// 4.0; one touched page of 40 rows for each of 4 sequences 4.3, which is the way from the lengths to
-// the table to the rows and back, for 4.6; all 4096 pages of 4 x 65536 rows 64 for 69 (1.5 TB/s: bound
-// by the codes' conversions and additions).
+// Of no more items than the SMs hold CTAs at once, each has one (kEach), which knows its item sooner:
+// one touched page of 64 rows for each of 4 sequences 5.3 us, the way from the lengths to the table to
+// the rows and back, for 5.6 walked.  Of more, few of which may have been touched, a CTA walks its
+// share, looked up 32 at a time: one of 32 for each of 256 requests 9.4 us for 16, of 9 for each of
+// 128 7.6 for 9.5; 61 x 1024 rows all touched 17.9, and 4096 pages of 4 x 65536 rows 71 for 65 (1.5
+// TB/s: bound by instructions, 77 % of the issue slots).
 // A latent is a multiple of 2^-9 and at most 384, so the maximum is a maximum of exact values.
 constexpr float kQ4Tiny = 1e-30f;
-constexpr int kIndexRows = 4, kEachPerSm = 8;
+constexpr int kIndexRows = 4;
+constexpr int kIndexPerSm = 4;   // CTAs
 template <bool kEach>
 __global__ void __launch_bounds__(32 * kWarps)
     page_index_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ table,
@@ -503,13 +504,13 @@ mla_status page_index_q4(const char* who, const mla_paging* paging, int batch, i
         static_cast<const uint8_t*>(cache), table, first_rows, lengths, codes, scales, status,
         page_shift_of(paging), paging->table_stride, paging->num_pages, max_new, most, batch);
   };
-  const int sms = sm_count();
-  if (items <= kEachPerSm * static_cast<long long>(sms))
+  const long long held = static_cast<long long>(kIndexPerSm) * sm_count();
+  if (items <= held)
     go(page_index_q4_kernel<true>, items);
   else
-    // As many as the SMs hold at once, but an odd number: where every request touches its first page
-    // alone, those are `most` items apart, often a power of two, and have to come to different CTAs.
-    go(page_index_q4_kernel<false>, 4ll * sms - 1);
+    // An odd number: where every request touches its first page alone, those are `most` items apart,
+    // often a power of two, and have to come to different CTAs.
+    go(page_index_q4_kernel<false>, held - 1);
   return launch_status(who);
 }
 
