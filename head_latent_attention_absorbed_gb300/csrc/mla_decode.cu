@@ -2086,15 +2086,15 @@ struct PlanOpts {
 // 4096 rows, 16 query rows 13.7 / 15.0, 32 17.7 / 15.7, 48 26.3 / 16.2, 64 24.5 / 17.1; 4 x
 // 65536, 16 rows 58 / 61, 32 68 / 65, 64 105 / 68; 64 sequences of 512 to 8192, 32 rows
 // 99 / 76, 128 268 / 89.  E4M3, 8 x 4096, 32 rows 15.8 / 17.8, 48 22.9 / 17.1; 4 x 65536,
-// 32 rows 61 / 53, 48 88 / 56.  4-bit, 8 x 4096, 32 rows 16.6 / 19.6, 64 25.9 / 20.7; 64
-// sequences of 512 to 8192, 32 rows 75 / 84, 128 264 / 102.
+// 32 rows 61 / 53, 48 88 / 56.  4-bit, 8 x 4096, 32 rows 15.8 / 18.2, 48 21.8 / 19.3, 64 23.9 / 20.0;
+// 64 sequences of 512 to 8192, 32 rows 68 / 75, 48 96 / 78, 128 232 / 94.
 constexpr int kPairMinBf16 = 32, kPairMinFp8 = 48, kPairMinFp4 = 48;
 // Tiles per CTA, were all sequences full, from which a paged FP8 or 4-bit cache is cut into equal
 // shares of the tiles instead of chunks.  Measured (16 heads, us, chunks / shares): 512 to
 // 8192 rows, 64 sequences 54 / 44, 16 (6.7 tiles) 22.5 / 19.0, 8 (3.4) 16.2 / 16.6; all
 // full, 256 x 2048 75 / 73, 64 x 4096 40.8 / 40.9, 32 x 4096 (6.7) 24.6 / 25.4, 16 x 4096
-// (3.4) 16.1 / 18.6.  4-bit: 512 to 8192 rows, 64 sequences 53 / 43, 16 23.3 / 19.3; all full,
-// 256 x 2048 74 / 74, 64 x 4096 40.0 / 40.6, 32 x 4096 24.6 / 25.9, 16 x 2048 12.9 / 14.9.
+// (3.4) 16.1 / 18.6.  4-bit: 512 to 8192 rows, 64 sequences 49 / 40, 16 21.7 / 18.2; all full,
+// 256 x 2048 67 / 68, 64 x 4096 36.2 / 37.5, 32 x 4096 22.8 / 24.0, 16 x 2048 12.7 / 14.5.
 constexpr int kShareMinTiles = 5;
 // The same for SM pairs: tiles per pair (bf16, E4M3), and sequences per pair up to which
 // (more are balanced as they are, with one chunk each and no combine).  64 heads, chunks /
@@ -2102,9 +2102,10 @@ constexpr int kShareMinTiles = 5;
 // 204 / 166, 200 245 / 214, 256 of 100 to 2048 95 / 106; 512 to 4096, 16 (6.7) 22.6 / 23.9,
 // 24 (10.1) 27.6 / 28.0; all full, 16 x 8192 40.7 / 44.4, 76 x 8192 127 / 136; E4M3, 32 of
 // 512 to 4096 (13.5) 33.0 / 35.4, 48 (20.2) 48.9 / 42.4, 76 of 512 to 8192 92 / 82; 4-bit of
-// 128 heads, 512 to 8192, 16 (13.5) 40.5 / 36.4, 48 87 / 72, 76 115 / 106, 152 210 / 186; all
-// full, 16 x 8192 42.2 / 47.3, 76 x 4096 68 / 81, 32 x 2048 (6.7) 30.7 / 37.5; one of 32768
-// among 32 of 2048 217 / 123.
+// 128 heads, 512 to 8192, 16 (13.5) 40.6 / 36.5, 48 89 / 71, 76 117 / 104, 152 209 / 184; all
+// full, 16 x 8192 43.0 / 47.4, 76 x 4096 70 / 79, 32 x 2048 (6.7) 31.0 / 38.0; one of 32768
+// among 32 of 2048 219 / 120.  (The host does not know the lengths: a batch whose sequences are all
+// full pays a tenth for what a ragged one gains.)
 constexpr int kSharePairTilesBf16 = 13, kSharePairTilesFp8 = 20, kSharePairTilesFp4 = 13,
               kSharePairSets = 3;
 bool pair_form(const mla_dims* d, const PlanOpts& o) {

@@ -122,8 +122,9 @@ struct Q4Lane {
 // behind the flag says, which is then none for the CTA's other waits.  The warp is suspended for up
 // to kSuspendNs at a time: so many warps of these kernels wait that their polling would take issue
 // slots from the others.  Out of line, since 20 to 32 warps share the instruction cache and a tile
-// meets some 25 waits: 32 x 16384 rows x 128 heads 119 us for 125 with each wait's loop in place, fp32
-// queries of 64 x 4096 rows 51.7 for 52.3 (bf16 67.9 for 67.4 of 256 x 2048 rows).
+// meets some 25 waits: 32 x 16384 rows x 128 heads, the same rows each time, 119 us for 125 with each
+// wait's loop in place, fp32 queries of 64 x 4096 rows 51.7 for 52.3 (bf16 67.9 for 67.4 of 256 x 2048
+// rows).
 constexpr uint32_t kSuspendNs = 20000;
 // Before any wait, by one thread, the CTA's barrier between them.
 __device__ __forceinline__ void q4_wait_init(const SplitParams& p, volatile int* abort) {
@@ -221,8 +222,9 @@ struct Q4Piece {
 // largest weight.  How many tiles the sum bears until the next look follows from the sum; a move to
 // a tile's maximum, which adds 2^4 or more, bears kBearsTiles.  So each d comes with 1 to 4 of the
 // sum, or with octaves that a move adds to it: over 512 tiles some two d of the sum are lost at
-// most.  Looks are few, and so are moves, by which O is rescaled.  (With the weights of every tile
-// looked at, 32 x 16384 rows x 128 heads whose scores spread by 2 nats take 159 us for 134.)
+// most.  Looks are few, and so are moves, by which O is rescaled: 32 x 16384 rows x 128 heads whose
+// scores spread by 1 nat 118 us, by 2, 3 and 5 131, 145 and 156 (with references that only rise 128, 134 and 143; with the weights
+// of every tile looked at 159, 180 and 181).
 constexpr float kNoRef = -3e38f;   // before a head's first score: below any, but finite, so that
                                    // scores of -infinity have no weight there either
 constexpr float kSpan = 40.f;      // how far below the highest it was a reference may go: the rows

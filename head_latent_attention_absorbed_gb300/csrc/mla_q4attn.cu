@@ -40,8 +40,8 @@
 // between), and the decoding warps, busy for nine tenths of a tile's 1.8 us, on a shared memory
 // that the tensor cores' reads (1440 of 3500 cycles), the threads' (1200) and copies (400) keep
 // busy; HBM would allow 1.15.
-// 64 sequences of 512 to 8192 rows 40.1 us (2.8 TB/s of cache), 4 x 65536 rows 36.5, with an E4M3
-// cache, whose rows are longer and need no decoding, 43.4 and 38.8.  Not kept (us of those two,
+// 64 sequences of 512 to 8192 rows 39.9 us (2.8 TB/s of cache), 4 x 65536 rows 36.3, with an E4M3
+// cache, whose rows are longer and need no decoding, 44.5 and 39.5.  Not kept (us of those two,
 // when they took 41.4 and 37.4): four teams on 72 registers 44.7 / 40.6, the scores' operand in
 // tensor memory, where the decoding warps put it too, 42.1 / 38.3 (and before they wait for the
 // tile's buffer, so that scores run ahead of the output, 9 % slower), boxes handed over one by one

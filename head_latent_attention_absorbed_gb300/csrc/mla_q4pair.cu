@@ -41,8 +41,8 @@
 // tile's 2.0 us; and shared memory, of whose 3800 cycles in that time the tensor cores' reads take
 // 1900 (both parts of Q and of P against every row), codes, boxes and copies some 1300.  The
 // operations alone would take 1.4 us.
-// 32 x 16384 rows x 128 heads 123 us (1.70 TB/s of cache; E4M3 cache 105, bf16 129), 64 sequences
-// of 512 to 8192 rows 98.  A change of item takes 5 to 6 us, of which 4.8 are its result's way
+// 32 x 16384 rows x 128 heads 123 us (1.70 TB/s of cache; E4M3 cache 103, bf16 131), 64 sequences
+// of 512 to 8192 rows 96.  A change of item takes 5 to 6 us, of which 4.8 are its result's way
 // through P; stored straight from registers, or 128 bytes of a row at a time, it takes no less.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>

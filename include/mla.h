@@ -21,7 +21,8 @@
  * Conventions for every call
  *  - All tensor pointers are DEVICE pointers, row-major and contiguous, and
  *    must be 16-byte aligned.  The caller owns every buffer; the library
- *    allocates no device memory, keeps no per-call state and never
+ *    allocates no device memory, keeps no per-call state (a thread keeps the
+ *    constants of the last rope_base that it appended with) and never
  *    synchronises the stream.  Work is enqueued on `stream` (a cudaStream_t;
  *    NULL means the legacy default stream) on the current device.
  *  - Argument errors are detected on the host before anything is enqueued and
@@ -57,7 +58,7 @@
  *    a kernel of the caller that allows early launch must not write those
  *    inputs.  mla_absorb_q on its own starts as usual.
  *  - Supported sizes: d_c = 512, d_rope = 64, d_nope = 128, d_v = 128;
- *    batch >= 1; s_max >= 1; heads >= 1 (a multiple of 16 for MLA_BF16 and
+ *    batch >= 1; s_max >= 1; heads >= 1 (a multiple of 16 for MLA_BF16,
  *    MLA_FP8_E4M3 and MLA_FP4_E2M1).
  *    Anything else returns MLA_ERR_UNSUPPORTED.
  */
@@ -807,7 +808,8 @@ int32_t mla_decode_heads_per_cta(const mla_dims* dims);
  * mla_decode_step's fused tail (the split kernels, the combines, the combine
  * with W_UV) test each shared-memory and global index they can compute before
  * the access: TMA rows of the cache, the query rows, the query and P tiles and
- * the zeroed rows in shared memory, the partials and chunk counts.  A failed
+ * the zeroed rows in shared memory, the partials and chunk counts.  The FP8 kernels
+ * and those of the paged cache's SM pairs and 4-bit pools have no such tests.  A failed
  * test skips the access, ORs MLA_DEV_BOUNDS into the call's dev_status (when
  * given) and into the library's bounds word.  Nothing asserts or traps.  In the
  * default build the tests compile away and the word is never written.
