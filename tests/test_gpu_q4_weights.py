@@ -77,20 +77,29 @@ def check(c, tokens=None):
     assert max(worst) <= 1.0, f"{worst[0]:.3g} of the output's bound, {worst[1]:.3g} of the lse's"
 
 
-def problem(mla, n, at, nats, spread, io, heads, q_len=1, splits=1, page=64, seed=0, tail=None,
-            noise=0.0):
-    """One sequence whose row `at` lies above the others by nats[0] .. nats[1] (head by head).
-    The others' scores vary by `spread` nats; their latents have mean 1, the heavy row's -1."""
-    rng = np.random.RandomState(seed)
+def sequence(rng, n, at, spread=0.0, tail=None, noise=0.0):
+    """Latents and keys of n rows, of which row `at` answers to a query's first key value.  The
+    others' scores vary by `spread` nats; their latents have mean 1, that row's -1."""
     lat = (1.0 + noise * rng.randn(n, D_C)).astype(np.float32)
     key = np.zeros((n, D_R), np.float32)
     key[:, 1] = rng.randn(n) * spread / SCALE if tail is None else tail / SCALE
     lat[at], key[at, 0], key[at, 1] = -1.0, 1.0 / SCALE, 0.0
-    q_abs = torch.zeros((q_len, heads, D_C))
-    q_pe = torch.zeros((q_len, heads, D_R))
+    return lat, key
+
+
+def queries(tokens, heads, nats):
+    """With which that row lies nats[0] .. nats[1] above the others, head by head."""
+    q_abs, q_pe = torch.zeros((tokens, heads, D_C)), torch.zeros((tokens, heads, D_R))
     q_pe[:, :, 0] = torch.linspace(nats[0], nats[1], heads)
     q_pe[:, :, 1] = 1.0
-    return Far(mla, [lat], [key], q_abs, q_pe, page, io, q_len, splits)
+    return q_abs, q_pe
+
+
+def problem(mla, n, at, nats, spread, io, heads, q_len=1, splits=1, page=64, seed=0, tail=None,
+            noise=0.0):
+    """One such sequence."""
+    lat, key = sequence(np.random.RandomState(seed), n, at, spread, tail, noise)
+    return Far(mla, [lat], [key], *queries(q_len, heads, nats), page, io, q_len, splits)
 
 
 FORMS = [(F32, 16), (BF16, 16), (BF16, 48), (BF16, 128)]
@@ -138,3 +147,22 @@ def test_ordinary_rows(cuda_lib, io, heads, q_len):
     """Random rows, no row far from the others: each form within its own bound."""
     rng = np.random.RandomState(heads + q_len)
     check(shifted(rng, cuda_lib, [np.zeros(n) for n in (2, 129, 700, 5000)], heads, io, q_len).run())
+
+
+@pytest.mark.parametrize("io,heads", [(F32, 256), (BF16, 1024)])
+def test_long_pieces_of_many_sequences(cuda_lib, io, heads):
+    """Equal shares of 43 tiles a CTA or pair: runs that end and begin inside a sequence and look
+    at their sums in each of its pieces, with the heavy row in some of them."""
+    mla = cuda_lib
+    mla.load().mla_test_set_split_form(1)
+    try:
+        rng = np.random.RandomState(4)
+        lat, key = zip(*(sequence(rng, n, at, 0.5) for n, at in
+                         [(4096, 0), (4000, 3999), (4096, 2000), (3900, 700), (130, 3), (4096, 4000),
+                          (4096, 100), (4095, 1500), (3000, 2900), (4096, 50), (4096, 3333), (4096, 9)]))
+        c = Far(mla, list(lat), list(key), *queries(len(lat), heads, (9.0, 14.0)), 64, io).run()
+        check(c, tokens=[0, 1, 2, 3, 4, 8, 11])
+        first = c.o.clone()
+        assert torch.equal(first, c.run().o)
+    finally:
+        mla.load().mla_test_set_split_form(0)
